@@ -59,7 +59,8 @@
  * Memory and ownership.  The caller allocates and owns every rank buffer
  * (device memory, e.g. from PyTorch).  A communicator copies the p input and
  * output pointers (host arrays are not retained) and allocates one small
- * device status block (256 bytes) that it frees in ccl_comm_destroy().  No
+ * device block (33 KB: the status record, and the scratch of the balance
+ * loss's sums) that it frees in ccl_comm_destroy().  No
  * call allocates memory proportional to the message.  Rank buffers may also
  * be page-locked host memory the device can address with the same pointer
  * (cudaHostAlloc, or torch's pin_memory): the ld/st kernels then read and
@@ -317,6 +318,129 @@ CCL_API ccl_status_t ccl_allreduce_residual_rmsnorm(ccl_comm_t comm, ccl_dtype_t
                                                     const void *residual_in, void *residual_out, const void *gamma,
                                                     float eps, ccl_schedule_t schedule, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators on logits.  The communicator's rank buffers hold the logits of a
+ * head; what crosses the ranks is not a reduction of the buffers but a
+ * (maximum, sum of exponentials) pair, a count, or nothing, so each operator
+ * is one call of its own.  No passage of the pages: the operators are defined
+ * here.  dtype is f32, f16 or bf16 (int32: CCL_ERR_UNSUPPORTED); arithmetic
+ * is fp32, sums and softmax statistics included, rounded once to dtype.  The
+ * same call on the same inputs gives the same bits.  Like the fused RMSNorm
+ * they use every SM and ignore the communicator's variant and schedule.
+ * Device arrays of int32 or float are 4-byte aligned, rank buffers aligned to
+ * their elements; 16-byte aligned buffers are fastest.  Nothing that is
+ * written may overlap anything else, except an output that is its own rank's
+ * input.  Calls only enqueue and can be captured in a CUDA graph once each
+ * operator has run once on the device with the same dtype and sizes.
+ *
+ * Vocabulary shards (ccl_logit_rules, ccl_distill_topk): rank r's buffers
+ * hold the columns of balanced chunk r of vocab (see "Schedules" above: the
+ * larger chunks first) of [rows, vocab] logits, row-major.  ld is the row
+ * stride of every rank buffer in elements, at least the widest chunk; 0: each
+ * rank's rows are contiguous.  vocab <= 2^30.
+ * ------------------------------------------------------------------------- */
+
+/* What a decode step does to its logits.  Device arrays; a NULL array (or a
+ * count of 0) leaves its rule out. */
+typedef struct {
+    const float *repetition;      /* [rows] factor > 0 of tokens that occurred (1: none) */
+    const float *frequency;       /* [rows] subtracted once per generated occurrence */
+    const float *presence;        /* [rows] subtracted if generated at least once */
+    const int32_t *history;       /* [rows, history_ld] the tokens so far: the prompt, then what was generated;
+                                     a token outside [0, vocab) counts for nothing */
+    size_t history_ld;            /* row stride of history in tokens, <= 2^30 - 1 */
+    const int32_t *history_len;   /* [rows] tokens so far (NULL: history_ld), held to [0, history_ld] */
+    const int32_t *prompt_len;    /* [rows] how many of them are prompt (NULL: none) */
+    const int32_t *bias_offsets;  /* [rows + 1] row i has bias entries [bias_offsets[i], bias_offsets[i+1]) */
+    const int32_t *bias_tokens;   /* [bias_count] in any order; entries of one token add up in list order; a
+                                     token outside [0, vocab) is left out */
+    const float *bias_values;     /* [bias_count] */
+    size_t bias_count;            /* entries in all; offsets are held to [0, bias_count] */
+    const uint32_t *mask;         /* [mask_rows, mask_ld] bit v % 32 of word v / 32 set: token v is allowed */
+    size_t mask_rows, mask_ld;    /* mask_ld >= ceil(vocab / 32) words */
+    const int32_t *mask_index;    /* [rows] a row's mask (NULL: mask i for row i); outside [0, mask_rows): none */
+} ccl_logit_rules_t;
+
+/* Penalties for repeated tokens, biases and grammar masks on the logits of one
+ * decode step: inputs -> outputs (in place or disjoint).  Per row and token v,
+ * with c its generated occurrences:
+ *   x += the row's bias entries for v
+ *   x = x > 0 ? x / repetition : x * repetition   if v occurs in the history
+ *   x = (x - frequency * c) - presence            if c > 0
+ *   x = -inf                                      if the row's mask forbids v
+ * A row that its mask leaves nothing is all -inf.
+ * Bytes moved: rows * vocab * s read and written, the history and the lists.
+ * Errors: CCL_ERR_INVALID_ARG (NULL rules, a size out of range, a missing
+ * array, overlap), CCL_ERR_UNSUPPORTED, CCL_ERR_CUDA. */
+CCL_API ccl_status_t ccl_logit_rules(ccl_comm_t comm, ccl_dtype_t dtype, size_t rows, size_t vocab, size_t ld,
+                                     const ccl_logit_rules_t *rules, void *stream);
+
+/* Which part of a loss a call computes.  BOTH takes the upstream gradient as
+ * known beforehand and reads the logits once. */
+typedef enum { CCL_PASS_FORWARD = 1, CCL_PASS_BACKWARD = 2, CCL_PASS_BOTH = 3 } ccl_pass_t;
+
+/* Distillation from a teacher's top k logits over the full student
+ * vocabulary.  Inputs: the student's logits z; outputs (BACKWARD and BOTH, in
+ * place or disjoint): the gradient.  Row i, with q = softmax(t / temperature)
+ * over its valid teacher entries, p = softmax(z / temperature):
+ *   loss[i] = temperature^2 * sum_k q_k (log q_k - log p[id_k])
+ *   dz[v]   = row_weight[i] * temperature * (p[v] - sum of q_k with id_k = v)
+ *  teacher_ids    : device [rows, k]; an id outside [0, vocab) (such as -1) is
+ *                   no entry.  Entries of one token add up.
+ *  teacher_logits : device [rows, k] of teacher_dtype (f32, f16, bf16); logits
+ *                   or log-probabilities.  -inf: no entry.
+ *  row_weight     : device [rows], the gradient of what follows by loss[i];
+ *                   NULL: 1.  Not read by FORWARD.
+ *  loss           : device [rows], written by FORWARD and BOTH.
+ *  stats          : device [rows, 2], the row's maximum of z and log sum exp((z -
+ *                   maximum) / temperature): written by FORWARD and BOTH if not
+ *                   NULL, read by BACKWARD.
+ * A row without an entry has loss 0 and gradient 0.  Logits of -inf have
+ * probability 0 (loss +inf if the teacher has weight there); a row of nothing
+ * but -inf has p = 0 and loss +inf.
+ * Bytes moved: rows * vocab * s read; BACKWARD and BOTH also write it.  BOTH
+ * reads the logits twice beyond 131072 columns.
+ * Errors: CCL_ERR_INVALID_ARG (a size, pass or temperature out of range, a
+ * missing array, overlap), CCL_ERR_UNSUPPORTED (int32, k > 1024),
+ * CCL_ERR_CUDA. */
+CCL_API ccl_status_t ccl_distill_topk(ccl_comm_t comm, ccl_dtype_t dtype, ccl_pass_t pass, size_t rows, size_t vocab,
+                                      size_t ld, size_t k, const int32_t *teacher_ids, const void *teacher_logits,
+                                      ccl_dtype_t teacher_dtype, float temperature, const float *row_weight,
+                                      float *loss, float *stats, void *stream);
+
+/* The load-balance loss of a router over p data-parallel ranks, the
+ * per-expert counts and the gradient.  Rank r's input: the router logits of
+ * its own tokens, [rows, experts] row-major; outputs (BACKWARD and BOTH, in
+ * place or disjoint): their gradient.  With N the valid rows of all ranks and
+ * count_e the valid rows' choices of expert e over all ranks:
+ *   loss = coef * experts * sum_e f_e P_e,   f_e = count_e / (k N),
+ *   P_e  = (1/N) * sum over the valid rows of softmax(x)_e
+ *   dx_te = dloss * p_te * (a_e - sum_j p_tj a_j),  a_e = coef experts count_e / (k N^2)
+ * (the counts have no gradient).
+ *  expert_ids : host array of p device pointers, each [rows, k]: the chosen
+ *               experts; an id outside [0, experts) (a dropped choice) counts for
+ *               nothing.  Not read by BACKWARD (may be NULL).
+ *  valid      : host array of p device pointers, each [rows] bytes: 0 is a
+ *               padding row, which counts for nothing and has gradient 0.  NULL: every
+ *               row is valid.
+ *  dloss      : device, one float, the upstream gradient; NULL: 1.  Not read by
+ *               FORWARD.
+ *  counts     : device [p, experts]; tokens: device [p], the valid rows.
+ *               Written by FORWARD and BOTH, read by BACKWARD.
+ *  loss       : device, one float, written by FORWARD and BOTH.
+ * Without a valid row the loss and every gradient are 0.  A valid row of
+ * nothing but -inf counts its choices and has p = 0.  At most 4096 experts;
+ * rows * k <= 2^31 - 1.  The sums across CTAs pass through the communicator's
+ * device block.
+ * Bytes moved: p * rows * (experts * s + 4 k) read; BACKWARD and BOTH also
+ * write the gradient, p * rows * experts * s.
+ * Errors: CCL_ERR_INVALID_ARG (a size or pass out of range, a missing array,
+ * overlap), CCL_ERR_UNSUPPORTED (int32, experts > 4096), CCL_ERR_CUDA. */
+CCL_API ccl_status_t ccl_balance_loss(ccl_comm_t comm, ccl_dtype_t dtype, ccl_pass_t pass, size_t rows, size_t experts,
+                                      size_t k, const int32_t *const *expert_ids, const uint8_t *const *valid,
+                                      float coef, const float *dloss, int32_t *counts, int32_t *tokens, float *loss,
+                                      void *stream);
+
 /* AllReduce for callers that cannot allocate device memory.  The pages have
  * no counterpart: this entry point exists for code that may not call
  * cudaMalloc -- a plug-in inside an application that owns all device memory
@@ -446,6 +570,9 @@ CCL_API ccl_status_t ccl_comm_last_launch(ccl_comm_t comm, char *buf, size_t len
 /* Number of kernels this communicator has launched since creation (no
  * passage of the pages: housekeeping; 0 for a NULL comm). */
 CCL_API uint64_t ccl_comm_launch_count(ccl_comm_t comm);
+
+/* The communicator's number of ranks p (housekeeping; 0 for a NULL comm). */
+CCL_API int ccl_comm_ranks(ccl_comm_t comm);
 
 /* CCL_VERSION of the loaded library (housekeeping). */
 CCL_API int ccl_version(void);

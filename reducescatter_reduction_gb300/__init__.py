@@ -28,6 +28,7 @@ CCL_F32, CCL_F16, CCL_BF16, CCL_I32 = range(4)
 CCL_SCHED_AUTO, CCL_SCHED_RING, CCL_SCHED_ALLPAIRS, CCL_SCHED_CUSTOM = range(4)
 (CCL_VARIANT_AUTO, CCL_VARIANT_LDST, CCL_VARIANT_TMA, CCL_VARIANT_TMA_BULKRED, CCL_VARIANT_RING_STEPWISE,
  CCL_VARIANT_ONE_PHASE) = range(6)
+CCL_PASS_FORWARD, CCL_PASS_BACKWARD, CCL_PASS_BOTH = 1, 2, 3
 CCL_MAX_RANKS = 64
 
 OPS = {"sum": CCL_SUM, "prod": CCL_PROD, "min": CCL_MIN, "max": CCL_MAX, "avg": CCL_AVG}
@@ -37,6 +38,7 @@ SCHEDULES = {"auto": CCL_SCHED_AUTO, "ring": CCL_SCHED_RING, "allpairs": CCL_SCH
 VARIANTS = {"auto": CCL_VARIANT_AUTO, "ldst": CCL_VARIANT_LDST, "tma": CCL_VARIANT_TMA,
             "tma_bulkred": CCL_VARIANT_TMA_BULKRED, "ring_stepwise": CCL_VARIANT_RING_STEPWISE,
             "one_phase": CCL_VARIANT_ONE_PHASE}
+PASSES = {"forward": CCL_PASS_FORWARD, "backward": CCL_PASS_BACKWARD, "both": CCL_PASS_BOTH}
 STATUS_NAMES = {CCL_OK: "CCL_OK", CCL_ERR_INVALID_ARG: "CCL_ERR_INVALID_ARG",
                 CCL_ERR_UNSUPPORTED: "CCL_ERR_UNSUPPORTED", CCL_ERR_CUDA: "CCL_ERR_CUDA",
                 CCL_ERR_TIMEOUT: "CCL_ERR_TIMEOUT", CCL_ERR_NOMEM: "CCL_ERR_NOMEM", CCL_ERR_BOUNDS: "CCL_ERR_BOUNDS"}
@@ -46,8 +48,9 @@ EXPORTS = (
     "ccl_comm_create", "ccl_comm_set_outputs", "ccl_comm_set_schedule", "ccl_set_launch", "ccl_comm_set_debug",
     "ccl_comm_destroy", "ccl_comm_check", "ccl_allreduce", "ccl_reduce_scatter", "ccl_all_gather",
     "ccl_allreduce_static", "ccl_allreduce_static_set_debug", "ccl_allreduce_residual_rmsnorm",
+    "ccl_logit_rules", "ccl_distill_topk", "ccl_balance_loss",
     "ccl_schedule_build", "ccl_schedule_check", "ccl_cost_estimate", "ccl_select_schedule", "ccl_launch_estimate",
-    "ccl_last_error", "ccl_comm_last_launch", "ccl_comm_launch_count", "ccl_version", "ccl_bounds_checked",
+    "ccl_last_error", "ccl_comm_last_launch", "ccl_comm_launch_count", "ccl_comm_ranks", "ccl_version", "ccl_bounds_checked",
 )
 
 
@@ -61,6 +64,15 @@ class CostParams(ctypes.Structure):
     """ccl_cost_params_t."""
     _fields_ = [("alpha_s", ctypes.c_double), ("bw_bytes_per_s", ctypes.c_double),
                 ("eff_ring", ctypes.c_double), ("eff_allpairs", ctypes.c_double)]
+
+
+class LogitRules(ctypes.Structure):
+    """ccl_logit_rules_t: device pointers as integers, by keyword; what is left out is no rule."""
+    _fields_ = [("repetition", ctypes.c_void_p), ("frequency", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("history", ctypes.c_void_p), ("history_ld", ctypes.c_size_t), ("history_len", ctypes.c_void_p),
+                ("prompt_len", ctypes.c_void_p), ("bias_offsets", ctypes.c_void_p), ("bias_tokens", ctypes.c_void_p),
+                ("bias_values", ctypes.c_void_p), ("bias_count", ctypes.c_size_t), ("mask", ctypes.c_void_p),
+                ("mask_rows", ctypes.c_size_t), ("mask_ld", ctypes.c_size_t), ("mask_index", ctypes.c_void_p)]
 
 
 _lib = None
@@ -90,6 +102,9 @@ def load_library(path: str = LIB_PATH):
         "ccl_allreduce_static": (i, [i, pvp, pvp, i, i, sz, i, vp]),
         "ccl_allreduce_static_set_debug": (i, [ctypes.c_longlong, i]),
         "ccl_allreduce_residual_rmsnorm": (i, [vp, i, sz, sz, vp, vp, vp, ctypes.c_float, i, vp]),
+        "ccl_logit_rules": (i, [vp, i, sz, sz, sz, ctypes.POINTER(LogitRules), vp]),
+        "ccl_distill_topk": (i, [vp, i, i, sz, sz, sz, sz, vp, vp, i, ctypes.c_float, vp, vp, vp, vp]),
+        "ccl_balance_loss": (i, [vp, i, i, sz, sz, sz, pvp, pvp, ctypes.c_float, vp, vp, vp, vp, vp]),
         "ccl_schedule_build": (i, [i, u64, i, ctypes.POINTER(u64), ctypes.POINTER(ctypes.c_uint8)]),
         "ccl_schedule_check": (i, [i, u64, ctypes.POINTER(u64), ctypes.POINTER(ctypes.c_uint8)]),
         "ccl_cost_estimate": (ctypes.c_double, [i, ctypes.c_double, i, ctypes.POINTER(CostParams)]),
@@ -98,6 +113,7 @@ def load_library(path: str = LIB_PATH):
         "ccl_last_error": (ctypes.c_char_p, []),
         "ccl_comm_last_launch": (i, [vp, ctypes.c_char_p, sz]),
         "ccl_comm_launch_count": (u64, [vp]),
+        "ccl_comm_ranks": (i, [vp]),
         "ccl_version": (i, []),
         "ccl_bounds_checked": (i, []),
     }
@@ -212,6 +228,36 @@ def ccl_allreduce_residual_rmsnorm(comm: int, dtype, rows: int, hidden: int, res
                                                          _code(SCHEDULES, schedule), stream or None))
 
 
+def ccl_logit_rules(comm: int, dtype, rows: int, vocab: int, rules: LogitRules, ld: int = 0, stream: int = 0) -> None:
+    """Penalties, biases and grammar masks on one decode step's logits (see include/ccl.h)."""
+    _check(load_library().ccl_logit_rules(comm, _code(DTYPES, dtype), int(rows), int(vocab), int(ld),
+                                          None if rules is None else ctypes.byref(rules), stream or None))
+
+
+def ccl_distill_topk(comm: int, dtype, steps, rows: int, vocab: int, k: int, teacher_ids: int, teacher_logits: int,
+                     teacher_dtype="f32", temperature: float = 1.0, row_weight: int = 0, loss: int = 0, stats: int = 0,
+                     ld: int = 0, stream: int = 0) -> None:
+    """The loss against a teacher's top k logits and its gradient; steps: "forward", "backward" or "both"."""
+    _check(load_library().ccl_distill_topk(comm, _code(DTYPES, dtype), _code(PASSES, steps), int(rows), int(vocab),
+                                           int(ld), int(k), teacher_ids, teacher_logits, _code(DTYPES, teacher_dtype),
+                                           float(temperature), row_weight or None, loss or None, stats or None,
+                                           stream or None))
+
+
+def ccl_balance_loss(comm: int, dtype, steps, rows: int, experts: int, k: int, expert_ids, valid, coef: float,
+                     dloss: int, counts: int, tokens: int, loss: int = 0, stream: int = 0) -> None:
+    """A router's load-balance loss, per-expert counts and gradient.  expert_ids and valid are lists with one device
+    pointer for each of the communicator's ranks (or None; see include/ccl.h)."""
+    lib = load_library()
+    p = lib.ccl_comm_ranks(comm)
+    for ptrs, what in ((expert_ids, "expert_ids"), (valid, "valid")):
+        _want_len(ptrs, p, what)
+    _check(lib.ccl_balance_loss(comm, _code(DTYPES, dtype), _code(PASSES, steps), int(rows), int(experts), int(k),
+                                None if expert_ids is None else _ptr_array(expert_ids),
+                                None if valid is None else _ptr_array(valid), float(coef), dloss or None,
+                                counts or None, tokens or None, loss or None, stream or None))
+
+
 def ccl_schedule_build(p: int, n: int, schedule):
     """Returns (bounds: list of p+1 ints, order: list of p rows of p ranks)."""
     bounds = (ctypes.c_uint64 * (p + 1))()
@@ -258,6 +304,10 @@ def ccl_comm_last_launch(comm: int) -> str:
 
 def ccl_comm_launch_count(comm: int) -> int:
     return load_library().ccl_comm_launch_count(comm)
+
+
+def ccl_comm_ranks(comm: int) -> int:
+    return load_library().ccl_comm_ranks(comm)
 
 
 def ccl_version() -> int:

@@ -12,30 +12,10 @@
 #include <new>
 #include <string>
 
+#include "comm.h"
 #include "internal.h"
 
 using namespace ccl;
-
-struct ccl_comm {
-    int p = 0;
-    int device = 0;
-    int num_sms = 0;
-    void *in[kMaxRanks] = {};
-    void *out[kMaxRanks] = {};
-    int sm_budget = 0;
-    int variant = CCL_VARIANT_AUTO;
-    size_t pipe_bytes = 0;
-    unsigned *d_status = nullptr;   // 256-byte device status block
-    bool has_custom = false;
-    uint8_t custom[kMaxRanks * kMaxRanks] = {};
-    Table table;                    // last built table (one-entry cache)
-    int table_sched = -1;
-    bool table_valid = false;
-    uint64_t launches = 0;
-    char last[320] = "";
-    long long wait_limit_ns = 2000000000LL;  // bounded device waits: 2 s
-    int stall_test = 0;
-};
 
 // ---------------------------------------------------------------------------
 // Errors.
@@ -43,7 +23,9 @@ struct ccl_comm {
 
 static thread_local std::string g_err;
 
-static ccl_status_t fail(ccl_status_t st, const char *fmt, ...)
+namespace ccl {
+
+ccl_status_t fail(ccl_status_t st, const char *fmt, ...)
 {
     char buf[512];
     va_list ap;
@@ -54,21 +36,19 @@ static ccl_status_t fail(ccl_status_t st, const char *fmt, ...)
     return st;
 }
 
-namespace ccl {
 // Lets other translation units of the library report through ccl_last_error().
 ccl_status_t record_error(ccl_status_t st, const char *msg)
 {
     g_err = msg;
     return st;
 }
-}  // namespace ccl
 
-static ccl_status_t cuda_fail(cudaError_t err, const char *what)
+ccl_status_t cuda_fail(cudaError_t err, const char *what)
 {
     return fail(CCL_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(err), cudaGetErrorString(err));
 }
 
-static bool debug_on()
+bool debug_on()
 {
     static int on = -1;
     if (on < 0) {
@@ -78,39 +58,11 @@ static bool debug_on()
     return on == 1;
 }
 
-// Restores the caller's current device when a call had to switch to the
-// communicator's device.
-struct DeviceGuard {
-    int prev = -1;
-    bool switched = false;
-    cudaError_t err = cudaSuccess;
-    explicit DeviceGuard(int dev)
-    {
-        err = cudaGetDevice(&prev);
-        if (err == cudaSuccess && prev != dev) {
-            err = cudaSetDevice(dev);
-            switched = (err == cudaSuccess);
-        }
-    }
-    ~DeviceGuard()
-    {
-        if (switched) cudaSetDevice(prev);
-    }
-};
+}  // namespace ccl
 
 // ---------------------------------------------------------------------------
 // Schedule builder.
 // ---------------------------------------------------------------------------
-
-// p balanced chunks, the first n % p one element larger.
-static void chunk_bounds(int p, uint64_t n, uint64_t *bounds)
-{
-    const uint64_t q = n / uint64_t(p), r = n % uint64_t(p);
-    for (int c = 0; c <= p; ++c) {
-        const uint64_t uc = uint64_t(c);
-        bounds[c] = uc * q + (uc < r ? uc : r);
-    }
-}
 
 // Ring ("Inside NCCL AllReduce", "The ring, exactly as the kernel runs it"):
 // a chunk starts at the rank after its owner and walks the ring, so the owner
@@ -281,8 +233,8 @@ extern "C" ccl_status_t ccl_comm_create(ccl_comm_t *out, int p, void *const *ran
     cudaError_t err = cudaGetDevice(&c->device);
     if (err == cudaSuccess)
         err = cudaDeviceGetAttribute(&c->num_sms, cudaDevAttrMultiProcessorCount, c->device);
-    if (err == cudaSuccess) err = cudaMalloc(&c->d_status, 256);
-    if (err == cudaSuccess) err = cudaMemset(c->d_status, 0, 256);
+    if (err == cudaSuccess) err = cudaMalloc(&c->d_status, kCommDeviceBytes);
+    if (err == cudaSuccess) err = cudaMemset(c->d_status, 0, kCommDeviceBytes);
     if (err != cudaSuccess) {
         if (c->d_status) cudaFree(c->d_status);
         delete c;
@@ -366,7 +318,7 @@ extern "C" ccl_status_t ccl_comm_check(ccl_comm_t c)
     if (err == cudaSuccess) err = cudaMemcpy(st, c->d_status, sizeof st, cudaMemcpyDeviceToHost);
     if (err != cudaSuccess) return cuda_fail(err, "ccl_comm_check");
     if (st[0] != 0) {
-        cudaMemset(c->d_status, 0, 256);
+        cudaMemset(c->d_status, 0, kCommStatusBytes);
         if (st[0] == kBoundsCode)
             return fail(CCL_ERR_BOUNDS, "an access outside a rank buffer was computed and skipped (site %u, block %u, "
                         "index %u)", st[3], st[1], st[2]);
@@ -392,6 +344,8 @@ extern "C" ccl_status_t ccl_comm_last_launch(ccl_comm_t c, char *buf, size_t len
     return CCL_OK;
 }
 
+extern "C" int ccl_comm_ranks(ccl_comm_t c) { return c ? c->p : 0; }
+
 extern "C" uint64_t ccl_comm_launch_count(ccl_comm_t c) { return c ? c->launches : 0; }
 
 // ---------------------------------------------------------------------------
@@ -399,18 +353,11 @@ extern "C" uint64_t ccl_comm_launch_count(ccl_comm_t c) { return c ? c->launches
 // ---------------------------------------------------------------------------
 
 static const char *kOpName[] = {"sum", "prod", "min", "max", "avg"};
-static const char *kDtypeName[] = {"f32", "f16", "bf16", "i32"};
 static const char *kSchedName[] = {"auto", "ring", "allpairs", "custom"};
 static const char *kCollName[] = {"allreduce", "reduce_scatter", "all_gather"};
 static const char *kVariantName[] = {"auto", "ldst", "tma", "tma_bulkred", "ring_stepwise", "one_phase"};
 
 enum Coll { COLL_AR = 0, COLL_RS = 1, COLL_AG = 2 };
-
-struct Range {
-    uintptr_t lo, hi;  // [lo, hi)
-};
-
-static bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo < a.hi && b.lo < b.hi; }
 
 // Every output must be disjoint from every other output and from everything
 // any rank reads, except the exact in-place alias of its own rank:

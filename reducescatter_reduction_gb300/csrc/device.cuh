@@ -39,6 +39,9 @@ enum BoundsSite : unsigned {
     kSiteGather = 5,        // AllGather kernel
     kSiteBulkred = 6,       // bulk-reduce kernel
     kSiteNorm = 7,          // fused AllReduce + residual + RMSNorm
+    kSiteRules = 8,         // logit rules
+    kSiteDistill = 9,       // top-K distillation
+    kSiteBalance = 10,      // router balance loss
 };
 
 __device__ __forceinline__ bool in_bounds(bool ok, unsigned *status, unsigned site, uint64_t index)

@@ -12,6 +12,15 @@ namespace ccl {
 
 constexpr int kMaxRanks = 64;
 
+// The device block of a communicator: the status record and tile counters,
+// then (kScratchOffset) the scratch of ccl_balance_loss: a ticket counter that
+// every call leaves at zero, and one pair of partial sums per CTA.
+constexpr size_t kCommStatusBytes = 256;
+constexpr size_t kScratchOffset = kCommStatusBytes;
+constexpr size_t kScratchHead = 256;          // the ticket, padded
+constexpr unsigned kMaxPartials = 2048;       // CTAs that may leave a pair of sums
+constexpr size_t kCommDeviceBytes = kScratchOffset + kScratchHead + size_t(kMaxPartials) * 16;
+
 enum Op : int { OP_SUM = 0, OP_PROD = 1, OP_MIN = 2, OP_MAX = 3, OP_AVG = 4 };
 enum Dtype : int { DT_F32 = 0, DT_F16 = 1, DT_BF16 = 2, DT_I32 = 3 };
 enum Mode : int { MODE_AR = 0, MODE_RS = 1 };
@@ -238,6 +247,48 @@ struct NormLaunch {
     float eps = 0.0f;
 };
 cudaError_t launch_allreduce_rmsnorm(const Launch &L, const NormLaunch &N, LaunchInfo *info);
+
+// The logit operators (logit_rules.cu, distill.cu, balance.cu).  L.alias: the
+// outputs are the inputs.
+struct RulesLaunch {
+    uint64_t rows = 0;
+    uint32_t vocab = 0;
+    uint64_t ld = 0;
+    const ccl_logit_rules_t *rules = nullptr;
+};
+cudaError_t launch_logit_rules(const Launch &L, const RulesLaunch &N, LaunchInfo *info);
+
+struct DistillLaunch {
+    int pass = 0;
+    uint64_t rows = 0;
+    uint32_t vocab = 0;
+    uint64_t ld = 0;
+    uint32_t k = 0;
+    const int32_t *ids = nullptr;
+    const void *teacher = nullptr;
+    int teacher_dtype = 0;
+    float temperature = 1.0f;
+    const float *weight = nullptr;
+    float *loss = nullptr;
+    float *stats = nullptr;
+};
+cudaError_t launch_distill(const Launch &L, const DistillLaunch &N, LaunchInfo *info);
+
+struct BalanceLaunch {
+    int pass = 0;
+    uint64_t rows = 0;
+    uint32_t experts = 0;
+    uint32_t k = 0;
+    const int32_t *const *ids = nullptr;
+    const uint8_t *const *valid = nullptr;
+    float coef = 0.0f;
+    const float *dloss = nullptr;
+    int32_t *counts = nullptr;
+    int32_t *tokens = nullptr;
+    float *loss = nullptr;
+    void *scratch = nullptr;    // the communicator's: kScratchHead bytes, then the partial sums
+};
+cudaError_t launch_balance(const Launch &L, const BalanceLaunch &N, LaunchInfo *info);
 
 // The measured launch table (launch_table.cpp): the estimated per-call time
 // (us) of an AllReduce with the ld/st or TMA kernel, and AUTO's choice.
