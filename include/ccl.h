@@ -59,8 +59,8 @@
  * Memory and ownership.  The caller allocates and owns every rank buffer
  * (device memory, e.g. from PyTorch).  A communicator copies the p input and
  * output pointers (host arrays are not retained) and allocates one small
- * device block (33 KB: the status record, and the scratch of the balance
- * loss's sums) that it frees in ccl_comm_destroy().  No
+ * device block (98 KB: the status record, and the scratch of the balance
+ * loss's sums and counts) that it frees in ccl_comm_destroy().  No
  * call allocates memory proportional to the message.  Rank buffers may also
  * be page-locked host memory the device can address with the same pointer
  * (cudaHostAlloc, or torch's pin_memory): the ld/st kernels then read and

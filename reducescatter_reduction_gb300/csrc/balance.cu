@@ -30,106 +30,132 @@ struct BalanceArgs {
     const uint8_t *valid[PM];
     uint64_t rows;
     uint32_t p, experts, k;
-    FastDiv by_k;
+    FastDiv by_k, by_choices, by_rows;   // choices per rank, rows per rank
     int pass, has_valid, count_here;
     double coef;
     const float *dloss;
-    int32_t *counts, *tokens;
+    int32_t *counts, *tokens;      // the caller's
+    int32_t *cells, *cell_tokens;  // where the counting kernel counts: the scratch, or the caller's own, zeroed
     float *loss;
     unsigned *ticket;
     double2 *partials;
     unsigned *status;
 };
 
-// Adds rank r's choices [j0, j1) with the given stride to hist[experts].
-template <int PM>
-__device__ __forceinline__ void count_choices(const BalanceArgs<PM> &a, uint32_t r, uint32_t first, uint32_t stride, int *hist)
-{
-    const uint32_t n = uint32_t(a.rows) * a.k;
-    for (uint64_t j = first; j < n; j += stride) {
-        const int id = a.ids[r][j];
-        if (uint32_t(id) >= a.experts) continue;
-        if (a.has_valid && !a.valid[r][div_by(uint32_t(j), a.by_k)]) continue;
-        atomicAdd(&hist[id], 1);
-    }
-}
-
-template <int PM>
-__device__ __forceinline__ int count_rows(const BalanceArgs<PM> &a, uint32_t r, uint32_t first, uint32_t stride)
-{
-    int n = 0;
-    for (uint64_t t = first; t < a.rows; t += stride) n += a.valid[r][t] != 0;
-    return n;
-}
-
-// Counts the choices of all ranks into counts and tokens, which are zero.
+// Counts the choices and valid rows of all ranks into cells, which are zero.
+// A CTA counts in shared memory first: integer atomics, so any order gives
+// the same counts.
 template <int PM>
 __global__ void __launch_bounds__(kBalanceThreads) balance_count_kernel(const __grid_constant__ BalanceArgs<PM> a)
 {
     extern __shared__ int hist[];
+    constexpr int BATCH = 4;
     const uint32_t r = blockIdx.y;
     for (uint32_t e = threadIdx.x; e < a.experts; e += kBalanceThreads) hist[e] = 0;
     grid_dependency_wait();
     grid_dependents_launch();
     __syncthreads();
-    const uint32_t first = blockIdx.x * kBalanceThreads + threadIdx.x, stride = gridDim.x * kBalanceThreads;
-    count_choices(a, r, first, stride, hist);
+    const uint64_t first = uint64_t(blockIdx.x) * kBalanceThreads + threadIdx.x, stride = uint64_t(gridDim.x) * kBalanceThreads;
+    const uint64_t n = a.rows * a.k;
+    const int32_t *ids = a.ids[r];
+    for (uint64_t j = first; j < n; j += BATCH * stride) {
+        int id[BATCH];
+        bool on[BATCH];
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const uint64_t at = j + b * stride;
+            id[b] = at < n ? ids[at] : -1;
+            on[b] = at < n && (!a.has_valid || a.valid[r][div_by(uint32_t(at), a.by_k)]);
+        }
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b)
+            if (on[b] && uint32_t(id[b]) < a.experts) atomicAdd(&hist[id[b]], 1);
+    }
     if (a.has_valid) {
-        int n = count_rows(a, r, first, stride);
-        n = __reduce_add_sync(0xffffffffu, n);
-        if (threadIdx.x % 32 == 0 && n) atomicAdd(&a.tokens[r], n);
+        int rows = 0;
+        for (uint64_t t = first; t < a.rows; t += stride) rows += a.valid[r][t] != 0;
+        rows = __reduce_add_sync(0xffffffffu, rows);
+        if (threadIdx.x % 32 == 0 && rows) atomicAdd(&a.cell_tokens[r], rows);
     } else if (blockIdx.x == 0 && threadIdx.x == 0) {
-        a.tokens[r] = int(a.rows);
+        a.cell_tokens[r] = int(a.rows);
     }
     __syncthreads();
     for (uint32_t e = threadIdx.x; e < a.experts; e += kBalanceThreads)
-        if (hist[e]) atomicAdd(&a.counts[uint64_t(r) * a.experts + e], hist[e]);
+        if (hist[e]) atomicAdd(&a.cells[uint64_t(r) * a.experts + e], hist[e]);
 }
 
 // d_e into shared memory; returns mean(a).  hist: p * experts counters and p
-// row counts when the CTA counts for itself.
+// row counts where the CTA counts for itself.
 template <int PM>
 __device__ __forceinline__ float balance_coefficients(const BalanceArgs<PM> &a, float *d_s, int *hist)
 {
     __shared__ unsigned long long sums[2];
     const uint32_t E = a.experts;
+    const int32_t *cells = a.cells, *tokens = a.cell_tokens;
     if (threadIdx.x < 2) sums[threadIdx.x] = 0;
-    const int32_t *counts = a.counts, *tokens = a.tokens;
     if (a.count_here) {
         int *rows_s = hist + a.p * E;
         for (uint32_t i = threadIdx.x; i < a.p * E + a.p; i += kBalanceThreads) hist[i] = 0;
-        grid_dependency_wait();
         __syncthreads();
-        for (uint32_t r = 0; r < a.p; ++r) {
-            count_choices(a, r, threadIdx.x, kBalanceThreads, hist + r * E);
-            int n = a.has_valid ? count_rows(a, r, threadIdx.x, kBalanceThreads) : threadIdx.x == 0 ? int(a.rows) : 0;
-            n = __reduce_add_sync(0xffffffffu, n);
-            if (threadIdx.x % 32 == 0 && n) atomicAdd(&rows_s[r], n);
+        constexpr int BATCH = 8;
+        const uint32_t n = a.by_choices.d, all = a.p * n, rows = uint32_t(a.rows);
+        for (uint32_t i = threadIdx.x; i < all; i += BATCH * kBalanceThreads) {
+            int id[BATCH];
+            uint32_t rank[BATCH];
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b) {
+                const uint32_t at = i + b * kBalanceThreads;
+                id[b] = -1;
+                if (at >= all) continue;
+                rank[b] = div_by(at, a.by_choices);
+                const uint32_t j = at - rank[b] * n;
+                id[b] = a.ids[rank[b]][j];
+                if (a.has_valid && !a.valid[rank[b]][div_by(j, a.by_k)]) id[b] = -1;
+            }
+#pragma unroll
+            for (int b = 0; b < BATCH; ++b)
+                if (uint32_t(id[b]) < E) atomicAdd(&hist[rank[b] * E + id[b]], 1);
         }
-        __syncthreads();
-        if (blockIdx.x == 0 && blockIdx.y == 0) {
-            for (uint32_t i = threadIdx.x; i < a.p * E; i += kBalanceThreads) a.counts[i] = hist[i];
-            for (uint32_t r = threadIdx.x; r < a.p; r += kBalanceThreads) a.tokens[r] = rows_s[r];
+        if (a.has_valid) {
+            for (uint32_t i = threadIdx.x; i < a.p * rows; i += kBalanceThreads) {
+                const uint32_t rank = div_by(i, a.by_rows);
+                if (a.valid[rank][i - rank * rows]) atomicAdd(&rows_s[rank], 1);
+            }
+        } else {
+            for (uint32_t r = threadIdx.x; r < a.p; r += kBalanceThreads) rows_s[r] = int(rows);
         }
-        counts = hist;
+        cells = hist;
         tokens = rows_s;
-    } else {
-        grid_dependency_wait();
-        __syncthreads();
     }
+    __syncthreads();
     // sums of integers: any order gives the same
-    for (uint32_t r = threadIdx.x; r < a.p; r += kBalanceThreads) atomicAdd(&sums[0], (unsigned long long)tokens[r]);
+    const bool writes = a.cells != a.counts && blockIdx.x == 0 && blockIdx.y == 0;
+    for (uint32_t r = threadIdx.x; r < a.p; r += kBalanceThreads) {
+        atomicAdd(&sums[0], (unsigned long long)tokens[r]);
+        if (writes) a.tokens[r] = tokens[r];
+    }
     unsigned long long mine = 0;
     for (uint32_t e = threadIdx.x; e < E; e += kBalanceThreads) {
-        for (uint32_t r = 0; r < a.p; ++r) mine += (unsigned long long)(long long)counts[uint64_t(r) * E + e];
+        unsigned total = 0;      // up to p (2^31 - 1): kept below in 64 bits where it can pass 32
+        unsigned long long wide = 0;
+        if (a.by_choices.d <= 0xffffffffu / kMaxRanks) {
+#pragma unroll 8
+            for (uint32_t r = 0; r < a.p; ++r) total += unsigned(cells[uint64_t(r) * E + e]);
+            wide = total;
+        } else {
+            for (uint32_t r = 0; r < a.p; ++r) wide += unsigned(cells[uint64_t(r) * E + e]);
+        }
+        if (writes)
+            for (uint32_t r = 0; r < a.p; ++r) a.counts[uint64_t(r) * E + e] = cells[uint64_t(r) * E + e];
+        mine += wide;
     }
     if (mine) atomicAdd(&sums[1], mine);
     __syncthreads();
     const double n = double(sums[0]), mean = double(sums[1]) / double(E);
     const double scale = sums[0] ? a.coef * double(E) / (double(a.k) * n * n) : 0.0;
     for (uint32_t e = threadIdx.x; e < E; e += kBalanceThreads) {
-        long long total = 0;
-        for (uint32_t r = 0; r < a.p; ++r) total += counts[uint64_t(r) * E + e];
+        unsigned long long total = 0;
+        for (uint32_t r = 0; r < a.p; ++r) total += unsigned(cells[uint64_t(r) * E + e]);
         d_s[e] = float((double(total) - mean) * scale);
     }
     __syncthreads();
@@ -137,7 +163,7 @@ __device__ __forceinline__ float balance_coefficients(const BalanceArgs<PM> &a, 
 }
 
 // The CTAs' sums: each leaves its pair, the last one adds the pairs in the
-// order of the CTAs, writes the loss and leaves the ticket at zero.
+// order of the CTAs, writes the loss and leaves the scratch at zero.
 template <int PM>
 __device__ __forceinline__ void balance_finish(const BalanceArgs<PM> &a, float lean, int live, float mean)
 {
@@ -167,10 +193,14 @@ __device__ __forceinline__ void balance_finish(const BalanceArgs<PM> &a, float l
         last = atomicAdd(a.ticket, 1u) == grid - 1;
     }
     __syncthreads();
-    if (!last || warp != 0) return;
+    if (!last) return;
     __threadfence();
+    if (a.cells != a.counts && !a.count_here) {
+        for (uint32_t i = threadIdx.x; i < a.p * a.experts; i += kBalanceThreads) a.cells[i] = 0;
+        for (uint32_t r = threadIdx.x; r < a.p; r += kBalanceThreads) a.cell_tokens[r] = 0;
+    }
     s = c = 0.0;
-    for (unsigned i = lane; i < grid; i += 32) {
+    for (unsigned i = threadIdx.x; i < grid; i += kBalanceThreads) {
         const double2 v = __ldcg(&a.partials[i]);
         s += v.x;
         c += v.y;
@@ -181,6 +211,16 @@ __device__ __forceinline__ void balance_finish(const BalanceArgs<PM> &a, float l
         c += __shfl_xor_sync(0xffffffffu, c, o);
     }
     if (lane == 0) {
+        red[0][warp] = s;
+        red[1][warp] = c;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        s = c = 0.0;
+        for (int w = 0; w < kBalanceWarps; ++w) {
+            s += red[0][w];
+            c += red[1][w];
+        }
         *a.loss = float(s + c * double(mean));
         *a.ticket = 0;
     }
@@ -189,88 +229,92 @@ __device__ __forceinline__ void balance_finish(const BalanceArgs<PM> &a, float l
 // L lanes of a warp take a row, 16-byte groups l, l + L, ... of it; NV groups
 // a lane hold the whole row, so the logits are read once.
 template <typename T, int PM, int L, int NV>
-__global__ void __launch_bounds__(kBalanceThreads) balance_kernel(const __grid_constant__ BalanceArgs<PM> a)
+__global__ void __launch_bounds__(kBalanceThreads, NV * Traits<T>::VEC > 16 ? 2 : NV > 2 ? 3 : 4) balance_kernel(const __grid_constant__ BalanceArgs<PM> a)
 {
     using Tr = Traits<T>;
-    constexpr int VEC = Tr::VEC, S = 16 / VEC, RPW = 32 / L;
+    using Gr = Group<T>;
+    constexpr int VEC = Tr::VEC, S = 16 / VEC, RPW = 32 / L, PAIRS = Gr::PAIRS;
     extern __shared__ float d_s[];
     const uint32_t E = a.experts, r = blockIdx.y;
-    const float mean = balance_coefficients(a, d_s, reinterpret_cast<int *>(d_s + E));
-    grid_dependents_launch();
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, l = lane % L;
-    float d[NV * VEC];
-#pragma unroll
-    for (int n = 0; n < NV; ++n)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const uint32_t col = (n * L + l) * VEC + i;
-            d[n * VEC + i] = col < E ? d_s[col] : 0.0f;
-        }
-    const uint32_t low = VEC == 4 ? 0xff800000u : Tr::kDtype == DT_BF16 ? 0xff80ff80u : 0xfc00fc00u;   // -inf
     const bool fwd = a.pass & CCL_PASS_FORWARD, bwd = a.pass & CCL_PASS_BACKWARD;
-    const float up = bwd && a.dloss ? *a.dloss : 1.0f;
     const char *in = static_cast<const char *>(a.in[r]);
     char *out = static_cast<char *>(a.out[r]);
+    const uint8_t *valid = a.has_valid ? a.valid[r] : nullptr;
     const uint64_t stride = uint64_t(gridDim.x) * kBalanceWarps * RPW;
-    auto fetch = [&](uint64_t t, uint4 (&raw)[NV]) {
+    bool on = false;
+    uint4 raw[NV];
+    auto fetch = [&](uint64_t t) {
+        on = t < a.rows && (!valid || valid[t]);
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const uint32_t col = (n * L + l) * VEC;
-            raw[n] = t < a.rows && col < E && in_bounds(col + VEC <= E, a.status, kSiteBalance, t)
-                         ? ld_coherent_v4(in + (t * E + col) * S)
-                         : make_uint4(low, low, low, low);
+            raw[n] = t < a.rows && col < E && in_bounds(col + VEC <= E, a.status, kSiteBalance, t) ? ld_coherent_v4(in + (t * E + col) * S)
+                                                                                                  : lowest_group<T>();
         }
     };
+    grid_dependency_wait();
+    grid_dependents_launch();
+    uint64_t base = (uint64_t(blockIdx.x) * kBalanceWarps + warp) * RPW;
+    fetch(base + lane / L);
+    const float mean = balance_coefficients(a, d_s, reinterpret_cast<int *>(d_s + E));
+    Pair d[NV * PAIRS];
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+            const uint32_t col = (n * L + l) * VEC + 2 * i;
+            d[n * PAIRS + i] = {col < E ? d_s[col] : 0.0f, col + 1 < E ? d_s[col + 1] : 0.0f};
+        }
+    const float up = bwd && a.dloss ? *a.dloss : 1.0f;
     float lean_sum = 0.0f;
     int live = 0;
-    uint64_t base = (uint64_t(blockIdx.x) * kBalanceWarps + warp) * RPW;
-    uint4 raw[NV];
-    fetch(base + lane / L, raw);
     for (; base < a.rows; base += stride) {
         const uint64_t t = base + lane / L;
-        const bool valid = t < a.rows && (!a.has_valid || a.valid[r][t]);
-        float x[NV * VEC], m = -INFINITY;
+        uint4 v[NV];
+        const bool valid_row = on;
 #pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            float f[VEC];
-            Tr::unpack(raw[n], f);
+        for (int n = 0; n < NV; ++n) v[n] = valid_row ? raw[n] : lowest_group<T>();   // padding: p = 0, whatever it holds
+        fetch(t + stride);
+        typename Gr::Max gm = Gr::lowest();
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) x[n * VEC + i] = f[i];
-        }
-        fetch(t + stride, raw);
-#pragma unroll
-        for (int i = 0; i < NV * VEC; ++i) m = fmaxf(m, x[i]);
+        for (int n = 0; n < NV; ++n) gm = Gr::max(gm, v[n]);
+        float m = Gr::value(gm);
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        m = m == -INFINITY ? 0.0f : m;
-        float s = 0.0f, dot = 0.0f;
+        m = finite_max(m);
+        Pair x[NV * PAIRS], sum = {0.0f, 0.0f}, dot = {0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < NV * VEC; ++i) {
-            x[i] = ex2((x[i] - m) * kLog2e);
-            s += x[i];
-            dot = fmaf(x[i], d[i], dot);
-        }
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) {
+                Pair &e = x[n * PAIRS + i];
+                e = ex2((Gr::pair(v[n], i) + Pair{-m, -m}) * Pair{kLog2e, kLog2e});
+                sum = sum + e;
+                dot = fma(e, d[n * PAIRS + i], dot);
+            }
+        float s = sum.x + sum.y, w = dot.x + dot.y;
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) {
             s += __shfl_xor_sync(0xffffffffu, s, o);
-            dot += __shfl_xor_sync(0xffffffffu, dot, o);
+            w += __shfl_xor_sync(0xffffffffu, w, o);
         }
-        const float inv = s == 0.0f ? 0.0f : 1.0f / s;    // a row of nothing but -inf has no softmax: p = 0
-        const float lean = dot * inv;
-        if (valid && l == 0 && s != 0.0f) {
+        const float inv = s == 0.0f ? 0.0f : __fdividef(1.0f, s);    // a row of nothing but -inf has no softmax: p = 0
+        const float lean = w * inv;
+        if (l == 0 && s != 0.0f) {
             lean_sum += lean;
             ++live;
         }
         if (bwd && t < a.rows) {
-            const float g = inv * up;
+            const Pair g = {inv * up, inv * up}, off = {-lean, -lean};
 #pragma unroll
             for (int n = 0; n < NV; ++n) {
                 const uint32_t col = (n * L + l) * VEC;
-                if (col >= E) continue;
-                float f[VEC];
+                if (col >= E || !in_bounds(col + VEC <= E, a.status, kSiteBalance, t)) continue;
+                Pair f[PAIRS];
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) f[i] = valid ? x[n * VEC + i] * (d[n * VEC + i] - lean) * g : 0.0f;
-                if (in_bounds(col + VEC <= E, a.status, kSiteBalance, t)) st_stream_v4(out + (t * E + col) * S, Tr::pack(f));
+                for (int i = 0; i < PAIRS; ++i) f[i] = (x[n * PAIRS + i] * (d[n * PAIRS + i] + off)) * g;
+                st_stream_v4(out + (t * E + col) * S, Gr::pack(f));
             }
         }
     }
@@ -285,8 +329,9 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_any_kernel(const __gr
     using Tr = Traits<T>;
     extern __shared__ float d_s[];
     const uint32_t E = a.experts, r = blockIdx.y;
-    const float mean = balance_coefficients(a, d_s, reinterpret_cast<int *>(d_s + E));
+    grid_dependency_wait();
     grid_dependents_launch();
+    const float mean = balance_coefficients(a, d_s, reinterpret_cast<int *>(d_s + E));
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const bool fwd = a.pass & CCL_PASS_FORWARD, bwd = a.pass & CCL_PASS_BACKWARD;
     const float up = bwd && a.dloss ? *a.dloss : 1.0f;
@@ -354,6 +399,8 @@ static cudaError_t balance_shape(const Launch &L, const BalanceLaunch &N, Launch
     a.experts = N.experts;
     a.k = N.k;
     a.by_k = fast_div(N.k);
+    a.by_choices = fast_div(N.rows ? uint32_t(N.rows * N.k) : 1);
+    a.by_rows = fast_div(N.rows ? uint32_t(N.rows) : 1);
     a.pass = N.pass;
     a.has_valid = N.valid ? 1 : 0;
     const uint64_t choices = uint64_t(L.p) * N.rows * N.k, cells = uint64_t(L.p) * N.experts;
@@ -365,12 +412,20 @@ static cudaError_t balance_shape(const Launch &L, const BalanceLaunch &N, Launch
     a.loss = N.loss;
     a.ticket = static_cast<unsigned *>(N.scratch);
     a.partials = reinterpret_cast<double2 *>(static_cast<char *>(N.scratch) + kScratchHead);
+    a.cells = N.counts;
+    a.cell_tokens = N.tokens;
+    const bool scratch = fwd && cells <= kScratchCells;
+    if (scratch) {
+        a.cells = reinterpret_cast<int32_t *>(a.partials + kMaxPartials);
+        a.cell_tokens = a.cells + kScratchCells;
+    }
     a.status = L.status;
     cudaError_t err = cudaSuccess;
     info->kernels = 0;
     if (fwd && !a.count_here) {
-        err = cudaMemsetAsync(N.counts, 0, cells * 4, L.stream);
-        if (err == cudaSuccess) err = cudaMemsetAsync(N.tokens, 0, size_t(L.p) * 4, L.stream);
+        // the scratch counters are zero already: the call that used them last left them so
+        if (!scratch) err = cudaMemsetAsync(N.counts, 0, cells * 4, L.stream);
+        if (!scratch && err == cudaSuccess) err = cudaMemsetAsync(N.tokens, 0, size_t(L.p) * 4, L.stream);
         if (err != cudaSuccess) return err;
         const uint64_t want = (N.rows * N.k + 4 * kBalanceThreads - 1) / (4 * kBalanceThreads);
         const uint64_t most = uint64_t(4 * L.num_sms) / uint64_t(L.p) + 1;
@@ -406,7 +461,7 @@ static cudaError_t balance_shape(const Launch &L, const BalanceLaunch &N, Launch
     }
     const uint64_t rows_per_cta = uint64_t(kBalanceWarps) * (32 / lanes);
     const uint64_t want = (N.rows + rows_per_cta - 1) / rows_per_cta;
-    const uint64_t most = uint64_t(6 * L.num_sms) < kMaxPartials ? uint64_t(6 * L.num_sms) / L.p : kMaxPartials / L.p;
+    const uint64_t most = uint64_t(4 * L.num_sms) < kMaxPartials ? uint64_t(4 * L.num_sms) / L.p : kMaxPartials / L.p;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(want < 1 ? 1 : want < most ? want : most), unsigned(L.p));
     cfg.blockDim = dim3(kBalanceThreads);

@@ -5,16 +5,20 @@
 // p = softmax(z / T) over the student's vocabulary:
 //   loss = T^2 sum_k q_k (log q_k - log p_{id_k})
 //   dz_v = w T (p_v - sum over the k with id_k = v of q_k)
-// A cluster of C CTAs takes a row, each CTA an equal part of its 16-byte
-// groups.  Every thread reads its groups once, keeps exp((z - m) / T) of the
-// first NV of them in registers against its own maximum m, and after the
+// A cluster of C CTAs takes a row.  Up to eight ranks, a CTA takes one of
+// `parts` parts of one rank's shard; beyond, `teams` teams of its warps take
+// one shard each.  Every thread reads its 16-byte groups once and keeps the
+// first NV of them in registers as they are (16-bit types: two elements per
+// register), takes the exponentials against its own maximum, and after the
 // exchange of (max, sum, the teacher's share of the loss) between the CTAs
-// scales them into the gradient: the logits are read once and the gradient
-// written once, 2 R V s bytes, with one exponential per element.  Groups past
-// the first NV per thread (vocabularies beyond C * THREADS * NV groups) are
-// read a second time.  The teacher's entries are then put right one by one:
-// after the CTA's barrier, the thread of an entry's first occurrence stores
-// the gradient of that token with the teacher's share taken off.
+// takes them again against the row's maximum and stores the gradient: the
+// logits are read once and the gradient is written once, 2 R V s bytes.
+// Keeping the exponentials instead would take twice the registers and halve
+// the CTAs per SM; exponentials are the cheaper of the two.  Groups past the
+// first NV per thread are read a second time.  The teacher's entries are then
+// put right one by one: after the CTA's barrier, the thread of an entry's
+// first occurrence stores the gradient of that token with the teacher's share
+// taken off.
 //
 // The CTAs of a row exchange their sums by writing them into one another's
 // shared memory before the cluster's hardware barrier; every CTA adds the
@@ -26,6 +30,7 @@
 namespace ccl {
 
 constexpr int kDistillMaxCluster = 8;
+constexpr int kDistillMaxThreads = 512;
 
 template <int PM>
 struct DistillArgs {
@@ -36,10 +41,13 @@ struct DistillArgs {
     float *loss;
     float *stats;
     float temperature;
-    float to_log2;       // log2(e) / T
+    float to_log2;        // log2(e) / T
     uint32_t k, kpad;
-    uint32_t cluster;    // CTAs per row
-    uint32_t total;      // group slots per row
+    uint32_t ctas;        // per row
+    uint32_t parts;       // parts of a shard (teams == 1), else 1
+    uint32_t teams;       // shards per CTA
+    uint32_t team;        // threads of a team
+    FastDiv by_ctas, by_parts, by_teams;
     int teacher_dtype;
 };
 
@@ -56,75 +64,82 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// A maximum of nothing but -inf: differences to it are formed against 0, so
-// that exp gives 0 and not NaN.
-__device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.0f : m; }
-
 __device__ __forceinline__ float load_any(const void *p, int dtype, uint64_t i)
 {
     return dtype == DT_F32 ? Traits<F32>::load1(p, i) : dtype == DT_F16 ? Traits<F16>::load1(p, i) : Traits<BF16>::load1(p, i);
 }
 
-// What one CTA of a row tells the others.
-struct Part {
-    float m, s;      // its maximum, sum exp((z - m) / T)
-    float dot, own;  // over the teacher's entries in its columns: sum e_k (z - m), sum e_k
-};
-
-template <typename T, int PM, int PASS, int THREADS, int NV>
-__global__ void __launch_bounds__(THREADS) distill_kernel(const __grid_constant__ DistillArgs<PM> a)
+template <typename T, int PM, int PASS, int NV, int MIN_CTAS>
+__global__ void __launch_bounds__(kDistillMaxThreads, MIN_CTAS) distill_kernel(const __grid_constant__ DistillArgs<PM> a)
 {
     using Tr = Traits<T>;
-    constexpr int VEC = Tr::VEC;
-    constexpr int WARPS = THREADS / 32;
+    using Gr = Group<T>;
+    constexpr int VEC = Tr::VEC, PAIRS = Gr::PAIRS, MAX_WARPS = kDistillMaxThreads / 32;
     constexpr bool FWD = PASS & CCL_PASS_FORWARD, BWD = PASS & CCL_PASS_BACKWARD;
     extern __shared__ uint4 smem4[];
-    int *id_s = reinterpret_cast<int *>(smem4);                    // ids, -1 where there is none
+    int *id_s = reinterpret_cast<int *>(smem4);                    // ids, negative where not in this CTA's columns
     float *e_s = reinterpret_cast<float *>(id_s + a.kpad);         // exp((t - tmax) / T)
     float *z_s = e_s + a.kpad;                                     // the student's logits at the ids in these columns
-    __shared__ float red[8][WARPS];
-    __shared__ float4 parts[kDistillMaxCluster];
+    __shared__ float red[7][MAX_WARPS];
+    __shared__ float4 parts[kDistillMaxCluster];                   // max, sum, teacher's dot, teacher's weight of a CTA
     const Shards<PM> &s = a.s;
-    const uint32_t C = a.cluster, q = blockIdx.x % C;
-    const uint64_t row = blockIdx.x / C;
-    const bool row_ok = row < s.rows;
+    const uint32_t row32 = div_by(blockIdx.x, a.by_ctas), q = blockIdx.x - row32 * a.ctas;
+    const uint64_t row = row32;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    if (FWD && C > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    const int threads = blockDim.x, warps = threads / 32;
+    if (FWD && a.ctas > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     grid_dependency_wait();
     grid_dependents_launch();
 
-    const uint32_t g0 = uint32_t(uint64_t(a.total) * q / C), g1 = uint32_t(uint64_t(a.total) * (q + 1) / C);
-    auto in_row = [&](uint32_t r) { return shard_row<T>(s.in[r], s.ld, row, shard_width(s, r)); };
-    auto load = [&](uint32_t slot) -> uint4 {
-        const uint32_t r = rank_of_slot(s, slot);
-        return load_group<T>(in_row(r), slot - r * s.nv, row_ok, s.status, kSiteDistill);
-    };
-    const uint32_t low = VEC == 4 ? 0xff800000u : Tr::kDtype == DT_BF16 ? 0xff80ff80u : 0xfc00fc00u;   // -inf
+    // this team's shard and part
+    uint32_t r, part = 0, tt = tid;
+    if (a.teams == 1) {
+        r = div_by(q, a.by_parts);
+        part = q - r * a.parts;
+    } else {
+        const uint32_t team = tid / a.team;
+        r = q * a.teams + team;
+        tt = tid - team * a.team;
+        if (r >= s.p || team >= a.teams) r = s.p;
+    }
+    const bool here = r < s.p && in_bounds(row < s.rows, s.status, kSiteDistill, row);
+    const uint32_t rr = here ? r : 0;
+    const ShardRow<T> in(s.in[rr], s.ld, row, here ? shard_width(s, rr) : 0);
+    const uint32_t whole = in.end - in.first;
+    const uint32_t j0 = in.first + uint32_t(uint64_t(whole) * part / a.parts), j1 = in.first + uint32_t(uint64_t(whole) * (part + 1) / a.parts);
+    const uint32_t step = a.teams == 1 ? threads : a.team;
+    const int edge = in.edge(tt, part == 0, part + 1 == a.parts);
+
+    // an id first: what it leads to comes a whole latency later
+    int my_id = tid < a.k ? a.ids[row * a.k + tid] : -1;
     uint4 raw[NV];
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-        const uint32_t slot = g0 + tid + n * THREADS;
-        raw[n] = slot < g1 ? load(slot) : make_uint4(low, low, low, low);
+        const uint32_t j = j0 + tt + n * step;
+        raw[n] = j < j1 ? ld_coherent_v4(in.group(j)) : lowest_group<T>();
     }
+    const float edge_z = edge >= 0 ? in.column(edge) : -INFINITY;
 
     // the teacher's entries
     float tm = -INFINITY;
-    for (uint32_t k = tid; k < a.kpad; k += THREADS) {
-        int id = k < a.k ? a.ids[row * a.k + k] : -1;
-        if (uint32_t(id) >= s.vocab) id = -1;
+    for (uint32_t k = tid; k < a.kpad; k += threads) {
+        int id = k == uint32_t(tid) ? my_id : k < a.k ? a.ids[row * a.k + k] : -1;
         float t = -INFINITY, z = 0.0f;
-        if (id >= 0) {
+        if (uint32_t(id) < s.vocab) {
             t = load_any(a.teacher, a.teacher_dtype, row * a.k + k);
-            const uint32_t r = rank_of_token(s, uint32_t(id));
-            const ShardRow sr = in_row(r);
-            const uint32_t at = uint32_t(id) - shard_begin(s, r) + sr.shift;
-            const uint32_t slot = r * s.nv + at / VEC;
-            // an entry of another CTA's columns keeps its id, with the sign bit set
-            if (slot >= g0 && slot < g1) {
-                if (in_bounds(row_ok, s.status, kSiteDistill, id)) z = Tr::load1(reinterpret_cast<const void *>(sr.base), at);
+            const uint32_t ir = rank_of_token(s, uint32_t(id)), c = uint32_t(id) - shard_begin(s, ir);
+            bool mine;
+            if (a.teams == 1) {
+                const uint32_t lo = part == 0 ? 0u : in.head() + (j0 - in.first) * VEC;
+                const uint32_t hi = part + 1 == a.parts ? in.width : in.head() + (j1 - in.first) * VEC;
+                mine = ir == r && c >= lo && c < hi;
             } else {
-                id |= int(0x80000000u);
+                mine = div_by(ir, a.by_teams) == q;
             }
+            if (mine) z = ShardRow<T>(s.in[ir], s.ld, row, shard_width(s, ir)).column(c);
+            else id |= int(0x80000000u);     // another CTA's: only its weight counts here
+        } else {
+            id = -1;
         }
         id_s[k] = id;
         e_s[k] = t;
@@ -132,66 +147,46 @@ __global__ void __launch_bounds__(THREADS) distill_kernel(const __grid_constant_
         tm = fmaxf(tm, t);
     }
 
-    // this thread's maximum and sum; e holds the first NV groups' exponentials
+    // this thread's maximum and sum
     hold_batch(raw);
-    float e[NV * VEC];
-    float m = -INFINITY, sum = 0.0f;
     const float c2 = a.to_log2;
+    const Pair cc = {c2, c2};
+    float m = -INFINITY, sum = 0.0f;
     float row_m = 0.0f, inv = 0.0f;
     if constexpr (FWD) {
+        typename Gr::Max gm = Gr::lowest();
 #pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            float f[VEC];
-            Tr::unpack(raw[n], f);
+        for (int n = 0; n < NV; ++n) gm = Gr::max(gm, raw[n]);
+        m = fmaxf(Gr::value(gm), edge_z);
+        float to = finite_max(m);
+        Pair acc = {ex2((edge_z - to) * c2), 0.0f};
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                e[n * VEC + i] = f[i];
-                m = fmaxf(m, f[i]);
-            }
-        }
-    } else {
-        row_m = finite_max(a.stats[2 * row]);
-        inv = a.stats[2 * row] == -INFINITY ? 0.0f : expf(-a.stats[2 * row + 1]);
+        for (int n = 0; n < NV; ++n)
 #pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            float f[VEC];
-            Tr::unpack(raw[n], f);
+            for (int i = 0; i < PAIRS; ++i) acc = acc + ex2((Gr::pair(raw[n], i) + Pair{-to, -to}) * cc);
+        sum = acc.x + acc.y;
+        for (uint32_t j = j0 + tt + NV * step; j < j1; j += 4 * step) {
+            uint4 more[4];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) e[n * VEC + i] = f[i];
-        }
-    }
-    const float first = m, m0 = FWD ? finite_max(m) : row_m;
-#pragma unroll
-    for (int i = 0; i < NV * VEC; ++i) {
-        e[i] = ex2((e[i] - m0) * c2);
-        if (FWD) sum += e[i];
-    }
-    if constexpr (FWD) {
-        for (uint32_t b = g0 + THREADS * NV; b < g1; b += THREADS * NV) {
-            uint4 more[NV];
-#pragma unroll
-            for (int n = 0; n < NV; ++n) {
-                const uint32_t slot = b + tid + n * THREADS;
-                more[n] = slot < g1 ? load(slot) : make_uint4(low, low, low, low);
-            }
+            for (int n = 0; n < 4; ++n) more[n] = j + n * step < j1 ? ld_coherent_v4(in.group(j + n * step)) : lowest_group<T>();
             hold_batch(more);
-            float bm = m, f[VEC];
+            gm = Gr::lowest();
 #pragma unroll
-            for (int n = 0; n < NV; ++n) {
-                Tr::unpack(more[n], f);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) bm = fmaxf(bm, f[i]);
-            }
-            const float to = finite_max(bm);
-            sum *= ex2((m - to) * c2);       // a thread without anything yet: 0 * 2^-inf
+            for (int n = 0; n < 4; ++n) gm = Gr::max(gm, more[n]);
+            const float bm = fmaxf(m, Gr::value(gm));
+            to = finite_max(bm);
+            acc = {sum * ex2((m - to) * c2), 0.0f};       // a thread without anything yet: 0 * 2^-inf
             m = bm;
 #pragma unroll
-            for (int n = 0; n < NV; ++n) {
-                Tr::unpack(more[n], f);
+            for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) sum += ex2((f[i] - to) * c2);
-            }
+                for (int i = 0; i < PAIRS; ++i) acc = acc + ex2((Gr::pair(more[n], i) + Pair{-to, -to}) * cc);
+            sum = acc.x + acc.y;
         }
+    } else {
+        row_m = a.stats[2 * row];
+        inv = row_m == -INFINITY ? 0.0f : expf(-a.stats[2 * row + 1]);
+        row_m = finite_max(row_m);
     }
 
     // the CTA's maxima
@@ -203,16 +198,13 @@ __global__ void __launch_bounds__(THREADS) distill_kernel(const __grid_constant_
         }
     }
     __syncthreads();
-    float tmax = -INFINITY, cmax = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-        tmax = fmaxf(tmax, red[0][w]);
-        if (FWD) cmax = fmaxf(cmax, red[1][w]);
-    }
-    const float t0 = finite_max(tmax), cm = FWD ? finite_max(cmax) : row_m;
+    const float tmax = warp_max(lane < warps ? red[0][lane] : -INFINITY);
+    const float cmax = FWD ? warp_max(lane < warps ? red[1][lane] : -INFINITY) : 0.0f;
+    const bool taught = tmax != -INFINITY;      // the row has a teacher
+    const float t0 = finite_max(tmax), cm = finite_max(cmax);
     // sums: the teacher's normaliser and sum e (t - tmax) / T; the CTA's part of the row
     float ts = 0.0f, tu = 0.0f, dot = 0.0f, own = 0.0f;
-    for (uint32_t k = tid; k < a.kpad; k += THREADS) {
+    for (uint32_t k = tid; k < a.kpad; k += threads) {
         const float u = (e_s[k] - t0) / a.temperature;
         const int id = id_s[k];
         const float w = id == -1 ? 0.0f : expf(u);
@@ -227,12 +219,15 @@ __global__ void __launch_bounds__(THREADS) distill_kernel(const __grid_constant_
         }
     }
     {
-        const float v0 = warp_sum(ts);
-        float v1 = 0, v2 = 0, v3 = 0, v4 = 0;
+        const bool has = warp * 32 < int(a.kpad);   // only the first warps hold entries
+        const float v0 = has ? warp_sum(ts) : 0.0f;
+        float v1 = 0.0f, v2 = 0.0f, v3 = 0.0f, v4 = 0.0f;
         if constexpr (FWD) {
-            v1 = warp_sum(tu);
-            v2 = warp_sum(dot);
-            v3 = warp_sum(own);
+            if (has) {
+                v1 = warp_sum(tu);
+                v2 = warp_sum(dot);
+                v3 = warp_sum(own);
+            }
             v4 = warp_sum(sum * ex2((m - cm) * c2));
         }
         if (lane == 0) {
@@ -246,89 +241,72 @@ __global__ void __launch_bounds__(THREADS) distill_kernel(const __grid_constant_
         }
     }
     __syncthreads();
+    const float tsum = warp_sum(lane < warps ? red[2][lane] : 0.0f);
     if constexpr (FWD) {
-        if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // every CTA of the row has begun
+        if (a.ctas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // every CTA of the row has begun
         if (warp == 0) {
-            Part v = {cmax, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
-                v.dot += red[4][w];
-                v.own += red[5][w];
-                v.s += red[6][w];
-            }
-            if (lane < int(C)) {
+            const float vd = warp_sum(lane < warps ? red[4][lane] : 0.0f);
+            const float vo = warp_sum(lane < warps ? red[5][lane] : 0.0f);
+            const float vs = warp_sum(lane < warps ? red[6][lane] : 0.0f);
+            if (lane < int(a.ctas)) {
                 uint32_t at;
                 asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(uint32_t(__cvta_generic_to_shared(&parts[q]))), "r"(lane));
-                asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.m), "f"(v.s), "f"(v.dot), "f"(v.own) : "memory");
+                asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(cmax), "f"(vs), "f"(vd), "f"(vo) : "memory");
             }
             __syncwarp();
         }
-        if (C > 1) {
+        if (a.ctas > 1) {
             asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
             asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
         } else {
             __syncthreads();
         }
-    }
-    float tsum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) tsum += red[2][w];
-    const bool taught = tmax != -INFINITY;      // the row has a teacher
-    float mx = -INFINITY, total = 0.0f;
-    if constexpr (FWD) {
-        for (uint32_t c = 0; c < C; ++c) mx = fmaxf(mx, parts[c].x);
+        const float4 mine = lane < int(a.ctas) ? parts[lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
+        const float mx = warp_max(mine.x);
         row_m = finite_max(mx);
-        for (uint32_t c = 0; c < C; ++c) total += parts[c].y * ex2((parts[c].x - row_m) * c2);
+        const float total = warp_sum(mine.y * ex2((mine.x - row_m) * c2));
         inv = total == 0.0f ? 0.0f : 1.0f / total;   // a row of nothing but -inf: p = 0
-        if (q == 0 && tid == 0) {
-            const float ls = logf(total);
-            float d = 0.0f, u = 0.0f;
-            for (uint32_t c = 0; c < C; ++c)
-                if (parts[c].w != 0.0f) d += parts[c].z + parts[c].w * (finite_max(parts[c].x) - row_m);
-            for (int w = 0; w < WARPS; ++w) u += red[3][w];
-            float loss = 0.0f;
-            if (taught) {
-                if (total == 0.0f) loss = INFINITY;
-                else loss = a.temperature * a.temperature * ((u / tsum - logf(tsum)) - (d / a.temperature / tsum - ls));
-            }
-            a.loss[row] = loss;
-            if (a.stats) {
-                a.stats[2 * row] = mx;
-                a.stats[2 * row + 1] = ls;
+        if (q == 0 && warp == 0) {
+            const float d = warp_sum(mine.w != 0.0f ? mine.z + mine.w * (finite_max(mine.x) - row_m) : 0.0f);
+            const float u = warp_sum(lane < warps ? red[3][lane] : 0.0f);
+            if (lane == 0) {
+                const float ls = logf(total);
+                float loss = 0.0f;
+                if (taught) {
+                    if (total == 0.0f) loss = INFINITY;
+                    else loss = a.temperature * a.temperature * ((u / tsum - logf(tsum)) - (d / a.temperature / tsum - ls));
+                }
+                a.loss[row] = loss;
+                if (a.stats) {
+                    a.stats[2 * row] = mx;
+                    a.stats[2 * row + 1] = ls;
+                }
             }
         }
     }
     if constexpr (BWD) {
         const float factor = (a.weight ? a.weight[row] : 1.0f) * a.temperature;
-        const float scale = FWD ? inv * ex2((first - row_m) * c2) : inv;
-        auto store = [&](uint32_t slot, const float (&g)[VEC]) {
-            const uint32_t r = rank_of_slot(s, slot), w = shard_width(s, r);
-            store_group<T>(shard_row<T>(s.out[r], s.ld, row, w), in_row(r), slot - r * s.nv, Tr::pack(g), row_ok, s.status, kSiteDistill);
+        const ShardRow<T> out(s.out[rr], s.ld, row, in.width);
+        const float g = inv * factor;
+        const Pair gg = {g, g}, off = {-row_m, -row_m};
+        auto gradient = [&](const uint4 &v) -> uint4 {
+            if (!taught) return make_uint4(0, 0, 0, 0);
+            Pair p[PAIRS];
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) p[i] = ex2((Gr::pair(v, i) + off) * cc) * gg;
+            return Gr::pack(p);
         };
-        for (uint32_t b = g0 + THREADS * NV; b < g1; b += THREADS * NV) {
-#pragma unroll
-            for (int n = 0; n < NV; ++n) {
-                const uint32_t slot = b + tid + n * THREADS;
-                if (slot >= g1) break;
-                float f[VEC];
-                Tr::unpack(load(slot), f);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) f[i] = taught ? ex2((f[i] - row_m) * c2) * inv * factor : 0.0f;
-                store(slot, f);
-            }
-        }
+        hold_batch(raw);    // the groups stay packed: without this the compiler keeps the unpacked values of the first pass
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            const uint32_t slot = g0 + tid + n * THREADS;
-            if (slot >= g1) break;
-            float f[VEC];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) f[i] = taught ? e[n * VEC + i] * scale * factor : 0.0f;
-            store(slot, f);
+            const uint32_t j = j0 + tt + n * step;
+            if (j < j1) store_group<T>(out, in, j, gradient(raw[n]));
         }
+        for (uint32_t j = j0 + tt + NV * step; j < j1; j += step) store_group<T>(out, in, j, gradient(ld_coherent_v4(in.group(j))));
+        if (edge >= 0) out.set_column(edge, taught ? ex2((edge_z - row_m) * c2) * g : 0.0f);
         __syncthreads();
         if (taught) {
-            for (uint32_t k = tid; k < a.k; k += THREADS) {
+            for (uint32_t k = tid; k < a.k; k += threads) {
                 const int id = id_s[k];
                 if (id < 0) continue;
                 float w = 0.0f;
@@ -341,40 +319,46 @@ __global__ void __launch_bounds__(THREADS) distill_kernel(const __grid_constant_
                     if (o.w == id) { w += e_s[j + 3]; mine = mine && j + 3 >= k; }
                 }
                 if (!mine) continue;
-                const float p = ex2((z_s[k] - row_m) * c2) * inv;
-                const uint32_t r = rank_of_token(s, uint32_t(id));
-                const ShardRow out = shard_row<T>(s.out[r], s.ld, row, shard_width(s, r));
-                if (in_bounds(row_ok, s.status, kSiteDistill, id))
-                    Tr::store1(reinterpret_cast<void *>(out.base), uint64_t(id) - shard_begin(s, r) + out.shift, (p - w / tsum) * factor);
+                const uint32_t ir = rank_of_token(s, uint32_t(id));
+                ShardRow<T>(s.out[ir], s.ld, row, shard_width(s, ir))
+                    .set_column(uint32_t(id) - shard_begin(s, ir), (ex2((z_s[k] - row_m) * c2) * inv - w / tsum) * factor);
             }
         }
     }
 }
 
-template <typename T, int PM, int PASS, int THREADS, int NV>
-static cudaError_t distill_launch(const Launch &L, DistillArgs<PM> &a, uint32_t cluster, LaunchInfo *info)
+template <typename T, int PM, int PASS, int NV, int MIN_CTAS>
+static cudaError_t distill_launch(const Launch &L, DistillArgs<PM> &a, uint32_t need, LaunchInfo *info)
 {
-    a.cluster = cluster;
-    if (a.s.rows * cluster > 0x7fffffffull) return cudaErrorInvalidValue;
+    // threads enough for the need of a CTA, in whole warps per team
+    const uint32_t per_team = (need + NV - 1) / NV, most = kDistillMaxThreads / a.teams;
+    a.team = (per_team < most ? per_team : most) / 32 * 32;
+    if (a.team < per_team && a.team + 32 <= most) a.team += 32;
+    if (a.team < 32) a.team = 32;
+    const uint32_t threads = a.team * a.teams;
+    if (a.s.rows * a.ctas > 0x7fffffffull) return cudaErrorInvalidValue;
+    a.by_ctas = fast_div(a.ctas);
+    a.by_parts = fast_div(a.parts);
+    a.by_teams = fast_div(a.teams);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(a.s.rows * cluster));
-    cfg.blockDim = dim3(THREADS);
+    cfg.gridDim = dim3(unsigned(a.s.rows * a.ctas));
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = size_t(a.kpad) * 12;
     cfg.stream = L.stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.x = a.ctas;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = (PASS & CCL_PASS_FORWARD) && cluster > 1 ? 2 : 1;
-    cudaError_t err = cudaLaunchKernelEx(&cfg, distill_kernel<T, PM, PASS, THREADS, NV>, a);
+    cfg.numAttrs = (PASS & CCL_PASS_FORWARD) && a.ctas > 1 ? 2 : 1;
+    cudaError_t err = cudaLaunchKernelEx(&cfg, distill_kernel<T, PM, PASS, NV, MIN_CTAS>, a);
     if (err != cudaSuccess) return err;
     info->kernel = "distill_topk";
     info->grid = int(cfg.gridDim.x);
-    info->block = THREADS;
+    info->block = int(threads);
     info->smem = cfg.dynamicSmemBytes;
     info->kernels = 1;
     return cudaGetLastError();
@@ -383,7 +367,6 @@ static cudaError_t distill_launch(const Launch &L, DistillArgs<PM> &a, uint32_t 
 template <typename T, int PM, int PASS>
 static cudaError_t distill_shape(const Launch &L, const DistillLaunch &N, LaunchInfo *info)
 {
-    constexpr int NV = 32 / Traits<T>::VEC;   // 32 elements a thread
     DistillArgs<PM> a;
     fill_shards(&a.s, L, N.rows, N.vocab, N.ld);
     a.ids = N.ids;
@@ -396,14 +379,24 @@ static cudaError_t distill_shape(const Launch &L, const DistillLaunch &N, Launch
     a.k = N.k;
     a.kpad = (N.k + 3) / 4 * 4;
     a.teacher_dtype = N.teacher_dtype;
-    a.total = a.s.p * a.s.nv;
-    const uint32_t per = 512 * NV;
-    uint32_t C = (a.total + per - 1) / per;
-    if (N.rows * C < uint64_t(L.num_sms)) {
-        C = (a.total + 127) / 128;
-        return distill_launch<T, PM, PASS, 128, NV>(L, a, C < 1 ? 1 : C > kDistillMaxCluster ? kDistillMaxCluster : C, info);
+    const uint32_t p = a.s.p, groups = widest_groups<T>(a.s);
+    a.teams = (p + kDistillMaxCluster - 1) / kDistillMaxCluster;
+    a.parts = 1;
+    uint32_t need = groups;            // groups a team takes
+    if (a.teams == 1) {
+        // parts: few enough groups a CTA that four per thread hold them, and
+        // CTAs enough for every SM
+        const uint32_t most = PASS == CCL_PASS_BACKWARD ? 64 : kDistillMaxCluster / p, want = 4 * kDistillMaxThreads;
+        while (a.parts < most && ((groups + a.parts - 1) / a.parts > want ||
+                                  (N.rows * p * a.parts < 2 * uint64_t(L.num_sms) && (groups + a.parts - 1) / a.parts > 128)))
+            ++a.parts;
+        need = (groups + a.parts - 1) / a.parts;
     }
-    return distill_launch<T, PM, PASS, 512, NV>(L, a, C < 1 ? 1 : C > kDistillMaxCluster ? kDistillMaxCluster : C, info);
+    a.ctas = a.teams == 1 ? p * a.parts : (p + a.teams - 1) / a.teams;
+    const uint32_t full = need * a.teams;
+    if (full <= 2 * kDistillMaxThreads) return distill_launch<T, PM, PASS, 2, 3>(L, a, need, info);
+    if (PASS != CCL_PASS_BOTH || full <= 4 * kDistillMaxThreads) return distill_launch<T, PM, PASS, 4, 3>(L, a, need, info);
+    return distill_launch<T, PM, PASS, 8, 2>(L, a, need, info);
 }
 
 template <typename T, int PM>
@@ -419,8 +412,7 @@ static cudaError_t distill_pass(const Launch &L, const DistillLaunch &N, LaunchI
 template <typename T>
 static cudaError_t distill_dtype(const Launch &L, const DistillLaunch &N, LaunchInfo *info)
 {
-    return L.p == 1 ? distill_pass<T, 1>(L, N, info) : L.p <= 8 ? distill_pass<T, 8>(L, N, info)
-                                                                : distill_pass<T, kMaxRanks>(L, N, info);
+    return L.p <= kDistillMaxCluster ? distill_pass<T, kDistillMaxCluster>(L, N, info) : distill_pass<T, kMaxRanks>(L, N, info);
 }
 
 cudaError_t launch_distill(const Launch &L, const DistillLaunch &N, LaunchInfo *info)

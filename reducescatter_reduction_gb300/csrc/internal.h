@@ -13,13 +13,16 @@ namespace ccl {
 constexpr int kMaxRanks = 64;
 
 // The device block of a communicator: the status record and tile counters,
-// then (kScratchOffset) the scratch of ccl_balance_loss: a ticket counter that
-// every call leaves at zero, and one pair of partial sums per CTA.
+// then (kScratchOffset) the scratch of ccl_balance_loss: a ticket counter, one
+// pair of partial sums per CTA, and counters (per rank and expert, and per
+// rank) that every call leaves at zero.
 constexpr size_t kCommStatusBytes = 256;
 constexpr size_t kScratchOffset = kCommStatusBytes;
 constexpr size_t kScratchHead = 256;          // the ticket, padded
 constexpr unsigned kMaxPartials = 2048;       // CTAs that may leave a pair of sums
-constexpr size_t kCommDeviceBytes = kScratchOffset + kScratchHead + size_t(kMaxPartials) * 16;
+constexpr unsigned kScratchCells = 16384;     // ranks * experts that the counters hold
+constexpr size_t kCommDeviceBytes =
+    kScratchOffset + kScratchHead + size_t(kMaxPartials) * 16 + size_t(kScratchCells + kMaxRanks) * 4;
 
 enum Op : int { OP_SUM = 0, OP_PROD = 1, OP_MIN = 2, OP_MAX = 3, OP_AVG = 4 };
 enum Dtype : int { DT_F32 = 0, DT_F16 = 1, DT_BF16 = 2, DT_I32 = 3 };
@@ -286,7 +289,7 @@ struct BalanceLaunch {
     int32_t *counts = nullptr;
     int32_t *tokens = nullptr;
     float *loss = nullptr;
-    void *scratch = nullptr;    // the communicator's: kScratchHead bytes, then the partial sums
+    void *scratch = nullptr;    // the communicator's: kScratchHead bytes, the partial sums, the counters
 };
 cudaError_t launch_balance(const Launch &L, const BalanceLaunch &N, LaunchInfo *info);
 

@@ -9,13 +9,14 @@
 //   y = -inf                           if the row's mask has bit v clear
 // in fp32, rounded once to the element type.
 //
-// One CTA per (row, slice of the vocabulary).  It keeps one counter per token
-// of its slice in shared memory, scans the row's history once and counts the
-// tokens that fall into the slice (integer atomics, so any order gives the same counts),
-// adds up the row's bias entries in list order, and then streams its slice:
-// a 16-byte group whose counters and biases are all zero is copied through
-// its mask.  Bytes: the logits once in and once out, plus the history once
-// per slice (L2).
+// One CTA per (row, rank, slice of the rank's columns).  It starts the loads
+// of its groups, then scans the row's history once and counts the tokens that
+// fall into the slice in one counter per column in shared memory (integer
+// atomics, so any order gives the same counts), adds up the row's bias entries
+// in list order, and finishes its groups: a group that neither touches is
+// copied through its mask bits as it is.  A group that its mask forbids
+// altogether is not read, and in place an untouched one is not written.
+// Bytes: the logits once in and once out, plus the history once per slice (L2).
 #include "logits.cuh"
 
 namespace ccl {
@@ -24,90 +25,162 @@ template <int PM>
 struct RulesArgs {
     Shards<PM> s;
     ccl_logit_rules_t r;
-    uint32_t slices;     // per row
-    uint32_t total;      // group slots per row
+    uint32_t slices;            // per rank
+    FastDiv by_row, by_slices;  // CTAs per row, slices per rank
     int in_place;
 };
 
 // Generated occurrences sit above bit 0, bit 0 says "in the prompt".
 constexpr uint32_t kSeenPrompt = 1, kGenerated = 2;
 
+// Clears the lanes of a group that the mask bits forbid to -inf.
+template <typename T>
+__device__ __forceinline__ uint4 forbid(const uint4 &v, uint32_t allowed)
+{
+    const uint32_t low = lowest_group<T>().x;
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (Traits<T>::VEC == 4) {
+            w[i] = (allowed >> i) & 1 ? w[i] : low;
+        } else {
+            const uint32_t keep = ((allowed >> (2 * i)) & 1 ? 0xffffu : 0u) | ((allowed >> (2 * i + 1)) & 1 ? 0xffff0000u : 0u);
+            w[i] = (w[i] & keep) | (low & ~keep);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 template <typename T, int PM, int THREADS, int NV>
 __global__ void __launch_bounds__(THREADS) logit_rules_kernel(const __grid_constant__ RulesArgs<PM> a)
 {
     using Tr = Traits<T>;
-    constexpr int VEC = Tr::VEC;
-    constexpr int SLOTS = THREADS * NV * VEC;
+    constexpr int VEC = Tr::VEC, GROUPS = THREADS * NV;
+    constexpr int CELLS = (GROUPS + 2) * VEC;       // a group's room before and after for the edges
     extern __shared__ uint4 smem4[];
     uint32_t *cnt = reinterpret_cast<uint32_t *>(smem4);
-    float *bias = reinterpret_cast<float *>(cnt + SLOTS);
+    float *bias = reinterpret_cast<float *>(cnt + CELLS);
+    __shared__ uint32_t touched[GROUPS / 32];       // bit g: group g has a counter or a bias
     const Shards<PM> &s = a.s;
-    const uint64_t row = blockIdx.x / a.slices;
-    const uint32_t slice = blockIdx.x % a.slices;
-    const uint32_t g0 = slice * (THREADS * NV), g1 = min(g0 + THREADS * NV, a.total);
-    const bool history = a.r.history != nullptr, biased = a.r.bias_count != 0;
-    const bool row_ok = row < s.rows;
+    const uint32_t row32 = div_by(blockIdx.x, a.by_row), rest = blockIdx.x - row32 * a.by_row.d;
+    const uint32_t rank = div_by(rest, a.by_slices), slice = rest - rank * a.slices;
+    const uint64_t row = row32;
+    const int tid = threadIdx.x;
+    const ShardRow<T> in(s.in[rank], s.ld, row, shard_width(s, rank)), out(s.out[rank], s.ld, row, in.width);
+    const uint32_t whole = in.end - in.first;
+    if (slice > 0 && slice * GROUPS >= whole) return;
+    if (!in_bounds(row < s.rows && rank < s.p, s.status, kSiteRules, row)) return;
+    const uint32_t j0 = in.first + slice * GROUPS, j1 = min(j0 + GROUPS, in.end);
+    const bool has_tail = j1 == in.end;
+    // the slice's columns are [c0, c1); column c has cell c - cell0
+    const uint32_t c0 = slice == 0 ? 0 : in.head() + slice * GROUPS * VEC, c1 = has_tail ? in.width : in.head() + (j1 - in.first) * VEC;
+    const int cell0 = int(in.head() + slice * GROUPS * VEC) - VEC;
+    const uint32_t token0 = shard_begin(s, rank);
+    const int edge = in.edge(tid, slice == 0, has_tail);
 
-    if (history)
-        for (int i = threadIdx.x; i < SLOTS / 4; i += THREADS) reinterpret_cast<uint4 *>(cnt)[i] = make_uint4(0, 0, 0, 0);
-    if (biased)
-        for (int i = threadIdx.x; i < SLOTS / 4; i += THREADS) reinterpret_cast<uint4 *>(bias)[i] = make_uint4(0, 0, 0, 0);
+    const bool history = a.r.history != nullptr;
+    if (tid < GROUPS / 32) touched[tid] = 0;
     grid_dependency_wait();
     grid_dependents_launch();
 
-    // the slice's tokens are [t0, t1): slots run through the ranks in order
-    auto token_at = [&](uint32_t slot) -> uint32_t {   // first token at or after the slot's begin
-        if (slot >= a.total) return s.vocab;
-        const uint32_t r = rank_of_slot(s, slot), w = shard_width(s, r);
-        const int e = group_begin<T>(shard_row<T>(s.in[r], s.ld, row, w), slot - r * s.nv);
-        return shard_begin(s, r) + (e < 0 ? 0u : min(uint32_t(e), w));
-    };
-    const uint32_t t0 = token_at(g0), t1 = token_at(g1);
-    auto slot_of = [&](uint32_t v) -> uint32_t {       // counter of a token of the slice
-        const uint32_t r = rank_of_token(s, v);
-        const ShardRow sr = shard_row<T>(s.in[r], s.ld, row, shard_width(s, r));
-        return (r * s.nv - g0) * VEC + (v - shard_begin(s, r)) + sr.shift;
-    };
-
+    // the row's mask bits of this thread's groups, then their logits
     const uint32_t *mask = nullptr;
-    uint32_t words = (s.vocab + 31) / 32;
+    const uint32_t words = (s.vocab + 31) / 32;
     if (a.r.mask) {
         const int64_t m = a.r.mask_index ? int64_t(a.r.mask_index[row]) : int64_t(row);
         if (m >= 0 && m < int64_t(a.r.mask_rows)) mask = a.r.mask + uint64_t(m) * a.r.mask_ld;
     }
-    __syncthreads();
-    if (history) {
-        const int32_t *h = a.r.history + row * a.r.history_ld;
-        const int64_t ld = int64_t(a.r.history_ld);
-        int64_t len = a.r.history_len ? int64_t(a.r.history_len[row]) : ld;
-        len = len < 0 ? 0 : len > ld ? ld : len;
-        const int64_t prompt = a.r.prompt_len ? int64_t(a.r.prompt_len[row]) : 0;
-        for (int64_t j = threadIdx.x; j < len; j += THREADS) {
-            const uint32_t v = uint32_t(h[j]);
-            if (v - t0 >= t1 - t0) continue;           // also a negative token, or one past the vocabulary
-            uint32_t *c = &cnt[slot_of(v)];
-            if (j < prompt) atomicOr(c, kSeenPrompt);
-            else atomicAdd(c, kGenerated);
+    constexpr uint32_t ALL = (1u << VEC) - 1;
+    uint32_t allowed[NV];
+    uint4 raw[NV];
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const uint32_t j = j0 + tid + n * THREADS;
+        allowed[n] = ALL;
+        if (mask && j < j1) {
+            const uint32_t v = token0 + j * VEC - in.shift, w = v >> 5;
+            const uint32_t lo = mask[w], hi = w + 1 < words ? mask[w + 1] : 0u;
+            allowed[n] = __funnelshift_r(lo, hi, v & 31) & ALL;
         }
     }
-    if (biased && threadIdx.x < 32) {
-        // one warp, 32 entries at a time: entries of one token add in list order
+    auto fetch = [&]() {
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const uint32_t j = j0 + tid + n * THREADS;
+            if (j < j1 && allowed[n]) raw[n] = ld_coherent_v4(in.group(j));
+            else raw[n] = lowest_group<T>();
+        }
+    };
+    if (!a.in_place) fetch();
+    const float edge_x = edge >= 0 ? in.column(edge) : 0.0f;
+
+    int64_t bias_lo = 0, bias_hi = 0;
+    if (a.r.bias_count) {
         const int64_t n = int64_t(a.r.bias_count);
-        int64_t lo = a.r.bias_offsets[row], hi = a.r.bias_offsets[row + 1];
-        lo = lo < 0 ? 0 : lo > n ? n : lo;
-        hi = hi < lo ? lo : hi > n ? n : hi;
-        for (int64_t b = lo; b < hi; b += 32) {
-            const int64_t k = b + threadIdx.x;
-            const uint32_t v = k < hi ? uint32_t(a.r.bias_tokens[k]) : 0xffffffffu;
-            const bool mine = k < hi && v - t0 < t1 - t0;
+        bias_lo = a.r.bias_offsets[row], bias_hi = a.r.bias_offsets[row + 1];
+        bias_lo = bias_lo < 0 ? 0 : bias_lo > n ? n : bias_lo;
+        bias_hi = bias_hi < bias_lo ? bias_lo : bias_hi > n ? n : bias_hi;
+    }
+    const bool biased = bias_hi > bias_lo;
+    int len = 0, prompt = 0;
+    if (history) {
+        const int ld = int(a.r.history_ld);
+        len = a.r.history_len ? a.r.history_len[row] : ld;
+        len = len < 0 ? 0 : len > ld ? ld : len;
+        prompt = a.r.prompt_len ? a.r.prompt_len[row] : 0;
+    }
+    if (len)
+        for (int i = tid; i < CELLS / 4; i += THREADS) reinterpret_cast<uint4 *>(cnt)[i] = make_uint4(0, 0, 0, 0);
+    if (biased)
+        for (int i = tid; i < CELLS / 4; i += THREADS) reinterpret_cast<uint4 *>(bias)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    auto touch = [&](int cell) {
+        const int g = cell / VEC - 1;
+        if (g >= 0 && g < GROUPS) atomicOr(&touched[g / 32], 1u << (g % 32));
+    };
+    if (len) {
+        const int32_t *h = a.r.history + row * a.r.history_ld;
+        auto count = [&](uint32_t token, int j) {
+            const uint32_t c = token - token0;
+            if (c - c0 >= c1 - c0) return;           // another slice's; also a negative token, or one past the vocabulary
+            const int cell = int(c) - cell0;
+            if (j < prompt) atomicOr(&cnt[cell], kSeenPrompt);
+            else atomicAdd(&cnt[cell], kGenerated);
+            touch(cell);
+        };
+        // eight loads in flight a thread
+        constexpr int BATCH = 8;
+        int j = tid;
+        for (; j + (BATCH - 1) * THREADS < len; j += BATCH * THREADS) {
+            int32_t t[BATCH];
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) t[k] = __ldg(h + j + k * THREADS);
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) count(uint32_t(t[k]), j + k * THREADS);
+        }
+        int32_t t[BATCH];
+#pragma unroll
+        for (int k = 0; k < BATCH - 1; ++k) t[k] = j + k * THREADS < len ? __ldg(h + j + k * THREADS) : -1;
+#pragma unroll
+        for (int k = 0; k < BATCH - 1; ++k)
+            if (j + k * THREADS < len) count(uint32_t(t[k]), j + k * THREADS);
+    }
+    if (biased && tid < 32) {
+        // one warp, 32 entries at a time: entries of one token add in list order
+        for (int64_t b = bias_lo; b < bias_hi; b += 32) {
+            const int64_t k = b + tid;
+            const uint32_t c = k < bias_hi ? uint32_t(a.r.bias_tokens[k]) - token0 : 0xffffffffu;
+            const bool mine = k < bias_hi && c - c0 < c1 - c0;
+            if (!__any_sync(0xffffffffu, mine)) continue;
             const float add = mine ? a.r.bias_values[k] : 0.0f;
-            const unsigned same = __match_any_sync(0xffffffffu, mine ? v : 0xffffffffu);
-            const int turn = mine ? __popc(same & ((1u << threadIdx.x) - 1)) : -1;
-            float *at = mine ? &bias[slot_of(v)] : bias;
+            const unsigned same = __match_any_sync(0xffffffffu, mine ? c : 0xffffffffu);
+            const int turn = mine ? __popc(same & ((1u << tid) - 1)) : -1;
+            const int cell = mine ? int(c) - cell0 : 0;
             for (int t = 0; __any_sync(0xffffffffu, turn >= t); ++t) {
-                if (turn == t) *at = __fadd_rn(*at, add);
+                if (turn == t) bias[cell] = __fadd_rn(bias[cell], add);
                 __syncwarp();
             }
+            if (mine) touch(cell);
         }
     }
     __syncthreads();
@@ -115,63 +188,56 @@ __global__ void __launch_bounds__(THREADS) logit_rules_kernel(const __grid_const
     const float rep = a.r.repetition ? a.r.repetition[row] : 1.0f;
     const float freq = a.r.frequency ? a.r.frequency[row] : 0.0f;
     const float pres = a.r.presence ? a.r.presence[row] : 0.0f;
-    constexpr uint32_t ALL = (1u << VEC) - 1;
+    auto apply = [&](float x, int cell) -> float {
+        const uint32_t c = len ? cnt[cell] : 0u;
+        const float b = biased ? bias[cell] : 0.0f;
+        if (b != 0.0f) x = __fadd_rn(x, b);
+        if (c) x = x > 0.0f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
+        if (c >= kGenerated) x = __fsub_rn(__fsub_rn(x, __fmul_rn(freq, float(c >> 1))), pres);
+        return x;
+    };
+    if (a.in_place) fetch();
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
-        const uint32_t local = threadIdx.x + n * THREADS, slot = g0 + local;
-        if (slot >= g1) break;
-        const uint32_t r = rank_of_slot(s, slot), w = shard_width(s, r), j = slot - r * s.nv;
-        const ShardRow in = shard_row<T>(s.in[r], s.ld, row, w), out = shard_row<T>(s.out[r], s.ld, row, w);
-        const int e = group_begin<T>(in, j);
-        if (e >= int(w)) continue;
-        uint32_t allowed = ALL;
-        if (mask) {
-            // bits [v, v + VEC) of the row's mask, two words at most; a bit before the shard's first token is unused
-            const int v = int(shard_begin(s, r)) + e;
-            const uint32_t at = v < 0 ? 0u : uint32_t(v);
-            const uint32_t lo = mask[at >> 5], hi = (at >> 5) + 1 < words ? mask[(at >> 5) + 1] : 0u;
-            allowed = __funnelshift_r(lo, hi, at & 31);
-            if (v < 0) allowed <<= -v;
-            allowed &= ALL;
-        }
-        uint32_t c[VEC], any = 0;
-        float b[VEC];
+        const int g = tid + n * THREADS;
+        const uint32_t j = j0 + g;
+        if (j >= j1) break;
+        uint4 v = raw[n];
+        const bool any = (touched[g / 32] >> (g % 32)) & 1;
+        if (any && allowed[n]) {
+            float x[VEC];
+            Tr::unpack(v, x);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            c[i] = history ? cnt[local * VEC + i] : 0u;
-            b[i] = biased ? bias[local * VEC + i] : 0.0f;
-            any |= c[i] | (b[i] != 0.0f ? 1u : 0u);
+            for (int i = 0; i < VEC; ++i) x[i] = apply(x[i], (g + 1) * VEC + i);
+            v = Tr::pack(x);
+        } else if (a.in_place && allowed[n] == ALL) {
+            continue;
         }
-        if (a.in_place && !any && allowed == ALL) continue;
-        float x[VEC];
-        Tr::unpack(load_group<T>(in, j, row_ok, s.status, kSiteRules), x);
-        if (any) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                if (b[i] != 0.0f) x[i] = __fadd_rn(x[i], b[i]);
-                if (c[i]) x[i] = x[i] > 0.0f ? __fdiv_rn(x[i], rep) : __fmul_rn(x[i], rep);
-                if (c[i] >= kGenerated) x[i] = __fsub_rn(__fsub_rn(x[i], __fmul_rn(freq, float(c[i] >> 1))), pres);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-            if (!((allowed >> i) & 1)) x[i] = -INFINITY;
-        store_group<T>(out, in, j, Tr::pack(x), row_ok, s.status, kSiteRules);
+        if (allowed[n] != ALL) v = forbid<T>(v, allowed[n]);
+        store_group<T>(out, in, j, v);
+    }
+    if (edge >= 0) {
+        const uint32_t v = token0 + edge;
+        const bool ok = !mask || (mask[v >> 5] >> (v & 31)) & 1;
+        out.set_column(edge, ok ? apply(edge_x, edge - cell0) : -INFINITY);
     }
 }
 
 template <typename T, int PM, int THREADS, int NV>
-static cudaError_t rules_launch(const Launch &L, RulesArgs<PM> &a, LaunchInfo *info)
+static cudaError_t rules_launch(const Launch &L, RulesArgs<PM> &a, uint32_t groups, LaunchInfo *info)
 {
     constexpr uint32_t GROUPS = THREADS * NV;
-    constexpr size_t table = size_t(GROUPS) * Traits<T>::VEC * 4;
-    a.slices = (a.total + GROUPS - 1) / GROUPS;
+    constexpr size_t table = size_t(GROUPS + 2) * Traits<T>::VEC * 4;
+    a.slices = groups ? (groups + GROUPS - 1) / GROUPS : 1;
+    const uint64_t per_row = uint64_t(a.slices) * a.s.p;
+    if (a.s.rows * per_row > 0x7fffffffull) return cudaErrorInvalidValue;
+    a.by_row = fast_div(uint32_t(per_row));
+    a.by_slices = fast_div(a.slices);
     const size_t smem = (a.r.bias_count ? 2 : 1) * table;
-    if (a.s.rows * a.slices > 0x7fffffffull) return cudaErrorInvalidValue;
     static std::atomic<unsigned long long> done{0};
     cudaError_t err = allow_dynamic_smem(logit_rules_kernel<T, PM, THREADS, NV>, 2 * table, L.device, done);
     if (err != cudaSuccess) return err;
-    const unsigned grid = unsigned(a.s.rows * a.slices);
+    const unsigned grid = unsigned(a.s.rows * per_row);
     err = launch_dependent(logit_rules_kernel<T, PM, THREADS, NV>, grid, THREADS, smem, L.stream, a);
     if (err != cudaSuccess) return err;
     info->kernel = "logit_rules";
@@ -190,17 +256,15 @@ static cudaError_t rules_shape(const Launch &L, const RulesLaunch &N, LaunchInfo
     fill_shards(&a.s, L, N.rows, N.vocab, N.ld);
     a.r = *N.rules;
     a.in_place = L.alias ? 1 : 0;
-    a.total = a.s.p * a.s.nv;
-    const uint64_t groups = N.rows * uint64_t(a.total);
-    if (groups < uint64_t(L.num_sms) * 1024 * PER16) return rules_launch<T, PM, 128, PER16>(L, a, info);
-    return rules_launch<T, PM, 512, 2 * PER16>(L, a, info);
+    const uint32_t groups = widest_groups<T>(a.s);
+    if (N.rows * a.s.p * uint64_t(groups) < uint64_t(L.num_sms) * 1024 * PER16) return rules_launch<T, PM, 128, PER16>(L, a, groups, info);
+    return rules_launch<T, PM, 512, 2 * PER16>(L, a, groups, info);
 }
 
 template <typename T>
 static cudaError_t rules_dtype(const Launch &L, const RulesLaunch &N, LaunchInfo *info)
 {
-    return L.p == 1 ? rules_shape<T, 1>(L, N, info) : L.p <= 8 ? rules_shape<T, 8>(L, N, info)
-                                                               : rules_shape<T, kMaxRanks>(L, N, info);
+    return L.p <= 8 ? rules_shape<T, 8>(L, N, info) : rules_shape<T, kMaxRanks>(L, N, info);
 }
 
 cudaError_t launch_logit_rules(const Launch &L, const RulesLaunch &N, LaunchInfo *info)

@@ -2,15 +2,14 @@
 // columns of balanced chunk r (the library's chunks: the larger ones first),
 // row-major with a row stride of its own.
 //
-// A row is worked through in 16-byte groups that lie on 16-byte boundaries of
-// memory wherever the row itself begins: group j of a row that begins s
-// elements past a boundary holds columns [j*VEC - s, (j+1)*VEC - s).  Groups
-// that lie wholly inside the row are moved with one 128-bit access, the ones
-// at its two ends element by element, so odd vocabularies, odd strides and
-// unaligned shards run at the speed of aligned ones.  Every rank has the same
-// number nv of group slots (enough for the widest shard at the worst s), so
-// that slot i of a row belongs to rank i / nv; slots past a row's end hold
-// nothing.
+// A shard's row is worked through in 16-byte groups that lie on 16-byte
+// boundaries of memory wherever the row itself begins: the groups that lie
+// wholly inside the row are moved with 128-bit accesses, the elements before
+// the first and after the last of them (fewer than a group each, the "edge")
+// one by one, each by a thread of its own.  So odd vocabularies, odd strides
+// and unaligned shards run at the speed of aligned ones.  A CTA (or a team of
+// its warps) works on one shard, so addresses are uniform and the inner loops
+// hold no arithmetic on ranks.
 #pragma once
 
 #include "device.cuh"
@@ -49,8 +48,7 @@ struct Shards {
     uint64_t rows;
     uint32_t p, vocab;
     uint32_t q, rem;    // widths: q + 1 for the first rem ranks, then q
-    uint32_t nv;        // group slots per rank
-    FastDiv by_nv, by_q1, by_q;
+    FastDiv by_q1, by_q;
     unsigned *status;   // the communicator's status block (checked build)
 };
 
@@ -60,78 +58,102 @@ template <int PM>
 __device__ __forceinline__ uint32_t shard_begin(const Shards<PM> &a, uint32_t r) { return r * a.q + min(r, a.rem); }
 
 template <int PM>
-__device__ __forceinline__ uint32_t rank_of_slot(const Shards<PM> &a, uint32_t slot)
-{
-    return PM == 1 ? 0u : div_by(slot, a.by_nv);
-}
-
-template <int PM>
 __device__ __forceinline__ uint32_t rank_of_token(const Shards<PM> &a, uint32_t v)
 {
-    if constexpr (PM == 1) return 0u;
     const uint32_t big = a.rem * (a.q + 1);
     return v < big ? div_by(v, a.by_q1) : a.rem + div_by(v - big, a.by_q);
 }
 
 // One row of one shard.
+template <typename T>
 struct ShardRow {
-    uintptr_t base;    // the 16-byte boundary at or below the row's first element
-    uint32_t shift;    // elements between the boundary and the row
-    uint32_t width;
+    static constexpr uint32_t VEC = Traits<T>::VEC, S = 16 / VEC;
+    uintptr_t base;      // the 16-byte boundary at or below the row's first element
+    uint32_t shift;      // elements between the boundary and the row
+    uint32_t width;      // columns
+    uint32_t first, end; // its whole groups are [first, end)
+
+    __device__ __forceinline__ ShardRow(const void *buf, uint64_t ld, uint64_t row, uint32_t w)
+    {
+        const uintptr_t at = uintptr_t(buf) + row * (ld ? ld : uint64_t(w)) * S;
+        base = at & ~uintptr_t(15);
+        shift = uint32_t(at & 15) / S;
+        width = w;
+        first = shift ? 1 : 0;
+        end = max(first, (shift + w) / VEC);
+    }
+    __device__ __forceinline__ uint32_t head() const { return min(width, first * VEC - shift); }         // columns before the groups
+    __device__ __forceinline__ uint32_t tail_begin() const { return head() + (end - first) * VEC; }      // first column after them
+    __device__ __forceinline__ const void *group(uint32_t j) const { return reinterpret_cast<const void *>(base + uintptr_t(j) * 16); }
+    __device__ __forceinline__ void *group_out(uint32_t j) const { return reinterpret_cast<void *>(base + uintptr_t(j) * 16); }
+    __device__ __forceinline__ float column(uint32_t c) const { return Traits<T>::load1(reinterpret_cast<const void *>(base), uint64_t(shift) + c); }
+    __device__ __forceinline__ void set_column(uint32_t c, float v) const { Traits<T>::store1(reinterpret_cast<void *>(base), uint64_t(shift) + c, v); }
+    // The edge column of thread t (or -1): t < VEC the head, the next VEC the tail.
+    __device__ __forceinline__ int edge(uint32_t t, bool has_head, bool has_tail) const
+    {
+        if (has_head && t < head()) return int(t);
+        if (has_tail && t >= VEC && t - VEC < width - tail_begin()) return int(tail_begin() + t - VEC);
+        return -1;
+    }
 };
 
+// Stores group j of the input row `in` to the same columns of `out`: one
+// 128-bit store where both rows begin at the same place between boundaries.
 template <typename T>
-__device__ __forceinline__ ShardRow shard_row(const void *buf, uint64_t ld, uint64_t row, uint32_t width)
-{
-    constexpr uint32_t S = 16 / Traits<T>::VEC;
-    const uintptr_t at = uintptr_t(buf) + row * (ld ? ld : uint64_t(width)) * S;
-    return {at & ~uintptr_t(15), uint32_t(at & 15) / S, width};
-}
-
-// Columns [e, e + VEC) of group j; e may be negative, and the end past the row.
-template <typename T>
-__device__ __forceinline__ int group_begin(const ShardRow &r, uint32_t j) { return int(j * Traits<T>::VEC) - int(r.shift); }
-
-template <typename T>
-__device__ __forceinline__ bool group_whole(const ShardRow &r, int e) { return e >= 0 && uint32_t(e) + Traits<T>::VEC <= r.width; }
-
-// Group j's values; columns outside the row read as -inf.
-template <typename T>
-__device__ __forceinline__ uint4 load_group(const ShardRow &r, uint32_t j, bool row_ok, unsigned *status, unsigned site)
+__device__ __forceinline__ void store_group(const ShardRow<T> &out, const ShardRow<T> &in, uint32_t j, const uint4 &v)
 {
     using Tr = Traits<T>;
-    const int e = group_begin<T>(r, j);
-    if (group_whole<T>(r, e) && in_bounds(row_ok, status, site, j))
-        return ld_coherent_v4(reinterpret_cast<const void *>(r.base + uintptr_t(j) * 16));
-    float f[Tr::VEC];
-#pragma unroll
-    for (int i = 0; i < Tr::VEC; ++i) {
-        const bool in = e + i >= 0 && uint32_t(e + i) < r.width;
-        f[i] = in && in_bounds(row_ok, status, site, j) ? Tr::load1(reinterpret_cast<const void *>(r.base), uint64_t(j) * Tr::VEC + i)
-                                                        : -INFINITY;
-    }
-    return Tr::pack(f);
-}
-
-// Stores the columns of input group j (input row `in`) to the same columns of
-// the output row: whole groups with one 128-bit store where both rows begin
-// at the same place between boundaries.
-template <typename T>
-__device__ __forceinline__ void store_group(const ShardRow &out, const ShardRow &in, uint32_t j, const uint4 &v, bool row_ok,
-                                            unsigned *status, unsigned site)
-{
-    using Tr = Traits<T>;
-    const int e = group_begin<T>(in, j);
-    if (out.shift == in.shift && group_whole<T>(in, e)) {
-        if (in_bounds(row_ok, status, site, j)) st_stream_v4(reinterpret_cast<void *>(out.base + uintptr_t(j) * 16), v);
+    if (out.shift == in.shift) {
+        st_stream_v4(out.group_out(j), v);
         return;
     }
     float f[Tr::VEC];
     Tr::unpack(v, f);
+    const uint32_t c = j * Tr::VEC - in.shift;
 #pragma unroll
-    for (int i = 0; i < Tr::VEC; ++i)
-        if (e + i >= 0 && uint32_t(e + i) < in.width && in_bounds(row_ok, status, site, j))
-            Tr::store1(reinterpret_cast<void *>(out.base), uint64_t(out.shift) + uint64_t(e + i), f[i]);
+    for (int i = 0; i < Tr::VEC; ++i) out.set_column(c + i, f[i]);
+}
+
+// Four words of -inf in the element type.
+template <typename T>
+__device__ __forceinline__ uint4 lowest_group()
+{
+    const uint32_t w = Traits<T>::VEC == 4 ? 0xff800000u : Traits<T>::kDtype == DT_BF16 ? 0xff80ff80u : 0xfc00fc00u;
+    return make_uint4(w, w, w, w);
+}
+
+// ---------------------------------------------------------------------------
+// Pairs of fp32 values, which sm_100 and later add and multiply in one
+// instruction.
+// ---------------------------------------------------------------------------
+
+struct Pair {
+    float x, y;
+};
+
+__device__ __forceinline__ Pair operator+(Pair a, Pair b)
+{
+    Pair r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b)
+{
+    Pair r;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ Pair fma(Pair a, Pair b, Pair c)
+{
+    Pair r;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
 }
 
 // 2^x; results below the normal range are zero.
@@ -141,14 +163,83 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ Pair ex2(Pair v) { return {ex2(v.x), ex2(v.y)}; }
+
+// The pairs of a group, the maximum of a group and a running one (a NaN is
+// passed over), and a group from its pairs.
+template <typename T>
+struct Group;
+
+template <>
+struct Group<F32> {
+    static constexpr int PAIRS = 2;
+    using Max = float;
+    __device__ static __forceinline__ Pair pair(const uint4 &v, int i)
+    {
+        return i == 0 ? Pair{__uint_as_float(v.x), __uint_as_float(v.y)} : Pair{__uint_as_float(v.z), __uint_as_float(v.w)};
+    }
+    __device__ static __forceinline__ Max lowest() { return -INFINITY; }
+    __device__ static __forceinline__ Max max(Max m, const uint4 &v)
+    {
+        return fmaxf(m, fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w))));
+    }
+    __device__ static __forceinline__ float value(Max m) { return m; }
+    __device__ static __forceinline__ uint4 pack(const Pair (&p)[2])
+    {
+        return make_uint4(__float_as_uint(p[0].x), __float_as_uint(p[0].y), __float_as_uint(p[1].x), __float_as_uint(p[1].y));
+    }
+};
+
+__device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+
+// 16-bit types compare two lanes at a time, in the type itself: widening keeps the order.
+template <typename T, typename H2>
+struct Group16 {
+    static constexpr int PAIRS = 4;
+    using Max = H2;
+    __device__ static __forceinline__ H2 h2(uint32_t w) { return *reinterpret_cast<const H2 *>(&w); }
+    __device__ static __forceinline__ Max lowest() { return h2(lowest_group<T>().x); }
+    __device__ static __forceinline__ Max max(Max m, const uint4 &v)
+    {
+        return __hmax2(m, __hmax2(__hmax2(h2(v.x), h2(v.y)), __hmax2(h2(v.z), h2(v.w))));
+    }
+    __device__ static __forceinline__ uint4 pack(const Pair (&p)[4])
+    {
+        using Tr = Traits<T>;
+        return make_uint4(Tr::pack2(p[0].x, p[0].y), Tr::pack2(p[1].x, p[1].y), Tr::pack2(p[2].x, p[2].y), Tr::pack2(p[3].x, p[3].y));
+    }
+};
+
+template <>
+struct Group<BF16> : Group16<BF16, __nv_bfloat162> {
+    __device__ static __forceinline__ Pair pair(const uint4 &v, int i)
+    {
+        const uint32_t w = word(v, i);
+        return {__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)};
+    }
+    __device__ static __forceinline__ float value(Max m) { return fmaxf(__low2float(m), __high2float(m)); }
+};
+
+template <>
+struct Group<F16> : Group16<F16, __half2> {
+    __device__ static __forceinline__ Pair pair(const uint4 &v, int i)
+    {
+        const float2 f = __half22float2(h2(word(v, i)));
+        return {f.x, f.y};
+    }
+    __device__ static __forceinline__ float value(Max m) { return fmaxf(__low2float(m), __high2float(m)); }
+};
+
+// A maximum of nothing but -inf: differences are formed against 0 instead, so
+// that their exponentials are 0 and not NaN.
+__device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0.0f : m; }
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Host: fills everything but the pointers' aliases checks have established.
 template <int PM>
 inline void fill_shards(Shards<PM> *s, const Launch &L, uint64_t rows, uint32_t vocab, uint64_t ld)
 {
-    const uint32_t p = uint32_t(L.p), es = uint32_t(elem_bytes(L.dtype)), vec = 16 / es;
+    const uint32_t p = uint32_t(L.p);
     for (uint32_t r = 0; r < p; ++r) {
         s->in[r] = L.src[r];
         s->out[r] = L.dst[r];
@@ -159,17 +250,13 @@ inline void fill_shards(Shards<PM> *s, const Launch &L, uint64_t rows, uint32_t 
     s->vocab = vocab;
     s->q = vocab / p;
     s->rem = vocab % p;
-    const uint32_t wide = s->q + (s->rem ? 1 : 0);
-    bool aligned = true;
-    for (uint32_t r = 0; r < p; ++r) {
-        const uint64_t stride = (ld ? ld : s->q + (r < s->rem ? 1 : 0)) * es;
-        aligned = aligned && uintptr_t(L.src[r]) % 16 == 0 && (rows == 1 || stride % 16 == 0);
-    }
-    s->nv = (wide + (aligned ? 0 : vec - 1) + vec - 1) / vec;
-    s->by_nv = fast_div(s->nv);
     s->by_q1 = fast_div(s->q + 1);
     s->by_q = fast_div(s->q ? s->q : 1);
     s->status = L.status;
 }
+
+// The most whole groups a row of the widest shard has.
+template <typename T, int PM>
+inline uint32_t widest_groups(const Shards<PM> &s) { return (s.q + (s.rem ? 1 : 0)) / Traits<T>::VEC; }
 
 }  // namespace ccl
