@@ -5,32 +5,64 @@
 // p = softmax(z / T) over the student's vocabulary:
 //   loss = T^2 sum_k q_k (log q_k - log p_{id_k})
 //   dz_v = w T (p_v - sum over the k with id_k = v of q_k)
-// A cluster of C CTAs takes a row.  Up to eight ranks, a CTA takes one of
-// `parts` parts of one rank's shard; beyond, `teams` teams of its warps take
-// one shard each.  Every thread reads its 16-byte groups once and keeps the
-// first NV of them in registers as they are (16-bit types: two elements per
-// register), takes the exponentials against its own maximum, and after the
-// exchange of (max, sum, the teacher's share of the loss) between the CTAs
-// takes them again against the row's maximum and stores the gradient: the
-// logits are read once and the gradient is written once, 2 R V s bytes.
-// Keeping the exponentials instead would take twice the registers and halve
-// the CTAs per SM; exponentials are the cheaper of the two.  Groups past the
-// first NV per thread are read a second time.  The teacher's entries are then
-// put right one by one: after the CTA's barrier, the thread of an entry's
-// first occurrence stores the gradient of that token with the teacher's share
-// taken off.
 //
-// The CTAs of a row exchange their sums by writing them into one another's
-// shared memory before the cluster's hardware barrier; every CTA adds the
-// same C values in the same order, so all parts of a row use the same bits.
+// A row is cut into Q pieces, each a part of one rank's shard (beyond 16
+// ranks: several whole shards), and a persistent CTA takes one piece of one
+// row after another.  Where the loss is computed the Q CTAs of a row form a
+// cluster and go through the rows together.  Ten warps, tied together by
+// mbarriers alone:
+//
+//   warp 8 (loads and patches)  brings the 16-byte groups of the piece of a
+//                               coming row into a stage of shared memory with
+//                               one bulk copy per shard, its edge elements and
+//                               where they go beside it, S stages ahead
+//   warp 9 (teacher)            softmax of the row's teacher entries, the
+//                               student's logits at those in the piece, and
+//                               their share of the loss
+//   warps 0-7 (consumers)       take a stage into registers and free it;
+//                               exponentials against the thread's own maximum,
+//                               (max, sum) per warp to every CTA of the row;
+//                               from all of them the row's maximum and sum;
+//                               scale the exponentials into the gradient and
+//                               store it
+//   warp 8 again                stores the gradient at the teacher's tokens
+//                               once the consumers' stores are out, each
+//                               token by its first entry
+//
+// So the logits are read once, the gradient is written once, each element
+// costs one exponential, and while a row's sums travel the next rows' loads
+// are in flight.  What the CTAs tell one another goes into double-buffered
+// slots with st.async and is counted by the receiver's mbarrier; every CTA
+// adds the same values in the same order, so all pieces of a row use the same
+// bits.  A sender is at most one row ahead of any receiver: its sums for row
+// k + 1 leave only after the whole row k has reached it.
+//
+// A piece beyond 2048 groups (vocabularies above 262144 16-bit or 131072
+// 32-bit columns on up to 16 ranks a power of two) is taken in chunks: the
+// sums go through them once, the gradient reads them a second time.
+//
 // Differences z - m are formed before the scaling by 1 / T, so that masks of
 // the type's lowest value do not turn into inf - inf.
+//
+// Every wait is bounded by the communicator's wait limit; one that gives up
+// records itself in the status block, and the CTA leaves its loops, waits
+// (bounded) for its copies in flight and for the other CTAs of the row, and
+// returns.
+#include "async.cuh"
 #include "logits.cuh"
 
 namespace ccl {
 
-constexpr int kDistillMaxCluster = 8;
-constexpr int kDistillMaxThreads = 512;
+constexpr int kDistillConsumers = 256;
+constexpr int kDistillWarps = kDistillConsumers / 32;
+constexpr int kDistillThreads = kDistillConsumers + 64;
+constexpr int kDistillGroups = 8;                                      // groups a consumer keeps
+constexpr uint32_t kDistillStage = kDistillConsumers * kDistillGroups; // groups of a stage
+constexpr uint32_t kDistillStageBytes = kDistillStage * 16;
+constexpr int kDistillMaxCluster = 16;
+constexpr int kDistillMaxSegments = 4;                                 // shards of a piece: 64 ranks in 16 CTAs
+constexpr uint32_t kDistillMaxStages = 3;
+constexpr size_t kDistillSmem = 113 * 1024;                            // two CTAs per SM
 
 template <int PM>
 struct DistillArgs {
@@ -43,12 +75,47 @@ struct DistillArgs {
     float temperature;
     float to_log2;        // log2(e) / T
     uint32_t k, kpad;
-    uint32_t ctas;        // per row
-    uint32_t parts;       // parts of a shard (teams == 1), else 1
-    uint32_t teams;       // shards per CTA
-    uint32_t team;        // threads of a team
-    FastDiv by_ctas, by_parts, by_teams;
+    uint32_t pieces;      // per row
+    uint32_t parts;       // parts of a shard (one shard a piece), else 1
+    uint32_t segments;    // shards of a piece
+    uint32_t chunks;      // of a piece
+    uint32_t stages;
+    uint32_t items;       // rows * pieces
+    FastDiv by_pieces, by_parts, by_segments;
     int teacher_dtype;
+    long long wait_ns;
+    int stall_test;       // 1: the second load of every CTA is withheld, so that a wait runs out (tests)
+};
+
+// Where a stage's groups and edge elements go.
+struct DistillDesc {
+    struct Segment {
+        uint64_t out;          // address of the output of its first group
+        uint32_t first;        // its first group in the stage
+        uint32_t aligned;      // the output's groups lie on 16-byte boundaries too
+    } seg[kDistillMaxSegments];
+    uint64_t edge_out[kDistillMaxSegments * 16];   // address of an edge element's output, 0: no such element
+    float edge[kDistillMaxSegments * 16];
+    uint32_t groups;
+};
+
+// What reaches a CTA from the CTAs of its row.
+struct DistillSums {
+    float2 warp[kDistillMaxCluster][kDistillWarps];   // max, sum
+    float4 teacher[kDistillMaxCluster][2];            // reference, sum e (z - reference), sum e here, sum e | sum e (t - tmax) / T, weight
+};
+constexpr uint32_t kDistillSumBytes = kDistillWarps * 8 + 32;   // from one CTA
+
+struct DistillShared {
+    DistillSums sums[2];
+    DistillDesc desc[kDistillMaxStages + 1];
+    uint64_t full[kDistillMaxStages], empty[kDistillMaxStages];
+    uint64_t sums_in[2], taught[2], taught_free[2], stored[2];
+    uint32_t entries[2];                              // the piece's teacher entries
+    float teacher_sum[2];
+    float weight[2], row_max[2], row_log_sum[2];      // of the row (the latter two for a gradient alone)
+    float used_max[2], used_inv[2];                   // what the consumers scaled by
+    int dead;
 };
 
 __device__ __forceinline__ float warp_max(float v)
@@ -69,299 +136,602 @@ __device__ __forceinline__ float load_any(const void *p, int dtype, uint64_t i)
     return dtype == DT_F32 ? Traits<F32>::load1(p, i) : dtype == DT_F16 ? Traits<F16>::load1(p, i) : Traits<BF16>::load1(p, i);
 }
 
-template <typename T, int PM, int PASS, int NV, int MIN_CTAS>
-__global__ void __launch_bounds__(kDistillMaxThreads, MIN_CTAS) distill_kernel(const __grid_constant__ DistillArgs<PM> a)
+__device__ __forceinline__ uint32_t remote(uint32_t local, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(local), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ void send2(uint32_t at, uint32_t bar, float x, float y)
+{
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];" ::"r"(at), "r"(__float_as_uint(x)),
+                 "r"(__float_as_uint(y)), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void send4(uint32_t at, uint32_t bar, float4 v)
+{
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(at),
+                 "r"(__float_as_uint(v.x)), "r"(__float_as_uint(v.y)), "r"(__float_as_uint(v.z)), "r"(__float_as_uint(v.w)), "r"(bar)
+                 : "memory");
+}
+
+// Values that other CTAs wrote: cluster scope.
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Waits for a phase, bounded; false if the wait, or any wait of this CTA, gave up.
+template <int PM>
+__device__ __forceinline__ bool distill_wait(const DistillArgs<PM> &a, DistillShared &sh, uint64_t *barrier, uint32_t parity, unsigned code,
+                                             uint32_t item)
+{
+    const uint32_t bar = smem_addr(barrier);
+    if (try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = global_ns();
+    volatile int *dead = &sh.dead;
+    while (!try_wait_cluster(bar, parity)) {
+        if (*dead) return false;
+        if (global_ns() - t0 > uint64_t(a.wait_ns)) {
+            if (atomicCAS(&a.s.status[0], 0u, code) == 0u) {
+                a.s.status[1] = blockIdx.x;
+                a.s.status[2] = item;
+                a.s.status[3] = threadIdx.x;
+            }
+            *dead = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
+// The part of shard `rank` that piece q of a row takes.
+template <typename T, int PM>
+struct Piece {
+    uint32_t rank, part;
+    uint32_t per;          // groups of a part
+    uint32_t j0, j1;       // its groups
+
+    __device__ __forceinline__ Piece(const DistillArgs<PM> &a, uint32_t q, uint32_t seg)
+    {
+        if (a.segments == 1) {
+            rank = div_by(q, a.by_parts);
+            part = q - rank * a.parts;
+        } else {
+            rank = q * a.segments + seg;
+            part = 0;
+        }
+    }
+    __device__ __forceinline__ void cut(const DistillArgs<PM> &a, const ShardRow<T> &row)
+    {
+        const uint32_t whole = row.end - row.first;
+        per = div_by(whole + a.parts - 1, a.by_parts);
+        j0 = row.first + min(whole, per * part);
+        j1 = row.first + min(whole, per * (part + 1));
+    }
+};
+
+template <typename T, int PM, int PASS>
+__global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __grid_constant__ DistillArgs<PM> a)
 {
     using Tr = Traits<T>;
     using Gr = Group<T>;
-    constexpr int VEC = Tr::VEC, PAIRS = Gr::PAIRS, MAX_WARPS = kDistillMaxThreads / 32;
+    constexpr int VEC = Tr::VEC, PAIRS = Gr::PAIRS, NG = kDistillGroups;
     constexpr bool FWD = PASS & CCL_PASS_FORWARD, BWD = PASS & CCL_PASS_BACKWARD;
-    extern __shared__ uint4 smem4[];
-    int *id_s = reinterpret_cast<int *>(smem4);                    // ids, negative where not in this CTA's columns
-    float *e_s = reinterpret_cast<float *>(id_s + a.kpad);         // exp((t - tmax) / T)
-    float *z_s = e_s + a.kpad;                                     // the student's logits at the ids in these columns
-    __shared__ float red[7][MAX_WARPS];
-    __shared__ float4 parts[kDistillMaxCluster];                   // max, sum, teacher's dot, teacher's weight of a CTA
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ DistillShared sh;
     const Shards<PM> &s = a.s;
-    const uint32_t row32 = div_by(blockIdx.x, a.by_ctas), q = blockIdx.x - row32 * a.ctas;
-    const uint64_t row = row32;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    const int threads = blockDim.x, warps = threads / 32;
-    if (FWD && a.ctas > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    const uint32_t S = a.stages;
+    // behind the stages: two slots of the piece's teacher entries (ids, exp((t - tmax) / T), logits), and the room of
+    // the teacher's warp for what its registers do not hold
+    int *id_s = reinterpret_cast<int *>(smem + size_t(S) * kDistillStageBytes);
+    float *e_s = reinterpret_cast<float *>(id_s + 2 * a.kpad), *z_s = e_s + 2 * a.kpad;
+    int *more_id = reinterpret_cast<int *>(z_s + 2 * a.kpad);
+    float *more_e = reinterpret_cast<float *>(more_id + a.kpad), *more_z = more_e + a.kpad;
+
+    if (tid == 0) {
+        for (uint32_t i = 0; i < S; ++i) {
+            mbar_init(smem_addr(&sh.full[i]), 1);
+            mbar_init(smem_addr(&sh.empty[i]), kDistillWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&sh.sums_in[i]), 1);
+            mbar_init(smem_addr(&sh.taught[i]), 1);
+            mbar_init(smem_addr(&sh.taught_free[i]), 1);
+            mbar_init(smem_addr(&sh.stored[i]), kDistillWarps);
+        }
+        sh.dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    if (FWD) {
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    }
     grid_dependency_wait();
     grid_dependents_launch();
 
-    // this team's shard and part
-    uint32_t r, part = 0, tt = tid;
-    if (a.teams == 1) {
-        r = div_by(q, a.by_parts);
-        part = q - r * a.parts;
-    } else {
-        const uint32_t team = tid / a.team;
-        r = q * a.teams + team;
-        tt = tid - team * a.team;
-        if (r >= s.p || team >= a.teams) r = s.p;
-    }
-    const bool here = r < s.p && in_bounds(row < s.rows, s.status, kSiteDistill, row);
-    const uint32_t rr = here ? r : 0;
-    const ShardRow<T> in(s.in[rr], s.ld, row, here ? shard_width(s, rr) : 0);
-    const uint32_t whole = in.end - in.first;
-    const uint32_t j0 = in.first + uint32_t(uint64_t(whole) * part / a.parts), j1 = in.first + uint32_t(uint64_t(whole) * (part + 1) / a.parts);
-    const uint32_t step = a.teams == 1 ? threads : a.team;
-    const int edge = in.edge(tt, part == 0, part + 1 == a.parts);
+    // chunks that an item loads: a piece of several is read once for the sums and once for the gradient
+    const uint32_t loads = PASS == CCL_PASS_BOTH && a.chunks > 1 ? 2 * a.chunks : a.chunks;
+    const uint32_t stride = gridDim.x;
+    uint32_t issued = 0;
 
-    // an id first: what it leads to comes a whole latency later
-    int my_id = tid < a.k ? a.ids[row * a.k + tid] : -1;
-    uint4 raw[NV];
-#pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const uint32_t j = j0 + tt + n * step;
-        raw[n] = j < j1 ? ld_coherent_v4(in.group(j)) : lowest_group<T>();
-    }
-    const float edge_z = edge >= 0 ? in.column(edge) : -INFINITY;
-
-    // the teacher's entries
-    float tm = -INFINITY;
-    for (uint32_t k = tid; k < a.kpad; k += threads) {
-        int id = k == uint32_t(tid) ? my_id : k < a.k ? a.ids[row * a.k + k] : -1;
-        float t = -INFINITY, z = 0.0f;
-        if (uint32_t(id) < s.vocab) {
-            t = load_any(a.teacher, a.teacher_dtype, row * a.k + k);
-            const uint32_t ir = rank_of_token(s, uint32_t(id)), c = uint32_t(id) - shard_begin(s, ir);
-            bool mine;
-            if (a.teams == 1) {
-                const uint32_t lo = part == 0 ? 0u : in.head() + (j0 - in.first) * VEC;
-                const uint32_t hi = part + 1 == a.parts ? in.width : in.head() + (j1 - in.first) * VEC;
-                mine = ir == r && c >= lo && c < hi;
-            } else {
-                mine = div_by(ir, a.by_teams) == q;
+    if (warp == kDistillWarps) {
+        // ---- loads, and the gradient at the teacher's tokens -------------
+        const uint32_t count = (a.items - blockIdx.x + stride - 1) / stride;   // items of this CTA: at least one
+        uint32_t item = blockIdx.x, load = 0;                                  // the next to issue
+        auto issue = [&]() -> bool {
+            const uint32_t st = issued % S;
+            if (issued >= S && !__all_sync(0xffffffffu, distill_wait(a, sh, &sh.empty[st], (issued / S - 1) & 1, 6, item))) return false;
+            DistillDesc &d = sh.desc[issued % (S + 1)];
+            const uint32_t row = div_by(item, a.by_pieces), q = item - row * a.pieces, c = load % a.chunks;
+            const uint32_t cap = a.segments == 1 ? kDistillStage : div_by(kDistillStage, a.by_segments);
+            // lane l: segment l
+            uint32_t n = 0;
+            const void *from = nullptr;
+            Piece<T, PM> pc(a, q, lane);
+            if (lane < int(a.segments) && pc.rank < s.p) {
+                const ShardRow<T> in(s.in[pc.rank], s.ld, row, shard_width(s, pc.rank));
+                pc.cut(a, in);
+                const uint32_t k0 = min(pc.j0 + c * cap, pc.j1), k1 = min(k0 + cap, pc.j1);
+                if (in_bounds(row < s.rows && k1 <= in.end, s.status, kSiteDistill, row)) n = k1 - k0;
+                from = in.group(k0);
+                if (BWD) {
+                    const ShardRow<T> out(s.out[pc.rank], s.ld, row, in.width);
+                    const uintptr_t at = out.base + (uint64_t(out.shift) + k0 * VEC - in.shift) * (16 / VEC);
+                    d.seg[lane].out = at;
+                    d.seg[lane].aligned = at % 16 == 0;
+                }
             }
-            if (mine) z = ShardRow<T>(s.in[ir], s.ld, row, shard_width(s, ir)).column(c);
-            else id |= int(0x80000000u);     // another CTA's: only its weight counts here
-        } else {
-            id = -1;
-        }
-        id_s[k] = id;
-        e_s[k] = t;
-        z_s[k] = z;
-        tm = fmaxf(tm, t);
-    }
-
-    // this thread's maximum and sum
-    hold_batch(raw);
-    const float c2 = a.to_log2;
-    const Pair cc = {c2, c2};
-    float m = -INFINITY, sum = 0.0f;
-    float row_m = 0.0f, inv = 0.0f;
-    if constexpr (FWD) {
-        typename Gr::Max gm = Gr::lowest();
+            uint32_t first = 0, all = 0;
 #pragma unroll
-        for (int n = 0; n < NV; ++n) gm = Gr::max(gm, raw[n]);
-        m = fmaxf(Gr::value(gm), edge_z);
-        float to = finite_max(m);
-        Pair acc = {ex2((edge_z - to) * c2), 0.0f};
-#pragma unroll
-        for (int n = 0; n < NV; ++n)
-#pragma unroll
-            for (int i = 0; i < PAIRS; ++i) acc = acc + ex2((Gr::pair(raw[n], i) + Pair{-to, -to}) * cc);
-        sum = acc.x + acc.y;
-        for (uint32_t j = j0 + tt + NV * step; j < j1; j += 4 * step) {
-            uint4 more[4];
-#pragma unroll
-            for (int n = 0; n < 4; ++n) more[n] = j + n * step < j1 ? ld_coherent_v4(in.group(j + n * step)) : lowest_group<T>();
-            hold_batch(more);
-            gm = Gr::lowest();
-#pragma unroll
-            for (int n = 0; n < 4; ++n) gm = Gr::max(gm, more[n]);
-            const float bm = fmaxf(m, Gr::value(gm));
-            to = finite_max(bm);
-            acc = {sum * ex2((m - to) * c2), 0.0f};       // a thread without anything yet: 0 * 2^-inf
-            m = bm;
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int i = 0; i < PAIRS; ++i) acc = acc + ex2((Gr::pair(more[n], i) + Pair{-to, -to}) * cc);
-            sum = acc.x + acc.y;
-        }
-    } else {
-        row_m = a.stats[2 * row];
-        inv = row_m == -INFINITY ? 0.0f : expf(-a.stats[2 * row + 1]);
-        row_m = finite_max(row_m);
-    }
-
-    // the CTA's maxima
-    {
-        const float wt = warp_max(tm), wm = FWD ? warp_max(m) : 0.0f;
-        if (lane == 0) {
-            red[0][warp] = wt;
-            red[1][warp] = wm;
-        }
-    }
-    __syncthreads();
-    const float tmax = warp_max(lane < warps ? red[0][lane] : -INFINITY);
-    const float cmax = FWD ? warp_max(lane < warps ? red[1][lane] : -INFINITY) : 0.0f;
-    const bool taught = tmax != -INFINITY;      // the row has a teacher
-    const float t0 = finite_max(tmax), cm = finite_max(cmax);
-    // sums: the teacher's normaliser and sum e (t - tmax) / T; the CTA's part of the row
-    float ts = 0.0f, tu = 0.0f, dot = 0.0f, own = 0.0f;
-    for (uint32_t k = tid; k < a.kpad; k += threads) {
-        const float u = (e_s[k] - t0) / a.temperature;
-        const int id = id_s[k];
-        const float w = id == -1 ? 0.0f : expf(u);
-        e_s[k] = w;
-        ts += w;
-        if (FWD && w != 0.0f) {
-            tu += w * u;
-            if (id >= 0) {
-                dot += w * (z_s[k] - cm);
-                own += w;
+            for (int l = 0; l < kDistillMaxSegments; ++l) {
+                const uint32_t m = __shfl_sync(0xffffffffu, n, l);
+                if (l < lane) first += m;
+                all += m;
             }
-        }
-    }
-    {
-        const bool has = warp * 32 < int(a.kpad);   // only the first warps hold entries
-        const float v0 = has ? warp_sum(ts) : 0.0f;
-        float v1 = 0.0f, v2 = 0.0f, v3 = 0.0f, v4 = 0.0f;
-        if constexpr (FWD) {
-            if (has) {
-                v1 = warp_sum(tu);
-                v2 = warp_sum(dot);
-                v3 = warp_sum(own);
+            const bool held = a.stall_test == 1 && issued == 1;
+            const uint32_t bar = smem_addr(&sh.full[st]);
+            if (n && !held) bulk_load(smem_addr(smem) + st * kDistillStageBytes + first * 16, from, n * 16, bar);
+            if (lane < int(a.segments)) d.seg[lane].first = first;
+            // edges: thread e of a segment, as ShardRow::edge numbers them
+            for (uint32_t e = lane; e < a.segments * 2 * VEC; e += 32) {
+                const uint32_t g = e / (2 * VEC);
+                Piece<T, PM> pe(a, q, g);
+                uint64_t to = 0;
+                float z = -INFINITY;
+                if (pe.rank < s.p) {
+                    const ShardRow<T> in(s.in[pe.rank], s.ld, row, shard_width(s, pe.rank));
+                    const int col = in.edge(e % (2 * VEC), pe.part == 0 && c == 0, pe.part + 1 == a.parts && c + 1 == a.chunks);
+                    if (col >= 0 && in_bounds(row < s.rows, s.status, kSiteDistill, row)) {
+                        z = in.column(col);
+                        const ShardRow<T> out(s.out[pe.rank], s.ld, row, in.width);
+                        to = out.base + (uint64_t(out.shift) + uint32_t(col)) * (16 / VEC);
+                    }
+                }
+                d.edge[e] = z;
+                d.edge_out[e] = to;
             }
-            v4 = warp_sum(sum * ex2((m - cm) * c2));
-        }
-        if (lane == 0) {
-            red[2][warp] = v0;
-            if constexpr (FWD) {
-                red[3][warp] = v1;
-                red[4][warp] = v2;
-                red[5][warp] = v3;
-                red[6][warp] = v4;
-            }
-        }
-    }
-    __syncthreads();
-    const float tsum = warp_sum(lane < warps ? red[2][lane] : 0.0f);
-    if constexpr (FWD) {
-        if (a.ctas > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // every CTA of the row has begun
-        if (warp == 0) {
-            const float vd = warp_sum(lane < warps ? red[4][lane] : 0.0f);
-            const float vo = warp_sum(lane < warps ? red[5][lane] : 0.0f);
-            const float vs = warp_sum(lane < warps ? red[6][lane] : 0.0f);
-            if (lane < int(a.ctas)) {
-                uint32_t at;
-                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(uint32_t(__cvta_generic_to_shared(&parts[q]))), "r"(lane));
-                asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(cmax), "f"(vs), "f"(vd), "f"(vo) : "memory");
-            }
+            if (lane == 0) d.groups = all;
             __syncwarp();
-        }
-        if (a.ctas > 1) {
-            asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-            asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-        } else {
-            __syncthreads();
-        }
-        const float4 mine = lane < int(a.ctas) ? parts[lane] : make_float4(-INFINITY, 0.0f, 0.0f, 0.0f);
-        const float mx = warp_max(mine.x);
-        row_m = finite_max(mx);
-        const float total = warp_sum(mine.y * ex2((mine.x - row_m) * c2));
-        inv = total == 0.0f ? 0.0f : 1.0f / total;   // a row of nothing but -inf: p = 0
-        if (q == 0 && warp == 0) {
-            const float d = warp_sum(mine.w != 0.0f ? mine.z + mine.w * (finite_max(mine.x) - row_m) : 0.0f);
-            const float u = warp_sum(lane < warps ? red[3][lane] : 0.0f);
-            if (lane == 0) {
-                const float ls = logf(total);
-                float loss = 0.0f;
-                if (taught) {
-                    if (total == 0.0f) loss = INFINITY;
-                    else loss = a.temperature * a.temperature * ((u / tsum - logf(tsum)) - (d / a.temperature / tsum - ls));
+            if (lane == 0 && !held) mbar_arrive_expect_tx(bar, all * 16);
+            ++issued;
+            if (++load == loads) {
+                load = 0;
+                item += stride;
+            }
+            return true;
+        };
+        const uint32_t every = count * loads;
+        bool ok = true;
+        uint32_t row_item = blockIdx.x;
+        for (uint32_t k = 0; k < count && ok; ++k, row_item += stride) {
+            // all of this item's loads, and S - 1 beyond: the last of them waits for the stage before this item's last
+            const uint64_t until = uint64_t(k + 1) * loads + S - 1;
+            while (ok && issued < every && issued < until) ok = issue();
+            if constexpr (BWD) {
+                const uint32_t slot = k & 1, parity = (k >> 1) & 1;
+                ok = ok && __all_sync(0xffffffffu, distill_wait(a, sh, &sh.taught[slot], parity, 7, row_item));
+                ok = ok && __all_sync(0xffffffffu, distill_wait(a, sh, &sh.stored[slot], parity, 7, row_item));
+                if (!ok) break;
+                const float tsum = sh.teacher_sum[slot], row_m = sh.used_max[slot], inv = sh.used_inv[slot];
+                const float factor = sh.weight[slot] * a.temperature;
+                const uint32_t row = div_by(row_item, a.by_pieces), n = sh.entries[slot];
+                const int *ids = id_s + slot * a.kpad;
+                const float *es = e_s + slot * a.kpad, *zs = z_s + slot * a.kpad;
+                for (uint32_t i = lane; i < n; i += 32) {
+                    const int id = ids[i];
+                    float w = 0.0f;
+                    bool mine = true;      // the token's first entry stores for all of them
+                    for (uint32_t j = 0; j < n; j += 4) {
+                        const int4 o = *reinterpret_cast<const int4 *>(&ids[j]);
+                        if (o.x == id) { w += es[j]; mine = mine && j >= i; }
+                        if (o.y == id) { w += es[j + 1]; mine = mine && j + 1 >= i; }
+                        if (o.z == id) { w += es[j + 2]; mine = mine && j + 2 >= i; }
+                        if (o.w == id) { w += es[j + 3]; mine = mine && j + 3 >= i; }
+                    }
+                    if (!mine) continue;
+                    const uint32_t r = rank_of_token(s, uint32_t(id));
+                    if (in_bounds(row < s.rows && r < s.p, s.status, kSiteDistill, row))
+                        ShardRow<T>(s.out[r], s.ld, row, shard_width(s, r))
+                            .set_column(uint32_t(id) - shard_begin(s, r), (ex2((zs[i] - row_m) * a.to_log2) * inv - w / tsum) * factor);
                 }
-                a.loss[row] = loss;
-                if (a.stats) {
-                    a.stats[2 * row] = mx;
-                    a.stats[2 * row + 1] = ls;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh.taught_free[slot]));
+            }
+        }
+    } else if (warp == kDistillWarps + 1) {
+        // ---- the teacher's entries ---------------------------------------
+        // 32 U of a row are held in registers, those of the next row coming
+        // in meanwhile; any others are kept in shared memory.
+        constexpr int U = 4;
+        int next_id[U];
+        float next_t[U], next_w = 1.0f, next_m = 0.0f, next_ls = 0.0f;
+        auto entry = [&](uint32_t row, uint32_t i, int &id, float &t) {
+            id = i < a.k ? a.ids[uint64_t(row) * a.k + i] : -1;
+            t = i < a.k ? load_any(a.teacher, a.teacher_dtype, uint64_t(row) * a.k + i) : -INFINITY;
+        };
+        auto prefetch = [&](uint32_t item) {
+            if (item >= a.items) return;
+            const uint32_t row = div_by(item, a.by_pieces);
+#pragma unroll
+            for (int u = 0; u < U; ++u) entry(row, lane + 32 * u, next_id[u], next_t[u]);
+            if (BWD && a.weight) next_w = a.weight[row];
+            if (!FWD) {
+                next_m = a.stats[2 * uint64_t(row)];
+                next_ls = a.stats[2 * uint64_t(row) + 1];
+            }
+        };
+        prefetch(blockIdx.x);
+        uint32_t k = 0;
+        for (uint32_t item = blockIdx.x; item < a.items; item += stride, ++k) {
+            const uint32_t slot = k & 1;
+            const uint32_t row = div_by(item, a.by_pieces), q = item - row * a.pieces;
+            Piece<T, PM> pc(a, q, 0);
+            uint32_t lo = 0, hi = 0;      // the piece's columns of its one shard
+            if (a.segments == 1) {
+                const ShardRow<T> in(s.in[pc.rank], s.ld, row, shard_width(s, pc.rank));
+                pc.cut(a, in);
+                lo = pc.part == 0 ? 0u : in.head() + (pc.j0 - in.first) * VEC;
+                hi = pc.part + 1 == a.parts ? in.width : in.head() + (pc.j1 - in.first) * VEC;
+            }
+            float tm = -INFINITY, ref = -INFINITY;
+            // an entry outside the vocabulary: id -1; of another piece: the sign bit set, only its weight counts here
+            auto place = [&](int &id, float &t, float &z) {
+                z = 0.0f;
+                if (uint32_t(id) >= s.vocab) {
+                    id = -1;
+                    t = -INFINITY;
+                    return;
                 }
+                const uint32_t r = rank_of_token(s, uint32_t(id)), c = uint32_t(id) - shard_begin(s, r);
+                const bool mine = a.segments == 1 ? r == pc.rank && c >= lo && c < hi : div_by(r, a.by_segments) == q;
+                if (mine && in_bounds(row < s.rows && r < s.p, s.status, kSiteDistill, row))
+                    z = ShardRow<T>(s.in[r], s.ld, row, shard_width(s, r)).column(c);
+                else
+                    id |= int(0x80000000u);
+            };
+            int id[U];
+            float t[U], z[U];
+            const float w = next_w, st_m = next_m, st_ls = next_ls;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                id[u] = next_id[u];
+                t[u] = next_t[u];
+                place(id[u], t[u], z[u]);
+            }
+            prefetch(item + stride);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                tm = fmaxf(tm, t[u]);
+                if (id[u] >= 0 && z[u] < INFINITY) ref = fmaxf(ref, z[u]);
+            }
+            for (uint32_t i = lane + 32 * U; i < a.kpad; i += 32) {
+                entry(row, i, more_id[i], more_e[i]);
+                place(more_id[i], more_e[i], more_z[i]);
+                tm = fmaxf(tm, more_e[i]);
+                if (more_id[i] >= 0 && more_z[i] < INFINITY) ref = fmaxf(ref, more_z[i]);
+            }
+            tm = finite_max(warp_max(tm));
+            if (FWD) ref = finite_max(warp_max(ref));
+            if (BWD && k >= 2 && !__all_sync(0xffffffffu, distill_wait(a, sh, &sh.taught_free[slot], ((k >> 1) - 1) & 1, 8, item))) break;
+            float ts = 0.0f, tu = 0.0f, dot = 0.0f, own = 0.0f;
+            uint32_t kept = 0;
+            auto weigh = [&](int eid, float et, float ez) {
+                const float u = (et - tm) / a.temperature;
+                const float e = eid == -1 ? 0.0f : expf(u);
+                ts += e;
+                const bool mine = e != 0.0f && eid >= 0;
+                if (FWD && e != 0.0f) tu += e * u;
+                if (FWD && mine) {
+                    dot += e * (ez - ref);
+                    own += e;
+                }
+                if (BWD) {
+                    const unsigned who = __ballot_sync(0xffffffffu, mine);
+                    const uint32_t at = slot * a.kpad + kept + __popc(who & ((1u << lane) - 1));
+                    if (mine) {
+                        id_s[at] = eid;
+                        e_s[at] = e;
+                        z_s[at] = ez;
+                    }
+                    kept += __popc(who);
+                }
+            };
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (32 * u < int(a.kpad)) weigh(id[u], t[u], z[u]);
+            for (uint32_t i0 = 32 * U; i0 < a.kpad; i0 += 32) {
+                const uint32_t i = i0 + lane;
+                const bool in = i < a.kpad;
+                weigh(in ? more_id[i] : -1, in ? more_e[i] : 0.0f, in ? more_z[i] : 0.0f);
+            }
+            ts = warp_sum(ts);
+            if constexpr (BWD) {
+                if (kept % 4 && lane < int(4 - kept % 4)) id_s[slot * a.kpad + kept + lane] = -1;
+                if (lane == 0) {
+                    sh.entries[slot] = ts != 0.0f ? kept : 0u;
+                    sh.teacher_sum[slot] = ts;
+                    sh.weight[slot] = w;
+                    sh.row_max[slot] = st_m;
+                    sh.row_log_sum[slot] = st_ls;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh.taught[slot]));
+            }
+            if constexpr (FWD) {
+                tu = warp_sum(tu);
+                dot = warp_sum(dot);
+                own = warp_sum(own);
+                // the slot's last contents have been used by every CTA of the row once the row before this one is complete
+                if (k >= 1 && !__all_sync(0xffffffffu, distill_wait(a, sh, &sh.sums_in[slot ^ 1], ((k - 1) >> 1) & 1, 9, item))) break;
+                if (lane == 0) mbar_arrive_expect_tx(smem_addr(&sh.sums_in[slot]), a.pieces * kDistillSumBytes);
+                if (lane < int(a.pieces)) {
+                    const uint32_t bar = remote(smem_addr(&sh.sums_in[slot]), lane), at = remote(smem_addr(&sh.sums[slot].teacher[q][0]), lane);
+                    send4(at, bar, make_float4(ref, dot, own, ts));
+                    send4(at + 16, bar, make_float4(tu, w, 0.0f, 0.0f));
+                }
+            }
+        }
+    } else {
+        // ---- consumers ---------------------------------------------------
+        const float c2 = a.to_log2;
+        const Pair cc = {c2, c2};
+        const uint32_t stages_at = smem_addr(smem);
+        // The row's maximum and 1 / sum from all its CTAs' sums, and its loss.
+        auto total_of = [&](uint32_t slot, uint32_t q, uint32_t row, float &row_m, float &inv, float &factor, bool &taught) {
+            const DistillSums &in = sh.sums[slot];
+            const float2 *pairs = &in.warp[0][0];
+            const uint32_t n = a.pieces * kDistillWarps;
+            float2 v[kDistillMaxCluster * kDistillWarps / 32];
+            float mx = -INFINITY, total = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kDistillMaxCluster * kDistillWarps / 32; ++i) {
+                v[i] = lane + 32 * i < n ? pairs[lane + 32 * i] : make_float2(-INFINITY, 0.0f);
+                mx = fmaxf(mx, v[i].x);
+            }
+            mx = warp_max(mx);
+            row_m = finite_max(mx);
+#pragma unroll
+            for (int i = 0; i < kDistillMaxCluster * kDistillWarps / 32; ++i) total += v[i].y * ex2((v[i].x - row_m) * c2);
+            total = warp_sum(total);
+            inv = total == 0.0f ? 0.0f : 1.0f / total;    // a row of nothing but -inf: p = 0
+            const float tsum = in.teacher[q][0].w;
+            taught = tsum != 0.0f;
+            factor = in.teacher[q][1].y * a.temperature;
+            if (q == 0 && warp == 0) {
+                const float4 t = lane < int(a.pieces) ? in.teacher[lane][0] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                const float dot = warp_sum(t.z != 0.0f ? t.y + t.z * (t.x - row_m) : 0.0f);
+                if (lane == 0) {
+                    const float ls = logf(total), T = a.temperature;
+                    float loss = 0.0f;
+                    if (taught) {
+                        if (total == 0.0f) loss = INFINITY;
+                        else loss = T * T * ((in.teacher[q][1].x / tsum - logf(tsum)) - (dot / T / tsum - ls));
+                    }
+                    a.loss[row] = loss;
+                    if (a.stats) {
+                        a.stats[2 * uint64_t(row)] = mx;
+                        a.stats[2 * uint64_t(row) + 1] = ls;
+                    }
+                }
+            }
+        };
+        uint32_t used = 0, k = 0;
+        for (uint32_t item = blockIdx.x; item < a.items; item += stride, ++k) {
+            const uint32_t slot = k & 1, parity = (k >> 1) & 1;
+            const uint32_t row = div_by(item, a.by_pieces), q = item - row * a.pieces;
+            Pair e[NG * PAIRS];
+            float m = -INFINITY, sum = 0.0f, edge = -INFINITY;
+            bool ok = true;
+            const DistillDesc *d = nullptr;
+            // one chunk into e and edge, and its stage free again
+            auto take = [&]() -> typename Gr::Max {
+                const uint32_t st = used % S;
+                ok = __all_sync(0xffffffffu, distill_wait(a, sh, &sh.full[st], (used / S) & 1, 10, item));
+                typename Gr::Max gm = Gr::lowest();
+                if (!ok) return gm;
+                d = &sh.desc[used % (S + 1)];
+                const uint32_t at = stages_at + st * kDistillStageBytes + tid * 16, groups = d->groups;
+#pragma unroll
+                for (int n = 0; n < NG; ++n) {
+                    const uint4 v = uint32_t(tid + n * kDistillConsumers) < groups ? lds_v4(at + n * kDistillConsumers * 16) : lowest_group<T>();
+                    gm = Gr::max(gm, v);
+#pragma unroll
+                    for (int i = 0; i < PAIRS; ++i) e[n * PAIRS + i] = Gr::pair(v, i);
+                }
+                edge = uint32_t(tid) < a.segments * 2 * VEC ? d->edge[tid] : -INFINITY;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh.empty[st]));
+                ++used;
+                return gm;
+            };
+            // stores e * g (edge: edge * g) where the chunk came from; zero for a row without a teacher
+            auto put = [&](float g, bool taught) {
+                const uint32_t groups = d->groups;
+                const Pair gg = {g, g};
+                auto value = [&](int n) -> uint4 {
+                    Pair p[PAIRS];
+#pragma unroll
+                    for (int i = 0; i < PAIRS; ++i) p[i] = e[n * PAIRS + i] * gg;
+                    const uint4 v = Gr::pack(p);
+                    return taught ? v : make_uint4(0, 0, 0, 0);
+                };
+                if (a.segments == 1 && d->seg[0].aligned) {
+                    char *to = reinterpret_cast<char *>(d->seg[0].out) + size_t(tid) * 16;
+#pragma unroll
+                    for (int n = 0; n < NG; ++n)
+                        if (uint32_t(tid + n * kDistillConsumers) < groups) st_stream_v4(to + n * kDistillConsumers * 16, value(n));
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NG; ++n) {
+                        const uint32_t g16 = tid + n * kDistillConsumers;
+                        if (g16 >= groups) continue;
+                        uint32_t sg = 0;
+                        while (sg + 1 < a.segments && d->seg[sg + 1].first <= g16) ++sg;
+                        const uintptr_t to = uintptr_t(d->seg[sg].out) + uintptr_t(g16 - d->seg[sg].first) * 16;
+                        const uint4 v = value(n);
+                        if (d->seg[sg].aligned) {
+                            st_stream_v4(reinterpret_cast<void *>(to), v);
+                        } else {
+                            float f[VEC];
+                            Tr::unpack(v, f);
+#pragma unroll
+                            for (int i = 0; i < VEC; ++i) Tr::store1(reinterpret_cast<void *>(to), i, f[i]);
+                        }
+                    }
+                }
+                if (uint32_t(tid) < a.segments * 2 * VEC && d->edge_out[tid])
+                    Tr::store1(reinterpret_cast<void *>(uintptr_t(d->edge_out[tid])), 0, taught ? edge * g : 0.0f);
+            };
+            float row_m = 0.0f, inv = 0.0f, factor = 0.0f;
+            bool taught = true;
+            if constexpr (FWD) {
+                for (uint32_t c = 0; c < a.chunks; ++c) {
+                    const float cm = Gr::value(take());
+                    if (!ok) break;
+                    const float bm = fmaxf(m, fmaxf(cm, edge)), to = finite_max(bm);
+                    sum *= ex2((m - to) * c2);            // nothing yet: 0 * 2^-inf
+                    m = bm;
+                    edge = ex2((edge - to) * c2);
+                    Pair acc = {edge, 0.0f}, acc2 = {0.0f, 0.0f};
+#pragma unroll
+                    for (int i = 0; i < NG * PAIRS; i += 2) {
+                        e[i] = ex2((e[i] + Pair{-to, -to}) * cc);
+                        e[i + 1] = ex2((e[i + 1] + Pair{-to, -to}) * cc);
+                        acc = acc + e[i];
+                        acc2 = acc2 + e[i + 1];
+                    }
+                    acc = acc + acc2;
+                    sum += acc.x + acc.y;
+                }
+                if (!ok) break;
+                const float wm = warp_max(m);
+                const float ws = warp_sum(sum * ex2((m - finite_max(wm)) * c2));
+                // The loss alone does not hold the consumers up: they see the row before this one complete (which also
+                // says that every CTA of the row is done with this row's slot), finish it, and go on to the next.
+                if (!BWD && k >= 1) {
+                    if (!__all_sync(0xffffffffu, distill_wait(a, sh, &sh.sums_in[slot ^ 1], ((k - 1) >> 1) & 1, 11, item))) break;
+                    if (q == 0 && warp == 0) total_of(slot ^ 1, q, div_by(item - stride, a.by_pieces), row_m, inv, factor, taught);
+                }
+                if (lane < int(a.pieces))
+                    send2(remote(smem_addr(&sh.sums[slot].warp[q][warp]), lane), remote(smem_addr(&sh.sums_in[slot]), lane), wm, ws);
+                if (BWD || item + stride >= a.items) {
+                    if (!__all_sync(0xffffffffu, distill_wait(a, sh, &sh.sums_in[slot], parity, 12, item))) break;
+                    if (BWD || (q == 0 && warp == 0)) total_of(slot, q, row, row_m, inv, factor, taught);
+                }
+            }
+            if constexpr (BWD) {
+                if (FWD && a.chunks == 1) {
+                    put(inv * ex2((m - row_m) * c2) * factor, taught);
+                } else {
+                    for (uint32_t c = 0; c < a.chunks; ++c) {
+                        take();
+                        if (!ok) break;
+                        if (!FWD && c == 0) {
+                            ok = __all_sync(0xffffffffu, distill_wait(a, sh, &sh.taught[slot], parity, 13, item));
+                            if (!ok) break;
+                            const float mx = sh.row_max[slot];
+                            row_m = finite_max(mx);
+                            inv = mx == -INFINITY ? 0.0f : expf(-sh.row_log_sum[slot]);
+                            factor = sh.weight[slot] * a.temperature;
+                            taught = sh.teacher_sum[slot] != 0.0f;
+                        }
+                        edge = ex2((edge - row_m) * c2);
+#pragma unroll
+                        for (int i = 0; i < NG * PAIRS; ++i) e[i] = ex2((e[i] + Pair{-row_m, -row_m}) * cc);
+                        put(inv * factor, taught);
+                    }
+                    if (!ok) break;
+                }
+                if (tid == 0) {
+                    sh.used_max[slot] = row_m;
+                    sh.used_inv[slot] = inv;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&sh.stored[slot]));
             }
         }
     }
-    if constexpr (BWD) {
-        const float factor = (a.weight ? a.weight[row] : 1.0f) * a.temperature;
-        const ShardRow<T> out(s.out[rr], s.ld, row, in.width);
-        const float g = inv * factor;
-        const Pair gg = {g, g}, off = {-row_m, -row_m};
-        auto gradient = [&](const uint4 &v) -> uint4 {
-            if (!taught) return make_uint4(0, 0, 0, 0);
-            Pair p[PAIRS];
-#pragma unroll
-            for (int i = 0; i < PAIRS; ++i) p[i] = ex2((Gr::pair(v, i) + off) * cc) * gg;
-            return Gr::pack(p);
-        };
-        hold_batch(raw);    // the groups stay packed: without this the compiler keeps the unpacked values of the first pass
-#pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            const uint32_t j = j0 + tt + n * step;
-            if (j < j1) store_group<T>(out, in, j, gradient(raw[n]));
+
+    // A CTA that gave up: its copies in flight land before it goes, and what
+    // the other CTAs of the row still send has a while to arrive.
+    __syncthreads();
+    if (warp == kDistillWarps && *static_cast<volatile int *>(&sh.dead)) {
+        const uint64_t t0 = global_ns();
+        for (uint32_t n = issued > S ? issued - S : 0; n < issued; ++n)
+            while (!mbar_try_wait(smem_addr(&sh.full[n % S]), (n / S) & 1))
+                if (global_ns() - t0 > uint64_t(a.wait_ns) + 1000000) break;
+        while (FWD && global_ns() - t0 < 1000000) {
         }
-        for (uint32_t j = j0 + tt + NV * step; j < j1; j += step) store_group<T>(out, in, j, gradient(ld_coherent_v4(in.group(j))));
-        if (edge >= 0) out.set_column(edge, taught ? ex2((edge_z - row_m) * c2) * g : 0.0f);
-        __syncthreads();
-        if (taught) {
-            for (uint32_t k = tid; k < a.k; k += threads) {
-                const int id = id_s[k];
-                if (id < 0) continue;
-                float w = 0.0f;
-                bool mine = true;
-                for (uint32_t j = 0; j < a.kpad; j += 4) {
-                    const int4 o = *reinterpret_cast<const int4 *>(&id_s[j]);
-                    if (o.x == id) { w += e_s[j]; mine = mine && j >= k; }
-                    if (o.y == id) { w += e_s[j + 1]; mine = mine && j + 1 >= k; }
-                    if (o.z == id) { w += e_s[j + 2]; mine = mine && j + 2 >= k; }
-                    if (o.w == id) { w += e_s[j + 3]; mine = mine && j + 3 >= k; }
-                }
-                if (!mine) continue;
-                const uint32_t ir = rank_of_token(s, uint32_t(id));
-                ShardRow<T>(s.out[ir], s.ld, row, shard_width(s, ir))
-                    .set_column(uint32_t(id) - shard_begin(s, ir), (ex2((z_s[k] - row_m) * c2) * inv - w / tsum) * factor);
-            }
-        }
+    }
+    if (FWD) {
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     }
 }
 
-template <typename T, int PM, int PASS, int NV, int MIN_CTAS>
-static cudaError_t distill_launch(const Launch &L, DistillArgs<PM> &a, uint32_t need, LaunchInfo *info)
+// Shared-memory and cluster attributes, set once per device, and the clusters
+// of each size that fit the GPU at once.
+template <typename T, int PM, int PASS>
+static cudaError_t distill_residents(const Launch &L, const cudaLaunchConfig_t &cfg, uint32_t pieces, uint32_t stages, uint32_t *ctas)
 {
-    // threads enough for the need of a CTA, in whole warps per team
-    const uint32_t per_team = (need + NV - 1) / NV, most = kDistillMaxThreads / a.teams;
-    a.team = (per_team < most ? per_team : most) / 32 * 32;
-    if (a.team < per_team && a.team + 32 <= most) a.team += 32;
-    if (a.team < 32) a.team = 32;
-    const uint32_t threads = a.team * a.teams;
-    if (a.s.rows * a.ctas > 0x7fffffffull) return cudaErrorInvalidValue;
-    a.by_ctas = fast_div(a.ctas);
-    a.by_parts = fast_div(a.parts);
-    a.by_teams = fast_div(a.teams);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned(a.s.rows * a.ctas));
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = size_t(a.kpad) * 12;
-    cfg.stream = L.stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = a.ctas;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = (PASS & CCL_PASS_FORWARD) && a.ctas > 1 ? 2 : 1;
-    cudaError_t err = cudaLaunchKernelEx(&cfg, distill_kernel<T, PM, PASS, NV, MIN_CTAS>, a);
-    if (err != cudaSuccess) return err;
-    info->kernel = "distill_topk";
-    info->grid = int(cfg.gridDim.x);
-    info->block = int(threads);
-    info->smem = cfg.dynamicSmemBytes;
-    info->kernels = 1;
-    return cudaGetLastError();
+    static std::atomic<unsigned long long> done{0};
+    static std::atomic<int> fit[kDistillMaxCluster + 1][kDistillMaxStages + 1];
+    static std::atomic<int> fit_device{-1};
+    auto kern = distill_kernel<T, PM, PASS>;
+    const unsigned long long bit = (L.device >= 0 && L.device < 64) ? (1ull << L.device) : 0ull;
+    if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
+        cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kDistillSmem));
+        if (err == cudaSuccess) err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (err != cudaSuccess) return err;
+        if (bit) done.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    if (!(PASS & CCL_PASS_FORWARD)) {
+        *ctas = 2 * uint32_t(L.num_sms);
+        return cudaSuccess;
+    }
+    int n = fit_device.load(std::memory_order_acquire) == L.device ? fit[pieces][stages].load(std::memory_order_acquire) : 0;
+    if (n == 0) {
+        const cudaError_t err = cudaOccupancyMaxActiveClusters(&n, kern, &cfg);
+        if (err != cudaSuccess) return err;
+        if (n < 1) return cudaErrorInvalidConfiguration;
+        int none = -1;
+        if (fit_device.compare_exchange_strong(none, L.device, std::memory_order_acq_rel) || none == L.device)
+            fit[pieces][stages].store(n, std::memory_order_release);
+    }
+    *ctas = uint32_t(n) * pieces;
+    return cudaSuccess;
 }
 
 template <typename T, int PM, int PASS>
@@ -379,24 +749,59 @@ static cudaError_t distill_shape(const Launch &L, const DistillLaunch &N, Launch
     a.k = N.k;
     a.kpad = (N.k + 3) / 4 * 4;
     a.teacher_dtype = N.teacher_dtype;
+    a.wait_ns = L.wait_limit_ns > 0 ? L.wait_limit_ns : 2000000000LL;
+    a.stall_test = L.stall_test;
     const uint32_t p = a.s.p, groups = widest_groups<T>(a.s);
-    a.teams = (p + kDistillMaxCluster - 1) / kDistillMaxCluster;
+    // Pieces: few enough groups that a stage holds one, in a cluster of the
+    // portable eight CTAs where that will do and of sixteen where not (a
+    // gradient alone needs no cluster, so any number); then, with fewer CTAs
+    // than two per SM, more and smaller pieces, for latency.
+    a.segments = (p + kDistillMaxCluster - 1) / kDistillMaxCluster;
     a.parts = 1;
-    uint32_t need = groups;            // groups a team takes
-    if (a.teams == 1) {
-        // parts: few enough groups a CTA that four per thread hold them, and
-        // CTAs enough for every SM
-        const uint32_t most = PASS == CCL_PASS_BACKWARD ? 64 : kDistillMaxCluster / p, want = 4 * kDistillMaxThreads;
-        while (a.parts < most && ((groups + a.parts - 1) / a.parts > want ||
-                                  (N.rows * p * a.parts < 2 * uint64_t(L.num_sms) && (groups + a.parts - 1) / a.parts > 128)))
-            ++a.parts;
-        need = (groups + a.parts - 1) / a.parts;
+    auto per_part = [&](uint32_t parts) { return (groups + parts - 1) / parts; };
+    uint32_t cap = kDistillStage / a.segments;
+    if (a.segments == 1) {
+        const uint32_t most = (PASS & CCL_PASS_FORWARD) ? kDistillMaxCluster / p : (1u << 20) / p, portable = (PASS & CCL_PASS_FORWARD) ? 8 / p : most;
+        while (a.parts < most && per_part(a.parts) > cap) ++a.parts;
+        while (a.parts < portable && N.rows * p * a.parts < 2 * uint64_t(L.num_sms) && per_part(a.parts) > kDistillConsumers) ++a.parts;
     }
-    a.ctas = a.teams == 1 ? p * a.parts : (p + a.teams - 1) / a.teams;
-    const uint32_t full = need * a.teams;
-    if (full <= 2 * kDistillMaxThreads) return distill_launch<T, PM, PASS, 2, 3>(L, a, need, info);
-    if (PASS != CCL_PASS_BOTH || full <= 4 * kDistillMaxThreads) return distill_launch<T, PM, PASS, 4, 3>(L, a, need, info);
-    return distill_launch<T, PM, PASS, 8, 2>(L, a, need, info);
+    a.pieces = a.segments == 1 ? p * a.parts : (p + a.segments - 1) / a.segments;
+    a.chunks = (per_part(a.parts) + cap - 1) / cap;
+    if (a.chunks < 1) a.chunks = 1;
+    if (N.rows * a.pieces > 0x7fffffffull) return cudaErrorInvalidValue;
+    a.items = uint32_t(N.rows * a.pieces);
+    a.by_pieces = fast_div(a.pieces);
+    a.by_parts = fast_div(a.parts);
+    a.by_segments = fast_div(a.segments);
+    const size_t entries = size_t(a.kpad) * (a.kpad > 128 ? 36 : 24);
+    a.stages = kDistillMaxStages;
+    while (a.stages * size_t(kDistillStageBytes) + entries + sizeof(DistillShared) + 1024 > kDistillSmem) --a.stages;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kDistillThreads);
+    cfg.dynamicSmemBytes = a.stages * size_t(kDistillStageBytes) + entries;
+    cfg.stream = L.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.pieces;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = (PASS & CCL_PASS_FORWARD) ? 2 : 1;
+    cfg.gridDim = dim3(a.pieces);
+    uint32_t ctas = 0;
+    cudaError_t err = distill_residents<T, PM, PASS>(L, cfg, a.pieces, a.stages, &ctas);
+    if (err != cudaSuccess) return err;
+    cfg.gridDim = dim3(a.items < ctas ? a.items : ctas);
+    err = cudaLaunchKernelEx(&cfg, distill_kernel<T, PM, PASS>, a);
+    if (err != cudaSuccess) return err;
+    info->kernel = "distill_topk";
+    info->grid = int(cfg.gridDim.x);
+    info->block = kDistillThreads;
+    info->smem = cfg.dynamicSmemBytes;
+    info->kernels = 1;
+    return cudaGetLastError();
 }
 
 template <typename T, int PM>
@@ -412,7 +817,7 @@ static cudaError_t distill_pass(const Launch &L, const DistillLaunch &N, LaunchI
 template <typename T>
 static cudaError_t distill_dtype(const Launch &L, const DistillLaunch &N, LaunchInfo *info)
 {
-    return L.p <= kDistillMaxCluster ? distill_pass<T, kDistillMaxCluster>(L, N, info) : distill_pass<T, kMaxRanks>(L, N, info);
+    return L.p <= 8 ? distill_pass<T, 8>(L, N, info) : distill_pass<T, kMaxRanks>(L, N, info);
 }
 
 cudaError_t launch_distill(const Launch &L, const DistillLaunch &N, LaunchInfo *info)

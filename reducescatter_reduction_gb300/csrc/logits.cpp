@@ -107,6 +107,8 @@ static Launch make_launch(ccl_comm *c, int dtype, bool alias, void *stream)
     L.device = c->device;
     L.num_sms = c->num_sms;
     L.status = c->d_status;
+    L.wait_limit_ns = c->wait_limit_ns;
+    L.stall_test = c->stall_test;
     L.stream = static_cast<cudaStream_t>(stream);
     return L;
 }

@@ -288,6 +288,34 @@ def test_offsets_beyond_32_bits():
     ccl.ccl_comm_destroy(comm)
 
 
+@pytest.mark.parametrize("steps", ["forward", "both", "backward"])
+def test_a_wait_that_runs_out_is_reported(steps):
+    """A load is withheld (the test hook): the call ends, ccl_comm_check reports it, and the next call is whole."""
+    rows, vocab = 700, 3000
+    ids, t = teacher(rows, vocab, 4, 20)
+    full = torch.from_numpy(rng(20).normal(0, 3, (rows, vocab))).cuda().bfloat16()
+    ids_d, t_d = torch.from_numpy(ids).cuda(), torch.from_numpy(t).cuda().float()
+    loss, stats = torch.empty(rows, device="cuda"), torch.zeros(rows, 2, device="cuda")
+    ranks = Ranks(shards(full, 3), "bf16")
+
+    def call():
+        ccl.ccl_distill_topk(ranks.comm, "bf16", steps, rows, vocab, 4, ids_d.data_ptr(), t_d.data_ptr(), loss=loss.data_ptr(),
+                             stats=stats.data_ptr(), stream=stream())
+
+    ccl.ccl_comm_set_debug(ranks.comm, 2_000_000, 1)
+    call()
+    with pytest.raises(ccl.CclError) as e:
+        ccl.ccl_comm_check(ranks.comm)
+    assert e.value.status == ccl.CCL_ERR_TIMEOUT
+    ccl.ccl_comm_set_debug(ranks.comm, 0, 0)
+    call()
+    ccl.ccl_comm_check(ranks.comm)
+    if steps != "backward":
+        want, *_, dloss, _, _ = exact(full.double().cpu().numpy(), ids, t_d.double().cpu().numpy(), 1.0, None)
+        assert_within(loss, torch.from_numpy(want), torch.from_numpy(dloss + 2 * U32 * np.abs(want)), "loss")
+    ccl.ccl_comm_destroy(ranks.comm)
+
+
 def test_no_rows():
     ranks = Ranks([torch.zeros(1, 8, device="cuda")], "f32")
     one = torch.zeros(8, device="cuda")
