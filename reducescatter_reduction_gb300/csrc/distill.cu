@@ -83,6 +83,7 @@ struct DistillArgs {
     uint32_t items;       // rows * pieces
     FastDiv by_pieces, by_parts, by_segments;
     int teacher_dtype;
+    int edges;            // some row begins or ends between 16-byte boundaries
     long long wait_ns;
     int stall_test;       // 1: the second load of every CTA is withheld, so that a wait runs out (tests)
 };
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
             if (n && !held) bulk_load(smem_addr(smem) + st * kDistillStageBytes + first * 16, from, n * 16, bar);
             if (lane < int(a.segments)) d.seg[lane].first = first;
             // edges: thread e of a segment, as ShardRow::edge numbers them
-            for (uint32_t e = lane; e < a.segments * 2 * VEC; e += 32) {
+            for (uint32_t e = lane; a.edges && e < a.segments * 2 * VEC; e += 32) {
                 const uint32_t g = e / (2 * VEC);
                 Piece<T, PM> pe(a, q, g);
                 uint64_t to = 0;
@@ -371,84 +372,127 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
         }
     } else if (warp == kDistillWarps + 1) {
         // ---- the teacher's entries ---------------------------------------
-        // 32 U of a row are held in registers, those of the next row coming
-        // in meanwhile; any others are kept in shared memory.
+        // 32 U of a row are held in registers: their ids and logits are
+        // loaded two rows ahead, the student's logits at them one row ahead.
+        // Any others are loaded when it is their turn and kept in shared memory.
         constexpr int U = 4;
-        int next_id[U];
-        float next_t[U], next_w = 1.0f, next_m = 0.0f, next_ls = 0.0f;
-        auto entry = [&](uint32_t row, uint32_t i, int &id, float &t) {
-            id = i < a.k ? a.ids[uint64_t(row) * a.k + i] : -1;
-            t = i < a.k ? load_any(a.teacher, a.teacher_dtype, uint64_t(row) * a.k + i) : -INFINITY;
+        constexpr uint32_t ES = 16 / VEC;
+        struct Held {
+            int id[U];
+            float t[U], z[U];
+            float w, max, log_sum;
         };
-        auto prefetch = [&](uint32_t item) {
+        Held coming, next, now;
+        auto fetch = [&](uint32_t item) {
             if (item >= a.items) return;
             const uint32_t row = div_by(item, a.by_pieces);
+            const uint64_t at = uint64_t(row) * a.k + lane;
 #pragma unroll
-            for (int u = 0; u < U; ++u) entry(row, lane + 32 * u, next_id[u], next_t[u]);
-            if (BWD && a.weight) next_w = a.weight[row];
+            for (int u = 0; u < U; ++u) {
+                const bool in = lane + 32 * u < a.k;
+                coming.id[u] = in ? a.ids[at + 32 * u] : -1;
+                coming.t[u] = in ? load_any(a.teacher, a.teacher_dtype, at + 32 * u) : -INFINITY;
+            }
+            coming.w = BWD && a.weight ? a.weight[row] : 1.0f;
             if (!FWD) {
-                next_m = a.stats[2 * uint64_t(row)];
-                next_ls = a.stats[2 * uint64_t(row) + 1];
+                coming.max = a.stats[2 * uint64_t(row)];
+                coming.log_sum = a.stats[2 * uint64_t(row) + 1];
             }
         };
-        prefetch(blockIdx.x);
+        // What a piece holds: tokens [from, to), consecutive in memory from `at` on where it is of one shard.
+        struct Hold {
+            uint32_t row, from, count;
+            uintptr_t at;
+        };
+        auto hold_of = [&](uint32_t item) -> Hold {
+            Hold h;
+            h.row = div_by(item, a.by_pieces);
+            const uint32_t q = item - h.row * a.pieces;
+            h.at = 0;
+            if (a.segments == 1) {
+                Piece<T, PM> pc(a, q, 0);
+                const ShardRow<T> in(s.in[pc.rank], s.ld, h.row, shard_width(s, pc.rank));
+                pc.cut(a, in);
+                const uint32_t lo = pc.part == 0 ? 0u : in.head() + (pc.j0 - in.first) * VEC;
+                const uint32_t hi = pc.part + 1 == a.parts ? in.width : in.head() + (pc.j1 - in.first) * VEC;
+                h.from = shard_begin(s, pc.rank) + lo;
+                h.count = hi - lo;
+                h.at = in.base + uint64_t(in.shift + lo) * ES;
+            } else {
+                h.from = shard_begin(s, min(q * a.segments, s.p));
+                h.count = shard_begin(s, min((q + 1) * a.segments, s.p)) - h.from;
+            }
+            return h;
+        };
+        // an entry outside the vocabulary: id -1; of another piece: the sign bit set, only its weight counts here
+        auto place = [&](const Hold &h, int &id, float &t, float &z) {
+            z = 0.0f;
+            if (uint32_t(id) - h.from < h.count) {
+                if (!in_bounds(h.row < s.rows && uint32_t(id) < s.vocab, s.status, kSiteDistill, h.row)) return;
+                if (a.segments == 1) {
+                    z = Tr::load1(reinterpret_cast<const void *>(h.at), uint32_t(id) - h.from);
+                } else {
+                    const uint32_t r = rank_of_token(s, uint32_t(id));
+                    z = ShardRow<T>(s.in[r], s.ld, h.row, shard_width(s, r)).column(uint32_t(id) - shard_begin(s, r));
+                }
+            } else if (uint32_t(id) < s.vocab) {
+                id |= int(0x80000000u);
+            } else {
+                id = -1;
+                t = -INFINITY;
+            }
+        };
+        auto place_all = [&](uint32_t item) {
+            if (item >= a.items) return;
+            const Hold h = hold_of(item);
+            next = coming;
+#pragma unroll
+            for (int u = 0; u < U; ++u) place(h, next.id[u], next.t[u], next.z[u]);
+        };
+        fetch(blockIdx.x);
+        place_all(blockIdx.x);
+        fetch(blockIdx.x + stride);
+        const float per_t = 1.0f / a.temperature;
         uint32_t k = 0;
         for (uint32_t item = blockIdx.x; item < a.items; item += stride, ++k) {
             const uint32_t slot = k & 1;
             const uint32_t row = div_by(item, a.by_pieces), q = item - row * a.pieces;
-            Piece<T, PM> pc(a, q, 0);
-            uint32_t lo = 0, hi = 0;      // the piece's columns of its one shard
-            if (a.segments == 1) {
-                const ShardRow<T> in(s.in[pc.rank], s.ld, row, shard_width(s, pc.rank));
-                pc.cut(a, in);
-                lo = pc.part == 0 ? 0u : in.head() + (pc.j0 - in.first) * VEC;
-                hi = pc.part + 1 == a.parts ? in.width : in.head() + (pc.j1 - in.first) * VEC;
-            }
+            now = next;
+            place_all(item + stride);
+            fetch(item + 2 * stride);
             float tm = -INFINITY, ref = -INFINITY;
-            // an entry outside the vocabulary: id -1; of another piece: the sign bit set, only its weight counts here
-            auto place = [&](int &id, float &t, float &z) {
-                z = 0.0f;
-                if (uint32_t(id) >= s.vocab) {
-                    id = -1;
-                    t = -INFINITY;
-                    return;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                tm = fmaxf(tm, now.t[u]);
+                if (now.id[u] >= 0 && now.z[u] < INFINITY) ref = fmaxf(ref, now.z[u]);
+            }
+            if (a.kpad > 32 * U) {
+                const Hold h = hold_of(item);
+                for (uint32_t i = lane + 32 * U; i < a.kpad; i += 32) {
+                    int id = i < a.k ? a.ids[uint64_t(row) * a.k + i] : -1;
+                    float t = i < a.k ? load_any(a.teacher, a.teacher_dtype, uint64_t(row) * a.k + i) : -INFINITY, z;
+                    place(h, id, t, z);
+                    more_id[i] = id;
+                    more_e[i] = t;
+                    more_z[i] = z;
+                    tm = fmaxf(tm, t);
+                    if (id >= 0 && z < INFINITY) ref = fmaxf(ref, z);
                 }
-                const uint32_t r = rank_of_token(s, uint32_t(id)), c = uint32_t(id) - shard_begin(s, r);
-                const bool mine = a.segments == 1 ? r == pc.rank && c >= lo && c < hi : div_by(r, a.by_segments) == q;
-                if (mine && in_bounds(row < s.rows && r < s.p, s.status, kSiteDistill, row))
-                    z = ShardRow<T>(s.in[r], s.ld, row, shard_width(s, r)).column(c);
-                else
-                    id |= int(0x80000000u);
-            };
-            int id[U];
-            float t[U], z[U];
-            const float w = next_w, st_m = next_m, st_ls = next_ls;
+            }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                id[u] = next_id[u];
-                t[u] = next_t[u];
-                place(id[u], t[u], z[u]);
+            for (int o = 16; o > 0; o >>= 1) {
+                const float x = __shfl_xor_sync(0xffffffffu, tm, o), y = __shfl_xor_sync(0xffffffffu, ref, o);
+                tm = fmaxf(tm, x);
+                ref = fmaxf(ref, y);
             }
-            prefetch(item + stride);
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                tm = fmaxf(tm, t[u]);
-                if (id[u] >= 0 && z[u] < INFINITY) ref = fmaxf(ref, z[u]);
-            }
-            for (uint32_t i = lane + 32 * U; i < a.kpad; i += 32) {
-                entry(row, i, more_id[i], more_e[i]);
-                place(more_id[i], more_e[i], more_z[i]);
-                tm = fmaxf(tm, more_e[i]);
-                if (more_id[i] >= 0 && more_z[i] < INFINITY) ref = fmaxf(ref, more_z[i]);
-            }
-            tm = finite_max(warp_max(tm));
-            if (FWD) ref = finite_max(warp_max(ref));
+            tm = finite_max(tm);
+            ref = finite_max(ref);
             if (BWD && k >= 2 && !__all_sync(0xffffffffu, distill_wait(a, sh, &sh.taught_free[slot], ((k >> 1) - 1) & 1, 8, item))) break;
             float ts = 0.0f, tu = 0.0f, dot = 0.0f, own = 0.0f;
             uint32_t kept = 0;
             auto weigh = [&](int eid, float et, float ez) {
-                const float u = (et - tm) / a.temperature;
-                const float e = eid == -1 ? 0.0f : expf(u);
+                const float u = (et - tm) * per_t;
+                const float e = eid == -1 ? 0.0f : ex2((et - tm) * a.to_log2);
                 ts += e;
                 const bool mine = e != 0.0f && eid >= 0;
                 if (FWD && e != 0.0f) tu += e * u;
@@ -469,36 +513,44 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
             };
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (32 * u < int(a.kpad)) weigh(id[u], t[u], z[u]);
+                if (32 * u < int(a.kpad)) weigh(now.id[u], now.t[u], now.z[u]);
             for (uint32_t i0 = 32 * U; i0 < a.kpad; i0 += 32) {
                 const uint32_t i = i0 + lane;
                 const bool in = i < a.kpad;
                 weigh(in ? more_id[i] : -1, in ? more_e[i] : 0.0f, in ? more_z[i] : 0.0f);
             }
-            ts = warp_sum(ts);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const float v0 = __shfl_xor_sync(0xffffffffu, ts, o);
+                if constexpr (FWD) {
+                    const float v1 = __shfl_xor_sync(0xffffffffu, tu, o), v2 = __shfl_xor_sync(0xffffffffu, dot, o),
+                                v3 = __shfl_xor_sync(0xffffffffu, own, o);
+                    tu += v1;
+                    dot += v2;
+                    own += v3;
+                }
+                ts += v0;
+            }
             if constexpr (BWD) {
                 if (kept % 4 && lane < int(4 - kept % 4)) id_s[slot * a.kpad + kept + lane] = -1;
                 if (lane == 0) {
                     sh.entries[slot] = ts != 0.0f ? kept : 0u;
                     sh.teacher_sum[slot] = ts;
-                    sh.weight[slot] = w;
-                    sh.row_max[slot] = st_m;
-                    sh.row_log_sum[slot] = st_ls;
+                    sh.weight[slot] = now.w;
+                    sh.row_max[slot] = now.max;
+                    sh.row_log_sum[slot] = now.log_sum;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sh.taught[slot]));
             }
             if constexpr (FWD) {
-                tu = warp_sum(tu);
-                dot = warp_sum(dot);
-                own = warp_sum(own);
                 // the slot's last contents have been used by every CTA of the row once the row before this one is complete
                 if (k >= 1 && !__all_sync(0xffffffffu, distill_wait(a, sh, &sh.sums_in[slot ^ 1], ((k - 1) >> 1) & 1, 9, item))) break;
                 if (lane == 0) mbar_arrive_expect_tx(smem_addr(&sh.sums_in[slot]), a.pieces * kDistillSumBytes);
                 if (lane < int(a.pieces)) {
                     const uint32_t bar = remote(smem_addr(&sh.sums_in[slot]), lane), at = remote(smem_addr(&sh.sums[slot].teacher[q][0]), lane);
                     send4(at, bar, make_float4(ref, dot, own, ts));
-                    send4(at + 16, bar, make_float4(tu, w, 0.0f, 0.0f));
+                    send4(at + 16, bar, make_float4(tu, now.w, 0.0f, 0.0f));
                 }
             }
         }
@@ -569,7 +621,7 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
 #pragma unroll
                     for (int i = 0; i < PAIRS; ++i) e[n * PAIRS + i] = Gr::pair(v, i);
                 }
-                edge = uint32_t(tid) < a.segments * 2 * VEC ? d->edge[tid] : -INFINITY;
+                edge = a.edges && uint32_t(tid) < a.segments * 2 * VEC ? d->edge[tid] : -INFINITY;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sh.empty[st]));
                 ++used;
@@ -610,7 +662,7 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
                         }
                     }
                 }
-                if (uint32_t(tid) < a.segments * 2 * VEC && d->edge_out[tid])
+                if (a.edges && uint32_t(tid) < a.segments * 2 * VEC && d->edge_out[tid])
                     Tr::store1(reinterpret_cast<void *>(uintptr_t(d->edge_out[tid])), 0, taught ? edge * g : 0.0f);
             };
             float row_m = 0.0f, inv = 0.0f, factor = 0.0f;
@@ -749,6 +801,9 @@ static cudaError_t distill_shape(const Launch &L, const DistillLaunch &N, Launch
     a.k = N.k;
     a.kpad = (N.k + 3) / 4 * 4;
     a.teacher_dtype = N.teacher_dtype;
+    constexpr uint32_t VEC = Traits<T>::VEC;
+    a.edges = a.s.q % VEC != 0 || a.s.rem != 0 || N.ld % VEC != 0;
+    for (int r = 0; r < L.p; ++r) a.edges = a.edges || uintptr_t(L.src[r]) % 16 != 0;
     a.wait_ns = L.wait_limit_ns > 0 ? L.wait_limit_ns : 2000000000LL;
     a.stall_test = L.stall_test;
     const uint32_t p = a.s.p, groups = widest_groups<T>(a.s);
