@@ -17,6 +17,7 @@ namespace ccl {
 
 constexpr int kBalanceThreads = 256;
 constexpr int kBalanceWarps = kBalanceThreads / 32;
+constexpr int kCountThreads = 1024;
 // Up to this many choices and counters in all, every CTA counts for itself
 // instead of waiting for a counting kernel.
 constexpr uint64_t kCountHereIds = 8192;
@@ -46,16 +47,16 @@ struct BalanceArgs {
 // A CTA counts in shared memory first: integer atomics, so any order gives
 // the same counts.
 template <int PM>
-__global__ void __launch_bounds__(kBalanceThreads) balance_count_kernel(const __grid_constant__ BalanceArgs<PM> a)
+__global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const __grid_constant__ BalanceArgs<PM> a)
 {
     extern __shared__ int hist[];
-    constexpr int BATCH = 4;
+    constexpr int BATCH = 8;
     const uint32_t r = blockIdx.y;
-    for (uint32_t e = threadIdx.x; e < a.experts; e += kBalanceThreads) hist[e] = 0;
+    for (uint32_t e = threadIdx.x; e < a.experts; e += kCountThreads) hist[e] = 0;
     grid_dependency_wait();
     grid_dependents_launch();
     __syncthreads();
-    const uint64_t first = uint64_t(blockIdx.x) * kBalanceThreads + threadIdx.x, stride = uint64_t(gridDim.x) * kBalanceThreads;
+    const uint64_t first = uint64_t(blockIdx.x) * kCountThreads + threadIdx.x, stride = uint64_t(gridDim.x) * kCountThreads;
     const uint64_t n = a.rows * a.k;
     const int32_t *ids = a.ids[r];
     for (uint64_t j = first; j < n; j += BATCH * stride) {
@@ -80,7 +81,7 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_count_kernel(const __
         a.cell_tokens[r] = int(a.rows);
     }
     __syncthreads();
-    for (uint32_t e = threadIdx.x; e < a.experts; e += kBalanceThreads)
+    for (uint32_t e = threadIdx.x; e < a.experts; e += kCountThreads)
         if (hist[e]) atomicAdd(&a.cells[uint64_t(r) * a.experts + e], hist[e]);
 }
 
@@ -134,32 +135,40 @@ __device__ __forceinline__ float balance_coefficients(const BalanceArgs<PM> &a, 
         atomicAdd(&sums[0], (unsigned long long)tokens[r]);
         if (writes) a.tokens[r] = tokens[r];
     }
-    unsigned long long mine = 0;
+    unsigned long long mine = 0, total = 0;    // total: of this thread's first expert
     for (uint32_t e = threadIdx.x; e < E; e += kBalanceThreads) {
-        unsigned total = 0;      // up to p (2^31 - 1): kept below in 64 bits where it can pass 32
-        unsigned long long wide = 0;
-        if (a.by_choices.d <= 0xffffffffu / kMaxRanks) {
+        unsigned long long t = 0;
 #pragma unroll 8
-            for (uint32_t r = 0; r < a.p; ++r) total += unsigned(cells[uint64_t(r) * E + e]);
-            wide = total;
-        } else {
-            for (uint32_t r = 0; r < a.p; ++r) wide += unsigned(cells[uint64_t(r) * E + e]);
-        }
+        for (uint32_t r = 0; r < a.p; ++r) t += unsigned(cells[uint64_t(r) * E + e]);
         if (writes)
             for (uint32_t r = 0; r < a.p; ++r) a.counts[uint64_t(r) * E + e] = cells[uint64_t(r) * E + e];
-        mine += wide;
+        if (e == threadIdx.x) total = t;
+        mine += t;
     }
     if (mine) atomicAdd(&sums[1], mine);
     __syncthreads();
-    const double n = double(sums[0]), mean = double(sums[1]) / double(E);
-    const double scale = sums[0] ? a.coef * double(E) / (double(a.k) * n * n) : 0.0;
-    for (uint32_t e = threadIdx.x; e < E; e += kBalanceThreads) {
-        unsigned long long total = 0;
-        for (uint32_t r = 0; r < a.p; ++r) total += unsigned(cells[uint64_t(r) * E + e]);
-        d_s[e] = float((double(total) - mean) * scale);
+    // One thread divides in fp64 (which this GPU does slowly): a_e = count_e scale, d_e = (E count_e - sum) scale / E.
+    // The difference is exact in 64-bit integers and is rounded once to fp32, its product with the scale a second time.
+    __shared__ float scale_s[2];
+    if (threadIdx.x == 0) {
+        const double n = double(sums[0]);
+        const double per = sums[0] ? a.coef / (double(a.k) * n * n) : 0.0;      // scale / E
+        scale_s[0] = float(per);
+        scale_s[1] = float(double(sums[1]) * per);                             // mean(a)
     }
     __syncthreads();
-    return float(mean * scale);
+    const float per = scale_s[0];
+    const long long sum = (long long)sums[1];
+    for (uint32_t e = threadIdx.x; e < E; e += kBalanceThreads) {
+        unsigned long long t = total;
+        if (e != threadIdx.x) {
+            t = 0;
+            for (uint32_t r = 0; r < a.p; ++r) t += unsigned(cells[uint64_t(r) * E + e]);
+        }
+        d_s[e] = float((long long)(t * E) - sum) * per;
+    }
+    __syncthreads();
+    return scale_s[1];
 }
 
 // The CTAs' sums: each leaves its pair, the last one adds the pairs in the
@@ -170,15 +179,13 @@ __device__ __forceinline__ void balance_finish(const BalanceArgs<PM> &a, float l
     __shared__ double red[2][kBalanceWarps];
     __shared__ bool last;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-    double s = lean, c = live;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, o);
-        c += __shfl_xor_sync(0xffffffffu, c, o);
-    }
+    for (int o = 16; o > 0; o >>= 1) lean += __shfl_xor_sync(0xffffffffu, lean, o);
+    live = __reduce_add_sync(0xffffffffu, live);
+    double s, c;
     if (lane == 0) {
-        red[0][warp] = s;
-        red[1][warp] = c;
+        red[0][warp] = lean;
+        red[1][warp] = live;
     }
     __syncthreads();
     const unsigned grid = gridDim.x * gridDim.y, me = blockIdx.y * gridDim.x + blockIdx.x;
@@ -238,25 +245,28 @@ __global__ void __launch_bounds__(kBalanceThreads, NV * Traits<T>::VEC > 16 ? 2 
     const uint32_t E = a.experts, r = blockIdx.y;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, l = lane % L;
     const bool fwd = a.pass & CCL_PASS_FORWARD, bwd = a.pass & CCL_PASS_BACKWARD;
-    const char *in = static_cast<const char *>(a.in[r]);
-    char *out = static_cast<char *>(a.out[r]);
     const uint8_t *valid = a.has_valid ? a.valid[r] : nullptr;
     const uint64_t stride = uint64_t(gridDim.x) * kBalanceWarps * RPW;
+    const uint64_t row_bytes = uint64_t(E) * S, hop = stride * row_bytes;
+    uint64_t t = (uint64_t(blockIdx.x) * kBalanceWarps + warp) * RPW + lane / L;   // this lane's row
+    const char *at = static_cast<const char *>(a.in[r]) + t * row_bytes + l * 16;
+    const ptrdiff_t to_out = static_cast<char *>(a.out[r]) - static_cast<const char *>(a.in[r]);
+    bool has[NV];       // group n of a row is this lane's
+#pragma unroll
+    for (int n = 0; n < NV; ++n) has[n] = uint32_t((n * L + l) * VEC) < E;
     bool on = false;
     uint4 raw[NV];
-    auto fetch = [&](uint64_t t) {
-        on = t < a.rows && (!valid || valid[t]);
+    auto fetch = [&](uint64_t row, const char *from) {
+        const bool in = row < a.rows;
+        on = in && (!valid || valid[row]);
 #pragma unroll
-        for (int n = 0; n < NV; ++n) {
-            const uint32_t col = (n * L + l) * VEC;
-            raw[n] = t < a.rows && col < E && in_bounds(col + VEC <= E, a.status, kSiteBalance, t) ? ld_coherent_v4(in + (t * E + col) * S)
-                                                                                                  : lowest_group<T>();
-        }
+        for (int n = 0; n < NV; ++n)
+            raw[n] = in && has[n] && in_bounds(uint32_t((n * L + l) * VEC) + VEC <= E, a.status, kSiteBalance, row) ? ld_coherent_v4(from + n * (L * 16))
+                                                                                                              : lowest_group<T>();
     };
     grid_dependency_wait();
     grid_dependents_launch();
-    uint64_t base = (uint64_t(blockIdx.x) * kBalanceWarps + warp) * RPW;
-    fetch(base + lane / L);
+    fetch(t, at);
     const float mean = balance_coefficients(a, d_s, reinterpret_cast<int *>(d_s + E));
     Pair d[NV * PAIRS];
 #pragma unroll
@@ -269,13 +279,12 @@ __global__ void __launch_bounds__(kBalanceThreads, NV * Traits<T>::VEC > 16 ? 2 
     const float up = bwd && a.dloss ? *a.dloss : 1.0f;
     float lean_sum = 0.0f;
     int live = 0;
-    for (; base < a.rows; base += stride) {
-        const uint64_t t = base + lane / L;
+    const uint64_t last = a.rows + lane / L;     // rows of a warp end together: its lanes leave together
+    for (; t < last; t += stride, at += hop) {
         uint4 v[NV];
-        const bool valid_row = on;
 #pragma unroll
-        for (int n = 0; n < NV; ++n) v[n] = valid_row ? raw[n] : lowest_group<T>();   // padding: p = 0, whatever it holds
-        fetch(t + stride);
+        for (int n = 0; n < NV; ++n) v[n] = on ? raw[n] : lowest_group<T>();   // padding: p = 0, whatever it holds
+        fetch(t + stride, at + hop);
         typename Gr::Max gm = Gr::lowest();
 #pragma unroll
         for (int n = 0; n < NV; ++n) gm = Gr::max(gm, v[n]);
@@ -284,20 +293,31 @@ __global__ void __launch_bounds__(kBalanceThreads, NV * Traits<T>::VEC > 16 ? 2 
         for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         m = finite_max(m);
         Pair x[NV * PAIRS], sum = {0.0f, 0.0f}, dot = {0.0f, 0.0f};
+        // 2^(x c - m c) in one step: the rounding of m c is the same for the whole row and divides out.  Where m c
+        // leaves fp32's range (a row of the type's lowest value), the difference comes first.
+        const float mc = m * kLog2e;
+        if (__all_sync(0xffffffffu, fabsf(mc) < INFINITY)) {
 #pragma unroll
-        for (int n = 0; n < NV; ++n)
+            for (int n = 0; n < NV; ++n)
 #pragma unroll
-            for (int i = 0; i < PAIRS; ++i) {
-                Pair &e = x[n * PAIRS + i];
-                e = ex2((Gr::pair(v[n], i) + Pair{-m, -m}) * Pair{kLog2e, kLog2e});
-                sum = sum + e;
-                dot = fma(e, d[n * PAIRS + i], dot);
-            }
+                for (int i = 0; i < PAIRS; ++i) x[n * PAIRS + i] = ex2(fma(Gr::pair(v[n], i), Pair{kLog2e, kLog2e}, Pair{-mc, -mc}));
+        } else {
+#pragma unroll
+            for (int n = 0; n < NV; ++n)
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) x[n * PAIRS + i] = ex2((Gr::pair(v[n], i) + Pair{-m, -m}) * Pair{kLog2e, kLog2e});
+        }
+#pragma unroll
+        for (int i = 0; i < NV * PAIRS; ++i) {
+            sum = sum + x[i];
+            dot = fma(x[i], d[i], dot);
+        }
         float s = sum.x + sum.y, w = dot.x + dot.y;
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) {
-            s += __shfl_xor_sync(0xffffffffu, s, o);
-            w += __shfl_xor_sync(0xffffffffu, w, o);
+            const float s2 = __shfl_xor_sync(0xffffffffu, s, o), w2 = __shfl_xor_sync(0xffffffffu, w, o);
+            s += s2;
+            w += w2;
         }
         const float inv = s == 0.0f ? 0.0f : __fdividef(1.0f, s);    // a row of nothing but -inf has no softmax: p = 0
         const float lean = w * inv;
@@ -309,12 +329,11 @@ __global__ void __launch_bounds__(kBalanceThreads, NV * Traits<T>::VEC > 16 ? 2 
             const Pair g = {inv * up, inv * up}, off = {-lean, -lean};
 #pragma unroll
             for (int n = 0; n < NV; ++n) {
-                const uint32_t col = (n * L + l) * VEC;
-                if (col >= E || !in_bounds(col + VEC <= E, a.status, kSiteBalance, t)) continue;
+                if (!has[n] || !in_bounds(uint32_t((n * L + l) * VEC) + VEC <= E, a.status, kSiteBalance, t)) continue;
                 Pair f[PAIRS];
 #pragma unroll
                 for (int i = 0; i < PAIRS; ++i) f[i] = (x[n * PAIRS + i] * (d[n * PAIRS + i] + off)) * g;
-                st_stream_v4(out + (t * E + col) * S, Gr::pack(f));
+                st_stream_v4(const_cast<char *>(at) + to_out + n * (L * 16), Gr::pack(f));
             }
         }
     }
@@ -427,11 +446,12 @@ static cudaError_t balance_shape(const Launch &L, const BalanceLaunch &N, Launch
         if (!scratch) err = cudaMemsetAsync(N.counts, 0, cells * 4, L.stream);
         if (!scratch && err == cudaSuccess) err = cudaMemsetAsync(N.tokens, 0, size_t(L.p) * 4, L.stream);
         if (err != cudaSuccess) return err;
-        const uint64_t want = (N.rows * N.k + 4 * kBalanceThreads - 1) / (4 * kBalanceThreads);
-        const uint64_t most = uint64_t(4 * L.num_sms) / uint64_t(L.p) + 1;
+        // one CTA per SM: every CTA ends with an atomic per expert it met
+        const uint64_t want = (N.rows * N.k + kCountThreads - 1) / kCountThreads;
+        const uint64_t most = uint64_t(L.num_sms) / uint64_t(L.p) + 1;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(unsigned(want < 1 ? 1 : want < most ? want : most), unsigned(L.p));
-        cfg.blockDim = dim3(kBalanceThreads);
+        cfg.blockDim = dim3(kCountThreads);
         cfg.dynamicSmemBytes = size_t(N.experts) * 4;
         cfg.stream = L.stream;
         cudaLaunchAttribute attr[1];

@@ -10,13 +10,16 @@
 // in fp32, rounded once to the element type.
 //
 // One CTA per (row, rank, slice of the rank's columns).  It starts the loads
-// of its groups, then scans the row's history once and counts the tokens that
-// fall into the slice in one counter per column in shared memory (integer
-// atomics, so any order gives the same counts), adds up the row's bias entries
-// in list order, and finishes its groups: a group that neither touches is
-// copied through its mask bits as it is.  A group that its mask forbids
-// altogether is not read, and in place an untouched one is not written.
-// Bytes: the logits once in and once out, plus the history once per slice (L2).
+// of the row's rules, of the first part of its history and of its own groups,
+// then counts the history's tokens that fall into the slice in one counter
+// per column in shared memory (integer atomics, so any order gives the same
+// counts), adds up the row's bias entries in list order (one warp), and
+// finishes its groups: one that neither touches is copied through its mask
+// bits as it is.  A group that its mask forbids altogether is not read, and in
+// place an untouched one is not written.  Counters are 16 bits wide where the
+// history is shorter than 2^15 tokens: half the shared memory to clear and to
+// read.  Bytes: the logits once in and once out, plus the history once per
+// slice (L2).
 #include "logits.cuh"
 
 namespace ccl {
@@ -51,22 +54,23 @@ __device__ __forceinline__ uint4 forbid(const uint4 &v, uint32_t allowed)
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <typename T, int PM, int THREADS, int NV>
+template <typename T, int PM, int THREADS, int NV, bool WIDE>
 __global__ void __launch_bounds__(THREADS) logit_rules_kernel(const __grid_constant__ RulesArgs<PM> a)
 {
     using Tr = Traits<T>;
-    constexpr int VEC = Tr::VEC, GROUPS = THREADS * NV;
+    constexpr int VEC = Tr::VEC, GROUPS = THREADS * NV, PER = WIDE ? 1 : 2;   // counters per word
     constexpr int CELLS = (GROUPS + 2) * VEC;       // a group's room before and after for the edges
+    static_assert(NV * VEC <= 32, "the mask bits of a thread fit one word");
     extern __shared__ uint4 smem4[];
     uint32_t *cnt = reinterpret_cast<uint32_t *>(smem4);
-    float *bias = reinterpret_cast<float *>(cnt + CELLS);
-    __shared__ uint32_t touched[GROUPS / 32];       // bit g: group g has a counter or a bias
+    float *bias = reinterpret_cast<float *>(cnt + CELLS / PER);
+    __shared__ uint32_t biased_groups[GROUPS / 32];       // bit g: group g has a bias entry
     const Shards<PM> &s = a.s;
     const uint32_t row32 = div_by(blockIdx.x, a.by_row), rest = blockIdx.x - row32 * a.by_row.d;
     const uint32_t rank = div_by(rest, a.by_slices), slice = rest - rank * a.slices;
     const uint64_t row = row32;
     const int tid = threadIdx.x;
-    const ShardRow<T> in(s.in[rank], s.ld, row, shard_width(s, rank)), out(s.out[rank], s.ld, row, in.width);
+    const ShardRow<T> in(s.in[rank], s.ld, row, shard_width(s, rank));
     const uint32_t whole = in.end - in.first;
     if (slice > 0 && slice * GROUPS >= whole) return;
     if (!in_bounds(row < s.rows && rank < s.p, s.status, kSiteRules, row)) return;
@@ -79,166 +83,198 @@ __global__ void __launch_bounds__(THREADS) logit_rules_kernel(const __grid_const
     const int edge = in.edge(tid, slice == 0, has_tail);
 
     const bool history = a.r.history != nullptr;
-    if (tid < GROUPS / 32) touched[tid] = 0;
+    if (tid < GROUPS / 32) biased_groups[tid] = 0;
+    if (history)
+        for (int i = tid; i < CELLS / PER / 4; i += THREADS) reinterpret_cast<uint4 *>(cnt)[i] = make_uint4(0, 0, 0, 0);
     grid_dependency_wait();
     grid_dependents_launch();
 
-    // the row's mask bits of this thread's groups, then their logits
-    const uint32_t *mask = nullptr;
-    const uint32_t words = (s.vocab + 31) / 32;
-    if (a.r.mask) {
-        const int64_t m = a.r.mask_index ? int64_t(a.r.mask_index[row]) : int64_t(row);
-        if (m >= 0 && m < int64_t(a.r.mask_rows)) mask = a.r.mask + uint64_t(m) * a.r.mask_ld;
-    }
-    constexpr uint32_t ALL = (1u << VEC) - 1;
-    uint32_t allowed[NV];
-    uint4 raw[NV];
+    // the row's rules, all loads at once, and the first tokens of its history whether they count or not
+    const int mask_at = a.r.mask && a.r.mask_index ? a.r.mask_index[row] : int(row);
+    constexpr int BATCH = 8;
+    const int ld = history ? int(a.r.history_ld) : 0;
+    const int32_t *h = a.r.history + row * a.r.history_ld;
+    int len = history && a.r.history_len ? a.r.history_len[row] : ld;
+    const int prompt = history && a.r.prompt_len ? a.r.prompt_len[row] : 0;
+    int bias_lo = a.r.bias_count ? a.r.bias_offsets[row] : 0, bias_hi = a.r.bias_count ? a.r.bias_offsets[row + 1] : 0;
+    const float rep = a.r.repetition ? a.r.repetition[row] : 1.0f;
+    const float freq = a.r.frequency ? a.r.frequency[row] : 0.0f;
+    const float pres = a.r.presence ? a.r.presence[row] : 0.0f;
+    int32_t token[BATCH];
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const uint32_t j = j0 + tid + n * THREADS;
-        allowed[n] = ALL;
-        if (mask && j < j1) {
-            const uint32_t v = token0 + j * VEC - in.shift, w = v >> 5;
-            const uint32_t lo = mask[w], hi = w + 1 < words ? mask[w + 1] : 0u;
-            allowed[n] = __funnelshift_r(lo, hi, v & 31) & ALL;
+    for (int k = 0; k < BATCH; ++k) token[k] = tid + k * THREADS < ld ? h[tid + k * THREADS] : -1;
+
+    // the mask bits of this thread's groups, VEC for each, then the logits of those that have any
+    const uint32_t *mask = a.r.mask && mask_at >= 0 && uint64_t(mask_at) < a.r.mask_rows ? a.r.mask + uint64_t(mask_at) * a.r.mask_ld : nullptr;
+    constexpr uint32_t ALL = (1u << VEC) - 1;
+    uint32_t allowed = 0xffffffffu;
+    if (mask) {
+        const uint32_t words = (s.vocab + 31) / 32;
+        const uint32_t v0 = token0 + (j0 + tid) * VEC - in.shift;
+        uint32_t lo[NV], hi[NV];
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const uint32_t w = (v0 + n * THREADS * VEC) >> 5;
+            const bool is = j0 + tid + n * THREADS < j1;
+            lo[n] = is ? mask[w] : 0u;
+            hi[n] = is && w + 1 < words ? mask[w + 1] : 0u;
         }
+        allowed = 0;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) allowed |= (__funnelshift_r(lo[n], hi[n], (v0 + n * THREADS * VEC) & 31) & ALL) << (n * VEC);
     }
+    uint4 raw[NV];
     auto fetch = [&]() {
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const uint32_t j = j0 + tid + n * THREADS;
-            if (j < j1 && allowed[n]) raw[n] = ld_coherent_v4(in.group(j));
+            if (j < j1 && (allowed >> (n * VEC)) & ALL) raw[n] = ld_coherent_v4(in.group(j));
             else raw[n] = lowest_group<T>();
         }
     };
     if (!a.in_place) fetch();
     const float edge_x = edge >= 0 ? in.column(edge) : 0.0f;
 
-    int64_t bias_lo = 0, bias_hi = 0;
     if (a.r.bias_count) {
-        const int64_t n = int64_t(a.r.bias_count);
-        bias_lo = a.r.bias_offsets[row], bias_hi = a.r.bias_offsets[row + 1];
+        const int n = int(a.r.bias_count);
         bias_lo = bias_lo < 0 ? 0 : bias_lo > n ? n : bias_lo;
         bias_hi = bias_hi < bias_lo ? bias_lo : bias_hi > n ? n : bias_hi;
     }
     const bool biased = bias_hi > bias_lo;
-    int len = 0, prompt = 0;
-    if (history) {
-        const int ld = int(a.r.history_ld);
-        len = a.r.history_len ? a.r.history_len[row] : ld;
-        len = len < 0 ? 0 : len > ld ? ld : len;
-        prompt = a.r.prompt_len ? a.r.prompt_len[row] : 0;
-    }
-    if (len)
-        for (int i = tid; i < CELLS / 4; i += THREADS) reinterpret_cast<uint4 *>(cnt)[i] = make_uint4(0, 0, 0, 0);
-    if (biased)
-        for (int i = tid; i < CELLS / 4; i += THREADS) reinterpret_cast<uint4 *>(bias)[i] = make_uint4(0, 0, 0, 0);
+    len = len < 0 ? 0 : len > ld ? ld : len;
     __syncthreads();
-    auto touch = [&](int cell) {
-        const int g = cell / VEC - 1;
-        if (g >= 0 && g < GROUPS) atomicOr(&touched[g / 32], 1u << (g % 32));
-    };
-    if (len) {
-        const int32_t *h = a.r.history + row * a.r.history_ld;
-        auto count = [&](uint32_t token, int j) {
-            const uint32_t c = token - token0;
-            if (c - c0 >= c1 - c0) return;           // another slice's; also a negative token, or one past the vocabulary
-            const int cell = int(c) - cell0;
-            if (j < prompt) atomicOr(&cnt[cell], kSeenPrompt);
-            else atomicAdd(&cnt[cell], kGenerated);
-            touch(cell);
-        };
-        // eight loads in flight a thread
-        constexpr int BATCH = 8;
-        int j = tid;
-        for (; j + (BATCH - 1) * THREADS < len; j += BATCH * THREADS) {
-            int32_t t[BATCH];
+    // the sums of the groups that a bias entry falls into, and of the edges, begin at zero
+    if (biased) {
+        const int tail = VEC + int(j1 - j0) * VEC;
+        if (tid < VEC) bias[tid] = 0.0f;
+        else if (tid < 2 * VEC) bias[tail + tid - VEC] = 0.0f;
+        for (int k = bias_lo + tid; k < bias_hi; k += THREADS) {
+            const uint32_t c = uint32_t(a.r.bias_tokens[k]) - token0;
+            if (c - c0 >= c1 - c0) continue;
+            const int g = (int(c) - cell0) / VEC - 1;
+            if (g < 0 || g >= int(j1 - j0)) continue;
+            atomicOr(&biased_groups[g / 32], 1u << (g % 32));
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k) t[k] = __ldg(h + j + k * THREADS);
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) count(uint32_t(t[k]), j + k * THREADS);
+            for (int i = 0; i < VEC; ++i) bias[(g + 1) * VEC + i] = 0.0f;
         }
-        int32_t t[BATCH];
-#pragma unroll
-        for (int k = 0; k < BATCH - 1; ++k) t[k] = j + k * THREADS < len ? __ldg(h + j + k * THREADS) : -1;
-#pragma unroll
-        for (int k = 0; k < BATCH - 1; ++k)
-            if (j + k * THREADS < len) count(uint32_t(t[k]), j + k * THREADS);
+        __syncthreads();
     }
-    if (biased && tid < 32) {
+    if (len) {
+        auto count = [&](uint32_t v, int j) {
+            const uint32_t c = v - token0;
+            if (c - c0 >= c1 - c0 || j >= len) return;       // another slice's; also a negative token, or one past the vocabulary
+            const int cell = int(c) - cell0;
+            const int at = WIDE ? cell : cell / 2, sh = WIDE ? 0 : (cell % 2) * 16;
+            if (j < prompt) atomicOr(&cnt[at], kSeenPrompt << sh);
+            else atomicAdd(&cnt[at], kGenerated << sh);
+        };
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k) count(uint32_t(token[k]), tid + k * THREADS);
+        for (int j = tid + BATCH * THREADS; j < len; j += BATCH * THREADS) {
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) token[k] = j + k * THREADS < len ? h[j + k * THREADS] : -1;
+#pragma unroll
+            for (int k = 0; k < BATCH; ++k) count(uint32_t(token[k]), j + k * THREADS);
+        }
+    }
+    if (biased && tid >= THREADS - 32) {
         // one warp, 32 entries at a time: entries of one token add in list order
-        for (int64_t b = bias_lo; b < bias_hi; b += 32) {
-            const int64_t k = b + tid;
-            const uint32_t c = k < bias_hi ? uint32_t(a.r.bias_tokens[k]) - token0 : 0xffffffffu;
-            const bool mine = k < bias_hi && c - c0 < c1 - c0;
-            if (!__any_sync(0xffffffffu, mine)) continue;
-            const float add = mine ? a.r.bias_values[k] : 0.0f;
-            const unsigned same = __match_any_sync(0xffffffffu, mine ? c : 0xffffffffu);
-            const int turn = mine ? __popc(same & ((1u << tid) - 1)) : -1;
-            const int cell = mine ? int(c) - cell0 : 0;
-            for (int t = 0; __any_sync(0xffffffffu, turn >= t); ++t) {
-                if (turn == t) bias[cell] = __fadd_rn(bias[cell], add);
-                __syncwarp();
+        const int lane = tid % 32;
+        constexpr int AHEAD = 4;
+        for (int b = bias_lo; b < bias_hi; b += 32 * AHEAD) {
+            uint32_t col[AHEAD];
+            float add[AHEAD];
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                const int k = b + 32 * u + lane;
+                col[u] = k < bias_hi ? uint32_t(a.r.bias_tokens[k]) - token0 : 0xffffffffu;
+                add[u] = k < bias_hi ? a.r.bias_values[k] : 0.0f;
             }
-            if (mine) touch(cell);
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                const bool mine = b + 32 * u + lane < bias_hi && col[u] - c0 < c1 - c0;
+                if (!__any_sync(0xffffffffu, mine)) continue;
+                const unsigned same = __match_any_sync(0xffffffffu, mine ? col[u] : 0xffffffffu);
+                const int turn = mine ? __popc(same & ((1u << lane) - 1)) : -1;
+                const int cell = mine ? int(col[u]) - cell0 : 0;
+                for (int t = 0; __any_sync(0xffffffffu, turn >= t); ++t) {
+                    if (turn == t) bias[cell] = __fadd_rn(bias[cell], add[u]);
+                    __syncwarp();
+                }
+            }
         }
     }
     __syncthreads();
 
-    const float rep = a.r.repetition ? a.r.repetition[row] : 1.0f;
-    const float freq = a.r.frequency ? a.r.frequency[row] : 0.0f;
-    const float pres = a.r.presence ? a.r.presence[row] : 0.0f;
-    auto apply = [&](float x, int cell) -> float {
-        const uint32_t c = len ? cnt[cell] : 0u;
-        const float b = biased ? bias[cell] : 0.0f;
+    auto apply = [&](float x, uint32_t c, float b) -> float {
         if (b != 0.0f) x = __fadd_rn(x, b);
         if (c) x = x > 0.0f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
         if (c >= kGenerated) x = __fsub_rn(__fsub_rn(x, __fmul_rn(freq, float(c >> 1))), pres);
         return x;
     };
+    const ShardRow<T> out(s.out[rank], s.ld, row, in.width);
     if (a.in_place) fetch();
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
         const int g = tid + n * THREADS;
-        const uint32_t j = j0 + g;
+        const uint32_t j = j0 + g, ok = (allowed >> (n * VEC)) & ALL;
         if (j >= j1) break;
         uint4 v = raw[n];
-        const bool any = (touched[g / 32] >> (g % 32)) & 1;
-        if (any && allowed[n]) {
-            float x[VEC];
-            Tr::unpack(v, x);
+        bool changed = ok != ALL;
+        if (ok) {
+            constexpr int WORDS = VEC / PER;
+            uint32_t c[WORDS], any = 0;
+            if (len) {
+                const uint32_t *at = cnt + (g + 1) * WORDS;
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) x[i] = apply(x[i], (g + 1) * VEC + i);
-            v = Tr::pack(x);
-        } else if (a.in_place && allowed[n] == ALL) {
-            continue;
+                for (int i = 0; i < WORDS; ++i) {
+                    c[i] = at[i];
+                    any |= c[i];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < WORDS; ++i) c[i] = 0;
+            }
+            const bool sums = biased && (biased_groups[g / 32] >> (g % 32)) & 1;
+            if (any || sums) {
+                float x[VEC];
+                Tr::unpack(v, x);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i)
+                    x[i] = apply(x[i], WIDE ? c[i] : (c[i / PER] >> (16 * (i % PER))) & 0xffffu, sums ? bias[(g + 1) * VEC + i] : 0.0f);
+                v = Tr::pack(x);
+                changed = true;
+            }
         }
-        if (allowed[n] != ALL) v = forbid<T>(v, allowed[n]);
+        if (a.in_place && !changed) continue;
+        if (ok != ALL) v = forbid<T>(v, ok);
         store_group<T>(out, in, j, v);
     }
     if (edge >= 0) {
         const uint32_t v = token0 + edge;
         const bool ok = !mask || (mask[v >> 5] >> (v & 31)) & 1;
-        out.set_column(edge, ok ? apply(edge_x, edge - cell0) : -INFINITY);
+        const int cell = edge - cell0;
+        const uint32_t c = !len ? 0u : WIDE ? cnt[cell] : (cnt[cell / 2] >> (16 * (cell % 2))) & 0xffffu;
+        out.set_column(edge, ok ? apply(edge_x, c, biased ? bias[cell] : 0.0f) : -INFINITY);
     }
 }
 
-template <typename T, int PM, int THREADS, int NV>
+template <typename T, int PM, int THREADS, int NV, bool WIDE>
 static cudaError_t rules_launch(const Launch &L, RulesArgs<PM> &a, uint32_t groups, LaunchInfo *info)
 {
     constexpr uint32_t GROUPS = THREADS * NV;
-    constexpr size_t table = size_t(GROUPS + 2) * Traits<T>::VEC * 4;
+    constexpr size_t cells = size_t(GROUPS + 2) * Traits<T>::VEC, counters = cells * (WIDE ? 4 : 2);
     a.slices = groups ? (groups + GROUPS - 1) / GROUPS : 1;
     const uint64_t per_row = uint64_t(a.slices) * a.s.p;
     if (a.s.rows * per_row > 0x7fffffffull) return cudaErrorInvalidValue;
     a.by_row = fast_div(uint32_t(per_row));
     a.by_slices = fast_div(a.slices);
-    const size_t smem = (a.r.bias_count ? 2 : 1) * table;
+    const size_t smem = counters + (a.r.bias_count ? cells * 4 : 0);
     static std::atomic<unsigned long long> done{0};
-    cudaError_t err = allow_dynamic_smem(logit_rules_kernel<T, PM, THREADS, NV>, 2 * table, L.device, done);
+    cudaError_t err = allow_dynamic_smem(logit_rules_kernel<T, PM, THREADS, NV, WIDE>, counters + cells * 4, L.device, done);
     if (err != cudaSuccess) return err;
     const unsigned grid = unsigned(a.s.rows * per_row);
-    err = launch_dependent(logit_rules_kernel<T, PM, THREADS, NV>, grid, THREADS, smem, L.stream, a);
+    err = launch_dependent(logit_rules_kernel<T, PM, THREADS, NV, WIDE>, grid, THREADS, smem, L.stream, a);
     if (err != cudaSuccess) return err;
     info->kernel = "logit_rules";
     info->grid = int(grid);
@@ -248,7 +284,7 @@ static cudaError_t rules_launch(const Launch &L, RulesArgs<PM> &a, uint32_t grou
     return cudaGetLastError();
 }
 
-template <typename T, int PM>
+template <typename T, int PM, bool WIDE>
 static cudaError_t rules_shape(const Launch &L, const RulesLaunch &N, LaunchInfo *info)
 {
     constexpr int PER16 = Traits<T>::VEC == 8 ? 1 : 2;   // groups that hold eight elements
@@ -257,14 +293,18 @@ static cudaError_t rules_shape(const Launch &L, const RulesLaunch &N, LaunchInfo
     a.r = *N.rules;
     a.in_place = L.alias ? 1 : 0;
     const uint32_t groups = widest_groups<T>(a.s);
-    if (N.rows * a.s.p * uint64_t(groups) < uint64_t(L.num_sms) * 1024 * PER16) return rules_launch<T, PM, 128, PER16>(L, a, groups, info);
-    return rules_launch<T, PM, 512, 2 * PER16>(L, a, groups, info);
+    if (N.rows * a.s.p * uint64_t(groups) < uint64_t(L.num_sms) * 1024 * PER16)
+        return rules_launch<T, PM, 128, PER16, WIDE>(L, a, groups, info);
+    return rules_launch<T, PM, 256, 4 * PER16, WIDE>(L, a, groups, info);
 }
 
 template <typename T>
 static cudaError_t rules_dtype(const Launch &L, const RulesLaunch &N, LaunchInfo *info)
 {
-    return L.p <= 8 ? rules_shape<T, 8>(L, N, info) : rules_shape<T, kMaxRanks>(L, N, info);
+    // a 16-bit counter holds twice the occurrences plus one
+    const bool wide = N.rules->history && N.rules->history_ld > 32767;
+    if (wide) return L.p <= 8 ? rules_shape<T, 8, true>(L, N, info) : rules_shape<T, kMaxRanks, true>(L, N, info);
+    return L.p <= 8 ? rules_shape<T, 8, false>(L, N, info) : rules_shape<T, kMaxRanks, false>(L, N, info);
 }
 
 cudaError_t launch_logit_rules(const Launch &L, const RulesLaunch &N, LaunchInfo *info)

@@ -155,6 +155,16 @@ def test_large_batches_take_the_wide_slices(dtype):
     check(x, 2, dtype, make_rules(rows, vocab, 4, 500, 20, True), in_place=True)
 
 
+@pytest.mark.parametrize("history", [32767, 32768, 70000])
+def test_a_token_repeated_through_a_long_history(history):
+    """Counts around what a 16-bit counter holds, beside a neighbour that must not feel them."""
+    a = make_rules(2, 300, 4).h
+    a["history"] = np.full((2, history), 7, dtype=np.int32)
+    a["history"][1, ::2] = 6
+    a["prompt_len"] = np.array([0, 5], dtype=np.int32)
+    check(rng(6).normal(0, 4, (2, 300)), 1, "f32", Rules(**a))
+
+
 def test_each_rule_alone_and_none():
     rows, vocab = 5, 700
     x = rng(3).normal(0, 4, (rows, vocab))
