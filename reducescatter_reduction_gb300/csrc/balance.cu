@@ -90,10 +90,9 @@ __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const __gr
 template <int PM>
 __device__ __forceinline__ float balance_coefficients(const BalanceArgs<PM> &a, float *d_s, int *hist)
 {
-    __shared__ unsigned long long sums[2];
+    __shared__ unsigned long long parts[2][kBalanceWarps];   // valid rows, choices
     const uint32_t E = a.experts;
     const int32_t *cells = a.cells, *tokens = a.cell_tokens;
-    if (threadIdx.x < 2) sums[threadIdx.x] = 0;
     if (a.count_here) {
         int *rows_s = hist + a.p * E;
         for (uint32_t i = threadIdx.x; i < a.p * E + a.p; i += kBalanceThreads) hist[i] = 0;
@@ -131,11 +130,11 @@ __device__ __forceinline__ float balance_coefficients(const BalanceArgs<PM> &a, 
     __syncthreads();
     // sums of integers: any order gives the same
     const bool writes = a.cells != a.counts && blockIdx.x == 0 && blockIdx.y == 0;
+    unsigned long long rows = 0, mine = 0, total = 0;    // total: of this thread's first expert
     for (uint32_t r = threadIdx.x; r < a.p; r += kBalanceThreads) {
-        atomicAdd(&sums[0], (unsigned long long)tokens[r]);
+        rows += unsigned(tokens[r]);
         if (writes) a.tokens[r] = tokens[r];
     }
-    unsigned long long mine = 0, total = 0;    // total: of this thread's first expert
     for (uint32_t e = threadIdx.x; e < E; e += kBalanceThreads) {
         unsigned long long t = 0;
 #pragma unroll 8
@@ -145,20 +144,34 @@ __device__ __forceinline__ float balance_coefficients(const BalanceArgs<PM> &a, 
         if (e == threadIdx.x) total = t;
         mine += t;
     }
-    if (mine) atomicAdd(&sums[1], mine);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        rows += __shfl_xor_sync(0xffffffffu, rows, o);
+        mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    }
+    if (threadIdx.x % 32 == 0) {
+        parts[0][threadIdx.x / 32] = rows;
+        parts[1][threadIdx.x / 32] = mine;
+    }
     __syncthreads();
+    unsigned long long all_rows = 0, all = 0;
+#pragma unroll
+    for (int w = 0; w < kBalanceWarps; ++w) {
+        all_rows += parts[0][w];
+        all += parts[1][w];
+    }
     // One thread divides in fp64 (which this GPU does slowly): a_e = count_e scale, d_e = (E count_e - sum) scale / E.
     // The difference is exact in 64-bit integers and is rounded once to fp32, its product with the scale a second time.
     __shared__ float scale_s[2];
     if (threadIdx.x == 0) {
-        const double n = double(sums[0]);
-        const double per = sums[0] ? a.coef / (double(a.k) * n * n) : 0.0;      // scale / E
+        const double n = double(all_rows);
+        const double per = all_rows ? a.coef / (double(a.k) * n * n) : 0.0;     // scale / E
         scale_s[0] = float(per);
-        scale_s[1] = float(double(sums[1]) * per);                             // mean(a)
+        scale_s[1] = float(double(all) * per);                                 // mean(a)
     }
     __syncthreads();
     const float per = scale_s[0];
-    const long long sum = (long long)sums[1];
+    const long long sum = (long long)all;
     for (uint32_t e = threadIdx.x; e < E; e += kBalanceThreads) {
         unsigned long long t = total;
         if (e != threadIdx.x) {

@@ -29,9 +29,15 @@ struct RulesArgs {
     Shards<PM> s;
     ccl_logit_rules_t r;
     uint32_t slices;            // per rank
-    FastDiv by_row, by_slices;  // CTAs per row, slices per rank
+    uint32_t cluster;           // CTAs that share the scan of a row's history
+    FastDiv by_row, by_slices;  // CTAs per row (whole clusters), slices per rank
     int in_place;
 };
+
+// From this many tokens on, the CTAs of a cluster share the scan of a row's
+// history; below, each scans it all and saves the cluster's barriers.
+constexpr size_t kShareHistory = 1024;
+constexpr uint32_t kScanCluster = 8;
 
 // Generated occurrences sit above bit 0, bit 0 says "in the prompt".
 constexpr uint32_t kSeenPrompt = 1, kGenerated = 2;
@@ -65,33 +71,51 @@ __global__ void __launch_bounds__(THREADS) logit_rules_kernel(const __grid_const
     uint32_t *cnt = reinterpret_cast<uint32_t *>(smem4);
     float *bias = reinterpret_cast<float *>(cnt + CELLS / PER);
     __shared__ uint32_t biased_groups[GROUPS / 32];       // bit g: group g has a bias entry
+    __shared__ uint32_t list_cell[THREADS], list_count[THREADS / 32];
+    __shared__ float list_value[THREADS];
+    __shared__ uint32_t head_s[PM], last_s[PM];           // a rank's head, its last slice (shared scan)
     const Shards<PM> &s = a.s;
-    const uint32_t row32 = div_by(blockIdx.x, a.by_row), rest = blockIdx.x - row32 * a.by_row.d;
-    const uint32_t rank = div_by(rest, a.by_slices), slice = rest - rank * a.slices;
+    const uint32_t row32 = div_by(blockIdx.x, a.by_row), mine = blockIdx.x - row32 * a.by_row.d;
+    const uint32_t rank_of_mine = div_by(mine, a.by_slices), slice = mine - rank_of_mine * a.slices;
     const uint64_t row = row32;
     const int tid = threadIdx.x;
+    const bool shared_scan = a.cluster > 1;
+    bool here = rank_of_mine < s.p;                       // else: only in the scan
+    const uint32_t rank = here ? rank_of_mine : 0;
     const ShardRow<T> in(s.in[rank], s.ld, row, shard_width(s, rank));
     const uint32_t whole = in.end - in.first;
-    if (slice > 0 && slice * GROUPS >= whole) return;
-    if (!in_bounds(row < s.rows && rank < s.p, s.status, kSiteRules, row)) return;
-    const uint32_t j0 = in.first + slice * GROUPS, j1 = min(j0 + GROUPS, in.end);
-    const bool has_tail = j1 == in.end;
+    here = here && (slice == 0 || slice * GROUPS < whole) && in_bounds(row < s.rows, s.status, kSiteRules, row);
+    if (!here && !shared_scan) return;
+    const uint32_t j0 = in.first + min(slice * GROUPS, whole), j1 = here ? min(j0 + GROUPS, in.end) : j0;
+    const bool has_tail = here && j1 == in.end;
     // the slice's columns are [c0, c1); column c has cell c - cell0
-    const uint32_t c0 = slice == 0 ? 0 : in.head() + slice * GROUPS * VEC, c1 = has_tail ? in.width : in.head() + (j1 - in.first) * VEC;
+    const uint32_t c0 = slice == 0 ? 0 : in.head() + slice * GROUPS * VEC, c1 = !here ? c0 : has_tail ? in.width : in.head() + (j1 - in.first) * VEC;
     const int cell0 = int(in.head() + slice * GROUPS * VEC) - VEC;
     const uint32_t token0 = shard_begin(s, rank);
-    const int edge = in.edge(tid, slice == 0, has_tail);
+    const int edge = here ? in.edge(tid, slice == 0, has_tail) : -1;
 
     const bool history = a.r.history != nullptr;
     if (tid < GROUPS / 32) biased_groups[tid] = 0;
     if (history)
         for (int i = tid; i < CELLS / PER / 4; i += THREADS) reinterpret_cast<uint4 *>(cnt)[i] = make_uint4(0, 0, 0, 0);
+    if (shared_scan) {
+        if (tid < int(s.p)) {
+            const ShardRow<T> sr(s.in[tid], s.ld, row, shard_width(s, tid));
+            head_s[tid] = sr.head();
+            last_s[tid] = sr.end > sr.first ? (sr.end - sr.first - 1) / GROUPS : 0;
+        }
+        // every counter of the cluster is zero before anyone counts
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    }
     grid_dependency_wait();
     grid_dependents_launch();
 
     // the row's rules, all loads at once, and the first tokens of its history whether they count or not
     const int mask_at = a.r.mask && a.r.mask_index ? a.r.mask_index[row] : int(row);
-    constexpr int BATCH = 8;
+    constexpr int BATCH = THREADS <= 128 ? 8 : 4;
+    const uint32_t scan_rank = shared_scan ? mine % a.cluster : 0, scan_step = THREADS * a.cluster;
+    const int scan0 = int(scan_rank) * THREADS + tid;
     const int ld = history ? int(a.r.history_ld) : 0;
     const int32_t *h = a.r.history + row * a.r.history_ld;
     int len = history && a.r.history_len ? a.r.history_len[row] : ld;
@@ -102,7 +126,7 @@ __global__ void __launch_bounds__(THREADS) logit_rules_kernel(const __grid_const
     const float pres = a.r.presence ? a.r.presence[row] : 0.0f;
     int32_t token[BATCH];
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k) token[k] = tid + k * THREADS < ld ? h[tid + k * THREADS] : -1;
+    for (int k = 0; k < BATCH; ++k) token[k] = scan0 + k * scan_step < ld ? h[scan0 + k * scan_step] : -1;
 
     // the mask bits of this thread's groups, VEC for each, then the logits of those that have any
     const uint32_t *mask = a.r.mask && mask_at >= 0 && uint64_t(mask_at) < a.r.mask_rows ? a.r.mask + uint64_t(mask_at) * a.r.mask_ld : nullptr;
@@ -140,71 +164,98 @@ __global__ void __launch_bounds__(THREADS) logit_rules_kernel(const __grid_const
         bias_lo = bias_lo < 0 ? 0 : bias_lo > n ? n : bias_lo;
         bias_hi = bias_hi < bias_lo ? bias_lo : bias_hi > n ? n : bias_hi;
     }
-    const bool biased = bias_hi > bias_lo;
+    const bool biased = here && bias_hi > bias_lo;
     len = len < 0 ? 0 : len > ld ? ld : len;
-    __syncthreads();
-    // the sums of the groups that a bias entry falls into, and of the edges, begin at zero
-    if (biased) {
-        const int tail = VEC + int(j1 - j0) * VEC;
-        if (tid < VEC) bias[tid] = 0.0f;
-        else if (tid < 2 * VEC) bias[tail + tid - VEC] = 0.0f;
-        for (int k = bias_lo + tid; k < bias_hi; k += THREADS) {
-            const uint32_t c = uint32_t(a.r.bias_tokens[k]) - token0;
-            if (c - c0 >= c1 - c0) continue;
-            const int g = (int(c) - cell0) / VEC - 1;
-            if (g < 0 || g >= int(j1 - j0)) continue;
-            atomicOr(&biased_groups[g / 32], 1u << (g % 32));
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) bias[(g + 1) * VEC + i] = 0.0f;
-        }
-        __syncthreads();
+    uint32_t bias_col = 0xffffffffu;      // this thread's entry of the first THREADS
+    float bias_add = 0.0f;
+    if (biased && bias_lo + tid < bias_hi) {
+        bias_col = uint32_t(a.r.bias_tokens[bias_lo + tid]) - token0;
+        bias_add = a.r.bias_values[bias_lo + tid];
     }
+    __syncwarp();
+    if (shared_scan) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    else __syncthreads();
     if (len) {
+        auto count_at = [&](uint32_t at, int cell, int j) {
+            // cell's counter in the shared memory at `at` (a cluster address)
+            const uint32_t word = at + uint32_t(WIDE ? cell : cell / 2) * 4, sh = WIDE ? 0 : (cell % 2) * 16;
+            if (j < prompt) asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(word), "r"(kSeenPrompt << sh) : "memory");
+            else asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(word), "r"(kGenerated << sh) : "memory");
+        };
+        const uint32_t cnt_at = uint32_t(__cvta_generic_to_shared(cnt));
         auto count = [&](uint32_t v, int j) {
-            const uint32_t c = v - token0;
-            if (c - c0 >= c1 - c0 || j >= len) return;       // another slice's; also a negative token, or one past the vocabulary
-            const int cell = int(c) - cell0;
-            const int at = WIDE ? cell : cell / 2, sh = WIDE ? 0 : (cell % 2) * 16;
-            if (j < prompt) atomicOr(&cnt[at], kSeenPrompt << sh);
-            else atomicAdd(&cnt[at], kGenerated << sh);
+            if (j >= len) return;
+            if (!shared_scan) {
+                const uint32_t c = v - token0;
+                if (c - c0 < c1 - c0) count_at(cnt_at, int(c) - cell0, j);   // else another slice's, or no token
+                return;
+            }
+            if (v >= s.vocab) return;
+            const uint32_t r = rank_of_token(s, v), c = v - shard_begin(s, r), head = head_s[r];
+            const uint32_t sl = c < head ? 0u : min((c - head) / (GROUPS * VEC), last_s[r]);
+            const uint32_t to = r * a.slices + sl - (mine - scan_rank);
+            if (to >= a.cluster) return;                                     // another cluster's
+            uint32_t at;
+            asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(cnt_at), "r"(to));
+            count_at(at, int(c) - int(head + sl * GROUPS * VEC) + VEC, j);
         };
 #pragma unroll
-        for (int k = 0; k < BATCH; ++k) count(uint32_t(token[k]), tid + k * THREADS);
-        for (int j = tid + BATCH * THREADS; j < len; j += BATCH * THREADS) {
+        for (int k = 0; k < BATCH; ++k) count(uint32_t(token[k]), scan0 + k * scan_step);
+        for (int j = scan0 + BATCH * scan_step; j < len; j += BATCH * scan_step) {
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k) token[k] = j + k * THREADS < len ? h[j + k * THREADS] : -1;
+            for (int k = 0; k < BATCH; ++k) token[k] = j + k * scan_step < uint32_t(len) ? h[j + k * scan_step] : -1;
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k) count(uint32_t(token[k]), j + k * THREADS);
+            for (int k = 0; k < BATCH; ++k) count(uint32_t(token[k]), j + k * scan_step);
         }
     }
-    if (biased && tid >= THREADS - 32) {
-        // one warp, 32 entries at a time: entries of one token add in list order
-        const int lane = tid % 32;
-        constexpr int AHEAD = 4;
-        for (int b = bias_lo; b < bias_hi; b += 32 * AHEAD) {
-            uint32_t col[AHEAD];
-            float add[AHEAD];
-#pragma unroll
-            for (int u = 0; u < AHEAD; ++u) {
-                const int k = b + 32 * u + lane;
-                col[u] = k < bias_hi ? uint32_t(a.r.bias_tokens[k]) - token0 : 0xffffffffu;
-                add[u] = k < bias_hi ? a.r.bias_values[k] : 0.0f;
+    __syncwarp();
+    if (shared_scan) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    if (biased) {
+        // The sums of the edges begin at zero, those of a group when its first entry comes.
+        const int tail = VEC + int(j1 - j0) * VEC, lane = tid % 32;
+        if (tid < VEC) bias[tid] = 0.0f;
+        else if (tid < 2 * VEC) bias[tail + tid - VEC] = 0.0f;
+        for (int b = bias_lo; b < bias_hi; b += THREADS) {
+            // a block of entries: each warp lists those of the slice in order ...
+            if (b > bias_lo) {
+                const bool is = b + tid < bias_hi;
+                bias_col = is ? uint32_t(a.r.bias_tokens[b + tid]) - token0 : 0xffffffffu;
+                bias_add = is ? a.r.bias_values[b + tid] : 0.0f;
+                __syncthreads();      // the last block's list is done with
             }
+            const bool in_slice = b + tid < bias_hi && bias_col - c0 < c1 - c0;
+            const unsigned who = __ballot_sync(0xffffffffu, in_slice);
+            if (lane == 0) list_count[tid / 32] = __popc(who);
+            if (in_slice) {
+                const int cell = int(bias_col) - cell0, g = cell / VEC - 1, at = tid - lane + __popc(who & ((1u << lane) - 1));
+                list_cell[at] = uint32_t(cell);
+                list_value[at] = bias_add;
+                if (g >= 0 && g < int(j1 - j0) && !((atomicOr(&biased_groups[g / 32], 1u << (g % 32)) >> (g % 32)) & 1)) {
 #pragma unroll
-            for (int u = 0; u < AHEAD; ++u) {
-                const bool mine = b + 32 * u + lane < bias_hi && col[u] - c0 < c1 - c0;
-                if (!__any_sync(0xffffffffu, mine)) continue;
-                const unsigned same = __match_any_sync(0xffffffffu, mine ? col[u] : 0xffffffffu);
-                const int turn = mine ? __popc(same & ((1u << lane) - 1)) : -1;
-                const int cell = mine ? int(col[u]) - cell0 : 0;
+                    for (int i = 0; i < VEC; ++i) bias[(g + 1) * VEC + i] = 0.0f;
+                }
+            }
+            __syncthreads();
+            // ... and the last warp adds the lists up, entries of one token in list order
+            if (tid < THREADS - 32) continue;
+            for (int w = 0; w < THREADS / 32; ++w) {
+                const int n = int(list_count[w]);
+                if (n == 0) continue;
+                const uint32_t cell = lane < n ? list_cell[32 * w + lane] : 0xffffffffu;
+                const float add = lane < n ? list_value[32 * w + lane] : 0.0f;
+                const unsigned same = __match_any_sync(0xffffffffu, cell);
+                const int turn = lane < n ? __popc(same & ((1u << lane) - 1)) : -1;
                 for (int t = 0; __any_sync(0xffffffffu, turn >= t); ++t) {
-                    if (turn == t) bias[cell] = __fadd_rn(bias[cell], add[u]);
+                    if (turn == t) bias[cell] = __fadd_rn(bias[cell], add);
                     __syncwarp();
                 }
             }
         }
     }
+    __syncwarp();
+    if (shared_scan) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     __syncthreads();
+    if (!here) return;
 
     auto apply = [&](float x, uint32_t c, float b) -> float {
         if (b != 0.0f) x = __fadd_rn(x, b);
@@ -260,12 +311,17 @@ __global__ void __launch_bounds__(THREADS) logit_rules_kernel(const __grid_const
 }
 
 template <typename T, int PM, int THREADS, int NV, bool WIDE>
-static cudaError_t rules_launch(const Launch &L, RulesArgs<PM> &a, uint32_t groups, LaunchInfo *info)
+static cudaError_t rules_launch(const Launch &L, RulesArgs<PM> &a, uint32_t groups, bool share, LaunchInfo *info)
 {
     constexpr uint32_t GROUPS = THREADS * NV;
     constexpr size_t cells = size_t(GROUPS + 2) * Traits<T>::VEC, counters = cells * (WIDE ? 4 : 2);
     a.slices = groups ? (groups + GROUPS - 1) / GROUPS : 1;
-    const uint64_t per_row = uint64_t(a.slices) * a.s.p;
+    uint64_t per_row = uint64_t(a.slices) * a.s.p;
+    a.cluster = 1;
+    if (share && a.r.history && a.r.history_ld >= kShareHistory && per_row > 1) {
+        a.cluster = per_row < kScanCluster ? uint32_t(per_row) : kScanCluster;
+        per_row = (per_row + a.cluster - 1) / a.cluster * a.cluster;
+    }
     if (a.s.rows * per_row > 0x7fffffffull) return cudaErrorInvalidValue;
     a.by_row = fast_div(uint32_t(per_row));
     a.by_slices = fast_div(a.slices);
@@ -274,7 +330,21 @@ static cudaError_t rules_launch(const Launch &L, RulesArgs<PM> &a, uint32_t grou
     cudaError_t err = allow_dynamic_smem(logit_rules_kernel<T, PM, THREADS, NV, WIDE>, counters + cells * 4, L.device, done);
     if (err != cudaSuccess) return err;
     const unsigned grid = unsigned(a.s.rows * per_row);
-    err = launch_dependent(logit_rules_kernel<T, PM, THREADS, NV, WIDE>, grid, THREADS, smem, L.stream, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = L.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+    err = cudaLaunchKernelEx(&cfg, logit_rules_kernel<T, PM, THREADS, NV, WIDE>, a);
     if (err != cudaSuccess) return err;
     info->kernel = "logit_rules";
     info->grid = int(grid);
@@ -294,8 +364,8 @@ static cudaError_t rules_shape(const Launch &L, const RulesLaunch &N, LaunchInfo
     a.in_place = L.alias ? 1 : 0;
     const uint32_t groups = widest_groups<T>(a.s);
     if (N.rows * a.s.p * uint64_t(groups) < uint64_t(L.num_sms) * 1024 * PER16)
-        return rules_launch<T, PM, 128, PER16, WIDE>(L, a, groups, info);
-    return rules_launch<T, PM, 256, 4 * PER16, WIDE>(L, a, groups, info);
+        return rules_launch<T, PM, 128, PER16, WIDE>(L, a, groups, false, info);
+    return rules_launch<T, PM, 256, 4 * PER16, WIDE>(L, a, groups, true, info);
 }
 
 template <typename T>

@@ -155,6 +155,15 @@ def test_large_batches_take_the_wide_slices(dtype):
     check(x, 2, dtype, make_rules(rows, vocab, 4, 500, 20, True), in_place=True)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("p,rows,vocab,history,bias,layout", [
+    (2, 40, 150001, 3000, 20, {}), (8, 40, 131072, 9000, 700, {}), (3, 60, 100003, 1024, 1, dict(offset=3)),
+    (1, 30, 200001, 40000, 5, dict(in_place=True)), (16, 60, 90011, 5000, 64, dict(offset=[0, 1] * 8)), (5, 400, 16000, 2000, 0, {})])
+def test_long_histories_are_scanned_by_a_cluster(dtype, p, rows, vocab, history, bias, layout):
+    x = rng(vocab).normal(0, 4, (rows, vocab))
+    check(x, p, dtype, make_rules(rows, vocab, 7, history, bias, True), **layout)
+
+
 @pytest.mark.parametrize("history", [32767, 32768, 70000])
 def test_a_token_repeated_through_a_long_history(history):
     """Counts around what a 16-bit counter holds, beside a neighbour that must not feel them."""
