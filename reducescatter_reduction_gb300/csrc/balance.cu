@@ -494,7 +494,9 @@ static cudaError_t balance_shape(const Launch &L, const BalanceLaunch &N, Launch
     }
     const uint64_t rows_per_cta = uint64_t(kBalanceWarps) * (32 / lanes);
     const uint64_t want = (N.rows + rows_per_cta - 1) / rows_per_cta;
-    const uint64_t most = uint64_t(4 * L.num_sms) < kMaxPartials ? uint64_t(4 * L.num_sms) / L.p : kMaxPartials / L.p;
+    // the CTAs that the kernel's registers let an SM hold, once (balance_kernel's launch bounds; the generic kernel's 40)
+    const int per_sm = lanes == 32 && (!vec || N.experts > 1024) ? 6 : N.experts > 512 ? 2 : NV > 2 ? 3 : 4;
+    const uint64_t all = uint64_t(per_sm) * L.num_sms < kMaxPartials ? uint64_t(per_sm) * L.num_sms : kMaxPartials, most = all / L.p;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(want < 1 ? 1 : want < most ? want : most), unsigned(L.p));
     cfg.blockDim = dim3(kBalanceThreads);

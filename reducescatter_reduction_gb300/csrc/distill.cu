@@ -630,14 +630,18 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
             // stores e * g (edge: edge * g) where the chunk came from; zero for a row without a teacher
             auto put = [&](float g, bool taught) {
                 const uint32_t groups = d->groups;
-                const Pair gg = {g, g};
+                const Pair gg = {taught ? g : 0.0f, taught ? g : 0.0f};
                 auto value = [&](int n) -> uint4 {
                     Pair p[PAIRS];
 #pragma unroll
                     for (int i = 0; i < PAIRS; ++i) p[i] = e[n * PAIRS + i] * gg;
-                    const uint4 v = Gr::pack(p);
-                    return taught ? v : make_uint4(0, 0, 0, 0);
+                    return Gr::pack(p);
                 };
+                if (!taught) {      // whatever the logits hold
+#pragma unroll
+                    for (int i = 0; i < NG * PAIRS; ++i) e[i] = {0.0f, 0.0f};
+                    edge = 0.0f;
+                }
                 if (a.segments == 1 && d->seg[0].aligned) {
                     char *to = reinterpret_cast<char *>(d->seg[0].out) + size_t(tid) * 16;
 #pragma unroll
@@ -663,7 +667,7 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
                     }
                 }
                 if (a.edges && uint32_t(tid) < a.segments * 2 * VEC && d->edge_out[tid])
-                    Tr::store1(reinterpret_cast<void *>(uintptr_t(d->edge_out[tid])), 0, taught ? edge * g : 0.0f);
+                    Tr::store1(reinterpret_cast<void *>(uintptr_t(d->edge_out[tid])), 0, edge * gg.x);
             };
             float row_m = 0.0f, inv = 0.0f, factor = 0.0f;
             bool taught = true;

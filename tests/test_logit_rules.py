@@ -159,12 +159,12 @@ def test_large_batches_take_the_wide_slices(dtype):
 @pytest.mark.parametrize("p,rows,vocab,history,bias,layout", [
     (2, 40, 150001, 3000, 20, {}), (8, 40, 131072, 9000, 700, {}), (3, 60, 100003, 1024, 1, dict(offset=3)),
     (1, 30, 200001, 40000, 5, dict(in_place=True)), (16, 60, 90011, 5000, 64, dict(offset=[0, 1] * 8)), (5, 400, 16000, 2000, 0, {})])
-def test_long_histories_are_scanned_by_a_cluster(dtype, p, rows, vocab, history, bias, layout):
+def test_long_histories_of_large_batches(dtype, p, rows, vocab, history, bias, layout):
     x = rng(vocab).normal(0, 4, (rows, vocab))
     check(x, p, dtype, make_rules(rows, vocab, 7, history, bias, True), **layout)
 
 
-@pytest.mark.parametrize("history", [32767, 32768, 70000])
+@pytest.mark.parametrize("history", [16383, 16384, 32768, 70000])
 def test_a_token_repeated_through_a_long_history(history):
     """Counts around what a 16-bit counter holds, beside a neighbour that must not feel them."""
     a = make_rules(2, 300, 4).h
@@ -231,6 +231,18 @@ def test_bias_entries_of_one_token_add_in_list_order():
     torch.cuda.synchronize()
     assert np.array_equal(ranks.outs[0].view.cpu().numpy()[0], want)
     ranks.finish()
+
+
+@pytest.mark.parametrize("entries", [600, 9000])
+def test_more_bias_entries_than_a_slice_keeps(entries):
+    """All of one row's entries in one slice, some tokens many times; the other row has few."""
+    g = rng(8)
+    rows, vocab = 2, 4000
+    a = {"bias_offsets": np.array([0, entries, entries + 3], dtype=np.int32),
+         "bias_tokens": g.integers(100, 400, entries + 3).astype(np.int32),
+         "bias_values": g.normal(0, 1, entries + 3).astype(np.float32)}
+    check(g.normal(0, 4, (rows, vocab)), 1, "f32", Rules(**a))
+    check(g.normal(0, 4, (rows, vocab)), 2, "bf16", Rules(**a), offset=3)
 
 
 def test_bad_offsets_and_lengths_are_held_to_the_lists():
