@@ -75,6 +75,7 @@ struct DistillArgs {
     float temperature;
     float to_log2;        // log2(e) / T
     uint32_t k, kpad;
+    uint32_t share;       // the entries of a piece for the loss alone: those of all pieces make a row's
     uint32_t pieces;      // per row
     uint32_t parts;       // parts of a shard (one shard a piece), else 1
     uint32_t segments;    // shards of a piece
@@ -100,10 +101,16 @@ struct DistillDesc {
     uint32_t groups;
 };
 
-// What reaches a CTA from the CTAs of its row.
+// What reaches a CTA from the CTAs of its row.  The teacher's part of the
+// loss is a sum over its entries, so for the loss alone each piece takes a
+// share of the entries, wherever in the vocabulary they are, against a maximum
+// of its own; where a gradient follows, each goes through all of them for the
+// weights of those in its columns.
 struct DistillSums {
     float2 warp[kDistillMaxCluster][kDistillWarps];   // max, sum
-    float4 teacher[kDistillMaxCluster][2];            // reference, sum e (z - reference), sum e here, sum e | sum e (t - tmax) / T, weight
+    // reference, mean of z - reference by e and sum e over the piece's entries, sum e over all of them (the loss alone: the
+    // maximum t that e is against) | sum e (t - maximum) / T, the row's weight
+    float4 teacher[kDistillMaxCluster][2];
 };
 constexpr uint32_t kDistillSumBytes = kDistillWarps * 8 + 32;   // from one CTA
 
@@ -383,13 +390,15 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
             float w, max, log_sum;
         };
         Held coming, next, now;
+        // this piece's entries of a row (the same piece of every row where the CTAs form a cluster)
+        const uint32_t begin = BWD ? 0u : min((blockIdx.x % a.pieces) * a.share, a.k), share = BWD ? a.k : min(a.share, a.k - begin);
         auto fetch = [&](uint32_t item) {
             if (item >= a.items) return;
             const uint32_t row = div_by(item, a.by_pieces);
-            const uint64_t at = uint64_t(row) * a.k + lane;
+            const uint64_t at = uint64_t(row) * a.k + begin + lane;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const bool in = lane + 32 * u < a.k;
+                const bool in = lane + 32 * u < share;
                 coming.id[u] = in ? a.ids[at + 32 * u] : -1;
                 coming.t[u] = in ? load_any(a.teacher, a.teacher_dtype, at + 32 * u) : -INFINITY;
             }
@@ -409,7 +418,10 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
             h.row = div_by(item, a.by_pieces);
             const uint32_t q = item - h.row * a.pieces;
             h.at = 0;
-            if (a.segments == 1) {
+            if (!BWD) {
+                h.from = 0;
+                h.count = s.vocab;
+            } else if (a.segments == 1) {
                 Piece<T, PM> pc(a, q, 0);
                 const ShardRow<T> in(s.in[pc.rank], s.ld, h.row, shard_width(s, pc.rank));
                 pc.cut(a, in);
@@ -429,7 +441,7 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
             z = 0.0f;
             if (uint32_t(id) - h.from < h.count) {
                 if (!in_bounds(h.row < s.rows && uint32_t(id) < s.vocab, s.status, kSiteDistill, h.row)) return;
-                if (a.segments == 1) {
+                if (BWD && a.segments == 1) {
                     z = Tr::load1(reinterpret_cast<const void *>(h.at), uint32_t(id) - h.from);
                 } else {
                     const uint32_t r = rank_of_token(s, uint32_t(id));
@@ -447,7 +459,8 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
             const Hold h = hold_of(item);
             next = coming;
 #pragma unroll
-            for (int u = 0; u < U; ++u) place(h, next.id[u], next.t[u], next.z[u]);
+            for (int u = 0; u < U; ++u)
+                if (32 * u < share) place(h, next.id[u], next.t[u], next.z[u]);
         };
         fetch(blockIdx.x);
         place_all(blockIdx.x);
@@ -466,11 +479,12 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
                 tm = fmaxf(tm, now.t[u]);
                 if (now.id[u] >= 0 && now.z[u] < INFINITY) ref = fmaxf(ref, now.z[u]);
             }
-            if (a.kpad > 32 * U) {
+            if (share > 32 * U) {
                 const Hold h = hold_of(item);
-                for (uint32_t i = lane + 32 * U; i < a.kpad; i += 32) {
-                    int id = i < a.k ? a.ids[uint64_t(row) * a.k + i] : -1;
-                    float t = i < a.k ? load_any(a.teacher, a.teacher_dtype, uint64_t(row) * a.k + i) : -INFINITY, z;
+                const uint64_t at = uint64_t(row) * a.k + begin;
+                for (uint32_t i = lane + 32 * U; i < share; i += 32) {
+                    int id = a.ids[at + i];
+                    float t = load_any(a.teacher, a.teacher_dtype, at + i), z;
                     place(h, id, t, z);
                     more_id[i] = id;
                     more_e[i] = t;
@@ -488,18 +502,16 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
             tm = finite_max(tm);
             ref = finite_max(ref);
             if (BWD && k >= 2 && !__all_sync(0xffffffffu, distill_wait(a, sh, &sh.taught_free[slot], ((k >> 1) - 1) & 1, 8, item))) break;
-            float ts = 0.0f, tu = 0.0f, dot = 0.0f, own = 0.0f;
+            float ts = 0.0f, tu = 0.0f, own = 0.0f;
             uint32_t kept = 0;
-            auto weigh = [&](int eid, float et, float ez) {
+            // an entry's weight: summed up, and kept where a gradient needs it
+            auto weigh = [&](int eid, float et, float ez) -> float {
                 const float u = (et - tm) * per_t;
                 const float e = eid == -1 ? 0.0f : ex2((et - tm) * a.to_log2);
                 ts += e;
                 const bool mine = e != 0.0f && eid >= 0;
                 if (FWD && e != 0.0f) tu += e * u;
-                if (FWD && mine) {
-                    dot += e * (ez - ref);
-                    own += e;
-                }
+                if (FWD && mine) own += e;
                 if (BWD) {
                     const unsigned who = __ballot_sync(0xffffffffu, mine);
                     const uint32_t at = slot * a.kpad + kept + __popc(who & ((1u << lane) - 1));
@@ -510,26 +522,37 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
                     }
                     kept += __popc(who);
                 }
+                return mine ? e : 0.0f;
             };
+            float weight[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (32 * u < int(a.kpad)) weigh(now.id[u], now.t[u], now.z[u]);
-            for (uint32_t i0 = 32 * U; i0 < a.kpad; i0 += 32) {
+            for (int u = 0; u < U; ++u) weight[u] = 32 * u < share ? weigh(now.id[u], now.t[u], now.z[u]) : 0.0f;
+            for (uint32_t i0 = 32 * U; i0 < share; i0 += 32) {
                 const uint32_t i = i0 + lane;
-                const bool in = i < a.kpad;
-                weigh(in ? more_id[i] : -1, in ? more_e[i] : 0.0f, in ? more_z[i] : 0.0f);
+                const bool in = i < share;
+                const float e = weigh(in ? more_id[i] : -1, in ? more_e[i] : 0.0f, in ? more_z[i] : 0.0f);
+                if (in) more_e[i] = e;
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
                 const float v0 = __shfl_xor_sync(0xffffffffu, ts, o);
                 if constexpr (FWD) {
-                    const float v1 = __shfl_xor_sync(0xffffffffu, tu, o), v2 = __shfl_xor_sync(0xffffffffu, dot, o),
-                                v3 = __shfl_xor_sync(0xffffffffu, own, o);
+                    const float v1 = __shfl_xor_sync(0xffffffffu, tu, o), v3 = __shfl_xor_sync(0xffffffffu, own, o);
                     tu += v1;
-                    dot += v2;
                     own += v3;
                 }
                 ts += v0;
+            }
+            // the mean of z - reference over the piece's entries: a sum could leave fp32's range at masks of the lowest value
+            float mean = 0.0f;
+            if constexpr (FWD) {
+                const float per = own != 0.0f ? 1.0f / own : 0.0f;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (weight[u] != 0.0f) mean += weight[u] * per * (now.z[u] - ref);
+                for (uint32_t i = lane + 32 * U; i < share; i += 32)
+                    if (more_e[i] != 0.0f) mean += more_e[i] * per * (more_z[i] - ref);
+                mean = warp_sum(mean);
             }
             if constexpr (BWD) {
                 if (kept % 4 && lane < int(4 - kept % 4)) id_s[slot * a.kpad + kept + lane] = -1;
@@ -549,7 +572,7 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
                 if (lane == 0) mbar_arrive_expect_tx(smem_addr(&sh.sums_in[slot]), a.pieces * kDistillSumBytes);
                 if (lane < int(a.pieces)) {
                     const uint32_t bar = remote(smem_addr(&sh.sums_in[slot]), lane), at = remote(smem_addr(&sh.sums[slot].teacher[q][0]), lane);
-                    send4(at, bar, make_float4(ref, dot, own, ts));
+                    send4(at, bar, make_float4(ref, mean, own, BWD ? ts : tm));
                     send4(at + 16, bar, make_float4(tu, now.w, 0.0f, 0.0f));
                 }
             }
@@ -577,18 +600,34 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
             for (int i = 0; i < kDistillMaxCluster * kDistillWarps / 32; ++i) total += v[i].y * ex2((v[i].x - row_m) * c2);
             total = warp_sum(total);
             inv = total == 0.0f ? 0.0f : 1.0f / total;    // a row of nothing but -inf: p = 0
-            const float tsum = in.teacher[q][0].w;
-            taught = tsum != 0.0f;
-            factor = in.teacher[q][1].y * a.temperature;
+            if constexpr (BWD) {
+                taught = in.teacher[q][0].w != 0.0f;
+                factor = in.teacher[q][1].y * a.temperature;
+            }
             if (q == 0 && warp == 0) {
-                const float4 t = lane < int(a.pieces) ? in.teacher[lane][0] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                const float dot = warp_sum(t.z != 0.0f ? t.y + t.z * (t.x - row_m) : 0.0f);
+                const bool is = lane < int(a.pieces);
+                const float4 t = is ? in.teacher[lane][0] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                float tsum, u, part = t.z;      // part: the entries' share of sum e
+                if constexpr (BWD) {
+                    tsum = in.teacher[q][0].w;
+                    u = in.teacher[q][1].x;
+                } else {
+                    // the shares' maxima and sums together
+                    const float top = warp_max(t.z != 0.0f ? t.w : -INFINITY), scale = t.z != 0.0f ? ex2((t.w - finite_max(top)) * c2) : 0.0f;
+                    u = t.z != 0.0f ? scale * (in.teacher[lane][1].x + t.z * (t.w - top) / a.temperature) : 0.0f;
+                    part *= scale;
+                    tsum = warp_sum(part);
+                    u = warp_sum(u);
+                    taught = tsum != 0.0f;
+                }
+                // sum q (z - the row's maximum)
+                const float dot = warp_sum(part != 0.0f ? part / tsum * (t.y + (t.x - row_m)) : 0.0f);
                 if (lane == 0) {
                     const float ls = logf(total), T = a.temperature;
                     float loss = 0.0f;
                     if (taught) {
                         if (total == 0.0f) loss = INFINITY;
-                        else loss = T * T * ((in.teacher[q][1].x / tsum - logf(tsum)) - (dot / T / tsum - ls));
+                        else loss = T * T * ((u / tsum - logf(tsum)) - (dot / T - ls));
                     }
                     a.loss[row] = loss;
                     if (a.stats) {
@@ -832,6 +871,7 @@ static cudaError_t distill_shape(const Launch &L, const DistillLaunch &N, Launch
     a.by_pieces = fast_div(a.pieces);
     a.by_parts = fast_div(a.parts);
     a.by_segments = fast_div(a.segments);
+    a.share = (a.k + a.pieces - 1) / a.pieces;
     const size_t entries = size_t(a.kpad) * (a.kpad > 128 ? 36 : 24);
     a.stages = kDistillMaxStages;
     while (a.stages * size_t(kDistillStageBytes) + entries + sizeof(DistillShared) + 1024 > kDistillSmem) --a.stages;

@@ -9,22 +9,23 @@
 //   y = -inf                           if the row's mask has bit v clear
 // in fp32, rounded once to the element type.
 //
-// One CTA per (row, rank, slice of the rank's columns).  It starts the loads
-// of the row's rules, of the first part of its history and of its own groups,
-// and counts the history's tokens that fall into the slice in one counter per
-// column in shared memory (integer atomics, so any order gives the same
-// counts); who raises a counter from zero puts its column on a list.  The
-// row's bias entries for the slice are kept in their order, and their columns
-// go on the list too.  The groups are copied through their mask bits, knowing
-// no other rule; one that its mask forbids altogether is not read, and in
-// place one that it leaves alone is neither read nor written.  After the CTA's
-// barrier the listed columns are done, each by a lane of its own: their logits
-// are read again, from L2.  (Done in the copy, the rules cost more than the
-// copy itself: a history of thousands of tokens touches few columns, but
-// nearly every group of 32 lanes has one.  Done by a kernel after the copy,
-// the columns come from and go to memory a second time, a sector each.)
-// Counters are 16 bits wide where the history is shorter than 2^14 tokens.
-// Bytes: the logits once in and once out, the history once per slice (L2).
+// One CTA per (row, rank, slice of the rank's columns).  It starts the copies
+// of its groups into shared memory, all but those that the row's mask forbids
+// altogether, and meanwhile counts the row's history: the tokens that fall
+// into the slice, in one counter per column in shared memory (integer
+// atomics, so any order gives the same counts); who raises a counter from
+// zero puts its column on a list.  Each warp queues the tokens that it finds,
+// so that the counting runs with full warps.  The row's bias entries for the
+// slice are kept in their order, and their columns go on the list too.  Then
+// the listed columns are done in shared memory, each by a lane of its own (in
+// the groups' own lanes the rules cost more than the copy: a history of
+// thousands of tokens touches few columns, but nearly every group of 32 lanes
+// has one), and the groups go out through their mask bits.  In place nothing
+// is staged: only groups that the mask changes are read and written, and the
+// listed columns in memory.  Counters are 16 bits wide where the history is
+// shorter than 2^14 tokens.  Bytes: the logits once in and once out, the
+// history once per slice (L2).
+#include "async.cuh"
 #include "logits.cuh"
 
 namespace ccl {
@@ -43,7 +44,7 @@ struct RulesArgs {
 constexpr uint32_t kSeenPrompt = 1, kGenerated = 2;
 // Bias entries of a slice that are kept in shared memory; with more, a column
 // that has one goes through the row's whole list.
-constexpr uint32_t kBiasKept = 512;
+constexpr uint32_t kBiasKept = 256;
 
 // Clears the lanes of a group that the mask bits forbid to -inf.
 template <typename T>
@@ -70,10 +71,12 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
     constexpr int VEC = Tr::VEC, GROUPS = THREADS * NV, PER = WIDE ? 1 : 2;   // counters per word
     constexpr int CELLS = (GROUPS + 2) * VEC;       // a group's room before and after for the edges
     constexpr uint32_t BITS = 32 / PER, BIASED = 1u << (BITS - 1), ONES = BIASED | (BIASED - 1);
-    constexpr uint32_t LIST = CELLS < 4096 ? CELLS : 4096;   // columns the list holds; with more, it is made anew for as many counters
-    constexpr int WARPS = THREADS / 32, BATCH = 8;
+    constexpr uint32_t LIST = CELLS < 2048 ? CELLS : 2048;   // columns the list holds; with more, it is made anew for as many counters
+    constexpr int WARPS = THREADS / 32, BATCH = 4;
     extern __shared__ uint4 smem4[];
-    uint32_t *cnt = reinterpret_cast<uint32_t *>(smem4);
+    uint4 *stage = smem4;                            // the slice's logits, a cell an element
+    uint32_t *cnt = reinterpret_cast<uint32_t *>(smem4 + (a.in_place ? 0 : CELLS / VEC));
+    __shared__ uint16_t queue[WARPS][32 * (BATCH + 1)];   // tokens found: cell, and whether generated in the top bit
     __shared__ uint16_t list[LIST];
     __shared__ uint16_t bias_cell[kBiasKept];
     __shared__ float bias_value[kBiasKept];
@@ -140,14 +143,16 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
         for (int n = 0; n < NV; ++n)
             allowed[n / PACK] |= (__funnelshift_r(lo[n], hi[n], (v0 + n * THREADS * VEC) & 31) & ALL) << (n % PACK * VEC);
     }
-    uint4 raw[NV];
+    if (!a.in_place) {
+        const uint32_t to = smem_addr(stage) + (tid + 1) * 16;
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const uint32_t j = j0 + tid + n * THREADS, ok = ok_of(n);
-        if (j < j1 && ok && !(a.in_place && ok == ALL)) raw[n] = ld_coherent_v4(in.group(j));
-        else raw[n] = lowest_group<T>();
+        for (int n = 0; n < NV; ++n) {
+            const uint32_t j = j0 + tid + n * THREADS;
+            if (j < j1 && ok_of(n))
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + n * THREADS * 16), "l"(in.group(j)) : "memory");
+        }
+        if (edge >= 0) Tr::store1(stage, uint64_t(edge - cell0), in.column(edge));
     }
-    const float edge_x = edge >= 0 ? in.column(edge) : 0.0f;
     if (a.r.bias_count) {
         const int n = int(a.r.bias_count);
         bias_lo = bias_lo < 0 ? 0 : bias_lo > n ? n : bias_lo;
@@ -176,6 +181,8 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
         at = __shfl_sync(0xffffffffu, at, __ffs(who) - 1) + __popc(who & ((1u << lane) - 1));
         if (fresh && at < LIST) list[at] = uint16_t(cell);
     };
+    uint16_t *q = queue[warp];
+    int queued = 0;
 #pragma unroll 1
     for (int j = tid; j - lane < len; j += BATCH * THREADS) {
         if (j != tid) {
@@ -187,8 +194,25 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
             const uint32_t c = uint32_t(token[k]) - from;        // another slice's, or no token: not below width
             const int at = j + k * THREADS;
             const bool is = c < width && at < len;
-            if (!__any_sync(0xffffffffu, is)) continue;
-            raise(is, c + cell_from, at < prompt ? kSeenPrompt : kGenerated, at < prompt);
+            const unsigned who = __ballot_sync(0xffffffffu, is);
+            if (is) q[queued + __popc(who & ((1u << lane) - 1))] = uint16_t((c + cell_from) | (at < prompt ? 0u : 0x8000u));
+            queued += __popc(who);
+        }
+        __syncwarp();
+        // whole warps of the queue; the rest stays for the next batch, or is done with the last
+        const bool more = j - lane + BATCH * THREADS < len;
+        int done = 0;
+#pragma unroll 1
+        for (; done + (more ? 32 : 1) <= queued; done += 32) {
+            const bool is = done + lane < queued;
+            const uint32_t e = is ? q[done + lane] : 0u, made = e >> 15;
+            raise(is, e & 0x7fff, made ? kGenerated : kSeenPrompt, !made);
+        }
+        if (more) {
+            const uint16_t rest = done + lane < queued ? q[done + lane] : uint16_t(0);
+            __syncwarp();
+            queued -= done;
+            if (lane < queued) q[lane] = rest;
         }
     }
     uint32_t kept = 0;
@@ -215,22 +239,22 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
         if (b + THREADS < bias_hi) __syncthreads();
     }
 
-    // the copy
     const ShardRow<T> out(s.out[rank], s.ld, row, in.width);
+    auto may = [&](uint32_t col) { return !mask || (mask[(token0 + col) >> 5] >> ((token0 + col) & 31)) & 1; };
+    if (a.in_place) {
+        // what the mask forbids
 #pragma unroll
-    for (int n = 0; n < NV; ++n) {
-        const uint32_t j = j0 + tid + n * THREADS, ok = ok_of(n);
-        if (j >= j1) break;
-        if (ok != ALL) store_group<T>(out, in, j, forbid<T>(raw[n], ok));
-        else if (!a.in_place) store_group<T>(out, in, j, raw[n]);
-    }
-    if (edge >= 0) {
-        const uint32_t v = token0 + edge;
-        out.set_column(edge, !mask || (mask[v >> 5] >> (v & 31)) & 1 ? edge_x : -INFINITY);
+        for (int n = 0; n < NV; ++n) {
+            const uint32_t j = j0 + tid + n * THREADS, ok = ok_of(n);
+            if (j < j1 && ok != ALL) store_group<T>(out, in, j, forbid<T>(ok ? ld_coherent_v4(in.group(j)) : lowest_group<T>(), ok));
+        }
+        if (edge >= 0 && !may(edge)) out.set_column(edge, -INFINITY);
+    } else {
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
     __syncthreads();
 
-    // the listed columns, as they came in (in place the copy has left the allowed ones alone)
+    // the listed columns: in shared memory, or in place where they are allowed
     const float rep = a.r.repetition ? a.r.repetition[row] : 1.0f;
     const float freq = a.r.frequency ? a.r.frequency[row] : 0.0f;
     const float pres = a.r.presence ? a.r.presence[row] : 0.0f;
@@ -258,9 +282,12 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
             for (int k = 0; k < AT_ONCE; ++k) {
                 const bool is = i + k * THREADS < count;
                 cell[k] = is ? list[i + k * THREADS] : cell_from;
-                const uint32_t col = cell[k] + uint32_t(cell0), v = token0 + col;
-                x[k] = is ? in.column(col) : 0.0f;
-                bits |= (is ? mask ? (mask[v >> 5] >> (v & 31)) & 1u : 1u : 0u) << k;
+                x[k] = 0.0f;
+                if (is) {
+                    const uint32_t col = cell[k] + uint32_t(cell0);
+                    x[k] = a.in_place ? in.column(col) : Tr::load1(stage, cell[k]);
+                    bits |= (!a.in_place || may(col) ? 1u : 0u) << k;
+                }
             }
 #pragma unroll
             for (int k = 0; k < AT_ONCE; ++k) {
@@ -281,24 +308,35 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
                 const uint32_t seen = c & (BIASED - 1);
                 if (seen) y = __fmul_rn(y, y > 0.0f ? rep_inv : rep);
                 if (seen >= kGenerated) y = __fsub_rn(__fsub_rn(y, __fmul_rn(freq, float(seen >> 1))), pres);
-                out.set_column(cell[k] + uint32_t(cell0), y);
+                if (a.in_place) out.set_column(cell[k] + uint32_t(cell0), y);
+                else Tr::store1(stage, cell[k], y);
             }
         }
     }
+    if (a.in_place) return;
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const uint32_t j = j0 + tid + n * THREADS, ok = ok_of(n);
+        if (j >= j1) break;
+        store_group<T>(out, in, j, ok == ALL ? stage[tid + n * THREADS + 1] : ok ? forbid<T>(stage[tid + n * THREADS + 1], ok) : lowest_group<T>());
+    }
+    if (edge >= 0) out.set_column(edge, may(edge) ? Tr::load1(stage, uint64_t(edge - cell0)) : -INFINITY);
 }
 
 template <typename T, int PM, int THREADS, int NV, bool WIDE>
 static cudaError_t rules_launch(const Launch &L, RulesArgs<PM> &a, uint32_t groups, LaunchInfo *info)
 {
     constexpr uint32_t GROUPS = THREADS * NV;
-    constexpr size_t smem = size_t(GROUPS + 2) * Traits<T>::VEC * (WIDE ? 4 : 2);
+    constexpr size_t counters = size_t(GROUPS + 2) * Traits<T>::VEC * (WIDE ? 4 : 2), staged = size_t(GROUPS + 2) * 16;
+    const size_t smem = counters + (a.in_place ? 0 : staged);
     a.slices = groups ? (groups + GROUPS - 1) / GROUPS : 1;
     const uint64_t per_row = uint64_t(a.slices) * a.s.p;
     if (a.s.rows * per_row > 0x7fffffffull) return cudaErrorInvalidValue;
     a.by_row = fast_div(uint32_t(per_row));
     a.by_slices = fast_div(a.slices);
     static std::atomic<unsigned long long> done{0};
-    cudaError_t err = allow_dynamic_smem(logit_rules_kernel<T, PM, THREADS, NV, WIDE>, smem, L.device, done);
+    cudaError_t err = allow_dynamic_smem(logit_rules_kernel<T, PM, THREADS, NV, WIDE>, counters + staged, L.device, done);
     if (err != cudaSuccess) return err;
     const unsigned grid = unsigned(a.s.rows * per_row);
     err = launch_dependent(logit_rules_kernel<T, PM, THREADS, NV, WIDE>, grid, THREADS, smem, L.stream, a);
