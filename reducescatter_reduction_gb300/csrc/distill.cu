@@ -108,7 +108,7 @@ struct DistillDesc {
 // weights of those in its columns.
 struct DistillSums {
     float2 warp[kDistillMaxCluster][kDistillWarps];   // max, sum
-    // reference, mean of z - reference by e and sum e over the piece's entries, sum e over all of them (the loss alone: the
+    // reference, sum e (z - reference) / 1024 and sum e over the piece's entries, sum e over all of them (the loss alone: the
     // maximum t that e is against) | sum e (t - maximum) / T, the row's weight
     float4 teacher[kDistillMaxCluster][2];
 };
@@ -502,16 +502,20 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
             tm = finite_max(tm);
             ref = finite_max(ref);
             if (BWD && k >= 2 && !__all_sync(0xffffffffu, distill_wait(a, sh, &sh.taught_free[slot], ((k >> 1) - 1) & 1, 8, item))) break;
-            float ts = 0.0f, tu = 0.0f, own = 0.0f;
+            float ts = 0.0f, tu = 0.0f, dot = 0.0f, own = 0.0f;
             uint32_t kept = 0;
             // an entry's weight: summed up, and kept where a gradient needs it
-            auto weigh = [&](int eid, float et, float ez) -> float {
+            auto weigh = [&](int eid, float et, float ez) {
                 const float u = (et - tm) * per_t;
                 const float e = eid == -1 ? 0.0f : ex2((et - tm) * a.to_log2);
                 ts += e;
                 const bool mine = e != 0.0f && eid >= 0;
                 if (FWD && e != 0.0f) tu += e * u;
-                if (FWD && mine) own += e;
+                if (FWD && mine) {
+                    own += e;
+                    // a 1024th: at most so many entries, so masks of the lowest value do not leave fp32's range
+                    dot += e * 0x1p-10f * (ez - ref);
+                }
                 if (BWD) {
                     const unsigned who = __ballot_sync(0xffffffffu, mine);
                     const uint32_t at = slot * a.kpad + kept + __popc(who & ((1u << lane) - 1));
@@ -522,37 +526,26 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
                     }
                     kept += __popc(who);
                 }
-                return mine ? e : 0.0f;
             };
-            float weight[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) weight[u] = 32 * u < share ? weigh(now.id[u], now.t[u], now.z[u]) : 0.0f;
+            for (int u = 0; u < U; ++u)
+                if (32 * u < share) weigh(now.id[u], now.t[u], now.z[u]);
             for (uint32_t i0 = 32 * U; i0 < share; i0 += 32) {
                 const uint32_t i = i0 + lane;
                 const bool in = i < share;
-                const float e = weigh(in ? more_id[i] : -1, in ? more_e[i] : 0.0f, in ? more_z[i] : 0.0f);
-                if (in) more_e[i] = e;
+                weigh(in ? more_id[i] : -1, in ? more_e[i] : 0.0f, in ? more_z[i] : 0.0f);
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) {
                 const float v0 = __shfl_xor_sync(0xffffffffu, ts, o);
                 if constexpr (FWD) {
-                    const float v1 = __shfl_xor_sync(0xffffffffu, tu, o), v3 = __shfl_xor_sync(0xffffffffu, own, o);
+                    const float v1 = __shfl_xor_sync(0xffffffffu, tu, o), v2 = __shfl_xor_sync(0xffffffffu, dot, o),
+                                v3 = __shfl_xor_sync(0xffffffffu, own, o);
                     tu += v1;
+                    dot += v2;
                     own += v3;
                 }
                 ts += v0;
-            }
-            // the mean of z - reference over the piece's entries: a sum could leave fp32's range at masks of the lowest value
-            float mean = 0.0f;
-            if constexpr (FWD) {
-                const float per = own != 0.0f ? 1.0f / own : 0.0f;
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (weight[u] != 0.0f) mean += weight[u] * per * (now.z[u] - ref);
-                for (uint32_t i = lane + 32 * U; i < share; i += 32)
-                    if (more_e[i] != 0.0f) mean += more_e[i] * per * (more_z[i] - ref);
-                mean = warp_sum(mean);
             }
             if constexpr (BWD) {
                 if (kept % 4 && lane < int(4 - kept % 4)) id_s[slot * a.kpad + kept + lane] = -1;
@@ -572,7 +565,7 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
                 if (lane == 0) mbar_arrive_expect_tx(smem_addr(&sh.sums_in[slot]), a.pieces * kDistillSumBytes);
                 if (lane < int(a.pieces)) {
                     const uint32_t bar = remote(smem_addr(&sh.sums_in[slot]), lane), at = remote(smem_addr(&sh.sums[slot].teacher[q][0]), lane);
-                    send4(at, bar, make_float4(ref, mean, own, BWD ? ts : tm));
+                    send4(at, bar, make_float4(ref, dot, own, BWD ? ts : tm));
                     send4(at + 16, bar, make_float4(tu, now.w, 0.0f, 0.0f));
                 }
             }
@@ -621,7 +614,7 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
                     taught = tsum != 0.0f;
                 }
                 // sum q (z - the row's maximum)
-                const float dot = warp_sum(part != 0.0f ? part / tsum * (t.y + (t.x - row_m)) : 0.0f);
+                const float dot = warp_sum(part != 0.0f ? part / tsum * (t.y / t.z * 1024.0f + (t.x - row_m)) : 0.0f);
                 if (lane == 0) {
                     const float ls = logf(total), T = a.temperature;
                     float loss = 0.0f;

@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
     constexpr int CELLS = (GROUPS + 2) * VEC;       // a group's room before and after for the edges
     constexpr uint32_t BITS = 32 / PER, BIASED = 1u << (BITS - 1), ONES = BIASED | (BIASED - 1);
     constexpr uint32_t LIST = CELLS < 2048 ? CELLS : 2048;   // columns the list holds; with more, it is made anew for as many counters
-    constexpr int WARPS = THREADS / 32, BATCH = 4;
+    constexpr int WARPS = THREADS / 32, BATCH = THREADS > 256 ? 4 : 8;   // tokens a thread loads at once
     extern __shared__ uint4 smem4[];
     uint4 *stage = smem4;                            // the slice's logits, a cell an element
     uint32_t *cnt = reinterpret_cast<uint32_t *>(smem4 + (a.in_place ? 0 : CELLS / VEC));
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
             __syncthreads();
         }
         const uint32_t count = listed;
-        constexpr int AT_ONCE = 4;
+        constexpr int AT_ONCE = 2;
 #pragma unroll 1
         for (uint32_t i = tid; i < count; i += AT_ONCE * THREADS) {
             uint32_t cell[AT_ONCE], bits = 0;
