@@ -31,11 +31,13 @@
 //
 // So the logits are read once, the gradient is written once, each element
 // costs one exponential, and while a row's sums travel the next rows' loads
-// are in flight.  What the CTAs tell one another goes into double-buffered
+// are in flight.  What the CTAs tell one another goes into
 // slots with st.async and is counted by the receiver's mbarrier; every CTA
 // adds the same values in the same order, so all pieces of a row use the same
-// bits.  A sender is at most one row ahead of any receiver: its sums for row
-// k + 1 leave only after the whole row k has reached it.
+// bits.  There are four slots, and a sender's sums for row k leave only after
+// all of row k - 2 has reached it: by then every CTA has sent its sums of row
+// k - 2, so it is done with the sums of row k - 4, which had the slot before.
+// (For the loss alone the consumers see a row complete two rows later.)
 //
 // A piece beyond 2048 groups (vocabularies above 262144 16-bit or 131072
 // 32-bit columns on up to 16 ranks a power of two) is taken in chunks: the
@@ -112,13 +114,14 @@ struct DistillSums {
     // maximum t that e is against) | sum e (t - maximum) / T, the row's weight
     float4 teacher[kDistillMaxCluster][2];
 };
+constexpr int kDistillSlots = 4, kDistillLag = 2;
 constexpr uint32_t kDistillSumBytes = kDistillWarps * 8 + 32;   // from one CTA
 
 struct DistillShared {
-    DistillSums sums[2];
+    DistillSums sums[kDistillSlots];
     DistillDesc desc[kDistillMaxStages + 1];
     uint64_t full[kDistillMaxStages], empty[kDistillMaxStages];
-    uint64_t sums_in[2], taught[2], taught_free[2], stored[2];
+    uint64_t sums_in[kDistillSlots], taught[2], taught_free[2], stored[2];
     uint32_t entries[2];                              // the piece's teacher entries
     float teacher_sum[2];
     float weight[2], row_max[2], row_log_sum[2];      // of the row (the latter two for a gradient alone)
@@ -201,6 +204,13 @@ __device__ __forceinline__ bool distill_wait(const DistillArgs<PM> &a, DistillSh
     return true;
 }
 
+// Waits for all of the sums of this CTA's k-th row.
+template <int PM>
+__device__ __forceinline__ bool wait_sums(const DistillArgs<PM> &a, DistillShared &sh, uint32_t k, unsigned code, uint32_t item)
+{
+    return __all_sync(0xffffffffu, distill_wait(a, sh, &sh.sums_in[k % kDistillSlots], (k / kDistillSlots) & 1, code, item));
+}
+
 // The part of shard `rank` that piece q of a row takes.
 template <typename T, int PM>
 struct Piece {
@@ -251,8 +261,8 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
             mbar_init(smem_addr(&sh.full[i]), 1);
             mbar_init(smem_addr(&sh.empty[i]), kDistillWarps);
         }
+        for (int i = 0; i < kDistillSlots; ++i) mbar_init(smem_addr(&sh.sums_in[i]), 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&sh.sums_in[i]), 1);
             mbar_init(smem_addr(&sh.taught[i]), 1);
             mbar_init(smem_addr(&sh.taught_free[i]), 1);
             mbar_init(smem_addr(&sh.stored[i]), kDistillWarps);
@@ -560,11 +570,11 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
                 if (lane == 0) mbar_arrive(smem_addr(&sh.taught[slot]));
             }
             if constexpr (FWD) {
-                // the slot's last contents have been used by every CTA of the row once the row before this one is complete
-                if (k >= 1 && !__all_sync(0xffffffffu, distill_wait(a, sh, &sh.sums_in[slot ^ 1], ((k - 1) >> 1) & 1, 9, item))) break;
-                if (lane == 0) mbar_arrive_expect_tx(smem_addr(&sh.sums_in[slot]), a.pieces * kDistillSumBytes);
+                if (k >= kDistillLag && !wait_sums(a, sh, k - kDistillLag, 9, item)) break;
+                const uint32_t to = k % kDistillSlots;
+                if (lane == 0) mbar_arrive_expect_tx(smem_addr(&sh.sums_in[to]), a.pieces * kDistillSumBytes);
                 if (lane < int(a.pieces)) {
-                    const uint32_t bar = remote(smem_addr(&sh.sums_in[slot]), lane), at = remote(smem_addr(&sh.sums[slot].teacher[q][0]), lane);
+                    const uint32_t bar = remote(smem_addr(&sh.sums_in[to]), lane), at = remote(smem_addr(&sh.sums[to].teacher[q][0]), lane);
                     send4(at, bar, make_float4(ref, dot, own, BWD ? ts : tm));
                     send4(at + 16, bar, make_float4(tu, now.w, 0.0f, 0.0f));
                 }
@@ -616,11 +626,11 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
                 // sum q (z - the row's maximum)
                 const float dot = warp_sum(part != 0.0f ? part / tsum * (t.y / t.z * 1024.0f + (t.x - row_m)) : 0.0f);
                 if (lane == 0) {
-                    const float ls = logf(total), T = a.temperature;
+                    const float ls = logf(total), heat = a.temperature;
                     float loss = 0.0f;
                     if (taught) {
                         if (total == 0.0f) loss = INFINITY;
-                        else loss = T * T * ((u / tsum - logf(tsum)) - (dot / T - ls));
+                        else loss = heat * heat * ((u / tsum - logf(tsum)) - (dot / heat - ls));
                     }
                     a.loss[row] = loss;
                     if (a.stats) {
@@ -725,17 +735,18 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
                 if (!ok) break;
                 const float wm = warp_max(m);
                 const float ws = warp_sum(sum * ex2((m - finite_max(wm)) * c2));
-                // The loss alone does not hold the consumers up: they see the row before this one complete (which also
-                // says that every CTA of the row is done with this row's slot), finish it, and go on to the next.
-                if (!BWD && k >= 1) {
-                    if (!__all_sync(0xffffffffu, distill_wait(a, sh, &sh.sums_in[slot ^ 1], ((k - 1) >> 1) & 1, 11, item))) break;
-                    if (q == 0 && warp == 0) total_of(slot ^ 1, q, div_by(item - stride, a.by_pieces), row_m, inv, factor, taught);
+                // the loss alone does not wait for this row's sums, only for those of two rows back
+                if (!BWD && k >= kDistillLag) {
+                    if (!wait_sums(a, sh, k - kDistillLag, 11, item)) break;
+                    if (q == 0 && warp == 0)
+                        total_of((k - kDistillLag) % kDistillSlots, q, div_by(item - kDistillLag * stride, a.by_pieces), row_m, inv, factor, taught);
                 }
+                const uint32_t to = k % kDistillSlots;
                 if (lane < int(a.pieces))
-                    send2(remote(smem_addr(&sh.sums[slot].warp[q][warp]), lane), remote(smem_addr(&sh.sums_in[slot]), lane), wm, ws);
-                if (BWD || item + stride >= a.items) {
-                    if (!__all_sync(0xffffffffu, distill_wait(a, sh, &sh.sums_in[slot], parity, 12, item))) break;
-                    if (BWD || (q == 0 && warp == 0)) total_of(slot, q, row, row_m, inv, factor, taught);
+                    send2(remote(smem_addr(&sh.sums[to].warp[q][warp]), lane), remote(smem_addr(&sh.sums_in[to]), lane), wm, ws);
+                if constexpr (BWD) {
+                    if (!wait_sums(a, sh, k, 12, item)) break;
+                    total_of(to, q, row, row_m, inv, factor, taught);
                 }
             }
             if constexpr (BWD) {
@@ -767,6 +778,16 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sh.stored[slot]));
+            }
+        }
+        if constexpr (!BWD) {
+            // the last rows' losses
+            for (uint32_t j = k > kDistillLag ? k - kDistillLag : 0u; j < k; ++j) {
+                const uint32_t item = blockIdx.x + j * stride, row = div_by(item, a.by_pieces), q = item - row * a.pieces;
+                float row_m, inv, factor;
+                bool taught;
+                if (!wait_sums(a, sh, j, 14, item)) break;
+                if (q == 0 && warp == 0) total_of(j % kDistillSlots, q, row, row_m, inv, factor, taught);
             }
         }
     }
