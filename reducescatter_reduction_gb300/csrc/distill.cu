@@ -58,13 +58,24 @@ namespace ccl {
 constexpr int kDistillConsumers = 256;
 constexpr int kDistillWarps = kDistillConsumers / 32;
 constexpr int kDistillThreads = kDistillConsumers + 64;
-constexpr int kDistillGroups = 8;                                      // groups a consumer keeps
+constexpr int kDistillGroups = 8;                                      // groups a consumer takes of a stage
 constexpr uint32_t kDistillStage = kDistillConsumers * kDistillGroups; // groups of a stage
 constexpr uint32_t kDistillStageBytes = kDistillStage * 16;
-constexpr int kDistillMaxCluster = 16;
-constexpr int kDistillMaxSegments = 4;                                 // shards of a piece: 64 ranks in 16 CTAs
-constexpr uint32_t kDistillMaxStages = 3;
-constexpr size_t kDistillSmem = 113 * 1024;                            // two CTAs per SM
+
+// What a pass is built for.  The loss alone keeps no exponentials, so an SM
+// holds three CTAs of it instead of two (of two stages instead of three), in
+// clusters of up to eight: beyond, its pieces come in chunks, which cost it
+// nothing.
+template <int PASS>
+struct DistillShape {
+    static constexpr bool loss_alone = PASS == CCL_PASS_FORWARD;
+    static constexpr int ctas = loss_alone ? 3 : 2;              // per SM
+    static constexpr uint32_t stages = loss_alone ? 2 : 3;
+    static constexpr int cluster = loss_alone ? 8 : 16;          // pieces of a row
+    static constexpr int segments = kMaxRanks / cluster;         // shards of a piece
+    static constexpr int held = loss_alone ? 2 : 4;              // teacher entries of a lane in registers
+    static constexpr size_t smem = (loss_alone ? 75 : 113) * 1024;   // of a CTA, a kilobyte of the system's included
+};
 
 template <int PM>
 struct DistillArgs {
@@ -92,14 +103,16 @@ struct DistillArgs {
 };
 
 // Where a stage's groups and edge elements go.
+template <int PASS>
 struct DistillDesc {
+    static constexpr int SEGS = DistillShape<PASS>::segments;
     struct Segment {
         uint64_t out;          // address of the output of its first group
         uint32_t first;        // its first group in the stage
         uint32_t aligned;      // the output's groups lie on 16-byte boundaries too
-    } seg[kDistillMaxSegments];
-    uint64_t edge_out[kDistillMaxSegments * 16];   // address of an edge element's output, 0: no such element
-    float edge[kDistillMaxSegments * 16];
+    } seg[SEGS];
+    uint64_t edge_out[SEGS * 16];   // address of an edge element's output, 0: no such element
+    float edge[SEGS * 16];
     uint32_t groups;
 };
 
@@ -108,19 +121,21 @@ struct DistillDesc {
 // share of the entries, wherever in the vocabulary they are, against a maximum
 // of its own; where a gradient follows, each goes through all of them for the
 // weights of those in its columns.
+template <int PASS>
 struct DistillSums {
-    float2 warp[kDistillMaxCluster][kDistillWarps];   // max, sum
+    float2 warp[DistillShape<PASS>::cluster][kDistillWarps];   // max, sum
     // reference, sum e (z - reference) / 1024 and sum e over the piece's entries, sum e over all of them (the loss alone: the
     // maximum t that e is against) | sum e (t - maximum) / T, the row's weight
-    float4 teacher[kDistillMaxCluster][2];
+    float4 teacher[DistillShape<PASS>::cluster][2];
 };
 constexpr int kDistillSlots = 4, kDistillLag = 2;
 constexpr uint32_t kDistillSumBytes = kDistillWarps * 8 + 32;   // from one CTA
 
+template <int PASS>
 struct DistillShared {
-    DistillSums sums[kDistillSlots];
-    DistillDesc desc[kDistillMaxStages + 1];
-    uint64_t full[kDistillMaxStages], empty[kDistillMaxStages];
+    DistillSums<PASS> sums[kDistillSlots];
+    DistillDesc<PASS> desc[DistillShape<PASS>::stages + 1];
+    uint64_t full[DistillShape<PASS>::stages], empty[DistillShape<PASS>::stages];
     uint64_t sums_in[kDistillSlots], taught[2], taught_free[2], stored[2];
     uint32_t entries[2];                              // the piece's teacher entries
     float teacher_sum[2];
@@ -181,8 +196,8 @@ __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity)
 }
 
 // Waits for a phase, bounded; false if the wait, or any wait of this CTA, gave up.
-template <int PM>
-__device__ __forceinline__ bool distill_wait(const DistillArgs<PM> &a, DistillShared &sh, uint64_t *barrier, uint32_t parity, unsigned code,
+template <int PM, int PASS>
+__device__ __forceinline__ bool distill_wait(const DistillArgs<PM> &a, DistillShared<PASS> &sh, uint64_t *barrier, uint32_t parity, unsigned code,
                                              uint32_t item)
 {
     const uint32_t bar = smem_addr(barrier);
@@ -205,8 +220,8 @@ __device__ __forceinline__ bool distill_wait(const DistillArgs<PM> &a, DistillSh
 }
 
 // Waits for all of the sums of this CTA's k-th row.
-template <int PM>
-__device__ __forceinline__ bool wait_sums(const DistillArgs<PM> &a, DistillShared &sh, uint32_t k, unsigned code, uint32_t item)
+template <int PM, int PASS>
+__device__ __forceinline__ bool wait_sums(const DistillArgs<PM> &a, DistillShared<PASS> &sh, uint32_t k, unsigned code, uint32_t item)
 {
     return __all_sync(0xffffffffu, distill_wait(a, sh, &sh.sums_in[k % kDistillSlots], (k / kDistillSlots) & 1, code, item));
 }
@@ -238,14 +253,14 @@ struct Piece {
 };
 
 template <typename T, int PM, int PASS>
-__global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __grid_constant__ DistillArgs<PM> a)
+__global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) distill_kernel(const __grid_constant__ DistillArgs<PM> a)
 {
     using Tr = Traits<T>;
     using Gr = Group<T>;
     constexpr int VEC = Tr::VEC, PAIRS = Gr::PAIRS, NG = kDistillGroups;
     constexpr bool FWD = PASS & CCL_PASS_FORWARD, BWD = PASS & CCL_PASS_BACKWARD;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ DistillShared sh;
+    __shared__ DistillShared<PASS> sh;
     const Shards<PM> &s = a.s;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const uint32_t S = a.stages;
@@ -253,7 +268,7 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
     // the teacher's warp for what its registers do not hold
     int *id_s = reinterpret_cast<int *>(smem + size_t(S) * kDistillStageBytes);
     float *e_s = reinterpret_cast<float *>(id_s + 2 * a.kpad), *z_s = e_s + 2 * a.kpad;
-    int *more_id = reinterpret_cast<int *>(z_s + 2 * a.kpad);
+    int *more_id = BWD ? reinterpret_cast<int *>(z_s + 2 * a.kpad) : id_s;
     float *more_e = reinterpret_cast<float *>(more_id + a.kpad), *more_z = more_e + a.kpad;
 
     if (tid == 0) {
@@ -290,7 +305,7 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
         auto issue = [&]() -> bool {
             const uint32_t st = issued % S;
             if (issued >= S && !__all_sync(0xffffffffu, distill_wait(a, sh, &sh.empty[st], (issued / S - 1) & 1, 6, item))) return false;
-            DistillDesc &d = sh.desc[issued % (S + 1)];
+            DistillDesc<PASS> &d = sh.desc[issued % (S + 1)];
             const uint32_t row = div_by(item, a.by_pieces), q = item - row * a.pieces, c = load % a.chunks;
             const uint32_t cap = a.segments == 1 ? kDistillStage : div_by(kDistillStage, a.by_segments);
             // lane l: segment l
@@ -312,7 +327,7 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
             }
             uint32_t first = 0, all = 0;
 #pragma unroll
-            for (int l = 0; l < kDistillMaxSegments; ++l) {
+            for (int l = 0; l < DistillShape<PASS>::segments; ++l) {
                 const uint32_t m = __shfl_sync(0xffffffffu, n, l);
                 if (l < lane) first += m;
                 all += m;
@@ -392,7 +407,7 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
         // 32 U of a row are held in registers: their ids and logits are
         // loaded two rows ahead, the student's logits at them one row ahead.
         // Any others are loaded when it is their turn and kept in shared memory.
-        constexpr int U = 4;
+        constexpr int U = DistillShape<PASS>::held;
         constexpr uint32_t ES = 16 / VEC;
         struct Held {
             int id[U];
@@ -587,20 +602,21 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
         const uint32_t stages_at = smem_addr(smem);
         // The row's maximum and 1 / sum from all its CTAs' sums, and its loss.
         auto total_of = [&](uint32_t slot, uint32_t q, uint32_t row, float &row_m, float &inv, float &factor, bool &taught) {
-            const DistillSums &in = sh.sums[slot];
+            const DistillSums<PASS> &in = sh.sums[slot];
+            constexpr int EACH = DistillShape<PASS>::cluster * kDistillWarps / 32;
             const float2 *pairs = &in.warp[0][0];
             const uint32_t n = a.pieces * kDistillWarps;
-            float2 v[kDistillMaxCluster * kDistillWarps / 32];
+            float2 v[EACH];
             float mx = -INFINITY, total = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kDistillMaxCluster * kDistillWarps / 32; ++i) {
+            for (int i = 0; i < EACH; ++i) {
                 v[i] = lane + 32 * i < n ? pairs[lane + 32 * i] : make_float2(-INFINITY, 0.0f);
                 mx = fmaxf(mx, v[i].x);
             }
             mx = warp_max(mx);
             row_m = finite_max(mx);
 #pragma unroll
-            for (int i = 0; i < kDistillMaxCluster * kDistillWarps / 32; ++i) total += v[i].y * ex2((v[i].x - row_m) * c2);
+            for (int i = 0; i < EACH; ++i) total += v[i].y * ex2((v[i].x - row_m) * c2);
             total = warp_sum(total);
             inv = total == 0.0f ? 0.0f : 1.0f / total;    // a row of nothing but -inf: p = 0
             if constexpr (BWD) {
@@ -644,29 +660,36 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
         for (uint32_t item = blockIdx.x; item < a.items; item += stride, ++k) {
             const uint32_t slot = k & 1, parity = (k >> 1) & 1;
             const uint32_t row = div_by(item, a.by_pieces), q = item - row * a.pieces;
-            Pair e[NG * PAIRS];
+            // the loss alone takes a stage by halves, the others keep all of it
+            constexpr int TAKE = BWD ? NG : NG / 2;
+            Pair e[TAKE * PAIRS];
             float m = -INFINITY, sum = 0.0f, edge = -INFINITY;
             bool ok = true;
-            const DistillDesc *d = nullptr;
-            // one chunk into e and edge, and its stage free again
-            auto take = [&]() -> typename Gr::Max {
-                const uint32_t st = used % S;
-                ok = __all_sync(0xffffffffu, distill_wait(a, sh, &sh.full[st], (used / S) & 1, 10, item));
-                typename Gr::Max gm = Gr::lowest();
-                if (!ok) return gm;
+            const DistillDesc<PASS> *d = nullptr;
+            // the next chunk's stage, once it is full
+            auto arrive = [&]() {
+                ok = __all_sync(0xffffffffu, distill_wait(a, sh, &sh.full[used % S], (used / S) & 1, 10, item));
+                if (!ok) return;
                 d = &sh.desc[used % (S + 1)];
-                const uint32_t at = stages_at + st * kDistillStageBytes + tid * 16, groups = d->groups;
+                edge = a.edges && uint32_t(tid) < a.segments * 2 * VEC ? d->edge[tid] : -INFINITY;
+            };
+            // its groups from `part` on into e; the stage free again after the last
+            auto take = [&](int part) -> typename Gr::Max {
+                const uint32_t st = used % S, at = stages_at + st * kDistillStageBytes + tid * 16, groups = d->groups;
+                typename Gr::Max gm = Gr::lowest();
 #pragma unroll
-                for (int n = 0; n < NG; ++n) {
-                    const uint4 v = uint32_t(tid + n * kDistillConsumers) < groups ? lds_v4(at + n * kDistillConsumers * 16) : lowest_group<T>();
+                for (int n = 0; n < TAKE; ++n) {
+                    const uint32_t g = (part + n) * kDistillConsumers;
+                    const uint4 v = tid + g < groups ? lds_v4(at + g * 16) : lowest_group<T>();
                     gm = Gr::max(gm, v);
 #pragma unroll
                     for (int i = 0; i < PAIRS; ++i) e[n * PAIRS + i] = Gr::pair(v, i);
                 }
-                edge = a.edges && uint32_t(tid) < a.segments * 2 * VEC ? d->edge[tid] : -INFINITY;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&sh.empty[st]));
-                ++used;
+                if (part + TAKE == NG) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(smem_addr(&sh.empty[st]));
+                    ++used;
+                }
                 return gm;
             };
             // stores e * g (edge: edge * g) where the chunk came from; zero for a row without a teacher
@@ -715,22 +738,26 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
             bool taught = true;
             if constexpr (FWD) {
                 for (uint32_t c = 0; c < a.chunks; ++c) {
-                    const float cm = Gr::value(take());
+                    arrive();
                     if (!ok) break;
-                    const float bm = fmaxf(m, fmaxf(cm, edge)), to = finite_max(bm);
-                    sum *= ex2((m - to) * c2);            // nothing yet: 0 * 2^-inf
-                    m = bm;
-                    edge = ex2((edge - to) * c2);
-                    Pair acc = {edge, 0.0f}, acc2 = {0.0f, 0.0f};
 #pragma unroll
-                    for (int i = 0; i < NG * PAIRS; i += 2) {
-                        e[i] = ex2((e[i] + Pair{-to, -to}) * cc);
-                        e[i + 1] = ex2((e[i + 1] + Pair{-to, -to}) * cc);
-                        acc = acc + e[i];
-                        acc2 = acc2 + e[i + 1];
+                    for (int part = 0; part < NG; part += TAKE) {
+                        const float cm = Gr::value(take(part));
+                        const float bm = fmaxf(m, part == 0 ? fmaxf(cm, edge) : cm), to = finite_max(bm);
+                        sum *= ex2((m - to) * c2);            // nothing yet: 0 * 2^-inf
+                        m = bm;
+                        Pair acc = {0.0f, 0.0f}, acc2 = {0.0f, 0.0f};
+                        if (part == 0) acc.x = edge = ex2((edge - to) * c2);
+#pragma unroll
+                        for (int i = 0; i < TAKE * PAIRS; i += 2) {
+                            e[i] = ex2((e[i] + Pair{-to, -to}) * cc);
+                            e[i + 1] = ex2((e[i + 1] + Pair{-to, -to}) * cc);
+                            acc = acc + e[i];
+                            acc2 = acc2 + e[i + 1];
+                        }
+                        acc = acc + acc2;
+                        sum += acc.x + acc.y;
                     }
-                    acc = acc + acc2;
-                    sum += acc.x + acc.y;
                 }
                 if (!ok) break;
                 const float wm = warp_max(m);
@@ -754,8 +781,9 @@ __global__ void __launch_bounds__(kDistillThreads, 2) distill_kernel(const __gri
                     put(inv * ex2((m - row_m) * c2) * factor, taught);
                 } else {
                     for (uint32_t c = 0; c < a.chunks; ++c) {
-                        take();
+                        arrive();
                         if (!ok) break;
+                        take(0);
                         if (!FWD && c == 0) {
                             ok = __all_sync(0xffffffffu, distill_wait(a, sh, &sh.taught[slot], parity, 13, item));
                             if (!ok) break;
@@ -816,18 +844,18 @@ template <typename T, int PM, int PASS>
 static cudaError_t distill_residents(const Launch &L, const cudaLaunchConfig_t &cfg, uint32_t pieces, uint32_t stages, uint32_t *ctas)
 {
     static std::atomic<unsigned long long> done{0};
-    static std::atomic<int> fit[kDistillMaxCluster + 1][kDistillMaxStages + 1];
+    static std::atomic<int> fit[DistillShape<PASS>::cluster + 1][DistillShape<PASS>::stages + 1];
     static std::atomic<int> fit_device{-1};
     auto kern = distill_kernel<T, PM, PASS>;
     const unsigned long long bit = (L.device >= 0 && L.device < 64) ? (1ull << L.device) : 0ull;
     if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
-        cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kDistillSmem));
+        cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(DistillShape<PASS>::smem));
         if (err == cudaSuccess) err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (err != cudaSuccess) return err;
         if (bit) done.fetch_or(bit, std::memory_order_acq_rel);
     }
     if (!(PASS & CCL_PASS_FORWARD)) {
-        *ctas = 2 * uint32_t(L.num_sms);
+        *ctas = DistillShape<PASS>::ctas * uint32_t(L.num_sms);
         return cudaSuccess;
     }
     int n = fit_device.load(std::memory_order_acquire) == L.device ? fit[pieces][stages].load(std::memory_order_acquire) : 0;
@@ -868,12 +896,13 @@ static cudaError_t distill_shape(const Launch &L, const DistillLaunch &N, Launch
     // portable eight CTAs where that will do and of sixteen where not (a
     // gradient alone needs no cluster, so any number); then, with fewer CTAs
     // than two per SM, more and smaller pieces, for latency.
-    a.segments = (p + kDistillMaxCluster - 1) / kDistillMaxCluster;
+    using Shape = DistillShape<PASS>;
+    a.segments = (p + Shape::cluster - 1) / Shape::cluster;
     a.parts = 1;
     auto per_part = [&](uint32_t parts) { return (groups + parts - 1) / parts; };
     uint32_t cap = kDistillStage / a.segments;
     if (a.segments == 1) {
-        const uint32_t most = (PASS & CCL_PASS_FORWARD) ? kDistillMaxCluster / p : (1u << 20) / p, portable = (PASS & CCL_PASS_FORWARD) ? 8 / p : most;
+        const uint32_t most = (PASS & CCL_PASS_FORWARD) ? Shape::cluster / p : (1u << 20) / p, portable = (PASS & CCL_PASS_FORWARD) ? 8 / p : most;
         while (a.parts < most && per_part(a.parts) > cap) ++a.parts;
         while (a.parts < portable && N.rows * p * a.parts < 2 * uint64_t(L.num_sms) && per_part(a.parts) > kDistillConsumers) ++a.parts;
     }
@@ -886,9 +915,10 @@ static cudaError_t distill_shape(const Launch &L, const DistillLaunch &N, Launch
     a.by_parts = fast_div(a.parts);
     a.by_segments = fast_div(a.segments);
     a.share = (a.k + a.pieces - 1) / a.pieces;
-    const size_t entries = size_t(a.kpad) * (a.kpad > 128 ? 36 : 24);
-    a.stages = kDistillMaxStages;
-    while (a.stages * size_t(kDistillStageBytes) + entries + sizeof(DistillShared) + 1024 > kDistillSmem) --a.stages;
+    const uint32_t in_registers = 32 * Shape::held, share = Shape::loss_alone ? a.share : a.k;
+    const size_t entries = size_t(a.kpad) * ((Shape::loss_alone ? 0 : 24) + (share > in_registers ? 12 : 0));
+    a.stages = Shape::stages;
+    while (a.stages > 1 && a.stages * size_t(kDistillStageBytes) + entries + sizeof(DistillShared<PASS>) + 1024 > Shape::smem) --a.stages;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kDistillThreads);
     cfg.dynamicSmemBytes = a.stages * size_t(kDistillStageBytes) + entries;
