@@ -302,6 +302,28 @@ __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) dis
         // ---- loads, and the gradient at the teacher's tokens -------------
         const uint32_t count = (a.items - blockIdx.x + stride - 1) / stride;   // items of this CTA: at least one
         uint32_t item = blockIdx.x, load = 0;                                  // the next to issue
+        // edge element e of the pieces of a load, as ShardRow::edge numbers them; a lane's first comes in ahead of its load
+        auto edge_of = [&](uint32_t of, uint32_t part, uint32_t e, float &z, uint64_t &to) {
+            const uint32_t row = div_by(of, a.by_pieces), c = part % a.chunks;
+            Piece<T, PM> pe(a, of - row * a.pieces, e / (2 * VEC));
+            z = -INFINITY;
+            to = 0;
+            if (pe.rank >= s.p || !in_bounds(row < s.rows, s.status, kSiteDistill, row)) return;
+            const ShardRow<T> in(s.in[pe.rank], s.ld, row, shard_width(s, pe.rank));
+            const int col = in.edge(e % (2 * VEC), pe.part == 0 && c == 0, pe.part + 1 == a.parts && c + 1 == a.chunks);
+            if (col < 0) return;
+            z = in.column(col);
+            if (BWD) {
+                const ShardRow<T> out(s.out[pe.rank], s.ld, row, in.width);
+                to = out.base + (uint64_t(out.shift) + uint32_t(col)) * (16 / VEC);
+            }
+        };
+        float edge_z = -INFINITY;
+        uint64_t edge_to = 0;
+        auto prefetch_edge = [&]() {
+            if (a.edges && item < a.items && lane < int(a.segments * 2 * VEC)) edge_of(item, load, lane, edge_z, edge_to);
+        };
+        prefetch_edge();
         auto issue = [&]() -> bool {
             const uint32_t st = issued % S;
             if (issued >= S && !__all_sync(0xffffffffu, distill_wait(a, sh, &sh.empty[st], (issued / S - 1) & 1, 6, item))) return false;
@@ -336,24 +358,11 @@ __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) dis
             const uint32_t bar = smem_addr(&sh.full[st]);
             if (n && !held) bulk_load(smem_addr(smem) + st * kDistillStageBytes + first * 16, from, n * 16, bar);
             if (lane < int(a.segments)) d.seg[lane].first = first;
-            // edges: thread e of a segment, as ShardRow::edge numbers them
-            for (uint32_t e = lane; a.edges && e < a.segments * 2 * VEC; e += 32) {
-                const uint32_t g = e / (2 * VEC);
-                Piece<T, PM> pe(a, q, g);
-                uint64_t to = 0;
-                float z = -INFINITY;
-                if (pe.rank < s.p) {
-                    const ShardRow<T> in(s.in[pe.rank], s.ld, row, shard_width(s, pe.rank));
-                    const int col = in.edge(e % (2 * VEC), pe.part == 0 && c == 0, pe.part + 1 == a.parts && c + 1 == a.chunks);
-                    if (col >= 0 && in_bounds(row < s.rows, s.status, kSiteDistill, row)) {
-                        z = in.column(col);
-                        const ShardRow<T> out(s.out[pe.rank], s.ld, row, in.width);
-                        to = out.base + (uint64_t(out.shift) + uint32_t(col)) * (16 / VEC);
-                    }
-                }
-                d.edge[e] = z;
-                d.edge_out[e] = to;
+            if (a.edges && lane < int(a.segments * 2 * VEC)) {
+                d.edge[lane] = edge_z;
+                d.edge_out[lane] = edge_to;
             }
+            for (uint32_t e = lane + 32; a.edges && e < a.segments * 2 * VEC; e += 32) edge_of(item, load, e, d.edge[e], d.edge_out[e]);
             if (lane == 0) d.groups = all;
             __syncwarp();
             if (lane == 0 && !held) mbar_arrive_expect_tx(bar, all * 16);
@@ -362,6 +371,7 @@ __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) dis
                 load = 0;
                 item += stride;
             }
+            prefetch_edge();
             return true;
         };
         const uint32_t every = count * loads;
