@@ -36,7 +36,8 @@
 // adds the same values in the same order, so all pieces of a row use the same
 // bits.  There are four slots, and a sender's sums for row k leave only after
 // all of row k - 2 has reached it: by then every CTA has sent its sums of row
-// k - 2, so it is done with the sums of row k - 4, which had the slot before.
+// k - 2, so it is done with the sums of row k - 4, which had the slot before
+// (its teacher's warp sends only after warp 8 is done with that row).
 // (For the loss alone the consumers see a row complete two rows later.)
 //
 // A piece beyond 2048 groups (vocabularies above 262144 16-bit or 131072
@@ -73,7 +74,7 @@ struct DistillShape {
     static constexpr uint32_t stages = loss_alone ? 2 : 3;
     static constexpr int cluster = loss_alone ? 8 : 16;          // pieces of a row
     static constexpr int segments = kMaxRanks / cluster;         // shards of a piece
-    static constexpr int held = loss_alone ? 2 : 4;              // teacher entries of a lane in registers
+    static constexpr int held = 2;                               // teacher entries of a lane in registers
     static constexpr size_t smem = (loss_alone ? 75 : 113) * 1024;   // of a CTA, a kilobyte of the system's included
 };
 
@@ -144,11 +145,12 @@ struct DistillShared {
     int dead;
 };
 
+// The maximum of a warp; a NaN is passed over.
 __device__ __forceinline__ float warp_max(float v)
 {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-    return v;
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
 }
 __device__ __forceinline__ float warp_sum(float v)
 {
@@ -298,6 +300,61 @@ __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) dis
     const uint32_t stride = gridDim.x;
     uint32_t issued = 0;
 
+    const float c2 = a.to_log2;
+    // The row's maximum and the sum of its exponentials, from all its CTAs' sums.
+    auto total_of = [&](uint32_t slot, float &mx) -> float {
+        constexpr int EACH = DistillShape<PASS>::cluster * kDistillWarps / 32;
+        const float2 *pairs = &sh.sums[slot].warp[0][0];
+        const uint32_t n = a.pieces * kDistillWarps;
+        float2 v[EACH];
+        mx = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+            v[i] = lane + 32 * i < n ? pairs[lane + 32 * i] : make_float2(-INFINITY, 0.0f);
+            mx = fmaxf(mx, v[i].x);
+        }
+        mx = warp_max(mx);
+        float total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) total += v[i].y * ex2((v[i].x - finite_max(mx)) * c2);
+        return warp_sum(total);
+    };
+    // The row's loss: one warp of its pieces in turn, two rows later, a consumer for the loss alone, else the teacher's.  (In the
+    // consumers' or the patching warp's way it would hold up all the CTAs of the row.)
+    auto finish_row = [&](uint32_t slot, uint32_t row) {
+        const DistillSums<PASS> &in = sh.sums[slot];
+        float mx;
+        const float total = total_of(slot, mx), row_m = finite_max(mx);
+        const float4 t = lane < int(a.pieces) ? in.teacher[lane][0] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float tsum, u, part = t.z;      // part: the entries' share of sum e
+        if constexpr (BWD) {
+            tsum = in.teacher[0][0].w;
+            u = in.teacher[0][1].x;
+        } else {
+            // the shares' maxima and sums together
+            const float top = warp_max(t.z != 0.0f ? t.w : -INFINITY), scale = t.z != 0.0f ? ex2((t.w - finite_max(top)) * c2) : 0.0f;
+            u = t.z != 0.0f ? scale * (in.teacher[lane][1].x + t.z * (t.w - top) / a.temperature) : 0.0f;
+            part *= scale;
+            tsum = warp_sum(part);
+            u = warp_sum(u);
+        }
+        // sum q (z - the row's maximum)
+        const float dot = warp_sum(part != 0.0f ? part / tsum * (t.y / t.z * 1024.0f + (t.x - row_m)) : 0.0f);
+        if (lane == 0) {
+            const float ls = logf(total), heat = a.temperature;
+            float loss = 0.0f;
+            if (tsum != 0.0f) {
+                if (total == 0.0f) loss = INFINITY;
+                else loss = heat * heat * ((u / tsum - logf(tsum)) - (dot / heat - ls));
+            }
+            a.loss[row] = loss;
+            if (a.stats) {
+                a.stats[2 * uint64_t(row)] = mx;
+                a.stats[2 * uint64_t(row) + 1] = ls;
+            }
+        }
+    };
+
     if (warp == kDistillWarps) {
         // ---- loads, and the gradient at the teacher's tokens -------------
         const uint32_t count = (a.items - blockIdx.x + stride - 1) / stride;   // items of this CTA: at least one
@@ -348,6 +405,8 @@ __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) dis
                 }
             }
             uint32_t first = 0, all = 0;
+            if (a.segments == 1) all = __shfl_sync(0xffffffffu, n, 0);
+            else
 #pragma unroll
             for (int l = 0; l < DistillShape<PASS>::segments; ++l) {
                 const uint32_t m = __shfl_sync(0xffffffffu, n, l);
@@ -386,9 +445,10 @@ __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) dis
                 ok = ok && __all_sync(0xffffffffu, distill_wait(a, sh, &sh.taught[slot], parity, 7, row_item));
                 ok = ok && __all_sync(0xffffffffu, distill_wait(a, sh, &sh.stored[slot], parity, 7, row_item));
                 if (!ok) break;
-                const float tsum = sh.teacher_sum[slot], row_m = sh.used_max[slot], inv = sh.used_inv[slot];
+                const uint32_t row = div_by(row_item, a.by_pieces);
+                const float tinv = __fdividef(1.0f, sh.teacher_sum[slot]), row_m = sh.used_max[slot], inv = sh.used_inv[slot];
                 const float factor = sh.weight[slot] * a.temperature;
-                const uint32_t row = div_by(row_item, a.by_pieces), n = sh.entries[slot];
+                const uint32_t n = sh.entries[slot];
                 const int *ids = id_s + slot * a.kpad;
                 const float *es = e_s + slot * a.kpad, *zs = z_s + slot * a.kpad;
                 for (uint32_t i = lane; i < n; i += 32) {
@@ -406,7 +466,7 @@ __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) dis
                     const uint32_t r = rank_of_token(s, uint32_t(id));
                     if (in_bounds(row < s.rows && r < s.p, s.status, kSiteDistill, row))
                         ShardRow<T>(s.out[r], s.ld, row, shard_width(s, r))
-                            .set_column(uint32_t(id) - shard_begin(s, r), (ex2((zs[i] - row_m) * a.to_log2) * inv - w / tsum) * factor);
+                            .set_column(uint32_t(id) - shard_begin(s, r), (ex2((zs[i] - row_m) * a.to_log2) * inv - w * tinv) * factor);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sh.taught_free[slot]));
@@ -433,6 +493,11 @@ __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) dis
             const uint64_t at = uint64_t(row) * a.k + begin + lane;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
+                if (32 * u >= share) {
+                    coming.id[u] = -1;
+                    coming.t[u] = -INFINITY;
+                    continue;
+                }
                 const bool in = lane + 32 * u < share;
                 coming.id[u] = in ? a.ids[at + 32 * u] : -1;
                 coming.t[u] = in ? load_any(a.teacher, a.teacher_dtype, at + 32 * u) : -INFINITY;
@@ -603,69 +668,22 @@ __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) dis
                     send4(at, bar, make_float4(ref, dot, own, BWD ? ts : tm));
                     send4(at + 16, bar, make_float4(tu, now.w, 0.0f, 0.0f));
                 }
+                if (BWD && k >= kDistillLag && q == (k - kDistillLag) % a.pieces)
+                    finish_row((k - kDistillLag) % kDistillSlots, div_by(item - kDistillLag * stride, a.by_pieces));
+            }
+        }
+        if constexpr (FWD && BWD) {
+            // the last rows' losses
+            for (uint32_t j = k > kDistillLag ? k - kDistillLag : 0u; j < k; ++j) {
+                const uint32_t item = blockIdx.x + j * stride, row = div_by(item, a.by_pieces);
+                if (!wait_sums(a, sh, j, 14, item)) break;
+                if (item - row * a.pieces == j % a.pieces) finish_row(j % kDistillSlots, row);
             }
         }
     } else {
         // ---- consumers ---------------------------------------------------
-        const float c2 = a.to_log2;
         const Pair cc = {c2, c2};
         const uint32_t stages_at = smem_addr(smem);
-        // The row's maximum and 1 / sum from all its CTAs' sums, and its loss.
-        auto total_of = [&](uint32_t slot, uint32_t q, uint32_t row, float &row_m, float &inv, float &factor, bool &taught) {
-            const DistillSums<PASS> &in = sh.sums[slot];
-            constexpr int EACH = DistillShape<PASS>::cluster * kDistillWarps / 32;
-            const float2 *pairs = &in.warp[0][0];
-            const uint32_t n = a.pieces * kDistillWarps;
-            float2 v[EACH];
-            float mx = -INFINITY, total = 0.0f;
-#pragma unroll
-            for (int i = 0; i < EACH; ++i) {
-                v[i] = lane + 32 * i < n ? pairs[lane + 32 * i] : make_float2(-INFINITY, 0.0f);
-                mx = fmaxf(mx, v[i].x);
-            }
-            mx = warp_max(mx);
-            row_m = finite_max(mx);
-#pragma unroll
-            for (int i = 0; i < EACH; ++i) total += v[i].y * ex2((v[i].x - row_m) * c2);
-            total = warp_sum(total);
-            inv = total == 0.0f ? 0.0f : 1.0f / total;    // a row of nothing but -inf: p = 0
-            if constexpr (BWD) {
-                taught = in.teacher[q][0].w != 0.0f;
-                factor = in.teacher[q][1].y * a.temperature;
-            }
-            if (q == 0 && warp == 0) {
-                const bool is = lane < int(a.pieces);
-                const float4 t = is ? in.teacher[lane][0] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                float tsum, u, part = t.z;      // part: the entries' share of sum e
-                if constexpr (BWD) {
-                    tsum = in.teacher[q][0].w;
-                    u = in.teacher[q][1].x;
-                } else {
-                    // the shares' maxima and sums together
-                    const float top = warp_max(t.z != 0.0f ? t.w : -INFINITY), scale = t.z != 0.0f ? ex2((t.w - finite_max(top)) * c2) : 0.0f;
-                    u = t.z != 0.0f ? scale * (in.teacher[lane][1].x + t.z * (t.w - top) / a.temperature) : 0.0f;
-                    part *= scale;
-                    tsum = warp_sum(part);
-                    u = warp_sum(u);
-                    taught = tsum != 0.0f;
-                }
-                // sum q (z - the row's maximum)
-                const float dot = warp_sum(part != 0.0f ? part / tsum * (t.y / t.z * 1024.0f + (t.x - row_m)) : 0.0f);
-                if (lane == 0) {
-                    const float ls = logf(total), heat = a.temperature;
-                    float loss = 0.0f;
-                    if (taught) {
-                        if (total == 0.0f) loss = INFINITY;
-                        else loss = heat * heat * ((u / tsum - logf(tsum)) - (dot / heat - ls));
-                    }
-                    a.loss[row] = loss;
-                    if (a.stats) {
-                        a.stats[2 * uint64_t(row)] = mx;
-                        a.stats[2 * uint64_t(row) + 1] = ls;
-                    }
-                }
-            }
-        };
         uint32_t used = 0, k = 0;
         for (uint32_t item = blockIdx.x; item < a.items; item += stride, ++k) {
             const uint32_t slot = k & 1, parity = (k >> 1) & 1;
@@ -775,15 +793,18 @@ __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) dis
                 // the loss alone does not wait for this row's sums, only for those of two rows back
                 if (!BWD && k >= kDistillLag) {
                     if (!wait_sums(a, sh, k - kDistillLag, 11, item)) break;
-                    if (q == 0 && warp == 0)
-                        total_of((k - kDistillLag) % kDistillSlots, q, div_by(item - kDistillLag * stride, a.by_pieces), row_m, inv, factor, taught);
+                    if (warp == 0 && q == (k - kDistillLag) % a.pieces) finish_row((k - kDistillLag) % kDistillSlots, div_by(item - kDistillLag * stride, a.by_pieces));
                 }
                 const uint32_t to = k % kDistillSlots;
                 if (lane < int(a.pieces))
                     send2(remote(smem_addr(&sh.sums[to].warp[q][warp]), lane), remote(smem_addr(&sh.sums_in[to]), lane), wm, ws);
                 if constexpr (BWD) {
                     if (!wait_sums(a, sh, k, 12, item)) break;
-                    total_of(to, q, row, row_m, inv, factor, taught);
+                    const float total = total_of(to, row_m);
+                    row_m = finite_max(row_m);
+                    inv = total == 0.0f ? 0.0f : 1.0f / total;    // a row of nothing but -inf: p = 0
+                    taught = sh.sums[to].teacher[q][0].w != 0.0f;
+                    factor = sh.sums[to].teacher[q][1].y * a.temperature;
                 }
             }
             if constexpr (BWD) {
@@ -822,10 +843,8 @@ __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) dis
             // the last rows' losses
             for (uint32_t j = k > kDistillLag ? k - kDistillLag : 0u; j < k; ++j) {
                 const uint32_t item = blockIdx.x + j * stride, row = div_by(item, a.by_pieces), q = item - row * a.pieces;
-                float row_m, inv, factor;
-                bool taught;
                 if (!wait_sums(a, sh, j, 14, item)) break;
-                if (q == 0 && warp == 0) total_of(j % kDistillSlots, q, row, row_m, inv, factor, taught);
+                if (warp == 0 && q == j % a.pieces) finish_row(j % kDistillSlots, row);
             }
         }
     }
