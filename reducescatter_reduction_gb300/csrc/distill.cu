@@ -74,7 +74,6 @@ struct DistillShape {
     static constexpr uint32_t stages = loss_alone ? 2 : 3;
     static constexpr int cluster = loss_alone ? 8 : 16;          // pieces of a row
     static constexpr int segments = kMaxRanks / cluster;         // shards of a piece
-    static constexpr int held = 2;                               // teacher entries of a lane in registers
     static constexpr size_t smem = (loss_alone ? 75 : 113) * 1024;   // of a CTA, a kilobyte of the system's included
 };
 
@@ -254,7 +253,9 @@ struct Piece {
     }
 };
 
-template <typename T, int PM, int PASS>
+// HELD: teacher entries of a lane in registers.  The teacher's warp bounds loss and gradient together, so it holds no
+// more than the call has: 64 entries, 4096 x 131072 bf16: 414 us with two a lane, 504 with four.
+template <typename T, int PM, int PASS, int HELD>
 __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) distill_kernel(const __grid_constant__ DistillArgs<PM> a)
 {
     using Tr = Traits<T>;
@@ -477,7 +478,7 @@ __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) dis
         // 32 U of a row are held in registers: their ids and logits are
         // loaded two rows ahead, the student's logits at them one row ahead.
         // Any others are loaded when it is their turn and kept in shared memory.
-        constexpr int U = DistillShape<PASS>::held;
+        constexpr int U = HELD;
         constexpr uint32_t ES = 16 / VEC;
         struct Held {
             int id[U];
@@ -582,25 +583,32 @@ __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) dis
             if (share > 32 * U) {
                 const Hold h = hold_of(item);
                 const uint64_t at = uint64_t(row) * a.k + begin;
-                for (uint32_t i = lane + 32 * U; i < share; i += 32) {
-                    int id = a.ids[at + i];
-                    float t = load_any(a.teacher, a.teacher_dtype, at + i), z;
-                    place(h, id, t, z);
-                    more_id[i] = id;
-                    more_e[i] = t;
-                    more_z[i] = z;
-                    tm = fmaxf(tm, t);
-                    if (id >= 0 && z < INFINITY) ref = fmaxf(ref, z);
+                constexpr int M = 4;          // loads in flight
+                for (uint32_t i0 = lane + 32 * U; i0 - lane < share; i0 += 32 * M) {
+                    int id[M];
+                    float t[M], z[M];
+#pragma unroll
+                    for (int u = 0; u < M; ++u) {
+                        const bool in = i0 + 32 * u < share;
+                        id[u] = in ? a.ids[at + i0 + 32 * u] : -1;
+                        t[u] = in ? load_any(a.teacher, a.teacher_dtype, at + i0 + 32 * u) : -INFINITY;
+                    }
+#pragma unroll
+                    for (int u = 0; u < M; ++u) place(h, id[u], t[u], z[u]);
+#pragma unroll
+                    for (int u = 0; u < M; ++u) {
+                        const uint32_t i = i0 + 32 * u;
+                        if (i >= share) break;
+                        more_id[i] = id[u];
+                        more_e[i] = t[u];
+                        more_z[i] = z[u];
+                        tm = fmaxf(tm, t[u]);
+                        if (id[u] >= 0 && z[u] < INFINITY) ref = fmaxf(ref, z[u]);
+                    }
                 }
             }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const float x = __shfl_xor_sync(0xffffffffu, tm, o), y = __shfl_xor_sync(0xffffffffu, ref, o);
-                tm = fmaxf(tm, x);
-                ref = fmaxf(ref, y);
-            }
-            tm = finite_max(tm);
-            ref = finite_max(ref);
+            tm = finite_max(warp_max(tm));
+            if (FWD) ref = finite_max(warp_max(ref));
             if (BWD && k >= 2 && !__all_sync(0xffffffffu, distill_wait(a, sh, &sh.taught_free[slot], ((k >> 1) - 1) & 1, 8, item))) break;
             float ts = 0.0f, tu = 0.0f, dot = 0.0f, own = 0.0f;
             uint32_t kept = 0;
@@ -661,6 +669,9 @@ __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) dis
             }
             if constexpr (FWD) {
                 if (k >= kDistillLag && !wait_sums(a, sh, k - kDistillLag, 9, item)) break;
+                // (before this row's sums leave: with them the others may go on to the row that gets its slot)
+                if (BWD && k >= kDistillLag && q == (k - kDistillLag) % a.pieces)
+                    finish_row((k - kDistillLag) % kDistillSlots, div_by(item - kDistillLag * stride, a.by_pieces));
                 const uint32_t to = k % kDistillSlots;
                 if (lane == 0) mbar_arrive_expect_tx(smem_addr(&sh.sums_in[to]), a.pieces * kDistillSumBytes);
                 if (lane < int(a.pieces)) {
@@ -668,8 +679,6 @@ __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) dis
                     send4(at, bar, make_float4(ref, dot, own, BWD ? ts : tm));
                     send4(at + 16, bar, make_float4(tu, now.w, 0.0f, 0.0f));
                 }
-                if (BWD && k >= kDistillLag && q == (k - kDistillLag) % a.pieces)
-                    finish_row((k - kDistillLag) % kDistillSlots, div_by(item - kDistillLag * stride, a.by_pieces));
             }
         }
         if constexpr (FWD && BWD) {
@@ -869,13 +878,13 @@ __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) dis
 
 // Shared-memory and cluster attributes, set once per device, and the clusters
 // of each size that fit the GPU at once.
-template <typename T, int PM, int PASS>
+template <typename T, int PM, int PASS, int HELD>
 static cudaError_t distill_residents(const Launch &L, const cudaLaunchConfig_t &cfg, uint32_t pieces, uint32_t stages, uint32_t *ctas)
 {
     static std::atomic<unsigned long long> done{0};
     static std::atomic<int> fit[DistillShape<PASS>::cluster + 1][DistillShape<PASS>::stages + 1];
     static std::atomic<int> fit_device{-1};
-    auto kern = distill_kernel<T, PM, PASS>;
+    auto kern = distill_kernel<T, PM, PASS, HELD>;
     const unsigned long long bit = (L.device >= 0 && L.device < 64) ? (1ull << L.device) : 0ull;
     if (!bit || !(done.load(std::memory_order_acquire) & bit)) {
         cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(DistillShape<PASS>::smem));
@@ -900,8 +909,8 @@ static cudaError_t distill_residents(const Launch &L, const cudaLaunchConfig_t &
     return cudaSuccess;
 }
 
-template <typename T, int PM, int PASS>
-static cudaError_t distill_shape(const Launch &L, const DistillLaunch &N, LaunchInfo *info)
+template <typename T, int PM, int PASS, int HELD>
+static cudaError_t distill_held(const Launch &L, const DistillLaunch &N, LaunchInfo *info)
 {
     DistillArgs<PM> a;
     fill_shards(&a.s, L, N.rows, N.vocab, N.ld);
@@ -944,7 +953,7 @@ static cudaError_t distill_shape(const Launch &L, const DistillLaunch &N, Launch
     a.by_parts = fast_div(a.parts);
     a.by_segments = fast_div(a.segments);
     a.share = (a.k + a.pieces - 1) / a.pieces;
-    const uint32_t in_registers = 32 * Shape::held, share = Shape::loss_alone ? a.share : a.k;
+    const uint32_t in_registers = 32 * HELD, share = Shape::loss_alone ? a.share : a.k;
     const size_t entries = size_t(a.kpad) * ((Shape::loss_alone ? 0 : 24) + (share > in_registers ? 12 : 0));
     a.stages = Shape::stages;
     while (a.stages > 1 && a.stages * size_t(kDistillStageBytes) + entries + sizeof(DistillShared<PASS>) + 1024 > Shape::smem) --a.stages;
@@ -963,10 +972,10 @@ static cudaError_t distill_shape(const Launch &L, const DistillLaunch &N, Launch
     cfg.numAttrs = (PASS & CCL_PASS_FORWARD) ? 2 : 1;
     cfg.gridDim = dim3(a.pieces);
     uint32_t ctas = 0;
-    cudaError_t err = distill_residents<T, PM, PASS>(L, cfg, a.pieces, a.stages, &ctas);
+    cudaError_t err = distill_residents<T, PM, PASS, HELD>(L, cfg, a.pieces, a.stages, &ctas);
     if (err != cudaSuccess) return err;
     cfg.gridDim = dim3(a.items < ctas ? a.items : ctas);
-    err = cudaLaunchKernelEx(&cfg, distill_kernel<T, PM, PASS>, a);
+    err = cudaLaunchKernelEx(&cfg, distill_kernel<T, PM, PASS, HELD>, a);
     if (err != cudaSuccess) return err;
     info->kernel = "distill_topk";
     info->grid = int(cfg.gridDim.x);
@@ -974,6 +983,14 @@ static cudaError_t distill_shape(const Launch &L, const DistillLaunch &N, Launch
     info->smem = cfg.dynamicSmemBytes;
     info->kernels = 1;
     return cudaGetLastError();
+}
+
+template <typename T, int PM, int PASS>
+static cudaError_t distill_shape(const Launch &L, const DistillLaunch &N, LaunchInfo *info)
+{
+    // the loss alone: of the entries each piece has a share
+    if (PASS == CCL_PASS_FORWARD || N.k <= 64) return distill_held<T, PM, PASS, 2>(L, N, info);
+    return distill_held<T, PM, PASS, 4>(L, N, info);
 }
 
 template <typename T, int PM>

@@ -115,7 +115,8 @@ def check(z, ids, t, T, p, dtype, steps="both", weight=None, teacher_dtype="f32"
 @pytest.mark.parametrize("steps", ["both", "forward", "each"])
 @pytest.mark.parametrize("p,rows,vocab,k,T", [
     (1, 1, 1, 1, 1.0), (1, 3, 7, 5, 2.0), (2, 4, 1000, 20, 1.0), (3, 5, 5003, 17, 0.5), (8, 4, 32768, 64, 2.0),
-    (3, 200, 33, 4, 1.5), (16, 3, 2051, 8, 1.0), (64, 2, 4099, 100, 3.0), (8, 3, 5, 3, 1.0), (1, 6, 50021, 1024, 2.0)])
+    (3, 200, 33, 4, 1.5), (16, 3, 2051, 8, 1.0), (64, 2, 4099, 100, 3.0), (8, 3, 5, 3, 1.0), (1, 6, 50021, 1024, 2.0),
+    (2, 9, 9001, 65, 1.0), (4, 5, 12007, 129, 2.0), (2, 4, 40009, 700, 1.0), (9, 40, 6001, 33, 1.0), (33, 3, 7001, 80, 1.0)])
 def test_matches_the_definition(dtype, steps, p, rows, vocab, k, T):
     g = rng(rows + vocab)
     ids, t = teacher(rows, vocab, k, 3)
