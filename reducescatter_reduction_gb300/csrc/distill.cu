@@ -9,14 +9,14 @@
 // A row is cut into Q pieces, each a part of one rank's shard (beyond 16
 // ranks: several whole shards), and a persistent CTA takes one piece of one
 // row after another.  Where the loss is computed the Q CTAs of a row form a
-// cluster and go through the rows together.  Ten warps, tied together by
-// mbarriers alone:
+// cluster and go through the rows together.  Ten or eleven warps, tied
+// together by mbarriers alone:
 //
 //   warp 8 (loads and patches)  brings the 16-byte groups of the piece of a
 //                               coming row into a stage of shared memory with
 //                               one bulk copy per shard, its edge elements and
 //                               where they go beside it, S stages ahead
-//   warp 9 (teacher)            softmax of the row's teacher entries, the
+//   warp 9, 10 (teacher)        softmax of the row's teacher entries, the
 //                               student's logits at those in the piece, and
 //                               their share of the loss
 //   warps 0-7 (consumers)       take a stage into registers and free it;
@@ -37,7 +37,8 @@
 // bits.  There are four slots, and a sender's sums for row k leave only after
 // all of row k - 2 has reached it: by then every CTA has sent its sums of row
 // k - 2, so it is done with the sums of row k - 4, which had the slot before
-// (its teacher's warp sends only after warp 8 is done with that row).
+// (its teacher's warp sends row k - 2 only after the loss of row k - 4; where
+// there are two, rows k, k - 2 and k - 4 are the same one's).
 // (For the loss alone the consumers see a row complete two rows later.)
 //
 // A piece beyond 2048 groups (vocabularies above 262144 16-bit or 131072
@@ -58,7 +59,15 @@ namespace ccl {
 
 constexpr int kDistillConsumers = 256;
 constexpr int kDistillWarps = kDistillConsumers / 32;
-constexpr int kDistillThreads = kDistillConsumers + 64;
+// One teacher's warp, or two that take the rows in turn.  4096 x 131072 bf16,
+// one against two: loss and gradient with 256 entries 1058 and 618 us, with
+// 128 entries 658 and 632; the gradient alone with 256 entries 663 and 461;
+// 2048 x 65536 f32 with 128 entries 175 and 186.  So two from 129 entries on,
+// with three in a lane's registers, as two have fewer registers each.
+template <int HELD>
+constexpr int kDistillTeachers = HELD == 3 ? 2 : 1;
+template <int HELD>
+constexpr int kDistillThreads = kDistillConsumers + 32 + 32 * kDistillTeachers<HELD>;
 constexpr int kDistillGroups = 8;                                      // groups a consumer takes of a stage
 constexpr uint32_t kDistillStage = kDistillConsumers * kDistillGroups; // groups of a stage
 constexpr uint32_t kDistillStageBytes = kDistillStage * 16;
@@ -254,9 +263,9 @@ struct Piece {
 };
 
 // HELD: teacher entries of a lane in registers.  The teacher's warp bounds loss and gradient together, so it holds no
-// more than the call has: 64 entries, 4096 x 131072 bf16: 414 us with two a lane, 504 with four.
+// more than the call has: 64 entries, 4096 x 131072 bf16: 410 us with two a lane, 446 with four.
 template <typename T, int PM, int PASS, int HELD>
-__global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) distill_kernel(const __grid_constant__ DistillArgs<PM> a)
+__global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::ctas) distill_kernel(const __grid_constant__ DistillArgs<PM> a)
 {
     using Tr = Traits<T>;
     using Gr = Group<T>;
@@ -271,8 +280,7 @@ __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) dis
     // the teacher's warp for what its registers do not hold
     int *id_s = reinterpret_cast<int *>(smem + size_t(S) * kDistillStageBytes);
     float *e_s = reinterpret_cast<float *>(id_s + 2 * a.kpad), *z_s = e_s + 2 * a.kpad;
-    int *more_id = BWD ? reinterpret_cast<int *>(z_s + 2 * a.kpad) : id_s;
-    float *more_e = reinterpret_cast<float *>(more_id + a.kpad), *more_z = more_e + a.kpad;
+    int *more = BWD ? reinterpret_cast<int *>(z_s + 2 * a.kpad) : id_s;
 
     if (tid == 0) {
         for (uint32_t i = 0; i < S; ++i) {
@@ -473,7 +481,7 @@ __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) dis
                 if (lane == 0) mbar_arrive(smem_addr(&sh.taught_free[slot]));
             }
         }
-    } else if (warp == kDistillWarps + 1) {
+    } else if (warp > kDistillWarps) {
         // ---- the teacher's entries ---------------------------------------
         // 32 U of a row are held in registers: their ids and logits are
         // loaded two rows ahead, the student's logits at them one row ahead.
@@ -563,17 +571,22 @@ __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) dis
             for (int u = 0; u < U; ++u)
                 if (32 * u < share) place(h, next.id[u], next.t[u], next.z[u]);
         };
-        fetch(blockIdx.x);
-        place_all(blockIdx.x);
-        fetch(blockIdx.x + stride);
+        constexpr uint32_t TEACHERS = kDistillTeachers<HELD>;
+        const uint32_t who_am_i = warp - kDistillWarps - 1, turn = TEACHERS * stride;
+        int *more_id = more + 3 * who_am_i * a.kpad;
+        float *more_e = reinterpret_cast<float *>(more_id + a.kpad), *more_z = more_e + a.kpad;
+        uint32_t k = who_am_i;
+        const uint32_t item0 = blockIdx.x + who_am_i * stride;
+        fetch(item0);
+        place_all(item0);
+        fetch(item0 + turn);
         const float per_t = 1.0f / a.temperature;
-        uint32_t k = 0;
-        for (uint32_t item = blockIdx.x; item < a.items; item += stride, ++k) {
+        for (uint32_t item = item0; item < a.items; item += turn, k += TEACHERS) {
             const uint32_t slot = k & 1;
             const uint32_t row = div_by(item, a.by_pieces), q = item - row * a.pieces;
             now = next;
-            place_all(item + stride);
-            fetch(item + 2 * stride);
+            place_all(item + turn);
+            fetch(item + 2 * turn);
             float tm = -INFINITY, ref = -INFINITY;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -683,8 +696,10 @@ __global__ void __launch_bounds__(kDistillThreads, DistillShape<PASS>::ctas) dis
         }
         if constexpr (FWD && BWD) {
             // the last rows' losses
-            for (uint32_t j = k > kDistillLag ? k - kDistillLag : 0u; j < k; ++j) {
+            const uint32_t rows = (a.items - blockIdx.x + stride - 1) / stride;
+            for (uint32_t j = rows > kDistillLag ? rows - kDistillLag : 0u; j < rows; ++j) {
                 const uint32_t item = blockIdx.x + j * stride, row = div_by(item, a.by_pieces);
+                if (j % TEACHERS != who_am_i) continue;
                 if (!wait_sums(a, sh, j, 14, item)) break;
                 if (item - row * a.pieces == j % a.pieces) finish_row(j % kDistillSlots, row);
             }
@@ -954,11 +969,11 @@ static cudaError_t distill_held(const Launch &L, const DistillLaunch &N, LaunchI
     a.by_segments = fast_div(a.segments);
     a.share = (a.k + a.pieces - 1) / a.pieces;
     const uint32_t in_registers = 32 * HELD, share = Shape::loss_alone ? a.share : a.k;
-    const size_t entries = size_t(a.kpad) * ((Shape::loss_alone ? 0 : 24) + (share > in_registers ? 12 : 0));
+    const size_t entries = size_t(a.kpad) * ((Shape::loss_alone ? 0 : 24) + (share > in_registers ? 12 * kDistillTeachers<HELD> : 0));
     a.stages = Shape::stages;
     while (a.stages > 1 && a.stages * size_t(kDistillStageBytes) + entries + sizeof(DistillShared<PASS>) + 1024 > Shape::smem) --a.stages;
     cudaLaunchConfig_t cfg = {};
-    cfg.blockDim = dim3(kDistillThreads);
+    cfg.blockDim = dim3(kDistillThreads<HELD>);
     cfg.dynamicSmemBytes = a.stages * size_t(kDistillStageBytes) + entries;
     cfg.stream = L.stream;
     cudaLaunchAttribute attr[2];
@@ -979,7 +994,7 @@ static cudaError_t distill_held(const Launch &L, const DistillLaunch &N, LaunchI
     if (err != cudaSuccess) return err;
     info->kernel = "distill_topk";
     info->grid = int(cfg.gridDim.x);
-    info->block = kDistillThreads;
+    info->block = kDistillThreads<HELD>;
     info->smem = cfg.dynamicSmemBytes;
     info->kernels = 1;
     return cudaGetLastError();
@@ -988,9 +1003,12 @@ static cudaError_t distill_held(const Launch &L, const DistillLaunch &N, LaunchI
 template <typename T, int PM, int PASS>
 static cudaError_t distill_shape(const Launch &L, const DistillLaunch &N, LaunchInfo *info)
 {
-    // the loss alone: of the entries each piece has a share
-    if (PASS == CCL_PASS_FORWARD || N.k <= 64) return distill_held<T, PM, PASS, 2>(L, N, info);
-    return distill_held<T, PM, PASS, 4>(L, N, info);
+    // (the loss alone: each piece has a share of the entries)
+    if constexpr (PASS != CCL_PASS_FORWARD) {
+        if (N.k > 128) return distill_held<T, PM, PASS, 3>(L, N, info);
+        if (N.k > 64) return distill_held<T, PM, PASS, 4>(L, N, info);
+    }
+    return distill_held<T, PM, PASS, 2>(L, N, info);
 }
 
 template <typename T, int PM>
