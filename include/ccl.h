@@ -219,13 +219,15 @@ CCL_API ccl_status_t ccl_set_launch(ccl_comm_t comm, int sm_budget, int variant,
 
 /* Failure-detection hooks (tests).
  *  wait_limit_ns : bound on any single wait inside a kernel that waits (the
- *                  TMA variant's pipeline barriers); 0 restores the default
+ *                  TMA variant's pipeline barriers, the fused RMSNorm's and
+ *                  the distillation's exchange); 0 restores the default
  *                  of 2 s.  On expiry the kernel records the wait in the
  *                  status block, stops, and ccl_comm_check() returns
  *                  CCL_ERR_TIMEOUT.
  *  stall_test    : 1 makes the TMA producer withhold its second tile, and the
  *                  fused RMSNorm's second CTA of a row withhold its partial
- *                  sum, so that a bounded wait runs out: the timeout path is
+ *                  sum, and every CTA of the distillation its second load, so
+ *                  that a bounded wait runs out: the timeout path is
  *                  exercised without faulting or hanging the GPU.  2 (the
  *                  checked build only; nothing otherwise) makes the TMA
  *                  producer's bounds check of its second tile fail, so that
@@ -366,6 +368,7 @@ typedef struct {
  * with c its generated occurrences:
  *   x += the row's bias entries for v
  *   x = x > 0 ? x / repetition : x * repetition   if v occurs in the history
+ *       (x / repetition as x times the rounded 1 / repetition)
  *   x = (x - frequency * c) - presence            if c > 0
  *   x = -inf                                      if the row's mask forbids v
  * A row that its mask leaves nothing is all -inf.
@@ -399,7 +402,11 @@ typedef enum { CCL_PASS_FORWARD = 1, CCL_PASS_BACKWARD = 2, CCL_PASS_BOTH = 3 } 
  * probability 0 (loss +inf if the teacher has weight there); a row of nothing
  * but -inf has p = 0 and loss +inf.
  * Bytes moved: rows * vocab * s read; BACKWARD and BOTH also write it.  BOTH
- * reads the logits twice beyond 131072 columns.
+ * reads the logits twice where a row does not fit on chip: beyond 512 KB of a
+ * row on 1, 2, 4, 8 or 16 ranks, somewhat earlier on others.
+ * FORWARD and BOTH exchange sums between CTAs: their waits are bounded by the
+ * communicator's wait limit, and one that gives up makes ccl_comm_check()
+ * return CCL_ERR_TIMEOUT (the outputs are then incomplete).
  * Errors: CCL_ERR_INVALID_ARG (a size, pass or temperature out of range, a
  * missing array, overlap), CCL_ERR_UNSUPPORTED (int32, k > 1024),
  * CCL_ERR_CUDA. */

@@ -11,7 +11,10 @@
 // integer counts in fp64 as d_e = a_e - mean(a) before fp32 sees them;
 // p_te (d_e - sum_j p_tj d_j) is the same gradient, and the loss is
 // mean(a) (rows with a softmax) + sum_t sum_e p_te d_e.
+#include "async.cuh"
 #include "logits.cuh"
+
+#include <utility>
 
 namespace ccl {
 
@@ -19,7 +22,10 @@ constexpr int kBalanceThreads = 256;
 constexpr int kBalanceWarps = kBalanceThreads / 32;
 constexpr int kCountThreads = 1024;
 // Up to this many choices and counters in all, every CTA counts for itself
-// instead of waiting for a counting kernel.
+// instead of waiting for a counting kernel: one launch less.  Measured (8
+// ranks, 64 bf16 experts, 6 choices; graph replay, us; counting here against
+// the kernel): 3072 choices 8.0, 8.7; 8160 9.6, 9.1; 16320 12.1, 9.0.  Called
+// one by one, the second launch costs the host about 3 us more.
 constexpr uint64_t kCountHereIds = 8192;
 constexpr uint64_t kCountHereCells = 4096;
 
@@ -45,7 +51,11 @@ struct BalanceArgs {
 
 // Counts the choices and valid rows of all ranks into cells, which are zero.
 // A CTA counts in shared memory first: integer atomics, so any order gives
-// the same counts.
+// the same counts.  Bound by latency and the shared-memory atomics: 1 Mi
+// choices of 256 experts add 8 us to the call.  The cells are the
+// communicator's scratch, left at zero by the call's last CTA; with a memset
+// of the caller's counters instead, 8 x 16384 x 256 bf16 took 37.4 us, not
+// 32.6 (what calls do whose p * experts the scratch does not hold).
 template <int PM>
 __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const __grid_constant__ BalanceArgs<PM> a)
 {
@@ -247,7 +257,11 @@ __device__ __forceinline__ void balance_finish(const BalanceArgs<PM> &a, float l
 }
 
 // L lanes of a warp take a row, 16-byte groups l, l + L, ... of it; NV groups
-// a lane hold the whole row, so the logits are read once.
+// a lane hold the whole row, so the logits are read once and the next row's
+// are on their way meanwhile; L is as small as holds the row, for fewer
+// shuffles.  Bound by memory and about 12 us of launches, counting and the
+// last CTA's sum: 8 x 16384 x 256 bf16, loss and gradient, 32.6 us (4.2 TB/s
+// in all); f32, 4 x 65536 x 128, the loss, 30.8 us (4.4 TB/s).
 template <typename T, int PM, int L, int NV>
 __global__ void __launch_bounds__(kBalanceThreads, NV * Traits<T>::VEC > 16 ? 2 : NV > 2 ? 3 : 4) balance_kernel(const __grid_constant__ BalanceArgs<PM> a)
 {
@@ -353,8 +367,194 @@ __global__ void __launch_bounds__(kBalanceThreads, NV * Traits<T>::VEC > 16 ? 2 
     if (fwd) balance_finish(a, lean_sum, live, mean);
 }
 
-// Any number of experts and any alignment: a warp per row, element by
-// element, the row read once per step (the later reads from cache).
+// Rows of up to 1024 experts that are not whole, aligned 16-byte groups.  A
+// warp takes 32 / L rows at a time: they are consecutive in memory, so it
+// brings the groups that hold them into shared memory asynchronously, STAGES
+// - 1 steps ahead, and its lanes read their elements l, l + L, ... from there;
+// the gradient goes back the same way, whole groups and a few edge elements.
+// Bound by instructions, element by element: 8 x 60000 x 60 bf16 61 us, 8 x
+// 20000 x 203 68, 8 x 400000 x 9 77 (a warp per row without the stages: 152,
+// 87, 721).  Where the rows are aligned groups balance_kernel is the faster:
+// 8 x 65536 x 64 bf16 35 against 85 us, 8 x 32768 x 128 f32 55 against 74.
+template <int NE>
+constexpr int kOddStages = NE > 16 ? 2 : 3;
+template <int NE>
+constexpr int kOddCtas = NE > 16 ? 2 : 3;     // per SM
+
+// f(0) ... f(N - 1), each with its number as a constant
+template <int N, typename F, int... I>
+__device__ __forceinline__ void each_of(F f, std::integer_sequence<int, I...>)
+{
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F f)
+{
+    each_of<N>(f, std::make_integer_sequence<int, N>{});
+}
+
+constexpr uint32_t kOddSlack = 256;           // bytes that reads past the last row may reach into
+// bytes of a step's groups, wherever in a group its rows begin
+__host__ __device__ inline uint32_t odd_span(uint32_t rows, uint32_t row_bytes) { return (rows * row_bytes + 30) / 16 * 16; }
+
+// One element from or to shared memory, OFF bytes beyond addr.
+template <typename T, int OFF>
+__device__ __forceinline__ float lds_element(uint32_t addr)
+{
+    uint32_t v;
+    if constexpr (Traits<T>::VEC == 4) {
+        asm volatile("ld.shared.u32 %0, [%1+%2];" : "=r"(v) : "r"(addr), "n"(OFF) : "memory");
+        return __uint_as_float(v);
+    } else {
+        asm volatile("ld.shared.u16 %0, [%1+%2];" : "=r"(v) : "r"(addr), "n"(OFF) : "memory");
+        return Group<T>::pair(make_uint4(v, 0, 0, 0), 0).x;
+    }
+}
+
+// The pair's elements, OFF and NEXT bytes beyond addr; the second only if `both`.
+template <typename T, int OFF, int NEXT>
+__device__ __forceinline__ void sts_pair(uint32_t addr, Pair v, bool first, bool both)
+{
+    if constexpr (Traits<T>::VEC == 4) {
+        if (first) asm volatile("st.shared.f32 [%0+%1], %2;" ::"r"(addr), "n"(OFF), "f"(v.x) : "memory");
+        if (both) asm volatile("st.shared.f32 [%0+%1], %2;" ::"r"(addr), "n"(NEXT), "f"(v.y) : "memory");
+    } else {
+        const uint32_t w = Traits<T>::pack2(v.x, v.y);
+        if (first) asm volatile("st.shared.u16 [%0+%1], %2;" ::"r"(addr), "n"(OFF), "r"(w) : "memory");
+        if (both) asm volatile("st.shared.u16 [%0+%1], %2;" ::"r"(addr), "n"(NEXT), "r"(w >> 16) : "memory");
+    }
+}
+
+template <typename T, int PM, int L, int NE>
+__global__ void __launch_bounds__(kBalanceThreads, kOddCtas<NE>) balance_odd_kernel(const __grid_constant__ BalanceArgs<PM> a)
+{
+    using Tr = Traits<T>;
+    constexpr int S = 16 / Tr::VEC, RPW = 32 / L, PAIRS = NE / 2, STAGES = kOddStages<NE>;
+    extern __shared__ __align__(16) unsigned char stages_s[];
+    const uint32_t E = a.experts, r = blockIdx.y, row_bytes = E * S, span = odd_span(RPW, row_bytes);
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, l = lane % L, mine = lane / L;
+    unsigned char *in_s = stages_s + warp * (STAGES + 1) * span, *out_s = in_s + STAGES * span;
+    // a row of -inf, which is what a padding row is read as
+    unsigned char *low_s = stages_s + kBalanceWarps * (STAGES + 1) * span;
+    float *d_s = reinterpret_cast<float *>(low_s + (row_bytes + 15) / 16 * 16 + kOddSlack);
+    for (uint32_t e = threadIdx.x; e < E; e += kBalanceThreads) Tr::store1(low_s, e, -INFINITY);
+    const bool fwd = a.pass & CCL_PASS_FORWARD, bwd = a.pass & CCL_PASS_BACKWARD;
+    const uint8_t *valid = a.has_valid ? a.valid[r] : nullptr;
+    const uint64_t stride = uint64_t(gridDim.x) * kBalanceWarps * RPW;
+    const uintptr_t in = uintptr_t(a.in[r]), in_end = in + a.rows * row_bytes, out = uintptr_t(a.out[r]), out_end = out + a.rows * row_bytes;
+    uint64_t t = (uint64_t(blockIdx.x) * kBalanceWarps + warp) * RPW;    // the warp's first row
+    auto fetch = [&](uint64_t row, uint32_t stage) {
+        if (row < a.rows) {
+            const uintptr_t b0 = in + row * row_bytes, b1 = min(b0 + RPW * row_bytes, in_end), lo = b0 & ~uintptr_t(15);
+            unsigned char *to = in_s + stage * span;
+            const uint32_t n = uint32_t(b1 - lo), to32 = smem_addr(to);
+            if (lo >= in && lo + (n + 15) / 16 * 16 <= in_end) {
+                for (uint32_t g = lane * 16; g < n; g += 512)
+                    if (in_bounds(g + 16 <= span, a.status, kSiteBalance, row))
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to32 + g), "l"(lo + g) : "memory");
+            } else {      // the first or last group of the buffer is not all of it
+                for (uint32_t g = lane * S; g < n; g += 32 * S)
+                    if (lo + g >= in && in_bounds(g + S <= span, a.status, kSiteBalance, row))
+                        Tr::store1(to + g, 0, Tr::load1(reinterpret_cast<const void *>(lo + g), 0));
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    grid_dependency_wait();
+    grid_dependents_launch();
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) fetch(t + i * stride, i);
+    auto is_on = [&](uint64_t row) { return row < a.rows && (!valid || valid[row]); };
+    bool coming = is_on(t + mine);
+    const float mean = balance_coefficients(a, d_s, reinterpret_cast<int *>(d_s + E));
+    Pair d[PAIRS];
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+        const uint32_t e = 2 * i * L + l;
+        d[i] = {e < E ? d_s[e] : 0.0f, e + L < E ? d_s[e + L] : 0.0f};
+    }
+    const float up = bwd && a.dloss ? *a.dloss : 1.0f;
+    float lean_sum = 0.0f;
+    int live = 0;
+    uint32_t stage = 0;
+    for (; t < a.rows; t += stride) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+        __syncwarp();
+        fetch(t + (STAGES - 1) * stride, stage == 0 ? STAGES - 1 : stage - 1);
+        const bool on = coming;
+        coming = is_on(t + stride + mine);
+        const uintptr_t b0 = in + t * row_bytes, o0 = out + t * row_bytes;
+        const uint32_t from = smem_addr(on ? in_s + stage * span + b0 % 16 + mine * row_bytes : low_s) + l * S;
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
+        Pair x[PAIRS];
+        float m = -INFINITY;
+        each<PAIRS>([&](auto I) {
+            constexpr int i = decltype(I)::value;
+            x[i] = {-INFINITY, -INFINITY};
+            if (2 * i * L >= E) return;          // the whole warp
+            // reads past the row, up to 2 L elements, are of shared memory all the same
+            const float v0 = lds_element<T, 2 * i * L * S>(from), v1 = lds_element<T, (2 * i + 1) * L * S>(from);
+            x[i] = {v0, v1};
+            if ((2 * i + 2) * L > E) {
+                if (2 * i * L + l >= E) x[i].x = -INFINITY;
+                if ((2 * i + 1) * L + l >= E) x[i].y = -INFINITY;
+            }
+            m = fmaxf(m, fmaxf(x[i].x, x[i].y));
+        });
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        m = finite_max(m);
+        Pair sum = {0.0f, 0.0f}, dot = {0.0f, 0.0f};
+        const float mc = m * kLog2e;             // (as in balance_kernel)
+        const bool tame = __all_sync(0xffffffffu, fabsf(mc) < INFINITY);
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+            if (2 * i * L >= E) continue;
+            if (tame) x[i] = ex2(fma(x[i], Pair{kLog2e, kLog2e}, Pair{-mc, -mc}));
+            else x[i] = ex2((x[i] + Pair{-m, -m}) * Pair{kLog2e, kLog2e});
+            sum = sum + x[i];
+            dot = fma(x[i], d[i], dot);
+        }
+        float s = sum.x + sum.y, w = dot.x + dot.y;
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) {
+            const float s2 = __shfl_xor_sync(0xffffffffu, s, o), w2 = __shfl_xor_sync(0xffffffffu, w, o);
+            s += s2;
+            w += w2;
+        }
+        const float inv = s == 0.0f ? 0.0f : __fdividef(1.0f, s);
+        const float lean = w * inv;
+        if (l == 0 && s != 0.0f) {
+            lean_sum += lean;
+            ++live;
+        }
+        if (bwd) {
+            const Pair g = {inv * up, inv * up}, off = {-lean, -lean};
+            const uint32_t to = smem_addr(out_s) + uint32_t(o0 % 16) + mine * row_bytes + l * S;
+            each<PAIRS>([&](auto I) {
+                constexpr int i = decltype(I)::value;
+                if (2 * i * L >= E) return;
+                const bool full = (2 * i + 2) * L <= E;
+                sts_pair<T, 2 * i * L * S, (2 * i + 1) * L * S>(to, (x[i] * (d[i] + off)) * g, full || 2 * i * L + l < E,
+                                                               full || (2 * i + 1) * L + l < E);
+            });
+            __syncwarp();
+            const uintptr_t o1 = min(o0 + RPW * row_bytes, out_end), low = o0 & ~uintptr_t(15);
+            const uintptr_t first = (o0 + 15) & ~uintptr_t(15), last = o1 & ~uintptr_t(15), head = min(first, o1), tail = max(last, head);
+            if (!in_bounds(o1 - low <= span, a.status, kSiteBalance, t)) continue;
+            const uint32_t skip = uint32_t(first - low), whole = last > first ? uint32_t(last - first) : 0u, out32 = smem_addr(out_s) + skip;
+            for (uint32_t g = lane * 16; g < whole; g += 512) st_stream_v4(reinterpret_cast<void *>(first + g), lds_v4(out32 + g));
+            const uintptr_t edge = lane < 8 ? o0 + lane * S : tail + (lane - 8) * S;     // at most seven before, and seven after
+            if (lane < 16 && edge < (lane < 8 ? head : o1))
+                Tr::store1(reinterpret_cast<void *>(edge), 0, Tr::load1(out_s + (edge - low), 0));
+        }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (fwd) balance_finish(a, lean_sum, live, mean);
+}
+
+// More than 1024 experts: a warp per row, element by element, the row read
+// once per step (the later reads from cache).  8 x 2048 x 2048 bf16: 89 us.
 template <typename T, int PM>
 __global__ void __launch_bounds__(kBalanceThreads) balance_any_kernel(const __grid_constant__ BalanceArgs<PM> a)
 {
@@ -410,6 +610,17 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_any_kernel(const __gr
         }
     }
     if (fwd) balance_finish(a, lean_sum, live, mean);
+}
+
+// The most shared memory: rows of the lanes' elements, an expert's coefficient, and a count per cell.
+template <typename T, int PM, int L, int NE>
+static cudaError_t odd_kernel(int device, void (**kern)(BalanceArgs<PM>))
+{
+    constexpr uint32_t most = L * NE;
+    static std::atomic<unsigned long long> done{0};
+    *kern = balance_odd_kernel<T, PM, L, NE>;
+    return allow_dynamic_smem(*kern, kBalanceWarps * (kOddStages<NE> + 1) * size_t(odd_span(32 / L, most * (16 / Traits<T>::VEC))) + kOddSlack + most * 8 +
+                                         (kCountHereCells + PM) * 4, device, done);
 }
 
 template <typename T, int PM>
@@ -477,8 +688,27 @@ static cudaError_t balance_shape(const Launch &L, const BalanceLaunch &N, Launch
         ++info->kernels;
     }
     void (*kern)(BalanceArgs<PM>) = balance_any_kernel<T, PM>;
-    int lanes = 32;
-    if (vec && N.experts <= 1024) {
+    int lanes = 32, per_sm = 6;      // CTAs that an SM holds at once: the kernels' launch bounds; this one's registers
+    size_t smem = size_t(N.experts) * 4 + (a.count_here ? size_t(cells + L.p) * 4 : 0);
+    if (!vec && N.experts <= 1024) {
+        lanes = 1;
+        while (lanes < 32 && uint32_t(lanes) * 16 < N.experts) lanes *= 2;
+        switch (lanes) {
+        case 1: err = odd_kernel<T, PM, 1, 16>(L.device, &kern); break;
+        case 2: err = odd_kernel<T, PM, 2, 16>(L.device, &kern); break;
+        case 4: err = odd_kernel<T, PM, 4, 16>(L.device, &kern); break;
+        case 8: err = odd_kernel<T, PM, 8, 16>(L.device, &kern); break;
+        case 16: err = odd_kernel<T, PM, 16, 16>(L.device, &kern); break;
+        default:
+            if (N.experts <= 512) err = odd_kernel<T, PM, 32, 16>(L.device, &kern);
+            else err = odd_kernel<T, PM, 32, 32>(L.device, &kern);
+        }
+        if (err != cudaSuccess) return err;
+        const bool wide = N.experts > 512;
+        per_sm = wide ? kOddCtas<32> : kOddCtas<16>;
+        smem += kBalanceWarps * ((wide ? kOddStages<32> : kOddStages<16>) + 1) * size_t(odd_span(32 / lanes, N.experts * (16 / VEC))) + (N.experts * (16 / VEC) + 15) / 16 * 16 + kOddSlack;
+    } else if (vec && N.experts <= 1024) {
+        per_sm = N.experts > 512 ? 2 : NV > 2 ? 3 : 4;
         lanes = 1;
         while (lanes < 32 && uint32_t(lanes) * 16 < N.experts) lanes *= 2;
         switch (lanes) {
@@ -494,13 +724,11 @@ static cudaError_t balance_shape(const Launch &L, const BalanceLaunch &N, Launch
     }
     const uint64_t rows_per_cta = uint64_t(kBalanceWarps) * (32 / lanes);
     const uint64_t want = (N.rows + rows_per_cta - 1) / rows_per_cta;
-    // the CTAs that the kernel's registers let an SM hold, once (balance_kernel's launch bounds; the generic kernel's 40)
-    const int per_sm = lanes == 32 && (!vec || N.experts > 1024) ? 6 : N.experts > 512 ? 2 : NV > 2 ? 3 : 4;
     const uint64_t all = uint64_t(per_sm) * L.num_sms < kMaxPartials ? uint64_t(per_sm) * L.num_sms : kMaxPartials, most = all / L.p;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(want < 1 ? 1 : want < most ? want : most), unsigned(L.p));
     cfg.blockDim = dim3(kBalanceThreads);
-    cfg.dynamicSmemBytes = size_t(N.experts) * 4 + (a.count_here ? size_t(cells + L.p) * 4 : 0);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = L.stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

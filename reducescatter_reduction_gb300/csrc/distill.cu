@@ -48,6 +48,12 @@
 // Differences z - m are formed before the scaling by 1 / T, so that masks of
 // the type's lowest value do not turn into inf - inf.
 //
+// Measured (graph replay): loss and gradient, 4096 x 131072 bf16 on 8 ranks,
+// 64 entries: 405-425 us (5.1-5.3 TB/s), bound by the teacher's warp and by
+// the exchange's latency (one entry: 368, 128: 632); 700 x 100003 bf16 on 3,
+// whose pieces fill two thirds of a stage: 88 us.  The loss alone, 2048 x
+// 65536 f16: 52 us (5.2 TB/s); the gradient alone, f32: 175 us (6.2 TB/s).
+//
 // Every wait is bounded by the communicator's wait limit; one that gives up
 // records itself in the status block, and the CTA leaves its loops, waits
 // (bounded) for its copies in flight and for the other CTAs of the row, and
@@ -75,7 +81,9 @@ constexpr uint32_t kDistillStageBytes = kDistillStage * 16;
 // What a pass is built for.  The loss alone keeps no exponentials, so an SM
 // holds three CTAs of it instead of two (of two stages instead of three), in
 // clusters of up to eight: beyond, its pieces come in chunks, which cost it
-// nothing.
+// less than clusters of sixteen (2048 x 262144 bf16 on 8 ranks: 194 against
+// 229 us; 2048 x 65536 f16 on 16: 116 against 235).  Three CTAs against two:
+// 2048 x 65536 f16, 62 against 75 us at the time.
 template <int PASS>
 struct DistillShape {
     static constexpr bool loss_alone = PASS == CCL_PASS_FORWARD;
@@ -948,7 +956,8 @@ static cudaError_t distill_held(const Launch &L, const DistillLaunch &N, LaunchI
     // Pieces: few enough groups that a stage holds one, in a cluster of the
     // portable eight CTAs where that will do and of sixteen where not (a
     // gradient alone needs no cluster, so any number); then, with fewer CTAs
-    // than two per SM, more and smaller pieces, for latency.
+    // than two per SM, more and smaller pieces, for latency (8 x 32000 f32:
+    // 3.9 us, else 4.2).
     using Shape = DistillShape<PASS>;
     a.segments = (p + Shape::cluster - 1) / Shape::cluster;
     a.parts = 1;
