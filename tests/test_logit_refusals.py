@@ -23,7 +23,9 @@ A = 1 << 20                        # distance between the buffers' made-up addre
 @pytest.fixture(scope="module")
 def front(tmp_path_factory):
     so = str(tmp_path_factory.mktemp("logit_checks") / "driver.so")
-    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Wextra", "-Werror", "-shared", "-fPIC", "-I", os.path.join(ROOT, "include"), "-I", CUDA,
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Wextra", "-Werror", "-shared", "-fPIC",
+                    "-Wl,-Bsymbolic",      # the driver's own fakes, whatever CUDA runtime the process has loaded
+                    "-I", os.path.join(ROOT, "include"), "-I", CUDA,
                     os.path.join(ROOT, "tests", "logit_checks", "driver.cpp"), "-o", so], check=True)
     L = ctypes.CDLL(so)
     real = ccl._lib
