@@ -372,10 +372,11 @@ __global__ void __launch_bounds__(kBalanceThreads, NV * Traits<T>::VEC > 16 ? 2 
 // brings the groups that hold them into shared memory asynchronously, STAGES
 // - 1 steps ahead, and its lanes read their elements l, l + L, ... from there;
 // the gradient goes back the same way, whole groups and a few edge elements.
-// Bound by instructions, element by element: 8 x 60000 x 60 bf16 61 us, 8 x
-// 20000 x 203 68, 8 x 400000 x 9 77 (a warp per row without the stages: 152,
-// 87, 721).  Where the rows are aligned groups balance_kernel is the faster:
-// 8 x 65536 x 64 bf16 35 against 85 us, 8 x 32768 x 128 f32 55 against 74.
+// Bound by instructions, element by element: 8 x 60000 x 60 bf16 50 us, 8 x
+// 20000 x 203 55, 8 x 400000 x 9 70, 8 x 6000 x 700 51 (a warp per row without
+// the stages: 152, 87, 721, 71); with four CTAs per SM, not three: 51, 59, 70.
+// Where the rows are aligned groups balance_kernel is the faster: 8 x 65536 x
+// 64 bf16 35 against 80 us, 8 x 32768 x 128 f32 55 against 64.
 template <int NE>
 constexpr int kOddStages = NE > 16 ? 2 : 3;
 template <int NE>
@@ -449,10 +450,12 @@ __global__ void __launch_bounds__(kBalanceThreads, kOddCtas<NE>) balance_odd_ker
             unsigned char *to = in_s + stage * span;
             const uint32_t n = uint32_t(b1 - lo), to32 = smem_addr(to);
             if (lo >= in && lo + (n + 15) / 16 * 16 <= in_end) {
+#pragma unroll 1
                 for (uint32_t g = lane * 16; g < n; g += 512)
                     if (in_bounds(g + 16 <= span, a.status, kSiteBalance, row))
                         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to32 + g), "l"(lo + g) : "memory");
             } else {      // the first or last group of the buffer is not all of it
+#pragma unroll 1
                 for (uint32_t g = lane * S; g < n; g += 32 * S)
                     if (lo + g >= in && in_bounds(g + S <= span, a.status, kSiteBalance, row))
                         Tr::store1(to + g, 0, Tr::load1(reinterpret_cast<const void *>(lo + g), 0));
@@ -476,6 +479,8 @@ __global__ void __launch_bounds__(kBalanceThreads, kOddCtas<NE>) balance_odd_ker
     const float up = bwd && a.dloss ? *a.dloss : 1.0f;
     float lean_sum = 0.0f;
     int live = 0;
+    // pair i is nobody's; L is the smallest that holds a row, so only the upper half can be
+    auto beyond = [&](int i) { return (L == 1 || i >= PAIRS / 2) && 2 * i * L >= int(E); };
     uint32_t stage = 0;
     for (; t < a.rows; t += stride) {
         asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
@@ -491,11 +496,11 @@ __global__ void __launch_bounds__(kBalanceThreads, kOddCtas<NE>) balance_odd_ker
         each<PAIRS>([&](auto I) {
             constexpr int i = decltype(I)::value;
             x[i] = {-INFINITY, -INFINITY};
-            if (2 * i * L >= E) return;          // the whole warp
+            if (beyond(i)) return;
             // reads past the row, up to 2 L elements, are of shared memory all the same
             const float v0 = lds_element<T, 2 * i * L * S>(from), v1 = lds_element<T, (2 * i + 1) * L * S>(from);
             x[i] = {v0, v1};
-            if ((2 * i + 2) * L > E) {
+            if ((L == 1 || i >= PAIRS / 2 - 1) && (2 * i + 2) * L > E) {
                 if (2 * i * L + l >= E) x[i].x = -INFINITY;
                 if ((2 * i + 1) * L + l >= E) x[i].y = -INFINITY;
             }
@@ -506,12 +511,18 @@ __global__ void __launch_bounds__(kBalanceThreads, kOddCtas<NE>) balance_odd_ker
         m = finite_max(m);
         Pair sum = {0.0f, 0.0f}, dot = {0.0f, 0.0f};
         const float mc = m * kLog2e;             // (as in balance_kernel)
-        const bool tame = __all_sync(0xffffffffu, fabsf(mc) < INFINITY);
+        if (__all_sync(0xffffffffu, fabsf(mc) < INFINITY)) {
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i)
+                if (!beyond(i)) x[i] = ex2(fma(x[i], Pair{kLog2e, kLog2e}, Pair{-mc, -mc}));
+        } else {
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i)
+                if (!beyond(i)) x[i] = ex2((x[i] + Pair{-m, -m}) * Pair{kLog2e, kLog2e});
+        }
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) {
-            if (2 * i * L >= E) continue;
-            if (tame) x[i] = ex2(fma(x[i], Pair{kLog2e, kLog2e}, Pair{-mc, -mc}));
-            else x[i] = ex2((x[i] + Pair{-m, -m}) * Pair{kLog2e, kLog2e});
+            if (beyond(i)) continue;
             sum = sum + x[i];
             dot = fma(x[i], d[i], dot);
         }
@@ -533,8 +544,8 @@ __global__ void __launch_bounds__(kBalanceThreads, kOddCtas<NE>) balance_odd_ker
             const uint32_t to = smem_addr(out_s) + uint32_t(o0 % 16) + mine * row_bytes + l * S;
             each<PAIRS>([&](auto I) {
                 constexpr int i = decltype(I)::value;
-                if (2 * i * L >= E) return;
-                const bool full = (2 * i + 2) * L <= E;
+                if (beyond(i)) return;
+                const bool full = (L > 1 && i < PAIRS / 2 - 1) || (2 * i + 2) * L <= E;
                 sts_pair<T, 2 * i * L * S, (2 * i + 1) * L * S>(to, (x[i] * (d[i] + off)) * g, full || 2 * i * L + l < E,
                                                                full || (2 * i + 1) * L + l < E);
             });
@@ -543,6 +554,7 @@ __global__ void __launch_bounds__(kBalanceThreads, kOddCtas<NE>) balance_odd_ker
             const uintptr_t first = (o0 + 15) & ~uintptr_t(15), last = o1 & ~uintptr_t(15), head = min(first, o1), tail = max(last, head);
             if (!in_bounds(o1 - low <= span, a.status, kSiteBalance, t)) continue;
             const uint32_t skip = uint32_t(first - low), whole = last > first ? uint32_t(last - first) : 0u, out32 = smem_addr(out_s) + skip;
+#pragma unroll 1
             for (uint32_t g = lane * 16; g < whole; g += 512) st_stream_v4(reinterpret_cast<void *>(first + g), lds_v4(out32 + g));
             const uintptr_t edge = lane < 8 ? o0 + lane * S : tail + (lane - 8) * S;     // at most seven before, and seven after
             if (lane < 16 && edge < (lane < 8 ? head : o1))
