@@ -258,3 +258,47 @@ def test_same_bits_again_on_another_stream_and_in_a_graph(rows):
     graph.replay()
     assert all(torch.equal(a, b) for a, b in zip(result(), want))
     ranks.finish()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("E", [1, 3, 9, 15, 17, 31, 45, 100, 127, 130, 255, 259, 500, 511, 513, 700, 1023])
+@pytest.mark.parametrize("layout", [dict(), dict(in_place=True, offset=1), dict(offset=[0, 1, 2], out_offset=3)])
+def test_rows_that_are_no_aligned_groups(dtype, E, layout):
+    g = rng(E)
+    rows = 37 if E > 100 else 211
+    xs = [g.normal(0, 2, (rows, E)) for _ in range(3)]
+    valid = padding(rows, 3, E)
+    for x, v in zip(xs, valid):
+        x[v == 0] = np.nan
+    check(xs, choices(rows, E, min(E, 3), 3, E), dtype, "both", valid, **layout)
+
+
+@pytest.mark.parametrize("E,offset", [(64, 0), (61, 0), (64, 1)])
+def test_offsets_beyond_32_bits(E, offset):
+    rows, some = 2 ** 32 // E + 77, 5
+    g = rng(E)
+    tail = torch.from_numpy(g.normal(0, 2, (some, E))).cuda().bfloat16()
+    x = torch.zeros(rows * E + offset, dtype=torch.bfloat16, device="cuda")
+    x[-some * E:] = tail.view(-1)
+    y = torch.full((rows * E + offset,), 7.0, dtype=torch.bfloat16, device="cuda")
+    size = x.element_size() * offset
+    counts, tokens = torch.from_numpy(g.integers(0, 1000, E).astype(np.int32)).cuda(), torch.tensor([1000], dtype=torch.int32, device="cuda")
+    up = torch.tensor([4096.0], device="cuda")
+    comm = ccl.ccl_comm_create(1, [x.data_ptr() + size])
+    ccl.ccl_comm_set_outputs(comm, [y.data_ptr() + size])
+    ccl.ccl_balance_loss(comm, "bf16", "backward", rows, E, 2, None, None, 1.0, up.data_ptr(), counts.data_ptr(),
+                         tokens.data_ptr(), 0, stream=stream())
+    ccl.ccl_comm_check(comm)
+    ccl.ccl_comm_destroy(comm)
+    c = counts.double().cpu()
+    d = (c - c.mean()) * E / (2 * 1000.0 ** 2)
+    z = torch.cat([torch.zeros(1, E), tail.double().cpu()])
+    prob = z.softmax(1)
+    want = 4096.0 * prob * (d - (prob * d).sum(1, keepdim=True))
+    R = z.max(1, keepdim=True).values - z.min(1, keepdim=True).values
+    tol = 4096.0 * prob * d.abs().max() * (3 * (6 * R + 80) + 160) * U32
+    tol = tol + HALF_STEP["bf16"] * (want.abs() + tol) + FLOOR["bf16"]
+    got = y[offset:].view(rows, E)
+    assert_within(got[-some:], want[1:], tol[1:], "the last rows")
+    for r in (0, 2 ** 31 // E, 2 ** 31 // E + 1, rows // 2, rows - some - 1):
+        assert_within(got[r], want[0], tol[0], f"row {r}")

@@ -282,3 +282,28 @@ def test_another_stream_and_a_graph():
     torch.cuda.synchronize()
     assert all(torch.equal(b.view.view(torch.int16), w.view(torch.int16)) for b, w in zip(ranks.outs, want))
     ranks.finish()
+
+
+def test_offsets_beyond_32_bits():
+    vocab, rows = 32768, 2 ** 32 // 32768 + 5
+    x = torch.zeros(rows, vocab, dtype=torch.bfloat16, device="cuda")
+    y = torch.full((rows, vocab), 7.0, dtype=torch.bfloat16, device="cuda")
+    history = torch.full((rows, 1), 5, dtype=torch.int32, device="cuda")
+    history[-1, 0] = vocab - 1
+    presence = torch.full((rows,), 0.5, device="cuda")
+    mask = torch.full((1, vocab // 32), -1, dtype=torch.int32, device="cuda")
+    mask[0, -1] = ~(1 << 30)
+    index = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    rules = ccl.LogitRules(presence=presence.data_ptr(), history=history.data_ptr(), history_ld=1, mask=mask.data_ptr(), mask_rows=1,
+                           mask_ld=vocab // 32, mask_index=index.data_ptr())
+    want = torch.zeros(rows, vocab, dtype=torch.bfloat16, device="cuda")
+    want[:, 5] = -0.5
+    want[-1, 5], want[-1, -1] = 0.0, -0.5
+    want[:, vocab - 2] = -float("inf")
+    for out in (y, x):                      # out of place, then in place
+        comm = ccl.ccl_comm_create(1, [x.data_ptr()])
+        ccl.ccl_comm_set_outputs(comm, [out.data_ptr()])
+        ccl.ccl_logit_rules(comm, "bf16", rows, vocab, rules, stream=stream())
+        ccl.ccl_comm_check(comm)
+        ccl.ccl_comm_destroy(comm)
+        assert torch.equal(out, want)
