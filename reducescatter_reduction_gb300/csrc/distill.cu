@@ -7,7 +7,8 @@
 //   dz_v = w T (p_v - sum over the k with id_k = v of q_k)
 //
 // A row is cut into Q pieces, each a part of one rank's shard or several
-// whole shards (small ones, and beyond 16 ranks), and a persistent CTA takes one piece of one
+// whole shards (small ones, and beyond 16 ranks; for the loss alone also parts
+// of neighbours), and a persistent CTA takes one piece of one
 // row after another.  Where the loss is computed the Q CTAs of a row form a
 // cluster and go through the rows together.  Ten or eleven warps, tied
 // together by mbarriers alone:
@@ -108,11 +109,13 @@ struct DistillArgs {
     uint32_t share;       // the entries of a piece for the loss alone: those of all pieces make a row's
     uint32_t pieces;      // per row
     uint32_t parts;       // parts of a shard (one shard a piece), else 1
-    uint32_t segments;    // shards of a piece
+    uint32_t segments;    // shards of a piece, at most
+    uint32_t span;        // the loss alone, if not 0: a piece's groups, counted as if every shard had `groups`
+    uint32_t groups;      // of the widest shard
     uint32_t chunks;      // of a piece
     uint32_t stages;
     uint32_t items;       // rows * pieces
-    FastDiv by_pieces, by_parts, by_segments;
+    FastDiv by_pieces, by_parts, by_segments, by_groups;
     int teacher_dtype;
     int edges;            // some row begins or ends between 16-byte boundaries
     long long wait_ns;
@@ -244,29 +247,48 @@ __device__ __forceinline__ bool wait_sums(const DistillArgs<PM> &a, DistillShare
     return __all_sync(0xffffffffu, distill_wait(a, sh, &sh.sums_in[k % kDistillSlots], (k / kDistillSlots) & 1, code, item));
 }
 
-// The part of shard `rank` that piece q of a row takes.
-template <typename T, int PM>
+// What piece q of a row takes of shard `rank`, its segment seg (rank >= p: there is none).
+template <typename T, int PM, int PASS>
 struct Piece {
-    uint32_t rank, part;
-    uint32_t per;          // groups of a part
+    uint32_t rank;
+    uint32_t lo, hi;       // of several shards: its groups of this one
+    uint32_t part;         // of one shard
+    bool head, tail;       // the shard's first and last columns are of this piece
     uint32_t j0, j1;       // its groups
 
     __device__ __forceinline__ Piece(const DistillArgs<PM> &a, uint32_t q, uint32_t seg)
     {
+        part = lo = 0;
+        hi = 0xffffffffu;
+        head = tail = true;
         if (a.segments == 1) {
             rank = div_by(q, a.by_parts);
             part = q - rank * a.parts;
-        } else {
+            head = part == 0;
+            tail = part + 1 == a.parts;
+        } else if (PASS != CCL_PASS_FORWARD || !a.span) {
             rank = q * a.segments + seg;
-            part = 0;
+        } else {
+            const uint32_t from = q * a.span, first = div_by(from, a.by_groups);
+            rank = first + seg;
+            lo = seg ? 0u : from - first * a.groups;
+            const uint32_t begin = rank * a.groups, end = from + a.span;
+            if (end <= begin) rank = a.s.p;
+            hi = min(a.groups, end - begin);
+            head = lo == 0;
+            tail = hi == a.groups;
         }
     }
     __device__ __forceinline__ void cut(const DistillArgs<PM> &a, const ShardRow<T> &row)
     {
         const uint32_t whole = row.end - row.first;
-        per = div_by(whole + a.parts - 1, a.by_parts);
-        j0 = row.first + min(whole, per * part);
-        j1 = row.first + min(whole, per * (part + 1));
+        if (a.segments == 1) {
+            const uint32_t per = div_by(whole + a.parts - 1, a.by_parts);
+            lo = per * part;
+            hi = per * (part + 1);
+        }
+        j0 = row.first + min(whole, lo);
+        j1 = row.first + min(whole, hi);
     }
 };
 
@@ -379,12 +401,12 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
         // edge element e of the pieces of a load, as ShardRow::edge numbers them; a lane's first comes in ahead of its load
         auto edge_of = [&](uint32_t of, uint32_t part, uint32_t e, float &z, uint64_t &to) {
             const uint32_t row = div_by(of, a.by_pieces), c = part % a.chunks;
-            Piece<T, PM> pe(a, of - row * a.pieces, e / (2 * VEC));
+            Piece<T, PM, PASS> pe(a, of - row * a.pieces, e / (2 * VEC));
             z = -INFINITY;
             to = 0;
             if (pe.rank >= s.p || !in_bounds(row < s.rows, s.status, kSiteDistill, row)) return;
             const ShardRow<T> in(s.in[pe.rank], s.ld, row, shard_width(s, pe.rank));
-            const int col = in.edge(e % (2 * VEC), pe.part == 0 && c == 0, pe.part + 1 == a.parts && c + 1 == a.chunks);
+            const int col = in.edge(e % (2 * VEC), pe.head && c == 0, pe.tail && c + 1 == a.chunks);
             if (col < 0) return;
             z = in.column(col);
             if (BWD) {
@@ -403,11 +425,11 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
             if (issued >= S && !__all_sync(0xffffffffu, distill_wait(a, sh, &sh.empty[st], (issued / S - 1) & 1, 6, item))) return false;
             DistillDesc<PASS> &d = sh.desc[issued % (S + 1)];
             const uint32_t row = div_by(item, a.by_pieces), q = item - row * a.pieces, c = load % a.chunks;
-            const uint32_t cap = a.segments == 1 ? kDistillStage : div_by(kDistillStage, a.by_segments);
+            const uint32_t cap = a.segments == 1 || (PASS == CCL_PASS_FORWARD && a.span) ? kDistillStage : div_by(kDistillStage, a.by_segments);
             // lane l: segment l
             uint32_t n = 0;
             const void *from = nullptr;
-            Piece<T, PM> pc(a, q, lane);
+            Piece<T, PM, PASS> pc(a, q, lane);
             if (lane < int(a.segments) && pc.rank < s.p) {
                 const ShardRow<T> in(s.in[pc.rank], s.ld, row, shard_width(s, pc.rank));
                 pc.cut(a, in);
@@ -539,11 +561,11 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
                 h.from = 0;
                 h.count = s.vocab;
             } else if (a.segments == 1) {
-                Piece<T, PM> pc(a, q, 0);
+                Piece<T, PM, PASS> pc(a, q, 0);
                 const ShardRow<T> in(s.in[pc.rank], s.ld, h.row, shard_width(s, pc.rank));
                 pc.cut(a, in);
-                const uint32_t lo = pc.part == 0 ? 0u : in.head() + (pc.j0 - in.first) * VEC;
-                const uint32_t hi = pc.part + 1 == a.parts ? in.width : in.head() + (pc.j1 - in.first) * VEC;
+                const uint32_t lo = pc.head ? 0u : in.head() + (pc.j0 - in.first) * VEC;
+                const uint32_t hi = pc.tail ? in.width : in.head() + (pc.j1 - in.first) * VEC;
                 h.from = shard_begin(s, pc.rank) + lo;
                 h.count = hi - lo;
                 h.at = in.base + uint64_t(in.shift + lo) * ES;
@@ -979,11 +1001,33 @@ static cudaError_t distill_held(const Launch &L, const DistillLaunch &N, LaunchI
     a.pieces = a.segments == 1 ? p * a.parts : (p + a.segments - 1) / a.segments;
     a.chunks = (per_part(a.parts) + cap - 1) / cap;
     if (a.chunks < 1) a.chunks = 1;
+    a.span = 0;
+    a.groups = groups;
+    // The loss alone: fewer pieces that go over the shards' bounds (2048 x
+    // 80768 bf16 on 8 ranks, five for eight: 69 us, 109; with the gradient,
+    // whose stores then have to look for their shard, 212 and 180).
+    const uint64_t total = uint64_t(groups) * p;
+    for (uint64_t pieces = (total + kDistillStage - 1) / kDistillStage; Shape::loss_alone && groups && pieces < a.pieces; ++pieces) {
+        if (pieces > Shape::cluster || N.rows * pieces < 2 * uint64_t(L.num_sms)) continue;
+        const uint64_t span = (total + pieces - 1) / pieces;
+        uint64_t most = 1;      // shards that a piece touches
+        for (uint64_t at = 0; at < total; at += span) {
+            const uint64_t end = at + span < total ? at + span : total, touched = (end - 1) / groups - at / groups + 1;
+            if (touched > most) most = touched;
+        }
+        if (most < 2 || most > Shape::segments) continue;
+        a.segments = uint32_t(most);
+        a.parts = a.chunks = 1;
+        a.pieces = uint32_t(pieces);
+        a.span = uint32_t(span);
+        break;
+    }
     if (N.rows * a.pieces > 0x7fffffffull) return cudaErrorInvalidValue;
     a.items = uint32_t(N.rows * a.pieces);
     a.by_pieces = fast_div(a.pieces);
     a.by_parts = fast_div(a.parts);
     a.by_segments = fast_div(a.segments);
+    a.by_groups = fast_div(groups ? groups : 1);
     a.share = (a.k + a.pieces - 1) / a.pieces;
     const uint32_t in_registers = 32 * HELD, share = Shape::loss_alone ? a.share : a.k;
     const size_t entries = size_t(a.kpad) * ((Shape::loss_alone ? 0 : 24) + (share > in_registers ? 12 * kDistillTeachers<HELD> : 0));

@@ -322,3 +322,18 @@ def test_no_rows():
     one = torch.zeros(8, device="cuda")
     ccl.ccl_distill_topk(ranks.comm, "f32", "both", 0, 8, 2, one.data_ptr(), one[4:].data_ptr(), loss=one[6:].data_ptr(), stream=stream())
     ranks.finish(wrote=False)
+
+
+@pytest.mark.parametrize("p,rows,vocab,dtype,layout", [
+    (3, 330, 5003, "bf16", {}), (8, 310, 8000, "f16", {}), (8, 160, 32000, "bf16", dict(in_place=True)), (5, 400, 1003, "f32", {}),
+    (7, 320, 61, "bf16", {}), (4, 310, 9001, "f32", dict(offset=[0, 3, 1, 2])), (3, 60, 100003, "bf16", {}),
+    (8, 70, 80725, "bf16", dict(offset=3, out_offset=1)), (8, 75, 80725, "bf16", dict(in_place=True)),
+    (6, 320, 2047, "f16", dict(ld=400, in_place=True)), (2, 320, 20, "f32", {}), (12, 80, 40009, "f32", {}), (20, 330, 1201, "bf16", {})])
+@pytest.mark.parametrize("steps", ["both", "forward", "each"])
+def test_pieces_over_several_shards(p, rows, vocab, dtype, layout, steps):
+    """Rows enough for every SM: then a piece may end inside one shard and go on in the next."""
+    g = rng(rows * p)
+    ids, t = teacher(rows, vocab, min(40, vocab), 8)
+    edge = np.cumsum([0] + [vocab // p + (r < vocab % p) for r in range(p)])
+    ids[1::3, 0], ids[2::3, 1] = edge[1] - 1, edge[1] % vocab      # on both sides of a bound
+    check(g.normal(0, 3, (rows, vocab)), ids, t, 1.5, p, dtype, steps, weight=g.normal(0, 1, rows), **layout)
