@@ -251,8 +251,8 @@ struct NormLaunch {
 };
 cudaError_t launch_allreduce_rmsnorm(const Launch &L, const NormLaunch &N, LaunchInfo *info);
 
-// The logit operators (logit_rules.cu, distill.cu, balance.cu).  L.alias: the
-// outputs are the inputs.
+// The logit operators (logit_rules.cu, distill.cu, balance.cu).  L.alias:
+// every rank's output is its input.
 struct RulesLaunch {
     uint64_t rows = 0;
     uint32_t vocab = 0;

@@ -20,14 +20,14 @@
 // the listed columns are done in shared memory, each by a lane of its own (in
 // the groups' own lanes the rules cost more than the copy: a history of
 // thousands of tokens touches few columns, but nearly every group of 32 lanes
-// has one), and the groups go out through their mask bits.  In place nothing
-// is staged: only groups that the mask changes are read and written, and the
-// listed columns in memory.  Counters are 16 bits wide where the history is
-// shorter than 2^14 tokens.  Bytes: the logits once in and once out, the
-// history once per slice (L2).  Bound by launch and latency where there are
-// few (1 x 32000 f32: 4.7 us), else by the counting of the history: 512 x
-// 131072 bf16 take 100 us (2.8 TB/s) with histories of up to 8192 tokens, 52
-// without, of which copy and mask alone are 46 (5.8 TB/s).
+// has one), and the groups go out through their mask bits.  Where every rank
+// is in place nothing is staged: only groups that the mask changes are read
+// and written, and the listed columns in memory.  Counters are 16 bits wide
+// where the history is shorter than 2^14 tokens.  Bytes: the logits once in
+// and once out, the history once per slice (L2).  Bound by launch and latency
+// where there are few (1 x 32000 f32: 4.7 us), else by the counting of the
+// history: 512 x 131072 bf16 take 100 us (2.8 TB/s) with histories of up to
+// 8192 tokens, 52 without, of which copy and mask alone are 46 (5.8 TB/s).
 #include "async.cuh"
 #include "logits.cuh"
 
@@ -39,7 +39,7 @@ struct RulesArgs {
     ccl_logit_rules_t r;
     uint32_t slices;            // per rank
     FastDiv by_row, by_slices;  // CTAs per row, slices per rank
-    int in_place;
+    int in_place;               // every rank's output is its input
 };
 
 // A column's counter: bit 0 says "in the prompt", the top bit "has a bias

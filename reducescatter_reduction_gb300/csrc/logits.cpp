@@ -41,14 +41,16 @@ static ccl_status_t check_aligned(const void *p, size_t to, const char *name)
 // Rank buffers of extent[r] bytes: aligned to their elements; where the call
 // writes the outputs, each is its own rank's input or disjoint from every
 // input and every other output.  What the call writes beside them overlaps
-// nothing, and nothing it reads overlaps an output.  *alias: an output is an
-// input.
+// nothing, and nothing it reads overlaps an output.  *alias: every output that
+// has elements is its rank's input; where that holds for some ranks alone, a
+// kernel has to write all of each output.
 static ccl_status_t check_buffers(const ccl_comm *c, const uint64_t *extent, size_t es, bool outputs, const Aux *aux, int n_aux,
                                   bool *alias)
 {
     const int p = c->p;
-    *alias = false;
+    *alias = outputs;
     for (int r = 0; r < p; ++r) {
+        if (extent[r] && c->out[r] != c->in[r]) *alias = false;
         if (uintptr_t(c->in[r]) % es || (outputs && uintptr_t(c->out[r]) % es))
             return fail(CCL_ERR_INVALID_ARG, "a buffer of rank %d is not aligned to its elements (%zu bytes)", r, es);
     }
@@ -60,7 +62,6 @@ static ccl_status_t check_buffers(const ccl_comm *c, const uint64_t *extent, siz
             if (!overlap(out, range_of(c->in[j], extent[j]))) continue;
             if (j != k || c->out[k] != c->in[k])
                 return fail(CCL_ERR_INVALID_ARG, "output of rank %d overlaps the input of rank %d", k, j);
-            *alias = true;
         }
     }
     for (int i = 0; i < n_aux; ++i) {
