@@ -28,6 +28,12 @@ constexpr int kCountThreads = 1024;
 // one by one, the second launch costs the host about 3 us more.
 constexpr uint64_t kCountHereIds = 8192;
 constexpr uint64_t kCountHereCells = 4096;
+// A row's exponentials are 2^(x c - m c) in one step up to this |m c|, with m
+// its maximum and c = log2(e): the rounding of m c, at most 2^-5 there, is a
+// factor of at most 1.022 that all of the row has and that divides out.
+// Beyond, the difference x - m comes first: the rounding grows with m, and
+// from some 10^9 on its power of two would be 0 or infinite.
+constexpr float kOneStep = 1048576.0f;
 
 template <int PM>
 struct BalanceArgs {
@@ -320,10 +326,8 @@ __global__ void __launch_bounds__(kBalanceThreads, NV * Traits<T>::VEC > 16 ? 2 
         for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         m = finite_max(m);
         Pair x[NV * PAIRS], sum = {0.0f, 0.0f}, dot = {0.0f, 0.0f};
-        // 2^(x c - m c) in one step: the rounding of m c is the same for the whole row and divides out.  Where m c
-        // leaves fp32's range (a row of the type's lowest value), the difference comes first.
         const float mc = m * kLog2e;
-        if (__all_sync(0xffffffffu, fabsf(mc) < INFINITY)) {
+        if (__all_sync(0xffffffffu, fabsf(mc) < kOneStep)) {
 #pragma unroll
             for (int n = 0; n < NV; ++n)
 #pragma unroll
@@ -511,7 +515,7 @@ __global__ void __launch_bounds__(kBalanceThreads, kOddCtas<NE>) balance_odd_ker
         m = finite_max(m);
         Pair sum = {0.0f, 0.0f}, dot = {0.0f, 0.0f};
         const float mc = m * kLog2e;             // (as in balance_kernel)
-        if (__all_sync(0xffffffffu, fabsf(mc) < INFINITY)) {
+        if (__all_sync(0xffffffffu, fabsf(mc) < kOneStep)) {
 #pragma unroll
             for (int i = 0; i < PAIRS; ++i)
                 if (!beyond(i)) x[i] = ex2(fma(x[i], Pair{kLog2e, kLog2e}, Pair{-mc, -mc}));

@@ -1,0 +1,35 @@
+"""GPU tests of ccl_balance_loss at the ends of its ranges: logits of large
+magnitude, no rows."""
+import numpy as np
+import pytest
+import torch
+
+from ccl_testutil import ensure_built
+from logit_testutil import rng
+from test_balance import check, choices
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    ensure_built()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("E", [8, 32, 33, 600, 700, 1500])
+@pytest.mark.parametrize("steps", ["both", "forward", "each"])
+def test_logits_of_large_magnitude(dtype, E, steps):
+    """Rows that are one large value throughout (all experts masked with a finite number) have a uniform softmax, rows
+    that are it in part have none there, and rows far from zero are what their differences make of them."""
+    g = rng(E)
+    values = [v * s for v in (1e5, 1e6, 2e7, 1e9, 3e9, 1e10, 1e20, 1e30, 1e38, 3e38) for s in (1, -1)]
+    x = g.normal(0, 2, (4 * len(values), E))
+    for i, v in enumerate(values):
+        x[4 * i] = v                                        # throughout
+        x[4 * i + 1, ::3] = -abs(v)                         # masked in part
+        x[4 * i + 2] += v                                   # far from zero: the type keeps what it keeps of it
+        x[4 * i + 3] = v * (1 - 0.5 * g.random(E))          # differences as large as the values
+    check([x, x[::-1].copy()], choices(len(x), E, 3, 2, 8), dtype, steps)
