@@ -114,7 +114,7 @@ __device__ __forceinline__ float balance_coefficients(const BalanceArgs<PM> &a, 
         for (uint32_t i = threadIdx.x; i < a.p * E + a.p; i += kBalanceThreads) hist[i] = 0;
         __syncthreads();
         constexpr int BATCH = 8;
-        const uint32_t n = a.by_choices.d, all = a.p * n, rows = uint32_t(a.rows);
+        const uint32_t rows = uint32_t(a.rows), n = rows * a.k, all = a.p * n;
         for (uint32_t i = threadIdx.x; i < all; i += BATCH * kBalanceThreads) {
             int id[BATCH];
             uint32_t rank[BATCH];
