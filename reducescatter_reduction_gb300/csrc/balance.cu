@@ -681,28 +681,6 @@ static cudaError_t balance_shape(const Launch &L, const BalanceLaunch &N, Launch
     a.status = L.status;
     cudaError_t err = cudaSuccess;
     info->kernels = 0;
-    if (fwd && !a.count_here) {
-        // the scratch counters are zero already: the call that used them last left them so
-        if (!scratch) err = cudaMemsetAsync(N.counts, 0, cells * 4, L.stream);
-        if (!scratch && err == cudaSuccess) err = cudaMemsetAsync(N.tokens, 0, size_t(L.p) * 4, L.stream);
-        if (err != cudaSuccess) return err;
-        // one CTA per SM: every CTA ends with an atomic per expert it met
-        const uint64_t want = (N.rows * N.k + kCountThreads - 1) / kCountThreads;
-        const uint64_t most = uint64_t(L.num_sms) / uint64_t(L.p) + 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(unsigned(want < 1 ? 1 : want < most ? want : most), unsigned(L.p));
-        cfg.blockDim = dim3(kCountThreads);
-        cfg.dynamicSmemBytes = size_t(N.experts) * 4;
-        cfg.stream = L.stream;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        err = cudaLaunchKernelEx(&cfg, balance_count_kernel<PM>, a);
-        if (err != cudaSuccess) return err;
-        ++info->kernels;
-    }
     void (*kern)(BalanceArgs<PM>) = balance_any_kernel<T, PM>;
     int lanes = 32, per_sm = 6;      // CTAs that an SM holds at once: the kernels' launch bounds; this one's registers
     size_t smem = size_t(N.experts) * 4 + (a.count_here ? size_t(cells + L.p) * 4 : 0);
@@ -738,6 +716,28 @@ static cudaError_t balance_shape(const Launch &L, const BalanceLaunch &N, Launch
             else kern = balance_kernel<T, PM, 32, 2 * NV>;
         }
     }
+    if (fwd && !a.count_here) {
+        // the scratch counters are zero already: the call that used them last left them so
+        if (!scratch) err = cudaMemsetAsync(N.counts, 0, cells * 4, L.stream);
+        if (!scratch && err == cudaSuccess) err = cudaMemsetAsync(N.tokens, 0, size_t(L.p) * 4, L.stream);
+        if (err != cudaSuccess) return err;
+        // one CTA per SM: every CTA ends with an atomic per expert it met
+        const uint64_t want = (N.rows * N.k + kCountThreads - 1) / kCountThreads;
+        const uint64_t most = uint64_t(L.num_sms) / uint64_t(L.p) + 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(unsigned(want < 1 ? 1 : want < most ? want : most), unsigned(L.p));
+        cfg.blockDim = dim3(kCountThreads);
+        cfg.dynamicSmemBytes = size_t(N.experts) * 4;
+        cfg.stream = L.stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        err = cudaLaunchKernelEx(&cfg, balance_count_kernel<PM>, a);
+        if (err != cudaSuccess) return err;
+        ++info->kernels;
+    }
     const uint64_t rows_per_cta = uint64_t(kBalanceWarps) * (32 / lanes);
     const uint64_t want = (N.rows + rows_per_cta - 1) / rows_per_cta;
     const uint64_t all = uint64_t(per_sm) * L.num_sms < kMaxPartials ? uint64_t(per_sm) * L.num_sms : kMaxPartials, most = all / L.p;
@@ -752,7 +752,11 @@ static cudaError_t balance_shape(const Launch &L, const BalanceLaunch &N, Launch
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     err = cudaLaunchKernelEx(&cfg, kern, a);
-    if (err != cudaSuccess) return err;
+    if (err != cudaSuccess) {
+        // what the counting kernel leaves in the scratch is cleared behind it: the next call finds it at zero
+        if (scratch && !a.count_here) cudaMemsetAsync(a.cells, 0, size_t(kScratchCells + kMaxRanks) * 4, L.stream);
+        return err;
+    }
     info->kernel = "balance_loss";
     info->grid = int(cfg.gridDim.x * cfg.gridDim.y);
     info->block = kBalanceThreads;
