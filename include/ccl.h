@@ -407,9 +407,9 @@ typedef enum { CCL_PASS_FORWARD = 1, CCL_PASS_BACKWARD = 2, CCL_PASS_BOTH = 3 } 
  * FORWARD and BOTH exchange sums between CTAs: their waits are bounded by the
  * communicator's wait limit, and one that gives up makes ccl_comm_check()
  * return CCL_ERR_TIMEOUT (the outputs are then incomplete).
- * Errors: CCL_ERR_INVALID_ARG (a size, pass or temperature out of range, a
- * missing array, overlap), CCL_ERR_UNSUPPORTED (int32, k > 1024),
- * CCL_ERR_CUDA. */
+ * Errors: CCL_ERR_INVALID_ARG (a size, pass or temperature out of range --
+ * temperatures are from 4.25e-39 to 3e38 --, a missing array, overlap),
+ * CCL_ERR_UNSUPPORTED (int32, k > 1024), CCL_ERR_CUDA. */
 CCL_API ccl_status_t ccl_distill_topk(ccl_comm_t comm, ccl_dtype_t dtype, ccl_pass_t pass, size_t rows, size_t vocab,
                                       size_t ld, size_t k, const int32_t *teacher_ids, const void *teacher_logits,
                                       ccl_dtype_t teacher_dtype, float temperature, const float *row_weight,

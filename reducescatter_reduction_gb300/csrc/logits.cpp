@@ -192,6 +192,8 @@ extern "C" ccl_status_t ccl_distill_topk(ccl_comm_t c, ccl_dtype_t dtype, ccl_pa
     if (teacher_dtype < CCL_F32 || teacher_dtype > CCL_BF16)
         return fail(CCL_ERR_INVALID_ARG, "teacher_dtype %d is not a floating-point type", int(teacher_dtype));
     if (!(temperature > 0.0f) || temperature > 3.0e38f) return fail(CCL_ERR_INVALID_ARG, "temperature must be finite and > 0");
+    if (temperature < 4.25e-39f)     // log2(e) / temperature would not be finite, and 0 times it not 0
+        return fail(CCL_ERR_INVALID_ARG, "temperature %g below 4.25e-39: its reciprocal leaves fp32's range", double(temperature));
     if (k == 0) return fail(CCL_ERR_INVALID_ARG, "k must be positive");
     if (k > 1024) return fail(CCL_ERR_UNSUPPORTED, "k=%zu above 1024 teacher entries a row", k);
     uint64_t extent[kMaxRanks];
