@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
             float loss = 0.0f;
             if (tsum != 0.0f) {
                 if (total == 0.0f) loss = INFINITY;
-                else loss = heat * heat * ((u / tsum - logf(tsum)) - (dot / heat - ls));
+                else loss = heat * (heat * ((u / tsum - logf(tsum)) - (dot / heat - ls)));   // heat^2 may be out of range
             }
             a.loss[row] = loss;
             if (a.stats) {
