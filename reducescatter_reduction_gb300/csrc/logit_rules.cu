@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
     const int32_t *h = history ? a.r.history + row * a.r.history_ld : nullptr;
     int len = history && a.r.history_len ? a.r.history_len[row] : ld;
     const int prompt = history && a.r.prompt_len ? a.r.prompt_len[row] : 0;
-    int bias_lo = a.r.bias_count ? a.r.bias_offsets[row] : 0, bias_hi = a.r.bias_count ? a.r.bias_offsets[row + 1] : 0;
+    const int offset0 = a.r.bias_count ? a.r.bias_offsets[row] : 0, offset1 = a.r.bias_count ? a.r.bias_offsets[row + 1] : 0;
     int32_t token[BATCH];
 #pragma unroll
     for (int k = 0; k < BATCH; ++k) token[k] = tid + k * THREADS < ld ? h[tid + k * THREADS] : -1;
@@ -156,15 +156,13 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
         }
         if (edge >= 0) Tr::store1(stage, uint64_t(edge - cell0), in.column(edge));
     }
-    if (a.r.bias_count) {
-        const int n = int(a.r.bias_count);
-        bias_lo = bias_lo < 0 ? 0 : bias_lo > n ? n : bias_lo;
-        bias_hi = bias_hi < bias_lo ? bias_lo : bias_hi > n ? n : bias_hi;
-    }
+    // the row's entries [bias_lo, bias_hi), held to the list; unsigned, as a block that begins below 2^31 may end beyond
+    const uint32_t bias_lo = min(uint32_t(max(offset0, 0)), uint32_t(a.r.bias_count));
+    const uint32_t bias_hi = max(bias_lo, min(uint32_t(max(offset1, 0)), uint32_t(a.r.bias_count)));
     len = len < 0 ? 0 : len > ld ? ld : len;
     uint32_t bias_token = 0xffffffffu;     // of this thread's entry in a block of the list, from the slice's first
     float bias_add = 0.0f;
-    auto entry = [&](int k) {
+    auto entry = [&](uint32_t k) {
         bias_token = k < bias_hi ? uint32_t(a.r.bias_tokens[k]) - from : 0xffffffffu;
         bias_add = k < bias_hi ? a.r.bias_values[k] : 0.0f;
     };
@@ -219,7 +217,7 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
         }
     }
     uint32_t kept = 0;
-    for (int b = bias_lo; b < bias_hi; b += THREADS) {
+    for (uint32_t b = bias_lo; b < bias_hi; b += THREADS) {
         // the list's entries for the slice, in their order
         if (b > bias_lo) entry(b + tid);
         const bool is = b + tid < bias_hi && bias_token < width;
@@ -303,7 +301,7 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
                         for (uint32_t b = 0; b < kept; ++b)
                             if (bias_cell[b] == cell[k]) sum = __fadd_rn(sum, bias_value[b]);
                     } else {
-                        for (int b = bias_lo; b < bias_hi; ++b)
+                        for (uint32_t b = bias_lo; b < bias_hi; ++b)
                             if (uint32_t(a.r.bias_tokens[b]) - from + cell_from == cell[k]) sum = __fadd_rn(sum, a.r.bias_values[b]);
                     }
                     y = __fadd_rn(y, sum);

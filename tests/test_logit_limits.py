@@ -8,6 +8,7 @@ import reducescatter_reduction_gb300 as ccl
 from ccl_testutil import ensure_built
 from logit_testutil import rng
 from test_logit_refusals import BAD, OK, distill_call, front, status      # noqa: F401 (front: a fixture)
+from test_logit_rules import Rules, check
 
 
 @pytest.mark.cpu
@@ -48,3 +49,21 @@ def test_losses_at_temperatures_whose_square_underflows(gpu, steps, T):
     want = float(np.float32(T)) * d
     err = np.abs(loss.double().cpu().numpy() - want)
     assert (err <= 8 * 2.0 ** -24 * want + 2.0 ** -149).all(), (loss.tolist(), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("vocab", [1000, 300000])
+def test_bias_entries_at_the_end_of_the_longest_list(gpu, vocab):
+    """2^31 - 1 entries: the blocks that a row's last entries are read in end beyond 2^31."""
+    n, some, rows = 2 ** 31 - 1, 600, 4
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB of device memory")
+    g = rng(1)
+    tokens, values = (torch.empty(n, dtype=t, device="cuda") for t in (torch.int32, torch.float32))
+    h = {"bias_offsets": np.array([0, some, some, some, some], dtype=np.int32),
+         "bias_tokens": g.integers(0, vocab, some).astype(np.int32), "bias_values": g.normal(0, 2, some).astype(np.float32)}
+    tokens[-some:], values[-some:] = torch.from_numpy(h["bias_tokens"]).cuda(), torch.from_numpy(h["bias_values"]).cuda()
+    offsets = torch.tensor([n - some, n, n, n, n], dtype=torch.int32, device="cuda")
+    rules = Rules(**h)
+    rules.s = ccl.LogitRules(bias_offsets=offsets.data_ptr(), bias_tokens=tokens.data_ptr(), bias_values=values.data_ptr(), bias_count=n)
+    check(g.normal(0, 4, (rows, vocab)), 2, "f32", rules)
