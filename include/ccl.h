@@ -368,7 +368,6 @@ typedef struct {
  * with c its generated occurrences:
  *   x += the row's bias entries for v
  *   x = x > 0 ? x / repetition : x * repetition   if v occurs in the history
- *       (x / repetition as x times the rounded 1 / repetition)
  *   x = (x - frequency * c) - presence            if c > 0
  *   x = -inf                                      if the row's mask forbids v
  * A row that its mask leaves nothing is all -inf.

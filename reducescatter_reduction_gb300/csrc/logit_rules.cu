@@ -266,12 +266,11 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
     const float rep = a.r.repetition ? a.r.repetition[row] : 1.0f;
     const float freq = a.r.frequency ? a.r.frequency[row] : 0.0f;
     const float pres = a.r.presence ? a.r.presence[row] : 0.0f;
-    const float rep_inv = __fdiv_rn(1.0f, rep);     // x * (1 / rep) for x / rep: one rounding more, no division per element
     auto counter = [&](uint32_t cell) -> uint32_t { return (cnt[cell / PER] >> (WIDE ? 0 : (cell % 2) * 16)) & ONES; };
     auto changed = [&](float y, uint32_t c, float bias) -> float {
         if (c & BIASED) y = __fadd_rn(y, bias);
         const uint32_t seen = c & (BIASED - 1);
-        if (seen) y = __fmul_rn(y, y > 0.0f ? rep_inv : rep);
+        if (seen) y = y > 0.0f ? __fdiv_rn(y, rep) : __fmul_rn(y, rep);
         if (seen >= kGenerated) y = __fsub_rn(__fsub_rn(y, __fmul_rn(freq, float(seen >> 1))), pres);
         return y;
     };
