@@ -101,10 +101,11 @@ __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const __gr
         if (hist[e]) atomicAdd(&a.cells[uint64_t(r) * a.experts + e], hist[e]);
 }
 
-// d_e into shared memory; returns mean(a).  hist: p * experts counters and p
-// row counts where the CTA counts for itself.
+// d_e into shared memory; returns where mean(a) is: in fp64, as the loss is
+// next to nothing but n times it where the experts are balanced.  hist: p *
+// experts counters and p row counts where the CTA counts for itself.
 template <int PM>
-__device__ __forceinline__ float balance_coefficients(const BalanceArgs<PM> &a, float *d_s, int *hist)
+__device__ __forceinline__ const double *balance_coefficients(const BalanceArgs<PM> &a, float *d_s, int *hist)
 {
     __shared__ unsigned long long parts[2][kBalanceWarps];   // valid rows, choices
     const uint32_t E = a.experts;
@@ -178,15 +179,16 @@ __device__ __forceinline__ float balance_coefficients(const BalanceArgs<PM> &a, 
     }
     // One thread divides in fp64 (which this GPU does slowly): a_e = count_e scale, d_e = (E count_e - sum) scale / E.
     // The difference is exact in 64-bit integers and is rounded once to fp32, its product with the scale a second time.
-    __shared__ float scale_s[2];
+    __shared__ float scale_s;
+    __shared__ double mean_s;
     if (threadIdx.x == 0) {
         const double n = double(all_rows);
         const double per = all_rows ? a.coef / (double(a.k) * n * n) : 0.0;     // scale / E
-        scale_s[0] = float(per);
-        scale_s[1] = float(double(all) * per);                                 // mean(a)
+        scale_s = float(per);
+        mean_s = double(all) * per;
     }
     __syncthreads();
-    const float per = scale_s[0];
+    const float per = scale_s;
     const long long sum = (long long)all;
     for (uint32_t e = threadIdx.x; e < E; e += kBalanceThreads) {
         unsigned long long t = total;
@@ -197,13 +199,13 @@ __device__ __forceinline__ float balance_coefficients(const BalanceArgs<PM> &a, 
         d_s[e] = float((long long)(t * E) - sum) * per;
     }
     __syncthreads();
-    return scale_s[1];
+    return &mean_s;
 }
 
 // The CTAs' sums: each leaves its pair, the last one adds the pairs in the
 // order of the CTAs, writes the loss and leaves the scratch at zero.
 template <int PM>
-__device__ __forceinline__ void balance_finish(const BalanceArgs<PM> &a, float lean, int live, float mean)
+__device__ __forceinline__ void balance_finish(const BalanceArgs<PM> &a, float lean, int live, const double *mean)
 {
     __shared__ double red[2][kBalanceWarps];
     __shared__ bool last;
@@ -257,7 +259,7 @@ __device__ __forceinline__ void balance_finish(const BalanceArgs<PM> &a, float l
             s += red[0][w];
             c += red[1][w];
         }
-        *a.loss = float(s + c * double(mean));
+        *a.loss = float(s + c * *mean);
         *a.ticket = 0;
     }
 }
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(kBalanceThreads, NV * Traits<T>::VEC > 16 ? 2 
     grid_dependency_wait();
     grid_dependents_launch();
     fetch(t, at);
-    const float mean = balance_coefficients(a, d_s, reinterpret_cast<int *>(d_s + E));
+    const double *mean = balance_coefficients(a, d_s, reinterpret_cast<int *>(d_s + E));
     Pair d[NV * PAIRS];
 #pragma unroll
     for (int n = 0; n < NV; ++n)
@@ -473,7 +475,7 @@ __global__ void __launch_bounds__(kBalanceThreads, kOddCtas<NE>) balance_odd_ker
     for (int i = 0; i < STAGES - 1; ++i) fetch(t + i * stride, i);
     auto is_on = [&](uint64_t row) { return row < a.rows && (!valid || valid[row]); };
     bool coming = is_on(t + mine);
-    const float mean = balance_coefficients(a, d_s, reinterpret_cast<int *>(d_s + E));
+    const double *mean = balance_coefficients(a, d_s, reinterpret_cast<int *>(d_s + E));
     Pair d[PAIRS];
 #pragma unroll
     for (int i = 0; i < PAIRS; ++i) {
@@ -579,7 +581,7 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_any_kernel(const __gr
     const uint32_t E = a.experts, r = blockIdx.y;
     grid_dependency_wait();
     grid_dependents_launch();
-    const float mean = balance_coefficients(a, d_s, reinterpret_cast<int *>(d_s + E));
+    const double *mean = balance_coefficients(a, d_s, reinterpret_cast<int *>(d_s + E));
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const bool fwd = a.pass & CCL_PASS_FORWARD, bwd = a.pass & CCL_PASS_BACKWARD;
     const float up = bwd && a.dloss ? *a.dloss : 1.0f;

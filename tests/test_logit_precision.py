@@ -51,3 +51,60 @@ def test_repetition_divides_once(in_place, biased):
     ranks.finish()
     differ = got.view(np.int32) != want.view(np.int32)
     assert not differ.any(), f"{int(differ.sum())} of {differ.size} values"
+
+
+def one_hot_case(rows, E, k, p, seed, even):
+    """Router rows of one finite logit each: their softmax is exactly 1 there, so the loss is sum_t a_e(t), and what is
+    left to round are the coefficients, the sums and the result."""
+    g = rng(seed)
+    at = [g.integers(0, E // 2, rows) for _ in range(p)]           # (a dropped or doubled row of these changes the loss)
+    xs = []
+    for a in at:
+        x = np.full((rows, E), -np.inf, dtype=np.float32)
+        x[np.arange(rows), a] = g.normal(0, 5, rows)
+        xs.append(x)
+    if even:        # nearly equal counts: next to the mean the differences are small
+        ids = [(np.arange(rows * k) % E).reshape(rows, k).astype(np.int32) for _ in range(p)]
+    else:           # the first half of the experts has two thirds of the choices
+        ids = [np.where(g.random((rows, k)) < 2 / 3, g.integers(0, E // 2, (rows, k)), g.integers(E // 2, E, (rows, k))).astype(np.int32)
+               for _ in range(p)]
+    return xs, at, ids
+
+
+@pytest.mark.parametrize("p,rows,E,k", [(1, 7, 64, 2), (2, 1000, 64, 4), (3, 4001, 61, 3), (8, 2100, 96, 1), (4, 10000, 128, 2), (2, 50, 1500, 8),
+                                        (8, 5000, 33, 4), (1, 30000, 8, 1)])
+@pytest.mark.parametrize("even", [False, True])
+def test_the_loss_misses_no_row_and_is_rounded_once(p, rows, E, k, even):
+    """loss = n mean(a) + sum_t d_e(t).  The first term is fp64.  d_e = fl(E count - sum) fl(scale): three roundings; over the row's
+    one exponential and its reciprocal (two ulps, 4 u): six more.  A thread adds the d of its own rows in fp32, at most m of them,
+    then five steps of a warp; the rest is fp64.  So the sum of d is off by at most (14 + m) u sum |d|, a small part of one row's |d|,
+    which the test sees to; the loss is rounded once more."""
+    worst = 0.0
+    for seed in range(6):
+        xs, at, ids = one_hot_case(rows, E, k, p, seed, even)
+        coef = float(np.float32(0.01 * (1 + seed / 7)))
+        n = p * rows
+        counts = sum(np.bincount(i.reshape(-1), minlength=E) for i in ids)
+        scale = coef * E / (k * float(n) ** 2)
+        d = (counts - counts.mean()) * scale
+        picked = [d[a] for a in at]
+        want = n * (counts.mean() * scale) + sum(float(v.sum()) for v in picked)
+        # a CTA has eight warps, and there are at least two CTAs an SM and 8 rows a CTA: a thread has at most this many rows
+        m = -(-rows * p // (152 * 8)) + 1
+        size = sum(float(np.abs(v).sum()) for v in picked)
+        off = (14 + m) * 2.0 ** -24 * size
+        if not even:
+            assert off < 0.25 * min(float(np.abs(v).min()) for v in picked), "the tolerance has to tell a row"
+        ranks = Ranks([torch.from_numpy(x).cuda() for x in xs], "f32")
+        ids_d = [torch.from_numpy(i).cuda() for i in ids]
+        cnt, tok = torch.empty(p, E, dtype=torch.int32, device="cuda"), torch.empty(p, dtype=torch.int32, device="cuda")
+        loss = torch.empty(1, device="cuda")
+        ccl.ccl_balance_loss(ranks.comm, "f32", "forward", rows, E, k, [i.data_ptr() for i in ids_d], None, coef, 0, cnt.data_ptr(),
+                             tok.data_ptr(), loss.data_ptr(), stream=stream())
+        torch.cuda.synchronize()
+        err = abs(float(loss) - want)
+        # half a step of the result, and 2^-40 for the fp64 sums
+        assert err <= (2.0 ** -24 + 2.0 ** -40) * abs(want) + off, (seed, err / abs(want) * 2 ** 24, off / abs(want) * 2 ** 24)
+        worst = max(worst, (err - off) / abs(want) * 2 ** 24)
+        ranks.finish(wrote=False)
+    print(f"worst beyond the sums: {worst:.2f} u")
