@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(kBalanceThreads, NV * Traits<T>::VEC > 16 ? 2 
             s += s2;
             w += w2;
         }
-        const float inv = s == 0.0f ? 0.0f : __fdividef(1.0f, s);    // a row of nothing but -inf has no softmax: p = 0
+        const float inv = s == 0.0f ? 0.0f : 1.0f / s;    // a row of nothing but -inf has no softmax: p = 0
         const float lean = w * inv;
         if (l == 0 && s != 0.0f) {
             lean_sum += lean;
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(kBalanceThreads, kOddCtas<NE>) balance_odd_ker
             s += s2;
             w += w2;
         }
-        const float inv = s == 0.0f ? 0.0f : __fdividef(1.0f, s);
+        const float inv = s == 0.0f ? 0.0f : 1.0f / s;
         const float lean = w * inv;
         if (l == 0 && s != 0.0f) {
             lean_sum += lean;

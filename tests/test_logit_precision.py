@@ -108,3 +108,26 @@ def test_the_loss_misses_no_row_and_is_rounded_once(p, rows, E, k, even):
         worst = max(worst, (err - off) / abs(want) * 2 ** 24)
         ranks.finish(wrote=False)
     print(f"worst beyond the sums: {worst:.2f} u")
+
+
+@pytest.mark.parametrize("E", list(range(2, 65)) + [100, 203, 511, 600, 700, 999, 1001, 1024])
+def test_the_softmax_divides_once(E):
+    """Rows of equal logits, coefficients that fp32 holds exactly and that add up to 0: each probability is fl(1 / E), each
+    gradient one product with it, bit for bit."""
+    rows, n = 64, 64
+    g = rng(E)
+    ids = np.minimum(g.integers(0, E, (rows, 1)), g.integers(0, E, (rows, 1))).astype(np.int32)
+    d = (E * np.bincount(ids.reshape(-1), minlength=E) - n) / float(n) ** 2          # coef E count / (k n^2) - its mean, k = coef = 1
+    assert np.abs(d).sum() * n ** 2 < 2 ** 24
+    want = d.astype(np.float32) * (np.float32(1) / np.float32(E))
+    for layout in (dict(), dict(offset=1)):
+        ranks = Ranks([torch.zeros(rows, E, device="cuda")], "f32", **layout)
+        ids_d = torch.from_numpy(ids).cuda()
+        cnt, tok = torch.empty(E, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+        loss = torch.empty(1, device="cuda")
+        ccl.ccl_balance_loss(ranks.comm, "f32", "both", rows, E, 1, [ids_d.data_ptr()], None, 1.0, 0, cnt.data_ptr(), tok.data_ptr(),
+                             loss.data_ptr(), stream=stream())
+        torch.cuda.synchronize()
+        got = ranks.outs[0].view.cpu().numpy()
+        ranks.finish()
+        assert np.array_equal(got.view(np.int32), np.broadcast_to(want, got.shape).view(np.int32))
