@@ -482,10 +482,12 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
             if constexpr (BWD) {
                 const uint32_t slot = k & 1, parity = (k >> 1) & 1;
                 ok = ok && __all_sync(0xffffffffu, distill_wait(a, sh, &sh.taught[slot], parity, 7, row_item));
-                ok = ok && __all_sync(0xffffffffu, distill_wait(a, sh, &sh.stored[slot], parity, 7, row_item));
                 if (!ok) break;
                 const uint32_t row = div_by(row_item, a.by_pieces);
-                const float tinv = __fdividef(1.0f, sh.teacher_sum[slot]), row_m = sh.used_max[slot], inv = sh.used_inv[slot];
+                const float tinv = 1.0f / sh.teacher_sum[slot];     // while the consumers store
+                ok = __all_sync(0xffffffffu, distill_wait(a, sh, &sh.stored[slot], parity, 7, row_item));
+                if (!ok) break;
+                const float row_m = sh.used_max[slot], inv = sh.used_inv[slot];
                 const float factor = sh.weight[slot] * a.temperature;
                 const uint32_t n = sh.entries[slot];
                 const int *ids = id_s + slot * a.kpad;

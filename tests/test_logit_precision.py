@@ -131,3 +131,24 @@ def test_the_softmax_divides_once(E):
         got = ranks.outs[0].view.cpu().numpy()
         ranks.finish()
         assert np.array_equal(got.view(np.int32), np.broadcast_to(want, got.shape).view(np.int32))
+
+
+@pytest.mark.parametrize("steps", ["both", "each"])
+def test_the_teachers_softmax_divides_once(steps):
+    """Equal teacher logits, at tokens whose own probability is 0 in fp32: each gradient is -fl(1 / k), bit for bit, for every
+    number of entries at once (row i has i + 1)."""
+    rows = k = 300
+    z = torch.zeros(rows, 1000, device="cuda")
+    z[:, 500:] = -200.0
+    ids = torch.where(torch.arange(k, device="cuda") <= torch.arange(rows, device="cuda")[:, None],
+                      600 + torch.arange(k, device="cuda"), -1).to(torch.int32)
+    t, loss, stats = torch.full((rows, k), 3.0, device="cuda"), torch.empty(rows, device="cuda"), torch.empty(rows, 2, device="cuda")
+    ranks = Ranks(shards(z, 2), "f32")
+    for s in {"both": ["both"], "each": ["forward", "backward"]}[steps]:
+        ccl.ccl_distill_topk(ranks.comm, "f32", s, rows, 1000, k, ids.data_ptr(), t.data_ptr(), loss=loss.data_ptr(),
+                             stats=stats.data_ptr(), stream=stream())
+    torch.cuda.synchronize()
+    got = torch.cat([b.view for b in ranks.outs], 1)[:, 600:600 + k].cpu().numpy()
+    ranks.finish()
+    want = np.where(ids.cpu().numpy() >= 0, -(np.float32(1) / np.arange(1, rows + 1, dtype=np.float32))[:, None], np.float32(0))
+    assert np.array_equal(got, want), f"{int((got != want).any(1).sum())} rows"
