@@ -63,6 +63,14 @@ __device__ __forceinline__ bool in_bounds(bool ok, unsigned *status, unsigned si
     }
 }
 
+// The same for an access to [at, at + bytes) of the buffer of `size` bytes that begins at `buf`.
+__device__ __forceinline__ bool in_buffer(const void *at, uint64_t bytes, const void *buf, uint64_t size, unsigned *status, unsigned site)
+{
+    if constexpr (!kBoundsCheck) return true;
+    const uint64_t from = uintptr_t(at) - uintptr_t(buf);       // (huge in front of it)
+    return in_bounds(from <= size && bytes <= size - from, status, site, from);
+}
+
 // ---------------------------------------------------------------------------
 // Memory access.  Inputs are streamed once: read without allocating in L1,
 // with a 256-byte L2 prefetch hint.  ld_stream_v4 reads through the

@@ -279,7 +279,7 @@ struct Piece {
             tail = hi == a.groups;
         }
     }
-    __device__ __forceinline__ void cut(const DistillArgs<PM> &a, const ShardRow<T> &row)
+    __device__ __forceinline__ void cut(const DistillArgs<PM> &a, const ShardRow<T, PM> &row)
     {
         const uint32_t whole = row.end - row.first;
         if (a.segments == 1) {
@@ -405,12 +405,12 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
             z = -INFINITY;
             to = 0;
             if (pe.rank >= s.p || !in_bounds(row < s.rows, s.status, kSiteDistill, row)) return;
-            const ShardRow<T> in(s.in[pe.rank], s.ld, row, shard_width(s, pe.rank));
+            const ShardRow<T, PM> in(s, s.in[pe.rank], pe.rank, row);
             const int col = in.edge(e % (2 * VEC), pe.head && c == 0, pe.tail && c + 1 == a.chunks);
             if (col < 0) return;
             z = in.column(col);
             if (BWD) {
-                const ShardRow<T> out(s.out[pe.rank], s.ld, row, in.width);
+                const ShardRow<T, PM> out(s, s.out[pe.rank], pe.rank, row);
                 to = out.base + (uint64_t(out.shift) + uint32_t(col)) * (16 / VEC);
             }
         };
@@ -431,13 +431,13 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
             const void *from = nullptr;
             Piece<T, PM, PASS> pc(a, q, lane);
             if (lane < int(a.segments) && pc.rank < s.p) {
-                const ShardRow<T> in(s.in[pc.rank], s.ld, row, shard_width(s, pc.rank));
+                const ShardRow<T, PM> in(s, s.in[pc.rank], pc.rank, row);
                 pc.cut(a, in);
                 const uint32_t k0 = min(pc.j0 + c * cap, pc.j1), k1 = min(k0 + cap, pc.j1);
                 if (in_bounds(row < s.rows && k1 <= in.end, s.status, kSiteDistill, row)) n = k1 - k0;
                 from = in.group(k0);
                 if (BWD) {
-                    const ShardRow<T> out(s.out[pc.rank], s.ld, row, in.width);
+                    const ShardRow<T, PM> out(s, s.out[pc.rank], pc.rank, row);
                     const uintptr_t at = out.base + (uint64_t(out.shift) + k0 * VEC - in.shift) * (16 / VEC);
                     d.seg[lane].out = at;
                     d.seg[lane].aligned = at % 16 == 0;
@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
                     if (!mine) continue;
                     const uint32_t r = rank_of_token(s, uint32_t(id));
                     if (in_bounds(row < s.rows && r < s.p, s.status, kSiteDistill, row))
-                        ShardRow<T>(s.out[r], s.ld, row, shard_width(s, r))
+                        ShardRow<T, PM>(s, s.out[r], r, row)
                             .set_column(uint32_t(id) - shard_begin(s, r), (ex2((zs[i] - row_m) * a.to_log2) * inv - w * tinv) * factor);
                 }
                 __syncwarp();
@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
                 h.count = s.vocab;
             } else if (a.segments == 1) {
                 Piece<T, PM, PASS> pc(a, q, 0);
-                const ShardRow<T> in(s.in[pc.rank], s.ld, h.row, shard_width(s, pc.rank));
+                const ShardRow<T, PM> in(s, s.in[pc.rank], pc.rank, h.row);
                 pc.cut(a, in);
                 const uint32_t lo = pc.head ? 0u : in.head() + (pc.j0 - in.first) * VEC;
                 const uint32_t hi = pc.tail ? in.width : in.head() + (pc.j1 - in.first) * VEC;
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
                     z = Tr::load1(reinterpret_cast<const void *>(h.at), uint32_t(id) - h.from);
                 } else {
                     const uint32_t r = rank_of_token(s, uint32_t(id));
-                    z = ShardRow<T>(s.in[r], s.ld, h.row, shard_width(s, r)).column(uint32_t(id) - shard_begin(s, r));
+                    z = ShardRow<T, PM>(s, s.in[r], r, h.row).column(uint32_t(id) - shard_begin(s, r));
                 }
             } else if (uint32_t(id) < s.vocab) {
                 id |= int(0x80000000u);
@@ -960,7 +960,7 @@ template <typename T, int PM, int PASS, int HELD>
 static cudaError_t distill_held(const Launch &L, const DistillLaunch &N, LaunchInfo *info)
 {
     DistillArgs<PM> a;
-    fill_shards(&a.s, L, N.rows, N.vocab, N.ld);
+    fill_shards(&a.s, L, N.rows, N.vocab, N.ld, kSiteDistill);
     a.ids = N.ids;
     a.teacher = N.teacher;
     a.weight = N.weight;

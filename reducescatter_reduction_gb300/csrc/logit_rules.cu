@@ -97,10 +97,9 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
     const uint32_t rank = div_by(rest, a.by_slices), slice = rest - rank * a.slices;
     const uint64_t row = row32;
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const ShardRow<T> in(s.in[rank], s.ld, row, shard_width(s, rank));
+    const ShardRow<T, PM> in(s, s.in[rank], rank, row);
     const uint32_t whole = in.end - in.first;
     if (slice > 0 && slice * GROUPS >= whole) return;
-    if (!in_bounds(row < s.rows && rank < s.p, s.status, kSiteRules, row)) return;
     const uint32_t j0 = in.first + slice * GROUPS, j1 = min(j0 + GROUPS, in.end);
     const bool has_tail = j1 == in.end;
     // the slice's columns are [c0, c1); column c has cell c - cell0
@@ -118,15 +117,18 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
     grid_dependents_launch();
 
     // the row's rules, all loads at once, and the first tokens of its history whether they count or not
-    const int mask_at = a.r.mask && a.r.mask_index ? a.r.mask_index[row] : int(row);
-    const int ld = history ? int(a.r.history_ld) : 0;
+    const bool listed_row = row_held(s, row);      // (checked build: the lists have this row)
+    const int mask_at = a.r.mask && a.r.mask_index ? (listed_row ? a.r.mask_index[row] : -1) : int(row);
+    const int ld = history && listed_row ? int(a.r.history_ld) : 0;
     const int32_t *h = history ? a.r.history + row * a.r.history_ld : nullptr;
-    int len = history && a.r.history_len ? a.r.history_len[row] : ld;
-    const int prompt = history && a.r.prompt_len ? a.r.prompt_len[row] : 0;
-    const int offset0 = a.r.bias_count ? a.r.bias_offsets[row] : 0, offset1 = a.r.bias_count ? a.r.bias_offsets[row + 1] : 0;
+    int len = ld && a.r.history_len ? a.r.history_len[row] : ld;
+    const int prompt = ld && a.r.prompt_len ? a.r.prompt_len[row] : 0;
+    const bool lists = a.r.bias_count && listed_row;
+    const int offset0 = lists ? a.r.bias_offsets[row] : 0, offset1 = lists ? a.r.bias_offsets[row + 1] : 0;
+    auto held_token = [&](int j) { return in_bounds(uint64_t(row) * a.r.history_ld + j < s.held * a.r.history_ld, s.status, s.site, j); };
     int32_t token[BATCH];
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k) token[k] = tid + k * THREADS < ld ? h[tid + k * THREADS] : -1;
+    for (int k = 0; k < BATCH; ++k) token[k] = tid + k * THREADS < ld && held_token(tid + k * THREADS) ? h[tid + k * THREADS] : -1;
 
     // the mask bits of this thread's groups, then the logits of those that have any
     const uint32_t *mask = a.r.mask && mask_at >= 0 && uint64_t(mask_at) < a.r.mask_rows ? a.r.mask + uint64_t(mask_at) * a.r.mask_ld : nullptr;
@@ -135,17 +137,20 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
     uint32_t allowed[MASKS];
 #pragma unroll
     for (int i = 0; i < MASKS; ++i) allowed[i] = 0xffffffffu;
+    const uint32_t words = (s.vocab + 31) / 32;
+    auto word_of = [&](uint32_t w) -> uint32_t {
+        return in_bounds(uint64_t(mask_at) < a.r.mask_rows && w < words, s.status, s.site, w) ? mask[w] : 0u;
+    };
     auto ok_of = [&](int n) -> uint32_t { return (allowed[n / PACK] >> (n % PACK * VEC)) & ALL; };
     if (mask) {
-        const uint32_t words = (s.vocab + 31) / 32;
         const uint32_t v0 = token0 + (j0 + tid) * VEC - in.shift;
         uint32_t lo[NV], hi[NV];
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const uint32_t w = (v0 + n * THREADS * VEC) >> 5;
             const bool is = j0 + tid + n * THREADS < j1;
-            lo[n] = is ? mask[w] : 0u;
-            hi[n] = is && w + 1 < words ? mask[w + 1] : 0u;
+            lo[n] = is ? word_of(w) : 0u;
+            hi[n] = is && w + 1 < words ? word_of(w + 1) : 0u;
         }
 #pragma unroll
         for (int i = 0; i < MASKS; ++i) allowed[i] = 0;
@@ -158,7 +163,7 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const uint32_t j = j0 + tid + n * THREADS;
-            if (j < j1 && ok_of(n))
+            if (j < j1 && ok_of(n) && in.holds_group(j))
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + n * THREADS * 16), "l"(in.group(j)) : "memory");
         }
         if (edge >= 0) Tr::store1(stage, uint64_t(edge - cell0), in.column(edge));
@@ -169,9 +174,11 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
     len = len < 0 ? 0 : len > ld ? ld : len;
     uint32_t bias_token = 0xffffffffu;     // of this thread's entry in a block of the list, from the slice's first
     float bias_add = 0.0f;
+    auto held_entry = [&](uint32_t k) { return in_bounds(k < a.r.bias_count, s.status, s.site, k); };
     auto entry = [&](uint32_t k) {
-        bias_token = k < bias_hi ? uint32_t(a.r.bias_tokens[k]) - from : 0xffffffffu;
-        bias_add = k < bias_hi ? a.r.bias_values[k] : 0.0f;
+        const bool is = k < bias_hi && held_entry(k);
+        bias_token = is ? uint32_t(a.r.bias_tokens[k]) - from : 0xffffffffu;
+        bias_add = is ? a.r.bias_values[k] : 0.0f;
     };
     entry(bias_lo + tid);
     __syncthreads();
@@ -195,7 +202,7 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
     for (int j = tid; j - lane < len; j += BATCH * THREADS) {
         if (j != tid) {
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k) token[k] = j + k * THREADS < len ? h[j + k * THREADS] : -1;
+            for (int k = 0; k < BATCH; ++k) token[k] = j + k * THREADS < len && held_token(j + k * THREADS) ? h[j + k * THREADS] : -1;
         }
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
@@ -247,14 +254,14 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
         if (b + THREADS < bias_hi) __syncthreads();
     }
 
-    const ShardRow<T> out(s.out[rank], s.ld, row, in.width);
-    auto may = [&](uint32_t col) { return !mask || (mask[(token0 + col) >> 5] >> ((token0 + col) & 31)) & 1; };
+    const ShardRow<T, PM> out(s, s.out[rank], rank, row);
+    auto may = [&](uint32_t col) { return !mask || (word_of((token0 + col) >> 5) >> ((token0 + col) & 31)) & 1; };
     if (a.in_place) {
         // what the mask forbids
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
             const uint32_t j = j0 + tid + n * THREADS, ok = ok_of(n);
-            if (j < j1 && ok != ALL) store_group<T>(out, in, j, forbid<T>(ok ? ld_coherent_v4(in.group(j)) : lowest_group<T>(), ok));
+            if (j < j1 && ok != ALL) store_group<T>(out, in, j, forbid<T>(ok && in.holds_group(j) ? ld_coherent_v4(in.group(j)) : lowest_group<T>(), ok));
         }
         if (edge >= 0 && !may(edge)) out.set_column(edge, -INFINITY);
     } else {
@@ -263,9 +270,9 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
     __syncthreads();
 
     // the listed columns: in shared memory, or in place where they are allowed
-    const float rep = a.r.repetition ? a.r.repetition[row] : 1.0f;
-    const float freq = a.r.frequency ? a.r.frequency[row] : 0.0f;
-    const float pres = a.r.presence ? a.r.presence[row] : 0.0f;
+    const float rep = a.r.repetition && listed_row ? a.r.repetition[row] : 1.0f;
+    const float freq = a.r.frequency && listed_row ? a.r.frequency[row] : 0.0f;
+    const float pres = a.r.presence && listed_row ? a.r.presence[row] : 0.0f;
     auto counter = [&](uint32_t cell) -> uint32_t { return (cnt[cell / PER] >> (WIDE ? 0 : (cell % 2) * 16)) & ONES; };
     auto changed = [&](float y, uint32_t c, float bias) -> float {
         if (c & BIASED) y = __fadd_rn(y, bias);
@@ -292,7 +299,7 @@ __global__ void __launch_bounds__(THREADS, THREADS > 256 ? 2 : 3) logit_rules_ke
                 float v[M];
 #pragma unroll
                 for (int k = 0; k < M; ++k) {
-                    const bool in = b + 32 * k < bias_hi;
+                    const bool in = b + 32 * k < bias_hi && held_entry(b + 32 * k);
                     at[k] = in ? uint32_t(a.r.bias_tokens[b + 32 * k]) - part : 0xffffffffu;
                     v[k] = in ? a.r.bias_values[b + 32 * k] : 0.0f;
                 }
@@ -403,7 +410,7 @@ static cudaError_t rules_shape(const Launch &L, const RulesLaunch &N, LaunchInfo
 {
     constexpr int PER16 = Traits<T>::VEC == 8 ? 1 : 2;   // groups that hold eight elements
     RulesArgs<PM> a;
-    fill_shards(&a.s, L, N.rows, N.vocab, N.ld);
+    fill_shards(&a.s, L, N.rows, N.vocab, N.ld, kSiteRules);
     a.r = *N.rules;
     a.in_place = L.alias ? 1 : 0;
     const uint32_t groups = widest_groups<T>(a.s);

@@ -49,7 +49,10 @@ struct Shards {
     uint32_t p, vocab;
     uint32_t q, rem;    // widths: q + 1 for the first rem ranks, then q
     FastDiv by_q1, by_q;
-    unsigned *status;   // the communicator's status block (checked build)
+    // checked build:
+    unsigned *status;   // the communicator's status block
+    unsigned site;
+    uint64_t held;      // rows that every buffer and list has: `rows`, or one less where the debug hook wants the checks to fail
 };
 
 template <int PM>
@@ -64,30 +67,59 @@ __device__ __forceinline__ uint32_t rank_of_token(const Shards<PM> &a, uint32_t 
     return v < big ? div_by(v, a.by_q1) : a.rem + div_by(v - big, a.by_q);
 }
 
-// One row of one shard.
-template <typename T>
+// Bytes of rank r's buffers (checked build).
+template <int PM>
+__device__ __forceinline__ uint64_t shard_bytes(const Shards<PM> &a, uint32_t r, uint32_t element)
+{
+    const uint64_t w = shard_width(a, r);
+    return a.held && w ? ((a.held - 1) * (a.ld ? a.ld : w) + w) * element : 0;
+}
+
+// Row `row` of a list with one entry, or one line of entries, a row.
+template <int PM>
+__device__ __forceinline__ bool row_held(const Shards<PM> &a, uint64_t row) { return in_bounds(row < a.held, a.status, a.site, row); }
+
+// One row of one shard: of rank r's input or output buffer `buf`.
+template <typename T, int PM>
 struct ShardRow {
     static constexpr uint32_t VEC = Traits<T>::VEC, S = 16 / VEC;
     uintptr_t base;      // the 16-byte boundary at or below the row's first element
     uint32_t shift;      // elements between the boundary and the row
     uint32_t width;      // columns
     uint32_t first, end; // its whole groups are [first, end)
+    const Shards<PM> &s; // (these for the checks)
+    const void *buf;
+    uint32_t rank;
 
-    __device__ __forceinline__ ShardRow(const void *buf, uint64_t ld, uint64_t row, uint32_t w)
+    __device__ __forceinline__ ShardRow(const Shards<PM> &a, const void *of, uint32_t r, uint64_t row) : s(a), buf(of), rank(r)
     {
-        const uintptr_t at = uintptr_t(buf) + row * (ld ? ld : uint64_t(w)) * S;
+        width = shard_width(a, r);
+        const uintptr_t at = uintptr_t(buf) + row * (a.ld ? a.ld : uint64_t(width)) * S;
         base = at & ~uintptr_t(15);
         shift = uint32_t(at & 15) / S;
-        width = w;
         first = shift ? 1 : 0;
-        end = max(first, (shift + w) / VEC);
+        end = max(first, (shift + width) / VEC);
     }
+    // the access lies in the buffer
+    __device__ __forceinline__ bool holds(const void *at, uint64_t bytes) const
+    {
+        return !kBoundsCheck || in_buffer(at, bytes, buf, shard_bytes(s, rank, S), s.status, s.site);
+    }
+    __device__ __forceinline__ bool holds_group(uint32_t j) const { return holds(group(j), 16); }
     __device__ __forceinline__ uint32_t head() const { return min(width, first * VEC - shift); }         // columns before the groups
     __device__ __forceinline__ uint32_t tail_begin() const { return head() + (end - first) * VEC; }      // first column after them
     __device__ __forceinline__ const void *group(uint32_t j) const { return reinterpret_cast<const void *>(base + uintptr_t(j) * 16); }
     __device__ __forceinline__ void *group_out(uint32_t j) const { return reinterpret_cast<void *>(base + uintptr_t(j) * 16); }
-    __device__ __forceinline__ float column(uint32_t c) const { return Traits<T>::load1(reinterpret_cast<const void *>(base), uint64_t(shift) + c); }
-    __device__ __forceinline__ void set_column(uint32_t c, float v) const { Traits<T>::store1(reinterpret_cast<void *>(base), uint64_t(shift) + c, v); }
+    __device__ __forceinline__ float column(uint32_t c) const
+    {
+        if (!holds(reinterpret_cast<const void *>(base + (uintptr_t(shift) + c) * S), S)) return 0.0f;
+        return Traits<T>::load1(reinterpret_cast<const void *>(base), uint64_t(shift) + c);
+    }
+    __device__ __forceinline__ void set_column(uint32_t c, float v) const
+    {
+        if (!holds(reinterpret_cast<const void *>(base + (uintptr_t(shift) + c) * S), S)) return;
+        Traits<T>::store1(reinterpret_cast<void *>(base), uint64_t(shift) + c, v);
+    }
     // The edge column of thread t (or -1): t < VEC the head, the next VEC the tail.
     __device__ __forceinline__ int edge(uint32_t t, bool has_head, bool has_tail) const
     {
@@ -99,11 +131,12 @@ struct ShardRow {
 
 // Stores group j of the input row `in` to the same columns of `out`: one
 // 128-bit store where both rows begin at the same place between boundaries.
-template <typename T>
-__device__ __forceinline__ void store_group(const ShardRow<T> &out, const ShardRow<T> &in, uint32_t j, const uint4 &v)
+template <typename T, int PM>
+__device__ __forceinline__ void store_group(const ShardRow<T, PM> &out, const ShardRow<T, PM> &in, uint32_t j, const uint4 &v)
 {
     using Tr = Traits<T>;
     if (out.shift == in.shift) {
+        if (!out.holds_group(j)) return;
         st_stream_v4(out.group_out(j), v);
         return;
     }
@@ -237,7 +270,7 @@ __device__ __forceinline__ float finite_max(float m) { return m == -INFINITY ? 0
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int PM>
-inline void fill_shards(Shards<PM> *s, const Launch &L, uint64_t rows, uint32_t vocab, uint64_t ld)
+inline void fill_shards(Shards<PM> *s, const Launch &L, uint64_t rows, uint32_t vocab, uint64_t ld, unsigned site)
 {
     const uint32_t p = uint32_t(L.p);
     for (uint32_t r = 0; r < p; ++r) {
@@ -253,6 +286,8 @@ inline void fill_shards(Shards<PM> *s, const Launch &L, uint64_t rows, uint32_t 
     s->by_q1 = fast_div(s->q + 1);
     s->by_q = fast_div(s->q ? s->q : 1);
     s->status = L.status;
+    s->site = site;
+    s->held = rows - (L.stall_test == 2 && rows ? 1 : 0);
 }
 
 // The most whole groups a row of the widest shard has.

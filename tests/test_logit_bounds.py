@@ -1,0 +1,75 @@
+"""The checked build's tests of the accesses that the operators on logits make
+(include/ccl.h, ccl_bounds_checked).  The debug hook has the checks take every
+rank buffer, and every list with an entry a row, for one row shorter than the
+call says: the last row's accesses are then recorded and not made, and the
+other rows come out as ever.  These tests run only against the checked library
+(test_zy_checked_logit_bounds.py runs them against it)."""
+import numpy as np
+import pytest
+import torch
+
+import reducescatter_reduction_gb300 as ccl
+from logit_testutil import Ranks, rng, shards, stream
+from test_logit_rules import make_rules
+
+pytestmark = pytest.mark.gpu
+
+LAYOUTS = [dict(), dict(offset=1), dict(offset=3, out_offset=1), dict(in_place=True), dict(in_place=True, offset=5)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _checked():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    ccl.load_library()
+    if not ccl.ccl_bounds_checked():
+        pytest.skip("the default build has no bounds checks (CCL_LIBRARY selects the checked build)")
+
+
+def bits(t):
+    return t.contiguous().view(torch.uint8)
+
+
+def violated(ranks, call, site):
+    """Runs `call` with the hook; the record, and that the outputs' last rows are what they were.  Their other rows."""
+    before = [b.view.clone() for b in ranks.outs]
+    ccl.ccl_comm_set_debug(ranks.comm, 0, 2)
+    call()
+    with pytest.raises(ccl.CclError) as e:
+        ccl.ccl_comm_check(ranks.comm)
+    assert e.value.status == ccl.CCL_ERR_BOUNDS and f"site {site}" in str(e.value)
+    ccl.ccl_comm_set_debug(ranks.comm, 0, 0)
+    for b, old in zip(ranks.outs, before):
+        assert torch.equal(bits(b.view[-1]), bits(old[-1]))
+    return [b.view[:-1].clone() for b in ranks.outs]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("rows,vocab", [(6, 8190), (40, 150001), (3, 5)])
+def test_rules(dtype, layout, rows, vocab):
+    full = torch.from_numpy(rng(rows).normal(0, 4, (rows, vocab))).cuda()
+    rules = make_rules(rows, vocab, 5, 300, 40, True)
+    call = lambda r: ccl.ccl_logit_rules(r.comm, dtype, rows, vocab, rules.s, stream=stream())
+    ranks = Ranks(shards(full, 2), dtype, **layout)
+    got = violated(ranks, lambda: call(ranks), 8)
+    ranks.finish()
+    ranks = Ranks(shards(full, 2), dtype, **layout)
+    call(ranks)
+    torch.cuda.synchronize()
+    for b, g in zip(ranks.outs, got):
+        assert torch.equal(bits(b.view[:-1]), bits(g))
+    ranks.finish()
+
+
+@pytest.mark.parametrize("what", ["history", "mask", "repetition"])
+def test_one_rule_alone(what):
+    """Lists are tested too, and not by the logits' own checks alone."""
+    rows, vocab = 4, 3000
+    h = make_rules(rows, vocab, 5, 300, 40, True).h
+    arrays = {"history": ("history", "history_len", "frequency"), "mask": ("mask", "mask_index"), "repetition": ("history", "repetition")}[what]
+    from test_logit_rules import Rules
+    rules = Rules(**{k: h[k] for k in arrays})
+    ranks = Ranks(shards(torch.zeros(rows, vocab, device="cuda"), 1), "f32")
+    violated(ranks, lambda: ccl.ccl_logit_rules(ranks.comm, "f32", rows, vocab, rules.s, stream=stream()), 8)
+    ranks.finish()
