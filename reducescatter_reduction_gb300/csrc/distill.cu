@@ -386,6 +386,7 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
                 if (total == 0.0f) loss = INFINITY;
                 else loss = heat * (heat * ((u / tsum - logf(tsum)) - (dot / heat - ls)));   // heat^2 may be out of range
             }
+            if (!row_held(s, row)) return;
             a.loss[row] = loss;
             if (a.stats) {
                 a.stats[2 * uint64_t(row)] = mx;
@@ -404,7 +405,7 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
             Piece<T, PM, PASS> pe(a, of - row * a.pieces, e / (2 * VEC));
             z = -INFINITY;
             to = 0;
-            if (pe.rank >= s.p || !in_bounds(row < s.rows, s.status, kSiteDistill, row)) return;
+            if (pe.rank >= s.p) return;
             const ShardRow<T, PM> in(s, s.in[pe.rank], pe.rank, row);
             const int col = in.edge(e % (2 * VEC), pe.head && c == 0, pe.tail && c + 1 == a.chunks);
             if (col < 0) return;
@@ -434,8 +435,8 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
                 const ShardRow<T, PM> in(s, s.in[pc.rank], pc.rank, row);
                 pc.cut(a, in);
                 const uint32_t k0 = min(pc.j0 + c * cap, pc.j1), k1 = min(k0 + cap, pc.j1);
-                if (in_bounds(row < s.rows && k1 <= in.end, s.status, kSiteDistill, row)) n = k1 - k0;
                 from = in.group(k0);
+                if (k0 == k1 || in.holds(from, (k1 - k0) * 16)) n = k1 - k0;
                 if (BWD) {
                     const ShardRow<T, PM> out(s, s.out[pc.rank], pc.rank, row);
                     const uintptr_t at = out.base + (uint64_t(out.shift) + k0 * VEC - in.shift) * (16 / VEC);
@@ -505,9 +506,8 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
                     }
                     if (!mine) continue;
                     const uint32_t r = rank_of_token(s, uint32_t(id));
-                    if (in_bounds(row < s.rows && r < s.p, s.status, kSiteDistill, row))
-                        ShardRow<T, PM>(s, s.out[r], r, row)
-                            .set_column(uint32_t(id) - shard_begin(s, r), (ex2((zs[i] - row_m) * a.to_log2) * inv - w * tinv) * factor);
+                    ShardRow<T, PM>(s, s.out[r], r, row)
+                        .set_column(uint32_t(id) - shard_begin(s, r), (ex2((zs[i] - row_m) * a.to_log2) * inv - w * tinv) * factor);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_addr(&sh.taught_free[slot]));
@@ -528,9 +528,11 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
         Held coming, next, now;
         // this piece's entries of a row (the same piece of every row where the CTAs form a cluster)
         const uint32_t begin = BWD ? 0u : min((blockIdx.x % a.pieces) * a.share, a.k), share = BWD ? a.k : min(a.share, a.k - begin);
+        auto held_entry = [&](uint64_t at) { return in_bounds(at < s.held * a.k, s.status, s.site, at); };
         auto fetch = [&](uint32_t item) {
             if (item >= a.items) return;
             const uint32_t row = div_by(item, a.by_pieces);
+            const bool listed = row_held(s, row);
             const uint64_t at = uint64_t(row) * a.k + begin + lane;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -539,14 +541,14 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
                     coming.t[u] = -INFINITY;
                     continue;
                 }
-                const bool in = lane + 32 * u < share;
+                const bool in = lane + 32 * u < share && listed && held_entry(at + 32 * u);
                 coming.id[u] = in ? a.ids[at + 32 * u] : -1;
                 coming.t[u] = in ? load_any(a.teacher, a.teacher_dtype, at + 32 * u) : -INFINITY;
             }
-            coming.w = BWD && a.weight ? a.weight[row] : 1.0f;
+            coming.w = BWD && a.weight && listed ? a.weight[row] : 1.0f;
             if (!FWD) {
-                coming.max = a.stats[2 * uint64_t(row)];
-                coming.log_sum = a.stats[2 * uint64_t(row) + 1];
+                coming.max = listed ? a.stats[2 * uint64_t(row)] : 0.0f;
+                coming.log_sum = listed ? a.stats[2 * uint64_t(row) + 1] : 0.0f;
             }
         };
         // What a piece holds: tokens [from, to), consecutive in memory from `at` on where it is of one shard.
@@ -581,8 +583,11 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
         auto place = [&](const Hold &h, int &id, float &t, float &z) {
             z = 0.0f;
             if (uint32_t(id) - h.from < h.count) {
-                if (!in_bounds(h.row < s.rows && uint32_t(id) < s.vocab, s.status, kSiteDistill, h.row)) return;
                 if (BWD && a.segments == 1) {
+                    if constexpr (kBoundsCheck) {
+                        const uint32_t r = rank_of_token(s, uint32_t(id));
+                        if (!ShardRow<T, PM>(s, s.in[r], r, h.row).holds(reinterpret_cast<const void *>(h.at + uintptr_t(uint32_t(id) - h.from) * ES), ES)) return;
+                    }
                     z = Tr::load1(reinterpret_cast<const void *>(h.at), uint32_t(id) - h.from);
                 } else {
                     const uint32_t r = rank_of_token(s, uint32_t(id));
@@ -634,7 +639,7 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
                     float t[M], z[M];
 #pragma unroll
                     for (int u = 0; u < M; ++u) {
-                        const bool in = i0 + 32 * u < share;
+                        const bool in = i0 + 32 * u < share && held_entry(at + i0 + 32 * u);
                         id[u] = in ? a.ids[at + i0 + 32 * u] : -1;
                         t[u] = in ? load_any(a.teacher, a.teacher_dtype, at + i0 + 32 * u) : -INFINITY;
                     }
@@ -776,6 +781,12 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
                 }
                 return gm;
             };
+            // (checked build) a store of segment sg's lies in the output of its rank
+            auto stores = [&](uint32_t sg, const void *to, uint32_t bytes) -> bool {
+                if constexpr (!kBoundsCheck) return true;
+                const Piece<T, PM, PASS> ps(a, q, sg);
+                return in_bounds(ps.rank < s.p, s.status, s.site, row) && ShardRow<T, PM>(s, s.out[ps.rank], ps.rank, row).holds(to, bytes);
+            };
             // stores e * g (edge: edge * g) where the chunk came from; zero for a row without a teacher
             auto put = [&](float g, bool taught) {
                 const uint32_t groups = d->groups;
@@ -795,7 +806,8 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
                     char *to = reinterpret_cast<char *>(d->seg[0].out) + size_t(tid) * 16;
 #pragma unroll
                     for (int n = 0; n < NG; ++n)
-                        if (uint32_t(tid + n * kDistillConsumers) < groups) st_stream_v4(to + n * kDistillConsumers * 16, value(n));
+                        if (uint32_t(tid + n * kDistillConsumers) < groups && stores(0, to + n * kDistillConsumers * 16, 16))
+                            st_stream_v4(to + n * kDistillConsumers * 16, value(n));
                 } else {
 #pragma unroll
                     for (int n = 0; n < NG; ++n) {
@@ -804,6 +816,7 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
                         uint32_t sg = 0;
                         while (sg + 1 < a.segments && d->seg[sg + 1].first <= g16) ++sg;
                         const uintptr_t to = uintptr_t(d->seg[sg].out) + uintptr_t(g16 - d->seg[sg].first) * 16;
+                        if (!stores(sg, reinterpret_cast<const void *>(to), 16)) continue;
                         const uint4 v = value(n);
                         if (d->seg[sg].aligned) {
                             st_stream_v4(reinterpret_cast<void *>(to), v);
@@ -815,7 +828,8 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
                         }
                     }
                 }
-                if (a.edges && uint32_t(tid) < a.segments * 2 * VEC && d->edge_out[tid])
+                if (a.edges && uint32_t(tid) < a.segments * 2 * VEC && d->edge_out[tid] &&
+                    stores(tid / (2 * VEC), reinterpret_cast<const void *>(uintptr_t(d->edge_out[tid])), 16 / VEC))
                     Tr::store1(reinterpret_cast<void *>(uintptr_t(d->edge_out[tid])), 0, edge * gg.x);
             };
             float row_m = 0.0f, inv = 0.0f, factor = 0.0f;

@@ -73,3 +73,34 @@ def test_one_rule_alone(what):
     ranks = Ranks(shards(torch.zeros(rows, vocab, device="cuda"), 1), "f32")
     violated(ranks, lambda: ccl.ccl_logit_rules(ranks.comm, "f32", rows, vocab, rules.s, stream=stream()), 8)
     ranks.finish()
+
+
+@pytest.mark.parametrize("steps", ["forward", "backward", "both"])
+@pytest.mark.parametrize("layout", LAYOUTS + [dict(ld=60000)])
+@pytest.mark.parametrize("p,rows,vocab,k", [(2, 5, 8190, 20), (2, 170, 100003, 200), (8, 330, 8003, 40), (1, 3, 7, 2)])
+def test_distillation(steps, layout, p, rows, vocab, k):
+    g = rng(vocab)
+    full = torch.from_numpy(g.normal(0, 3, (rows, vocab))).cuda()
+    ids = torch.from_numpy(g.integers(-1, vocab, (rows, k)).astype(np.int32)).cuda()
+    t, w = torch.from_numpy(g.normal(0, 3, (rows, k))).cuda().float(), torch.ones(rows, device="cuda")
+
+    def run(loss, stats, broken):
+        ranks = Ranks(shards(full, p), "bf16", **layout)
+        call = lambda: ccl.ccl_distill_topk(ranks.comm, "bf16", steps, rows, vocab, k, ids.data_ptr(), t.data_ptr(), temperature=2.0,
+                                            row_weight=w.data_ptr(), loss=loss.data_ptr(), stats=stats.data_ptr(), ld=layout.get("ld", 0),
+                                            stream=stream())
+        if broken:
+            out = violated(ranks, call, 9)
+        else:
+            call()
+            torch.cuda.synchronize()
+            out = [b.view[:-1].clone() for b in ranks.outs]
+        ranks.finish(wrote=steps != "forward")
+        return out
+
+    stats = [torch.full((rows, 2), 1.5, device="cuda") for _ in range(2)]
+    loss = [torch.full((rows,), 1.5, device="cuda") for _ in range(2)]
+    got, want = run(loss[0], stats[0], True), run(loss[1], stats[1], False)
+    for a, b in zip(got + [loss[0][:-1], stats[0][:-1]], want + [loss[1][:-1], stats[1][:-1]]):
+        assert torch.equal(bits(a), bits(b))
+    assert float(loss[0][-1]) == 1.5 and bool((stats[0][-1] == 1.5).all())
