@@ -232,7 +232,9 @@ CCL_API ccl_status_t ccl_set_launch(ccl_comm_t comm, int sm_budget, int variant,
  *                  checked build only; nothing otherwise) makes the TMA
  *                  producer's bounds check of its second tile fail, so that
  *                  the CCL_ERR_BOUNDS path is exercised: the tile's copies
- *                  are not made.  0 = off.
+ *                  are not made; and the operators on logits test their
+ *                  accesses against buffers and lists of one row less, so the
+ *                  last row's are not made.  0 = off.
  * Errors: CCL_ERR_INVALID_ARG for negative values or stall_test > 2. */
 CCL_API ccl_status_t ccl_comm_set_debug(ccl_comm_t comm, long long wait_limit_ns, int stall_test);
 

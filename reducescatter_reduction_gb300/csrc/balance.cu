@@ -52,8 +52,33 @@ struct BalanceArgs {
     float *loss;
     unsigned *ticket;
     double2 *partials;
+    // checked build:
     unsigned *status;
+    uint64_t held;                 // rows that every buffer and list has: `rows`, or one less where the debug hook wants the checks to fail
+    uint32_t cell_room;            // counters that `cells` has
 };
+
+// The accesses that the checked build tests: to a rank buffer of elements of S bytes, a row's choices, its padding byte, a counter.
+template <int PM>
+__device__ __forceinline__ bool balance_holds(const BalanceArgs<PM> &a, const void *buf, uint32_t S, const void *at, uint32_t bytes)
+{
+    return !kBoundsCheck || in_buffer(at, bytes, buf, a.held * a.experts * S, a.status, kSiteBalance);
+}
+template <int PM>
+__device__ __forceinline__ int balance_choice(const BalanceArgs<PM> &a, const int32_t *ids, uint64_t at)
+{
+    return in_bounds(at < a.held * a.k, a.status, kSiteBalance, at) ? ids[at] : -1;
+}
+template <int PM>
+__device__ __forceinline__ bool balance_valid(const BalanceArgs<PM> &a, const uint8_t *valid, uint64_t row)
+{
+    return in_bounds(row < a.held, a.status, kSiteBalance, row) && valid[row];
+}
+template <int PM>
+__device__ __forceinline__ bool balance_cell(const BalanceArgs<PM> &a, uint64_t cell)
+{
+    return in_bounds(cell < a.cell_room, a.status, kSiteBalance, cell);
+}
 
 // Counts the choices and valid rows of all ranks into cells, which are zero.
 // A CTA counts in shared memory first: integer atomics, so any order gives
@@ -81,8 +106,8 @@ __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const __gr
 #pragma unroll
         for (int b = 0; b < BATCH; ++b) {
             const uint64_t at = j + b * stride;
-            id[b] = at < n ? ids[at] : -1;
-            on[b] = at < n && (!a.has_valid || a.valid[r][div_by(uint32_t(at), a.by_k)]);
+            id[b] = at < n ? balance_choice(a, ids, at) : -1;
+            on[b] = at < n && (!a.has_valid || balance_valid(a, a.valid[r], div_by(uint32_t(at), a.by_k)));
         }
 #pragma unroll
         for (int b = 0; b < BATCH; ++b)
@@ -90,7 +115,7 @@ __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const __gr
     }
     if (a.has_valid) {
         int rows = 0;
-        for (uint64_t t = first; t < a.rows; t += stride) rows += a.valid[r][t] != 0;
+        for (uint64_t t = first; t < a.rows; t += stride) rows += balance_valid(a, a.valid[r], t);
         rows = __reduce_add_sync(0xffffffffu, rows);
         if (threadIdx.x % 32 == 0 && rows) atomicAdd(&a.cell_tokens[r], rows);
     } else if (blockIdx.x == 0 && threadIdx.x == 0) {
@@ -98,7 +123,7 @@ __global__ void __launch_bounds__(kCountThreads) balance_count_kernel(const __gr
     }
     __syncthreads();
     for (uint32_t e = threadIdx.x; e < a.experts; e += kCountThreads)
-        if (hist[e]) atomicAdd(&a.cells[uint64_t(r) * a.experts + e], hist[e]);
+        if (hist[e] && balance_cell(a, uint64_t(r) * a.experts + e)) atomicAdd(&a.cells[uint64_t(r) * a.experts + e], hist[e]);
 }
 
 // d_e into shared memory; returns where mean(a) is: in fp64, as the loss is
@@ -126,8 +151,8 @@ __device__ __forceinline__ const double *balance_coefficients(const BalanceArgs<
                 if (at >= all) continue;
                 rank[b] = div_by(at, a.by_choices);
                 const uint32_t j = at - rank[b] * n;
-                id[b] = a.ids[rank[b]][j];
-                if (a.has_valid && !a.valid[rank[b]][div_by(j, a.by_k)]) id[b] = -1;
+                id[b] = balance_choice(a, a.ids[rank[b]], j);
+                if (a.has_valid && !balance_valid(a, a.valid[rank[b]], div_by(j, a.by_k))) id[b] = -1;
             }
 #pragma unroll
             for (int b = 0; b < BATCH; ++b)
@@ -136,7 +161,7 @@ __device__ __forceinline__ const double *balance_coefficients(const BalanceArgs<
         if (a.has_valid) {
             for (uint32_t i = threadIdx.x; i < a.p * rows; i += kBalanceThreads) {
                 const uint32_t rank = div_by(i, a.by_rows);
-                if (a.valid[rank][i - rank * rows]) atomicAdd(&rows_s[rank], 1);
+                if (balance_valid(a, a.valid[rank], i - rank * rows)) atomicAdd(&rows_s[rank], 1);
             }
         } else {
             for (uint32_t r = threadIdx.x; r < a.p; r += kBalanceThreads) rows_s[r] = int(rows);
@@ -145,6 +170,10 @@ __device__ __forceinline__ const double *balance_coefficients(const BalanceArgs<
         tokens = rows_s;
     }
     __syncthreads();
+    auto count_of = [&](uint32_t r, uint32_t e) -> unsigned {
+        const uint64_t cell = uint64_t(r) * E + e;
+        return balance_cell(a, cell) ? unsigned(cells[cell]) : 0u;
+    };
     // sums of integers: any order gives the same
     const bool writes = a.cells != a.counts && blockIdx.x == 0 && blockIdx.y == 0;
     unsigned long long rows = 0, mine = 0, total = 0;    // total: of this thread's first expert
@@ -155,9 +184,9 @@ __device__ __forceinline__ const double *balance_coefficients(const BalanceArgs<
     for (uint32_t e = threadIdx.x; e < E; e += kBalanceThreads) {
         unsigned long long t = 0;
 #pragma unroll 8
-        for (uint32_t r = 0; r < a.p; ++r) t += unsigned(cells[uint64_t(r) * E + e]);
+        for (uint32_t r = 0; r < a.p; ++r) t += count_of(r, e);
         if (writes)
-            for (uint32_t r = 0; r < a.p; ++r) a.counts[uint64_t(r) * E + e] = cells[uint64_t(r) * E + e];
+            for (uint32_t r = 0; r < a.p; ++r) a.counts[uint64_t(r) * E + e] = int(count_of(r, e));
         if (e == threadIdx.x) total = t;
         mine += t;
     }
@@ -194,7 +223,7 @@ __device__ __forceinline__ const double *balance_coefficients(const BalanceArgs<
         unsigned long long t = total;
         if (e != threadIdx.x) {
             t = 0;
-            for (uint32_t r = 0; r < a.p; ++r) t += unsigned(cells[uint64_t(r) * E + e]);
+            for (uint32_t r = 0; r < a.p; ++r) t += count_of(r, e);
         }
         d_s[e] = float((long long)(t * E) - sum) * per;
     }
@@ -226,7 +255,7 @@ __device__ __forceinline__ void balance_finish(const BalanceArgs<PM> &a, float l
             s += red[0][w];
             c += red[1][w];
         }
-        a.partials[me] = make_double2(s, c);
+        if (in_bounds(me < kMaxPartials, a.status, kSiteBalance, me)) a.partials[me] = make_double2(s, c);
         __threadfence();
         last = atomicAdd(a.ticket, 1u) == grid - 1;
     }
@@ -234,7 +263,8 @@ __device__ __forceinline__ void balance_finish(const BalanceArgs<PM> &a, float l
     if (!last) return;
     __threadfence();
     if (a.cells != a.counts && !a.count_here) {
-        for (uint32_t i = threadIdx.x; i < a.p * a.experts; i += kBalanceThreads) a.cells[i] = 0;
+        for (uint32_t i = threadIdx.x; i < a.p * a.experts; i += kBalanceThreads)
+            if (balance_cell(a, i)) a.cells[i] = 0;
         for (uint32_t r = threadIdx.x; r < a.p; r += kBalanceThreads) a.cell_tokens[r] = 0;
     }
     s = c = 0.0;
@@ -293,11 +323,10 @@ __global__ void __launch_bounds__(kBalanceThreads, NV * Traits<T>::VEC > 16 ? 2 
     uint4 raw[NV];
     auto fetch = [&](uint64_t row, const char *from) {
         const bool in = row < a.rows;
-        on = in && (!valid || valid[row]);
+        on = in && (!valid || balance_valid(a, valid, row));
 #pragma unroll
         for (int n = 0; n < NV; ++n)
-            raw[n] = in && has[n] && in_bounds(uint32_t((n * L + l) * VEC) + VEC <= E, a.status, kSiteBalance, row) ? ld_coherent_v4(from + n * (L * 16))
-                                                                                                              : lowest_group<T>();
+            raw[n] = in && has[n] && balance_holds(a, a.in[r], S, from + n * (L * 16), 16) ? ld_coherent_v4(from + n * (L * 16)) : lowest_group<T>();
     };
     grid_dependency_wait();
     grid_dependents_launch();
@@ -362,7 +391,7 @@ __global__ void __launch_bounds__(kBalanceThreads, NV * Traits<T>::VEC > 16 ? 2 
             const Pair g = {inv * up, inv * up}, off = {-lean, -lean};
 #pragma unroll
             for (int n = 0; n < NV; ++n) {
-                if (!has[n] || !in_bounds(uint32_t((n * L + l) * VEC) + VEC <= E, a.status, kSiteBalance, t)) continue;
+                if (!has[n] || !balance_holds(a, a.out[r], S, at + to_out + n * (L * 16), 16)) continue;
                 Pair f[PAIRS];
 #pragma unroll
                 for (int i = 0; i < PAIRS; ++i) f[i] = (x[n * PAIRS + i] * (d[n * PAIRS + i] + off)) * g;
@@ -458,12 +487,13 @@ __global__ void __launch_bounds__(kBalanceThreads, kOddCtas<NE>) balance_odd_ker
             if (lo >= in && lo + (n + 15) / 16 * 16 <= in_end) {
 #pragma unroll 1
                 for (uint32_t g = lane * 16; g < n; g += 512)
-                    if (in_bounds(g + 16 <= span, a.status, kSiteBalance, row))
+                    if (in_bounds(g + 16 <= span, a.status, kSiteBalance, row) && balance_holds(a, a.in[r], S, reinterpret_cast<const void *>(lo + g), 16))
                         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to32 + g), "l"(lo + g) : "memory");
             } else {      // the first or last group of the buffer is not all of it
 #pragma unroll 1
                 for (uint32_t g = lane * S; g < n; g += 32 * S)
-                    if (lo + g >= in && in_bounds(g + S <= span, a.status, kSiteBalance, row))
+                    if (lo + g >= in && in_bounds(g + S <= span, a.status, kSiteBalance, row) &&
+                        balance_holds(a, a.in[r], S, reinterpret_cast<const void *>(lo + g), S))
                         Tr::store1(to + g, 0, Tr::load1(reinterpret_cast<const void *>(lo + g), 0));
             }
         }
@@ -473,7 +503,7 @@ __global__ void __launch_bounds__(kBalanceThreads, kOddCtas<NE>) balance_odd_ker
     grid_dependents_launch();
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i) fetch(t + i * stride, i);
-    auto is_on = [&](uint64_t row) { return row < a.rows && (!valid || valid[row]); };
+    auto is_on = [&](uint64_t row) { return row < a.rows && (!valid || balance_valid(a, valid, row)); };
     bool coming = is_on(t + mine);
     const double *mean = balance_coefficients(a, d_s, reinterpret_cast<int *>(d_s + E));
     Pair d[PAIRS];
@@ -561,9 +591,11 @@ __global__ void __launch_bounds__(kBalanceThreads, kOddCtas<NE>) balance_odd_ker
             if (!in_bounds(o1 - low <= span, a.status, kSiteBalance, t)) continue;
             const uint32_t skip = uint32_t(first - low), whole = last > first ? uint32_t(last - first) : 0u, out32 = smem_addr(out_s) + skip;
 #pragma unroll 1
-            for (uint32_t g = lane * 16; g < whole; g += 512) st_stream_v4(reinterpret_cast<void *>(first + g), lds_v4(out32 + g));
+            for (uint32_t g = lane * 16; g < whole; g += 512)
+                if (balance_holds(a, a.out[r], S, reinterpret_cast<const void *>(first + g), 16))
+                    st_stream_v4(reinterpret_cast<void *>(first + g), lds_v4(out32 + g));
             const uintptr_t edge = lane < 8 ? o0 + lane * S : tail + (lane - 8) * S;     // at most seven before, and seven after
-            if (lane < 16 && edge < (lane < 8 ? head : o1))
+            if (lane < 16 && edge < (lane < 8 ? head : o1) && balance_holds(a, a.out[r], S, reinterpret_cast<const void *>(edge), S))
                 Tr::store1(reinterpret_cast<void *>(edge), 0, Tr::load1(out_s + (edge - low), 0));
         }
     }
@@ -589,22 +621,27 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_any_kernel(const __gr
     int live = 0;
     for (uint64_t t = uint64_t(blockIdx.x) * kBalanceWarps + warp; t < a.rows; t += uint64_t(gridDim.x) * kBalanceWarps) {
         const uint64_t at = t * E;
-        const bool valid = !a.has_valid || a.valid[r][t];
+        constexpr uint32_t S = 16 / Tr::VEC;
+        auto load = [&](uint32_t e) -> float {
+            return balance_holds(a, a.in[r], S, static_cast<const char *>(a.in[r]) + (at + e) * S, S) ? Tr::load1(a.in[r], at + e) : -INFINITY;
+        };
+        auto store = [&](uint32_t e, float v) {
+            if (balance_holds(a, a.out[r], S, static_cast<const char *>(a.out[r]) + (at + e) * S, S)) Tr::store1(a.out[r], at + e, v);
+        };
+        const bool valid = !a.has_valid || balance_valid(a, a.valid[r], t);
         if (!valid) {
             if (bwd)
-                for (uint32_t e = lane; e < E; e += 32)
-                    if (in_bounds(t < a.rows, a.status, kSiteBalance, t)) Tr::store1(a.out[r], at + e, 0.0f);
+                for (uint32_t e = lane; e < E; e += 32) store(e, 0.0f);
             continue;
         }
         float m = -INFINITY;
-        for (uint32_t e = lane; e < E; e += 32)
-            if (in_bounds(t < a.rows, a.status, kSiteBalance, t)) m = fmaxf(m, Tr::load1(a.in[r], at + e));
+        for (uint32_t e = lane; e < E; e += 32) m = fmaxf(m, load(e));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         m = m == -INFINITY ? 0.0f : m;
         float s = 0.0f, dot = 0.0f;
         for (uint32_t e = lane; e < E; e += 32) {
-            const float v = ex2((Tr::load1(a.in[r], at + e) - m) * kLog2e);
+            const float v = ex2((load(e) - m) * kLog2e);
             s += v;
             dot = fmaf(v, d_s[e], dot);
         }
@@ -622,8 +659,8 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_any_kernel(const __gr
         if (bwd) {
             const float g = inv * up;
             for (uint32_t e = lane; e < E; e += 32) {
-                const float v = ex2((Tr::load1(a.in[r], at + e) - m) * kLog2e);
-                Tr::store1(a.out[r], at + e, v * (d_s[e] - lean) * g);
+                const float v = ex2((load(e) - m) * kLog2e);
+                store(e, v * (d_s[e] - lean) * g);
             }
         }
     }
@@ -680,7 +717,9 @@ static cudaError_t balance_shape(const Launch &L, const BalanceLaunch &N, Launch
         a.cells = reinterpret_cast<int32_t *>(a.partials + kMaxPartials);
         a.cell_tokens = a.cells + kScratchCells;
     }
+    a.cell_room = scratch ? kScratchCells : uint32_t(cells);
     a.status = L.status;
+    a.held = N.rows - (L.stall_test == 2 && N.rows ? 1 : 0);
     cudaError_t err = cudaSuccess;
     info->kernels = 0;
     void (*kern)(BalanceArgs<PM>) = balance_any_kernel<T, PM>;

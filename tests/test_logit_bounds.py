@@ -104,3 +104,29 @@ def test_distillation(steps, layout, p, rows, vocab, k):
     for a, b in zip(got + [loss[0][:-1], stats[0][:-1]], want + [loss[1][:-1], stats[1][:-1]]):
         assert torch.equal(bits(a), bits(b))
     assert float(loss[0][-1]) == 1.5 and bool((stats[0][-1] == 1.5).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("steps", ["forward", "backward", "both"])
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("p,rows,E,k", [(2, 20, 64, 4), (8, 3000, 64, 6), (2, 50, 61, 3), (3, 4000, 33, 2), (1, 40, 700, 2), (2, 30, 1500, 4)])
+@pytest.mark.parametrize("padded", [False, True])
+def test_balance_loss(dtype, steps, layout, p, rows, E, k, padded):
+    """(All rows' gradients hang on the last row's choices: that it is recorded and left alone is what is tested.)"""
+    g = rng(E)
+    ranks = Ranks([torch.from_numpy(g.normal(0, 2, (rows, E))).cuda() for _ in range(p)], dtype, **layout)
+    ids = [torch.from_numpy(g.integers(0, E, (rows, k)).astype(np.int32)).cuda() for _ in range(p)]
+    valid = [torch.ones(rows, dtype=torch.uint8, device="cuda") for _ in range(p)]
+    counts, tokens = torch.ones(p, E, dtype=torch.int32, device="cuda"), torch.full((p,), rows, dtype=torch.int32, device="cuda")
+    loss = torch.empty(1, device="cuda")
+    call = lambda: ccl.ccl_balance_loss(ranks.comm, dtype, steps, rows, E, k, [t.data_ptr() for t in ids],
+                                        [t.data_ptr() for t in valid] if padded else None, 0.01, 0, counts.data_ptr(), tokens.data_ptr(),
+                                        loss.data_ptr(), stream=stream())
+    violated(ranks, call, 10)
+    if steps != "backward":
+        assert int(counts.sum()) == p * (rows - 1) * k and tokens.tolist() == [rows - 1 if padded else rows] * p
+    call()
+    ccl.ccl_comm_check(ranks.comm)
+    if steps != "backward":
+        assert int(counts.sum()) == p * rows * k and tokens.tolist() == [rows] * p
+    ranks.finish(wrote=steps != "forward")
