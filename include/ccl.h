@@ -341,7 +341,9 @@ CCL_API ccl_status_t ccl_allreduce_residual_rmsnorm(ccl_comm_t comm, ccl_dtype_t
  * hold the columns of balanced chunk r of vocab (see "Schedules" above: the
  * larger chunks first) of [rows, vocab] logits, row-major.  ld is the row
  * stride of every rank buffer in elements, at least the widest chunk; 0: each
- * rank's rows are contiguous.  vocab <= 2^30.
+ * rank's rows are contiguous.  The rows of buffers may lie between one
+ * another's (the ranks' columns of one matrix): only the elements may not
+ * overlap.  vocab <= 2^30.
  * ------------------------------------------------------------------------- */
 
 /* What a decode step does to its logits.  Device arrays; a NULL array (or a

@@ -38,29 +38,49 @@ static ccl_status_t check_aligned(const void *p, size_t to, const char *name)
     return CCL_OK;
 }
 
-// Rank buffers of extent[r] bytes: aligned to their elements; where the call
-// writes the outputs, each is its own rank's input or disjoint from every
-// input and every other output.  What the call writes beside them overlaps
-// nothing, and nothing it reads overlaps an output.  *alias: every output that
-// has elements is its rank's input; where that holds for some ranks alone, a
-// kernel has to write all of each output.
-static ccl_status_t check_buffers(const ccl_comm *c, const uint64_t *extent, size_t es, bool outputs, const Aux *aux, int n_aux,
+// A rank buffer: `rows` pieces of `width` bytes, `stride` bytes apart; bytes from the first to the last of them.
+struct Shape {
+    uint64_t rows = 0, width = 0, stride = 0;
+    uint64_t extent() const { return rows && width ? (rows - 1) * stride + width : 0; }
+};
+
+// Whether two buffers have a byte in common.  Rows of one stride may lie
+// between one another's, as the columns of one matrix do.
+static bool meet(const void *pa, const Shape &a, const void *pb, const Shape &b)
+{
+    if (!overlap(range_of(pa, a.extent()), range_of(pb, b.extent()))) return false;
+    if (a.rows != b.rows || a.stride != b.stride || a.rows < 2) return true;
+    // b's row i + k begins d + k stride behind a's row i: the least k for which it ends behind the latter's begin
+    const int64_t d = int64_t(uintptr_t(pb) - uintptr_t(pa)), s = int64_t(a.stride), last = int64_t(a.rows) - 1;
+    const int64_t n = -int64_t(b.width) - d;
+    int64_t k = n / s - (n % s < 0 ? 1 : 0) + 1;
+    if (k < -last) k = -last;
+    return k <= last && d + k * s < int64_t(a.width);
+}
+
+// Rank buffers: aligned to their elements; where the call writes the outputs,
+// each is its own rank's input or disjoint from every input and every other
+// output.  What the call writes beside them overlaps nothing, and nothing it
+// reads overlaps an output.  *alias: every output that has elements is its
+// rank's input; where that holds for some ranks alone, a kernel has to write
+// all of each output.
+static ccl_status_t check_buffers(const ccl_comm *c, const Shape *shape, size_t es, bool outputs, const Aux *aux, int n_aux,
                                   bool *alias)
 {
     const int p = c->p;
+    uint64_t extent[kMaxRanks];
     *alias = outputs;
     for (int r = 0; r < p; ++r) {
+        extent[r] = shape[r].extent();
         if (extent[r] && c->out[r] != c->in[r]) *alias = false;
         if (uintptr_t(c->in[r]) % es || (outputs && uintptr_t(c->out[r]) % es))
             return fail(CCL_ERR_INVALID_ARG, "a buffer of rank %d is not aligned to its elements (%zu bytes)", r, es);
     }
     for (int k = 0; outputs && k < p; ++k) {
-        const Range out = range_of(c->out[k], extent[k]);
         for (int j = 0; j < p; ++j) {
-            if (j > k && overlap(out, range_of(c->out[j], extent[j])))
+            if (j > k && meet(c->out[k], shape[k], c->out[j], shape[j]))
                 return fail(CCL_ERR_INVALID_ARG, "outputs of ranks %d and %d overlap", k, j);
-            if (!overlap(out, range_of(c->in[j], extent[j]))) continue;
-            if (j != k || c->out[k] != c->in[k])
+            if ((j != k || c->out[k] != c->in[k]) && meet(c->out[k], shape[k], c->in[j], shape[j]))
                 return fail(CCL_ERR_INVALID_ARG, "output of rank %d overlaps the input of rank %d", k, j);
         }
     }
@@ -78,8 +98,8 @@ static ccl_status_t check_buffers(const ccl_comm *c, const uint64_t *extent, siz
     return CCL_OK;
 }
 
-// [rows, vocab] logits over the ranks' shards: the extent of each shard.
-static ccl_status_t shard_extents(const ccl_comm *c, size_t rows, size_t vocab, size_t ld, size_t es, uint64_t *extent)
+// [rows, vocab] logits over the ranks' shards: the shape of each shard.
+static ccl_status_t shard_shapes(const ccl_comm *c, size_t rows, size_t vocab, size_t ld, size_t es, Shape *shape)
 {
     if (vocab == 0 || vocab > (size_t(1) << 30)) return fail(CCL_ERR_INVALID_ARG, "vocab %zu outside [1, 2^30]", vocab);
     if (rows > 0x7fffffffull) return fail(CCL_ERR_INVALID_ARG, "rows %zu above 2^31 - 1", rows);
@@ -89,8 +109,8 @@ static ccl_status_t shard_extents(const ccl_comm *c, size_t rows, size_t vocab, 
     const uint64_t widest = ld ? ld : bound[1];
     if (rows && widest > (SIZE_MAX / 4) / rows / es) return fail(CCL_ERR_INVALID_ARG, "rows * columns too large");
     for (int r = 0; r < c->p; ++r) {
-        const uint64_t w = bound[r + 1] - bound[r], stride = ld ? ld : w;
-        extent[r] = rows && w ? ((rows - 1) * stride + w) * es : 0;
+        const uint64_t w = bound[r + 1] - bound[r];
+        shape[r] = {rows, w * es, (ld ? ld : w) * es};
     }
     return CCL_OK;
 }
@@ -132,9 +152,9 @@ extern "C" ccl_status_t ccl_logit_rules(ccl_comm_t c, ccl_dtype_t dtype, size_t 
     ccl_status_t st = check_floats(c, dtype, "ccl_logit_rules");
     if (st != CCL_OK) return st;
     if (!rules) return fail(CCL_ERR_INVALID_ARG, "rules is NULL");
-    uint64_t extent[kMaxRanks];
+    Shape shape[kMaxRanks];
     const size_t es = elem_bytes(dtype);
-    st = shard_extents(c, rows, vocab, ld, es, extent);
+    st = shard_shapes(c, rows, vocab, ld, es, shape);
     if (st != CCL_OK) return st;
     if (rows == 0) return CCL_OK;
     ccl_logit_rules_t r = *rules;
@@ -167,7 +187,7 @@ extern "C" ccl_status_t ccl_logit_rules(ccl_comm_t c, ccl_dtype_t dtype, size_t 
     for (const Aux &a : aux)
         if (a.at.lo % 4) return fail(CCL_ERR_INVALID_ARG, "%s is not aligned to its elements (4 bytes)", a.name);
     bool alias = false;
-    st = check_buffers(c, extent, es, true, aux, int(sizeof aux / sizeof aux[0]), &alias);
+    st = check_buffers(c, shape, es, true, aux, int(sizeof aux / sizeof aux[0]), &alias);
     if (st != CCL_OK) return st;
     DeviceGuard g(c->device);
     if (g.err != cudaSuccess) return cuda_fail(g.err, "logit_rules");
@@ -196,9 +216,9 @@ extern "C" ccl_status_t ccl_distill_topk(ccl_comm_t c, ccl_dtype_t dtype, ccl_pa
         return fail(CCL_ERR_INVALID_ARG, "temperature %g below 4.25e-39: its reciprocal leaves fp32's range", double(temperature));
     if (k == 0) return fail(CCL_ERR_INVALID_ARG, "k must be positive");
     if (k > 1024) return fail(CCL_ERR_UNSUPPORTED, "k=%zu above 1024 teacher entries a row", k);
-    uint64_t extent[kMaxRanks];
+    Shape shape[kMaxRanks];
     const size_t es = elem_bytes(dtype), ts = elem_bytes(teacher_dtype);
-    st = shard_extents(c, rows, vocab, ld, es, extent);
+    st = shard_shapes(c, rows, vocab, ld, es, shape);
     if (st != CCL_OK) return st;
     if (rows == 0) return CCL_OK;
     const bool fwd = pass & CCL_PASS_FORWARD, bwd = pass & CCL_PASS_BACKWARD;
@@ -217,7 +237,7 @@ extern "C" ccl_status_t ccl_distill_topk(ccl_comm_t c, ccl_dtype_t dtype, ccl_pa
     for (int i = 0; i < 5; ++i)
         if ((st = check_aligned(reinterpret_cast<const void *>(aux[i].at.lo), i == 1 ? ts : 4, aux[i].name)) != CCL_OK) return st;
     bool alias = false;
-    st = check_buffers(c, extent, es, bwd, aux, 5, &alias);
+    st = check_buffers(c, shape, es, bwd, aux, 5, &alias);
     if (st != CCL_OK) return st;
     DeviceGuard g(c->device);
     if (g.err != cudaSuccess) return cuda_fail(g.err, "distill_topk");
@@ -279,10 +299,10 @@ extern "C" ccl_status_t ccl_balance_loss(ccl_comm_t c, ccl_dtype_t dtype, ccl_pa
     }
     for (int i = 0; i < n; ++i)
         if (aux[i].name[0] != 'v' && (st = check_aligned(reinterpret_cast<const void *>(aux[i].at.lo), 4, aux[i].name)) != CCL_OK) return st;
-    uint64_t extent[kMaxRanks];
-    for (int r = 0; r < p; ++r) extent[r] = uint64_t(rows) * experts * es;
+    Shape shape[kMaxRanks];
+    for (int r = 0; r < p; ++r) shape[r] = {rows, experts * es, experts * es};
     bool alias = false;
-    st = check_buffers(c, extent, es, bwd, aux, n, &alias);
+    st = check_buffers(c, shape, es, bwd, aux, n, &alias);
     if (st != CCL_OK) return st;
     DeviceGuard g(c->device);
     if (g.err != cudaSuccess) return cuda_fail(g.err, "balance_loss");
