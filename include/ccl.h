@@ -377,7 +377,8 @@ typedef struct {
  * A row that its mask leaves nothing is all -inf.
  * Bytes moved: rows * vocab * s read and written, the history and the lists.
  * Errors: CCL_ERR_INVALID_ARG (NULL rules, a size out of range, a missing
- * array, overlap), CCL_ERR_UNSUPPORTED, CCL_ERR_CUDA. */
+ * array, overlap), CCL_ERR_UNSUPPORTED (int32, or above 2^31 - 1 pieces of
+ * rows: a rank's part of a row is one, or one per 32 KB), CCL_ERR_CUDA. */
 CCL_API ccl_status_t ccl_logit_rules(ccl_comm_t comm, ccl_dtype_t dtype, size_t rows, size_t vocab, size_t ld,
                                      const ccl_logit_rules_t *rules, void *stream);
 
@@ -412,7 +413,9 @@ typedef enum { CCL_PASS_FORWARD = 1, CCL_PASS_BACKWARD = 2, CCL_PASS_BOTH = 3 } 
  * return CCL_ERR_TIMEOUT (the outputs are then incomplete).
  * Errors: CCL_ERR_INVALID_ARG (a size, pass or temperature out of range --
  * temperatures are from 4.25e-39 to 3e38 --, a missing array, overlap),
- * CCL_ERR_UNSUPPORTED (int32, k > 1024), CCL_ERR_CUDA. */
+ * CCL_ERR_UNSUPPORTED (int32, k > 1024, or above 2^31 - 1 pieces of rows: a
+ * row has at most 16, the gradient alone one per rank, or per 32 KB of it),
+ * CCL_ERR_CUDA. */
 CCL_API ccl_status_t ccl_distill_topk(ccl_comm_t comm, ccl_dtype_t dtype, ccl_pass_t pass, size_t rows, size_t vocab,
                                       size_t ld, size_t k, const int32_t *teacher_ids, const void *teacher_logits,
                                       ccl_dtype_t teacher_dtype, float temperature, const float *row_weight,

@@ -1038,7 +1038,7 @@ static cudaError_t distill_held(const Launch &L, const DistillLaunch &N, LaunchI
         a.span = uint32_t(span);
         break;
     }
-    if (N.rows * a.pieces > 0x7fffffffull) return cudaErrorInvalidValue;
+    if (N.rows * a.pieces > 0x7fffffffull) return kTooManyPieces;
     a.items = uint32_t(N.rows * a.pieces);
     a.by_pieces = fast_div(a.pieces);
     a.by_parts = fast_div(a.parts);

@@ -251,6 +251,10 @@ struct NormLaunch {
 };
 cudaError_t launch_allreduce_rmsnorm(const Launch &L, const NormLaunch &N, LaunchInfo *info);
 
+// What a launcher returns, nothing having been launched, for more pieces of
+// rows than one launch numbers.
+constexpr cudaError_t kTooManyPieces = cudaErrorNotSupported;
+
 // The logit operators (logit_rules.cu, distill.cu, balance.cu).  L.alias:
 // every rank's output is its input.
 struct RulesLaunch {

@@ -388,7 +388,7 @@ static cudaError_t rules_launch(const Launch &L, RulesArgs<PM> &a, uint32_t grou
     const size_t smem = counters + (a.in_place ? 0 : staged);
     a.slices = groups ? (groups + GROUPS - 1) / GROUPS : 1;
     const uint64_t per_row = uint64_t(a.slices) * a.s.p;
-    if (a.s.rows * per_row > 0x7fffffffull) return cudaErrorInvalidValue;
+    if (a.s.rows * per_row > 0x7fffffffull) return kTooManyPieces;
     a.by_row = fast_div(uint32_t(per_row));
     a.by_slices = fast_div(a.slices);
     static std::atomic<unsigned long long> done{0};

@@ -137,6 +137,8 @@ static Launch make_launch(ccl_comm *c, int dtype, bool alias, void *stream)
 static ccl_status_t finish(ccl_comm *c, cudaError_t err, const LaunchInfo &info, int dtype, size_t rows, size_t cols, const char *what,
                            const char *pass)
 {
+    if (err == kTooManyPieces && info.kernels == 0)
+        return fail(CCL_ERR_UNSUPPORTED, "%s: %zu rows of %zu columns over %d ranks are more than 2^31 - 1 pieces", what, rows, cols, c->p);
     c->launches += uint64_t(info.kernels);
     snprintf(c->last, sizeof c->last, "%s dtype=%s p=%d rows=%zu columns=%zu pass=%s grid=%d block=%d smem=%zu kernels=%d", info.kernel,
              kDtypeName[dtype], c->p, rows, cols, pass, info.grid, info.block, info.smem, info.kernels);
