@@ -7,8 +7,8 @@
 //   dx_te = dloss p_te (a_e - sum_j p_tj a_j),  a_e = coef E count_e / (k N^2)
 // Both need the counts only as a_e, so once the choices are counted one pass
 // over the logits gives loss = sum_t sum_e p_te a_e and the gradient together.
-// Differences of nearly equal a_e make the gradient: they are formed from the
-// integer counts in fp64 as d_e = a_e - mean(a) before fp32 sees them;
+// Differences of nearly equal a_e make the gradient: d_e = a_e - mean(a) is
+// formed from the integer counts and rounded to fp32 once;
 // p_te (d_e - sum_j p_tj d_j) is the same gradient, and the loss is
 // mean(a) (rows with a softmax) + sum_t sum_e p_te d_e.
 #include "async.cuh"
@@ -206,18 +206,21 @@ __device__ __forceinline__ const double *balance_coefficients(const BalanceArgs<
         all_rows += parts[0][w];
         all += parts[1][w];
     }
-    // One thread divides in fp64 (which this GPU does slowly): a_e = count_e scale, d_e = (E count_e - sum) scale / E.
-    // The difference is exact in 64-bit integers and is rounded once to fp32, its product with the scale a second time.
-    __shared__ float scale_s;
+    // a_e = count_e scale, d_e = (E count_e - sum) scale / E.  The difference is exact in 64-bit integers; it and scale / E are
+    // taken as a sum of two fp32 values each, so that d_e is rounded once.  scale / E = coef / (k n^2) comes by products whose
+    // roundings are kept (fma), a quotient and what it leaves: fp64, which this GPU does slowly, is for the mean alone.
+    __shared__ float scale_s[2];
     __shared__ double mean_s;
     if (threadIdx.x == 0) {
-        const double n = double(all_rows);
-        const double per = all_rows ? a.coef / (double(a.k) * n * n) : 0.0;     // scale / E
-        scale_s = float(per);
-        mean_s = double(all) * per;
+        const float k = float(a.k), n = float(all_rows), n_rest = float((long long)(all_rows - (unsigned long long)n));
+        const float nn = __fmul_rn(n, n), nn_rest = fmaf(n, n, -nn) + 2.0f * n * n_rest;
+        const float by = __fmul_rn(nn, k), by_rest = fmaf(nn, k, -by) + nn_rest * k;
+        const float coef = float(a.coef), hi = all_rows ? __fdiv_rn(coef, by) : 0.0f;
+        scale_s[0] = hi;
+        scale_s[1] = all_rows ? __fdiv_rn(fmaf(-hi, by_rest, fmaf(-hi, by, coef)), by) : 0.0f;
     }
     __syncthreads();
-    const float per = scale_s;
+    const float per = scale_s[0], per_rest = scale_s[1];
     const long long sum = (long long)all;
     for (uint32_t e = threadIdx.x; e < E; e += kBalanceThreads) {
         unsigned long long t = total;
@@ -225,9 +228,15 @@ __device__ __forceinline__ const double *balance_coefficients(const BalanceArgs<
             t = 0;
             for (uint32_t r = 0; r < a.p; ++r) t += count_of(r, e);
         }
-        d_s[e] = float((long long)(t * E) - sum) * per;
+        const long long off = (long long)(t * E) - sum;
+        const float hi = float(off), lo = fabsf(hi) < 16777216.0f ? 0.0f : float(off - (long long)hi);
+        d_s[e] = fmaf(hi, per, fmaf(hi, per_rest, lo * per));
     }
     __syncthreads();
+    if (threadIdx.x == kBalanceThreads - 1 && a.pass != CCL_PASS_BACKWARD) {    // (read at the end, behind other barriers)
+        const double n = double(all_rows);
+        mean_s = all_rows ? double(all) * (a.coef / (double(a.k) * n * n)) : 0.0;
+    }
     return &mean_s;
 }
 

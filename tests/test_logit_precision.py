@@ -152,3 +152,29 @@ def test_the_teachers_softmax_divides_once(steps):
     ranks.finish()
     want = np.where(ids.cpu().numpy() >= 0, -(np.float32(1) / np.arange(1, rows + 1, dtype=np.float32))[:, None], np.float32(0))
     assert np.array_equal(got, want), f"{int((got != want).any(1).sum())} rows"
+
+
+def test_differences_of_the_counts_are_rounded_once():
+    """Two experts, equal logits, counts given: the gradient is half of d_e = coef (2 count_e - n) / n^2, the other's with the
+    other sign, so what is seen is d_e itself: the fp64 value rounded to fp32."""
+    g = rng(5)
+    x = torch.zeros(1, 2, device="cuda")
+    y = torch.empty_like(x)
+    comm = ccl.ccl_comm_create(1, [x.data_ptr()])
+    ccl.ccl_comm_set_outputs(comm, [y.data_ptr()])
+    got, want = [], []
+    for _ in range(300):
+        n = int(2 ** g.uniform(1, 30.9))
+        c0 = int(g.integers(0, n + 1))
+        coef = float(np.float32(10 ** g.uniform(-4, 1)))
+        counts = torch.tensor([c0, n - c0], dtype=torch.int32, device="cuda")
+        tokens = torch.tensor([n], dtype=torch.int32, device="cuda")
+        ccl.ccl_balance_loss(comm, "f32", "backward", 1, 2, 1, None, None, coef, 0, counts.data_ptr(), tokens.data_ptr(), 0, stream=stream())
+        got.append(2 * y[0].cpu().numpy())
+        d = (2 * c0 - n) * (coef / float(n) ** 2)
+        want.append(np.array([d, -d]).astype(np.float32))
+    ccl.ccl_comm_destroy(comm)
+    got, want = np.stack(got), np.stack(want)
+    # (fp64's own roundings may turn a tie: one in 2^27)
+    off = got != want
+    assert off.sum() == 0, f"{int(off.any(1).sum())} of 300, by up to {float(np.abs(got / want - 1)[off].max() * 2 ** 24):.2f} u"
