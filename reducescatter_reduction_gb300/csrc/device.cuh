@@ -39,9 +39,6 @@ enum BoundsSite : unsigned {
     kSiteGather = 5,        // AllGather kernel
     kSiteBulkred = 6,       // bulk-reduce kernel
     kSiteNorm = 7,          // fused AllReduce + residual + RMSNorm
-    kSiteRules = 8,         // logit rules
-    kSiteDistill = 9,       // top-K distillation
-    kSiteBalance = 10,      // router balance loss
 };
 
 __device__ __forceinline__ bool in_bounds(bool ok, unsigned *status, unsigned site, uint64_t index)
@@ -61,14 +58,6 @@ __device__ __forceinline__ bool in_bounds(bool ok, unsigned *status, unsigned si
         }
         return false;
     }
-}
-
-// The same for an access to [at, at + bytes) of the buffer of `size` bytes that begins at `buf`.
-__device__ __forceinline__ bool in_buffer(const void *at, uint64_t bytes, const void *buf, uint64_t size, unsigned *status, unsigned site)
-{
-    if constexpr (!kBoundsCheck) return true;
-    const uint64_t from = uintptr_t(at) - uintptr_t(buf);       // (huge in front of it)
-    return in_bounds(from <= size && bytes <= size - from, status, site, from);
 }
 
 // ---------------------------------------------------------------------------

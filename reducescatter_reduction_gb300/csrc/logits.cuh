@@ -16,6 +16,17 @@
 
 namespace ccl {
 
+// Sites of the checked build's record (after BoundsSite).
+constexpr unsigned kSiteRules = 8, kSiteDistill = 9, kSiteBalance = 10;
+
+// in_bounds for an access to [at, at + bytes) of the buffer of `size` bytes that begins at `buf`.
+__device__ __forceinline__ bool in_buffer(const void *at, uint64_t bytes, const void *buf, uint64_t size, unsigned *status, unsigned site)
+{
+    if constexpr (!kBoundsCheck) return true;
+    const uint64_t from = uintptr_t(at) - uintptr_t(buf);       // (huge in front of it)
+    return in_bounds(from <= size && bytes <= size - from, status, site, from);
+}
+
 // n / d for n < 2^31 by a multiplication.
 struct FastDiv {
     uint32_t d, mul, shift;
