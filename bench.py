@@ -1117,6 +1117,16 @@ def run_single(args, dist: Dist, p: int, n: int, mode: dict) -> int:
     return 0
 
 
+def result_line(res) -> str:
+    """The one JSON line of a run.  What reads it may keep no more than its last 16 KB, and a line without its beginning is no
+    result: the tables' rows go without the launch descriptions, which were a third of it (`CCL_DEBUG=1` logs them)."""
+    def short(x):
+        if isinstance(x, dict):
+            return {k: short(v) for k, v in x.items() if k != "launch"}
+        return [short(v) for v in x] if isinstance(x, list) else x
+    return json.dumps({k: v if k == "config" else short(v) for k, v in res.items()}, separators=(",", ":"))
+
+
 def main(argv=None):
     args = parse_args(argv)
     dist = Dist()
@@ -1205,7 +1215,7 @@ def main(argv=None):
     else:
         res = run_ours(args, dist)
     if dist.rank == 0 and res is not None:
-        print(json.dumps(res), flush=True)
+        print(result_line(res), flush=True)
     return 0
 
 
