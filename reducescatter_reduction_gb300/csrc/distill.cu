@@ -485,7 +485,9 @@ __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::cta
                 ok = ok && __all_sync(0xffffffffu, distill_wait(a, sh, &sh.taught[slot], parity, 7, row_item));
                 if (!ok) break;
                 const uint32_t row = div_by(row_item, a.by_pieces);
-                const float tinv = 1.0f / sh.teacher_sum[slot];     // while the consumers store
+                // 1 / the teacher's sum, which is 1 or more: the approximate reciprocal and a step of Newton's iteration, right to
+                // half an ulp.  Measured (2048 x 80768 bf16 on 8 ranks): 208 us, with a division in its place 218.
+                const float tsum = sh.teacher_sum[slot], approx = __fdividef(1.0f, tsum), tinv = fmaf(fmaf(-tsum, approx, 1.0f), approx, approx);
                 ok = __all_sync(0xffffffffu, distill_wait(a, sh, &sh.stored[slot], parity, 7, row_item));
                 if (!ok) break;
                 const float row_m = sh.used_max[slot], inv = sh.used_inv[slot];
