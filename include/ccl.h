@@ -85,7 +85,8 @@
  * them on one stream, or order the streams.  On large messages the TMA
  * variants and the SM-budget ld/st kernel hand out work from counters in the
  * communicator's status block, so two collectives of one communicator
- * running at the same time would share them.  Different
+ * running at the same time would share them, as two calls of the balance loss
+ * would share its counts and sums.  Different
  * communicators are independent.  ccl_last_error() is per host thread.
  */
 #ifndef CCL_H

@@ -24,7 +24,7 @@ constexpr int kCountThreads = 1024;
 // Up to this many choices and counters in all, every CTA counts for itself
 // instead of waiting for a counting kernel: one launch less.  Measured (8
 // ranks, 64 bf16 experts, 6 choices; graph replay, us; counting here against
-// the kernel): 3072 choices 8.0, 8.7; 8160 9.6, 9.1; 16320 12.1, 9.0.  Called
+// the kernel): 3072 choices 7.6, 8.6; 8160 9.1, 9.1; 16320 11.7, 9.1.  Called
 // one by one, the second launch costs the host about 3 us more.
 constexpr uint64_t kCountHereIds = 8192;
 constexpr uint64_t kCountHereCells = 4096;
@@ -307,8 +307,8 @@ __device__ __forceinline__ void balance_finish(const BalanceArgs<PM> &a, float l
 // a lane hold the whole row, so the logits are read once and the next row's
 // are on their way meanwhile; L is as small as holds the row, for fewer
 // shuffles.  Bound by memory and about 12 us of launches, counting and the
-// last CTA's sum: 8 x 16384 x 256 bf16, loss and gradient, 32.6 us (4.2 TB/s
-// in all); f32, 4 x 65536 x 128, the loss, 30.8 us (4.4 TB/s).
+// last CTA's sum: 8 x 16384 x 256 bf16, loss and gradient, 32.9 us (4.2 TB/s
+// in all); f32, 4 x 65536 x 128, the loss, 30.9 us (4.4 TB/s).
 template <typename T, int PM, int L, int NV>
 __global__ void __launch_bounds__(kBalanceThreads, NV * Traits<T>::VEC > 16 ? 2 : NV > 2 ? 3 : 4) balance_kernel(const __grid_constant__ BalanceArgs<PM> a)
 {
@@ -416,11 +416,12 @@ __global__ void __launch_bounds__(kBalanceThreads, NV * Traits<T>::VEC > 16 ? 2 
 // brings the groups that hold them into shared memory asynchronously, STAGES
 // - 1 steps ahead, and its lanes read their elements l, l + L, ... from there;
 // the gradient goes back the same way, whole groups and a few edge elements.
-// Bound by instructions, element by element: 8 x 60000 x 60 bf16 50 us, 8 x
-// 20000 x 203 55, 8 x 400000 x 9 70, 8 x 6000 x 700 51 (a warp per row without
-// the stages: 152, 87, 721, 71); with four CTAs per SM, not three: 51, 59, 70.
+// Bound by instructions, element by element: 8 x 60000 x 60 bf16 with four
+// choices 44 us, 8 x 20000 x 203 51, 8 x 400000 x 9 73, 8 x 6000 x 700 47.  (At
+// the time, a warp per row without the stages: 152, 87, 721, 71 for 61, 68, 77
+// and 51; four CTAs per SM for three: 51, 59, 70 for 50, 55, 70.)
 // Where the rows are aligned groups balance_kernel is the faster: 8 x 65536 x
-// 64 bf16 35 against 80 us, 8 x 32768 x 128 f32 55 against 64.
+// 64 bf16 32 against 76 us, 8 x 32768 x 128 f32 50 against 57.
 template <int NE>
 constexpr int kOddStages = NE > 16 ? 2 : 3;
 template <int NE>

@@ -50,10 +50,11 @@
 // the type's lowest value do not turn into inf - inf.
 //
 // Measured (graph replay): loss and gradient, 4096 x 131072 bf16 on 8 ranks,
-// 64 entries: 405-425 us (5.1-5.3 TB/s), bound by the teacher's warp and by
-// the exchange's latency (one entry: 368, 128: 632); 700 x 100003 bf16 on 3,
-// whose pieces fill two thirds of a stage: 88 us.  The loss alone, 2048 x
-// 65536 f16: 52 us (5.2 TB/s); the gradient alone, f32: 175 us (6.2 TB/s).
+// 64 entries: 410-430 us (5.0-5.2 TB/s), bound by the teacher's warp and by
+// the exchange's latency (8 entries: 386, 128: 665, 256: 620); 700 x 100003
+// bf16 on 3, whose pieces fill two thirds of a stage: 87-93 us.  The loss
+// alone, 2048 x 65536 f16: 53 us (5.1 TB/s); the gradient alone, f32: 179 us
+// (6.0 TB/s).
 //
 // Every wait is bounded by the communicator's wait limit; one that gives up
 // records itself in the status block, and the CTA leaves its loops, waits
@@ -66,11 +67,13 @@ namespace ccl {
 
 constexpr int kDistillConsumers = 256;
 constexpr int kDistillWarps = kDistillConsumers / 32;
-// One teacher's warp, or two that take the rows in turn.  4096 x 131072 bf16,
-// one against two: loss and gradient with 256 entries 1058 and 618 us, with
-// 128 entries 658 and 632; the gradient alone with 256 entries 663 and 461;
-// 2048 x 65536 f32 with 128 entries 175 and 186.  So two from 129 entries on,
-// with three in a lane's registers, as two have fewer registers each.
+// One teacher's warp, or two that take the rows in turn.  One against two, us:
+// 4096 x 131072 bf16 with 256 entries, loss and gradient 1026 and 632, the
+// gradient alone 671 and 467.  With 128 entries it is this way and that: 664
+// and 628, the gradient alone 374 and 383; 700 x 100003 bf16 113 and 123; 16 x
+// 32000 f32 5.3 and 5.8; the gradient of 2048 x 65536 f32 177 and 165.  So two
+// from 129 entries on, with three in a lane's registers, as two have fewer
+// registers each.
 template <int HELD>
 constexpr int kDistillTeachers = HELD == 3 ? 2 : 1;
 template <int HELD>
@@ -293,7 +296,7 @@ struct Piece {
 };
 
 // HELD: teacher entries of a lane in registers.  The teacher's warp bounds loss and gradient together, so it holds no
-// more than the call has: 64 entries, 4096 x 131072 bf16: 410 us with two a lane, 446 with four.
+// more than the call has: 64 entries, 4096 x 131072 bf16: 423 us with two a lane, 528 with four.
 template <typename T, int PM, int PASS, int HELD>
 __global__ void __launch_bounds__(kDistillThreads<HELD>, DistillShape<PASS>::ctas) distill_kernel(const __grid_constant__ DistillArgs<PM> a)
 {
@@ -1022,8 +1025,8 @@ static cudaError_t distill_held(const Launch &L, const DistillLaunch &N, LaunchI
     a.span = 0;
     a.groups = groups;
     // The loss alone: fewer pieces that go over the shards' bounds (2048 x
-    // 80768 bf16 on 8 ranks, five for eight: 69 us, 109; with the gradient,
-    // whose stores then have to look for their shard, 212 and 180).
+    // 80768 bf16 on 8 ranks, 8 entries, five for eight: 69 us, 109; with the
+    // gradient, whose stores then have to look for their shard, 212 and 180).
     const uint64_t total = uint64_t(groups) * p;
     for (uint64_t pieces = (total + kDistillStage - 1) / kDistillStage; Shape::loss_alone && groups && pieces < a.pieces; ++pieces) {
         if (pieces > Shape::cluster || N.rows * pieces < 2 * uint64_t(L.num_sms)) continue;

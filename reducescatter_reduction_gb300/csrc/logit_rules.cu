@@ -25,9 +25,9 @@
 // and written, and the listed columns in memory.  Counters are 16 bits wide
 // where the history is shorter than 2^14 tokens.  Bytes: the logits once in
 // and once out, the history once per slice (L2).  Bound by launch and latency
-// where there are few (1 x 32000 f32: 4.7 us), else by the counting of the
+// where there are few (1 x 32000 f32: 4.5 us), else by the counting of the
 // history: 512 x 131072 bf16 take 100 us (2.8 TB/s) with histories of up to
-// 8192 tokens, 52 without, of which copy and mask alone are 46 (5.8 TB/s).
+// 8192 tokens, 48 without, of which copy and mask alone are 45 (6.1 TB/s).
 #include "async.cuh"
 #include "logits.cuh"
 
@@ -418,9 +418,9 @@ static cudaError_t rules_shape(const Launch &L, const RulesLaunch &N, LaunchInfo
     // Few logits: small slices and many threads to go through the history at
     // once; many: large slices, as each goes through the history again.
     // Measured (graph replay, us; 512 x PER16, 512 x 4, 256 x 8 threads x
-    // groups): 1 x 32000 f32, history 2048: 4.8, 5.4, 6.5; 48 x 50021 f16,
-    // history 4000: 15.9, 10.7, 13.4; 512 x 131072 bf16, history up to 8192:
-    // 285, 115, 100, and next to none: 178, 66, 52.
+    // groups): 1 x 32000 f32, history 2048: 4.5, 5.2, 6.0; 48 x 50021 f16,
+    // history 4000: 15.8, 10.4, 13.2; 512 x 131072 bf16, history up to 8192:
+    // 286, 118, 100, and next to none: 178, 65, 48.
     if (all < sms * 1024 * PER16) return rules_launch<T, PM, 512, PER16, WIDE>(L, a, groups, info);
     if (all < sms * 4096 * PER16) return rules_launch<T, PM, 512, 4, WIDE>(L, a, groups, info);
     return rules_launch<T, PM, 256, 8, WIDE>(L, a, groups, info);
