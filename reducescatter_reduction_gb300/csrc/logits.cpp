@@ -44,14 +44,13 @@ struct Shape {
     uint64_t extent() const { return rows && width ? (rows - 1) * stride + width : 0; }
 };
 
-// Whether two buffers have a byte in common.  Rows of one stride may lie
-// between one another's, as the columns of one matrix do.
-static bool meet(const void *pa, const Shape &a, const void *pb, const Shape &b)
+// Whether two buffers whose ranges overlap have a byte in common.  Rows of one
+// stride may lie between one another's, as the columns of one matrix do.
+static bool rows_meet(uintptr_t pa, const Shape &a, uintptr_t pb, const Shape &b)
 {
-    if (!overlap(range_of(pa, a.extent()), range_of(pb, b.extent()))) return false;
     if (a.rows != b.rows || a.stride != b.stride || a.rows < 2) return true;
     // b's row i + k begins d + k stride behind a's row i: the least k for which it ends behind the latter's begin
-    const int64_t d = int64_t(uintptr_t(pb) - uintptr_t(pa)), s = int64_t(a.stride), last = int64_t(a.rows) - 1;
+    const int64_t d = int64_t(pb - pa), s = int64_t(a.stride), last = int64_t(a.rows) - 1;
     const int64_t n = -int64_t(b.width) - d;
     int64_t k = n / s - (n % s < 0 ? 1 : 0) + 1;
     if (k < -last) k = -last;
@@ -68,27 +67,28 @@ static ccl_status_t check_buffers(const ccl_comm *c, const Shape *shape, size_t 
                                   bool *alias)
 {
     const int p = c->p;
-    uint64_t extent[kMaxRanks];
+    Range in[kMaxRanks], out[kMaxRanks];
     *alias = outputs;
     for (int r = 0; r < p; ++r) {
-        extent[r] = shape[r].extent();
-        if (extent[r] && c->out[r] != c->in[r]) *alias = false;
+        in[r] = range_of(c->in[r], shape[r].extent());
+        out[r] = range_of(c->out[r], shape[r].extent());
+        if (in[r].lo < in[r].hi && out[r].lo != in[r].lo) *alias = false;
         if (uintptr_t(c->in[r]) % es || (outputs && uintptr_t(c->out[r]) % es))
             return fail(CCL_ERR_INVALID_ARG, "a buffer of rank %d is not aligned to its elements (%zu bytes)", r, es);
     }
     for (int k = 0; outputs && k < p; ++k) {
         for (int j = 0; j < p; ++j) {
-            if (j > k && meet(c->out[k], shape[k], c->out[j], shape[j]))
+            if (j > k && overlap(out[k], out[j]) && rows_meet(out[k].lo, shape[k], out[j].lo, shape[j]))
                 return fail(CCL_ERR_INVALID_ARG, "outputs of ranks %d and %d overlap", k, j);
-            if ((j != k || c->out[k] != c->in[k]) && meet(c->out[k], shape[k], c->in[j], shape[j]))
+            if (overlap(out[k], in[j]) && (j != k || out[k].lo != in[k].lo) && rows_meet(out[k].lo, shape[k], in[j].lo, shape[j]))
                 return fail(CCL_ERR_INVALID_ARG, "output of rank %d overlaps the input of rank %d", k, j);
         }
     }
     for (int i = 0; i < n_aux; ++i) {
         for (int r = 0; r < p; ++r) {
-            if (outputs && overlap(aux[i].at, range_of(c->out[r], extent[r])))
+            if (outputs && overlap(aux[i].at, out[r]))
                 return fail(CCL_ERR_INVALID_ARG, "%s overlaps the output of rank %d", aux[i].name, r);
-            if (aux[i].written && overlap(aux[i].at, range_of(c->in[r], extent[r])))
+            if (aux[i].written && overlap(aux[i].at, in[r]))
                 return fail(CCL_ERR_INVALID_ARG, "%s overlaps the input of rank %d", aux[i].name, r);
         }
         for (int j = 0; aux[i].written && j < n_aux; ++j)
