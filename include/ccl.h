@@ -59,8 +59,8 @@
  * Memory and ownership.  The caller allocates and owns every rank buffer
  * (device memory, e.g. from PyTorch).  A communicator copies the p input and
  * output pointers (host arrays are not retained) and allocates one small
- * device block (98 KB: the status record, and the scratch of the balance
- * loss's sums and counts) that it frees in ccl_comm_destroy().  No
+ * device block (1.2 MB: the status record, and the scratch of the sums and
+ * counts of the balance loss, the expert sort and the gradient norm) that it frees in ccl_comm_destroy().  No
  * call allocates memory proportional to the message.  Rank buffers may also
  * be page-locked host memory the device can address with the same pointer
  * (cudaHostAlloc, or torch's pin_memory): the ld/st kernels then read and
@@ -85,8 +85,8 @@
  * them on one stream, or order the streams.  On large messages the TMA
  * variants and the SM-budget ld/st kernel hand out work from counters in the
  * communicator's status block, so two collectives of one communicator
- * running at the same time would share them, as two calls of the balance loss
- * would share its counts and sums.  Different
+ * running at the same time would share them, as two calls of the balance loss,
+ * the expert sort or the gradient norm would share their counts and sums.  Different
  * communicators are independent.  ccl_last_error() is per host thread.
  */
 #ifndef CCL_H
@@ -220,21 +220,22 @@ CCL_API ccl_status_t ccl_set_launch(ccl_comm_t comm, int sm_budget, int variant,
 
 /* Failure-detection hooks (tests).
  *  wait_limit_ns : bound on any single wait inside a kernel that waits (the
- *                  TMA variant's pipeline barriers, the fused RMSNorm's and
+ *                  TMA variant's pipeline barriers, the fused RMSNorms' and
  *                  the distillation's exchange); 0 restores the default
  *                  of 2 s.  On expiry the kernel records the wait in the
  *                  status block, stops, and ccl_comm_check() returns
  *                  CCL_ERR_TIMEOUT.
  *  stall_test    : 1 makes the TMA producer withhold its second tile, and the
- *                  fused RMSNorm's second CTA of a row withhold its partial
+ *                  fused RMSNorms' second CTA of a row withhold its partial
  *                  sum, and every CTA of the distillation its second load, so
  *                  that a bounded wait runs out: the timeout path is
  *                  exercised without faulting or hanging the GPU.  2 (the
  *                  checked build only; nothing otherwise) makes the TMA
  *                  producer's bounds check of its second tile fail, so that
  *                  the CCL_ERR_BOUNDS path is exercised: the tile's copies
- *                  are not made; and the operators on logits test their
- *                  accesses against buffers and lists of one row less, so the
+ *                  are not made; and the operators on logits and around
+ *                  layers test their accesses against buffers and lists of one
+ *                  row (ccl_grad_norm and ccl_grad_clip: tensors of one element) less, so the
  *                  last row's are not made.  0 = off.
  * Errors: CCL_ERR_INVALID_ARG for negative values or stall_test > 2. */
 CCL_API ccl_status_t ccl_comm_set_debug(ccl_comm_t comm, long long wait_limit_ns, int stall_test);
@@ -454,6 +455,156 @@ CCL_API ccl_status_t ccl_balance_loss(ccl_comm_t comm, ccl_dtype_t dtype, ccl_pa
                                       size_t k, const int32_t *const *expert_ids, const uint8_t *const *valid,
                                       float coef, const float *dloss, int32_t *counts, int32_t *tokens, float *loss,
                                       void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Operators around a layer with experts and a training step.  No passage of
+ * the pages: the operators are defined here.  What holds for the operators on
+ * logits holds for them: arithmetic and sums in fp32 or more, each result
+ * rounded once to its type, the same bits for the same inputs; every SM is
+ * used, the communicator's variant does not matter; arrays and rank buffers are aligned
+ * to their elements, and 16-byte aligned buffers and rows are fastest.  Nothing
+ * that is written may overlap anything else, but for what an operator names.
+ * Calls only enqueue and can be captured in a CUDA graph once each operator has
+ * run once on the device with the same dtype and sizes.
+ * ------------------------------------------------------------------------- */
+
+/* ccl_allreduce_residual_rmsnorm with an 8-bit output: the communicator's
+ * output buffers receive e4m3 codes, [rows, hidden] bytes, and every rank a
+ * copy of their scales.  Per row, with h as there (rounded, written to
+ * residual_out):
+ *   o     = (h * gamma[col]) * (1/sqrt(mean_row(h^2) + eps))      in fp32, not rounded to dtype
+ *   scale = max(max |o| over a group of columns / 448, 2^-126)
+ *   code  = e4m3(o / scale), nearest even
+ *  group  : columns that share a scale: 32, 64 or 128 (the last group of a row
+ *           may be shorter), or 0: a row has one scale.
+ *  scales : host array of p device pointers, each float [rows, ceil(hidden /
+ *           group)] ([rows] with group 0).
+ * A group with a NaN has scale NaN, one with an infinity scale infinity (its
+ * finite values then have code 0).  As in ccl_allreduce_residual_rmsnorm, a
+ * row whose squares overflow fp32 has 1/sqrt(...) = 0.
+ * residual_out may be residual_in.  Outputs overlap no input (in place is
+ * refused: set them with ccl_comm_set_outputs).
+ * Bytes moved: n ((p + 2) s + p) + hidden s + the scales.  The exchange between the
+ * CTAs of a row is a bounded wait, reported by ccl_comm_check() as
+ * CCL_ERR_TIMEOUT.
+ * Errors: CCL_ERR_INVALID_ARG (a size, group, eps or schedule out of range, a
+ * missing array, overlap), CCL_ERR_UNSUPPORTED (int32, above 2^28 - 1 rows), CCL_ERR_CUDA. */
+CCL_API ccl_status_t ccl_allreduce_residual_rmsnorm_e4m3(ccl_comm_t comm, ccl_dtype_t dtype, size_t rows, size_t hidden,
+                                                         const void *residual_in, void *residual_out, const void *gamma,
+                                                         float *const *scales, size_t group, float eps,
+                                                         ccl_schedule_t schedule, void *stream);
+
+/* Tokens by expert.  p ranks have `rows` tokens each; every token chose k of
+ * `experts` experts; rank r holds the experts of balanced chunk r of experts
+ * (see "Schedules" above: the larger chunks first) and a buffer of `capacity`
+ * rows for the tokens that chose them.  A slot is an int32: slot / capacity is a
+ * rank, slot % capacity a row of its buffer; any value outside [0, p *
+ * capacity) is no row. */
+
+/* The rows of all choices: a stable sort by expert.  A rank's buffer holds its
+ * experts' rows in the order of the experts; an expert's rows are in the order
+ * of source rank, token and choice.  Choices that find the buffer full have
+ * no row.
+ *  expert_ids : host array of p device pointers, each [rows, k]; an id outside
+ *               [0, experts) has no row.  An expert may be in a token's list more than once.
+ *  valid      : host array of p device pointers, each [rows] bytes: the choices
+ *               of a row with 0 have no row.  NULL: every row is valid.
+ *  slots      : host array of p device pointers, each [rows, k], written: the
+ *               slot of each choice, -1 for none.
+ *  offsets    : device [experts + p], written: for each rank, in order, the
+ *               begins of its experts' rows in its buffer and then their end (so rank r's part begins
+ *               at r + its first expert, and n + 1 entries serve n experts).
+ * The communicator's rank buffers are not touched.  At most 4096 experts, p *
+ * rows * k and p * capacity <= 2^31 - 1.  The counts of parts pass through the
+ * communicator's device block.
+ * Bytes moved: 8 p rows k, the valid bytes, the offsets.
+ * Errors: CCL_ERR_INVALID_ARG (a size out of range, a missing array, overlap),
+ * CCL_ERR_UNSUPPORTED (experts > 4096), CCL_ERR_CUDA. */
+CCL_API ccl_status_t ccl_expert_sort(ccl_comm_t comm, size_t rows, size_t experts, size_t k, const int32_t *const *expert_ids,
+                                     const uint8_t *const *valid, size_t capacity, int32_t *const *slots, int32_t *offsets,
+                                     void *stream);
+
+/* Tokens to their experts' ranks.  Inputs: the ranks' tokens, [rows, hidden]
+ * row-major; outputs: the experts' rows, [capacity, hidden].  For every choice
+ * j of token t of every rank that has a row:
+ *   row of slot(t, j) = weights ? round(weights[t, j] * token t) : token t
+ * Other rows of the outputs are left as they were.  Without weights the bytes
+ * are copied, and dtype may also be CCL_I32 (rows of 8-bit codes, four to an
+ * element, or their scales).
+ *  slots   : host array of p device pointers, each [rows, k], as
+ *            ccl_expert_sort writes them: no slot twice.
+ *  weights : host array of p device pointers, each float [rows, k]; NULL: 1.
+ * Its gradient by the tokens is ccl_expert_combine of the rows' gradient with
+ * the same slots and weights.
+ * k <= 4096, p * rows * k and p * capacity <= 2^31 - 1.
+ * Bytes moved: p rows hidden s (1 + k), the lists.
+ * Errors: CCL_ERR_INVALID_ARG (a size out of range, a missing array, overlap;
+ * in place is overlap), CCL_ERR_UNSUPPORTED (int32 with weights), CCL_ERR_CUDA. */
+CCL_API ccl_status_t ccl_expert_dispatch(ccl_comm_t comm, ccl_dtype_t dtype, size_t rows, size_t hidden, size_t k,
+                                         const int32_t *const *slots, const float *const *weights, size_t capacity,
+                                         void *stream);
+
+/* The experts' rows back to their tokens.  Inputs: the experts' rows,
+ * [capacity, hidden]; outputs: the ranks' tokens, [rows, hidden]:
+ *   token t = round(sum over j, in order, of weights[t, j] * row of slot(t, j))
+ * over the choices that have a row (weights NULL: 1); a token without one is 0.
+ * Sizes, lists and errors as ccl_expert_dispatch (int32: CCL_ERR_UNSUPPORTED); a
+ * slot may occur more than once.  Bytes moved: p rows hidden s (k + 1), the lists. */
+CCL_API ccl_status_t ccl_expert_combine(ccl_comm_t comm, ccl_dtype_t dtype, size_t rows, size_t hidden, size_t k,
+                                        const int32_t *const *slots, const float *const *weights, size_t capacity,
+                                        void *stream);
+
+/* The gradient of ccl_expert_combine.  Inputs: the gradient of the tokens,
+ * [rows, hidden]; outputs: that of the experts' rows, [capacity, hidden]:
+ *   row of slot(t, j) = round(weights[t, j] * dy_t)
+ *   dweights[t, j]    = sum over the columns of dy_t * expert_rows[slot(t, j)]
+ * for choices with a row; without one dweights is 0.  Rows of no choice are left as
+ * they were.
+ *  weights     : as above; NULL: 1.
+ *  expert_rows : host array of p device pointers, each [capacity, hidden]: the
+ *                inputs that combine had.
+ *  dweights    : host array of p device pointers, each float [rows, k], written.
+ * Sizes, lists and errors as ccl_expert_dispatch (no slot twice; int32:
+ * CCL_ERR_UNSUPPORTED).  Bytes moved: p rows hidden s (1 + 2 k), the lists. */
+CCL_API ccl_status_t ccl_expert_combine_grad(ccl_comm_t comm, ccl_dtype_t dtype, size_t rows, size_t hidden, size_t k,
+                                             const int32_t *const *slots, const float *const *weights,
+                                             const void *const *expert_rows, size_t capacity, float *const *dweights,
+                                             void *stream);
+
+/* One gradient tensor: n contiguous elements in device memory. */
+typedef struct {
+    const void *in;    /* the gradient */
+    void *out;         /* where ccl_grad_clip writes it: in itself, or disjoint; not read by ccl_grad_norm */
+    size_t n;          /* 0: nothing (in and out may then be NULL) */
+    ccl_dtype_t dtype; /* f32, f16 or bf16 */
+    int32_t copy;      /* not 0: another rank's copy of a tensor of the list; clipped, not counted in the norm */
+} ccl_tensor_t;
+
+/* The global norm of `count` gradient tensors (a host array, read before the
+ * call returns), for example the ranks' shards after ccl_reduce_scatter:
+ *   norm[0] = sqrt(sum of x^2 over the elements of every tensor that is not a copy)
+ * in fp32, also where the squares leave fp32's range; NaN if an element is NaN, else
+ * infinity if one is infinite or the norm is above fp32's range.
+ *  norm : device, two floats; norm[0] is written.
+ * The tensors lie on the communicator's device; its rank buffers are not
+ * touched.  The partial sums pass through the communicator's device block.
+ * Bytes moved: the counted tensors' once.
+ * Errors: CCL_ERR_INVALID_ARG (a missing or misaligned array, a dtype, sizes beyond 2^40
+ * elements in all, norm overlapping a tensor), CCL_ERR_UNSUPPORTED (int32), CCL_ERR_CUDA. */
+CCL_API ccl_status_t ccl_grad_norm(ccl_comm_t comm, size_t count, const ccl_tensor_t *tensors, float *norm, void *stream);
+
+/* Clips the tensors, copies among them, by a global norm:
+ *   norm[1] = factor = min(1, max_norm / (norm[0] + 1e-6))     (NaN if norm[0] is NaN)
+ *   out     = round(in * factor)
+ *  max_norm : finite, >= 0.
+ *  norm     : device, two floats: norm[0] is read (ccl_grad_norm's, or any
+ *             other), norm[1] written.
+ * With factor 1 a tensor in place is left as it is.  Bytes moved: the tensors'
+ * twice.
+ * Errors: as ccl_grad_norm; also tensors that overlap (CCL_ERR_INVALID_ARG),
+ * CCL_ERR_NOMEM (no host memory for that check, 32 bytes a tensor). */
+CCL_API ccl_status_t ccl_grad_clip(ccl_comm_t comm, size_t count, const ccl_tensor_t *tensors, float max_norm, float *norm,
+                                   void *stream);
 
 /* AllReduce for callers that cannot allocate device memory.  The pages have
  * no counterpart: this entry point exists for code that may not call

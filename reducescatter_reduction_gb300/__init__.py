@@ -49,6 +49,8 @@ EXPORTS = (
     "ccl_comm_destroy", "ccl_comm_check", "ccl_allreduce", "ccl_reduce_scatter", "ccl_all_gather",
     "ccl_allreduce_static", "ccl_allreduce_static_set_debug", "ccl_allreduce_residual_rmsnorm",
     "ccl_logit_rules", "ccl_distill_topk", "ccl_balance_loss",
+    "ccl_allreduce_residual_rmsnorm_e4m3", "ccl_expert_sort", "ccl_expert_dispatch", "ccl_expert_combine",
+    "ccl_expert_combine_grad", "ccl_grad_norm", "ccl_grad_clip",
     "ccl_schedule_build", "ccl_schedule_check", "ccl_cost_estimate", "ccl_select_schedule", "ccl_launch_estimate",
     "ccl_last_error", "ccl_comm_last_launch", "ccl_comm_launch_count", "ccl_comm_ranks", "ccl_version", "ccl_bounds_checked",
 )
@@ -73,6 +75,12 @@ class LogitRules(ctypes.Structure):
                 ("prompt_len", ctypes.c_void_p), ("bias_offsets", ctypes.c_void_p), ("bias_tokens", ctypes.c_void_p),
                 ("bias_values", ctypes.c_void_p), ("bias_count", ctypes.c_size_t), ("mask", ctypes.c_void_p),
                 ("mask_rows", ctypes.c_size_t), ("mask_ld", ctypes.c_size_t), ("mask_index", ctypes.c_void_p)]
+
+
+class Tensor(ctypes.Structure):
+    """ccl_tensor_t: device pointers as integers; dtype a CCL_ value; an array of them is (Tensor * n)(...)."""
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_size_t), ("dtype", ctypes.c_int),
+                ("copy", ctypes.c_int32)]
 
 
 _lib = None
@@ -105,6 +113,13 @@ def load_library(path: str = LIB_PATH):
         "ccl_logit_rules": (i, [vp, i, sz, sz, sz, ctypes.POINTER(LogitRules), vp]),
         "ccl_distill_topk": (i, [vp, i, i, sz, sz, sz, sz, vp, vp, i, ctypes.c_float, vp, vp, vp, vp]),
         "ccl_balance_loss": (i, [vp, i, i, sz, sz, sz, pvp, pvp, ctypes.c_float, vp, vp, vp, vp, vp]),
+        "ccl_allreduce_residual_rmsnorm_e4m3": (i, [vp, i, sz, sz, vp, vp, vp, pvp, sz, ctypes.c_float, i, vp]),
+        "ccl_expert_sort": (i, [vp, sz, sz, sz, pvp, pvp, sz, pvp, vp, vp]),
+        "ccl_expert_dispatch": (i, [vp, i, sz, sz, sz, pvp, pvp, sz, vp]),
+        "ccl_expert_combine": (i, [vp, i, sz, sz, sz, pvp, pvp, sz, vp]),
+        "ccl_expert_combine_grad": (i, [vp, i, sz, sz, sz, pvp, pvp, pvp, sz, pvp, vp]),
+        "ccl_grad_norm": (i, [vp, sz, ctypes.POINTER(Tensor), vp, vp]),
+        "ccl_grad_clip": (i, [vp, sz, ctypes.POINTER(Tensor), ctypes.c_float, vp, vp]),
         "ccl_schedule_build": (i, [i, u64, i, ctypes.POINTER(u64), ctypes.POINTER(ctypes.c_uint8)]),
         "ccl_schedule_check": (i, [i, u64, ctypes.POINTER(u64), ctypes.POINTER(ctypes.c_uint8)]),
         "ccl_cost_estimate": (ctypes.c_double, [i, ctypes.c_double, i, ctypes.POINTER(CostParams)]),
@@ -256,6 +271,78 @@ def ccl_balance_loss(comm: int, dtype, steps, rows: int, experts: int, k: int, e
                                 None if expert_ids is None else _ptr_array(expert_ids),
                                 None if valid is None else _ptr_array(valid), float(coef), dloss or None,
                                 counts or None, tokens or None, loss or None, stream or None))
+
+
+def _rank_arrays(lib, comm, **lists):
+    """Pointer arrays of lists with one device pointer for each rank; a list of None is NULL."""
+    p = lib.ccl_comm_ranks(comm)
+    for what, ptrs in lists.items():
+        _want_len(ptrs, p, what)
+    return [None if ptrs is None else _ptr_array(ptrs) for ptrs in lists.values()]
+
+
+def _tensors(tensors):
+    return tensors if isinstance(tensors, ctypes.Array) else (Tensor * len(tensors))(*tensors)
+
+
+def ccl_allreduce_residual_rmsnorm_e4m3(comm: int, dtype, rows: int, hidden: int, residual_in: int, residual_out: int,
+                                        gamma: int, scales, group: int = 0, eps: float = 1e-6, schedule=CCL_SCHED_AUTO,
+                                        stream: int = 0) -> None:
+    """AllReduce, residual and RMSNorm with e4m3 codes in the outputs; scales: a device pointer for each rank."""
+    lib = load_library()
+    (arr,) = _rank_arrays(lib, comm, scales=scales)
+    _check(lib.ccl_allreduce_residual_rmsnorm_e4m3(comm, _code(DTYPES, dtype), int(rows), int(hidden), residual_in or None,
+                                                   residual_out or None, gamma or None, arr, int(group), float(eps),
+                                                   _code(SCHEDULES, schedule), stream or None))
+
+
+def ccl_expert_sort(comm: int, rows: int, experts: int, k: int, expert_ids, valid, capacity: int, slots, offsets: int,
+                    stream: int = 0) -> None:
+    """The rows of all ranks' choices in their experts' buffers (see include/ccl.h); expert_ids, valid (or None) and
+    slots: lists with a device pointer for each rank."""
+    lib = load_library()
+    ids, val, out = _rank_arrays(lib, comm, expert_ids=expert_ids, valid=valid, slots=slots)
+    _check(lib.ccl_expert_sort(comm, int(rows), int(experts), int(k), ids, val, int(capacity), out, offsets or None,
+                               stream or None))
+
+
+def ccl_expert_dispatch(comm: int, dtype, rows: int, hidden: int, k: int, slots, weights, capacity: int,
+                        stream: int = 0) -> None:
+    """Tokens to the rows of their experts; slots and weights (or None): lists with a device pointer for each rank."""
+    lib = load_library()
+    sl, w = _rank_arrays(lib, comm, slots=slots, weights=weights)
+    _check(lib.ccl_expert_dispatch(comm, _code(DTYPES, dtype), int(rows), int(hidden), int(k), sl, w, int(capacity),
+                                   stream or None))
+
+
+def ccl_expert_combine(comm: int, dtype, rows: int, hidden: int, k: int, slots, weights, capacity: int,
+                       stream: int = 0) -> None:
+    """The experts' rows back to their tokens, weighted and summed; lists as ccl_expert_dispatch."""
+    lib = load_library()
+    sl, w = _rank_arrays(lib, comm, slots=slots, weights=weights)
+    _check(lib.ccl_expert_combine(comm, _code(DTYPES, dtype), int(rows), int(hidden), int(k), sl, w, int(capacity),
+                                  stream or None))
+
+
+def ccl_expert_combine_grad(comm: int, dtype, rows: int, hidden: int, k: int, slots, weights, expert_rows, capacity: int,
+                            dweights, stream: int = 0) -> None:
+    """The gradient of ccl_expert_combine by the experts' rows (the outputs) and by the weights."""
+    lib = load_library()
+    sl, w, z, dw = _rank_arrays(lib, comm, slots=slots, weights=weights, expert_rows=expert_rows, dweights=dweights)
+    _check(lib.ccl_expert_combine_grad(comm, _code(DTYPES, dtype), int(rows), int(hidden), int(k), sl, w, z, int(capacity),
+                                       dw, stream or None))
+
+
+def ccl_grad_norm(comm: int, tensors, norm: int, stream: int = 0) -> None:
+    """The global norm of gradient tensors; tensors: a list of Tensor, or an array of them kept from call to call."""
+    arr = _tensors(tensors)
+    _check(load_library().ccl_grad_norm(comm, len(arr), arr, norm or None, stream or None))
+
+
+def ccl_grad_clip(comm: int, tensors, max_norm: float, norm: int, stream: int = 0) -> None:
+    """Clips gradient tensors by the global norm that norm[0] holds; norm[1] receives the factor."""
+    arr = _tensors(tensors)
+    _check(load_library().ccl_grad_clip(comm, len(arr), arr, float(max_norm), norm or None, stream or None))
 
 
 def ccl_schedule_build(p: int, n: int, schedule):

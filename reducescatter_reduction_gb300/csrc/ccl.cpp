@@ -14,6 +14,7 @@
 
 #include "comm.h"
 #include "internal.h"
+#include "spans.h"
 
 using namespace ccl;
 
@@ -686,5 +687,98 @@ extern "C" ccl_status_t ccl_allreduce_residual_rmsnorm(ccl_comm_t c, ccl_dtype_t
              kDtypeName[dtype], p, n, rows, hidden, kSchedName[sched], L.vec ? 1 : 0, info.grid, info.block);
     if (debug_on()) fprintf(stderr, "[ccl] %s\n", c->last);
     if (err != cudaSuccess) return cuda_fail(err, "allreduce_residual_rmsnorm");
+    return CCL_OK;
+}
+
+extern "C" ccl_status_t ccl_allreduce_residual_rmsnorm_e4m3(ccl_comm_t c, ccl_dtype_t dtype, size_t rows, size_t hidden,
+                                                            const void *residual_in, void *residual_out, const void *gamma,
+                                                            float *const *scales, size_t group, float eps,
+                                                            ccl_schedule_t schedule, void *stream)
+{
+    const char *what = "allreduce_residual_rmsnorm_e4m3";
+    if (!c) return fail(CCL_ERR_INVALID_ARG, "comm is NULL");
+    if (dtype == CCL_I32) return fail(CCL_ERR_UNSUPPORTED, "RMSNorm needs a floating-point dtype");
+    if (dtype < CCL_F32 || dtype > CCL_BF16) return fail(CCL_ERR_INVALID_ARG, "unknown dtype %d", int(dtype));
+    if (schedule < CCL_SCHED_AUTO || schedule > CCL_SCHED_CUSTOM)
+        return fail(CCL_ERR_INVALID_ARG, "unknown schedule %d", int(schedule));
+    if (schedule == CCL_SCHED_CUSTOM && !c->has_custom)
+        return fail(CCL_ERR_INVALID_ARG, "custom schedule requested but none set");
+    if (hidden == 0) return fail(CCL_ERR_INVALID_ARG, "hidden must be positive");
+    if (group != 0 && group != 32 && group != 64 && group != 128)
+        return fail(CCL_ERR_INVALID_ARG, "group %zu is not 0, 32, 64 or 128", group);
+    if (!(eps >= 0.0f) || eps > 3.0e38f) return fail(CCL_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    const size_t s = elem_bytes(dtype);
+    if (rows > (SIZE_MAX / 4) / hidden / s) return fail(CCL_ERR_INVALID_ARG, "rows * hidden too large");
+    if (rows > 0xfffffffull) return fail(CCL_ERR_UNSUPPORTED, "rows %zu above 2^28 - 1", rows);   // eight CTAs a row at most
+    const size_t n = rows * hidden;
+    if (n == 0) return CCL_OK;
+    if (!residual_in || !residual_out || !gamma) return fail(CCL_ERR_INVALID_ARG, "NULL residual or gamma");
+    ccl_status_t st = check_list(c, scales, "scales", 4);
+    if (st != CCL_OK) return st;
+    const int p = c->p;
+    const size_t groups = group ? (hidden + group - 1) / group : 1;
+    const size_t vec_elems = 16 / s;
+    bool aligned = uintptr_t(residual_in) % 16 == 0 && uintptr_t(residual_out) % 16 == 0 && uintptr_t(gamma) % 16 == 0 &&
+                   hidden % vec_elems == 0;
+    if (uintptr_t(residual_in) % s || uintptr_t(residual_out) % s || uintptr_t(gamma) % s)
+        return fail(CCL_ERR_INVALID_ARG, "residual or gamma is not aligned to its elements (%zu bytes)", s);
+    Spans spans;
+    for (int r = 0; r < p; ++r) {
+        if (uintptr_t(c->in[r]) % s)
+            return fail(CCL_ERR_INVALID_ARG, "the input of rank %d is not aligned to its elements (%zu bytes)", r, s);
+        // a group of elements becomes vec_elems bytes, stored at once
+        aligned = aligned && uintptr_t(c->in[r]) % 16 == 0 && uintptr_t(c->out[r]) % vec_elems == 0;
+        spans.add("the input of rank", r, c->in[r], n * s, false);
+        spans.add("the output of rank", r, c->out[r], n, true);
+        spans.add("scales", r, scales[r], rows * groups * 4, true);
+    }
+    if (residual_in != residual_out) spans.add("residual_in", -1, residual_in, n * s, false);
+    spans.add("residual_out", -1, residual_out, n * s, true);
+    spans.add("gamma", -1, gamma, hidden * s, false);
+    if ((st = check_spans(spans.s, size_t(spans.n))) != CCL_OK) return st;
+
+    DeviceGuard g(c->device);
+    if (g.err != cudaSuccess) return cuda_fail(g.err, what);
+    Launch L;
+    L.p = p;
+    L.op = CCL_SUM;
+    L.dtype = dtype;
+    L.mode = MODE_AR;
+    L.n = n;
+    for (int r = 0; r < p; ++r) {
+        L.src[r] = c->in[r];
+        L.dst[r] = c->out[r];
+    }
+    L.device = c->device;
+    L.num_sms = c->num_sms;
+    L.stream = static_cast<cudaStream_t>(stream);
+    L.status = c->d_status;
+    L.wait_limit_ns = c->wait_limit_ns;
+    L.stall_test = c->stall_test;
+    const int sched = resolve_schedule(c, schedule, double(n) * double(s));
+    if (sched < 0)
+        return fail(CCL_ERR_INVALID_ARG, "CCL_SCHEDULE=%s is not ring, allpairs or auto", getenv("CCL_SCHEDULE"));
+    L.table = get_table(c, n, sched);
+    for (int k = 0; k <= p && aligned; ++k) aligned = L.table->bound[k] % vec_elems == 0;
+    L.vec = aligned;
+    NormE4m3Launch N;
+    N.norm.residual = residual_in;
+    N.norm.residual_out = residual_out;
+    N.norm.gamma = gamma;
+    N.norm.rows = rows;
+    N.norm.hidden = hidden;
+    N.norm.eps = eps;
+    N.scales = scales;
+    N.group = uint32_t(group);
+    LaunchInfo info;
+    const cudaError_t err = dtype == CCL_F32   ? launch_allreduce_rmsnorm_e4m3_f32(L, N, &info)
+                            : dtype == CCL_F16 ? launch_allreduce_rmsnorm_e4m3_f16(L, N, &info)
+                                               : launch_allreduce_rmsnorm_e4m3_bf16(L, N, &info);
+    c->launches += uint64_t(info.kernels);
+    snprintf(c->last, sizeof c->last,
+             "%s dtype=%s op=sum p=%d n=%zu rows=%zu hidden=%zu group=%zu schedule=%s vec=%d grid=%d block=%d", info.kernel,
+             kDtypeName[dtype], p, n, rows, hidden, group, kSchedName[sched], L.vec ? 1 : 0, info.grid, info.block);
+    if (debug_on()) fprintf(stderr, "[ccl] %s\n", c->last);
+    if (err != cudaSuccess) return cuda_fail(err, what);
     return CCL_OK;
 }

@@ -1,5 +1,5 @@
 // The communicator and the helpers that the host front ends share (ccl.cpp:
-// the collectives; logits.cpp: the logit operators).
+// the collectives; logits.cpp: the logit operators; layers.cpp: those around layers).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -18,7 +18,7 @@ struct ccl_comm {
     int sm_budget = 0;
     int variant = CCL_VARIANT_AUTO;
     size_t pipe_bytes = 0;
-    unsigned *d_status = nullptr;   // device block: kCommStatusBytes of status, then the scratch of the loss sums
+    unsigned *d_status = nullptr;   // device block: kCommStatusBytes of status, then the operators' scratch
     bool has_custom = false;
     uint8_t custom[ccl::kMaxRanks * ccl::kMaxRanks] = {};
     ccl::Table table;               // last built table (one-entry cache)

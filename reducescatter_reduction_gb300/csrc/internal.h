@@ -15,14 +15,19 @@ constexpr int kMaxRanks = 64;
 // The device block of a communicator: the status record and tile counters,
 // then (kScratchOffset) the scratch of ccl_balance_loss: a ticket counter, one
 // pair of partial sums per CTA, and counters (per rank and expert, and per
-// rank) that every call leaves at zero.
+// rank) that every call leaves at zero; then (kGradOffset) that of
+// ccl_grad_norm: a ticket left at zero, a running total, one partial sum per
+// CTA; then (kSortOffset) the counts of ccl_expert_sort's parts.
 constexpr size_t kCommStatusBytes = 256;
 constexpr size_t kScratchOffset = kCommStatusBytes;
 constexpr size_t kScratchHead = 256;          // the ticket, padded
 constexpr unsigned kMaxPartials = 2048;       // CTAs that may leave a pair of sums
 constexpr unsigned kScratchCells = 16384;     // ranks * experts that the counters hold
-constexpr size_t kCommDeviceBytes =
-    kScratchOffset + kScratchHead + size_t(kMaxPartials) * 16 + size_t(kScratchCells + kMaxRanks) * 4;
+constexpr size_t kGradOffset = kScratchOffset + kScratchHead + size_t(kMaxPartials) * 16 + size_t(kScratchCells + kMaxRanks) * 4;
+constexpr size_t kSortOffset = kGradOffset + kScratchHead + size_t(kMaxPartials) * 8;
+constexpr unsigned kSortCells = 1u << 18;     // parts * experts that the sort's counts hold
+constexpr size_t kCommDeviceBytes = kSortOffset + size_t(kSortCells) * 4;
+static_assert(kGradOffset % 16 == 0 && kSortOffset % 16 == 0, "");
 
 enum Op : int { OP_SUM = 0, OP_PROD = 1, OP_MIN = 2, OP_MAX = 3, OP_AVG = 4 };
 enum Dtype : int { DT_F32 = 0, DT_F16 = 1, DT_BF16 = 2, DT_I32 = 3 };
@@ -296,6 +301,54 @@ struct BalanceLaunch {
     void *scratch = nullptr;    // the communicator's: kScratchHead bytes, the partial sums, the counters
 };
 cudaError_t launch_balance(const Launch &L, const BalanceLaunch &N, LaunchInfo *info);
+
+// The operators around layers (norm_e4m3.cuh, expert_sort.cu, expert_rows.cu,
+// grads.cu).
+struct NormE4m3Launch {
+    NormLaunch norm;
+    float *const *scales = nullptr;
+    uint32_t group = 0;         // columns that share a scale; 0: a row
+};
+cudaError_t launch_allreduce_rmsnorm_e4m3_f32(const Launch &L, const NormE4m3Launch &N, LaunchInfo *info);
+cudaError_t launch_allreduce_rmsnorm_e4m3_f16(const Launch &L, const NormE4m3Launch &N, LaunchInfo *info);
+cudaError_t launch_allreduce_rmsnorm_e4m3_bf16(const Launch &L, const NormE4m3Launch &N, LaunchInfo *info);
+
+struct SortLaunch {
+    uint64_t rows = 0;
+    uint32_t experts = 0;
+    uint32_t k = 0;
+    uint32_t capacity = 0;
+    const int32_t *const *ids = nullptr;
+    const uint8_t *const *valid = nullptr;
+    int32_t *const *slots = nullptr;
+    int32_t *offsets = nullptr;
+    int32_t *cells = nullptr;   // the communicator's: kSortCells counts
+};
+cudaError_t launch_expert_sort(const Launch &L, const SortLaunch &N, LaunchInfo *info);
+
+enum RowsOp : int { ROWS_DISPATCH = 0, ROWS_COMBINE = 1, ROWS_GRAD = 2 };
+struct RowsLaunch {
+    int op = ROWS_DISPATCH;
+    uint64_t rows = 0;
+    uint64_t hidden = 0;
+    uint32_t k = 0;
+    uint32_t capacity = 0;
+    const int32_t *const *slots = nullptr;
+    const float *const *weights = nullptr;
+    const void *const *experts = nullptr;   // ROWS_GRAD
+    float *const *dweights = nullptr;       // ROWS_GRAD
+};
+cudaError_t launch_expert_rows(const Launch &L, const RowsLaunch &N, LaunchInfo *info);
+
+struct GradLaunch {
+    size_t count = 0;
+    const ccl_tensor_t *tensors = nullptr;
+    bool clip = false;
+    float max_norm = 0.0f;
+    float *norm = nullptr;
+    void *scratch = nullptr;    // the communicator's: kScratchHead bytes, the partial sums
+};
+cudaError_t launch_grads(const Launch &L, const GradLaunch &N, LaunchInfo *info);
 
 // The measured launch table (launch_table.cpp): the estimated per-call time
 // (us) of an AllReduce with the ld/st or TMA kernel, and AUTO's choice.

@@ -4,10 +4,7 @@
 
 #include <cuda_runtime.h>
 
-#include <cstdio>
-
-#include "comm.h"
-#include "internal.h"
+#include "front.h"
 
 using namespace ccl;
 
@@ -18,25 +15,6 @@ struct Aux {
     Range at;
     bool written;
 };
-
-static Range range_of(const void *p, uint64_t bytes)
-{
-    return {uintptr_t(p), p ? uintptr_t(p) + bytes : uintptr_t(p)};
-}
-
-static ccl_status_t check_floats(const ccl_comm *c, int dtype, const char *what)
-{
-    if (!c) return fail(CCL_ERR_INVALID_ARG, "comm is NULL");
-    if (dtype == CCL_I32) return fail(CCL_ERR_UNSUPPORTED, "%s needs a floating-point dtype", what);
-    if (dtype < CCL_F32 || dtype > CCL_BF16) return fail(CCL_ERR_INVALID_ARG, "unknown dtype %d", dtype);
-    return CCL_OK;
-}
-
-static ccl_status_t check_aligned(const void *p, size_t to, const char *name)
-{
-    if (uintptr_t(p) % to) return fail(CCL_ERR_INVALID_ARG, "%s is not aligned to its elements (%zu bytes)", name, to);
-    return CCL_OK;
-}
 
 // A rank buffer: `rows` pieces of `width` bytes, `stride` bytes apart; bytes from the first to the last of them.
 struct Shape {
@@ -113,37 +91,6 @@ static ccl_status_t shard_shapes(const ccl_comm *c, size_t rows, size_t vocab, s
         shape[r] = {rows, w * es, (ld ? ld : w) * es};
     }
     return CCL_OK;
-}
-
-static Launch make_launch(ccl_comm *c, int dtype, bool alias, void *stream)
-{
-    Launch L;
-    L.p = c->p;
-    L.dtype = dtype;
-    for (int r = 0; r < c->p; ++r) {
-        L.src[r] = c->in[r];
-        L.dst[r] = c->out[r];
-    }
-    L.alias = alias;
-    L.device = c->device;
-    L.num_sms = c->num_sms;
-    L.status = c->d_status;
-    L.wait_limit_ns = c->wait_limit_ns;
-    L.stall_test = c->stall_test;
-    L.stream = static_cast<cudaStream_t>(stream);
-    return L;
-}
-
-static ccl_status_t finish(ccl_comm *c, cudaError_t err, const LaunchInfo &info, int dtype, size_t rows, size_t cols, const char *what,
-                           const char *pass)
-{
-    if (err == kTooManyPieces && info.kernels == 0)
-        return fail(CCL_ERR_UNSUPPORTED, "%s: %zu rows of %zu columns over %d ranks are more than 2^31 - 1 pieces", what, rows, cols, c->p);
-    c->launches += uint64_t(info.kernels);
-    snprintf(c->last, sizeof c->last, "%s dtype=%s p=%d rows=%zu columns=%zu pass=%s grid=%d block=%d smem=%zu kernels=%d", info.kernel,
-             kDtypeName[dtype], c->p, rows, cols, pass, info.grid, info.block, info.smem, info.kernels);
-    if (debug_on()) fprintf(stderr, "[ccl] %s\n", c->last);
-    return err == cudaSuccess ? CCL_OK : cuda_fail(err, what);
 }
 
 static const char *kPassName[] = {"-", "forward", "backward", "both"};

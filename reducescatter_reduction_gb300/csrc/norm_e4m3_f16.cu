@@ -1,0 +1,8 @@
+// AllReduce + residual + RMSNorm with e4m3 outputs, f16 inputs (norm_e4m3.cuh).
+#include "norm_e4m3.cuh"
+
+namespace ccl {
+
+cudaError_t launch_allreduce_rmsnorm_e4m3_f16(const Launch &L, const NormE4m3Launch &N, LaunchInfo *info) { return quant_dtype<F16>(L, N, info); }
+
+}  // namespace ccl
