@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 # CCL_LIBRARY names another build of this library to load instead (the
@@ -113,11 +114,11 @@ def load_library(path: str = LIB_PATH):
         "ccl_logit_rules": (i, [vp, i, sz, sz, sz, ctypes.POINTER(LogitRules), vp]),
         "ccl_distill_topk": (i, [vp, i, i, sz, sz, sz, sz, vp, vp, i, ctypes.c_float, vp, vp, vp, vp]),
         "ccl_balance_loss": (i, [vp, i, i, sz, sz, sz, pvp, pvp, ctypes.c_float, vp, vp, vp, vp, vp]),
-        "ccl_allreduce_residual_rmsnorm_e4m3": (i, [vp, i, sz, sz, vp, vp, vp, pvp, sz, ctypes.c_float, i, vp]),
-        "ccl_expert_sort": (i, [vp, sz, sz, sz, pvp, pvp, sz, pvp, vp, vp]),
-        "ccl_expert_dispatch": (i, [vp, i, sz, sz, sz, pvp, pvp, sz, vp]),
-        "ccl_expert_combine": (i, [vp, i, sz, sz, sz, pvp, pvp, sz, vp]),
-        "ccl_expert_combine_grad": (i, [vp, i, sz, sz, sz, pvp, pvp, pvp, sz, pvp, vp]),
+        "ccl_allreduce_residual_rmsnorm_e4m3": (i, [vp, i, sz, sz, vp, vp, vp, vp, sz, ctypes.c_float, i, vp]),
+        "ccl_expert_sort": (i, [vp, sz, sz, sz, vp, vp, sz, vp, vp, vp]),
+        "ccl_expert_dispatch": (i, [vp, i, sz, sz, sz, vp, vp, sz, vp]),
+        "ccl_expert_combine": (i, [vp, i, sz, sz, sz, vp, vp, sz, vp]),
+        "ccl_expert_combine_grad": (i, [vp, i, sz, sz, sz, vp, vp, vp, sz, vp, vp]),
         "ccl_grad_norm": (i, [vp, sz, ctypes.POINTER(Tensor), vp, vp]),
         "ccl_grad_clip": (i, [vp, sz, ctypes.POINTER(Tensor), ctypes.c_float, vp, vp]),
         "ccl_schedule_build": (i, [i, u64, i, ctypes.POINTER(u64), ctypes.POINTER(ctypes.c_uint8)]),
@@ -273,12 +274,13 @@ def ccl_balance_loss(comm: int, dtype, steps, rows: int, experts: int, k: int, e
                                 counts or None, tokens or None, loss or None, stream or None))
 
 
-def _rank_arrays(lib, comm, **lists):
-    """Pointer arrays of lists with one device pointer for each rank; a list of None is NULL."""
-    p = lib.ccl_comm_ranks(comm)
-    for what, ptrs in lists.items():
+def _rank_array(p: int, ptrs, what: str):
+    """One device pointer for each of p ranks, as the bytes of the C array (None: NULL)."""
+    if ptrs is None:
+        return None
+    if len(ptrs) != p:
         _want_len(ptrs, p, what)
-    return [None if ptrs is None else _ptr_array(ptrs) for ptrs in lists.values()]
+    return struct.pack(f"{p}Q", *ptrs)
 
 
 def _tensors(tensors):
@@ -290,10 +292,10 @@ def ccl_allreduce_residual_rmsnorm_e4m3(comm: int, dtype, rows: int, hidden: int
                                         stream: int = 0) -> None:
     """AllReduce, residual and RMSNorm with e4m3 codes in the outputs; scales: a device pointer for each rank."""
     lib = load_library()
-    (arr,) = _rank_arrays(lib, comm, scales=scales)
+    p = lib.ccl_comm_ranks(comm)
     _check(lib.ccl_allreduce_residual_rmsnorm_e4m3(comm, _code(DTYPES, dtype), int(rows), int(hidden), residual_in or None,
-                                                   residual_out or None, gamma or None, arr, int(group), float(eps),
-                                                   _code(SCHEDULES, schedule), stream or None))
+                                                   residual_out or None, gamma or None, _rank_array(p, scales, "scales"),
+                                                   int(group), float(eps), _code(SCHEDULES, schedule), stream or None))
 
 
 def ccl_expert_sort(comm: int, rows: int, experts: int, k: int, expert_ids, valid, capacity: int, slots, offsets: int,
@@ -301,36 +303,39 @@ def ccl_expert_sort(comm: int, rows: int, experts: int, k: int, expert_ids, vali
     """The rows of all ranks' choices in their experts' buffers (see include/ccl.h); expert_ids, valid (or None) and
     slots: lists with a device pointer for each rank."""
     lib = load_library()
-    ids, val, out = _rank_arrays(lib, comm, expert_ids=expert_ids, valid=valid, slots=slots)
-    _check(lib.ccl_expert_sort(comm, int(rows), int(experts), int(k), ids, val, int(capacity), out, offsets or None,
-                               stream or None))
+    p = lib.ccl_comm_ranks(comm)
+    _check(lib.ccl_expert_sort(comm, int(rows), int(experts), int(k), _rank_array(p, expert_ids, "expert_ids"),
+                               _rank_array(p, valid, "valid"), int(capacity), _rank_array(p, slots, "slots"),
+                               offsets or None, stream or None))
 
 
 def ccl_expert_dispatch(comm: int, dtype, rows: int, hidden: int, k: int, slots, weights, capacity: int,
                         stream: int = 0) -> None:
     """Tokens to the rows of their experts; slots and weights (or None): lists with a device pointer for each rank."""
     lib = load_library()
-    sl, w = _rank_arrays(lib, comm, slots=slots, weights=weights)
-    _check(lib.ccl_expert_dispatch(comm, _code(DTYPES, dtype), int(rows), int(hidden), int(k), sl, w, int(capacity),
-                                   stream or None))
+    p = lib.ccl_comm_ranks(comm)
+    _check(lib.ccl_expert_dispatch(comm, _code(DTYPES, dtype), int(rows), int(hidden), int(k), _rank_array(p, slots, "slots"),
+                                   _rank_array(p, weights, "weights"), int(capacity), stream or None))
 
 
 def ccl_expert_combine(comm: int, dtype, rows: int, hidden: int, k: int, slots, weights, capacity: int,
                        stream: int = 0) -> None:
     """The experts' rows back to their tokens, weighted and summed; lists as ccl_expert_dispatch."""
     lib = load_library()
-    sl, w = _rank_arrays(lib, comm, slots=slots, weights=weights)
-    _check(lib.ccl_expert_combine(comm, _code(DTYPES, dtype), int(rows), int(hidden), int(k), sl, w, int(capacity),
-                                  stream or None))
+    p = lib.ccl_comm_ranks(comm)
+    _check(lib.ccl_expert_combine(comm, _code(DTYPES, dtype), int(rows), int(hidden), int(k), _rank_array(p, slots, "slots"),
+                                  _rank_array(p, weights, "weights"), int(capacity), stream or None))
 
 
 def ccl_expert_combine_grad(comm: int, dtype, rows: int, hidden: int, k: int, slots, weights, expert_rows, capacity: int,
                             dweights, stream: int = 0) -> None:
     """The gradient of ccl_expert_combine by the experts' rows (the outputs) and by the weights."""
     lib = load_library()
-    sl, w, z, dw = _rank_arrays(lib, comm, slots=slots, weights=weights, expert_rows=expert_rows, dweights=dweights)
-    _check(lib.ccl_expert_combine_grad(comm, _code(DTYPES, dtype), int(rows), int(hidden), int(k), sl, w, z, int(capacity),
-                                       dw, stream or None))
+    p = lib.ccl_comm_ranks(comm)
+    _check(lib.ccl_expert_combine_grad(comm, _code(DTYPES, dtype), int(rows), int(hidden), int(k),
+                                       _rank_array(p, slots, "slots"), _rank_array(p, weights, "weights"),
+                                       _rank_array(p, expert_rows, "expert_rows"), int(capacity),
+                                       _rank_array(p, dweights, "dweights"), stream or None))
 
 
 def ccl_grad_norm(comm: int, tensors, norm: int, stream: int = 0) -> None:
