@@ -473,8 +473,8 @@ CCL_API ccl_status_t ccl_balance_loss(ccl_comm_t comm, ccl_dtype_t dtype, ccl_pa
  * copy of their scales.  Per row, with h as there (rounded, written to
  * residual_out):
  *   o     = (h * gamma[col]) * (1/sqrt(mean_row(h^2) + eps))      in fp32, not rounded to dtype
- *   scale = max(max |o| over a group of columns / 448, 2^-126)
- *   code  = e4m3(o / scale), nearest even
+ *   scale = max(max |o| over a group of columns * (1/448), 2^-126)   448: the largest code
+ *   code  = e4m3(o * (1/scale)), nearest even; reciprocals and products rounded to fp32
  *  group  : columns that share a scale: 32, 64 or 128 (the last group of a row
  *           may be shorter), or 0: a row has one scale.
  *  scales : host array of p device pointers, each float [rows, ceil(hidden /
@@ -488,7 +488,7 @@ CCL_API ccl_status_t ccl_balance_loss(ccl_comm_t comm, ccl_dtype_t dtype, ccl_pa
  * CTAs of a row is a bounded wait, reported by ccl_comm_check() as
  * CCL_ERR_TIMEOUT.
  * Errors: CCL_ERR_INVALID_ARG (a size, group, eps or schedule out of range, a
- * missing array, overlap), CCL_ERR_UNSUPPORTED (int32, above 2^28 - 1 rows), CCL_ERR_CUDA. */
+ * missing array, overlap), CCL_ERR_UNSUPPORTED (int32, above 2^28 - 1 rows or 2^31 - 1 columns), CCL_ERR_CUDA. */
 CCL_API ccl_status_t ccl_allreduce_residual_rmsnorm_e4m3(ccl_comm_t comm, ccl_dtype_t dtype, size_t rows, size_t hidden,
                                                          const void *residual_in, void *residual_out, const void *gamma,
                                                          float *const *scales, size_t group, float eps,

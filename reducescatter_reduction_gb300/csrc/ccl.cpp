@@ -710,6 +710,7 @@ extern "C" ccl_status_t ccl_allreduce_residual_rmsnorm_e4m3(ccl_comm_t c, ccl_dt
     const size_t s = elem_bytes(dtype);
     if (rows > (SIZE_MAX / 4) / hidden / s) return fail(CCL_ERR_INVALID_ARG, "rows * hidden too large");
     if (rows > 0xfffffffull) return fail(CCL_ERR_UNSUPPORTED, "rows %zu above 2^28 - 1", rows);   // eight CTAs a row at most
+    if (hidden > 0x7fffffffull) return fail(CCL_ERR_UNSUPPORTED, "hidden %zu above 2^31 - 1", hidden);
     const size_t n = rows * hidden;
     if (n == 0) return CCL_OK;
     if (!residual_in || !residual_out || !gamma) return fail(CCL_ERR_INVALID_ARG, "NULL residual or gamma");

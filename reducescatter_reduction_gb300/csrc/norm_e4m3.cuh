@@ -1,8 +1,8 @@
 // AllReduce fused with the residual merge and RMSNorm, with e4m3 codes and
 // their scales as outputs.  Per row:
 //   y = round(sum of the p rank rows), h = round(y + residual)
-//   o = (h gamma) (1 / sqrt(mean(h^2) + eps)), scale = max(max |o| / 448, 2^-126)
-//   code = e4m3(o / scale), one scale for a group of columns or for the row
+//   o = (h gamma) (1 / sqrt(mean(h^2) + eps)), scale = max(max |o| (1/448), 2^-126)
+//   code = e4m3(o (1 / scale)), one scale for a group of columns or for the row
 // As in rmsnorm.cu a cluster of C CTAs has a row, and each CTA pushes its part
 // of the row's sums into every CTA of the cluster.  Multiplying by gamma before
 // 1/rms makes the row's largest |o| the rounded product of its largest |h
@@ -12,7 +12,7 @@
 
 #include <cooperative_groups.h>
 
-#include "device.cuh"
+#include "logits.cuh"
 
 namespace ccl {
 
@@ -30,11 +30,11 @@ struct QuantArgs {
     const void *residual;
     void *residual_out;
     const void *gamma;
-    uint64_t rows, hidden;
+    uint64_t rows;
+    uint32_t hidden;
     uint32_t groups;    // scales of a row
     uint32_t lanes;     // lanes of a warp that share a scale; 0: the row has one
     int p;
-    int vec;            // 16-byte groups: pointers aligned, hidden and every chunk boundary multiples of VEC
     float eps;
     unsigned *status;
     long long wait_ns;
@@ -78,11 +78,20 @@ __device__ __forceinline__ bool wait_bounded(uint32_t bar, long long limit)
     return true;
 }
 
-// The larger; NaN if one is.
-__device__ __forceinline__ float max_nan(float a, float b)
+// A load that keeps its place among the others (the buffers may be written in
+// place, by the thread that read them).
+__device__ __forceinline__ uint4 load_v4(const void *p)
+{
+    uint4 r;
+    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
+}
+
+// The largest size; NaN if one is.
+__device__ __forceinline__ float max_abs(float a, float b, float c)
 {
     float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
@@ -96,18 +105,69 @@ __device__ __forceinline__ uint32_t e4m3_pair(float lo, float hi)
 // The scale of a group whose largest |o| is m.
 __device__ __forceinline__ float scale_of(float m)
 {
-    const float s = __fdiv_rn(m, 448.0f);
+    const float s = __fmul_rn(m, 1.0f / 448.0f);
     return s < 0x1p-126f ? 0x1p-126f : s;      // (NaN stays NaN)
 }
 
-// One unit, VEC columns of a row, a thread at a time.
-template <typename T, int P, int THREADS, int KEEP>
-__global__ void __launch_bounds__(THREADS) ar_rmsnorm_e4m3_kernel(const __grid_constant__ QuantArgs<(P > 0 ? P : kMaxRanks)> a)
-{
+// The columns of a unit, as pairs.
+template <typename T, bool VECTOR>
+struct QuantUnit {
     using Tr = Traits<T>;
-    using F = Fold<T, OP_SUM>;
-    constexpr int VEC = Tr::VEC, S = 16 / VEC, WARPS = THREADS / 32;
-    __shared__ float2 red[32];
+    static constexpr int VEC = Tr::VEC, S = 16 / VEC, PAIRS = VEC / 2;
+    __device__ static __forceinline__ void unpack(const uint4 &v, Pair (&f)[PAIRS])
+    {
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) f[i] = Group<T>::pair(v, i);
+    }
+    // unit u of the row that begins at `row`, of `hidden` columns
+    __device__ static __forceinline__ uint4 load(const void *row, uint32_t u, uint32_t hidden)
+    {
+        if constexpr (VECTOR) {
+            return load_v4(static_cast<const char *>(row) + uint64_t(u) * 16);
+        } else {
+            float f[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) f[i] = u * VEC + i < hidden ? Tr::load1(row, u * VEC + i) : 0.0f;
+            return Tr::pack(f);
+        }
+    }
+    __device__ static __forceinline__ void store(void *row, uint32_t u, uint32_t hidden, const uint4 &v)
+    {
+        if constexpr (VECTOR) {
+            st_v4(static_cast<char *>(row) + uint64_t(u) * 16, v);
+        } else {
+            float f[VEC];
+            Tr::unpack(v, f);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (u * VEC + i < hidden) Tr::store1(row, u * VEC + i, f[i]);
+        }
+    }
+    __device__ static __forceinline__ void store_codes(void *row, uint32_t u, uint32_t hidden, const uint32_t (&w)[VEC / 4])
+    {
+        char *to = static_cast<char *>(row) + uint64_t(u) * VEC;
+        if constexpr (VECTOR && VEC == 8) {
+            asm volatile("st.global.cs.v2.u32 [%0], {%1, %2};" ::"l"(to), "r"(w[0]), "r"(w[1]) : "memory");
+        } else if constexpr (VECTOR) {
+            asm volatile("st.global.cs.u32 [%0], %1;" ::"l"(to), "r"(w[0]) : "memory");
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i)
+                if (u * VEC + i < hidden) to[i] = char(w[i / 4] >> (i % 4 * 8));
+        }
+    }
+};
+
+// A thread has a unit of VEC columns at a time, KEEP of them in registers
+// between the passes; further units are read again.  VECTOR: units are 16-byte
+// groups, and no unit lies in two chunks.
+template <typename T, int P, int THREADS, int KEEP, bool VECTOR>
+__global__ void __launch_bounds__(THREADS, KEEP > 1 ? 1024 / THREADS : 1) ar_rmsnorm_e4m3_kernel(const __grid_constant__ QuantArgs<(P > 0 ? P : kMaxRanks)> a)
+{
+    using U = QuantUnit<T, VECTOR>;
+    constexpr int VEC = U::VEC, S = U::S, PAIRS = U::PAIRS, WARPS = THREADS / 32;
+    __shared__ float2 red[WARPS];
+    __shared__ float2 row_s;            // 1/rms, the row's largest |o|
     __shared__ __align__(8) float2 parts[kQuantMaxCluster];
     __shared__ __align__(8) uint64_t xbar;
     cg::cluster_group cluster = cg::this_cluster();
@@ -125,213 +185,231 @@ __global__ void __launch_bounds__(THREADS) ar_rmsnorm_e4m3_kernel(const __grid_c
     grid_dependency_wait();
     grid_dependents_launch();
     const int p = P > 0 ? P : a.p;
-    const uint64_t H = a.hidden, row = blockIdx.x / C, base = row * H;
-    const uint64_t held = (a.rows - (a.stall_test == 2 ? 1 : 0)) * H;       // (checked build)
-    // this CTA's columns: whole warps of units, so that the lanes that share a scale are in one warp
-    const uint64_t blocks = (H + 32 * VEC - 1) / (32 * VEC);
-    const uint64_t b0 = blocks * q / C, b1 = blocks * (q + 1) / C;
+    const uint32_t H = a.hidden, units = (H + VEC - 1) / VEC;
+    const uint64_t row = C > 1 ? blockIdx.x / C : blockIdx.x, base = row * H;
+    const bool held = in_bounds(row < a.rows - (a.stall_test == 2 ? 1 : 0), a.status, kSiteNorm, base);
+    // this CTA's units: whole warps of them, so that the lanes that share a scale are in one warp
+    const uint32_t blocks = (units + 31) / 32;
+    const uint32_t u0 = C > 1 ? uint32_t(uint64_t(blocks) * q / C) * 32 : 0;
+    const uint32_t u1 = !held ? u0 : C > 1 ? min(units, uint32_t(uint64_t(blocks) * (q + 1) / C) * 32) : units;
+    const char *residual = static_cast<const char *>(a.residual) + base * S;
+    char *merged = static_cast<char *>(a.residual_out) + base * S;
 
-    auto load_unit = [&](const void *buf, uint64_t c, uint64_t at, float (&f)[VEC]) {    // columns c ... from element `at`
-        if (a.vec) {
-            Tr::unpack(ld_coherent_v4(static_cast<const char *>(buf) + at * S), f);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) f[i] = c + i < H ? Tr::load1(buf, at + i) : 0.0f;
-        }
+    // most rows lie in one chunk
+    int chunk = 0;
+    while (base >= a.bound[chunk + 1]) ++chunk;
+    const bool one_chunk = base + H <= a.bound[chunk + 1];
+    auto source = [&](uint32_t u, int k) -> const void * {
+        int c = chunk;
+        if (!one_chunk)
+            while (base + uint64_t(u) * VEC >= a.bound[c + 1]) ++c;
+        return static_cast<const char *>(a.src[a.order[c][k]]) + base * S;
     };
-    float ss = 0.0f, top = 0.0f;
-    // pass 1: fold, merge, store h, its squares and largest |h gamma|
-    auto pass1 = [&](uint64_t b) -> uint4 {
-        const uint64_t c = (b * 32 + lane) * VEC, e = base + c;
-        const uint64_t end = c + VEC < H ? c + VEC : H;
-        if (c >= H || !in_bounds(base + end <= held, a.status, kSiteNorm, e)) return make_uint4(0, 0, 0, 0);
-        float acc[VEC], v[VEC];
-        if (a.vec) {
-            int ch = 0;
-            while (e >= a.bound[ch + 1]) ++ch;
-            if constexpr (P > 0) {
-                uint4 r[P];
+    Pair ss = {0.0f, 0.0f};
+    float top = 0.0f;
+    // pass 1: fold, merge, store h, add its squares and find the largest |h gamma|
+    auto merge = [&](uint32_t u, Pair (&acc)[PAIRS], const uint4 &res) -> uint4 {
+        Pair v[PAIRS];
+        if constexpr (P != 1) U::unpack(Group<T>::pack(acc), acc);       // y, rounded
+        U::unpack(res, v);
 #pragma unroll
-                for (int k = 0; k < P; ++k) r[k] = ld_coherent_v4(static_cast<const char *>(a.src[a.order[ch][k]]) + e * S);
-                if constexpr (THREADS <= 128) hold_batch(r);
-                Tr::unpack(r[0], acc);
+        for (int i = 0; i < PAIRS; ++i) acc[i] = acc[i] + v[i];          // the merge
+        const uint4 h = Group<T>::pack(acc);
+        U::store(merged, u, H, h);
+        U::unpack(h, acc);                                               // h, rounded
 #pragma unroll
-                for (int k = 1; k < P; ++k) {
-                    Tr::unpack(r[k], v);
+        for (int i = 0; i < PAIRS; ++i) ss = fma(acc[i], acc[i], ss);
+        if (a.lanes == 0) {
+            U::unpack(U::load(a.gamma, u, H), v);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) acc[i] = F::fold(acc[i], v[i], 1.0f);
-                }
-            } else {
-                Tr::unpack(ld_coherent_v4(static_cast<const char *>(a.src[a.order[ch][0]]) + e * S), acc);
-                for (int k = 1; k < p; ++k) {
-                    Tr::unpack(ld_coherent_v4(static_cast<const char *>(a.src[a.order[ch][k]]) + e * S), v);
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) acc[i] = F::fold(acc[i], v[i], 1.0f);
-                }
+            for (int i = 0; i < PAIRS; ++i) {
+                const Pair o = acc[i] * v[i];
+                top = max_abs(top, o.x, o.y);
             }
-        } else {
-            int ch = 0;
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                acc[i] = 0.0f;
-                if (c + i >= H) continue;
-                while (e + i >= a.bound[ch + 1]) ++ch;
-                acc[i] = Tr::load1(a.src[a.order[ch][0]], e + i);
-                for (int k = 1; k < p; ++k) acc[i] = F::fold(acc[i], Tr::load1(a.src[a.order[ch][k]], e + i), 1.0f);
-            }
-        }
-        Tr::unpack(Tr::pack(acc), acc);                                  // y, rounded
-        load_unit(a.residual, c, e, v);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) acc[i] = __fadd_rn(acc[i], v[i]);   // the merge
-        const uint4 h = Tr::pack(acc);
-        Tr::unpack(h, acc);                                              // h, rounded
-        if (a.vec) {
-            st_v4(static_cast<char *>(a.residual_out) + e * S, h);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i)
-                if (c + i < H) Tr::store1(a.residual_out, e + i, acc[i]);
-        }
-        load_unit(a.gamma, c, c, v);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            ss = __fadd_rn(ss, __fmul_rn(acc[i], acc[i]));
-            top = max_nan(top, fabsf(__fmul_rn(acc[i], v[i])));
         }
         return h;
     };
+    // N units, THREADS apart: all loads go out before the first fold
+    auto pass1 = [&](auto count, uint32_t u, uint4 *kept) {
+        constexpr int N = decltype(count)::value;
+        if constexpr (P > 0) {
+            uint4 r[N][P + 1];
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                if (u + j * THREADS >= u1) continue;
+#pragma unroll
+                for (int k = 0; k < P; ++k) r[j][k] = U::load(source(u + j * THREADS, k), u + j * THREADS, H);
+                r[j][P] = U::load(residual, u + j * THREADS, H);
+            }
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                if (u + j * THREADS >= u1) continue;
+                Pair acc[PAIRS], v[PAIRS];
+                U::unpack(r[j][0], acc);
+#pragma unroll
+                for (int k = 1; k < P; ++k) {
+                    U::unpack(r[j][k], v);
+#pragma unroll
+                    for (int i = 0; i < PAIRS; ++i) acc[i] = acc[i] + v[i];
+                }
+                const uint4 h = merge(u + j * THREADS, acc, r[j][P]);
+                if (kept) kept[j] = h;
+            }
+        } else {
+            static_assert(N == 1, "");
+            if (u >= u1) return;
+            Pair acc[PAIRS], v[PAIRS];
+            if constexpr (VECTOR) {
+                U::unpack(U::load(source(u, 0), u, H), acc);
+#pragma unroll 4
+                for (int k = 1; k < p; ++k) {
+                    U::unpack(U::load(source(u, k), u, H), v);
+#pragma unroll
+                    for (int i = 0; i < PAIRS; ++i) acc[i] = acc[i] + v[i];
+                }
+            } else {
+                float f[VEC];
+                int c = 0;
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const uint64_t e = base + uint64_t(u) * VEC + i;
+                    f[i] = 0.0f;
+                    if (u * VEC + i >= H) continue;
+                    while (e >= a.bound[c + 1]) ++c;
+                    f[i] = Traits<T>::load1(a.src[a.order[c][0]], e);
+                    for (int k = 1; k < p; ++k) f[i] = __fadd_rn(f[i], Traits<T>::load1(a.src[a.order[c][k]], e));
+                }
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) acc[i] = {f[2 * i], f[2 * i + 1]};
+            }
+            const uint4 h = merge(u, acc, U::load(residual, u, H));
+            if (kept) kept[0] = h;
+        }
+    };
+    constexpr int MOST = P == 1 ? 4 : P == 2 || P == 4 ? 2 : 1, BATCH = KEEP < MOST ? KEEP : MOST;
+    const uint32_t first = u0 + threadIdx.x;
     uint4 keep[KEEP];
 #pragma unroll
-    for (int j = 0; j < KEEP; ++j) {
-        const uint64_t b = b0 + warp + uint64_t(j) * WARPS;
-        if (b < b1) keep[j] = pass1(b);
-    }
-    for (uint64_t b = b0 + warp + uint64_t(KEEP) * WARPS; b < b1; b += WARPS) pass1(b);
+    for (int j = 0; j < KEEP; j += BATCH) pass1(std::integral_constant<int, BATCH>(), first + j * THREADS, keep + j);
+    for (uint32_t u = first + KEEP * THREADS; u < u1; u += BATCH * THREADS) pass1(std::integral_constant<int, BATCH>(), u, nullptr);
 
-    // the row's sum and maximum
+    // the row's sum and maximum: the warps', then (warp 0) the CTA's, then the cluster's
+    float sum = ss.x + ss.y;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-    }
-    if (lane == 0) red[warp] = make_float2(ss, top);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (a.lanes == 0)
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, o), 0.0f);
+    if (lane == 0) red[warp] = make_float2(sum, top);
     __syncthreads();
-    ss = 0.0f;
-    top = 0.0f;
+    if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (warp == 0) {
+        const float2 mine = lane < WARPS ? red[lane] : make_float2(0.0f, 0.0f);
+        sum = mine.x;
+        top = mine.y;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-        ss = __fadd_rn(ss, red[w].x);
-        top = max_nan(top, red[w].y);
-    }
-    if (C > 1) {
-        // every CTA writes its pair into parts[q] of every CTA of the row and waits for the C pairs in its own; it
-        // leaves only after all writes into it have landed
-        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-        if (threadIdx.x == 0)
-            asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(uint32_t(C * 8)) : "memory");
-        if (int(threadIdx.x) < C && !(a.stall_test == 1 && q == 1))
-            asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];"
-                         ::"r"(map_shared(uint32_t(__cvta_generic_to_shared(&parts[q])), threadIdx.x)), "r"(__float_as_uint(ss)),
-                         "r"(__float_as_uint(top)), "r"(map_shared(bar, threadIdx.x))
-                         : "memory");
-        if (!wait_bounded(bar, a.wait_ns)) {
-            // A pair is missing (this call's outputs are wrong).  Once more, again bounded, so that a late peer's write
-            // does not land after this CTA has gone.
-            if (a.status && atomicCAS(&a.status[0], 0u, 5u) == 0u) {
-                a.status[1] = blockIdx.x;
-                a.status[2] = unsigned(row);
-                a.status[3] = threadIdx.x;
+        for (int o = WARPS / 2; o > 0; o >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            top = max_abs(top, __shfl_xor_sync(0xffffffffu, top, o), 0.0f);
+        }
+        if (C > 1) {
+            sum = __shfl_sync(0xffffffffu, sum, 0);
+            top = __shfl_sync(0xffffffffu, top, 0);
+            // every CTA writes its pair into parts[q] of every CTA of the row and waits for the C pairs in its own; it
+            // leaves only after all writes into it have landed
+            if (lane == 0)
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(uint32_t(C * 8)) : "memory");
+            __syncwarp();
+            if (lane < C && !(a.stall_test == 1 && q == 1))
+                asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.b32 [%0], {%1, %2}, [%3];"
+                             ::"r"(map_shared(uint32_t(__cvta_generic_to_shared(&parts[q])), lane)), "r"(__float_as_uint(sum)),
+                             "r"(__float_as_uint(top)), "r"(map_shared(bar, lane))
+                             : "memory");
+            if (!wait_bounded(bar, a.wait_ns)) {
+                // A pair is missing (this call's outputs are wrong).  Once more, again bounded, so that a late peer's
+                // write does not land after this CTA has gone.
+                if (a.status && atomicCAS(&a.status[0], 0u, 5u) == 0u) {
+                    a.status[1] = blockIdx.x;
+                    a.status[2] = unsigned(row);
+                    a.status[3] = threadIdx.x;
+                }
+                wait_bounded(bar, a.wait_ns);
             }
-            wait_bounded(bar, a.wait_ns);
+            sum = 0.0f;
+            top = 0.0f;
+            for (int k = 0; k < C; ++k) {
+                sum = __fadd_rn(sum, parts[k].x);
+                top = max_abs(top, parts[k].y, 0.0f);
+            }
         }
-        ss = 0.0f;
-        top = 0.0f;
-        for (int k = 0; k < C; ++k) {
-            ss = __fadd_rn(ss, parts[k].x);
-            top = max_nan(top, parts[k].y);
+        if (lane == 0) {
+            const float inv = 1.0f / sqrtf(__fadd_rn(__fdiv_rn(sum, float(H)), a.eps));
+            row_s = make_float2(inv, __fmul_rn(top, inv));
         }
     }
-    const float inv = 1.0f / sqrtf(__fadd_rn(__fdiv_rn(ss, float(H)), a.eps));
-    const float row_scale = scale_of(__fmul_rn(top, inv));
-    if (a.lanes == 0 && q == 0)
-        for (int k = threadIdx.x; k < p; k += THREADS)
-            if (in_bounds(base + H <= held, a.status, kSiteNorm, row)) a.scales[k][row] = row_scale;
+    __syncthreads();
+    const float inv = row_s.x;
+    float back = 0.0f;
+    if (a.lanes == 0) {
+        const float scale = scale_of(row_s.y);
+        back = __frcp_rn(scale);
+        if (q == 0 && held)
+            for (int k = threadIdx.x; k < p; k += THREADS) a.scales[k][row] = scale;
+    }
 
-    // pass 2: codes to every rank
-    auto pass2 = [&](uint64_t b, const uint4 &h) {
-        const uint64_t c = (b * 32 + lane) * VEC, e = base + c;
-        const uint64_t end = c + VEC < H ? c + VEC : H;
-        const bool has = c < H && in_bounds(base + end <= held, a.status, kSiteNorm, e);
-        float o[VEC], g[VEC];
+    // pass 2: codes to every rank.  `on`: the thread has a unit; all lanes come here together.
+    auto pass2 = [&](uint32_t u, const uint4 &h, bool on) {
+        Pair o[PAIRS], g[PAIRS];
         float m = 0.0f;
+        if (on) {
+            U::unpack(h, o);
+            U::unpack(U::load(a.gamma, u, H), g);
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) o[i] = 0.0f;
-        if (has) {
-            Tr::unpack(h, o);
-            load_unit(a.gamma, c, c, g);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                o[i] = __fmul_rn(__fmul_rn(o[i], g[i]), inv);
-                if (a.vec || c + i < H) m = max_nan(m, fabsf(o[i]));
+            for (int i = 0; i < PAIRS; ++i) {
+                o[i] = o[i] * g[i] * Pair{inv, inv};
+                if constexpr (VECTOR) {
+                    m = max_abs(m, o[i].x, o[i].y);
+                } else {     // (columns beyond the row are 0 times 1/rms, which may be NaN)
+                    if (u * VEC + 2 * i < H) m = max_abs(m, o[i].x, 0.0f);
+                    if (u * VEC + 2 * i + 1 < H) m = max_abs(m, o[i].y, 0.0f);
+                }
             }
         }
-        float scale = row_scale;
         if (a.lanes) {
-            for (uint32_t l = 1; l < a.lanes; l <<= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, l));
-            scale = scale_of(m);
-            if (has && lane % a.lanes == 0) {
-                const uint64_t at = row * a.groups + c / (a.lanes * VEC);
+            for (uint32_t l = 1; l < a.lanes; l <<= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, l), 0.0f);
+            const float scale = scale_of(m);
+            back = __frcp_rn(scale);
+            if (on && lane % a.lanes == 0) {
+                const uint64_t at = row * a.groups + u / a.lanes;
                 for (int k = 0; k < p; ++k) a.scales[k][at] = scale;
             }
         }
-        if (!has) return;
+        if (!on) return;
         uint32_t w[VEC / 4];
 #pragma unroll
-        for (int i = 0; i < VEC / 4; ++i)
-            w[i] = e4m3_pair(__fdiv_rn(o[4 * i], scale), __fdiv_rn(o[4 * i + 1], scale)) |
-                   e4m3_pair(__fdiv_rn(o[4 * i + 2], scale), __fdiv_rn(o[4 * i + 3], scale)) << 16;
-        auto store = [&](void *dst) {
-            char *to = static_cast<char *>(dst) + e;
-            if (a.vec) {
-                if constexpr (VEC == 8) asm volatile("st.global.cs.v2.u32 [%0], {%1, %2};" ::"l"(to), "r"(w[0]), "r"(w[1]) : "memory");
-                else asm volatile("st.global.cs.u32 [%0], %1;" ::"l"(to), "r"(w[0]) : "memory");
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i)
-                    if (c + i < H) to[i] = char(w[i / 4] >> (i % 4 * 8));
-            }
-        };
+        for (int i = 0; i < VEC / 4; ++i) {
+            const Pair lo = o[2 * i] * Pair{back, back}, hi = o[2 * i + 1] * Pair{back, back};
+            w[i] = e4m3_pair(lo.x, lo.y) | e4m3_pair(hi.x, hi.y) << 16;
+        }
         if constexpr (P > 0) {
 #pragma unroll
-            for (int k = 0; k < P; ++k) store(a.dst[k]);
+            for (int k = 0; k < P; ++k) U::store_codes(static_cast<char *>(a.dst[k]) + base, u, H, w);
         } else {
-            for (int k = 0; k < p; ++k) store(a.dst[k]);
+            for (int k = 0; k < p; ++k) U::store_codes(static_cast<char *>(a.dst[k]) + base, u, H, w);
         }
     };
 #pragma unroll
-    for (int j = 0; j < KEEP; ++j) {
-        const uint64_t b = b0 + warp + uint64_t(j) * WARPS;
-        if (b < b1) pass2(b, keep[j]);
-    }
-    for (uint64_t b = b0 + warp + uint64_t(KEEP) * WARPS; b < b1; b += WARPS) {
-        const uint64_t c = (b * 32 + lane) * VEC;
-        uint4 h = make_uint4(0, 0, 0, 0);
-        const uint64_t end = c + VEC < H ? c + VEC : H;
-        if (c < H && in_bounds(base + end <= held, a.status, kSiteNorm, base + c)) {
-            float f[VEC];
-            load_unit(a.residual_out, c, base + c, f);      // (this thread's own stores)
-            h = Tr::pack(f);
-        }
-        pass2(b, h);
-    }
+    for (int j = 0; j < KEEP; ++j)
+        if (u0 + warp * 32 + j * THREADS < u1) pass2(first + j * THREADS, keep[j], first + j * THREADS < u1);
+    for (uint32_t u = first + KEEP * THREADS; u - lane < u1; u += THREADS)
+        pass2(u, u < u1 ? U::load(merged, u, H) : make_uint4(0, 0, 0, 0), u < u1);      // (this thread's own stores)
 }
 
-template <typename T, int P>
+template <typename T, int P, bool VECTOR>
 static cudaError_t quant_launch(const Launch &L, const NormE4m3Launch &N, LaunchInfo *info)
 {
     constexpr int PM = P > 0 ? P : kMaxRanks, VEC = Traits<T>::VEC;
-    QuantArgs<PM> a = {};
+    QuantArgs<PM> a;
     for (int k = 0; k < L.p; ++k) {
         a.src[k] = L.src[k];
         a.dst[k] = L.dst[k];
@@ -344,20 +422,20 @@ static cudaError_t quant_launch(const Launch &L, const NormE4m3Launch &N, Launch
     a.residual_out = N.norm.residual_out;
     a.gamma = N.norm.gamma;
     a.rows = N.norm.rows;
-    a.hidden = N.norm.hidden;
+    a.hidden = uint32_t(N.norm.hidden);
     a.groups = N.group ? uint32_t((N.norm.hidden + N.group - 1) / N.group) : 1;
     a.lanes = N.group / VEC;
     a.p = L.p;
-    a.vec = L.vec ? 1 : 0;
     a.eps = N.norm.eps;
     a.status = L.status;
     a.wait_ns = L.wait_limit_ns > 0 ? L.wait_limit_ns : 2000000000LL;
     a.stall_test = L.stall_test;
-    // the shapes of rmsnorm.cu: decode, one to two rows an SM, prefill
-    const uint64_t blocks = (N.norm.hidden + 32 * VEC - 1) / (32 * VEC), sms = uint64_t(L.num_sms), rows = N.norm.rows;
-    const int threads = rows < sms ? 128 : rows < 2 * sms ? 1024 : 256;
-    const uint64_t per_cta = uint64_t(threads / 32) * (rows < 2 * sms ? 1 : 4);
-    const uint64_t want = (blocks + per_cta - 1) / per_cta;
+    // CTA shape by rows against the SMs, as in rmsnorm.cu
+    const uint64_t units = (N.norm.hidden + VEC - 1) / VEC, sms = uint64_t(L.num_sms), rows = N.norm.rows;
+    const int keep = rows < 2 * sms ? 1 : 4;
+    const int threads = rows < sms ? 128 : rows < 2 * sms && VECTOR ? 1024 : units <= 256 && VECTOR ? 64 : units <= 512 && VECTOR ? 128 : units <= 1024 || !VECTOR ? 256 : 512;
+    const uint64_t per_cta = uint64_t(threads) * keep;
+    const uint64_t want = (units + per_cta - 1) / per_cta;
     const int C = int(want > uint64_t(kQuantMaxCluster) ? kQuantMaxCluster : want);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(rows * C));
@@ -372,9 +450,17 @@ static cudaError_t quant_launch(const Launch &L, const NormE4m3Launch &N, Launch
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = C > 1 ? 2 : 1;
-    const cudaError_t err = threads == 128    ? cudaLaunchKernelEx(&cfg, ar_rmsnorm_e4m3_kernel<T, P, 128, 1>, a)
-                            : threads == 1024 ? cudaLaunchKernelEx(&cfg, ar_rmsnorm_e4m3_kernel<T, P, 1024, 1>, a)
-                                              : cudaLaunchKernelEx(&cfg, ar_rmsnorm_e4m3_kernel<T, P, 256, 4>, a);
+    void (*kern)(QuantArgs<PM>) = nullptr;
+    if constexpr (VECTOR) {
+        kern = keep == 1 ? (threads == 128 ? ar_rmsnorm_e4m3_kernel<T, P, 128, 1, true> : ar_rmsnorm_e4m3_kernel<T, P, 1024, 1, true>)
+               : threads == 64  ? ar_rmsnorm_e4m3_kernel<T, P, 64, 4, true>
+               : threads == 128 ? ar_rmsnorm_e4m3_kernel<T, P, 128, 4, true>
+               : threads == 512 ? ar_rmsnorm_e4m3_kernel<T, P, 512, 4, true>
+                                : ar_rmsnorm_e4m3_kernel<T, P, 256, 4, true>;
+    } else {
+        kern = threads == 128 ? ar_rmsnorm_e4m3_kernel<T, P, 128, 1, false> : ar_rmsnorm_e4m3_kernel<T, P, 256, 4, false>;
+    }
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, a);
     if (err != cudaSuccess) return err;
     info->kernel = "allreduce_residual_rmsnorm_e4m3";
     info->grid = int(rows * C);
@@ -387,12 +473,13 @@ static cudaError_t quant_launch(const Launch &L, const NormE4m3Launch &N, Launch
 template <typename T>
 static cudaError_t quant_dtype(const Launch &L, const NormE4m3Launch &N, LaunchInfo *info)
 {
+    if (!L.vec) return quant_launch<T, 0, false>(L, N, info);
     switch (L.p) {
-    case 1: return quant_launch<T, 1>(L, N, info);
-    case 2: return quant_launch<T, 2>(L, N, info);
-    case 4: return quant_launch<T, 4>(L, N, info);
-    case 8: return quant_launch<T, 8>(L, N, info);
-    default: return quant_launch<T, 0>(L, N, info);
+    case 1: return quant_launch<T, 1, true>(L, N, info);
+    case 2: return quant_launch<T, 2, true>(L, N, info);
+    case 4: return quant_launch<T, 4, true>(L, N, info);
+    case 8: return quant_launch<T, 8, true>(L, N, info);
+    default: return quant_launch<T, 0, true>(L, N, info);
     }
 }
 
