@@ -33,7 +33,7 @@ struct QuantArgs {
     uint64_t rows;
     uint32_t hidden;
     uint32_t groups;    // scales of a row
-    uint32_t lanes;     // lanes of a warp that share a scale; 0: the row has one
+    uint32_t lanes;     // units that share a scale; 0: the row has one
     int p;
     float eps;
     unsigned *status;
@@ -109,7 +109,9 @@ __device__ __forceinline__ float scale_of(float m)
     return s < 0x1p-126f ? 0x1p-126f : s;      // (NaN stays NaN)
 }
 
-// The columns of a unit, as pairs.
+// The VEC columns of a unit, as pairs.  VECTOR: they follow one another.  Other
+// rows are read element by element, so that the 32 lanes of a load take neighbouring columns: unit u of
+// a warp's 32 has every 32nd column of their 32 VEC.
 template <typename T, bool VECTOR>
 struct QuantUnit {
     using Tr = Traits<T>;
@@ -119,6 +121,7 @@ struct QuantUnit {
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) f[i] = Group<T>::pair(v, i);
     }
+    __device__ static __forceinline__ uint32_t column(uint32_t u, int i) { return VECTOR ? u * VEC + i : u / 32 * (32 * VEC) + i * 32 + u % 32; }
     // unit u of the row that begins at `row`, of `hidden` columns
     __device__ static __forceinline__ uint4 load(const void *row, uint32_t u, uint32_t hidden)
     {
@@ -127,7 +130,7 @@ struct QuantUnit {
         } else {
             float f[VEC];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) f[i] = u * VEC + i < hidden ? Tr::load1(row, u * VEC + i) : 0.0f;
+            for (int i = 0; i < VEC; ++i) f[i] = column(u, i) < hidden ? Tr::load1(row, column(u, i)) : 0.0f;
             return Tr::pack(f);
         }
     }
@@ -140,12 +143,12 @@ struct QuantUnit {
             Tr::unpack(v, f);
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
-                if (u * VEC + i < hidden) Tr::store1(row, u * VEC + i, f[i]);
+                if (column(u, i) < hidden) Tr::store1(row, column(u, i), f[i]);
         }
     }
     __device__ static __forceinline__ void store_codes(void *row, uint32_t u, uint32_t hidden, const uint32_t (&w)[VEC / 4])
     {
-        char *to = static_cast<char *>(row) + uint64_t(u) * VEC;
+        char *to = static_cast<char *>(row) + (VECTOR ? uint64_t(u) * VEC : 0);
         if constexpr (VECTOR && VEC == 8) {
             asm volatile("st.global.cs.v2.u32 [%0], {%1, %2};" ::"l"(to), "r"(w[0]), "r"(w[1]) : "memory");
         } else if constexpr (VECTOR) {
@@ -153,7 +156,7 @@ struct QuantUnit {
         } else {
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
-                if (u * VEC + i < hidden) to[i] = char(w[i / 4] >> (i % 4 * 8));
+                if (column(u, i) < hidden) to[column(u, i)] = char(w[i / 4] >> (i % 4 * 8));
         }
     }
 };
@@ -185,7 +188,7 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? 1024 / THREADS : 1) ar_rms
     grid_dependency_wait();
     grid_dependents_launch();
     const int p = P > 0 ? P : a.p;
-    const uint32_t H = a.hidden, units = (H + VEC - 1) / VEC;
+    const uint32_t H = a.hidden, units = VECTOR ? H / VEC : (H + 32 * VEC - 1) / (32 * VEC) * 32;
     const uint64_t row = C > 1 ? blockIdx.x / C : blockIdx.x, base = row * H;
     const bool held = in_bounds(row < a.rows - (a.stall_test == 2 ? 1 : 0), a.status, kSiteNorm, base);
     // this CTA's units: whole warps of them, so that the lanes that share a scale are in one warp
@@ -269,15 +272,29 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? 1024 / THREADS : 1) ar_rms
                 }
             } else {
                 float f[VEC];
-                int c = 0;
+                if (one_chunk) {
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const uint64_t e = base + uint64_t(u) * VEC + i;
-                    f[i] = 0.0f;
-                    if (u * VEC + i >= H) continue;
-                    while (e >= a.bound[c + 1]) ++c;
-                    f[i] = Traits<T>::load1(a.src[a.order[c][0]], e);
-                    for (int k = 1; k < p; ++k) f[i] = __fadd_rn(f[i], Traits<T>::load1(a.src[a.order[c][k]], e));
+                    for (int i = 0; i < VEC; ++i) f[i] = 0.0f;
+#pragma unroll 4
+                    for (int k = 0; k < p; ++k) {
+                        const void *from = source(u, k);
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) {
+                            const float v = U::column(u, i) < H ? Traits<T>::load1(from, U::column(u, i)) : 0.0f;
+                            f[i] = k == 0 ? v : __fadd_rn(f[i], v);
+                        }
+                    }
+                } else {
+                    int c = chunk;
+#pragma unroll
+                    for (int i = 0; i < VEC; ++i) {
+                        const uint64_t e = base + U::column(u, i);
+                        f[i] = 0.0f;
+                        if (U::column(u, i) >= H) continue;
+                        while (e >= a.bound[c + 1]) ++c;
+                        f[i] = Traits<T>::load1(a.src[a.order[c][0]], e);
+                        for (int k = 1; k < p; ++k) f[i] = __fadd_rn(f[i], Traits<T>::load1(a.src[a.order[c][k]], e));
+                    }
                 }
 #pragma unroll
                 for (int i = 0; i < PAIRS; ++i) acc[i] = {f[2 * i], f[2 * i + 1]};
@@ -360,37 +377,60 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? 1024 / THREADS : 1) ar_rms
     // pass 2: codes to every rank.  `on`: the thread has a unit; all lanes come here together.
     auto pass2 = [&](uint32_t u, const uint4 &h, bool on) {
         Pair o[PAIRS], g[PAIRS];
-        float m = 0.0f;
         if (on) {
             U::unpack(h, o);
             U::unpack(U::load(a.gamma, u, H), g);
 #pragma unroll
-            for (int i = 0; i < PAIRS; ++i) {
-                o[i] = o[i] * g[i] * Pair{inv, inv};
-                if constexpr (VECTOR) {
-                    m = max_abs(m, o[i].x, o[i].y);
-                } else {     // (columns beyond the row are 0 times 1/rms, which may be NaN)
-                    if (u * VEC + 2 * i < H) m = max_abs(m, o[i].x, 0.0f);
-                    if (u * VEC + 2 * i + 1 < H) m = max_abs(m, o[i].y, 0.0f);
-                }
-            }
+            for (int i = 0; i < PAIRS; ++i) o[i] = o[i] * g[i] * Pair{inv, inv};
         }
-        if (a.lanes) {
+        uint32_t w[VEC / 4];
+        auto code = [&](const float (&by)[VEC]) {
+#pragma unroll
+            for (int i = 0; i < VEC / 4; ++i) {
+                const Pair lo = o[2 * i] * Pair{by[4 * i], by[4 * i + 1]}, hi = o[2 * i + 1] * Pair{by[4 * i + 2], by[4 * i + 3]};
+                w[i] = e4m3_pair(lo.x, lo.y) | e4m3_pair(hi.x, hi.y) << 16;
+            }
+        };
+        float by[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) by[i] = back;
+        if (a.lanes && VECTOR) {
+            // the lanes of a group have its units
+            float m = 0.0f;
+            if (on)
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) m = max_abs(m, o[i].x, o[i].y);
             for (uint32_t l = 1; l < a.lanes; l <<= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, l), 0.0f);
-            const float scale = scale_of(m);
-            back = __frcp_rn(scale);
+            const float scale = scale_of(m), each = __frcp_rn(scale);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) by[i] = each;
             if (on && lane % a.lanes == 0) {
                 const uint64_t at = row * a.groups + u / a.lanes;
                 for (int k = 0; k < p; ++k) a.scales[k][at] = scale;
             }
+        } else if (a.lanes) {
+            // 32 columns of a group at a time
+            const uint32_t span = a.lanes * VEC / 32, block = u / 32 * VEC;
+            float m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                // (columns beyond the row are 0 times 1/rms, which may be NaN)
+                if (on && U::column(u, i) < H) m = max_abs(m, i % 2 ? o[i / 2].y : o[i / 2].x, 0.0f);
+                if ((i + 1) % span) continue;
+#pragma unroll
+                for (int l = 16; l > 0; l >>= 1) m = max_abs(m, __shfl_xor_sync(0xffffffffu, m, l), 0.0f);
+                const float scale = scale_of(m), each = __frcp_rn(scale);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j)
+                    if (j <= i && j + int(span) > i) by[j] = each;
+                const uint32_t group = (block + i) / span;
+                if (group < a.groups)
+                    for (int k = lane; k < p; k += 32) a.scales[k][row * a.groups + group] = scale;
+                m = 0.0f;
+            }
         }
         if (!on) return;
-        uint32_t w[VEC / 4];
-#pragma unroll
-        for (int i = 0; i < VEC / 4; ++i) {
-            const Pair lo = o[2 * i] * Pair{back, back}, hi = o[2 * i + 1] * Pair{back, back};
-            w[i] = e4m3_pair(lo.x, lo.y) | e4m3_pair(hi.x, hi.y) << 16;
-        }
+        code(by);
         if constexpr (P > 0) {
 #pragma unroll
             for (int k = 0; k < P; ++k) U::store_codes(static_cast<char *>(a.dst[k]) + base, u, H, w);
@@ -432,8 +472,14 @@ static cudaError_t quant_launch(const Launch &L, const NormE4m3Launch &N, Launch
     a.stall_test = L.stall_test;
     // CTA shape by rows against the SMs, as in rmsnorm.cu
     const uint64_t units = (N.norm.hidden + VEC - 1) / VEC, sms = uint64_t(L.num_sms), rows = N.norm.rows;
-    const int keep = rows < 2 * sms ? 1 : 4;
-    const int threads = rows < sms ? 128 : rows < 2 * sms && VECTOR ? 1024 : units <= 256 && VECTOR ? 64 : units <= 512 && VECTOR ? 128 : units <= 1024 || !VECTOR ? 256 : 512;
+    const int threads = rows < sms      ? 128
+                        : !VECTOR       ? 512
+                        : rows < 2 * sms ? 1024
+                        : units <= 256  ? 64
+                        : units <= 512  ? 128
+                        : units <= 1024 ? 256
+                                        : 512;
+    const int keep = rows < sms ? 1 : !VECTOR ? 2 : rows < 2 * sms ? 1 : 4;
     const uint64_t per_cta = uint64_t(threads) * keep;
     const uint64_t want = (units + per_cta - 1) / per_cta;
     const int C = int(want > uint64_t(kQuantMaxCluster) ? kQuantMaxCluster : want);
@@ -458,7 +504,7 @@ static cudaError_t quant_launch(const Launch &L, const NormE4m3Launch &N, Launch
                : threads == 512 ? ar_rmsnorm_e4m3_kernel<T, P, 512, 4, true>
                                 : ar_rmsnorm_e4m3_kernel<T, P, 256, 4, true>;
     } else {
-        kern = threads == 128 ? ar_rmsnorm_e4m3_kernel<T, P, 128, 1, false> : ar_rmsnorm_e4m3_kernel<T, P, 256, 4, false>;
+        kern = threads == 128 ? ar_rmsnorm_e4m3_kernel<T, P, 128, 1, false> : ar_rmsnorm_e4m3_kernel<T, P, 512, 2, false>;
     }
     const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, a);
     if (err != cudaSuccess) return err;
