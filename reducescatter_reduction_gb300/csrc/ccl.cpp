@@ -341,6 +341,10 @@ extern "C" int ccl_bounds_checked(void)
 extern "C" ccl_status_t ccl_comm_last_launch(ccl_comm_t c, char *buf, size_t len)
 {
     if (!c || !buf || len == 0) return fail(CCL_ERR_INVALID_ARG, "NULL comm or buffer");
+    if (c->describe) {
+        c->describe(c);
+        c->describe = nullptr;
+    }
     snprintf(buf, len, "%s", c->last);
     return CCL_OK;
 }
@@ -572,6 +576,7 @@ static ccl_status_t run(ccl_comm *c, int coll, int op, int dtype, size_t n, int 
         }
     }
     c->launches += uint64_t(info.kernels);
+    c->describe = nullptr;
     snprintf(c->last, sizeof c->last,
              "%s dtype=%s op=%s p=%d n=%zu schedule=%s variant=%s vec=%d grid=%d block=%d smem=%zu sm_budget=%d "
              "counter=%d inplace=%d",
@@ -682,12 +687,22 @@ extern "C" ccl_status_t ccl_allreduce_residual_rmsnorm(ccl_comm_t c, ccl_dtype_t
     LaunchInfo info;
     cudaError_t err = launch_allreduce_rmsnorm(L, N, &info);
     c->launches += uint64_t(info.kernels);
+    c->describe = nullptr;
     snprintf(c->last, sizeof c->last,
              "%s dtype=%s op=sum p=%d n=%zu rows=%zu hidden=%zu schedule=%s vec=%d grid=%d block=%d", info.kernel,
              kDtypeName[dtype], p, n, rows, hidden, kSchedName[sched], L.vec ? 1 : 0, info.grid, info.block);
     if (debug_on()) fprintf(stderr, "[ccl] %s\n", c->last);
     if (err != cudaSuccess) return cuda_fail(err, "allreduce_residual_rmsnorm");
     return CCL_OK;
+}
+
+static void describe_norm_e4m3(ccl_comm *c)
+{
+    snprintf(c->last, sizeof c->last,
+             "%s dtype=%s op=sum p=%d n=%llu rows=%llu hidden=%llu group=%llu schedule=%s vec=%llu grid=%d block=%d", c->call.kernel,
+             kDtypeName[c->call_dtype], c->p, (unsigned long long)c->call_size[0], (unsigned long long)c->call_size[1],
+             (unsigned long long)c->call_size[2], (unsigned long long)c->call_size[3], c->call_word, (unsigned long long)c->call_size[4],
+             c->call.grid, c->call.block);
 }
 
 extern "C" ccl_status_t ccl_allreduce_residual_rmsnorm_e4m3(ccl_comm_t c, ccl_dtype_t dtype, size_t rows, size_t hidden,
@@ -776,10 +791,16 @@ extern "C" ccl_status_t ccl_allreduce_residual_rmsnorm_e4m3(ccl_comm_t c, ccl_dt
                             : dtype == CCL_F16 ? launch_allreduce_rmsnorm_e4m3_f16(L, N, &info)
                                                : launch_allreduce_rmsnorm_e4m3_bf16(L, N, &info);
     c->launches += uint64_t(info.kernels);
-    snprintf(c->last, sizeof c->last,
-             "%s dtype=%s op=sum p=%d n=%zu rows=%zu hidden=%zu group=%zu schedule=%s vec=%d grid=%d block=%d", info.kernel,
-             kDtypeName[dtype], p, n, rows, hidden, group, kSchedName[sched], L.vec ? 1 : 0, info.grid, info.block);
-    if (debug_on()) fprintf(stderr, "[ccl] %s\n", c->last);
+    c->call = info;
+    c->call_word = kSchedName[sched];
+    c->call_dtype = dtype;
+    const uint64_t sizes[5] = {n, rows, hidden, group, L.vec ? 1u : 0u};
+    memcpy(c->call_size, sizes, sizeof sizes);
+    c->describe = describe_norm_e4m3;
+    if (debug_on()) {
+        describe_norm_e4m3(c);
+        fprintf(stderr, "[ccl] %s\n", c->last);
+    }
     if (err != cudaSuccess) return cuda_fail(err, what);
     return CCL_OK;
 }

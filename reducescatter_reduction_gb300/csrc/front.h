@@ -47,15 +47,29 @@ inline Launch make_launch(ccl_comm *c, int dtype, bool alias, void *stream)
     return L;
 }
 
+inline void describe_rows(ccl_comm *c)
+{
+    snprintf(c->last, sizeof c->last, "%s dtype=%s p=%d rows=%llu columns=%llu pass=%s grid=%d block=%d smem=%zu kernels=%d", c->call.kernel,
+             kDtypeName[c->call_dtype], c->p, (unsigned long long)c->call_size[0], (unsigned long long)c->call_size[1], c->call_word, c->call.grid,
+             c->call.block, c->call.smem, c->call.kernels);
+}
+
 inline ccl_status_t finish(ccl_comm *c, cudaError_t err, const LaunchInfo &info, int dtype, size_t rows, size_t cols, const char *what,
                            const char *pass)
 {
     if (err == kTooManyPieces && info.kernels == 0)
         return fail(CCL_ERR_UNSUPPORTED, "%s: %zu rows of %zu columns over %d ranks are more than 2^31 - 1 pieces", what, rows, cols, c->p);
     c->launches += uint64_t(info.kernels);
-    snprintf(c->last, sizeof c->last, "%s dtype=%s p=%d rows=%zu columns=%zu pass=%s grid=%d block=%d smem=%zu kernels=%d", info.kernel,
-             kDtypeName[dtype], c->p, rows, cols, pass, info.grid, info.block, info.smem, info.kernels);
-    if (debug_on()) fprintf(stderr, "[ccl] %s\n", c->last);
+    c->call = info;
+    c->call_word = pass;
+    c->call_dtype = dtype;
+    c->call_size[0] = rows;
+    c->call_size[1] = cols;
+    c->describe = describe_rows;
+    if (debug_on()) {
+        describe_rows(c);
+        fprintf(stderr, "[ccl] %s\n", c->last);
+    }
     return err == cudaSuccess ? CCL_OK : cuda_fail(err, what);
 }
 
