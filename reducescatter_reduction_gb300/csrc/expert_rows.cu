@@ -4,8 +4,10 @@
 //   dispatch  row[slot_tj] = w_tj x_t
 //   combine   y_t          = sum_j w_tj row[slot_tj]
 //   gradient  drow[slot_tj] = w_tj dy_t,  dw_tj = <dy_t, row[slot_tj]>
-// Each is driven by the tokens: a CTA takes one, so a token's row is read (or
-// written) once and its k expert rows once each, which is all the traffic there has to be.
+// Each is driven by the tokens: a team of 32 to 256 threads takes one, so a
+// token's row is read (or written) once and its k expert rows once each, which
+// is all the traffic there has to be.  A thread loads a batch of KB choices of
+// UN units before it uses the first.
 #include "logits.cuh"
 
 namespace ccl {
@@ -25,6 +27,7 @@ struct RowsArgs {
     uint32_t rows, p, k, capacity, slot_end;   // slot_end: p * capacity
     FastDiv by_rows, by_capacity;
     int weighted;
+    int team_shift;       // a team has 2^team_shift threads
     // checked build:
     unsigned *status;
     uint32_t held;        // tokens that every token buffer and list has: `rows`, or one less where the debug hook wants the checks to fail
@@ -46,179 +49,263 @@ __device__ __forceinline__ bool entry_held(const RowsArgs<PM> &a, uint64_t entry
     return in_bounds(entry < uint64_t(a.held) * a.k, a.status, kSiteExperts, entry);
 }
 
-// A unit of a row: a 16-byte group, or one element where rows are not groups.
-template <typename T, bool VECTOR>
-struct RowUnit;
-template <typename T>
-struct RowUnit<T, true> {
+// A unit of a row: 16 bytes, 4 bytes or one element.
+template <typename T, int BYTES>
+struct RowUnit {
     using Tr = Traits<T>;
-    static constexpr int N = Tr::VEC, BYTES = 16;
-    using Raw = uint4;
-    __device__ static __forceinline__ Raw load(const void *p) { return ld_stream_v4(p); }
-    __device__ static __forceinline__ void store(void *p, const Raw &v) { st_stream_v4(p, v); }
-    __device__ static __forceinline__ void unpack(const Raw &v, typename Tr::Acc (&f)[N]) { Tr::unpack(v, f); }
-    __device__ static __forceinline__ Raw pack(const typename Tr::Acc (&f)[N]) { return Tr::pack(f); }
-};
-template <typename T>
-struct RowUnit<T, false> {
-    using Tr = Traits<T>;
-    static constexpr int N = 1, BYTES = 16 / Tr::VEC;
-    using Raw = typename std::conditional<BYTES == 2, uint16_t, uint32_t>::type;
-    __device__ static __forceinline__ Raw load(const void *p) { return *static_cast<const Raw *>(p); }
-    __device__ static __forceinline__ void store(void *p, const Raw &v) { *static_cast<Raw *>(p) = v; }
-    __device__ static __forceinline__ void unpack(const Raw &v, typename Tr::Acc (&f)[1]) { f[0] = Tr::load1(&v, 0); }
-    __device__ static __forceinline__ Raw pack(const typename Tr::Acc (&f)[1])
+    using Acc = typename Tr::Acc;
+    static constexpr int S = 16 / Tr::VEC, N = BYTES / S;
+    using Raw = typename std::conditional<BYTES == 16, uint4, typename std::conditional<BYTES == 4, uint32_t, uint16_t>::type>::type;
+    __device__ static __forceinline__ Raw zero()
     {
-        Raw v;
-        Tr::store1(&v, 0, f[0]);
-        return v;
+        if constexpr (BYTES == 16) return make_uint4(0, 0, 0, 0);
+        else return Raw(0);
+    }
+    __device__ static __forceinline__ Raw load(const void *p)
+    {
+        if constexpr (BYTES == 16) return ld_stream_v4(p);
+        else return __ldg(static_cast<const Raw *>(p));
+    }
+    __device__ static __forceinline__ void store(void *p, const Raw &v)
+    {
+        if constexpr (BYTES == 16) st_stream_v4(p, v);
+        else *static_cast<Raw *>(p) = v;
+    }
+    __device__ static __forceinline__ void unpack(const Raw &v, Acc (&f)[N])
+    {
+        if constexpr (BYTES == 16) {
+            Tr::unpack(v, f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[i] = Tr::load1(&v, i);
+        }
+    }
+    __device__ static __forceinline__ Raw pack(const Acc (&f)[N])
+    {
+        if constexpr (BYTES == 16) {
+            return Tr::pack(f);
+        } else {
+            Raw v;
+#pragma unroll
+            for (int i = 0; i < N; ++i) Tr::store1(&v, i, f[i]);
+            return v;
+        }
     }
 };
 
-// One choice of the CTA's token: where its row begins, and its weight.
+// One choice of a team's token: where its row begins, and its weight.
 struct Choice {
     char *row;            // null: none
     float weight;
     uint32_t rank;
 };
 
-// Choices first, first + 1, ... of token `t` of rank `r` into shared memory; `of` has the experts' buffers.
+// A team of threads, its token and its choices.
 template <int PM>
-__device__ __forceinline__ void read_choices(const RowsArgs<PM> &a, uint32_t r, uint32_t t, const void *const *of, uint32_t element,
-                                             Choice *list)
-{
-    for (uint32_t j = threadIdx.x; j < a.k; j += kRowsThreads) {
-        const uint64_t entry = uint64_t(t) * a.k + j;
-        Choice c = {nullptr, 1.0f, 0};
-        if (entry_held(a, entry)) {
-            const uint32_t slot = uint32_t(a.slots[r][entry]);
-            if (a.weighted) c.weight = a.weights[r][entry];
-            if (slot < a.slot_end) {
-                c.rank = div_by(slot, a.by_capacity);
-                c.row = static_cast<char *>(const_cast<void *>(of[c.rank])) + uint64_t(slot - c.rank * a.capacity) * a.hidden * element;
-            }
-        }
-        list[j] = c;
-    }
-    __syncthreads();
-}
+struct Team {
+    uint32_t thread, threads;   // of the team
+    uint32_t rank, token;
+    uint64_t first, end;        // the team's units
+    bool on;                    // it has a token
+    Choice *list;
 
-template <typename T, int PM, bool VECTOR>
-__global__ void __launch_bounds__(kRowsThreads) dispatch_kernel(const __grid_constant__ RowsArgs<PM> a)
-{
-    using U = RowUnit<T, VECTOR>;
-    constexpr uint32_t S = 16 / Traits<T>::VEC;
-    extern __shared__ Choice list[];
-    grid_dependency_wait();
-    grid_dependents_launch();
-    const uint32_t r = div_by(blockIdx.x, a.by_rows), t = blockIdx.x - r * a.rows;
-    read_choices(a, r, t, a.out, S, list);
-    const char *token = static_cast<const char *>(a.in[r]) + uint64_t(t) * a.hidden * S;
-    const uint64_t units = a.hidden / U::N;
-    for (uint64_t u = threadIdx.x; u < units; u += kRowsThreads) {
-        if (!token_held(a, a.in[r], token + u * U::BYTES, U::BYTES, S)) continue;
-        const typename U::Raw v = U::load(token + u * U::BYTES);
-        typename Traits<T>::Acc f[U::N], g[U::N];
-        U::unpack(v, f);
-        for (uint32_t j = 0; j < a.k; ++j) {
-            const Choice c = list[j];
-            if (!c.row || !row_of_expert_held(a, a.out[c.rank], c.row + u * U::BYTES, U::BYTES, S)) continue;
-            typename U::Raw w = v;
-            if constexpr (!std::is_same<T, I32>::value) {
-                if (a.weighted) {
-#pragma unroll
-                    for (int i = 0; i < U::N; ++i) g[i] = __fmul_rn(f[i], c.weight);
-                    w = U::pack(g);
+    // `of` has the experts' buffers; `list` room for the choices of all teams.
+    __device__ __forceinline__ Team(const RowsArgs<PM> &a, const void *const *of, uint32_t S, uint32_t bytes, Choice *all)
+    {
+        threads = 1u << a.team_shift;
+        thread = threadIdx.x & (threads - 1);
+        const uint32_t team = threadIdx.x >> a.team_shift, t = blockIdx.x * (kRowsThreads >> a.team_shift) + team;
+        on = t < a.rows * a.p;
+        rank = on ? div_by(t, a.by_rows) : 0;
+        token = t - rank * a.rows;
+        const uint64_t units = a.hidden * S / bytes;
+        first = units * blockIdx.y / gridDim.y + thread;
+        end = on ? units * (blockIdx.y + 1) / gridDim.y : 0;
+        list = all + team * a.k;
+        for (uint32_t j = thread; j < a.k; j += threads) {
+            const uint64_t entry = uint64_t(token) * a.k + j;
+            Choice c = {nullptr, 1.0f, 0};
+            if (on && entry_held(a, entry)) {
+                const uint32_t slot = uint32_t(a.slots[rank][entry]);
+                if (a.weighted) c.weight = a.weights[rank][entry];
+                if (slot < a.slot_end) {
+                    c.rank = div_by(slot, a.by_capacity);
+                    c.row = static_cast<char *>(const_cast<void *>(of[c.rank])) + uint64_t(slot - c.rank * a.capacity) * a.hidden * S;
                 }
             }
-            U::store(c.row + u * U::BYTES, w);
+            list[j] = c;
         }
+        __syncthreads();
     }
-}
+};
 
-template <typename T, int PM, bool VECTOR>
-__global__ void __launch_bounds__(kRowsThreads) combine_kernel(const __grid_constant__ RowsArgs<PM> a)
+template <typename T, int PM, int BYTES, int UN>
+__global__ void __launch_bounds__(kRowsThreads) dispatch_kernel(const __grid_constant__ RowsArgs<PM> a)
 {
-    using U = RowUnit<T, VECTOR>;
-    constexpr uint32_t S = 16 / Traits<T>::VEC;
-    extern __shared__ Choice list[];
+    using U = RowUnit<T, BYTES>;
+    constexpr uint32_t S = U::S;
+    extern __shared__ Choice lists[];
     grid_dependency_wait();
     grid_dependents_launch();
-    const uint32_t r = div_by(blockIdx.x, a.by_rows), t = blockIdx.x - r * a.rows;
-    read_choices(a, r, t, a.in, S, list);
-    char *token = static_cast<char *>(a.out[r]) + uint64_t(t) * a.hidden * S;
-    const uint64_t units = a.hidden / U::N;
-    for (uint64_t u = threadIdx.x; u < units; u += kRowsThreads) {
-        float sum[U::N], f[U::N];
+    const Team<PM> t(a, a.out, S, BYTES, lists);
+    const char *token = static_cast<const char *>(a.in[t.rank]) + uint64_t(t.token) * a.hidden * S;
+    for (uint64_t u = t.first; u < t.end; u += UN * t.threads) {
+        typename U::Raw v[UN];
 #pragma unroll
-        for (int i = 0; i < U::N; ++i) sum[i] = 0.0f;
-        for (uint32_t j = 0; j < a.k; ++j) {
-            const Choice c = list[j];
-            if (!c.row || !row_of_expert_held(a, a.in[c.rank], c.row + u * U::BYTES, U::BYTES, S)) continue;
-            U::unpack(U::load(c.row + u * U::BYTES), f);
-#pragma unroll
-            for (int i = 0; i < U::N; ++i) sum[i] = fmaf(c.weight, f[i], sum[i]);
+        for (int n = 0; n < UN; ++n) {
+            const char *at = token + (u + n * t.threads) * BYTES;
+            if (u + n * t.threads < t.end && token_held(a, a.in[t.rank], at, BYTES, S)) v[n] = U::load(at);
         }
-        if (token_held(a, a.out[r], token + u * U::BYTES, U::BYTES, S)) U::store(token + u * U::BYTES, U::pack(sum));
+        for (uint32_t j = 0; j < a.k; ++j) {
+            const Choice c = t.list[j];
+            if (!c.row) continue;
+#pragma unroll
+            for (int n = 0; n < UN; ++n) {
+                const uint64_t at = (u + n * t.threads) * BYTES;
+                if (u + n * t.threads >= t.end || !token_held(a, a.in[t.rank], token + at, BYTES, S) ||
+                    !row_of_expert_held(a, a.out[c.rank], c.row + at, BYTES, S))
+                    continue;
+                typename U::Raw w = v[n];
+                if constexpr (!std::is_same<T, I32>::value) {
+                    if (a.weighted) {
+                        float f[U::N];
+                        U::unpack(w, f);
+#pragma unroll
+                        for (int i = 0; i < U::N; ++i) f[i] = __fmul_rn(f[i], c.weight);
+                        w = U::pack(f);
+                    }
+                }
+                U::store(c.row + at, w);
+            }
+        }
     }
 }
 
-template <typename T, int PM, bool VECTOR>
+template <typename T, int PM, int BYTES, int KB, int UN>
+__global__ void __launch_bounds__(kRowsThreads) combine_kernel(const __grid_constant__ RowsArgs<PM> a)
+{
+    using U = RowUnit<T, BYTES>;
+    constexpr uint32_t S = U::S;
+    extern __shared__ Choice lists[];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const Team<PM> t(a, a.in, S, BYTES, lists);
+    char *token = static_cast<char *>(a.out[t.rank]) + uint64_t(t.token) * a.hidden * S;
+    for (uint64_t u = t.first; u < t.end; u += UN * t.threads) {
+        float sum[UN][U::N];
+#pragma unroll
+        for (int n = 0; n < UN; ++n)
+#pragma unroll
+            for (int i = 0; i < U::N; ++i) sum[n][i] = 0.0f;
+        for (uint32_t first = 0; first < a.k; first += KB) {
+            typename U::Raw z[KB][UN];
+#pragma unroll
+            for (int j = 0; j < KB; ++j) {
+                const Choice c = first + j < a.k ? t.list[first + j] : Choice{nullptr, 0.0f, 0};
+#pragma unroll
+                for (int n = 0; n < UN; ++n) {
+                    const char *at = c.row + (u + n * t.threads) * BYTES;
+                    z[j][n] = U::zero();
+                    if (c.row && u + n * t.threads < t.end && row_of_expert_held(a, a.in[c.rank], at, BYTES, S)) z[j][n] = U::load(at);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < KB; ++j) {
+                if (first + j >= a.k) break;
+                const Choice c = t.list[first + j];
+                if (!c.row) continue;
+#pragma unroll
+                for (int n = 0; n < UN; ++n) {
+                    float f[U::N];
+                    U::unpack(z[j][n], f);
+#pragma unroll
+                    for (int i = 0; i < U::N; ++i) sum[n][i] = fmaf(c.weight, f[i], sum[n][i]);
+                }
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < UN; ++n) {
+            char *at = token + (u + n * t.threads) * BYTES;
+            if (u + n * t.threads < t.end && token_held(a, a.out[t.rank], at, BYTES, S)) U::store(at, U::pack(sum[n]));
+        }
+    }
+}
+
+template <typename T, int PM, int BYTES, int KB, int UN>
 __global__ void __launch_bounds__(kRowsThreads) combine_grad_kernel(const __grid_constant__ RowsArgs<PM> a)
 {
-    using U = RowUnit<T, VECTOR>;
-    constexpr uint32_t S = 16 / Traits<T>::VEC;
-    constexpr int KB = 8;      // choices whose products are summed at a time
-    extern __shared__ Choice list[];
+    using U = RowUnit<T, BYTES>;
+    constexpr uint32_t S = U::S;
+    extern __shared__ Choice lists[];
     __shared__ float parts[kRowsThreads / 32][KB];
     grid_dependency_wait();
     grid_dependents_launch();
-    const uint32_t r = div_by(blockIdx.x, a.by_rows), t = blockIdx.x - r * a.rows;
-    read_choices(a, r, t, a.out, S, list);
-    const char *token = static_cast<const char *>(a.in[r]) + uint64_t(t) * a.hidden * S;
-    const uint64_t units = a.hidden / U::N;
-    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const Team<PM> t(a, a.out, S, BYTES, lists);
+    const char *token = static_cast<const char *>(a.in[t.rank]) + uint64_t(t.token) * a.hidden * S;
+    const uint32_t warps = t.threads / 32, warp = threadIdx.x / 32;
     for (uint32_t first = 0; first < a.k; first += KB) {
         float sum[KB];
 #pragma unroll
         for (int j = 0; j < KB; ++j) sum[j] = 0.0f;
-        for (uint64_t u = threadIdx.x; u < units; u += kRowsThreads) {
-            if (!token_held(a, a.in[r], token + u * U::BYTES, U::BYTES, S)) continue;
-            float f[U::N], g[U::N];
-            U::unpack(U::load(token + u * U::BYTES), f);
+        for (uint64_t u = t.first; u < t.end; u += UN * t.threads) {
+            typename U::Raw v[UN], z[KB][UN];
+#pragma unroll
+            for (int n = 0; n < UN; ++n) {
+                const char *at = token + (u + n * t.threads) * BYTES;
+                v[n] = U::zero();
+                if (u + n * t.threads < t.end && token_held(a, a.in[t.rank], at, BYTES, S)) v[n] = U::load(at);
+            }
+#pragma unroll
+            for (int j = 0; j < KB; ++j) {
+                const Choice c = first + j < a.k ? t.list[first + j] : Choice{nullptr, 0.0f, 0};
+                const char *row = c.row ? static_cast<const char *>(a.experts[c.rank]) + (c.row - static_cast<char *>(a.out[c.rank])) : nullptr;
+#pragma unroll
+                for (int n = 0; n < UN; ++n) {
+                    const char *at = row + (u + n * t.threads) * BYTES;
+                    z[j][n] = U::zero();
+                    if (c.row && u + n * t.threads < t.end && row_of_expert_held(a, a.experts[c.rank], at, BYTES, S)) z[j][n] = U::load(at);
+                }
+            }
 #pragma unroll
             for (int j = 0; j < KB; ++j) {
                 if (first + j >= a.k) break;
-                const Choice c = list[first + j];
-                if (!c.row || !row_of_expert_held(a, a.out[c.rank], c.row + u * U::BYTES, U::BYTES, S)) continue;
-                const char *z = static_cast<const char *>(a.experts[c.rank]) + (c.row - static_cast<char *>(a.out[c.rank]));
-                U::unpack(U::load(z + u * U::BYTES), g);
+                const Choice c = t.list[first + j];
+                if (!c.row) continue;
 #pragma unroll
-                for (int i = 0; i < U::N; ++i) sum[j] = fmaf(f[i], g[i], sum[j]);
+                for (int n = 0; n < UN; ++n) {
+                    char *at = c.row + (u + n * t.threads) * BYTES;
+                    float f[U::N], g[U::N];
+                    U::unpack(v[n], f);
+                    U::unpack(z[j][n], g);
 #pragma unroll
-                for (int i = 0; i < U::N; ++i) g[i] = __fmul_rn(f[i], c.weight);
-                U::store(c.row + u * U::BYTES, U::pack(g));
+                    for (int i = 0; i < U::N; ++i) sum[j] = fmaf(f[i], g[i], sum[j]);
+#pragma unroll
+                    for (int i = 0; i < U::N; ++i) f[i] = __fmul_rn(f[i], c.weight);
+                    if (u + n * t.threads < t.end && token_held(a, a.in[t.rank], token + (u + n * t.threads) * BYTES, BYTES, S) &&
+                        row_of_expert_held(a, a.out[c.rank], at, BYTES, S))
+                        U::store(at, U::pack(f));
+                }
             }
         }
+        // the team's sums: its warps', in order
 #pragma unroll
         for (int j = 0; j < KB; ++j) {
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
-            if (lane == 0) parts[warp][j] = sum[j];
+            if (threadIdx.x % 32 == 0) parts[warp][j] = sum[j];
         }
         __syncthreads();
-        if (threadIdx.x < KB && first + threadIdx.x < a.k) {
+        if (t.on && t.thread < KB && first + t.thread < a.k) {
             float s = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kRowsThreads / 32; ++w) s += parts[w][threadIdx.x];
-            const uint64_t entry = uint64_t(t) * a.k + first + threadIdx.x;
-            if (entry_held(a, entry)) a.dweights[r][entry] = s;
+            for (uint32_t w = 0; w < warps; ++w) s += parts[warp + w][t.thread];
+            const uint64_t entry = uint64_t(t.token) * a.k + first + t.thread;
+            if (entry_held(a, entry)) a.dweights[t.rank][entry] = t.list[first + t.thread].row ? s : 0.0f;
         }
         __syncthreads();
     }
 }
 
-template <typename T, int PM, bool VECTOR>
+template <typename T, int PM, int BYTES, int KB, int UN>
 static cudaError_t rows_launch(const Launch &L, const RowsLaunch &N, LaunchInfo *info)
 {
     RowsArgs<PM> a = {};
@@ -241,30 +328,67 @@ static cudaError_t rows_launch(const Launch &L, const RowsLaunch &N, LaunchInfo 
     a.weighted = N.weights ? 1 : 0;
     a.status = L.status;
     a.held = a.rows - (L.stall_test == 2 ? 1 : 0);
-    const unsigned grid = a.rows * a.p;
-    const size_t smem = N.k * sizeof(Choice);
+    // a team has about four units a thread, and more threads where there are few tokens or many choices
+    const uint64_t units = N.hidden * elem_bytes(L.dtype) / BYTES, tokens = N.rows * uint64_t(L.p), sms = uint64_t(L.num_sms);
+    a.team_shift = 5;
+    while (a.team_shift < 8 && ((uint64_t(4 * UN) << a.team_shift) < units || tokens >> (8 - a.team_shift) < 4 * sms || N.k > 32)) ++a.team_shift;
+    const uint32_t teams = kRowsThreads >> a.team_shift;
+    const unsigned grid = unsigned((tokens + teams - 1) / teams);
+    // few tokens: a row over several CTAs (the gradient's sums stay in one)
+    uint64_t split = 1;
+    if (N.op != ROWS_GRAD && grid < 4 * sms) {
+        const uint64_t most = (units + kRowsThreads - 1) / kRowsThreads;
+        split = (4 * sms + grid - 1) / grid;
+        if (split > most) split = most;
+        if (split < 1) split = 1;
+    }
+    const size_t smem = teams * N.k * sizeof(Choice);
     static std::atomic<unsigned long long> ready[3];
     void (*kern)(RowsArgs<PM>) = nullptr;
     if constexpr (std::is_same<T, I32>::value)
-        kern = dispatch_kernel<T, PM, VECTOR>;
+        kern = dispatch_kernel<T, PM, BYTES, 4>;
     else
-        kern = N.op == ROWS_DISPATCH ? dispatch_kernel<T, PM, VECTOR> : N.op == ROWS_COMBINE ? combine_kernel<T, PM, VECTOR> : combine_grad_kernel<T, PM, VECTOR>;
+        kern = N.op == ROWS_DISPATCH ? dispatch_kernel<T, PM, BYTES, 4> : N.op == ROWS_COMBINE ? combine_kernel<T, PM, BYTES, KB, UN> : combine_grad_kernel<T, PM, BYTES, KB, UN>;
     cudaError_t err = smem > 48 * 1024 ? allow_dynamic_smem(kern, 4096 * sizeof(Choice), L.device, ready[N.op]) : cudaSuccess;
-    if (err == cudaSuccess) err = launch_dependent(kern, grid, kRowsThreads, smem, L.stream, a);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, unsigned(split));
+    cfg.blockDim = dim3(kRowsThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = L.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    err = cudaLaunchKernelEx(&cfg, kern, a);
     if (err != cudaSuccess) return err;
     info->kernel = N.op == ROWS_DISPATCH ? "expert_dispatch" : N.op == ROWS_COMBINE ? "expert_combine" : "expert_combine_grad";
-    info->grid = int(grid);
+    info->grid = int(grid * split);
     info->block = kRowsThreads;
     info->smem = smem;
     info->kernels = 1;
     return cudaSuccess;
 }
 
+// Units as wide as every address and the row allow.
+template <typename T, int PM>
+static cudaError_t rows_width(const Launch &L, const RowsLaunch &N, LaunchInfo *info)
+{
+    constexpr bool wide = Traits<T>::VEC == 4;
+    if (N.align >= 16) {
+        if (PM > 8 || N.k > 4 || N.op == ROWS_DISPATCH) return rows_launch<T, PM, 16, 8, 1>(L, N, info);
+        if constexpr (PM <= 8) return N.k > 2 ? rows_launch<T, PM, 16, 4, 2>(L, N, info) : rows_launch<T, PM, 16, 2, 4>(L, N, info);
+    }
+    if (wide || N.align >= 4) return rows_launch<T, PM, 4, 8, 4>(L, N, info);
+    if constexpr (!wide) return rows_launch<T, PM, 2, 8, 4>(L, N, info);
+    return cudaErrorInvalidValue;
+}
+
 template <typename T>
 static cudaError_t rows_dtype(const Launch &L, const RowsLaunch &N, LaunchInfo *info)
 {
-    if (L.p <= 8) return L.vec ? rows_launch<T, 8, true>(L, N, info) : rows_launch<T, 8, false>(L, N, info);
-    return L.vec ? rows_launch<T, kMaxRanks, true>(L, N, info) : rows_launch<T, kMaxRanks, false>(L, N, info);
+    return L.p <= 8 ? rows_width<T, 8>(L, N, info) : rows_width<T, kMaxRanks>(L, N, info);
 }
 
 cudaError_t launch_expert_rows(const Launch &L, const RowsLaunch &N, LaunchInfo *info)

@@ -88,12 +88,12 @@ static ccl_status_t expert_rows(ccl_comm *c, int op, int dtype, size_t rows, siz
     const size_t token_bytes = rows * hidden * es, expert_bytes = capacity * hidden * es;
     const bool to_tokens = op == ROWS_COMBINE;
     Spans s;
-    bool vec = hidden * es % 16 == 0;
+    uintptr_t bits = hidden * es | 16;       // of every address and the row's bytes
     for (int r = 0; r < c->p; ++r) {
         const uintptr_t in = uintptr_t(c->in[r]), out = uintptr_t(c->out[r]);
         if (in % es || out % es)
             return fail(CCL_ERR_INVALID_ARG, "a buffer of rank %d is not aligned to its elements (%zu bytes)", r, es);
-        vec = vec && in % 16 == 0 && out % 16 == 0;
+        bits |= in | out;
         s.add("the input of rank", r, c->in[r], to_tokens ? expert_bytes : token_bytes, false);
         s.add("the output of rank", r, c->out[r], to_tokens ? token_bytes : expert_bytes, true);
         s.add("slots", r, slots[r], rows * k * 4, false);
@@ -103,7 +103,7 @@ static ccl_status_t expert_rows(ccl_comm *c, int op, int dtype, size_t rows, siz
         if ((st = check_list(c, experts, "expert_rows", es)) != CCL_OK) return st;
         if ((st = check_list(c, dweights, "dweights", 4)) != CCL_OK) return st;
         for (int r = 0; r < c->p; ++r) {
-            vec = vec && uintptr_t(experts[r]) % 16 == 0;
+            bits |= uintptr_t(experts[r]);
             s.add("expert_rows", r, experts[r], expert_bytes, false);
             s.add("dweights", r, dweights[r], rows * k * 4, true);
         }
@@ -111,9 +111,9 @@ static ccl_status_t expert_rows(ccl_comm *c, int op, int dtype, size_t rows, siz
     if ((st = check_spans(s.s, size_t(s.n))) != CCL_OK) return st;
     DeviceGuard g(c->device);
     if (g.err != cudaSuccess) return cuda_fail(g.err, what);
-    Launch L = make_launch(c, dtype, false, stream);
-    L.vec = vec;
+    const Launch L = make_launch(c, dtype, false, stream);
     RowsLaunch N;
+    N.align = uint32_t(bits & (~bits + 1));
     N.op = op;
     N.rows = rows;
     N.hidden = hidden;
