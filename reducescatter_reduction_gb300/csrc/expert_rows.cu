@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kRowsThreads) dispatch_kernel(const __grid_con
 }
 
 template <typename T, int PM, int BYTES, int KB, int UN>
-__global__ void __launch_bounds__(kRowsThreads) combine_kernel(const __grid_constant__ RowsArgs<PM> a)
+__global__ void __launch_bounds__(kRowsThreads, BYTES == 16 && KB * UN == 8 ? 3 : 4) combine_kernel(const __grid_constant__ RowsArgs<PM> a)
 {
     using U = RowUnit<T, BYTES>;
     constexpr uint32_t S = U::S;
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kRowsThreads) combine_kernel(const __grid_cons
 }
 
 template <typename T, int PM, int BYTES, int KB, int UN>
-__global__ void __launch_bounds__(kRowsThreads) combine_grad_kernel(const __grid_constant__ RowsArgs<PM> a)
+__global__ void __launch_bounds__(kRowsThreads, BYTES == 16 && KB * UN == 8 ? 3 : 4) combine_grad_kernel(const __grid_constant__ RowsArgs<PM> a)
 {
     using U = RowUnit<T, BYTES>;
     constexpr uint32_t S = U::S;
@@ -371,17 +371,31 @@ static cudaError_t rows_launch(const Launch &L, const RowsLaunch &N, LaunchInfo 
     return cudaSuccess;
 }
 
-// Units as wide as every address and the row allow.
+// Units as wide as every address and the row allow, and batches by the number
+// of choices.  Measured (graph replay, us; 16-byte units unless said; batches
+// as choices x units):
+//   combine, 8 x 4000 x 4096 bf16, k=2       2x4 102   2x2 106
+//   combine's gradient, the same             2x4 160   2x2 162-170
+//   gradient, 4 x 20000 x 512 f16, k=1       2x4 64    2x2 48: a row of 64 units fills two for each of 32 threads
+//   gradient, 8 x 4000 x 2048 bf16, k=4      4x2 155
+//   gradient, 2 x 4000 x 1002 f16, k=3       4-byte units, 8x4 27   4x2 30
+//   gradient, 2 x 4000 x 1001 bf16, k=4      2-byte units, 8x4 104  4x2 94
+//   combine, the same                        2-byte units, 8x4 52   4x2 36
+// with the registers held to three CTAs an SM for 8 units of 16 bytes (four:
+// 8 x 2048 x 7168 bf16, k=8, 602 and not 587) and to four for the others.
 template <typename T, int PM>
 static cudaError_t rows_width(const Launch &L, const RowsLaunch &N, LaunchInfo *info)
 {
     constexpr bool wide = Traits<T>::VEC == 4;
     if (N.align >= 16) {
         if (PM > 8 || N.k > 4 || N.op == ROWS_DISPATCH) return rows_launch<T, PM, 16, 8, 1>(L, N, info);
-        if constexpr (PM <= 8) return N.k > 2 ? rows_launch<T, PM, 16, 4, 2>(L, N, info) : rows_launch<T, PM, 16, 2, 4>(L, N, info);
+        if constexpr (PM <= 8) {
+            if (N.k > 2) return rows_launch<T, PM, 16, 4, 2>(L, N, info);
+            return N.hidden < 128 * Traits<T>::VEC ? rows_launch<T, PM, 16, 2, 2>(L, N, info) : rows_launch<T, PM, 16, 2, 4>(L, N, info);
+        }
     }
     if (wide || N.align >= 4) return rows_launch<T, PM, 4, 8, 4>(L, N, info);
-    if constexpr (!wide) return rows_launch<T, PM, 2, 8, 4>(L, N, info);
+    if constexpr (!wide) return rows_launch<T, PM, 2, 4, 2>(L, N, info);
     return cudaErrorInvalidValue;
 }
 
