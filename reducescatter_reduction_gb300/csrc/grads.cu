@@ -1,10 +1,15 @@
 // The global norm of many gradient tensors, and their clipping by it.
 //
 //   norm = sqrt(sum x^2),  out = x min(1, max_norm / (norm + 1e-6))
-// A tensor is cut into tiles of 16-byte groups that lie on 16-byte boundaries
-// of memory wherever the tensor begins; the tiles of all tensors are numbered
+// A tensor is cut into tiles of 16-byte groups that begin on 128-byte boundaries
+// of memory wherever the tensor begins (on 16-byte boundaries a warp's
+// loads go over 17 sectors, not 16: with that and the sums below, the norm of 300 bf16 tensors of 1.2 GB 190 -> 177 us,
+// their clipping 391 -> 374); the tiles of all tensors are numbered
 // through, and a CTA takes consecutive ones, so tensors of any size share the
-// SMs evenly.  The tensors' addresses travel as kernel parameters.
+// SMs evenly.  The tensors' addresses and each CTA's first tensor travel as
+// kernel parameters.  Bound by memory where the tensors are large: three
+// passes over 300 bf16 tensors of 1.2 GB, out of place, in 580 us, 6.2 TB/s; below some MB by the
+// launches and the join of the CTAs' sums (3 + 2 us for 1000 values).
 #include "logits.cuh"
 
 namespace ccl {
@@ -13,6 +18,11 @@ constexpr unsigned kSiteGrads = 13;
 constexpr int kGradThreads = 256;
 constexpr int kGradBatch = 4;                                    // groups a thread has of a tile
 constexpr uint32_t kGradTile = kGradThreads * kGradBatch;        // groups of a tile
+constexpr uint32_t kGradMaxGrid = 1280;
+// CTAs an SM at most.  Measured (us; 4 against 8 an SM): the norm of 400 f32 tensors of 12 MB 7.3, 10.3, of 20 bf16 ones of 100 MB
+// 17.9, 20.5, of 300 of 1.2 GB 177, 179; clipping the last 402, 374.
+constexpr uint32_t kGradNormCtas = 4, kGradClipCtas = 8;
+static_assert(kGradMaxGrid <= kMaxPartials, "");
 
 struct GradRecord {
     const void *in;
@@ -25,6 +35,7 @@ struct GradRecord {
 template <int CAP>
 struct GradArgs {
     GradRecord t[CAP];
+    uint16_t start[kGradMaxGrid];        // the tensor of a CTA's first tile
     uint32_t count, tiles;
     float max_norm;
     int first_launch, last_launch;
@@ -48,7 +59,7 @@ template <typename T>
 struct GradGroups {
     using Tr = Traits<T>;
     static constexpr uint32_t VEC = Tr::VEC, S = 16 / VEC;
-    uintptr_t base;      // the boundary at or below the tensor's begin
+    uintptr_t base;      // the 128-byte boundary at or below the tensor's begin
     uint64_t first;      // this thread's first group
     uint64_t n;
     uint32_t shift;      // elements between the boundary and the tensor
@@ -58,7 +69,7 @@ struct GradGroups {
     __device__ __forceinline__ bool inside(uint64_t at) const { return at >= shift && at < shift + n; }
     __device__ __forceinline__ GradGroups(const GradRecord &t, uint32_t tile, uint32_t short_by, unsigned *status)
     {
-        base = uintptr_t(t.in) & ~uintptr_t(15);
+        base = uintptr_t(t.in) & ~uintptr_t(127);
         shift = uint32_t(uintptr_t(t.in) - base) / S;
         n = t.n;
         first = uint64_t(tile - t.first) * kGradTile + threadIdx.x;
@@ -69,7 +80,7 @@ struct GradGroups {
             const char *at = reinterpret_cast<const char *>(base) + g * 16;
             if (whole(g)) {
                 if (grad_held(t.in, n, at, 16, S, short_by, status)) v[i] = ld_coherent_v4(at);
-            } else if (g * VEC < shift + n) {
+            } else if (g * VEC < shift + n && (g + 1) * VEC > shift) {
                 float f[VEC];
 #pragma unroll
                 for (uint32_t e = 0; e < VEC; ++e) {
@@ -82,69 +93,65 @@ struct GradGroups {
     }
 };
 
+// A sum and what its roundings left out (Knuth's two-sum): fp32 twice, as
+// this GPU takes 16 cycles for a warp's fp64 addition.  (The norm of 400 f32
+// tensors, 1000 tiles: with an fp64 sum in every thread 14.8 us, with these 10.3.)
+struct Twofold {
+    float hi = 0.0f, lo = 0.0f;
+    __device__ __forceinline__ void add(float v)
+    {
+        const float s = __fadd_rn(hi, v), b = __fsub_rn(s, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(v, b)));
+        hi = s;
+    }
+    __device__ __forceinline__ void add(const Twofold &o)
+    {
+        add(o.hi);
+        lo = __fadd_rn(lo, o.lo);
+    }
+};
+
 // The sum of the squares of a thread's groups.  In fp32 where that loses
 // nothing: squares below 2^-149 vanish, and those below 2^-126 lose digits, but
-// beside a sum of 2^-80 neither is seen.  Smaller and larger sums, infinities and NaN go through fp64,
-// element by element.
+// beside a sum of 2^-100 neither is seen; sums up to 2^100, of 2^18 tiles and
+// 2^8 threads, stay in range.  Smaller and larger sums, infinities and NaN go
+// through fp64, element by element, and into `rest`.
 template <typename T>
-__device__ __forceinline__ double grad_squares(const GradRecord &t, uint32_t tile, uint32_t short_by, unsigned *status)
+__device__ __forceinline__ void grad_squares(const GradRecord &t, uint32_t tile, uint32_t short_by, unsigned *status, Twofold &sum, double &rest)
 {
     using G = GradGroups<T>;
     const G g(t, tile, short_by, status);
-    float part[kGradBatch];
+    Pair part[2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll
-    for (int i = 0; i < kGradBatch; ++i) {
-        float f[G::VEC];
-        Traits<T>::unpack(g.v[i], f);
-        float a = 0.0f, b = 0.0f;
+    for (int i = 0; i < kGradBatch; ++i)
 #pragma unroll
-        for (uint32_t e = 0; e < G::VEC; e += 2) {
-            a = fmaf(f[e], f[e], a);
-            b = fmaf(f[e + 1], f[e + 1], b);
+        for (int e = 0; e < Group<T>::PAIRS; ++e) {
+            const Pair f = Group<T>::pair(g.v[i], e);
+            part[e % 2] = fma(f, f, part[e % 2]);
         }
-        part[i] = a + b;
+    const Pair both = part[0] + part[1];
+    const float s = both.x + both.y;
+    if (s >= 0x1p-100f && s <= 0x1p100f) {
+        sum.add(s);
+        return;
     }
-    const float s = (part[0] + part[1]) + (part[2] + part[3]);
-    if (s >= 0x1p-80f && s <= 0x1p126f) return double(s);
-    double d = 0.0;
     uint32_t any = 0;
 #pragma unroll
     for (int i = 0; i < kGradBatch; ++i) any |= g.v[i].x | g.v[i].y | g.v[i].z | g.v[i].w;
-    if (any == 0) return d;
+    if (any == 0) return;
 #pragma unroll
     for (int i = 0; i < kGradBatch; ++i) {
         float f[G::VEC];
         Traits<T>::unpack(g.v[i], f);
 #pragma unroll
-        for (uint32_t e = 0; e < G::VEC; ++e) d = ::fma(double(f[e]), double(f[e]), d);
+        for (uint32_t e = 0; e < G::VEC; ++e) rest = ::fma(double(f[e]), double(f[e]), rest);
     }
-    return d;
 }
 
-// The tensor that has a tile.
-template <int CAP>
-__device__ __forceinline__ uint32_t grad_tensor(const GradArgs<CAP> &a, uint32_t tile)
+__device__ __forceinline__ double warp_sum(double v)
 {
-    uint32_t lo = 0, hi = a.count;      // t[lo].first <= tile < t[hi].first
-    while (hi - lo > 1) {
-        const uint32_t mid = (lo + hi) / 2;
-        if (a.t[mid].first <= tile) lo = mid;
-        else hi = mid;
-    }
-    return lo;
-}
-
-__device__ __forceinline__ double block_sum(double v)
-{
-    __shared__ double red[kGradThreads / 32];
-    __syncthreads();
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
-    __syncthreads();
-    v = 0.0;
-#pragma unroll
-    for (int w = 0; w < kGradThreads / 32; ++w) v += red[w];
     return v;
 }
 
@@ -155,31 +162,65 @@ __global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const __grid_co
     grid_dependency_wait();
     grid_dependents_launch();
     const uint32_t begin = uint32_t(uint64_t(a.tiles) * blockIdx.x / gridDim.x), end = uint32_t(uint64_t(a.tiles) * (blockIdx.x + 1) / gridDim.x);
-    double sum = 0.0;
-    uint32_t i = begin < end ? grad_tensor(a, begin) : 0;
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    Twofold mine;
+    double rest = 0.0;
+    uint32_t i = a.start[blockIdx.x];
     for (uint32_t tile = begin; tile < end; ++tile) {
         while (i + 1 < a.count && a.t[i + 1].first <= tile) ++i;
         const GradRecord &t = a.t[i];
-        sum += t.dtype == DT_F32 ? grad_squares<F32>(t, tile, a.short_by, a.status) : t.dtype == DT_F16 ? grad_squares<F16>(t, tile, a.short_by, a.status)
-                                                                                               : grad_squares<BF16>(t, tile, a.short_by, a.status);
+        if (t.dtype == DT_F32) grad_squares<F32>(t, tile, a.short_by, a.status, mine, rest);
+        else if (t.dtype == DT_F16) grad_squares<F16>(t, tile, a.short_by, a.status, mine, rest);
+        else grad_squares<BF16>(t, tile, a.short_by, a.status, mine, rest);
     }
-    sum = block_sum(sum);
-    if (threadIdx.x == 0) {
-        a.partials[blockIdx.x] = sum;
-        __threadfence();
-        last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+    // the CTA's sum, in a fixed order
+    __shared__ Twofold part_s[kGradThreads / 32];
+    __shared__ double rest_s[kGradThreads / 32];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        Twofold other;
+        other.hi = __shfl_xor_sync(0xffffffffu, mine.hi, o);
+        other.lo = __shfl_xor_sync(0xffffffffu, mine.lo, o);
+        mine.add(other);
+    }
+    if (__any_sync(0xffffffffu, rest != 0.0)) rest = warp_sum(rest);     // (NaN is not 0)
+    if (lane == 0) {
+        part_s[warp] = mine;
+        rest_s[warp] = rest;
     }
     __syncthreads();
-    if (!last) return;
-    __threadfence();
-    sum = 0.0;
-    for (uint32_t b = threadIdx.x; b < gridDim.x; b += kGradThreads) sum += __ldcg(&a.partials[b]);
-    sum = block_sum(sum);
+    double sum = 0.0;
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kGradThreads / 32; ++w) mine.add(part_s[w]);
+        sum = double(mine.hi) + double(mine.lo);
+        for (int w = 0; w < kGradThreads / 32; ++w)
+            if (rest_s[w] != 0.0) sum += rest_s[w];
+        last = true;
+        if (gridDim.x > 1) {
+            a.partials[blockIdx.x] = sum;
+            __threadfence();
+            last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+        }
+    }
+    if (gridDim.x > 1) {
+        __syncthreads();
+        if (!last) return;
+        __threadfence();
+        sum = 0.0;
+        for (uint32_t b = threadIdx.x; b < gridDim.x; b += kGradThreads) sum += __ldcg(&a.partials[b]);
+        sum = warp_sum(sum);
+        if (lane == 0) rest_s[warp] = sum;
+        __syncthreads();
+        sum = 0.0;
+        if (threadIdx.x == 0) {
+            for (int w = 0; w < kGradThreads / 32; ++w) sum += rest_s[w];
+            *a.ticket = 0;
+        }
+    }
     if (threadIdx.x == 0) {
         if (!a.first_launch) sum += *a.total;
         if (a.last_launch) a.norm[0] = float(sqrt(sum));
         else *a.total = sum;
-        *a.ticket = 0;
     }
 }
 
@@ -219,7 +260,8 @@ __global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_co
     if (a.last_launch && blockIdx.x == 0 && threadIdx.x == 0) a.norm[1] = factor;
     const uint32_t begin = uint32_t(uint64_t(a.tiles) * blockIdx.x / gridDim.x), end = uint32_t(uint64_t(a.tiles) * (blockIdx.x + 1) / gridDim.x);
     if (begin == end) return;
-    uint32_t i = grad_tensor(a, end - 1);
+    uint32_t i = a.start[blockIdx.x];
+    while (i + 1 < a.count && a.t[i + 1].first < end) ++i;
     // backwards: what the norm's pass read last is still in L2
     for (uint32_t tile = end; tile-- > begin;) {
         while (a.t[i].first > tile) --i;
@@ -241,7 +283,7 @@ static cudaError_t grad_launch(const Launch &L, const GradLaunch &N, size_t *nex
         const ccl_tensor_t &t = N.tensors[*next];
         if (t.n == 0 || (t.copy && !N.clip)) continue;
         const uint32_t S = uint32_t(elem_bytes(t.dtype)), vec = 16 / S;
-        const uint64_t groups = (uintptr_t(t.in) % 16 / S + t.n + vec - 1) / vec;
+        const uint64_t groups = (uintptr_t(t.in) % 128 / S + t.n + vec - 1) / vec;
         a.t[a.count++] = {t.in, t.out, t.n, uint32_t(tiles), uint32_t(t.dtype)};
         tiles += (groups + kGradTile - 1) / kGradTile;
     }
@@ -256,8 +298,13 @@ static cudaError_t grad_launch(const Launch &L, const GradLaunch &N, size_t *nex
     a.partials = reinterpret_cast<double *>(static_cast<char *>(N.scratch) + kScratchHead);
     a.status = L.status;
     a.short_by = L.stall_test == 2 ? 1 : 0;
-    const uint64_t most = uint64_t(L.num_sms) * 8 < kMaxPartials ? uint64_t(L.num_sms) * 8 : kMaxPartials;
+    const uint64_t ctas = uint64_t(L.num_sms) * (N.clip ? kGradClipCtas : kGradNormCtas), most = ctas < kGradMaxGrid ? ctas : kGradMaxGrid;
     const unsigned grid = unsigned(tiles < 1 ? 1 : tiles < most ? tiles : most);
+    for (unsigned b = 0, i = 0; b < grid; ++b) {
+        const uint32_t tile = uint32_t(tiles * b / grid);
+        while (i + 1 < a.count && a.t[i + 1].first <= tile) ++i;
+        a.start[b] = uint16_t(i);
+    }
     const cudaError_t err = launch_dependent(N.clip ? grad_clip_kernel<CAP> : grad_norm_kernel<CAP>, grid, kGradThreads, 0, L.stream, a);
     if (err != cudaSuccess) return err;
     info->kernel = N.clip ? "grad_clip" : "grad_norm";
