@@ -161,11 +161,15 @@ struct QuantUnit {
     }
 };
 
-// A thread has a unit of VEC columns at a time, KEEP of them in registers
-// between the passes; further units are read again.  VECTOR: units are 16-byte
-// groups, and no unit lies in two chunks.
+// A thread has a unit of VEC columns at a time; KEEP of them stay in shared
+// memory between the passes, further ones are read again.  VECTOR: units are
+// 16-byte groups, and no unit lies in two chunks.  Bound by memory and by how
+// many rows are under way: 4000 x 8192 f16 p=4 in 87 us (6.0 TB/s), 4096 x 8192
+// bf16 p=8 156 (6.1), 4096 x 4096 bf16 p=1 27 (4.3).  With the units in registers instead, at four CTAs of 256 threads an
+// SM, 93, 158 and 31; here eight CTAs (six at p=8: 156, eight 172, the loads' registers spill).  Loading two or four units at
+// once cost more CTAs than it gained.
 template <typename T, int P, int THREADS, int KEEP, bool VECTOR>
-__global__ void __launch_bounds__(THREADS, KEEP > 1 ? 1024 / THREADS : 1) ar_rmsnorm_e4m3_kernel(const __grid_constant__ QuantArgs<(P > 0 ? P : kMaxRanks)> a)
+__global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P == 8 ? 1536 : 2048) / THREADS : 1) ar_rmsnorm_e4m3_kernel(const __grid_constant__ QuantArgs<(P > 0 ? P : kMaxRanks)> a)
 {
     using U = QuantUnit<T, VECTOR>;
     constexpr int VEC = U::VEC, S = U::S, PAIRS = U::PAIRS, WARPS = THREADS / 32;
@@ -232,83 +236,69 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? 1024 / THREADS : 1) ar_rms
         }
         return h;
     };
-    // N units, THREADS apart: all loads go out before the first fold
-    auto pass1 = [&](auto count, uint32_t u, uint4 *kept) {
-        constexpr int N = decltype(count)::value;
+    auto pass1 = [&](uint32_t u, uint4 *kept) {
+        if (u >= u1) return;
+        Pair acc[PAIRS], v[PAIRS];
+        uint4 res;
         if constexpr (P > 0) {
-            uint4 r[N][P + 1];
+            uint4 r[P];
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                if (u + j * THREADS >= u1) continue;
+            for (int k = 0; k < P; ++k) r[k] = U::load(source(u, k), u, H);
+            res = U::load(residual, u, H);
+            U::unpack(r[0], acc);
 #pragma unroll
-                for (int k = 0; k < P; ++k) r[j][k] = U::load(source(u + j * THREADS, k), u + j * THREADS, H);
-                r[j][P] = U::load(residual, u + j * THREADS, H);
+            for (int k = 1; k < P; ++k) {
+                U::unpack(r[k], v);
+#pragma unroll
+                for (int i = 0; i < PAIRS; ++i) acc[i] = acc[i] + v[i];
             }
+        } else if constexpr (VECTOR) {
+            U::unpack(U::load(source(u, 0), u, H), acc);
+#pragma unroll 4
+            for (int k = 1; k < p; ++k) {
+                U::unpack(U::load(source(u, k), u, H), v);
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                if (u + j * THREADS >= u1) continue;
-                Pair acc[PAIRS], v[PAIRS];
-                U::unpack(r[j][0], acc);
-#pragma unroll
-                for (int k = 1; k < P; ++k) {
-                    U::unpack(r[j][k], v);
-#pragma unroll
-                    for (int i = 0; i < PAIRS; ++i) acc[i] = acc[i] + v[i];
-                }
-                const uint4 h = merge(u + j * THREADS, acc, r[j][P]);
-                if (kept) kept[j] = h;
+                for (int i = 0; i < PAIRS; ++i) acc[i] = acc[i] + v[i];
             }
+            res = U::load(residual, u, H);
         } else {
-            static_assert(N == 1, "");
-            if (u >= u1) return;
-            Pair acc[PAIRS], v[PAIRS];
-            if constexpr (VECTOR) {
-                U::unpack(U::load(source(u, 0), u, H), acc);
+            float f[VEC];
+            if (one_chunk) {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) f[i] = 0.0f;
 #pragma unroll 4
-                for (int k = 1; k < p; ++k) {
-                    U::unpack(U::load(source(u, k), u, H), v);
-#pragma unroll
-                    for (int i = 0; i < PAIRS; ++i) acc[i] = acc[i] + v[i];
-                }
-            } else {
-                float f[VEC];
-                if (one_chunk) {
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) f[i] = 0.0f;
-#pragma unroll 4
-                    for (int k = 0; k < p; ++k) {
-                        const void *from = source(u, k);
-#pragma unroll
-                        for (int i = 0; i < VEC; ++i) {
-                            const float v = U::column(u, i) < H ? Traits<T>::load1(from, U::column(u, i)) : 0.0f;
-                            f[i] = k == 0 ? v : __fadd_rn(f[i], v);
-                        }
-                    }
-                } else {
-                    int c = chunk;
+                for (int k = 0; k < p; ++k) {
+                    const void *from = source(u, k);
 #pragma unroll
                     for (int i = 0; i < VEC; ++i) {
-                        const uint64_t e = base + U::column(u, i);
-                        f[i] = 0.0f;
-                        if (U::column(u, i) >= H) continue;
-                        while (e >= a.bound[c + 1]) ++c;
-                        f[i] = Traits<T>::load1(a.src[a.order[c][0]], e);
-                        for (int k = 1; k < p; ++k) f[i] = __fadd_rn(f[i], Traits<T>::load1(a.src[a.order[c][k]], e));
+                        const float x = U::column(u, i) < H ? Traits<T>::load1(from, U::column(u, i)) : 0.0f;
+                        f[i] = k == 0 ? x : __fadd_rn(f[i], x);
                     }
                 }
+            } else {
+                int c = chunk;
 #pragma unroll
-                for (int i = 0; i < PAIRS; ++i) acc[i] = {f[2 * i], f[2 * i + 1]};
+                for (int i = 0; i < VEC; ++i) {
+                    const uint64_t e = base + U::column(u, i);
+                    f[i] = 0.0f;
+                    if (U::column(u, i) >= H) continue;
+                    while (e >= a.bound[c + 1]) ++c;
+                    f[i] = Traits<T>::load1(a.src[a.order[c][0]], e);
+                    for (int k = 1; k < p; ++k) f[i] = __fadd_rn(f[i], Traits<T>::load1(a.src[a.order[c][k]], e));
+                }
             }
-            const uint4 h = merge(u, acc, U::load(residual, u, H));
-            if (kept) kept[0] = h;
-        }
-    };
-    constexpr int MOST = P == 1 ? 4 : P == 2 || P == 4 ? 2 : 1, BATCH = KEEP < MOST ? KEEP : MOST;
-    const uint32_t first = u0 + threadIdx.x;
-    uint4 keep[KEEP];
 #pragma unroll
-    for (int j = 0; j < KEEP; j += BATCH) pass1(std::integral_constant<int, BATCH>(), first + j * THREADS, keep + j);
-    for (uint32_t u = first + KEEP * THREADS; u < u1; u += BATCH * THREADS) pass1(std::integral_constant<int, BATCH>(), u, nullptr);
+            for (int i = 0; i < PAIRS; ++i) acc[i] = {f[2 * i], f[2 * i + 1]};
+            res = U::load(residual, u, H);
+        }
+        const uint4 h = merge(u, acc, res);
+        if (kept) *kept = h;
+    };
+    const uint32_t first = u0 + threadIdx.x;
+    __shared__ uint4 kept_s[KEEP][THREADS];      // each thread's own
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j) pass1(first + j * THREADS, &kept_s[j][threadIdx.x]);
+    for (uint32_t u = first + KEEP * THREADS; u < u1; u += THREADS) pass1(u, nullptr);
 
     // the row's sum and maximum: the warps', then (warp 0) the CTA's, then the cluster's
     float sum = ss.x + ss.y;
@@ -440,7 +430,7 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? 1024 / THREADS : 1) ar_rms
     };
 #pragma unroll
     for (int j = 0; j < KEEP; ++j)
-        if (u0 + warp * 32 + j * THREADS < u1) pass2(first + j * THREADS, keep[j], first + j * THREADS < u1);
+        if (u0 + warp * 32 + j * THREADS < u1) pass2(first + j * THREADS, kept_s[j][threadIdx.x], first + j * THREADS < u1);
     for (uint32_t u = first + KEEP * THREADS; u - lane < u1; u += THREADS)
         pass2(u, u < u1 ? U::load(merged, u, H) : make_uint4(0, 0, 0, 0), u < u1);      // (this thread's own stores)
 }
