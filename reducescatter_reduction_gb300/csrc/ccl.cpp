@@ -775,7 +775,6 @@ extern "C" ccl_status_t ccl_allreduce_residual_rmsnorm_e4m3(ccl_comm_t c, ccl_dt
     if (sched < 0)
         return fail(CCL_ERR_INVALID_ARG, "CCL_SCHEDULE=%s is not ring, allpairs or auto", getenv("CCL_SCHEDULE"));
     L.table = get_table(c, n, sched);
-    for (int k = 0; k <= p && aligned; ++k) aligned = L.table->bound[k] % vec_elems == 0;
     L.vec = aligned;
     NormE4m3Launch N;
     N.norm.residual = residual_in;

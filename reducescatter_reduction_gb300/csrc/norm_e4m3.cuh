@@ -163,7 +163,7 @@ struct QuantUnit {
 
 // A thread has a unit of VEC columns at a time; KEEP of them stay in shared
 // memory between the passes, further ones are read again.  VECTOR: units are
-// 16-byte groups, and no unit lies in two chunks.  Bound by memory and by how
+// 16-byte groups.  Bound by memory and by how
 // many rows are under way: 4000 x 8192 f16 p=4 in 87 us (6.0 TB/s), 4096 x 8192
 // bf16 p=8 156 (6.1), 4096 x 4096 bf16 p=1 27 (4.3).  With the units in registers instead, at four CTAs of 256 threads an
 // SM, 93, 158 and 31; here eight CTAs (six at p=8: 156, eight 172, the loads' registers spill).  Loading two or four units at
@@ -212,6 +212,12 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P == 8 ? 1536 : 2048) / T
             while (base + uint64_t(u) * VEC >= a.bound[c + 1]) ++c;
         return static_cast<const char *>(a.src[a.order[c][k]]) + base * S;
     };
+    auto two_chunks = [&](uint32_t u) {
+        const uint64_t e = base + uint64_t(u) * VEC;
+        int c = chunk;
+        while (e >= a.bound[c + 1]) ++c;
+        return e + VEC > a.bound[c + 1];
+    };
     Pair ss = {0.0f, 0.0f};
     float top = 0.0f;
     // pass 1: fold, merge, store h, add its squares and find the largest |h gamma|
@@ -236,11 +242,30 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P == 8 ? 1536 : 2048) / T
         }
         return h;
     };
+    // a unit element by element, each in its own chunk's order
+    auto fold_elements = [&](uint32_t u, Pair (&acc)[PAIRS]) {
+        float f[VEC];
+        int c = chunk;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const uint64_t e = base + U::column(u, i);
+            f[i] = 0.0f;
+            if (U::column(u, i) >= H) continue;
+            while (e >= a.bound[c + 1]) ++c;
+            f[i] = Traits<T>::load1(a.src[a.order[c][0]], e);
+            for (int k = 1; k < p; ++k) f[i] = __fadd_rn(f[i], Traits<T>::load1(a.src[a.order[c][k]], e));
+        }
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) acc[i] = {f[2 * i], f[2 * i + 1]};
+    };
     auto pass1 = [&](uint32_t u, uint4 *kept) {
         if (u >= u1) return;
         Pair acc[PAIRS], v[PAIRS];
         uint4 res;
-        if constexpr (P > 0) {
+        if (!one_chunk && (!VECTOR || two_chunks(u))) {
+            fold_elements(u, acc);
+            res = U::load(residual, u, H);
+        } else if constexpr (P > 0) {
             uint4 r[P];
 #pragma unroll
             for (int k = 0; k < P; ++k) r[k] = U::load(source(u, k), u, H);
@@ -252,7 +277,7 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P == 8 ? 1536 : 2048) / T
 #pragma unroll
                 for (int i = 0; i < PAIRS; ++i) acc[i] = acc[i] + v[i];
             }
-        } else if constexpr (VECTOR) {
+        } else {
             U::unpack(U::load(source(u, 0), u, H), acc);
 #pragma unroll 4
             for (int k = 1; k < p; ++k) {
@@ -260,35 +285,6 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P == 8 ? 1536 : 2048) / T
 #pragma unroll
                 for (int i = 0; i < PAIRS; ++i) acc[i] = acc[i] + v[i];
             }
-            res = U::load(residual, u, H);
-        } else {
-            float f[VEC];
-            if (one_chunk) {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) f[i] = 0.0f;
-#pragma unroll 4
-                for (int k = 0; k < p; ++k) {
-                    const void *from = source(u, k);
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        const float x = U::column(u, i) < H ? Traits<T>::load1(from, U::column(u, i)) : 0.0f;
-                        f[i] = k == 0 ? x : __fadd_rn(f[i], x);
-                    }
-                }
-            } else {
-                int c = chunk;
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const uint64_t e = base + U::column(u, i);
-                    f[i] = 0.0f;
-                    if (U::column(u, i) >= H) continue;
-                    while (e >= a.bound[c + 1]) ++c;
-                    f[i] = Traits<T>::load1(a.src[a.order[c][0]], e);
-                    for (int k = 1; k < p; ++k) f[i] = __fadd_rn(f[i], Traits<T>::load1(a.src[a.order[c][k]], e));
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < PAIRS; ++i) acc[i] = {f[2 * i], f[2 * i + 1]};
             res = U::load(residual, u, H);
         }
         const uint4 h = merge(u, acc, res);

@@ -116,6 +116,15 @@ def test_in_place_residual_and_schedules(rows, schedule):
     run("f16", 3, rows, 1025, 32, in_place=True, schedule=schedule)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("p, rows, hidden", [(3, 1, 8), (3, 1, 40), (8, 3, 6104), (3, 7, 2056), (4, 401, 968), (8, 1, 24), (7, 500, 264), (64, 5, 72)])
+@pytest.mark.parametrize("schedule", ["ring", "allpairs"])
+def test_chunks_that_end_inside_a_group_of_elements(dtype, p, rows, hidden, schedule):
+    """Rows of whole 16-byte groups whose chunks end anywhere: each element has its own chunk's order."""
+    assert rows * hidden % p or rows * hidden // p % 8
+    run(dtype, p, rows, hidden, 32, schedule=schedule)
+
+
 @pytest.mark.parametrize("group", [0, 32])
 @pytest.mark.parametrize("rows", [3, 400])
 def test_zeros_and_small_rows(group, rows):
