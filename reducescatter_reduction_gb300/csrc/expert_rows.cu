@@ -49,48 +49,65 @@ __device__ __forceinline__ bool entry_held(const RowsArgs<PM> &a, uint64_t entry
     return in_bounds(entry < uint64_t(a.held) * a.k, a.status, kSiteExperts, entry);
 }
 
-// A unit of a row: 16 bytes, 4 bytes or one element.
-template <typename T, int BYTES>
-struct RowUnit {
-    using Tr = Traits<T>;
-    using Acc = typename Tr::Acc;
-    static constexpr int S = 16 / Tr::VEC, N = BYTES / S;
-    using Raw = typename std::conditional<BYTES == 16, uint4, typename std::conditional<BYTES == 4, uint32_t, uint16_t>::type>::type;
-    __device__ static __forceinline__ Raw zero()
+// A row anywhere in memory, in 16-byte groups that lie on 16-byte boundaries:
+// group g has columns g VEC - shift and on.
+template <typename T>
+struct RowView {
+    static constexpr int VEC = Traits<T>::VEC, S = 16 / VEC;
+    char *base;            // the boundary at or below the row's begin
+    int shift;             // elements between the boundary and the row
+    __device__ __forceinline__ explicit RowView(const void *row)
     {
-        if constexpr (BYTES == 16) return make_uint4(0, 0, 0, 0);
-        else return Raw(0);
+        base = reinterpret_cast<char *>(uintptr_t(row) & ~uintptr_t(15));
+        shift = int(uintptr_t(row) & 15) / S;
     }
-    __device__ static __forceinline__ Raw load(const void *p)
+    __device__ __forceinline__ char *at(int g) const { return base + int64_t(g) * 16; }
+    __device__ __forceinline__ char *column(int c) const { return base + int64_t(shift + c) * S; }
+    // The columns of group g of a row with shift `other`: two groups (a neighbouring thread has one of them too) and a shift
+    // that is the same for all of the two rows.  For groups in `inner` both lie in the row.
+    __device__ __forceinline__ uint4 load_for(int g, int other) const
     {
-        if constexpr (BYTES == 16) return ld_stream_v4(p);
-        else return __ldg(static_cast<const Raw *>(p));
-    }
-    __device__ static __forceinline__ void store(void *p, const Raw &v)
-    {
-        if constexpr (BYTES == 16) st_stream_v4(p, v);
-        else *static_cast<Raw *>(p) = v;
-    }
-    __device__ static __forceinline__ void unpack(const Raw &v, Acc (&f)[N])
-    {
-        if constexpr (BYTES == 16) {
-            Tr::unpack(v, f);
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) f[i] = Tr::load1(&v, i);
+        int by = (shift - other) * S;
+        if (by < 0) {
+            by += 16;
+            --g;
         }
-    }
-    __device__ static __forceinline__ Raw pack(const Acc (&f)[N])
-    {
-        if constexpr (BYTES == 16) {
-            return Tr::pack(f);
-        } else {
-            Raw v;
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(at(g)));
+        if (by == 0) return a;
+        const uint4 b = __ldg(reinterpret_cast<const uint4 *>(at(g + 1)));
+        uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        if (by & 8)
 #pragma unroll
-            for (int i = 0; i < N; ++i) Tr::store1(&v, i, f[i]);
-            return v;
-        }
+            for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+        if (by & 4)
+#pragma unroll
+            for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+        if (by & 2)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+        return make_uint4(w[0], w[1], w[2], w[3]);
     }
+};
+
+// The groups of a written row of `width` columns that are moved whole, [2,
+// last): two groups from its begin and one before its last whole one, whatever
+// the shift of the row that is read, the groups read lie in that row.  The
+// columns before and after them, 16 at most each, go element by element, a thread each; so do all
+// columns of rows without such groups.
+template <typename T>
+struct Inner {
+    static constexpr int VEC = Traits<T>::VEC;
+    int last, head, tail, width;     // columns [0, head) and [tail, width)
+    __device__ __forceinline__ Inner(int shift, int w) : width(w)
+    {
+        last = (shift + w) / VEC - 1;
+        head = 2 * VEC - shift;
+        tail = last * VEC - shift;
+        if (last <= 2) head = tail = w;
+    }
+    // The edge column of a thread, or from `width` on; then that + step.
+    __device__ __forceinline__ int first(int thread) const { return thread < head ? thread : tail + thread - head; }
+    __device__ __forceinline__ int next(int c, int thread, int step) const { return head == width ? c + step : c < head ? tail + thread + step - head : c + step; }
 };
 
 // One choice of a team's token: where its row begins, and its weight.
@@ -105,12 +122,12 @@ template <int PM>
 struct Team {
     uint32_t thread, threads;   // of the team
     uint32_t rank, token;
-    uint64_t first, end;        // the team's units
+    uint64_t first, end;        // the team's units: of a row, or of a row and as many more as it may lie over
     bool on;                    // it has a token
     Choice *list;
 
     // `of` has the experts' buffers; `list` room for the choices of all teams.
-    __device__ __forceinline__ Team(const RowsArgs<PM> &a, const void *const *of, uint32_t S, uint32_t bytes, Choice *all)
+    __device__ __forceinline__ Team(const RowsArgs<PM> &a, const void *const *of, uint32_t S, uint64_t units, Choice *all)
     {
         threads = 1u << a.team_shift;
         thread = threadIdx.x & (threads - 1);
@@ -118,7 +135,6 @@ struct Team {
         on = t < a.rows * a.p;
         rank = on ? div_by(t, a.by_rows) : 0;
         token = t - rank * a.rows;
-        const uint64_t units = a.hidden * S / bytes;
         first = units * blockIdx.y / gridDim.y + thread;
         end = on ? units * (blockIdx.y + 1) / gridDim.y : 0;
         list = all + team * a.k;
@@ -139,74 +155,74 @@ struct Team {
     }
 };
 
-template <typename T, int PM, int BYTES, int UN>
+template <typename T, int PM, int UN>
 __global__ void __launch_bounds__(kRowsThreads) dispatch_kernel(const __grid_constant__ RowsArgs<PM> a)
 {
-    using U = RowUnit<T, BYTES>;
-    constexpr uint32_t S = U::S;
+    using Tr = Traits<T>;
+    constexpr uint32_t VEC = Tr::VEC, S = 16 / VEC;
     extern __shared__ Choice lists[];
     grid_dependency_wait();
     grid_dependents_launch();
-    const Team<PM> t(a, a.out, S, BYTES, lists);
+    const Team<PM> t(a, a.out, S, a.hidden / VEC, lists);
     const char *token = static_cast<const char *>(a.in[t.rank]) + uint64_t(t.token) * a.hidden * S;
     for (uint64_t u = t.first; u < t.end; u += UN * t.threads) {
-        typename U::Raw v[UN];
+        uint4 v[UN];
 #pragma unroll
         for (int n = 0; n < UN; ++n) {
-            const char *at = token + (u + n * t.threads) * BYTES;
-            if (u + n * t.threads < t.end && token_held(a, a.in[t.rank], at, BYTES, S)) v[n] = U::load(at);
+            const char *at = token + (u + n * t.threads) * 16;
+            if (u + n * t.threads < t.end && token_held(a, a.in[t.rank], at, 16, S)) v[n] = ld_stream_v4(at);
         }
         for (uint32_t j = 0; j < a.k; ++j) {
             const Choice c = t.list[j];
             if (!c.row) continue;
 #pragma unroll
             for (int n = 0; n < UN; ++n) {
-                const uint64_t at = (u + n * t.threads) * BYTES;
-                if (u + n * t.threads >= t.end || !token_held(a, a.in[t.rank], token + at, BYTES, S) ||
-                    !row_of_expert_held(a, a.out[c.rank], c.row + at, BYTES, S))
+                const uint64_t at = (u + n * t.threads) * 16;
+                if (u + n * t.threads >= t.end || !token_held(a, a.in[t.rank], token + at, 16, S) ||
+                    !row_of_expert_held(a, a.out[c.rank], c.row + at, 16, S))
                     continue;
-                typename U::Raw w = v[n];
+                uint4 w = v[n];
                 if constexpr (!std::is_same<T, I32>::value) {
                     if (a.weighted) {
-                        float f[U::N];
-                        U::unpack(w, f);
+                        float f[int(VEC)];
+                        Tr::unpack(w, f);
 #pragma unroll
-                        for (int i = 0; i < U::N; ++i) f[i] = __fmul_rn(f[i], c.weight);
-                        w = U::pack(f);
+                        for (int i = 0; i < int(VEC); ++i) f[i] = __fmul_rn(f[i], c.weight);
+                        w = Tr::pack(f);
                     }
                 }
-                U::store(c.row + at, w);
+                st_stream_v4(c.row + at, w);
             }
         }
     }
 }
 
-template <typename T, int PM, int BYTES, int KB, int UN>
-__global__ void __launch_bounds__(kRowsThreads, BYTES == 16 && KB * UN == 8 ? 3 : 4) combine_kernel(const __grid_constant__ RowsArgs<PM> a)
+template <typename T, int PM, int KB, int UN>
+__global__ void __launch_bounds__(kRowsThreads, KB * UN == 8 ? 3 : 4) combine_kernel(const __grid_constant__ RowsArgs<PM> a)
 {
-    using U = RowUnit<T, BYTES>;
-    constexpr uint32_t S = U::S;
+    using Tr = Traits<T>;
+    constexpr uint32_t VEC = Tr::VEC, S = 16 / VEC;
     extern __shared__ Choice lists[];
     grid_dependency_wait();
     grid_dependents_launch();
-    const Team<PM> t(a, a.in, S, BYTES, lists);
+    const Team<PM> t(a, a.in, S, a.hidden / VEC, lists);
     char *token = static_cast<char *>(a.out[t.rank]) + uint64_t(t.token) * a.hidden * S;
     for (uint64_t u = t.first; u < t.end; u += UN * t.threads) {
-        float sum[UN][U::N];
+        float sum[UN][int(VEC)];
 #pragma unroll
         for (int n = 0; n < UN; ++n)
 #pragma unroll
-            for (int i = 0; i < U::N; ++i) sum[n][i] = 0.0f;
+            for (int i = 0; i < int(VEC); ++i) sum[n][i] = 0.0f;
         for (uint32_t first = 0; first < a.k; first += KB) {
-            typename U::Raw z[KB][UN];
+            uint4 z[KB][UN];
 #pragma unroll
             for (int j = 0; j < KB; ++j) {
                 const Choice c = first + j < a.k ? t.list[first + j] : Choice{nullptr, 0.0f, 0};
 #pragma unroll
                 for (int n = 0; n < UN; ++n) {
-                    const char *at = c.row + (u + n * t.threads) * BYTES;
-                    z[j][n] = U::zero();
-                    if (c.row && u + n * t.threads < t.end && row_of_expert_held(a, a.in[c.rank], at, BYTES, S)) z[j][n] = U::load(at);
+                    const char *at = c.row + (u + n * t.threads) * 16;
+                    z[j][n] = make_uint4(0, 0, 0, 0);
+                    if (c.row && u + n * t.threads < t.end && row_of_expert_held(a, a.in[c.rank], at, 16, S)) z[j][n] = ld_stream_v4(at);
                 }
             }
 #pragma unroll
@@ -216,31 +232,31 @@ __global__ void __launch_bounds__(kRowsThreads, BYTES == 16 && KB * UN == 8 ? 3 
                 if (!c.row) continue;
 #pragma unroll
                 for (int n = 0; n < UN; ++n) {
-                    float f[U::N];
-                    U::unpack(z[j][n], f);
+                    float f[int(VEC)];
+                    Tr::unpack(z[j][n], f);
 #pragma unroll
-                    for (int i = 0; i < U::N; ++i) sum[n][i] = fmaf(c.weight, f[i], sum[n][i]);
+                    for (int i = 0; i < int(VEC); ++i) sum[n][i] = fmaf(c.weight, f[i], sum[n][i]);
                 }
             }
         }
 #pragma unroll
         for (int n = 0; n < UN; ++n) {
-            char *at = token + (u + n * t.threads) * BYTES;
-            if (u + n * t.threads < t.end && token_held(a, a.out[t.rank], at, BYTES, S)) U::store(at, U::pack(sum[n]));
+            char *at = token + (u + n * t.threads) * 16;
+            if (u + n * t.threads < t.end && token_held(a, a.out[t.rank], at, 16, S)) st_stream_v4(at, Tr::pack(sum[n]));
         }
     }
 }
 
-template <typename T, int PM, int BYTES, int KB, int UN>
-__global__ void __launch_bounds__(kRowsThreads, BYTES == 16 && KB * UN == 8 ? 3 : 4) combine_grad_kernel(const __grid_constant__ RowsArgs<PM> a)
+template <typename T, int PM, int KB, int UN>
+__global__ void __launch_bounds__(kRowsThreads, KB * UN == 8 ? 3 : 4) combine_grad_kernel(const __grid_constant__ RowsArgs<PM> a)
 {
-    using U = RowUnit<T, BYTES>;
-    constexpr uint32_t S = U::S;
+    using Tr = Traits<T>;
+    constexpr uint32_t VEC = Tr::VEC, S = 16 / VEC;
     extern __shared__ Choice lists[];
     __shared__ float parts[kRowsThreads / 32][KB];
     grid_dependency_wait();
     grid_dependents_launch();
-    const Team<PM> t(a, a.out, S, BYTES, lists);
+    const Team<PM> t(a, a.out, S, a.hidden / VEC, lists);
     const char *token = static_cast<const char *>(a.in[t.rank]) + uint64_t(t.token) * a.hidden * S;
     const uint32_t warps = t.threads / 32, warp = threadIdx.x / 32;
     for (uint32_t first = 0; first < a.k; first += KB) {
@@ -248,12 +264,12 @@ __global__ void __launch_bounds__(kRowsThreads, BYTES == 16 && KB * UN == 8 ? 3 
 #pragma unroll
         for (int j = 0; j < KB; ++j) sum[j] = 0.0f;
         for (uint64_t u = t.first; u < t.end; u += UN * t.threads) {
-            typename U::Raw v[UN], z[KB][UN];
+            uint4 v[UN], z[KB][UN];
 #pragma unroll
             for (int n = 0; n < UN; ++n) {
-                const char *at = token + (u + n * t.threads) * BYTES;
-                v[n] = U::zero();
-                if (u + n * t.threads < t.end && token_held(a, a.in[t.rank], at, BYTES, S)) v[n] = U::load(at);
+                const char *at = token + (u + n * t.threads) * 16;
+                v[n] = make_uint4(0, 0, 0, 0);
+                if (u + n * t.threads < t.end && token_held(a, a.in[t.rank], at, 16, S)) v[n] = ld_stream_v4(at);
             }
 #pragma unroll
             for (int j = 0; j < KB; ++j) {
@@ -261,9 +277,9 @@ __global__ void __launch_bounds__(kRowsThreads, BYTES == 16 && KB * UN == 8 ? 3 
                 const char *row = c.row ? static_cast<const char *>(a.experts[c.rank]) + (c.row - static_cast<char *>(a.out[c.rank])) : nullptr;
 #pragma unroll
                 for (int n = 0; n < UN; ++n) {
-                    const char *at = row + (u + n * t.threads) * BYTES;
-                    z[j][n] = U::zero();
-                    if (c.row && u + n * t.threads < t.end && row_of_expert_held(a, a.experts[c.rank], at, BYTES, S)) z[j][n] = U::load(at);
+                    const char *at = row + (u + n * t.threads) * 16;
+                    z[j][n] = make_uint4(0, 0, 0, 0);
+                    if (c.row && u + n * t.threads < t.end && row_of_expert_held(a, a.experts[c.rank], at, 16, S)) z[j][n] = ld_stream_v4(at);
                 }
             }
 #pragma unroll
@@ -273,17 +289,17 @@ __global__ void __launch_bounds__(kRowsThreads, BYTES == 16 && KB * UN == 8 ? 3 
                 if (!c.row) continue;
 #pragma unroll
                 for (int n = 0; n < UN; ++n) {
-                    char *at = c.row + (u + n * t.threads) * BYTES;
-                    float f[U::N], g[U::N];
-                    U::unpack(v[n], f);
-                    U::unpack(z[j][n], g);
+                    char *at = c.row + (u + n * t.threads) * 16;
+                    float f[int(VEC)], g[int(VEC)];
+                    Tr::unpack(v[n], f);
+                    Tr::unpack(z[j][n], g);
 #pragma unroll
-                    for (int i = 0; i < U::N; ++i) sum[j] = fmaf(f[i], g[i], sum[j]);
+                    for (int i = 0; i < int(VEC); ++i) sum[j] = fmaf(f[i], g[i], sum[j]);
 #pragma unroll
-                    for (int i = 0; i < U::N; ++i) f[i] = __fmul_rn(f[i], c.weight);
-                    if (u + n * t.threads < t.end && token_held(a, a.in[t.rank], token + (u + n * t.threads) * BYTES, BYTES, S) &&
-                        row_of_expert_held(a, a.out[c.rank], at, BYTES, S))
-                        U::store(at, U::pack(f));
+                    for (int i = 0; i < int(VEC); ++i) f[i] = __fmul_rn(f[i], c.weight);
+                    if (u + n * t.threads < t.end && token_held(a, a.in[t.rank], token + (u + n * t.threads) * 16, 16, S) &&
+                        row_of_expert_held(a, a.out[c.rank], at, 16, S))
+                        st_stream_v4(at, Tr::pack(f));
                 }
             }
         }
@@ -305,7 +321,159 @@ __global__ void __launch_bounds__(kRowsThreads, BYTES == 16 && KB * UN == 8 ? 3 
     }
 }
 
-template <typename T, int PM, int BYTES, int KB, int UN>
+// ---------------------------------------------------------------------------
+// Rows that are no 16-byte groups, or do not begin on a boundary.  A load at
+// any column is two aligned ones and a shift; what is written goes by the
+// groups of the row that is written.  Measured (us; against accesses of one
+// element, or of 4 bytes where they are aligned): combine, 2 x 4000 x 1001 bf16, k=4, 36 -> 23.5; its gradient
+// 94 -> 39, of 3 x 12400 x 731 bf16, k=2, 224 -> 95; dispatch, 3 x 1111 x 1001 f32, 7.6 -> 7.5.
+// ---------------------------------------------------------------------------
+
+// The checked build tests rows as a whole here: the views keep to them.
+template <typename T, int PM>
+__device__ __forceinline__ bool rows_held(const RowsArgs<PM> &a, uint32_t rank, uint32_t token, const void *tokens, const Choice &c, const void *expert, const void *row)
+{
+    constexpr uint32_t S = 16 / Traits<T>::VEC;
+    const uint64_t bytes = a.hidden * S;
+    if (!kBoundsCheck) return true;
+    return in_buffer(static_cast<const char *>(tokens) + token * bytes, bytes, tokens, a.held * bytes, a.status, kSiteExperts) &&
+           (!c.row || in_buffer(row, bytes, expert, a.capacity * bytes, a.status, kSiteExperts));
+}
+
+template <typename T, int PM, bool GRAD>
+__global__ void __launch_bounds__(kRowsThreads, 5) scatter_odd_kernel(const __grid_constant__ RowsArgs<PM> a)
+{
+    using Tr = Traits<T>;
+    constexpr int VEC = Tr::VEC, S = 16 / VEC, KB = 8;
+    constexpr bool RAW = std::is_same<T, I32>::value;
+    extern __shared__ Choice lists[];
+    __shared__ float parts[kRowsThreads / 32][KB];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const Team<PM> t(a, a.out, S, a.hidden / VEC + 2, lists);
+    const int width = int(a.hidden), thread = int(t.thread), threads = int(t.threads);
+    const char *token = static_cast<const char *>(a.in[t.rank]) + uint64_t(t.token) * a.hidden * S;
+    const RowView<T> x(token);
+    const uint32_t warps = t.threads / 32, warp = threadIdx.x / 32;
+    for (uint32_t first = 0; first < a.k; first += KB) {
+        for (uint32_t j = 0; j < KB && first + j < a.k; ++j) {
+            const Choice c = t.list[first + j];
+            float sum = 0.0f;
+            const char *row = c.row && GRAD ? static_cast<const char *>(a.experts[c.rank]) + (c.row - static_cast<char *>(a.out[c.rank])) : nullptr;
+            if (c.row && t.on && rows_held<T>(a, t.rank, t.token, a.in[t.rank], c, a.out[c.rank], c.row) &&
+                (!GRAD || rows_held<T>(a, t.rank, t.token, a.in[t.rank], c, a.experts[c.rank], row))) {
+                const RowView<T> to(c.row), z(row);
+                const Inner<T> in(to.shift, width);
+                for (int g = 2 + int(t.first); g < in.last && g - 2 < int(t.end); g += threads) {
+                    uint4 v = x.load_for(g, to.shift);
+                    if constexpr (!RAW) {
+                        if (GRAD || a.weighted) {
+                            float f[VEC];
+                            if constexpr (GRAD) {
+                                const uint4 h = z.shift == to.shift ? ld_stream_v4(z.at(g)) : z.load_for(g, to.shift);
+                                float e[VEC];
+                                Tr::unpack(h, e);
+                                Tr::unpack(v, f);
+#pragma unroll
+                                for (int i = 0; i < VEC; ++i) sum = fmaf(f[i], e[i], sum);
+                            } else {
+                                Tr::unpack(v, f);
+                            }
+#pragma unroll
+                            for (int i = 0; i < VEC; ++i) f[i] = __fmul_rn(f[i], c.weight);
+                            if (a.weighted) v = Tr::pack(f);
+                        }
+                    }
+                    st_stream_v4(to.at(g), v);
+                }
+                if (blockIdx.y == 0)
+                    for (int col = in.first(thread); col < width; col = in.next(col, thread, threads)) {
+                        if constexpr (RAW) {
+                            *reinterpret_cast<uint32_t *>(to.column(col)) = *reinterpret_cast<const uint32_t *>(x.column(col));
+                        } else if (!GRAD && !a.weighted) {
+                            using Bits = typename std::conditional<S == 2, uint16_t, uint32_t>::type;
+                            *reinterpret_cast<Bits *>(to.column(col)) = *reinterpret_cast<const Bits *>(x.column(col));
+                        } else {
+                            const float f = Tr::load1(x.column(col), 0);
+                            if constexpr (GRAD) sum = fmaf(f, Tr::load1(z.column(col), 0), sum);
+                            Tr::store1(to.column(col), 0, __fmul_rn(f, c.weight));
+                        }
+                    }
+            }
+            if constexpr (GRAD) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                if (threadIdx.x % 32 == 0) parts[warp][j] = sum;
+            }
+        }
+        if constexpr (GRAD) {
+            __syncthreads();
+            if (t.on && t.thread < KB && first + t.thread < a.k) {
+                float s = 0.0f;
+                for (uint32_t w = 0; w < warps; ++w) s += parts[warp + w][t.thread];
+                const uint64_t entry = uint64_t(t.token) * a.k + first + t.thread;
+                if (entry_held(a, entry)) a.dweights[t.rank][entry] = s;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+template <typename T, int PM>
+__global__ void __launch_bounds__(kRowsThreads, 5) combine_odd_kernel(const __grid_constant__ RowsArgs<PM> a)
+{
+    using Tr = Traits<T>;
+    constexpr int VEC = Tr::VEC, S = 16 / VEC, KB = 2;
+    extern __shared__ Choice lists[];
+    grid_dependency_wait();
+    grid_dependents_launch();
+    const Team<PM> t(a, a.in, S, a.hidden / VEC + 2, lists);
+    if (!t.on) return;
+    const int width = int(a.hidden), thread = int(t.thread), threads = int(t.threads);
+    const RowView<T> to(static_cast<char *>(a.out[t.rank]) + uint64_t(t.token) * a.hidden * S);
+    if (!rows_held<T>(a, t.rank, t.token, a.out[t.rank], Choice{nullptr, 0.0f, 0}, nullptr, nullptr)) return;
+    const Inner<T> in(to.shift, width);
+    auto held = [&](const Choice &c) { return c.row && rows_held<T>(a, t.rank, t.token, a.out[t.rank], c, a.in[c.rank], c.row); };
+    for (int g = 2 + int(t.first); g < in.last && g - 2 < int(t.end); g += threads) {
+        float sum[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) sum[i] = 0.0f;
+        for (uint32_t first = 0; first < a.k; first += KB) {
+            uint4 z[KB];
+            float weight[KB];
+            bool has[KB];
+#pragma unroll
+            for (int j = 0; j < KB; ++j) {
+                const Choice c = first + j < a.k ? t.list[first + j] : Choice{nullptr, 0.0f, 0};
+                has[j] = held(c);
+                weight[j] = c.weight;
+                if (has[j]) z[j] = RowView<T>(c.row).load_for(g, to.shift);
+            }
+#pragma unroll
+            for (int j = 0; j < KB; ++j) {
+                if (!has[j]) continue;
+                float f[VEC];
+                Tr::unpack(z[j], f);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) sum[i] = fmaf(weight[j], f[i], sum[i]);
+            }
+        }
+        st_stream_v4(to.at(g), Tr::pack(sum));
+    }
+    if (blockIdx.y == 0)
+        for (int col = in.first(thread); col < width; col = in.next(col, thread, threads)) {
+            float sum = 0.0f;
+#pragma unroll 4
+            for (uint32_t j = 0; j < a.k; ++j) {
+                const Choice c = t.list[j];
+                if (held(c)) sum = fmaf(c.weight, Tr::load1(c.row, col), sum);
+            }
+            Tr::store1(to.column(col), 0, sum);
+        }
+}
+
+// KB, UN: batches of the aligned kernels; KB 0: the others.
+template <typename T, int PM, int KB, int UN>
 static cudaError_t rows_launch(const Launch &L, const RowsLaunch &N, LaunchInfo *info)
 {
     RowsArgs<PM> a = {};
@@ -328,10 +496,11 @@ static cudaError_t rows_launch(const Launch &L, const RowsLaunch &N, LaunchInfo 
     a.weighted = N.weights ? 1 : 0;
     a.status = L.status;
     a.held = a.rows - (L.stall_test == 2 ? 1 : 0);
-    // a team has about four units a thread, and more threads where there are few tokens or many choices
-    const uint64_t units = N.hidden * elem_bytes(L.dtype) / BYTES, tokens = N.rows * uint64_t(L.p), sms = uint64_t(L.num_sms);
+    // a team has about four units (two batches; of odd rows two units) a thread, and more threads where there are few tokens or many choices
+    constexpr uint64_t VEC = Traits<T>::VEC;
+    const uint64_t units = N.hidden / VEC + (KB ? 0 : 2), tokens = N.rows * uint64_t(L.p), sms = uint64_t(L.num_sms);
     a.team_shift = 5;
-    while (a.team_shift < 8 && ((uint64_t(4 * UN) << a.team_shift) < units || tokens >> (8 - a.team_shift) < 4 * sms || N.k > 32)) ++a.team_shift;
+    while (a.team_shift < 8 && ((uint64_t(KB ? 4 * UN : 2) << a.team_shift) < units || tokens >> (8 - a.team_shift) < 4 * sms || N.k > 32)) ++a.team_shift;
     const uint32_t teams = kRowsThreads >> a.team_shift;
     const unsigned grid = unsigned((tokens + teams - 1) / teams);
     // few tokens: a row over several CTAs (the gradient's sums stay in one)
@@ -345,10 +514,14 @@ static cudaError_t rows_launch(const Launch &L, const RowsLaunch &N, LaunchInfo 
     const size_t smem = teams * N.k * sizeof(Choice);
     static std::atomic<unsigned long long> ready[3];
     void (*kern)(RowsArgs<PM>) = nullptr;
-    if constexpr (std::is_same<T, I32>::value)
-        kern = dispatch_kernel<T, PM, BYTES, 4>;
-    else
-        kern = N.op == ROWS_DISPATCH ? dispatch_kernel<T, PM, BYTES, 4> : N.op == ROWS_COMBINE ? combine_kernel<T, PM, BYTES, KB, UN> : combine_grad_kernel<T, PM, BYTES, KB, UN>;
+    if constexpr (std::is_same<T, I32>::value) {
+        if constexpr (KB == 0) kern = scatter_odd_kernel<T, PM, false>;
+        else kern = dispatch_kernel<T, PM, 4>;
+    } else if constexpr (KB == 0) {
+        kern = N.op == ROWS_DISPATCH ? scatter_odd_kernel<T, PM, false> : N.op == ROWS_COMBINE ? combine_odd_kernel<T, PM> : scatter_odd_kernel<T, PM, true>;
+    } else {
+        kern = N.op == ROWS_DISPATCH ? dispatch_kernel<T, PM, 4> : N.op == ROWS_COMBINE ? combine_kernel<T, PM, KB, UN> : combine_grad_kernel<T, PM, KB, UN>;
+    }
     cudaError_t err = smem > 48 * 1024 ? allow_dynamic_smem(kern, 4096 * sizeof(Choice), L.device, ready[N.op]) : cudaSuccess;
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
@@ -371,38 +544,30 @@ static cudaError_t rows_launch(const Launch &L, const RowsLaunch &N, LaunchInfo 
     return cudaSuccess;
 }
 
-// Units as wide as every address and the row allow, and batches by the number
-// of choices.  Measured (graph replay, us; 16-byte units unless said; batches
-// as choices x units):
+// Batches by the number of choices.  Measured (graph replay, us; batches as
+// choices x units):
 //   combine, 8 x 4000 x 4096 bf16, k=2       2x4 102   2x2 106
 //   combine's gradient, the same             2x4 160   2x2 162-170
 //   gradient, 4 x 20000 x 512 f16, k=1       2x4 64    2x2 48: a row of 64 units fills two for each of 32 threads
 //   gradient, 8 x 4000 x 2048 bf16, k=4      4x2 155
-//   gradient, 2 x 4000 x 1002 f16, k=3       4-byte units, 8x4 27   4x2 30
-//   gradient, 2 x 4000 x 1001 bf16, k=4      2-byte units, 8x4 104  4x2 94
-//   combine, the same                        2-byte units, 8x4 52   4x2 36
-// with the registers held to three CTAs an SM for 8 units of 16 bytes (four:
-// 8 x 2048 x 7168 bf16, k=8, 602 and not 587) and to four for the others.
+// with the registers held to three CTAs an SM for 8 units (four: 8 x 2048 x
+// 7168 bf16, k=8, 602 and not 587) and to four for the others.
 template <typename T, int PM>
-static cudaError_t rows_width(const Launch &L, const RowsLaunch &N, LaunchInfo *info)
+static cudaError_t rows_batches(const Launch &L, const RowsLaunch &N, LaunchInfo *info)
 {
-    constexpr bool wide = Traits<T>::VEC == 4;
-    if (N.align >= 16) {
-        if (PM > 8 || N.k > 4 || N.op == ROWS_DISPATCH) return rows_launch<T, PM, 16, 8, 1>(L, N, info);
-        if constexpr (PM <= 8) {
-            if (N.k > 2) return rows_launch<T, PM, 16, 4, 2>(L, N, info);
-            return N.hidden < 128 * Traits<T>::VEC ? rows_launch<T, PM, 16, 2, 2>(L, N, info) : rows_launch<T, PM, 16, 2, 4>(L, N, info);
-        }
+    if (!L.vec) return rows_launch<T, PM, 0, 1>(L, N, info);
+    if (PM > 8 || N.k > 4 || N.op == ROWS_DISPATCH) return rows_launch<T, PM, 8, 1>(L, N, info);
+    if constexpr (PM <= 8) {
+        if (N.k > 2) return rows_launch<T, PM, 4, 2>(L, N, info);
+        return N.hidden < 128 * Traits<T>::VEC ? rows_launch<T, PM, 2, 2>(L, N, info) : rows_launch<T, PM, 2, 4>(L, N, info);
     }
-    if (wide || N.align >= 4) return rows_launch<T, PM, 4, 8, 4>(L, N, info);
-    if constexpr (!wide) return rows_launch<T, PM, 2, 4, 2>(L, N, info);
     return cudaErrorInvalidValue;
 }
 
 template <typename T>
 static cudaError_t rows_dtype(const Launch &L, const RowsLaunch &N, LaunchInfo *info)
 {
-    return L.p <= 8 ? rows_width<T, 8>(L, N, info) : rows_width<T, kMaxRanks>(L, N, info);
+    return L.p <= 8 ? rows_batches<T, 8>(L, N, info) : rows_batches<T, kMaxRanks>(L, N, info);
 }
 
 cudaError_t launch_expert_rows(const Launch &L, const RowsLaunch &N, LaunchInfo *info)

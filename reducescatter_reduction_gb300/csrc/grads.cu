@@ -36,7 +36,7 @@ template <int CAP>
 struct GradArgs {
     GradRecord t[CAP];
     uint16_t start[kGradMaxGrid];        // the tensor of a CTA's first tile
-    uint32_t count, tiles;
+    uint32_t count, share, more;         // tiles of a CTA: share, and one more for the first `more`
     float max_norm;
     int first_launch, last_launch;
     float *norm;
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const __grid_co
     __shared__ bool last;
     grid_dependency_wait();
     grid_dependents_launch();
-    const uint32_t begin = uint32_t(uint64_t(a.tiles) * blockIdx.x / gridDim.x), end = uint32_t(uint64_t(a.tiles) * (blockIdx.x + 1) / gridDim.x);
+    const uint32_t begin = blockIdx.x * a.share + min(blockIdx.x, a.more), end = begin + a.share + (blockIdx.x < a.more ? 1 : 0);
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     Twofold mine;
     double rest = 0.0;
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_co
     const float by = __fdiv_rn(a.max_norm, a.norm[0] + 1e-6f);
     const float factor = by > 1.0f ? 1.0f : by;                  // (NaN stays NaN)
     if (a.last_launch && blockIdx.x == 0 && threadIdx.x == 0) a.norm[1] = factor;
-    const uint32_t begin = uint32_t(uint64_t(a.tiles) * blockIdx.x / gridDim.x), end = uint32_t(uint64_t(a.tiles) * (blockIdx.x + 1) / gridDim.x);
+    const uint32_t begin = blockIdx.x * a.share + min(blockIdx.x, a.more), end = begin + a.share + (blockIdx.x < a.more ? 1 : 0);
     if (begin == end) return;
     uint32_t i = a.start[blockIdx.x];
     while (i + 1 < a.count && a.t[i + 1].first < end) ++i;
@@ -288,7 +288,6 @@ static cudaError_t grad_launch(const Launch &L, const GradLaunch &N, size_t *nex
         tiles += (groups + kGradTile - 1) / kGradTile;
     }
     while (*next < N.count && (N.tensors[*next].n == 0 || (N.tensors[*next].copy && !N.clip))) ++*next;
-    a.tiles = uint32_t(tiles);
     a.max_norm = N.max_norm;
     a.first_launch = first;
     a.last_launch = *next == N.count;
@@ -300,10 +299,13 @@ static cudaError_t grad_launch(const Launch &L, const GradLaunch &N, size_t *nex
     a.short_by = L.stall_test == 2 ? 1 : 0;
     const uint64_t ctas = uint64_t(L.num_sms) * (N.clip ? kGradClipCtas : kGradNormCtas), most = ctas < kGradMaxGrid ? ctas : kGradMaxGrid;
     const unsigned grid = unsigned(tiles < 1 ? 1 : tiles < most ? tiles : most);
+    a.share = uint32_t(tiles / grid);
+    a.more = uint32_t(tiles % grid);
+    uint32_t tile = 0;
     for (unsigned b = 0, i = 0; b < grid; ++b) {
-        const uint32_t tile = uint32_t(tiles * b / grid);
         while (i + 1 < a.count && a.t[i + 1].first <= tile) ++i;
         a.start[b] = uint16_t(i);
+        tile += a.share + (b < a.more ? 1 : 0);
     }
     const cudaError_t err = launch_dependent(N.clip ? grad_clip_kernel<CAP> : grad_norm_kernel<CAP>, grid, kGradThreads, 0, L.stream, a);
     if (err != cudaSuccess) return err;
@@ -319,7 +321,9 @@ cudaError_t launch_grads(const Launch &L, const GradLaunch &N, LaunchInfo *info)
     size_t next = 0;
     bool first = true;
     do {
-        const cudaError_t err = N.count <= 64 ? grad_launch<64>(L, N, &next, first, info) : grad_launch<896>(L, N, &next, first, info);
+        const cudaError_t err = N.count <= 64    ? grad_launch<64>(L, N, &next, first, info)
+                                : N.count <= 448 ? grad_launch<448>(L, N, &next, first, info)
+                                                 : grad_launch<896>(L, N, &next, first, info);
         if (err != cudaSuccess) return err;
         first = false;
     } while (next < N.count);

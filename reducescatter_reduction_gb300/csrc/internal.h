@@ -337,8 +337,8 @@ struct RowsLaunch {
     const float *const *weights = nullptr;
     const void *const *experts = nullptr;   // ROWS_GRAD
     float *const *dweights = nullptr;       // ROWS_GRAD
-    uint32_t align = 1;                     // a power of two up to 16 that divides every buffer's address and the bytes of a row
 };
+// (L.vec: buffers and rows are 16-byte groups.)
 cudaError_t launch_expert_rows(const Launch &L, const RowsLaunch &N, LaunchInfo *info);
 
 struct GradLaunch {

@@ -80,6 +80,7 @@ static ccl_status_t expert_rows(ccl_comm *c, int op, int dtype, size_t rows, siz
     if ((st = check_choices(c, rows, k, capacity)) != CCL_OK) return st;
     const size_t es = elem_bytes(dtype);
     if (hidden == 0) return fail(CCL_ERR_INVALID_ARG, "hidden must be positive");
+    if (hidden > 0x7ffffff0ull) return fail(CCL_ERR_UNSUPPORTED, "%s: hidden %zu above 2^31 - 16", what, hidden);
     const size_t most = rows > capacity ? rows : capacity;
     if (most && hidden > (SIZE_MAX / 4) / most / es) return fail(CCL_ERR_INVALID_ARG, "rows * hidden too large");
     if (rows == 0) return CCL_OK;
@@ -88,7 +89,7 @@ static ccl_status_t expert_rows(ccl_comm *c, int op, int dtype, size_t rows, siz
     const size_t token_bytes = rows * hidden * es, expert_bytes = capacity * hidden * es;
     const bool to_tokens = op == ROWS_COMBINE;
     Spans s;
-    uintptr_t bits = hidden * es | 16;       // of every address and the row's bytes
+    uintptr_t bits = hidden * es;            // of every address and the row's bytes
     for (int r = 0; r < c->p; ++r) {
         const uintptr_t in = uintptr_t(c->in[r]), out = uintptr_t(c->out[r]);
         if (in % es || out % es)
@@ -111,9 +112,9 @@ static ccl_status_t expert_rows(ccl_comm *c, int op, int dtype, size_t rows, siz
     if ((st = check_spans(s.s, size_t(s.n))) != CCL_OK) return st;
     DeviceGuard g(c->device);
     if (g.err != cudaSuccess) return cuda_fail(g.err, what);
-    const Launch L = make_launch(c, dtype, false, stream);
+    Launch L = make_launch(c, dtype, false, stream);
+    L.vec = bits % 16 == 0;
     RowsLaunch N;
-    N.align = uint32_t(bits & (~bits + 1));
     N.op = op;
     N.rows = rows;
     N.hidden = hidden;

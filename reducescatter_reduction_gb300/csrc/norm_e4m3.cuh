@@ -509,6 +509,7 @@ static cudaError_t quant_dtype(const Launch &L, const NormE4m3Launch &N, LaunchI
     switch (L.p) {
     case 1: return quant_launch<T, 1, true>(L, N, info);
     case 2: return quant_launch<T, 2, true>(L, N, info);
+    case 3: return quant_launch<T, 3, true>(L, N, info);
     case 4: return quant_launch<T, 4, true>(L, N, info);
     case 8: return quant_launch<T, 8, true>(L, N, info);
     default: return quant_launch<T, 0, true>(L, N, info);

@@ -111,7 +111,7 @@ IN_BYTES = 2 * NORM_OUT             # of a bf16 input
     (dict(hidden=0), BAD), (dict(group=32), OK), (dict(group=64), OK), (dict(group=128), OK), (dict(group=16), BAD),
     (dict(group=256), BAD), (dict(eps=-1.0), BAD), (dict(eps=NAN), BAD), (dict(eps=INF), BAD), (dict(eps=0.0), OK),
     (dict(schedule=9), BAD), (dict(schedule=ccl.CCL_SCHED_CUSTOM), BAD), (dict(rows=1 << 62), BAD),
-    (dict(rows=1 << 28, hidden=1), UNSUPPORTED), (dict(residual=0), BAD), (dict(residual_out=0), BAD),
+    (dict(rows=1 << 28, hidden=1), UNSUPPORTED), (dict(hidden=1 << 31, rows=1), UNSUPPORTED), (dict(residual=0), BAD), (dict(residual_out=0), BAD),
     (dict(gamma=0), BAD), (dict(scales=None), BAD), (dict(scales=(13 * A, 0)), BAD), (dict(scales=(13 * A, 14 * A + 2)), BAD),
     (dict(residual=10 * A + 1), BAD), (dict(residual=10 * A + 2), OK), (dict(residual_out=10 * A), OK),
     (dict(residual_out=10 * A + 2), BAD), (dict(gamma=11 * A + 8), BAD), (dict(gamma=3 * A), BAD),
@@ -152,7 +152,7 @@ def test_sort(front, change, want):
 
 @pytest.mark.parametrize("name", ["dispatch", "combine", "grad"])
 @pytest.mark.parametrize("change, want", [
-    (dict(), OK), (dict(dtype=7), BAD), (dict(hidden=0), BAD), (dict(hidden=1 << 61), BAD), (dict(k=0), BAD),
+    (dict(), OK), (dict(dtype=7), BAD), (dict(hidden=0), BAD), (dict(hidden=1 << 61), UNSUPPORTED), (dict(hidden=(1 << 31) - 15), UNSUPPORTED), (dict(k=0), BAD),
     (dict(k=4097), BAD), (dict(rows=(1 << 30) // K + 1), BAD), (dict(capacity=1 << 30), BAD), (dict(capacity=0), OK),
     (dict(slots=None), BAD), (dict(slots=(10 * A, 0)), BAD), (dict(slots=(10 * A, 11 * A + 2)), BAD),
     (dict(weights=None), OK), (dict(weights=(12 * A, 0)), BAD), (dict(weights=(12 * A + 1, 13 * A)), BAD),
