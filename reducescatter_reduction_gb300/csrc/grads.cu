@@ -282,8 +282,8 @@ static cudaError_t grad_launch(const Launch &L, const GradLaunch &N, size_t *nex
     for (; *next < N.count && a.count < CAP; ++*next) {
         const ccl_tensor_t &t = N.tensors[*next];
         if (t.n == 0 || (t.copy && !N.clip)) continue;
-        const uint32_t S = uint32_t(elem_bytes(t.dtype)), vec = 16 / S;
-        const uint64_t groups = (uintptr_t(t.in) % 128 / S + t.n + vec - 1) / vec;
+        const unsigned by = t.dtype == CCL_F32 ? 2 : 1;      // log2 of an element's bytes
+        const uint64_t groups = (uintptr_t(t.in) % 128 + (t.n << by) + 15) >> 4;
         a.t[a.count++] = {t.in, t.out, t.n, uint32_t(tiles), uint32_t(t.dtype)};
         tiles += (groups + kGradTile - 1) / kGradTile;
     }

@@ -176,7 +176,7 @@ static ccl_status_t grads(ccl_comm *c, size_t count, const ccl_tensor_t *tensors
         if (t.n > (uint64_t(1) << 40) || (total += t.n) > (uint64_t(1) << 40))
             return fail(CCL_ERR_INVALID_ARG, "more than 2^40 elements in all");
         if (!t.in || (clip && !t.out)) return fail(CCL_ERR_INVALID_ARG, "tensor %zu is NULL", i);
-        if (uintptr_t(t.in) % es || (clip && uintptr_t(t.out) % es))
+        if ((uintptr_t(t.in) | (clip ? uintptr_t(t.out) : 0)) & (es - 1))
             return fail(CCL_ERR_INVALID_ARG, "tensor %zu is not aligned to its elements (%zu bytes)", i, es);
         const Range in = range_of(t.in, t.n * es), out = range_of(t.out, t.n * es);
         if (overlap(in, at) || (clip && overlap(out, at))) return fail(CCL_ERR_INVALID_ARG, "norm overlaps tensor %zu", i);
