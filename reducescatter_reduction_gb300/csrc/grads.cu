@@ -113,8 +113,8 @@ struct Twofold {
 
 // The sum of the squares of a thread's groups.  In fp32 where that loses
 // nothing: squares below 2^-149 vanish, and those below 2^-126 lose digits, but
-// beside a sum of 2^-100 neither is seen; sums up to 2^100, of 2^18 tiles and
-// 2^8 threads, stay in range.  Smaller and larger sums, infinities and NaN go
+// beside a sum of 2^-100 neither is seen; sums up to 2^100, of 2^19 tiles and
+// 2^8 threads, stay in range (2^40 elements are at most 2^28 tiles, over 608 CTAs).  Smaller and larger sums, infinities and NaN go
 // through fp64, element by element, and into `rest`.
 template <typename T>
 __device__ __forceinline__ void grad_squares(const GradRecord &t, uint32_t tile, uint32_t short_by, unsigned *status, Twofold &sum, double &rest)
@@ -138,7 +138,7 @@ __device__ __forceinline__ void grad_squares(const GradRecord &t, uint32_t tile,
     uint32_t any = 0;
 #pragma unroll
     for (int i = 0; i < kGradBatch; ++i) any |= g.v[i].x | g.v[i].y | g.v[i].z | g.v[i].w;
-    if (any == 0) return;
+    if ((any & (G::VEC == 4 ? 0x7fffffffu : 0x7fff7fffu)) == 0) return;       // zeros of either sign
 #pragma unroll
     for (int i = 0; i < kGradBatch; ++i) {
         float f[G::VEC];

@@ -68,6 +68,45 @@ def test_sizes(p, rows, k, experts, padded):
     run(random_ids(p, rows, k, experts), valid, experts)
 
 
+def sort_at_once(ids, valid, experts, capacity):
+    """sort_by_expert's values by whole arrays, on the GPU: ids [p, rows, k], valid [p, rows] or None."""
+    p, rows, k = ids.shape
+    e = ids.reshape(-1).long()
+    e = torch.where((e >= 0) & (e < experts), e, experts)
+    if valid is not None:
+        e = torch.where(valid.reshape(-1, 1).expand(-1, k).reshape(-1) != 0, e, experts)
+    counts = torch.bincount(e, minlength=experts + 1)
+    begin = counts.cumsum(0) - counts
+    held = [experts // p + (r < experts % p) for r in range(p)]
+    first = [sum(held[:r]) for r in range(p + 1)]
+    owner = torch.tensor([r for r in range(p) for _ in range(held[r])] + [p - 1], device=e.device)
+    base = torch.stack([begin[f] for f in first])
+    order = torch.sort(e, stable=True).indices
+    of = e[order]
+    at = torch.arange(e.numel(), device=e.device) - base[owner[of]]
+    slot = torch.where((of < experts) & (at < capacity), owner[of] * capacity + at, -1)
+    slots = torch.empty_like(e).scatter_(0, order, slot).view(p, rows, k).int()
+    offsets = [min(int(begin[x] - base[r]), capacity) for r in range(p) for x in range(first[r], first[r + 1] + 1)]
+    return slots, torch.tensor(offsets, dtype=torch.int32, device=e.device)
+
+
+@pytest.mark.parametrize("p, rows, k, experts", [(1, 2000003, 1, 16), (2, 700001, 3, 256), (1, 400001, 2, 4096), (8, 20011, 16, 1000), (3, 30000000, 2, 100)])
+@pytest.mark.parametrize("padded", [False, True])
+def test_long_lists(p, rows, k, experts, padded):
+    """Stretches longer than a warp keeps in registers, up to 180 million choices."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    ids = (torch.rand(p, rows, k, device="cuda", generator=g) ** 2 * (experts + 1)).int() - (torch.rand(p, rows, k, device="cuda", generator=g) < 0.01).int()
+    valid = (torch.rand(p, rows, device="cuda", generator=g) < 0.9).to(torch.uint8) if padded else None
+    capacity = rows * k * 9 // 10
+    slots = torch.full((p, rows, k), 7, dtype=torch.int32, device="cuda")
+    offsets, buffers = Array((experts + p,), torch.int32), [Array((4,), torch.float32) for _ in range(p)]
+    with Comm(buffers) as h:
+        ccl.ccl_expert_sort(h, rows, experts, k, [t.data_ptr() for t in ids], None if valid is None else [t.data_ptr() for t in valid],
+                            capacity, [t.data_ptr() for t in slots], offsets.ptr(), stream())
+    want, want_offsets = sort_at_once(ids, valid, experts, capacity)
+    assert torch.equal(offsets.t, want_offsets) and torch.equal(slots, want)
+
+
 @pytest.mark.parametrize("offset", [1, 2, 3])
 def test_alignment(offset):
     run(random_ids(3, 501, 5, 40), np.ones((3, 501), dtype=np.uint8), 40, offset=offset)

@@ -211,6 +211,30 @@ def test_another_norm():
     assert torch.equal(g.outs[0].t, g.ins[0].t * factor)
 
 
+def test_zeros_of_either_sign():
+    for dtype in ("f32", "bf16"):
+        g = Grads([(9000, dtype, 0), (5, dtype, 0)])
+        g.ins[0].t.fill_(-0.0)
+        g.ins[1].t.fill_(0.0)
+        with g.comm as h:
+            g.call(h, 1.0)
+        assert g.norm.t.tolist() == [0.0, 1.0]
+        assert torch.equal(g.outs[0].t.view(torch.uint8), g.ins[0].t.view(torch.uint8))
+
+
+def test_the_last_launch_is_described():
+    """An operator's words, then a collective's, from one communicator."""
+    g = Grads([(100, "f32", 0)] * 2)
+    with g.comm as h:
+        ccl.ccl_grad_norm(h, g.tensors(), g.norm.ptr(), stream())
+        assert ccl.ccl_comm_last_launch(h).startswith("grad_norm ") and "kernels=1" in ccl.ccl_comm_last_launch(h)
+        ccl.ccl_allreduce(h, "sum", "f32", 4, "ring", stream())
+        assert ccl.ccl_comm_last_launch(h).startswith("allreduce")
+        before = ccl.ccl_comm_launch_count(h)
+        ccl.ccl_grad_clip(h, g.tensors(), 1.0, g.norm.ptr(), stream())
+        assert ccl.ccl_comm_last_launch(h).startswith("grad_clip ") and ccl.ccl_comm_launch_count(h) == before + 1
+
+
 def test_the_same_bits():
     a, b = Grads([(3000001, "bf16", 0), (70000, "f32", 0)]), Grads([(3000001, "bf16", 0), (70000, "f32", 0)])
     for g in (a, b):
