@@ -173,25 +173,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
     uint32_t *mine = count_s + warp * row;
     const bool kept = end - begin <= 32 * kSortItems;      // the stretch stays in registers; of others the numbers go through the slots
     uint32_t e[kSortItems], number[kSortItems];
-    for (uint32_t g0 = begin; g0 < end; g0 += 32 * kSortItems) {
-        part.experts(g0 + lane, 32, e);
-#pragma unroll
-        for (int i = 0; i < kSortItems; ++i) {
-            if (g0 + i * 32 >= end) break;
-            uint32_t same = __ballot_sync(0xffffffffu, e[i] < E);
-#pragma unroll
-            for (int b = 0; b < BITS; ++b) {
-                const int set = int(e[i] << (31 - b)) >> 31;       // all ones or none
-                same &= ~(__ballot_sync(0xffffffffu, set) ^ uint32_t(set));
-            }
-            number[i] = e[i] < E ? mine[e[i]] + __popc(same & ((1u << lane) - 1)) : 0;
-            __syncwarp();
-            if (e[i] < E && lane == 31 - __clz(same)) mine[e[i]] = number[i] + 1;
-            __syncwarp();
-            if (!kept && g0 + i * 32 + lane < end)
-                if (int32_t *to = part.slot(g0 + i * 32 + lane)) *to = int32_t(number[i]);
-        }
-    }
+    part.experts(begin + lane, 32, e);      // (under way while the cells are summed)
     if (!ALONE) {
         // Four experts a load; threads side by side take experts, and then shares of the parts, so that the loads of all
         // parts are under way at once.
@@ -216,8 +198,28 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(const __grid_c
                 }
         }
     }
+    for (uint32_t g0 = begin; g0 < end; g0 += 32 * kSortItems) {
+        if (g0 != begin) part.experts(g0 + lane, 32, e);
+#pragma unroll
+        for (int i = 0; i < kSortItems; ++i) {
+            if (g0 + i * 32 >= end) break;
+            uint32_t same = __ballot_sync(0xffffffffu, e[i] < E);
+#pragma unroll
+            for (int b = 0; b < BITS; ++b) {
+                const int set = int(e[i] << (31 - b)) >> 31;       // all ones or none
+                same &= ~(__ballot_sync(0xffffffffu, set) ^ uint32_t(set));
+            }
+            number[i] = e[i] < E ? mine[e[i]] + __popc(same & ((1u << lane) - 1)) : 0;
+            __syncwarp();
+            if (e[i] < E && lane == 31 - __clz(same)) mine[e[i]] = number[i] + 1;
+            __syncwarp();
+            if (!kept && g0 + i * 32 + lane < end)
+                if (int32_t *to = part.slot(g0 + i * 32 + lane)) *to = int32_t(number[i]);
+        }
+    }
     __syncthreads();
     // a warp takes an expert at a time, a lane a warp's count
+#pragma unroll 4
     for (uint32_t x = warp; x < E; x += kSortThreads / 32) {
         const uint32_t own = lane < a.warps ? count_s[lane * row + x] : 0;
         uint32_t up = own;

@@ -456,10 +456,11 @@ static cudaError_t quant_launch(const Launch &L, const NormE4m3Launch &N, Launch
     a.status = L.status;
     a.wait_ns = L.wait_limit_ns > 0 ? L.wait_limit_ns : 2000000000LL;
     a.stall_test = L.stall_test;
-    // CTA shape by rows against the SMs, as in rmsnorm.cu
-    const uint64_t units = (N.norm.hidden + VEC - 1) / VEC, sms = uint64_t(L.num_sms), rows = N.norm.rows;
+    // CTA shape by rows against the SMs, as in rmsnorm.cu, and by width.  Rows that are no 16-byte groups, us with 64 / 512
+    // threads (128): 2320 x 372 f16 p=1 8.9 / 21, 9217 x 499 f32 p=1 15 / 45; 914 x 1795 bf16 p=8 (128: 34) / 26.
+    const uint64_t units = VECTOR ? N.norm.hidden / VEC : (N.norm.hidden + 32 * VEC - 1) / (32 * VEC) * 32, sms = uint64_t(L.num_sms), rows = N.norm.rows;
     const int threads = rows < sms      ? 128
-                        : !VECTOR       ? 512
+                        : !VECTOR       ? (units <= 128 ? 64 : 512)
                         : rows < 2 * sms ? 1024
                         : units <= 256  ? 64
                         : units <= 512  ? 128
@@ -490,7 +491,9 @@ static cudaError_t quant_launch(const Launch &L, const NormE4m3Launch &N, Launch
                : threads == 512 ? ar_rmsnorm_e4m3_kernel<T, P, 512, 4, true>
                                 : ar_rmsnorm_e4m3_kernel<T, P, 256, 4, true>;
     } else {
-        kern = threads == 128 ? ar_rmsnorm_e4m3_kernel<T, P, 128, 1, false> : ar_rmsnorm_e4m3_kernel<T, P, 512, 2, false>;
+        kern = keep == 1        ? ar_rmsnorm_e4m3_kernel<T, P, 128, 1, false>
+               : threads == 64  ? ar_rmsnorm_e4m3_kernel<T, P, 64, 2, false>
+                                : ar_rmsnorm_e4m3_kernel<T, P, 512, 2, false>;
     }
     const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, a);
     if (err != cudaSuccess) return err;

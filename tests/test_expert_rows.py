@@ -199,6 +199,23 @@ def test_bits_are_copied():
     layer.check_rows()
 
 
+@pytest.mark.parametrize("hidden, offset", [(33, 0), (64, 1), (2, 0), (1, 3), (1000, 2)])
+def test_int32_rows_anywhere(hidden, offset):
+    """Rows of 4-byte words that are no 16-byte groups: scales, or codes of an odd width."""
+    layer = Layer("f32", 3, 30, hidden, 2, offset=offset, weighted=False)
+    for a in layer.tokens:
+        a.t.view(torch.int32).copy_(torch.randint(-2 ** 31, 2 ** 31 - 1, a.t.shape, device="cuda"))
+    with layer.there as h:
+        ccl.ccl_expert_dispatch(h, "i32", 30, hidden, 2, ptrs(layer.slots), None, layer.capacity, stream())
+    layer.check_rows()
+
+
+@pytest.mark.parametrize("hidden", [16, 13])
+def test_thousands_of_choices(hidden):
+    """Lists of choices that need more shared memory than a kernel has without asking."""
+    Layer("bf16", 1, 2, hidden, 3100).all()
+
+
 @pytest.mark.parametrize("weighted", [False, True])
 def test_gradients_by_differences(weighted):
     """The three operators' gradients against central differences of sum(c * y), in fp32 with inputs that are small whole
