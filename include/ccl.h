@@ -540,7 +540,7 @@ CCL_API ccl_status_t ccl_expert_sort(ccl_comm_t comm, size_t rows, size_t expert
  * Bytes moved: p rows hidden s (1 + k), the lists.
  * Errors: CCL_ERR_INVALID_ARG (a size out of range, a missing array, overlap;
  * in place is overlap), CCL_ERR_UNSUPPORTED (int32 with weights, hidden above
- * 2^31 - 16), CCL_ERR_CUDA. */
+ * 2^30), CCL_ERR_CUDA. */
 CCL_API ccl_status_t ccl_expert_dispatch(ccl_comm_t comm, ccl_dtype_t dtype, size_t rows, size_t hidden, size_t k,
                                          const int32_t *const *slots, const float *const *weights, size_t capacity,
                                          void *stream);

@@ -274,13 +274,16 @@ def ccl_balance_loss(comm: int, dtype, steps, rows: int, experts: int, k: int, e
                                 counts or None, tokens or None, loss or None, stream or None))
 
 
+_PACK = [struct.Struct(f"{p}Q").pack for p in range(CCL_MAX_RANKS + 1)]
+
+
 def _rank_array(p: int, ptrs, what: str):
     """One device pointer for each of p ranks, as the bytes of the C array (None: NULL)."""
     if ptrs is None:
         return None
     if len(ptrs) != p:
         _want_len(ptrs, p, what)
-    return struct.pack(f"{p}Q", *ptrs)
+    return _PACK[p](*ptrs)
 
 
 def _tensors(tensors):

@@ -80,7 +80,7 @@ static ccl_status_t expert_rows(ccl_comm *c, int op, int dtype, size_t rows, siz
     if ((st = check_choices(c, rows, k, capacity)) != CCL_OK) return st;
     const size_t es = elem_bytes(dtype);
     if (hidden == 0) return fail(CCL_ERR_INVALID_ARG, "hidden must be positive");
-    if (hidden > 0x7ffffff0ull) return fail(CCL_ERR_UNSUPPORTED, "%s: hidden %zu above 2^31 - 16", what, hidden);
+    if (hidden > (size_t(1) << 30)) return fail(CCL_ERR_UNSUPPORTED, "%s: hidden %zu above 2^30", what, hidden);   // columns are 32-bit
     const size_t most = rows > capacity ? rows : capacity;
     if (most && hidden > (SIZE_MAX / 4) / most / es) return fail(CCL_ERR_INVALID_ARG, "rows * hidden too large");
     if (rows == 0) return CCL_OK;

@@ -152,7 +152,7 @@ def test_sort(front, change, want):
 
 @pytest.mark.parametrize("name", ["dispatch", "combine", "grad"])
 @pytest.mark.parametrize("change, want", [
-    (dict(), OK), (dict(dtype=7), BAD), (dict(hidden=0), BAD), (dict(hidden=1 << 61), UNSUPPORTED), (dict(hidden=(1 << 31) - 15), UNSUPPORTED), (dict(k=0), BAD),
+    (dict(), OK), (dict(dtype=7), BAD), (dict(hidden=0), BAD), (dict(hidden=1 << 61), UNSUPPORTED), (dict(hidden=(1 << 30) + 1), UNSUPPORTED), (dict(k=0), BAD),
     (dict(k=4097), BAD), (dict(rows=(1 << 30) // K + 1), BAD), (dict(capacity=1 << 30), BAD), (dict(capacity=0), OK),
     (dict(slots=None), BAD), (dict(slots=(10 * A, 0)), BAD), (dict(slots=(10 * A, 11 * A + 2)), BAD),
     (dict(weights=None), OK), (dict(weights=(12 * A, 0)), BAD), (dict(weights=(12 * A + 1, 13 * A)), BAD),
