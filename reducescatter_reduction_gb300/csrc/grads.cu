@@ -6,7 +6,7 @@
 // loads go over 17 sectors, not 16: with that and the sums below, the norm of 300 bf16 tensors of 1.2 GB 190 -> 177 us,
 // their clipping 391 -> 374); the tiles of all tensors are numbered
 // through, and a CTA takes consecutive ones, so tensors of any size share the
-// SMs evenly.  The tensors' addresses and each CTA's first tensor travel as
+// SMs evenly.  The tensors' addresses, and where every fourth CTA begins among them, travel as
 // kernel parameters.  Bound by memory where the tensors are large: three
 // passes over 300 bf16 tensors of 1.2 GB, out of place, in 580 us, 6.2 TB/s; below some MB by the
 // launches and the join of the CTAs' sums (3 + 2 us for 1000 values).
@@ -19,6 +19,7 @@ constexpr int kGradThreads = 256;
 constexpr int kGradBatch = 4;                                    // groups a thread has of a tile
 constexpr uint32_t kGradTile = kGradThreads * kGradBatch;        // groups of a tile
 constexpr uint32_t kGradMaxGrid = 1280;
+constexpr uint32_t kGradSteps = 4;
 // CTAs an SM at most.  Measured (us; 4 against 8 an SM): the norm of 400 f32 tensors of 12 MB 7.3, 10.3, of 20 bf16 ones of 100 MB
 // 17.9, 20.5, of 300 of 1.2 GB 177, 179; clipping the last 402, 374.
 constexpr uint32_t kGradNormCtas = 4, kGradClipCtas = 8;
@@ -35,7 +36,7 @@ struct GradRecord {
 template <int CAP>
 struct GradArgs {
     GradRecord t[CAP];
-    uint16_t start[kGradMaxGrid];        // the tensor of a CTA's first tile
+    uint16_t start[kGradMaxGrid / kGradSteps];   // the tensor of the first tile of every fourth CTA
     uint32_t count, share, more;         // tiles of a CTA: share, and one more for the first `more`
     float max_norm;
     int first_launch, last_launch;
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const __grid_co
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     Twofold mine;
     double rest = 0.0;
-    uint32_t i = a.start[blockIdx.x];
+    uint32_t i = a.start[blockIdx.x / kGradSteps];
     for (uint32_t tile = begin; tile < end; ++tile) {
         while (i + 1 < a.count && a.t[i + 1].first <= tile) ++i;
         const GradRecord &t = a.t[i];
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_co
     if (a.last_launch && blockIdx.x == 0 && threadIdx.x == 0) a.norm[1] = factor;
     const uint32_t begin = blockIdx.x * a.share + min(blockIdx.x, a.more), end = begin + a.share + (blockIdx.x < a.more ? 1 : 0);
     if (begin == end) return;
-    uint32_t i = a.start[blockIdx.x];
+    uint32_t i = a.start[blockIdx.x / kGradSteps];
     while (i + 1 < a.count && a.t[i + 1].first < end) ++i;
     // backwards: what the norm's pass read last is still in L2
     for (uint32_t tile = end; tile-- > begin;) {
@@ -301,11 +302,10 @@ static cudaError_t grad_launch(const Launch &L, const GradLaunch &N, size_t *nex
     const unsigned grid = unsigned(tiles < 1 ? 1 : tiles < most ? tiles : most);
     a.share = uint32_t(tiles / grid);
     a.more = uint32_t(tiles % grid);
-    uint32_t tile = 0;
-    for (unsigned b = 0, i = 0; b < grid; ++b) {
+    for (uint32_t b = 0, i = 0; b < grid; b += kGradSteps) {
+        const uint32_t tile = b * a.share + (b < a.more ? b : a.more);
         while (i + 1 < a.count && a.t[i + 1].first <= tile) ++i;
-        a.start[b] = uint16_t(i);
-        tile += a.share + (b < a.more ? 1 : 0);
+        a.start[b / kGradSteps] = uint16_t(i);
     }
     const cudaError_t err = launch_dependent(N.clip ? grad_clip_kernel<CAP> : grad_norm_kernel<CAP>, grid, kGradThreads, 0, L.stream, a);
     if (err != cudaSuccess) return err;

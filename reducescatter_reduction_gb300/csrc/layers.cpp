@@ -164,56 +164,53 @@ static ccl_status_t grads(ccl_comm *c, size_t count, const ccl_tensor_t *tensors
     if ((st = check_aligned(norm, 4, "norm")) != CCL_OK) return st;
     if (clip && !(max_norm >= 0.0f && max_norm <= 3.4e38f)) return fail(CCL_ERR_INVALID_ARG, "max_norm must be finite and >= 0");
     const Range at = range_of(norm, 8);
+    // the stretches of memory that clipping reads and writes: tensors that follow one another are one; more than 64 go to the heap
+    // (what is read in front and what is written behind it, as each often is in order already)
+    Span few[64], *spans = few;
+    size_t room = 32, reads = 0, writes = 0;
     uint64_t total = 0;
-    size_t reads = 0, writes = 0;     // stretches of memory: tensors that follow one another are one
-    uintptr_t read_end = 0, write_end = 0;
-    for (size_t i = 0; i < count; ++i) {
+    st = CCL_OK;
+    for (size_t i = 0; i < count && st == CCL_OK; ++i) {
         const ccl_tensor_t &t = tensors[i];
-        if (t.dtype == CCL_I32) return fail(CCL_ERR_UNSUPPORTED, "%s: tensor %zu needs a floating-point dtype", what, i);
-        if (t.dtype < CCL_F32 || t.dtype > CCL_BF16) return fail(CCL_ERR_INVALID_ARG, "tensor %zu: unknown dtype %d", i, int(t.dtype));
-        if (t.n == 0) continue;
+        if (t.dtype == CCL_I32) st = fail(CCL_ERR_UNSUPPORTED, "%s: tensor %zu needs a floating-point dtype", what, i);
+        else if (t.dtype < CCL_F32 || t.dtype > CCL_BF16) st = fail(CCL_ERR_INVALID_ARG, "tensor %zu: unknown dtype %d", i, int(t.dtype));
+        if (st != CCL_OK || t.n == 0) continue;
         const size_t es = elem_bytes(t.dtype);
-        if (t.n > (uint64_t(1) << 40) || (total += t.n) > (uint64_t(1) << 40))
-            return fail(CCL_ERR_INVALID_ARG, "more than 2^40 elements in all");
-        if (!t.in || (clip && !t.out)) return fail(CCL_ERR_INVALID_ARG, "tensor %zu is NULL", i);
-        if ((uintptr_t(t.in) | (clip ? uintptr_t(t.out) : 0)) & (es - 1))
-            return fail(CCL_ERR_INVALID_ARG, "tensor %zu is not aligned to its elements (%zu bytes)", i, es);
-        const Range in = range_of(t.in, t.n * es), out = range_of(t.out, t.n * es);
-        if (overlap(in, at) || (clip && overlap(out, at))) return fail(CCL_ERR_INVALID_ARG, "norm overlaps tensor %zu", i);
-        if (!clip) continue;
-        if (t.out != t.in) {
-            reads += in.lo != read_end;
-            read_end = in.hi;
-        }
-        writes += out.lo != write_end;
-        write_end = out.hi;
-    }
-    if (clip && reads + writes) {
-        Span few[64], *s = few;
-        if (reads + writes > 64) {
-            s = new (std::nothrow) Span[reads + writes];
-            if (!s) return fail(CCL_ERR_NOMEM, "host allocation failed");
-        }
-        Span *r = s, *w = s + reads;
-        read_end = write_end = 0;
-        for (size_t i = 0; i < count; ++i) {
-            const ccl_tensor_t &t = tensors[i];
-            if (t.n == 0) continue;
-            const uint64_t bytes = t.n * elem_bytes(t.dtype);
-            const Range in = range_of(t.in, bytes), out = range_of(t.out, bytes);
-            if (t.out != t.in) {
-                if (in.lo != read_end) *r++ = {in, "the input of tensor", int(i), false};
-                else r[-1].at.hi = in.hi;
-                read_end = in.hi;
+        const Range in = range_of(t.in, t.n * es), out = clip ? range_of(t.out, t.n * es) : in;
+        if (t.n > (uint64_t(1) << 40) || (total += t.n) > (uint64_t(1) << 40)) st = fail(CCL_ERR_INVALID_ARG, "more than 2^40 elements in all");
+        else if (!in.lo || !out.lo) st = fail(CCL_ERR_INVALID_ARG, "tensor %zu is NULL", i);
+        else if ((in.lo | out.lo) & (es - 1)) st = fail(CCL_ERR_INVALID_ARG, "tensor %zu is not aligned to its elements (%zu bytes)", i, es);
+        else if (overlap(in, at) || overlap(out, at)) st = fail(CCL_ERR_INVALID_ARG, "norm overlaps tensor %zu", i);
+        if (st != CCL_OK || !clip) continue;
+        if (reads == room || writes == room) {
+            Span *more = new (std::nothrow) Span[2 * count];
+            if (!more) {
+                st = fail(CCL_ERR_NOMEM, "host allocation failed");
+                continue;
             }
-            if (out.lo != write_end) *w++ = {out, "the output of tensor", int(i), true};
-            else w[-1].at.hi = out.hi;
-            write_end = out.hi;
+            std::copy(spans, spans + reads, more);
+            std::copy(spans + room, spans + room + writes, more + count);
+            spans = more;
+            room = count;
         }
-        st = check_spans(s, reads + writes);
-        if (s != few) delete[] s;
-        if (st != CCL_OK) return st;
+        if (t.out != t.in) {
+            if (reads && spans[reads - 1].at.hi == in.lo) spans[reads - 1].at.hi = in.hi;
+            else spans[reads++] = {in, "the input of tensor", int(i), false};
+        }
+        Span *last = spans + room + writes;
+        if (writes && last[-1].at.hi == out.lo) {
+            last[-1].at.hi = out.hi;
+        } else {
+            *last = {out, "the output of tensor", int(i), true};
+            ++writes;
+        }
     }
+    if (st == CCL_OK && writes) {
+        std::copy(spans + room, spans + room + writes, spans + reads);
+        st = check_spans(spans, reads + writes);
+    }
+    if (spans != few) delete[] spans;
+    if (st != CCL_OK) return st;
     DeviceGuard g(c->device);
     if (g.err != cudaSuccess) return cuda_fail(g.err, what);
     GradLaunch N;
