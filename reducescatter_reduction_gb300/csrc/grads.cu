@@ -3,12 +3,11 @@
 //   norm = sqrt(sum x^2),  out = x min(1, max_norm / (norm + 1e-6))
 // A tensor is cut into tiles of 16-byte groups that begin on 128-byte boundaries
 // of memory wherever the tensor begins (on 16-byte boundaries a warp's
-// loads go over 17 sectors, not 16: with that and the sums below, the norm of 300 bf16 tensors of 1.2 GB 190 -> 177 us,
-// their clipping 391 -> 374); the tiles of all tensors are numbered
+// loads go over 17 sectors, not 16: with that and the sums below, the norm of 300 bf16 tensors of 1.2 GB 190 -> 177 us); the tiles of all tensors are numbered
 // through, and a CTA takes consecutive ones, so tensors of any size share the
-// SMs evenly.  The tensors' addresses, and where every fourth CTA begins among them, travel as
+// SMs evenly.  The tensors' addresses, and where every fourth share begins among them, travel as
 // kernel parameters.  Bound by memory where the tensors are large: three
-// passes over 300 bf16 tensors of 1.2 GB, out of place, in 580 us, 6.2 TB/s; below some MB by the
+// passes over 300 bf16 tensors of 1.2 GB, out of place, in 553 us, 6.5 TB/s; below some MB by the
 // launches and the join of the CTAs' sums (3 + 2 us for 1000 values).
 #include "logits.cuh"
 
@@ -20,9 +19,9 @@ constexpr int kGradBatch = 4;                                    // groups a thr
 constexpr uint32_t kGradTile = kGradThreads * kGradBatch;        // groups of a tile
 constexpr uint32_t kGradMaxGrid = 1280;
 constexpr uint32_t kGradSteps = 4;
-// CTAs an SM at most.  Measured (us; 4 against 8 an SM): the norm of 400 f32 tensors of 12 MB 7.3, 10.3, of 20 bf16 ones of 100 MB
-// 17.9, 20.5, of 300 of 1.2 GB 177, 179; clipping the last 402, 374.
-constexpr uint32_t kGradNormCtas = 4, kGradClipCtas = 8;
+// Shares of the tiles, an SM: one CTA of the norm has each.  (us; 4 against 8 an SM: the norm of 400 f32 tensors of 12 MB 7.3, 10.3,
+// of 20 bf16 ones of 100 MB 17.9, 20.5, of 300 of 1.2 GB 177, 179.)
+constexpr uint32_t kGradShares = 4;
 static_assert(kGradMaxGrid <= kMaxPartials, "");
 
 struct GradRecord {
@@ -36,8 +35,9 @@ struct GradRecord {
 template <int CAP>
 struct GradArgs {
     GradRecord t[CAP];
-    uint16_t start[kGradMaxGrid / kGradSteps];   // the tensor of the first tile of every fourth CTA
-    uint32_t count, share, more;         // tiles of a CTA: share, and one more for the first `more`
+    uint16_t start[kGradMaxGrid / kGradSteps];   // the tensor of the first tile of every fourth share
+    uint32_t count, share, more;         // tiles of a share; one more for the first `more`
+    uint32_t team_shift;                 // clipping: 2^team_shift CTAs have a share
     float max_norm;
     int first_launch, last_launch;
     float *norm;
@@ -259,12 +259,13 @@ __global__ void __launch_bounds__(kGradThreads) grad_clip_kernel(const __grid_co
     const float by = __fdiv_rn(a.max_norm, a.norm[0] + 1e-6f);
     const float factor = by > 1.0f ? 1.0f : by;                  // (NaN stays NaN)
     if (a.last_launch && blockIdx.x == 0 && threadIdx.x == 0) a.norm[1] = factor;
-    const uint32_t begin = blockIdx.x * a.share + min(blockIdx.x, a.more), end = begin + a.share + (blockIdx.x < a.more ? 1 : 0);
+    const uint32_t part = blockIdx.x >> a.team_shift, begin = part * a.share + min(part, a.more), end = begin + a.share + (part < a.more ? 1 : 0);
     if (begin == end) return;
-    uint32_t i = a.start[blockIdx.x / kGradSteps];
+    uint32_t i = a.start[part / kGradSteps];
     while (i + 1 < a.count && a.t[i + 1].first < end) ++i;
     // backwards: what the norm's pass read last is still in L2
-    for (uint32_t tile = end; tile-- > begin;) {
+    for (uint32_t at = blockIdx.x & ((1u << a.team_shift) - 1); at < end - begin; at += 1u << a.team_shift) {
+        const uint32_t tile = end - 1 - at;
         while (a.t[i].first > tile) --i;
         const GradRecord &t = a.t[i];
         if (factor == 1.0f && t.out == t.in) continue;
@@ -298,19 +299,22 @@ static cudaError_t grad_launch(const Launch &L, const GradLaunch &N, size_t *nex
     a.partials = reinterpret_cast<double *>(static_cast<char *>(N.scratch) + kScratchHead);
     a.status = L.status;
     a.short_by = L.stall_test == 2 ? 1 : 0;
-    const uint64_t ctas = uint64_t(L.num_sms) * (N.clip ? kGradClipCtas : kGradNormCtas), most = ctas < kGradMaxGrid ? ctas : kGradMaxGrid;
+    const uint64_t ctas = uint64_t(L.num_sms) * kGradShares, most = ctas < kGradMaxGrid ? ctas : kGradMaxGrid;
     const unsigned grid = unsigned(tiles < 1 ? 1 : tiles < most ? tiles : most);
     a.share = uint32_t(tiles / grid);
     a.more = uint32_t(tiles % grid);
+    // Clipping, CTAs a share.  Measured (us for norm and clipping; 1 / 2 / 4 / 8): 370 tiles - / 9.9 / 10.0 / 11.1, 1000 tiles
+    // - / 11.4 / 11.9 / 13.4, 12000 - / 49.4 / 49.1 / 49.3, 73000 614 / 587 / 557 / 552.
+    a.team_shift = tiles <= grid ? 0 : a.share < 8 ? 1 : a.share < 32 ? 2 : 3;
     for (uint32_t b = 0, i = 0; b < grid; b += kGradSteps) {
         const uint32_t tile = b * a.share + (b < a.more ? b : a.more);
         while (i + 1 < a.count && a.t[i + 1].first <= tile) ++i;
         a.start[b / kGradSteps] = uint16_t(i);
     }
-    const cudaError_t err = launch_dependent(N.clip ? grad_clip_kernel<CAP> : grad_norm_kernel<CAP>, grid, kGradThreads, 0, L.stream, a);
+    const cudaError_t err = launch_dependent(N.clip ? grad_clip_kernel<CAP> : grad_norm_kernel<CAP>, N.clip ? grid << a.team_shift : grid, kGradThreads, 0, L.stream, a);
     if (err != cudaSuccess) return err;
     info->kernel = N.clip ? "grad_clip" : "grad_norm";
-    info->grid = int(grid);
+    info->grid = int(N.clip ? grid << a.team_shift : grid);
     info->block = kGradThreads;
     ++info->kernels;
     return cudaSuccess;
