@@ -4,7 +4,7 @@
 //   dispatch  row[slot_tj] = w_tj x_t
 //   combine   y_t          = sum_j w_tj row[slot_tj]
 //   gradient  drow[slot_tj] = w_tj dy_t,  dw_tj = <dy_t, row[slot_tj]>
-// Each is driven by the tokens: a team of 32 to 256 threads takes one, so a
+// Each is driven by the tokens: a team of 8 to 256 threads takes one, so a
 // token's row is read (or written) once and its k expert rows once each, which
 // is all the traffic there has to be.  A thread loads a batch of KB choices of
 // UN units before it uses the first.
@@ -14,6 +14,7 @@ namespace ccl {
 
 constexpr unsigned kSiteExperts = 11;
 constexpr int kRowsThreads = 256;
+constexpr int kRowsTeam = 8;       // threads of a team, at least
 
 template <int PM>
 struct RowsArgs {
@@ -97,17 +98,16 @@ struct RowView {
 template <typename T>
 struct Inner {
     static constexpr int VEC = Traits<T>::VEC;
-    int last, head, tail, width;     // columns [0, head) and [tail, width)
-    __device__ __forceinline__ Inner(int shift, int w) : width(w)
+    int last, head, tail, edges;     // columns [0, head) and from `tail` on are the edges
+    __device__ __forceinline__ Inner(int shift, int width)
     {
-        last = (shift + w) / VEC - 1;
+        last = (shift + width) / VEC - 1;
         head = 2 * VEC - shift;
         tail = last * VEC - shift;
-        if (last <= 2) head = tail = w;
+        if (last <= 2) head = tail = width;
+        edges = head + width - tail;
     }
-    // The edge column of a thread, or from `width` on; then that + step.
-    __device__ __forceinline__ int first(int thread) const { return thread < head ? thread : tail + thread - head; }
-    __device__ __forceinline__ int next(int c, int thread, int step) const { return head == width ? c + step : c < head ? tail + thread + step - head : c + step; }
+    __device__ __forceinline__ int edge(int n) const { return n < head ? n : tail + n - head; }
 };
 
 // One choice of a team's token: where its row begins, and its weight.
@@ -125,6 +125,27 @@ struct Team {
     uint64_t first, end;        // the team's units: of a row, or of a row and as many more as it may lie over
     bool on;                    // it has a token
     Choice *list;
+
+    // The sums of a team's threads, N of them: its lanes' in every thread of a warp, or of the team where that is less ...
+    template <int N>
+    __device__ __forceinline__ void lanes(float (&v)[N]) const
+    {
+        if (threads >= 32) {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
+        } else {
+            for (uint32_t o = threads / 2; o > 0; o >>= 1)
+#pragma unroll
+                for (int j = 0; j < N; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
+        }
+    }
+    // ... left in parts[part()] by its first, and added up from parts[first_part()] on.
+    __device__ __forceinline__ uint32_t part() const { return threadIdx.x / min(threads, 32u); }
+    __device__ __forceinline__ bool leads() const { return thread % 32 == 0; }
+    __device__ __forceinline__ uint32_t parts() const { return max(1u, threads / 32); }
+    __device__ __forceinline__ uint32_t first_part() const { return (threadIdx.x - thread) / min(threads, 32u); }
 
     // `of` has the experts' buffers; `list` room for the choices of all teams.
     __device__ __forceinline__ Team(const RowsArgs<PM> &a, const void *const *of, uint32_t S, uint64_t units, Choice *all)
@@ -253,12 +274,11 @@ __global__ void __launch_bounds__(kRowsThreads, KB * UN == 8 ? 3 : 4) combine_gr
     using Tr = Traits<T>;
     constexpr uint32_t VEC = Tr::VEC, S = 16 / VEC;
     extern __shared__ Choice lists[];
-    __shared__ float parts[kRowsThreads / 32][KB];
+    __shared__ float parts[kRowsThreads / kRowsTeam][KB];
     grid_dependency_wait();
     grid_dependents_launch();
     const Team<PM> t(a, a.out, S, a.hidden / VEC, lists);
     const char *token = static_cast<const char *>(a.in[t.rank]) + uint64_t(t.token) * a.hidden * S;
-    const uint32_t warps = t.threads / 32, warp = threadIdx.x / 32;
     for (uint32_t first = 0; first < a.k; first += KB) {
         float sum[KB];
 #pragma unroll
@@ -304,16 +324,14 @@ __global__ void __launch_bounds__(kRowsThreads, KB * UN == 8 ? 3 : 4) combine_gr
             }
         }
         // the team's sums: its warps', in order
+        t.lanes(sum);
+        if (t.leads())
 #pragma unroll
-        for (int j = 0; j < KB; ++j) {
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], o);
-            if (threadIdx.x % 32 == 0) parts[warp][j] = sum[j];
-        }
+            for (int j = 0; j < KB; ++j) parts[t.part()][j] = sum[j];
         __syncthreads();
         if (t.on && t.thread < KB && first + t.thread < a.k) {
             float s = 0.0f;
-            for (uint32_t w = 0; w < warps; ++w) s += parts[warp + w][t.thread];
+            for (uint32_t w = 0; w < t.parts(); ++w) s += parts[t.first_part() + w][t.thread];
             const uint64_t entry = uint64_t(t.token) * a.k + first + t.thread;
             if (entry_held(a, entry)) a.dweights[t.rank][entry] = t.list[first + t.thread].row ? s : 0.0f;
         }
@@ -347,14 +365,13 @@ __global__ void __launch_bounds__(kRowsThreads, 5) scatter_odd_kernel(const __gr
     constexpr int VEC = Tr::VEC, S = 16 / VEC, KB = 8;
     constexpr bool RAW = std::is_same<T, I32>::value;
     extern __shared__ Choice lists[];
-    __shared__ float parts[kRowsThreads / 32][KB];
+    __shared__ float parts[kRowsThreads / kRowsTeam][KB];
     grid_dependency_wait();
     grid_dependents_launch();
     const Team<PM> t(a, a.out, S, a.hidden / VEC + 2, lists);
     const int width = int(a.hidden), thread = int(t.thread), threads = int(t.threads);
     const char *token = static_cast<const char *>(a.in[t.rank]) + uint64_t(t.token) * a.hidden * S;
     const RowView<T> x(token);
-    const uint32_t warps = t.threads / 32, warp = threadIdx.x / 32;
     for (uint32_t first = 0; first < a.k; first += KB) {
         for (uint32_t j = 0; j < KB && first + j < a.k; ++j) {
             const Choice c = t.list[first + j];
@@ -387,7 +404,8 @@ __global__ void __launch_bounds__(kRowsThreads, 5) scatter_odd_kernel(const __gr
                     st_stream_v4(to.at(g), v);
                 }
                 if (blockIdx.y == 0)
-                    for (int col = in.first(thread); col < width; col = in.next(col, thread, threads)) {
+                    for (int n = thread; n < in.edges; n += threads) {
+                        const int col = in.edge(n);
                         if constexpr (RAW) {
                             *reinterpret_cast<uint32_t *>(to.column(col)) = *reinterpret_cast<const uint32_t *>(x.column(col));
                         } else if (!GRAD && !a.weighted) {
@@ -401,16 +419,16 @@ __global__ void __launch_bounds__(kRowsThreads, 5) scatter_odd_kernel(const __gr
                     }
             }
             if constexpr (GRAD) {
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (threadIdx.x % 32 == 0) parts[warp][j] = sum;
+                float one[1] = {sum};
+                t.lanes(one);
+                if (t.leads()) parts[t.part()][j] = one[0];
             }
         }
         if constexpr (GRAD) {
             __syncthreads();
             if (t.on && t.thread < KB && first + t.thread < a.k) {
                 float s = 0.0f;
-                for (uint32_t w = 0; w < warps; ++w) s += parts[warp + w][t.thread];
+                for (uint32_t w = 0; w < t.parts(); ++w) s += parts[t.first_part() + w][t.thread];
                 const uint64_t entry = uint64_t(t.token) * a.k + first + t.thread;
                 if (entry_held(a, entry)) a.dweights[t.rank][entry] = s;
             }
@@ -461,7 +479,8 @@ __global__ void __launch_bounds__(kRowsThreads, 5) combine_odd_kernel(const __gr
         st_stream_v4(to.at(g), Tr::pack(sum));
     }
     if (blockIdx.y == 0)
-        for (int col = in.first(thread); col < width; col = in.next(col, thread, threads)) {
+        for (int n = thread; n < in.edges; n += threads) {
+            const int col = in.edge(n);
             float sum = 0.0f;
 #pragma unroll 4
             for (uint32_t j = 0; j < a.k; ++j) {
@@ -496,11 +515,15 @@ static cudaError_t rows_launch(const Launch &L, const RowsLaunch &N, LaunchInfo 
     a.weighted = N.weights ? 1 : 0;
     a.status = L.status;
     a.held = a.rows - (L.stall_test == 2 ? 1 : 0);
-    // a team has about four units (two batches; of odd rows two units) a thread, and more threads where there are few tokens or many choices
+    // A team has four batches of units a thread (of odd rows two units), at least a warp where the row has a unit for each lane, and
+    // more threads where there are few tokens or many choices.  (Rows of 8 units, 100000 bf16 tokens, k=2, with teams of 32 and 8:
+    // dispatch 39, 12.4 us; combine 43, 13.5; its gradient 62, 20.)
     constexpr uint64_t VEC = Traits<T>::VEC;
     const uint64_t units = N.hidden / VEC + (KB ? 0 : 2), tokens = N.rows * uint64_t(L.p), sms = uint64_t(L.num_sms);
-    a.team_shift = 5;
-    while (a.team_shift < 8 && ((uint64_t(KB ? 4 * UN : 2) << a.team_shift) < units || tokens >> (8 - a.team_shift) < 4 * sms || N.k > 32)) ++a.team_shift;
+    a.team_shift = 3;
+    while (a.team_shift < 8 && ((a.team_shift < 5 && (uint64_t(1) << a.team_shift) < units) || (uint64_t(KB ? 4 * UN : 2) << a.team_shift) < units ||
+                                tokens >> (8 - a.team_shift) < 4 * sms || N.k > 32))
+        ++a.team_shift;
     const uint32_t teams = kRowsThreads >> a.team_shift;
     const unsigned grid = unsigned((tokens + teams - 1) / teams);
     // few tokens: a row over several CTAs (the gradient's sums stay in one)

@@ -210,6 +210,18 @@ def test_int32_rows_anywhere(hidden, offset):
     layer.check_rows()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows, hidden, k", [
+    (25000, 8, 2), (25000, 64, 3), (25000, 100, 1), (24999, 128, 8), (12001, 256, 2), (12001, 512, 1), (9001, 1024, 5), (5003, 2048, 2),
+    (4001, 4096, 2), (25000, 3, 2), (25000, 31, 3), (25000, 61, 2), (20001, 129, 2), (12001, 203, 9), (9001, 301, 2), (5003, 1001, 3), (3001, 2002, 2)])
+def test_many_tokens(dtype, rows, hidden, k):
+    """Teams of 8 to 256 threads: few threads a token where there are many tokens; some choices without a row."""
+    p, capacity = 2, rows * k
+    slots = rng(hidden).permutation(p * capacity).astype(np.int32).reshape(p, rows, k)
+    slots[rng(rows).random((p, rows, k)) < 0.05] = -1
+    Layer(dtype, p, rows, hidden, k, capacity=capacity, slots=slots).all()
+
+
 @pytest.mark.parametrize("hidden", [16, 13])
 def test_thousands_of_choices(hidden):
     """Lists of choices that need more shared memory than a kernel has without asking."""

@@ -103,6 +103,13 @@ def test_many_tensors(count, in_place):
     run(parts, in_place=in_place, offset=int(g.integers(0, 4)))
 
 
+@pytest.mark.parametrize("parts", [[(60000001, "bf16", 0), (70, "f32", 0), (9000003, "f16", 1)], [(150000000, "f32", 0), (50000003, "f32", 0), (1, "bf16", 0)]])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_large_tensors(parts, in_place):
+    """Several CTAs have a share of the tiles."""
+    run(parts, in_place=in_place, offset=1)
+
+
 def test_no_tensor():
     for parts in ([], [(0, "f32", 0)], [(5, "f32", 1)], [(0, "bf16", 0)] * 100):
         g = Grads(parts)
