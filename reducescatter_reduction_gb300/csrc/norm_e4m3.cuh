@@ -163,13 +163,13 @@ struct QuantUnit {
 
 // A thread has a unit of VEC columns at a time; KEEP of them stay in shared
 // memory between the passes, further ones are read again.  VECTOR: units are
-// 16-byte groups.  Bound by memory and by how
-// many rows are under way: 4000 x 8192 f16 p=4 in 87 us (6.0 TB/s), 4096 x 8192
-// bf16 p=8 156 (6.1), 4096 x 4096 bf16 p=1 27 (4.3).  With the units in registers instead, at four CTAs of 256 threads an
-// SM, 93, 158 and 31; here eight CTAs (six at p=8: 156, eight 172, the loads' registers spill).  Loading two or four units at
-// once cost more CTAs than it gained.
+// 16-byte groups.  Bound by memory and by how many rows are under way: 4000 x
+// 8192 f16 p=4 in 86 us (6.1 TB/s), 4096 x 8192 bf16 p=8 153 (6.2), 4096 x 4096
+// bf16 p=1 27 (4.3; 32768 rows 154-164, 6.0).  With the units in registers
+// instead, at four CTAs of 256 threads an SM, 93, 158 and 31; here eight CTAs, or six from four ranks on (p=4 with eight: 90,
+// p=8 172, the loads' registers spill).  Loading two or four units at once cost more CTAs than it gained.
 template <typename T, int P, int THREADS, int KEEP, bool VECTOR>
-__global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P == 8 ? 1536 : 2048) / THREADS : 1) ar_rmsnorm_e4m3_kernel(const __grid_constant__ QuantArgs<(P > 0 ? P : kMaxRanks)> a)
+__global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P >= 4 ? 1536 : 2048) / THREADS : 1) ar_rmsnorm_e4m3_kernel(const __grid_constant__ QuantArgs<(P > 0 ? P : kMaxRanks)> a)
 {
     using U = QuantUnit<T, VECTOR>;
     constexpr int VEC = U::VEC, S = U::S, PAIRS = U::PAIRS, WARPS = THREADS / 32;
@@ -204,20 +204,29 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P == 8 ? 1536 : 2048) / T
 
     // most rows lie in one chunk
     int chunk = 0;
-    while (base >= a.bound[chunk + 1]) ++chunk;
+    for (int hi = p; hi - chunk > 1;) {
+        const int mid = (chunk + hi) / 2;
+        if (base >= a.bound[mid]) chunk = mid;
+        else hi = mid;
+    }
     const bool one_chunk = base + H <= a.bound[chunk + 1];
-    auto source = [&](uint32_t u, int k) -> const void * {
-        int c = chunk;
-        if (!one_chunk)
-            while (base + uint64_t(u) * VEC >= a.bound[c + 1]) ++c;
-        return static_cast<const char *>(a.src[a.order[c][k]]) + base * S;
+    // the chunk of element e of the buffers, of this row
+    auto chunk_of = [&](uint64_t e) {
+        int lo = chunk;
+        if (one_chunk) return lo;
+        if constexpr (KEEP > 1) {      // many rows: two chunks, seldom more
+            while (e >= a.bound[lo + 1]) ++lo;
+        } else {
+            for (int hi = p; hi - lo > 1;) {
+                const int mid = (lo + hi) / 2;
+                if (e >= a.bound[mid]) lo = mid;
+                else hi = mid;
+            }
+        }
+        return lo;
     };
-    auto two_chunks = [&](uint32_t u) {
-        const uint64_t e = base + uint64_t(u) * VEC;
-        int c = chunk;
-        while (e >= a.bound[c + 1]) ++c;
-        return e + VEC > a.bound[c + 1];
-    };
+    // the row of the k-th rank that chunk c folds
+    auto source = [&](int c, int k) -> const void * { return static_cast<const char *>(a.src[a.order[c][k]]) + base * S; };
     Pair ss = {0.0f, 0.0f};
     float top = 0.0f;
     // pass 1: fold, merge, store h, add its squares and find the largest |h gamma|
@@ -243,9 +252,8 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P == 8 ? 1536 : 2048) / T
         return h;
     };
     // a unit element by element, each in its own chunk's order
-    auto fold_elements = [&](uint32_t u, Pair (&acc)[PAIRS]) {
+    auto fold_elements = [&](uint32_t u, int c, Pair (&acc)[PAIRS]) {
         float f[VEC];
-        int c = chunk;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
             const uint64_t e = base + U::column(u, i);
@@ -262,13 +270,14 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P == 8 ? 1536 : 2048) / T
         if (u >= u1) return;
         Pair acc[PAIRS], v[PAIRS];
         uint4 res;
-        if (!one_chunk && (!VECTOR || two_chunks(u))) {
-            fold_elements(u, acc);
+        const int c = chunk_of(base + U::column(u, 0));
+        if (!one_chunk && (!VECTOR || base + (uint64_t(u) + 1) * VEC > a.bound[c + 1])) {
+            fold_elements(u, c, acc);
             res = U::load(residual, u, H);
         } else if constexpr (P > 0) {
             uint4 r[P];
 #pragma unroll
-            for (int k = 0; k < P; ++k) r[k] = U::load(source(u, k), u, H);
+            for (int k = 0; k < P; ++k) r[k] = U::load(source(c, k), u, H);
             res = U::load(residual, u, H);
             U::unpack(r[0], acc);
 #pragma unroll
@@ -277,11 +286,29 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P == 8 ? 1536 : 2048) / T
 #pragma unroll
                 for (int i = 0; i < PAIRS; ++i) acc[i] = acc[i] + v[i];
             }
+        } else if constexpr (THREADS == 128 && KEEP == 1 && VECTOR) {
+            // few rows: the loads of eight ranks go out before the first is folded (4 x 4096 bf16 p=64 51 -> 17 us, with its chunks found by halving); with many
+            // rows their registers would cost CTAs (15683 x 2056 bf16 p=3, four at once: 144 us, one by one 108)
+            res = U::load(residual, u, H);
+#pragma unroll
+            for (int i = 0; i < PAIRS; ++i) acc[i] = {0.0f, 0.0f};
+            for (int k = 0; k < p; k += 8) {
+                uint4 r[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) r[i] = U::load(source(c, min(k + i, p - 1)), u, H);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (k + i >= p) break;
+                    U::unpack(r[i], v);
+#pragma unroll
+                    for (int j = 0; j < PAIRS; ++j) acc[j] = k + i == 0 ? v[j] : acc[j] + v[j];
+                }
+            }
         } else {
-            U::unpack(U::load(source(u, 0), u, H), acc);
+            U::unpack(U::load(source(c, 0), u, H), acc);
 #pragma unroll 4
             for (int k = 1; k < p; ++k) {
-                U::unpack(U::load(source(u, k), u, H), v);
+                U::unpack(U::load(source(c, k), u, H), v);
 #pragma unroll
                 for (int i = 0; i < PAIRS; ++i) acc[i] = acc[i] + v[i];
             }
