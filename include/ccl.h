@@ -481,7 +481,9 @@ CCL_API ccl_status_t ccl_balance_loss(ccl_comm_t comm, ccl_dtype_t dtype, ccl_pa
  *           group)] ([rows] with group 0).
  * A group with a NaN has scale NaN, one with an infinity scale infinity (its
  * finite values then have code 0).  As in ccl_allreduce_residual_rmsnorm, a
- * row whose squares overflow fp32 has 1/sqrt(...) = 0.
+ * row whose squares overflow fp32 has 1/sqrt(...) = 0; with eps 0 a row whose
+ * mean square vanishes in fp32 has 1/sqrt(...) = infinity: then o is NaN where
+ * h * gamma is 0 and infinite elsewhere.
  * residual_out may be residual_in.  Outputs overlap no input (in place is
  * refused: set them with ccl_comm_set_outputs).
  * Bytes moved: n ((p + 2) s + p) + hidden s + the scales.  The exchange between the
