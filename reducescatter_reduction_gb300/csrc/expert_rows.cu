@@ -545,7 +545,8 @@ static cudaError_t rows_launch(const Launch &L, const RowsLaunch &N, LaunchInfo 
     } else {
         kern = N.op == ROWS_DISPATCH ? dispatch_kernel<T, PM, 4> : N.op == ROWS_COMBINE ? combine_kernel<T, PM, KB, UN> : combine_grad_kernel<T, PM, KB, UN>;
     }
-    cudaError_t err = smem > 48 * 1024 ? allow_dynamic_smem(kern, 4096 * sizeof(Choice), L.device, ready[N.op]) : cudaSuccess;
+    // (a kernel has 48 KB without asking, its own arrays among them: the gradient's are 1 KB)
+    cudaError_t err = smem > 32 * 1024 ? allow_dynamic_smem(kern, 4096 * sizeof(Choice), L.device, ready[N.op]) : cudaSuccess;
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid, unsigned(split));
