@@ -13,6 +13,7 @@
 #include <cooperative_groups.h>
 #include <math_constants.h>
 
+#include "chunks.h"
 #include "logits.cuh"
 
 namespace ccl {
@@ -216,7 +217,7 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P >= 4 ? 1536 : 2048) / T
         int lo = chunk;
         if (one_chunk) return lo;
         if constexpr (KEEP > 1) {      // many rows: two chunks, seldom more
-            while (e >= a.bound[lo + 1]) ++lo;
+            lo = chunk_from(a.bound, lo, e);
         } else {
             for (int hi = p; hi - lo > 1;) {
                 const int mid = (lo + hi) / 2;
@@ -271,7 +272,7 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P >= 4 ? 1536 : 2048) / T
         if (u >= u1) return;
         Pair acc[PAIRS], v[PAIRS];
         uint4 res;
-        const int c = chunk_of(base + U::column(u, 0));
+        const int c = chunk_of(base + (VECTOR ? U::column(u, 0) : lookup_column(U::column(u, 0), H)));
         if (!one_chunk && (!VECTOR || base + (uint64_t(u) + 1) * VEC > a.bound[c + 1])) {
             fold_elements(u, c, acc);
             res = U::load(residual, u, H);
