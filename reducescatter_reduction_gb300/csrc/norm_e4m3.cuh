@@ -179,6 +179,7 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P >= 4 ? 1536 : 2048) / T
     __shared__ float2 row_s;            // 1/rms, the row's largest |o|
     __shared__ __align__(8) float2 parts[kQuantMaxCluster];
     __shared__ __align__(8) uint64_t xbar;
+    __shared__ bool gave_up;
     cg::cluster_group cluster = cg::this_cluster();
     const int C = int(cluster.num_blocks()), q = int(cluster.block_rank());
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -186,6 +187,7 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P >= 4 ? 1536 : 2048) / T
     if (C > 1) {
         // the barrier is there before a peer signals it: arrive now, wait before the first remote write
         if (threadIdx.x == 0) {
+            gave_up = false;
             asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         }
@@ -358,14 +360,13 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P >= 4 ? 1536 : 2048) / T
                              "r"(__float_as_uint(top)), "r"(map_shared(bar, lane))
                              : "memory");
             if (!wait_bounded(bar, a.wait_ns)) {
-                // A pair is missing (this call's outputs are wrong).  Once more, again bounded, so that a late peer's
-                // write does not land after this CTA has gone.
+                // a pair is missing: this call's outputs are wrong
                 if (a.status && atomicCAS(&a.status[0], 0u, 5u) == 0u) {
                     a.status[1] = blockIdx.x;
                     a.status[2] = unsigned(row);
                     a.status[3] = threadIdx.x;
                 }
-                wait_bounded(bar, a.wait_ns);
+                gave_up = true;
             }
             sum = 0.0f;
             top = 0.0f;
@@ -459,6 +460,14 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P >= 4 ? 1536 : 2048) / T
         if (u0 + warp * 32 + j * THREADS < u1) pass2(first + j * THREADS, kept_s[j][threadIdx.x], first + j * THREADS < u1);
     for (uint32_t u = first + KEEP * THREADS; u - lane < u1; u += THREADS)
         pass2(u, u < u1 ? U::load(merged, u, H) : make_uint4(0, 0, 0, 0), u < u1);      // (this thread's own stores)
+    if (C > 1 && gave_up) {
+        // A late peer's write must not land after this CTA has gone.  The row's other CTAs come here or end, none of them
+        // waits without a limit, and each has sent its pair by then; the last one's has a while to arrive.
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        wait_bounded(bar, 1000000);
+    }
 }
 
 // With eps 0 a row whose mean square vanishes in fp32 has an infinite 1/rms: its products h gamma of 0 have o = NaN, which
