@@ -17,9 +17,9 @@
 // the same thread produced (kept in registers, with gamma, for the first few
 // units of each thread) and writes the slice to all p outputs.  The exchange
 // wait is bounded by the communicator's wait limit; on expiry the CTA records
-// it in the status block (ccl_comm_check reports CCL_ERR_TIMEOUT), waits once
-// more, bounded, for late writes into its shared memory, and finishes.  The
-// only barrier is the cluster barrier before the first remote write, which
+// it in the status block (ccl_comm_check reports CCL_ERR_TIMEOUT), goes on, and
+// leaves only when the row's other CTAs have sent their sums.  The only barrier
+// otherwise is the cluster barrier before the first remote write, which
 // every CTA of the row reaches.  Each element
 // is read from the rank inputs once; all arithmetic is fp32 with explicit
 // round-to-nearest operations (1/sqrtf is IEEE-rounded under the default
@@ -232,8 +232,8 @@ __global__ void __launch_bounds__(THREADS) ar_rmsnorm_kernel(const __grid_consta
     }
     const float part = block_sum(ss, red);
     float total = part;
+    bool gave_up = false;
     if (C > 1) {
-        bool gave_up = false;
         // push: every CTA writes its slice sum into parts[q] of every CTA of the
         // row (itself included) and waits for the C sums to land in its own
         // shared memory -- no cluster barrier round trip, no remote reads.  A
@@ -268,19 +268,6 @@ __global__ void __launch_bounds__(THREADS) ar_rmsnorm_kernel(const __grid_consta
                     gave_up = true;
                     break;
                 }
-            }
-        }
-        if (gave_up) {
-            // A sum is missing (recorded above; this call's outputs are
-            // wrong).  Wait once more, again bounded, so that a late peer's
-            // write is not left to land after this CTA has gone, then go on.
-            uint64_t t1;
-            asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t1));
-            for (;;) {
-                if (cl_try_wait(lbar, 0)) break;
-                uint64_t t;
-                asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-                if (t - t1 > uint64_t(a.wait_ns)) break;
             }
         }
         total = 0.0f;
@@ -324,6 +311,19 @@ __global__ void __launch_bounds__(THREADS) ar_rmsnorm_kernel(const __grid_consta
             const float o = __fmul_rn(__fmul_rn(Tr::load1(a.residual_out, e), inv), Tr::load1(a.gamma, j));
             for (int k = 0; k < p; ++k) Tr::store1(a.dst[k], e, o);
         }
+    }
+    if (C > 1 && __any_sync(0xffffffffu, gave_up)) {
+        // A sum is missing (recorded above; this call's outputs are wrong).
+        // A late one must not be written after this CTA has gone: the row's
+        // other CTAs come here or end, none of them waits without a limit, and
+        // each has sent its sum by then; the last one's has 1 ms to arrive.
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+        const uint32_t lbar = uint32_t(__cvta_generic_to_shared(&xbar));
+        uint64_t t0, t;
+        asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+        do asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+        while (!cl_try_wait(lbar, 0) && t - t0 < 1000000);
     }
 }
 
