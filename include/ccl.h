@@ -605,7 +605,7 @@ CCL_API ccl_status_t ccl_grad_norm(ccl_comm_t comm, size_t count, const ccl_tens
  * With factor 1 a tensor in place is left as it is.  Bytes moved: the tensors'
  * twice.
  * Errors: as ccl_grad_norm; also tensors that overlap (CCL_ERR_INVALID_ARG),
- * CCL_ERR_NOMEM (no host memory for that check, 80 bytes a tensor). */
+ * CCL_ERR_NOMEM (no host memory for that check, 64 bytes a tensor). */
 CCL_API ccl_status_t ccl_grad_clip(ccl_comm_t comm, size_t count, const ccl_tensor_t *tensors, float max_norm, float *norm,
                                    void *stream);
 

@@ -5,6 +5,7 @@
 
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <new>
 
 #include "front.h"
@@ -162,7 +163,7 @@ static ccl_status_t grads(ccl_comm *c, size_t count, const ccl_tensor_t *tensors
     if (!norm) return fail(CCL_ERR_INVALID_ARG, "norm is NULL");
     ccl_status_t st;
     if ((st = check_aligned(norm, 4, "norm")) != CCL_OK) return st;
-    if (clip && !(max_norm >= 0.0f && max_norm <= 3.4e38f)) return fail(CCL_ERR_INVALID_ARG, "max_norm must be finite and >= 0");
+    if (clip && !(max_norm >= 0.0f && max_norm <= FLT_MAX)) return fail(CCL_ERR_INVALID_ARG, "max_norm must be finite and >= 0");
     const Range at = range_of(norm, 8);
     // the stretches of memory that clipping reads and writes: tensors that follow one another are one; more than 64 go to the heap
     // (what is read in front and what is written behind it, as each often is in order already)
