@@ -111,12 +111,28 @@ __device__ __forceinline__ float scale_of(float m)
     return s < 0x1p-126f ? 0x1p-126f : s;      // (NaN stays NaN)
 }
 
+// Checked build: an access lies in the row [row, row + bytes) of a buffer, or is recorded and not made.
+template <bool CHECKED>
+struct RowCheck {
+    __device__ static __forceinline__ RowCheck of(const void *, uint64_t, unsigned *) { return {}; }
+    __device__ __forceinline__ bool holds(const void *, uint32_t) const { return true; }
+};
+template <>
+struct RowCheck<true> {
+    const void *row;
+    uint64_t bytes;
+    unsigned *status;
+    __device__ static __forceinline__ RowCheck of(const void *row, uint64_t bytes, unsigned *status) { return {row, bytes, status}; }
+    __device__ __forceinline__ bool holds(const void *at, uint32_t n) const { return in_buffer(at, n, row, bytes, status, kSiteNorm); }
+};
+
 // The VEC columns of a unit, as pairs.  VECTOR: they follow one another.  Other
 // rows are read element by element, so that the 32 lanes of a load take neighbouring columns: unit u of
 // a warp's 32 has every 32nd column of their 32 VEC.
 template <typename T, bool VECTOR>
 struct QuantUnit {
     using Tr = Traits<T>;
+    using Check = RowCheck<kBoundsCheck>;
     static constexpr int VEC = Tr::VEC, S = 16 / VEC, PAIRS = VEC / 2;
     __device__ static __forceinline__ void unpack(const uint4 &v, Pair (&f)[PAIRS])
     {
@@ -125,32 +141,35 @@ struct QuantUnit {
     }
     __device__ static __forceinline__ uint32_t column(uint32_t u, int i) { return VECTOR ? u * VEC + i : u / 32 * (32 * VEC) + i * 32 + u % 32; }
     // unit u of the row that begins at `row`, of `hidden` columns
-    __device__ static __forceinline__ uint4 load(const void *row, uint32_t u, uint32_t hidden)
+    __device__ static __forceinline__ uint4 load(const void *row, uint32_t u, uint32_t hidden, Check check)
     {
         if constexpr (VECTOR) {
-            return load_v4(static_cast<const char *>(row) + uint64_t(u) * 16);
+            const char *at = static_cast<const char *>(row) + uint64_t(u) * 16;
+            return check.holds(at, 16) ? load_v4(at) : make_uint4(0, 0, 0, 0);
         } else {
             float f[VEC];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) f[i] = column(u, i) < hidden ? Tr::load1(row, column(u, i)) : 0.0f;
+            for (int i = 0; i < VEC; ++i) f[i] = column(u, i) < hidden && check.holds(static_cast<const char *>(row) + uint64_t(column(u, i)) * S, S) ? Tr::load1(row, column(u, i)) : 0.0f;
             return Tr::pack(f);
         }
     }
-    __device__ static __forceinline__ void store(void *row, uint32_t u, uint32_t hidden, const uint4 &v)
+    __device__ static __forceinline__ void store(void *row, uint32_t u, uint32_t hidden, const uint4 &v, Check check)
     {
         if constexpr (VECTOR) {
-            st_v4(static_cast<char *>(row) + uint64_t(u) * 16, v);
+            char *at = static_cast<char *>(row) + uint64_t(u) * 16;
+            if (check.holds(at, 16)) st_v4(at, v);
         } else {
             float f[VEC];
             Tr::unpack(v, f);
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
-                if (column(u, i) < hidden) Tr::store1(row, column(u, i), f[i]);
+                if (column(u, i) < hidden && check.holds(static_cast<char *>(row) + uint64_t(column(u, i)) * S, S)) Tr::store1(row, column(u, i), f[i]);
         }
     }
-    __device__ static __forceinline__ void store_codes(void *row, uint32_t u, uint32_t hidden, const uint32_t (&w)[VEC / 4])
+    __device__ static __forceinline__ void store_codes(void *row, uint32_t u, uint32_t hidden, const uint32_t (&w)[VEC / 4], Check check)
     {
         char *to = static_cast<char *>(row) + (VECTOR ? uint64_t(u) * VEC : 0);
+        if (VECTOR && !check.holds(to, VEC)) return;
         if constexpr (VECTOR && VEC == 8) {
             asm volatile("st.global.cs.v2.u32 [%0], {%1, %2};" ::"l"(to), "r"(w[0]), "r"(w[1]) : "memory");
         } else if constexpr (VECTOR) {
@@ -158,7 +177,7 @@ struct QuantUnit {
         } else {
 #pragma unroll
             for (int i = 0; i < VEC; ++i)
-                if (column(u, i) < hidden) to[column(u, i)] = char(w[i / 4] >> (i % 4 * 8));
+                if (column(u, i) < hidden && check.holds(to + column(u, i), 1)) to[column(u, i)] = char(w[i / 4] >> (i % 4 * 8));
         }
     }
 };
@@ -198,11 +217,16 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P >= 4 ? 1536 : 2048) / T
     const int p = P > 0 ? P : a.p;
     const uint32_t H = a.hidden, units = VECTOR ? H / VEC : (H + 32 * VEC - 1) / (32 * VEC) * 32;
     const uint64_t row = C > 1 ? blockIdx.x / C : blockIdx.x, base = row * H;
-    const bool held = in_bounds(row < a.rows - (a.stall_test == 2 ? 1 : 0), a.status, kSiteNorm, base);
+    // checked build: the row's `element` bytes a column at `at`, none where the debug hook takes the buffers to lack the row;
+    // gamma's; a scale's number
+    const bool held = !kBoundsCheck || row < a.rows - (a.stall_test == 2 ? 1 : 0);
+    auto in_row = [&](const void *at, uint32_t element) { return U::Check::of(at, held ? uint64_t(H) * element : 0, a.status); };
+    const auto in_gamma = U::Check::of(a.gamma, uint64_t(H) * S, a.status);
+    auto scale_held = [&](uint32_t group) { return in_bounds(held && group < a.groups, a.status, kSiteNorm, group); };
     // this CTA's units: whole warps of them, so that the lanes that share a scale are in one warp
     const uint32_t blocks = (units + 31) / 32;
     const uint32_t u0 = C > 1 ? uint32_t(uint64_t(blocks) * q / C) * 32 : 0;
-    const uint32_t u1 = !held ? u0 : C > 1 ? min(units, uint32_t(uint64_t(blocks) * (q + 1) / C) * 32) : units;
+    const uint32_t u1 = C > 1 ? min(units, uint32_t(uint64_t(blocks) * (q + 1) / C) * 32) : units;
     const char *residual = static_cast<const char *>(a.residual) + base * S;
     char *merged = static_cast<char *>(a.residual_out) + base * S;
 
@@ -231,6 +255,7 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P >= 4 ? 1536 : 2048) / T
     };
     // the row of the k-th rank that chunk c folds
     auto source = [&](int c, int k) -> const void * { return static_cast<const char *>(a.src[a.order[c][k]]) + base * S; };
+    auto load_source = [&](int c, int k, uint32_t u) { return U::load(source(c, k), u, H, in_row(source(c, k), S)); };
     Pair ss = {0.0f, 0.0f};
     float top = 0.0f;
     // pass 1: fold, merge, store h, add its squares and find the largest |h gamma|
@@ -241,12 +266,12 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P >= 4 ? 1536 : 2048) / T
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) acc[i] = acc[i] + v[i];          // the merge
         const uint4 h = Group<T>::pack(acc);
-        U::store(merged, u, H, h);
+        U::store(merged, u, H, h, in_row(merged, S));
         U::unpack(h, acc);                                               // h, rounded
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) ss = fma(acc[i], acc[i], ss);
         if (a.lanes == 0) {
-            U::unpack(U::load(a.gamma, u, H), v);
+            U::unpack(U::load(a.gamma, u, H, in_gamma), v);
 #pragma unroll
             for (int i = 0; i < PAIRS; ++i) {
                 const Pair o = acc[i] * v[i];
@@ -264,8 +289,11 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P >= 4 ? 1536 : 2048) / T
             f[i] = 0.0f;
             if (U::column(u, i) >= H) continue;
             while (e >= a.bound[c + 1]) ++c;
+            auto held_source = [&](int k) { return in_row(source(c, k), S).holds(static_cast<const char *>(a.src[a.order[c][k]]) + e * S, S); };
+            if (!held_source(0)) continue;
             f[i] = Traits<T>::load1(a.src[a.order[c][0]], e);
-            for (int k = 1; k < p; ++k) f[i] = __fadd_rn(f[i], Traits<T>::load1(a.src[a.order[c][k]], e));
+            for (int k = 1; k < p; ++k)
+                if (held_source(k)) f[i] = __fadd_rn(f[i], Traits<T>::load1(a.src[a.order[c][k]], e));
         }
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) acc[i] = {f[2 * i], f[2 * i + 1]};
@@ -275,14 +303,15 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P >= 4 ? 1536 : 2048) / T
         Pair acc[PAIRS], v[PAIRS];
         uint4 res;
         const int c = chunk_of(base + (VECTOR ? U::column(u, 0) : lookup_column(U::column(u, 0), H)));
+        if (!in_bounds(c < p, a.status, kSiteNorm, uint64_t(c))) return;
         if (!one_chunk && (!VECTOR || base + (uint64_t(u) + 1) * VEC > a.bound[c + 1])) {
             fold_elements(u, c, acc);
-            res = U::load(residual, u, H);
+            res = U::load(residual, u, H, in_row(residual, S));
         } else if constexpr (P > 0) {
             uint4 r[P];
 #pragma unroll
-            for (int k = 0; k < P; ++k) r[k] = U::load(source(c, k), u, H);
-            res = U::load(residual, u, H);
+            for (int k = 0; k < P; ++k) r[k] = load_source(c, k, u);
+            res = U::load(residual, u, H, in_row(residual, S));
             U::unpack(r[0], acc);
 #pragma unroll
             for (int k = 1; k < P; ++k) {
@@ -293,13 +322,13 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P >= 4 ? 1536 : 2048) / T
         } else if constexpr (THREADS == 128 && KEEP == 1 && VECTOR) {
             // few rows: the loads of eight ranks go out before the first is folded (4 x 4096 bf16 p=64 51 -> 17 us, with its chunks found by halving); with many
             // rows their registers would cost CTAs (15683 x 2056 bf16 p=3, four at once: 144 us, one by one 108)
-            res = U::load(residual, u, H);
+            res = U::load(residual, u, H, in_row(residual, S));
 #pragma unroll
             for (int i = 0; i < PAIRS; ++i) acc[i] = {0.0f, 0.0f};
             for (int k = 0; k < p; k += 8) {
                 uint4 r[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) r[i] = U::load(source(c, min(k + i, p - 1)), u, H);
+                for (int i = 0; i < 8; ++i) r[i] = load_source(c, min(k + i, p - 1), u);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     if (k + i >= p) break;
@@ -309,14 +338,14 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P >= 4 ? 1536 : 2048) / T
                 }
             }
         } else {
-            U::unpack(U::load(source(c, 0), u, H), acc);
+            U::unpack(load_source(c, 0, u), acc);
 #pragma unroll 4
             for (int k = 1; k < p; ++k) {
-                U::unpack(U::load(source(c, k), u, H), v);
+                U::unpack(load_source(c, k, u), v);
 #pragma unroll
                 for (int i = 0; i < PAIRS; ++i) acc[i] = acc[i] + v[i];
             }
-            res = U::load(residual, u, H);
+            res = U::load(residual, u, H, in_row(residual, S));
         }
         const uint4 h = merge(u, acc, res);
         if (kept) *kept = h;
@@ -386,7 +415,7 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P >= 4 ? 1536 : 2048) / T
     if (a.lanes == 0) {
         const float scale = scale_of(row_s.y);
         back = __frcp_rn(scale);
-        if (q == 0 && held)
+        if (q == 0 && scale_held(0))
             // (-infinity: 1/rms is infinite, and ar_rmsnorm_e4m3_rest_kernel finds out what the scale is)
             for (int k = threadIdx.x; k < p; k += THREADS) a.scales[k][row] = inv == CUDART_INF_F && scale == inv ? -inv : scale;
     }
@@ -396,7 +425,7 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P >= 4 ? 1536 : 2048) / T
         Pair o[PAIRS], g[PAIRS];
         if (on) {
             U::unpack(h, o);
-            U::unpack(U::load(a.gamma, u, H), g);
+            U::unpack(U::load(a.gamma, u, H, in_gamma), g);
 #pragma unroll
             for (int i = 0; i < PAIRS; ++i) o[i] = o[i] * g[i] * Pair{inv, inv};
         }
@@ -421,7 +450,7 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P >= 4 ? 1536 : 2048) / T
             const float scale = scale_of(m), each = __frcp_rn(scale);
 #pragma unroll
             for (int i = 0; i < VEC; ++i) by[i] = each;
-            if (on && lane % a.lanes == 0) {
+            if (on && lane % a.lanes == 0 && scale_held(u / a.lanes)) {
                 const uint64_t at = row * a.groups + u / a.lanes;
                 for (int k = 0; k < p; ++k) a.scales[k][at] = scale;
             }
@@ -441,25 +470,29 @@ __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P >= 4 ? 1536 : 2048) / T
                 for (int j = 0; j < VEC; ++j)
                     if (j <= i && j + int(span) > i) by[j] = each;
                 const uint32_t group = (block + i) / span;
-                if (group < a.groups)
+                if (group < a.groups && scale_held(group))
                     for (int k = lane; k < p; k += 32) a.scales[k][row * a.groups + group] = scale;
                 m = 0.0f;
             }
         }
         if (!on) return;
         code(by);
+        auto store_codes = [&](int k) {
+            char *to = static_cast<char *>(a.dst[k]) + base;
+            U::store_codes(to, u, H, w, in_row(to, 1));
+        };
         if constexpr (P > 0) {
 #pragma unroll
-            for (int k = 0; k < P; ++k) U::store_codes(static_cast<char *>(a.dst[k]) + base, u, H, w);
+            for (int k = 0; k < P; ++k) store_codes(k);
         } else {
-            for (int k = 0; k < p; ++k) U::store_codes(static_cast<char *>(a.dst[k]) + base, u, H, w);
+            for (int k = 0; k < p; ++k) store_codes(k);
         }
     };
 #pragma unroll
     for (int j = 0; j < KEEP; ++j)
         if (u0 + warp * 32 + j * THREADS < u1) pass2(first + j * THREADS, kept_s[j][threadIdx.x], first + j * THREADS < u1);
     for (uint32_t u = first + KEEP * THREADS; u - lane < u1; u += THREADS)
-        pass2(u, u < u1 ? U::load(merged, u, H) : make_uint4(0, 0, 0, 0), u < u1);      // (this thread's own stores)
+        pass2(u, u < u1 ? U::load(merged, u, H, in_row(merged, S)) : make_uint4(0, 0, 0, 0), u < u1);      // (this thread's own stores)
     if (C > 1 && gave_up) {
         // A late peer's write must not land after this CTA has gone.  The row's other CTAs come here or end, none of them
         // waits without a limit, and each has sent its pair by then; the last one's has a while to arrive.
