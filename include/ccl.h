@@ -537,7 +537,9 @@ CCL_API ccl_status_t ccl_expert_sort(ccl_comm_t comm, size_t rows, size_t expert
  *            ccl_expert_sort writes them: no slot twice.
  *  weights : host array of p device pointers, each float [rows, k]; NULL: 1.
  * Its gradient by the tokens is ccl_expert_combine of the rows' gradient with
- * the same slots and weights.
+ * the same slots and weights; by the weights it is dweights of
+ * ccl_expert_combine_grad called with the tokens as inputs and the rows'
+ * gradient as expert_rows (that call's outputs are then dispatch's again).
  * k <= 4096, p * rows * k and p * capacity <= 2^31 - 1.
  * Bytes moved: p rows hidden s (1 + k), the lists.
  * Errors: CCL_ERR_INVALID_ARG (a size out of range, a missing array, overlap;
