@@ -460,9 +460,11 @@ CCL_API ccl_status_t ccl_balance_loss(ccl_comm_t comm, ccl_dtype_t dtype, ccl_pa
  * Operators around a layer with experts and a training step.  No passage of
  * the pages: the operators are defined here.  What holds for the operators on
  * logits holds for them: arithmetic and sums in fp32 or more, each result
- * rounded once to its type, the same bits for the same inputs; every SM is
- * used, the communicator's variant does not matter; arrays and rank buffers are aligned
- * to their elements, and 16-byte aligned buffers and rows are fastest.  Nothing
+ * rounded once to its type, and the same call on the same inputs gives the same
+ * bits (the same values elsewhere between 16- or 128-byte boundaries of memory
+ * may be added in another order); every SM is used, the communicator's variant
+ * does not matter; arrays and rank buffers are aligned to their elements, and
+ * 16-byte aligned buffers and rows are fastest.  Nothing
  * that is written may overlap anything else, but for what an operator names.
  * Calls only enqueue and can be captured in a CUDA graph once each operator has
  * run once on the device with the same dtype and sizes.
@@ -519,7 +521,10 @@ CCL_API ccl_status_t ccl_allreduce_residual_rmsnorm_e4m3(ccl_comm_t comm, ccl_dt
  * The communicator's rank buffers are not touched.  At most 4096 experts, p *
  * rows * k and p * capacity <= 2^31 - 1.  The counts of parts pass through the
  * communicator's device block.
- * Bytes moved: 8 p rows k, the valid bytes, the offsets.
+ * Bytes moved: 8 p rows k, the valid bytes and the offsets up to 4096 choices;
+ * beyond, the ids are read twice (12 p rows k), and from 256 choices for each of
+ * a CTA's warps on (1.2 million choices in all with up to 1200 experts, 150 thousand
+ * with 4096) three times, with slots written, read and written again (24 p rows k).
  * Errors: CCL_ERR_INVALID_ARG (a size out of range, a missing array, overlap),
  * CCL_ERR_UNSUPPORTED (experts > 4096), CCL_ERR_CUDA. */
 CCL_API ccl_status_t ccl_expert_sort(ccl_comm_t comm, size_t rows, size_t experts, size_t k, const int32_t *const *expert_ids,
@@ -605,7 +610,8 @@ CCL_API ccl_status_t ccl_grad_norm(ccl_comm_t comm, size_t count, const ccl_tens
  *  norm     : device, two floats: norm[0] is read (ccl_grad_norm's, or any
  *             other), norm[1] written.
  * With factor 1 a tensor in place is left as it is.  Bytes moved: the tensors'
- * twice.
+ * twice.  A tensor's out that lies otherwise between 16-byte boundaries than its
+ * in is written element by element, which takes four times as long.
  * Errors: as ccl_grad_norm; also tensors that overlap (CCL_ERR_INVALID_ARG),
  * CCL_ERR_NOMEM (no host memory for that check, 64 bytes a tensor). */
 CCL_API ccl_status_t ccl_grad_clip(ccl_comm_t comm, size_t count, const ccl_tensor_t *tensors, float max_norm, float *norm,

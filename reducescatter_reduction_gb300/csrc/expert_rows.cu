@@ -344,7 +344,8 @@ __global__ void __launch_bounds__(kRowsThreads, KB * UN == 8 ? 3 : 4) combine_gr
 // any column is two aligned ones and a shift; what is written goes by the
 // groups of the row that is written.  Measured (us; against accesses of one
 // element, or of 4 bytes where they are aligned): combine, 2 x 4000 x 1001 bf16, k=4, 36 -> 23.5; its gradient
-// 94 -> 39, of 3 x 12400 x 731 bf16, k=2, 224 -> 95; dispatch, 3 x 1111 x 1001 f32, 7.6 -> 7.5.
+// 94 -> 39, of 3 x 12400 x 731 bf16, k=2, 224 -> 95; dispatch, 3 x 1111 x 1001 f32, 7.6 -> 7.5.  With choices sorted by expert
+// 2 x 4000 x 1001 bf16, k=4, takes 13.7 (dispatch, copy rate 11.7), 17.0 (combine, 11.8) and 34 (gradient, 21.1).
 // ---------------------------------------------------------------------------
 
 // The checked build tests rows as a whole here: the views keep to them.

@@ -9,10 +9,12 @@
 // number among its expert's in the stretch is what the warp has counted so
 // far plus the lanes before it with the same expert; those are found by a
 // ballot for each bit of the expert's number (match.any takes a step for each
-// different expert among the lanes: 1 Mi choices of 256 experts on 8 ranks 21.8 us, with ballots, and quads of cells in the sums, 17.6).
+// different expert among the lanes: with it 1 Mi choices of 256 experts on 8 ranks took 21.8 us, with ballots, and quads of cells
+// in the sums, 17.6 then).
 // All sums are of integers, and the order is fixed.  Bound by instructions and
-// latency: 1 Mi choices of 256 experts, 8 MB moved, take 15.0 us (of 8 experts 12.3, of 512 17.7), 131072 of 64
-// experts 8.3: two launches, and in each CTA a chain of loads, ballots, sums and barriers.
+// latency: 1 Mi choices of 256 experts on 8 ranks, 12.6 MB moved, take 15.5 us (padded 17.9; of 8 experts 13.1, of 512 18.2, of
+// 4096 67, whose counters leave 9 warps and 64 parts), 2 Mi 27.5, 8 Mi 79, where numbers pass through the slots (200 MB):
+// two launches, and in each CTA a chain of loads, ballots, sums and barriers.
 #include <algorithm>
 
 #include "logits.cuh"
@@ -27,7 +29,7 @@ constexpr int kSortItems = 8;                // choices a thread reads at once
 // Measured (256 experts, graph replay, us; one CTA against two kernels): 512 choices 4.6; 4096 7.0, 6.6; 8192 10.6, 6.8.
 constexpr uint32_t kSortAlone = 4096;
 // Choices of a part, at least: a part takes about 0.4 us for each 1024 of them, and every part more makes the sums before it
-// longer (256 experts, us, with 512 and 2048: 8192 choices 6.8, 8.3; 65536 9.4, 9.0; 1 Mi, of which an SM has 6900, 15.5).
+// longer (256 experts, us, with 512 and 2048: 8192 choices 6.8, 8.3; 65536 9.4, 9.0; 1 Mi has 6900 for each SM with either).
 constexpr uint32_t kSortPart = 512;
 
 template <int PM>

@@ -185,10 +185,14 @@ struct QuantUnit {
 // A thread has a unit of VEC columns at a time; KEEP of them stay in shared
 // memory between the passes, further ones are read again.  VECTOR: units are
 // 16-byte groups.  Bound by memory and by how many rows are under way: 4000 x
-// 8192 f16 p=4 in 86 us (6.1 TB/s), 4096 x 8192 bf16 p=8 153 (6.2), 4096 x 4096
-// bf16 p=1 27 (4.3; 32768 rows 154-164, 6.0).  With the units in registers
-// instead, at four CTAs of 256 threads an SM, 93, 158 and 31; here eight CTAs, or six from four ranks on (p=4 with eight: 90,
-// p=8 172, the loads' registers spill).  Loading two or four units at once cost more CTAs than it gained.
+// 8192 f16 p=4 in 85 us (6.1 TB/s), 4096 x 8192 bf16 p=8 153 (6.2), 4096 x 4096
+// bf16 p=1 21 with a scale a row, 24 with scales of 128 columns (4.8; 32768 rows 168, 5.6).  With the units in registers
+// instead, at four CTAs of 256 threads an SM, of then 86, 153 and 27 us 93, 158 and 31.  Here 2048 threads an SM, or 1536 where
+// four or eight ranks' loads are in registers at once (p=4 with 2048: 90, p=8 172, they spill).  A rank count of the launch
+// and odd rows go rank by rank and keep 2048, although they spill 100 to 450 bytes: us with 2048 / 1536 / 1024,
+//   4096 x 4096 bf16 p=5 69 / 67 / 72, p=6 74 / 76 / 83, p=7 84 / 85 / 93, p=16 145 / 152 / 156, p=64 537 / 567 / 544
+//   20000 x 2001 bf16 p=1 169 / 183 / 233, 4000 x 1001 f32 p=4 41 / 49 / 60, 40000 x 301 bf16 p=1 56 / 53 / 57
+// Loading two or four units at once cost more CTAs than it gained.
 template <typename T, int P, int THREADS, int KEEP, bool VECTOR>
 __global__ void __launch_bounds__(THREADS, KEEP > 1 ? (P >= 4 ? 1536 : 2048) / THREADS : 1) ar_rmsnorm_e4m3_kernel(const __grid_constant__ QuantArgs<(P > 0 ? P : kMaxRanks)> a)
 {
@@ -575,7 +579,15 @@ static cudaError_t quant_launch(const Launch &L, const NormE4m3Launch &N, Launch
     a.status = L.status;
     a.wait_ns = L.wait_limit_ns > 0 ? L.wait_limit_ns : 2000000000LL;
     a.stall_test = L.stall_test;
-    // CTA shape by rows against the SMs, as in rmsnorm.cu, and by width.  Rows that are no 16-byte groups, us with 64 / 512
+    // CTA shape by rows against the SMs, as in rmsnorm.cu, and by width.  Whole groups, us (bf16 p=8, scales of 128 columns)
+    // with threads x units kept of 128x1 / 1024x1 / 64x4 / 128x4 / 256x4 / 512x4:
+    //   100 rows of 1536     4.5 /  4.6 /  6.6 /  5.4 /  4.2 /  4.2     4096 rows of 768    17 /  77 /  17 /  15 /  20 /  34
+    //   100 rows of 8192     5.9 /  7.1 /  8.9 /  9.6 /  9.2 /  7.1     4096 rows of 1536   44 /  86 /  33 /  32 /  32 /  43
+    //   200 rows of 1536     4.9 /  6.7 /  6.7 /  5.6 /  4.7 /  4.6     4096 rows of 4096  100 / 115 / 106 /  80 /  78 /  78
+    //   200 rows of 8192    10.3 / 11.3 / 11.2 / 10.8 / 10.9 /  9.7     4096 rows of 8192  206 / 170 / 212 / 159 / 153 / 155
+    //   300 rows of 16384     30 /   36 /   43 /   34 /   27 /   27     4096 rows of 16384 366 / 429 / 454 / 320 / 308 / 303
+    // (between SMs and twice as many rows the 1024 threads of rmsnorm.cu are not the best here.)  Rows that are no 16-byte
+    // groups, us with 64 / 512
     // threads (128): 2320 x 372 f16 p=1 8.9 / 21, 9217 x 499 f32 p=1 15 / 45; 914 x 1795 bf16 p=8 (128: 34) / 26.
     const uint64_t units = VECTOR ? N.norm.hidden / VEC : (N.norm.hidden + 32 * VEC - 1) / (32 * VEC) * 32, sms = uint64_t(L.num_sms), rows = N.norm.rows;
     const int threads = rows < sms      ? 128

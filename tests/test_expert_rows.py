@@ -6,7 +6,8 @@ a step).  combine adds k products with k fused multiply-adds, each rounded: k
 U32 of the sum of the products' sizes.  A weight's gradient is a sum over the
 hidden columns in fp32: a thread adds at most hidden / 32 + 8 products in a
 row (a warp or more shares a row, 8 columns at a time), then at most 15 more
-additions join the threads."""
+additions join the threads; of a narrow row, which 8 or 16 threads share, a
+thread adds at most 12 (8 columns, and 4 of the edges'), and 4 more join them."""
 import numpy as np
 import pytest
 import torch

@@ -1,8 +1,10 @@
 """ccl_grad_norm and ccl_grad_clip against their formulas in 64 bits.
 
-Tolerances.  The norm: at most 16 values are squared and added in fp32 before
-their sum goes on in fp64, so a sum has at most 16 roundings (U32 each), its
-root half of that, and the norm is rounded once more: 9 U32.  A clipped value
+Tolerances.  The norm: a thread squares and adds 32 values (fp32: 16) in four
+chains of at most 8 fused multiply-adds, joined by two additions: at most 10
+roundings (U32 each).  Their sum goes on as two fp32 numbers or in fp64, where
+less than one U32 is lost; the root halves it, and the norm is rounded once
+more: 7 U32, of which 9 are asked.  A clipped value
 is its product with the factor, rounded to fp32 and to the type; the factor is
 checked by itself (a sum and a quotient: 2 U32)."""
 import math
