@@ -467,7 +467,8 @@ CCL_API ccl_status_t ccl_balance_loss(ccl_comm_t comm, ccl_dtype_t dtype, ccl_pa
  * 16-byte aligned buffers and rows are fastest.  Nothing
  * that is written may overlap anything else, but for what an operator names.
  * Calls only enqueue and can be captured in a CUDA graph once each operator has
- * run once on the device with the same dtype and sizes.
+ * run once on the device with the same dtype, sizes and alignment (the norm with
+ * e4m3 output also with eps 0, where that is captured: it takes a kernel more).
  * ------------------------------------------------------------------------- */
 
 /* ccl_allreduce_residual_rmsnorm with an 8-bit output: the communicator's
